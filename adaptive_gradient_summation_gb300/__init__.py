@@ -11,6 +11,9 @@ include/adasum.h (libadasum_gb300.so).  This module only marshals torch tensors 
 that ABI: it checks dtypes, devices, lengths and contiguity, passes pointers and the
 current CUDA stream, and raises AdasumError on a non-OK status.  There is no CPU or
 PyTorch fallback: if the library is not built, every call raises.
+
+The operators of the training step that leaves those gradients (token embeddings, layer
+norm, activations kept in 8 bits) are in training.py and exported here.
 """
 from __future__ import annotations
 
@@ -21,10 +24,16 @@ import numpy as np
 import torch
 
 from ._native import AdasumError, KernelStat, Status, check, library_path, load_library
+from .training import (Checkpoint, checkpoint_pack, checkpoint_unpack, embedding, embedding_backward,
+                       gelu_checkpointed, gelu_checkpointed_backward, layer_norm, layer_norm_backward,
+                       layer_norm_checkpointed, layer_norm_checkpointed_backward)
 
 __all__ = ["reduce", "pair", "pair_noalloc", "reduce_momentum_sgd", "local_momentum_reduce", "reduce_from_host", "AdasumError",
            "Status", "load_library", "library_path", "get_last_error", "release_workspace",
-           "launch_count", "recomputed_segments", "profile_enable", "profile_collect", "version"]
+           "launch_count", "recomputed_segments", "profile_enable", "profile_collect", "version",
+           "Checkpoint", "checkpoint_pack", "checkpoint_unpack", "embedding", "embedding_backward",
+           "gelu_checkpointed", "gelu_checkpointed_backward", "layer_norm", "layer_norm_backward",
+           "layer_norm_checkpointed", "layer_norm_checkpointed_backward"]
 
 _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}
 

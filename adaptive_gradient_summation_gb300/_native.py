@@ -39,6 +39,8 @@ class KernelStat(ctypes.Structure):
                 ("total_ms", ctypes.c_double), ("total_bytes", ctypes.c_double)]
 
 
+_P, _I, _I64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+
 #: Every symbol include/adasum.h declares, with (restype, argtypes).
 SIGNATURES = {
     "adasum_reduce": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int,
@@ -65,6 +67,20 @@ SIGNATURES = {
         ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, ctypes.POINTER(ctypes.c_int64),
         ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p,
         ctypes.c_float, ctypes.c_float, ctypes.c_void_p]),
+    "adasum_embedding": (ctypes.c_int, [_P, _I64, _I64, _I, _P, _I, _I64, _F, _P, _P]),
+    "adasum_embedding_backward": (ctypes.c_int, [_P, _I64, _I64, _I, _P, _I, _P, _I, _I64, _F, _I64,
+                                                 _P, _I, _I, _P, _I64, _P]),
+    "adasum_embedding_backward_scratch_bytes": (ctypes.c_int64, [_I64, _I64, _I]),
+    "adasum_layer_norm": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P]),
+    "adasum_layer_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I64, _I, _P, _I, _P, _I,
+                                                  _P, _P, _P, _I, _I, _P, _I64, _P]),
+    "adasum_layer_norm_backward_scratch_bytes": (ctypes.c_int64, [_I64, _I64, _I]),
+    "adasum_layer_norm_backward_checkpointed": (ctypes.c_int, [
+        _P, _I64, _P, _P, _P, _I64, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _I64, _P]),
+    "adasum_checkpoint_pack": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _P, _P, _P]),
+    "adasum_checkpoint_unpack": (ctypes.c_int, [_P, _P, _I64, _I64, _I, _P, _P]),
+    "adasum_gelu_checkpointed": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P]),
+    "adasum_gelu_checkpointed_backward": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I64, _I, _I, _P, _P, _P]),
     "adasum_get_last_error": (ctypes.c_int, []),
     "adasum_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "adasum_release_workspace": (ctypes.c_int, []),

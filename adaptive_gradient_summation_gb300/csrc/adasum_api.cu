@@ -22,6 +22,7 @@
 #include <vector>
 
 #include "../../include/adasum.h"
+#include "adasum_host.h"
 #include "adasum_internal.h"
 
 namespace adasum {
@@ -1293,6 +1294,15 @@ adasum_status_t reduce_host_impl(const void* const* host_grads, int K, const int
 }
 
 }  // namespace
+
+// What the translation units of the training operators share with this one (adasum_host.h).
+std::mutex& entry_mutex() { return g_mu; }
+cudaEvent_t profile_start(cudaStream_t stream) { return maybe_start(stream); }
+adasum_status_t profile_launched(int rc, const char* name, cudaEvent_t start, cudaStream_t stream,
+                                 double bytes) {
+  return record_launch(rc, name, start, stream, bytes) ? ADASUM_ERR_CUDA : ADASUM_OK;
+}
+
 }  // namespace adasum
 
 using namespace adasum;

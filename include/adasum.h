@@ -300,6 +300,169 @@ ADASUM_API adasum_status_t adasum_pair_noalloc(const void *a, const void *b, int
                                                adasum_dtype_t dtype, void *out,
                                                adasum_stream_t stream);
 
+/* ---- Operators of the training step around the combine ---------------------------- */
+
+/*
+ * The operators below are the memory-bound ends of a training step: token embeddings,
+ * layer norm, and activations kept in 8 bits between the forward and the backward pass.
+ * Their parameter gradients are written per worker, into the flat gradient buffers that
+ * adasum_reduce takes: the rows of one call are the microbatches of K workers one after
+ * the other, worker k's being rows [worker_offsets[k], worker_offsets[k+1]), and
+ * gradient k is the sum over those rows only.
+ *
+ * Conventions, in addition to those at the top of this file:
+ *   - a matrix of rows x cols elements has its columns next to each other; `ld` is the
+ *     distance in elements between the starts of two rows (>= cols; inputs only: outputs
+ *     are dense, ld = cols);
+ *   - bf16 and fp32 are accepted independently for activations, parameters and parameter
+ *     gradients.  All arithmetic and all sums are fp32, each output is rounded once;
+ *   - worker_offsets is a HOST array of K+1 int64 values, worker_offsets[0] = 0,
+ *     non-decreasing, ending at the row count; it and the host pointer arrays are copied
+ *     before the call returns.  A worker without rows gets a zero gradient (or, with
+ *     accumulate, keeps its own);
+ *   - accumulate = 0 overwrites the gradients, anything else adds to them: the old value
+ *     is widened, the new sum added in fp32, and the result rounded once;
+ *   - results do not depend on timing: every sum has a fixed order, so equal calls give
+ *     equal bits;
+ *   - no output may overlap an input or another output (ADASUM_ERR_ALIAS);
+ *   - they use none of the library workspace.  Where scratch memory is needed the caller
+ *     passes it (its size from the matching *_scratch_bytes function; 256-byte aligned,
+ *     contents arbitrary, free for reuse by later work on the same stream).  So calls on
+ *     different streams may overlap, and any call may be captured in a CUDA graph.
+ */
+
+/* Columns per scale of an 8-bit checkpoint. */
+#define ADASUM_CHECKPOINT_BLOCK 128
+/* Distance in bytes between two rows of an 8-bit checkpoint's codes. */
+#define ADASUM_CHECKPOINT_PITCH(cols) (((cols) + 15) / 16 * 16)
+/* Scales per row of an 8-bit checkpoint. */
+#define ADASUM_CHECKPOINT_SCALES(cols) (((cols) + ADASUM_CHECKPOINT_BLOCK - 1) / ADASUM_CHECKPOINT_BLOCK)
+/* Longest row of the layer norm entry points. */
+#define ADASUM_NORM_MAX_COLS 16384
+
+/*
+ * adasum_embedding -- out[i] = scale * table[tokens[i]], i < n.
+ *   table         num_rows x cols elements of dtype
+ *   tokens        n device integers of token_bytes (4 or 8) bytes, signed.  A token
+ *                 outside [0, num_rows), such as the -1 that marks padding, gives zeros.
+ *   out           n x cols elements of dtype (rounded once, after the scaling)
+ */
+ADASUM_API adasum_status_t adasum_embedding(const void *table, int64_t num_rows, int64_t cols,
+                                            adasum_dtype_t dtype, const void *tokens,
+                                            int token_bytes, int64_t n, float scale, void *out,
+                                            adasum_stream_t stream);
+
+/*
+ * adasum_embedding_backward -- the gradient of the table, per worker:
+ *     grads[k][v] = scale * sum of grad_out[i] over worker k's i with tokens[i] = v,
+ * the whole num_rows x cols gradient (rows without a token become zero), or with
+ * accumulate the same added to what is there (rows without a token are not touched).
+ * The sum of a row runs over its tokens in their order, in runs of bounded length.
+ *   grad_out      worker_offsets[K] rows of cols elements of dtype, ld apart
+ *   padding_idx   a token that gets no gradient (any value outside [0, num_rows): none);
+ *                 tokens outside the table get none either
+ *   grads         host array of K device pointers, num_rows x cols elements of grad_dtype
+ *   scratch       adasum_embedding_backward_scratch_bytes(worker_offsets[K], cols, K)
+ * 1 <= K <= ADASUM_MAX_K; fewer than 2^31 tokens and table rows, else
+ * ADASUM_ERR_UNSUPPORTED.
+ */
+ADASUM_API adasum_status_t adasum_embedding_backward(
+    const void *grad_out, int64_t cols, int64_t ld, adasum_dtype_t dtype, const void *tokens,
+    int token_bytes, const int64_t *worker_offsets, int K, int64_t num_rows, float scale,
+    int64_t padding_idx, void *const *grads, adasum_dtype_t grad_dtype, int accumulate,
+    void *scratch, int64_t scratch_bytes, adasum_stream_t stream);
+ADASUM_API int64_t adasum_embedding_backward_scratch_bytes(int64_t n, int64_t cols, int K);
+
+/*
+ * adasum_layer_norm -- per row: mean and variance over the columns, rstd =
+ * 1/sqrt(var + eps), h = (x - mean) rstd, y = h weight + bias.
+ *   x             rows x cols elements of dtype, ld apart; cols <= ADASUM_NORM_MAX_COLS
+ *   weight, bias  cols elements of weight_dtype; NULL: 1 and 0
+ *   y             rows x cols elements of dtype
+ *   mean, rstd    rows floats each, for the backward pass; either may be NULL
+ *   codes, scales both NULL, or the 8-bit checkpoint of h (adasum_checkpoint_pack's
+ *                 format): with it the backward pass needs neither x nor mean
+ */
+ADASUM_API adasum_status_t adasum_layer_norm(const void *x, int64_t rows, int64_t cols, int64_t ld,
+                                             adasum_dtype_t dtype, const void *weight,
+                                             const void *bias, adasum_dtype_t weight_dtype,
+                                             float eps, void *y, float *mean, float *rstd,
+                                             int8_t *codes, float *scales,
+                                             adasum_stream_t stream);
+
+/*
+ * adasum_layer_norm_backward -- with h = (x - mean) rstd and g = grad_out * weight,
+ *     grad_x = rstd (g - mean(g) - h mean(g h)),
+ *     grad_weights[k] = sum of grad_out h,  grad_biases[k] = sum of grad_out,
+ * the last two over worker k's rows.
+ *   grad_out, x   rows x cols elements of dtype, ld_grad and ld_x apart
+ *   mean, rstd    as the forward pass left them
+ *   grad_x        rows x cols elements of dtype
+ *   grad_weights, grad_biases  host arrays of K device pointers to cols elements of
+ *                 grad_dtype; either may be NULL: not wanted
+ *   scratch       adasum_layer_norm_backward_scratch_bytes(rows, cols, K); may be NULL
+ *                 when neither gradient is wanted
+ */
+ADASUM_API adasum_status_t adasum_layer_norm_backward(
+    const void *grad_out, int64_t ld_grad, const void *x, int64_t ld_x, const float *mean,
+    const float *rstd, int64_t cols, adasum_dtype_t dtype, const void *weight,
+    adasum_dtype_t weight_dtype, const int64_t *worker_offsets, int K, void *grad_x,
+    void *const *grad_weights, void *const *grad_biases, adasum_dtype_t grad_dtype,
+    int accumulate, void *scratch, int64_t scratch_bytes, adasum_stream_t stream);
+ADASUM_API int64_t adasum_layer_norm_backward_scratch_bytes(int64_t rows, int64_t cols, int K);
+
+/*
+ * adasum_layer_norm_backward_checkpointed -- the same from the 8-bit checkpoint of h that
+ * adasum_layer_norm left: h is what the codes stand for.
+ *   y             NULL, or rows x cols elements of dtype: h weight + bias, the forward
+ *                 pass's output again (for the weight gradient of the layer that read it,
+ *                 so that the output itself need not be kept)
+ *   bias          used for y only
+ */
+ADASUM_API adasum_status_t adasum_layer_norm_backward_checkpointed(
+    const void *grad_out, int64_t ld_grad, const int8_t *codes, const float *scales,
+    const float *rstd, int64_t cols, adasum_dtype_t dtype, const void *weight, const void *bias,
+    adasum_dtype_t weight_dtype, const int64_t *worker_offsets, int K, void *grad_x, void *y,
+    void *const *grad_weights, void *const *grad_biases, adasum_dtype_t grad_dtype,
+    int accumulate, void *scratch, int64_t scratch_bytes, adasum_stream_t stream);
+
+/*
+ * adasum_checkpoint_pack -- 8-bit checkpoint of an activation.  Every row is cut into
+ * blocks of 128 columns (the last may be shorter).  A block with the largest magnitude m
+ * gets the scale m / 127 and the codes q = round(x * (127 / m)), ties to even, and stands
+ * for q * scale: each value within m / 254 (plus fp32 rounding) of the original.
+ *   codes         rows x ADASUM_CHECKPOINT_PITCH(cols) bytes, 16-byte aligned (the bytes
+ *                 past cols are unspecified)
+ *   scales        rows x ADASUM_CHECKPOINT_SCALES(cols) floats
+ * A block with a NaN or an infinity gets the scale NaN, so all of it is restored as NaN:
+ * nothing non-finite is lost.  A block whose largest magnitude is below 2^-119 is kept as
+ * zeros.
+ */
+ADASUM_API adasum_status_t adasum_checkpoint_pack(const void *x, int64_t rows, int64_t cols,
+                                                  int64_t ld, adasum_dtype_t dtype, int8_t *codes,
+                                                  float *scales, adasum_stream_t stream);
+/* adasum_checkpoint_unpack -- the values the codes stand for, rows x cols of dtype. */
+ADASUM_API adasum_status_t adasum_checkpoint_unpack(const int8_t *codes, const float *scales,
+                                                    int64_t rows, int64_t cols,
+                                                    adasum_dtype_t dtype, void *out,
+                                                    adasum_stream_t stream);
+
+/*
+ * adasum_gelu_checkpointed -- y = gelu(x), and the 8-bit checkpoint of x, in one pass.
+ * tanh_form = 0: x Phi(x) with the normal distribution function Phi; otherwise
+ * 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))).
+ * adasum_gelu_checkpointed_backward -- grad_x = grad_out gelu'(x) for the x that the codes
+ * stand for; with y (else NULL) also gelu(x) of it, so that the output need not be kept.
+ */
+ADASUM_API adasum_status_t adasum_gelu_checkpointed(const void *x, int64_t rows, int64_t cols,
+                                                    int64_t ld, adasum_dtype_t dtype,
+                                                    int tanh_form, void *y, int8_t *codes,
+                                                    float *scales, adasum_stream_t stream);
+ADASUM_API adasum_status_t adasum_gelu_checkpointed_backward(
+    const void *grad_out, int64_t ld_grad, const int8_t *codes, const float *scales, int64_t rows,
+    int64_t cols, adasum_dtype_t dtype, int tanh_form, void *grad_x, void *y,
+    adasum_stream_t stream);
+
 /* ---- Instrumentation (used by the benchmark; not needed for normal use) ---------- */
 
 /*
