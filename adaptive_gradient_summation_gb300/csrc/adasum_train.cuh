@@ -42,6 +42,85 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// ------------------------------------------------------------- eight columns of a lane
+
+// A warp covers 256 columns of a row at a time, eight per lane.  kVec: lane l holds the
+// neighbouring columns 8 l .. 8 l + 7, moved as 16-byte vectors; it needs rows that start
+// on 16-byte boundaries.  kStrided: lane l holds columns l, l + 32, ..., l + 224, moved one
+// by one but coalesced over the lanes; for every other address.
+enum Layout : int { kStrided = 0, kVec = 1 };
+
+template <int LAYOUT>
+__device__ __forceinline__ int lane_col(int lane, int e) {
+  return LAYOUT == kVec ? lane * 8 + e : e * 32 + lane;
+}
+
+// Raw bits of a lane's eight values.
+template <typename T>
+struct Raw8 {
+  uint32_t w[sizeof(T) * 2];
+};
+
+template <typename T>
+__device__ __forceinline__ float raw_value(const Raw8<T>& r, int e) {
+  if constexpr (sizeof(T) == 2) return __uint_as_float(e & 1 ? r.w[e >> 1] & 0xFFFF0000u : r.w[e >> 1] << 16);
+  else return __uint_as_float(r.w[e]);
+}
+
+// Loads the values of 256 columns starting at p, of which `left` exist (others are 0).
+// KEEP: the data will be read again (default: streaming).
+template <typename T, int LAYOUT, bool KEEP = false>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int64_t left, int lane) {
+  Raw8<T> r;
+  if (LAYOUT == kVec && lane * 8 + 8 <= left) {
+    const uint4* q = reinterpret_cast<const uint4*>(p + lane * 8);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+      const uint4 v = KEEP ? __ldg(q + i) : __ldcs(q + i);
+      r.w[4 * i] = v.x;
+      r.w[4 * i + 1] = v.y;
+      r.w[4 * i + 2] = v.z;
+      r.w[4 * i + 3] = v.w;
+    }
+    return r;
+  }
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) * 2; ++i) r.w[i] = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = lane_col<LAYOUT>(lane, e);
+    if (c >= left) continue;
+    if constexpr (sizeof(T) == 2) r.w[e >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[c]) << (16 * (e & 1));
+    else r.w[e] = reinterpret_cast<const uint32_t*>(p)[c];
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Stores eight values of 256 columns starting at p, of which `left` exist.
+template <typename T, int LAYOUT>
+__device__ __forceinline__ void store8(T* p, int64_t left, int lane, const float (&v)[8]) {
+  if (LAYOUT == kVec && lane * 8 + 8 <= left) {
+    uint4* q = reinterpret_cast<uint4*>(p + lane * 8);
+    if constexpr (sizeof(T) == 2) {
+      __stcs(q, make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])));
+    } else {
+      __stcs(reinterpret_cast<float4*>(q), make_float4(v[0], v[1], v[2], v[3]));
+      __stcs(reinterpret_cast<float4*>(q) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = lane_col<LAYOUT>(lane, e);
+    if (c < left) p[c] = narrow<T>(v[e]);
+  }
+}
+
 // ------------------------------------------------------------------- 8-bit checkpoints
 
 constexpr int kCkptBlock = 128;
