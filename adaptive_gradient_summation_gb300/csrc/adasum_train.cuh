@@ -42,6 +42,56 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// ------------------------------------------------------------- pairs of fp32 operations
+
+// Two fp32 operations per instruction (each rounded as the scalar one would be).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ float2 parts(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// max of magnitudes that keeps a NaN.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ------------------------------------------------------------- eight columns of a lane
 
 // A warp covers 256 columns of a row at a time, eight per lane.  kVec: lane l holds the
@@ -96,6 +146,29 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int64_t left, int lane) {
   return r;
 }
 
+// Eight floats of a lane in shared memory, the columns of its layout.
+template <int LAYOUT>
+__device__ __forceinline__ void lds8(const float* p, int lane, float (&v)[8]) {
+  if constexpr (LAYOUT == kVec) {
+    const float4 a = reinterpret_cast<const float4*>(p)[lane * 2], b = reinterpret_cast<const float4*>(p)[lane * 2 + 1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[e * 32 + lane];
+  }
+}
+template <int LAYOUT>
+__device__ __forceinline__ void sts8(float* p, int lane, const float (&v)[8]) {
+  if constexpr (LAYOUT == kVec) {
+    reinterpret_cast<float4*>(p)[lane * 2] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[lane * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e * 32 + lane] = v[e];
+  }
+}
+
 __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -141,12 +214,118 @@ __device__ __forceinline__ CkptScale ckpt_scale(float top, bool bad) {
   if (top < kCkptTiny) return {0.f, 0.f};
   return {__fdiv_rn(top, 127.f), __fdiv_rn(127.f, top)};
 }
-// round(x * inv), ties to even; |x * inv| <= 127 up to rounding, so adding 1.5 * 2^23
-// leaves the integer in the low bits of the sum.  (A NaN or infinity, in a block whose
-// scale is NaN, gives an arbitrary code.)
-__device__ __forceinline__ uint32_t ckpt_code(float x, float inv) {
-  return __float_as_uint(__fadd_rn(__fmul_rn(x, inv), 12582912.f)) & 0xFFu;
+// Codes are round(x * inv), ties to even; |x * inv| <= 127 up to rounding, so adding
+// 1.5 * 2^23 leaves the integer in the low bits of the sum.  (A NaN or infinity, in a block
+// whose scale is NaN, gives an arbitrary code.)
+// The codes of eight values (two words, in the order of the values): the sum's low byte of
+// each.  (The products are scalar: a packed product and sum were measured to be contracted
+// to a fused one, which rounds differently next to ties.)
+__device__ __forceinline__ uint2 ckpt_codes8(const float (&v)[8], float inv_lo, float inv_hi) {
+  uint32_t b[8];
+  const F2 magic = f2(12582912.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float k = i < 2 ? inv_lo : inv_hi;
+    const float2 s = parts(add2(f2(__fmul_rn(v[2 * i], k), __fmul_rn(v[2 * i + 1], k)), magic));
+    b[2 * i] = __float_as_uint(s.x);
+    b[2 * i + 1] = __float_as_uint(s.y);
+  }
+  return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
 }
-__device__ __forceinline__ float ckpt_value(int8_t q, float scale) { return __fmul_rn(static_cast<float>(q), scale); }
+// The values of eight codes: a code plus 128 becomes the low byte of 2^23 as a float, and
+// the rest is exact up to the product with the scale.
+__device__ __forceinline__ void ckpt_values8(uint2 q, float lo_scale, float hi_scale, float (&v)[8]) {
+  const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
+  const F2 bias = f2(-8388736.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = w[i >> 1];
+    const float lo = __uint_as_float(__byte_perm(x, 0x4B000000u, i & 1 ? 0x7442 : 0x7440));
+    const float hi = __uint_as_float(__byte_perm(x, 0x4B000000u, i & 1 ? 0x7443 : 0x7441));
+    const float2 s = parts(mul2(add2(f2(lo, hi), bias), f2(i < 2 ? lo_scale : hi_scale)));
+    v[2 * i] = s.x;
+    v[2 * i + 1] = s.y;
+  }
+}
+
+// Codes of 256 columns, the same columns per lane as the values'; rows of codes start on
+// 16-byte boundaries whatever the layout of the values.
+template <int LAYOUT>
+__device__ __forceinline__ uint2 load_codes8(const int8_t* p, int64_t left, int lane) {
+  if constexpr (LAYOUT == kVec) {  // (rows of codes are padded to 16, so a begun eight is always there)
+    return lane * 8 < left ? __ldcs(reinterpret_cast<const uint2*>(p) + lane) : make_uint2(0u, 0u);
+  } else {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = lane_col<LAYOUT>(lane, e);
+      if (c < left) w[e >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(p[c])) << (8 * (e & 3));
+    }
+    return make_uint2(w[0], w[1]);
+  }
+}
+template <int LAYOUT>
+__device__ __forceinline__ void store_codes8(int8_t* p, int64_t left, int lane, uint2 q) {
+  if constexpr (LAYOUT == kVec) {
+    if (lane * 8 < left) __stcs(reinterpret_cast<uint2*>(p) + lane, q);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = lane_col<LAYOUT>(lane, e);
+      if (c < left) p[c] = static_cast<int8_t>(((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 0xFFu);
+    }
+  }
+}
+
+// Scales of the (one or two) blocks that a lane's eight of 256 columns lie in, from all the
+// lanes' values; columns past the row's end hold 0.  kVec: a block is half a warp; kStrided:
+// a block is four values of every lane.
+template <int LAYOUT>
+__device__ __forceinline__ void ckpt_scales8(const float (&v)[8], CkptScale (&s)[2]) {
+  const float inf = __int_as_float(0x7F800000);
+  float top[2];
+  top[0] = max_abs_nan(max_abs_nan(v[0], v[1], v[2]), v[3], v[3]);
+  top[1] = max_abs_nan(max_abs_nan(v[4], v[5], v[6]), v[7], v[7]);
+  if constexpr (LAYOUT == kVec) {
+    top[0] = max_nan(top[0], top[1]);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) top[0] = max_nan(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], d));
+    s[0] = s[1] = ckpt_scale(top[0], !(top[0] < inf));
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      // (magnitudes as integers are ordered like the values, with NaN above infinity)
+      top[b] = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top[b])));
+      s[b] = ckpt_scale(top[b], !(top[b] < inf));
+    }
+  }
+}
+// Stores the scales of 256 columns, of which `left` exist, at p.
+template <int LAYOUT>
+__device__ __forceinline__ void store_scales(float* p, int64_t left, int lane, const CkptScale (&s)[2]) {
+  if constexpr (LAYOUT == kVec) {
+    if ((lane & 15) == 0 && lane * 8 < left) p[lane >> 4] = s[0].scale;
+  } else {
+    if (lane == 0) {
+      p[0] = s[0].scale;
+      if (left > kCkptBlock) p[1] = s[1].scale;
+    }
+  }
+}
+template <int LAYOUT>
+__device__ __forceinline__ uint2 ckpt_codes(const float (&v)[8], const CkptScale (&s)[2]) {
+  return ckpt_codes8(v, s[0].inv, LAYOUT == kVec ? s[0].inv : s[1].inv);
+}
+// Values of 256 columns' codes, of which `left` columns exist; p: their scales.
+template <int LAYOUT>
+__device__ __forceinline__ void ckpt_values(uint2 q, const float* p, int64_t left, int lane, float (&v)[8]) {
+  if constexpr (LAYOUT == kVec) {
+    const float s = lane * 8 < left ? p[lane >> 4] : 0.f;
+    ckpt_values8(q, s, s, v);
+  } else {
+    ckpt_values8(q, p[0], left > kCkptBlock ? p[1] : 0.f, v);
+  }
+}
 
 }  // namespace adasum

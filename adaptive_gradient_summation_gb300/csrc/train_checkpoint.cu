@@ -8,25 +8,83 @@ namespace adasum {
 namespace {
 
 constexpr int kCkptThreads = 256;
+constexpr int kCkptWarps = kCkptThreads / 32;
+constexpr int kSlice = 256;  // columns a warp moves at a time
+constexpr int kItems = 4;    // of them in flight
 
 enum Act : int { kActNone = 0, kActErf = 1, kActTanh = 2 };
 
-// gelu(x) and its slope.
-template <int ACT>
-__device__ float gelu_value(float x) {
-  if constexpr (ACT == kActTanh) {
-    const float u = 0.7978845608f * (x + 0.044715f * x * x * x);
-    return 0.5f * x * (1.f + tanhf(u));
-  }
-  return 0.5f * x * (1.f + erff(x * 0.70710678f));
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-template <int ACT>
-__device__ float gelu_slope(float x) {
-  if constexpr (ACT == kActTanh) {
-    const float t = tanhf(0.7978845608f * (x + 0.044715f * x * x * x));
-    return 0.5f * (1.f + t) + 0.5f * x * (1.f - t * t) * 0.7978845608f * (1.f + 0.134145f * x * x);
+__device__ __forceinline__ float ex2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ F2 rcp2(F2 x) {
+  const float2 p = parts(x);
+  return f2(rcp_approx(p.x), rcp_approx(p.y));
+}
+__device__ __forceinline__ F2 exp2_2(F2 x) {
+  const float2 p = parts(x);
+  return f2(ex2_approx(p.x), ex2_approx(p.y));
+}
+
+// gelu of two values, and its slope.
+//
+// Erf form: with a = |x|, the upper tail of the normal distribution is
+//     q = 1/2 erfc(a / sqrt 2) = 1/2 (a1 t + ... + a5 t^5) exp(-a^2 / 2),
+//     t = 1 / (1 + p a / sqrt 2)
+// (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26; the error of erf is
+// below 1.5e-7).  gelu = max(x, 0) - a q; slope = Phi + x phi, where the density phi takes
+// the same exponential.  Two special-function operations and about a dozen others per value,
+// where the library's erf and exp would be bound by instruction issue.
+// Tanh form: 1/2 (1 + tanh u) is the logistic function of 2 u, s = 1 / (1 + exp(-2 u));
+// gelu = x s, slope = s + x s (1 - s) (2 u)', with 1 - s = s exp(-2 u) so that nothing cancels.
+// x is held within the range where s differs from 0 and 1 in fp32's normal range, so that no
+// product of zero and infinity arises; NaN passes.
+template <int ACT, bool VALUE, bool SLOPE>
+__device__ __forceinline__ void gelu2(F2 x, F2& value, F2& slope) {
+  const float2 xs = parts(x);
+  if constexpr (ACT == kActErf) {
+    // (|x| beyond 16 has q = 0; the bound keeps 0 * infinity out)
+    const F2 a = f2(min_nan(fabsf(xs.x), 16.f), min_nan(fabsf(xs.y), 16.f));
+    const F2 t = rcp2(fma2(a, f2(0.3275911f * 0.70710678118f), f2(1.f)));
+    const F2 e = exp2_2(mul2(mul2(a, a), f2(-0.72134752044f)));
+    F2 p = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
+    p = fma2(p, t, f2(0.5f * 1.421413741f));
+    p = fma2(p, t, f2(0.5f * -0.284496736f));
+    p = fma2(p, t, f2(0.5f * 0.254829592f));
+    const F2 q = mul2(mul2(p, t), e);
+    if constexpr (VALUE) {
+      const float2 as = parts(a);
+      value = fma2(f2(-as.x, -as.y), q, f2(max_nan(xs.x, 0.f), max_nan(xs.y, 0.f)));
+    }
+    if constexpr (SLOPE) {
+      const float2 qs = parts(q);
+      const F2 phi = add2(f2(copysignf(0.5f - qs.x, xs.x), copysignf(0.5f - qs.y, xs.y)), f2(0.5f));
+      slope = fma2(mul2(x, f2(0.39894228040f)), e, phi);
+    }
+  } else {
+    constexpr float kTwoC = 1.5957691216f, kLog2e = 1.4426950409f, kCube = 0.044715f;
+    const F2 c = f2(max_nan(xs.x, -8.f), max_nan(xs.y, -8.f));
+    F2 b = c;
+    if constexpr (SLOPE) {
+      const float2 cs = parts(c);
+      b = f2(min_nan(cs.x, 8.f), min_nan(cs.y, 8.f));
+    }
+    const F2 sq = mul2(b, b);
+    const F2 e = exp2_2(mul2(b, fma2(sq, f2(-kTwoC * kLog2e * kCube), f2(-kTwoC * kLog2e))));
+    const F2 s = rcp2(add2(e, f2(1.f)));
+    if constexpr (VALUE) value = mul2(c, s);
+    if constexpr (SLOPE) {
+      const F2 du = mul2(b, fma2(sq, f2(3.f * kTwoC * kCube), f2(kTwoC)));
+      slope = fma2(mul2(du, s), mul2(s, e), s);
+    }
   }
-  return 0.5f * (1.f + erff(x * 0.70710678f)) + x * 0.3989422804f * expf(-0.5f * x * x);
 }
 
 struct PackArgs {
@@ -35,6 +93,8 @@ struct PackArgs {
   int8_t* codes;
   float* scales;
   void* y;  // the activation's output (kActNone: null)
+  int64_t pitch, nscales;   // of a row's codes and scales
+  uint32_t slices, items;   // slices of 256 columns in a row, in all
 };
 struct UnpackArgs {
   const int8_t* codes;
@@ -44,75 +104,137 @@ struct UnpackArgs {
   int64_t ld_dy;
   void* out;       // the values (kActNone) or grad_x
   void* y;         // the activation again; null: not wanted
+  int64_t pitch, nscales;
+  uint32_t slices, items;
 };
 
-// One warp per block of 128 columns.
-template <typename T, int ACT>
+// A warp takes kItems slices of 256 columns, of one row or of several, and loads them all
+// before it works on the first.  Bound by bytes: each value is read and written once.
+struct Slice {
+  int64_t row, c0;
+};
+__device__ __forceinline__ Slice slice_of(uint32_t item, uint32_t slices) {
+  const uint32_t row = item / slices;
+  return {static_cast<int64_t>(row), static_cast<int64_t>(item - row * slices) * kSlice};
+}
+
+template <typename T, int ACT, int LAYOUT>
 __global__ void __launch_bounds__(kCkptThreads) pack_kernel(const PackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t nb = ckpt_scales(a.cols);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kCkptThreads / 32) + (threadIdx.x >> 5); i < a.rows * nb; i += step) {
-    const int64_t row = i / nb, c0 = (i - row * nb) * kCkptBlock;
-    const T* x = static_cast<const T*>(a.x) + row * a.ld;
-    float v[4], top = 0.f;
-    bool bad = false;
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = c0 + e * 32 + lane;
-      v[e] = c < a.cols ? widen(x[c]) : 0.f;
-      bad |= !isfinite(v[e]);
-      top = fmaxf(top, fabsf(v[e]));
+  const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
+  Raw8<T> r[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (first + i >= a.items) break;
+    const Slice s = slice_of(first + i, a.slices);
+    r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.row * a.ld + s.c0, a.cols - s.c0, lane);
+  }
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (first + i >= a.items) break;
+    const Slice s = slice_of(first + i, a.slices);
+    const int64_t left = a.cols - s.c0;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = raw_value<T>(r[i], e);
+    CkptScale sc[2];
+    ckpt_scales8<LAYOUT>(v, sc);
+    store_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, left, lane, ckpt_codes<LAYOUT>(v, sc));
+    store_scales<LAYOUT>(a.scales + s.row * a.nscales + s.c0 / kCkptBlock, left, lane, sc);
+    if constexpr (ACT != kActNone) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        F2 value, slope;
+        gelu2<ACT, true, false>(f2(v[e], v[e + 1]), value, slope);
+        const float2 p = parts(value);
+        y[e] = p.x;
+        y[e + 1] = p.y;
+      }
+      store8<T, LAYOUT>(static_cast<T*>(a.y) + s.row * a.cols + s.c0, left, lane, y);
     }
-    const CkptScale sc = ckpt_scale(warp_max(top), __any_sync(0xFFFFFFFFu, bad));
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = c0 + e * 32 + lane;
-      if (c >= a.cols) continue;
-      a.codes[row * ckpt_pitch(a.cols) + c] = static_cast<int8_t>(ckpt_code(v[e], sc.inv));
-      if constexpr (ACT != kActNone) static_cast<T*>(a.y)[row * a.cols + c] = narrow<T>(gelu_value<ACT>(v[e]));
-    }
-    if (lane == 0) a.scales[i] = sc.scale;
   }
 }
 
-template <typename T, int ACT>
+template <typename T, int ACT, bool AGAIN, int LAYOUT>
 __global__ void __launch_bounds__(kCkptThreads) unpack_kernel(const UnpackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t nb = ckpt_scales(a.cols);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kCkptThreads / 32);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kCkptThreads / 32) + (threadIdx.x >> 5); i < a.rows * nb; i += step) {
-    const int64_t row = i / nb, c0 = (i - row * nb) * kCkptBlock;
-    const float scale = a.scales[i];
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = c0 + e * 32 + lane;
-      if (c >= a.cols) continue;
-      const float v = ckpt_value(a.codes[row * ckpt_pitch(a.cols) + c], scale);
-      T* out = static_cast<T*>(a.out) + row * a.cols + c;
-      if constexpr (ACT == kActNone) {
-        *out = narrow<T>(v);
-      } else {
-        *out = narrow<T>(widen(static_cast<const T*>(a.dy)[row * a.ld_dy + c]) * gelu_slope<ACT>(v));
-        if (a.y != nullptr) static_cast<T*>(a.y)[row * a.cols + c] = narrow<T>(gelu_value<ACT>(v));
+  const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
+  uint2 q[kItems];
+  Raw8<T> r[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (first + i >= a.items) break;
+    const Slice s = slice_of(first + i, a.slices);
+    q[i] = load_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, a.cols - s.c0, lane);
+    if constexpr (ACT != kActNone)
+      r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.row * a.ld_dy + s.c0, a.cols - s.c0, lane);
+  }
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    if (first + i >= a.items) break;
+    const Slice s = slice_of(first + i, a.slices);
+    const int64_t left = a.cols - s.c0, at = s.row * a.cols + s.c0;
+    float v[8];
+    ckpt_values<LAYOUT>(q[i], a.scales + s.row * a.nscales + s.c0 / kCkptBlock, left, lane, v);
+    if constexpr (ACT != kActNone) {
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        F2 value, slope;
+        gelu2<ACT, AGAIN, true>(f2(v[e], v[e + 1]), value, slope);
+        const float2 d = parts(mul2(slope, f2(raw_value<T>(r[i], e), raw_value<T>(r[i], e + 1))));
+        v[e] = d.x;
+        v[e + 1] = d.y;
+        if constexpr (AGAIN) {
+          const float2 p = parts(value);
+          y[e] = p.x;
+          y[e + 1] = p.y;
+        }
       }
+      if constexpr (AGAIN) store8<T, LAYOUT>(static_cast<T*>(a.y) + at, left, lane, y);
     }
+    store8<T, LAYOUT>(static_cast<T*>(a.out) + at, left, lane, v);
   }
 }
 
-unsigned ckpt_grid(int64_t rows, int64_t cols) {
-  const int64_t need = (rows * ckpt_scales(cols) + kCkptThreads / 32 - 1) / (kCkptThreads / 32);
-  return static_cast<unsigned>(std::min<int64_t>(need, 8 * static_cast<int64_t>(sm_count())));
+template <typename A>
+dim3 ckpt_grid(const A& a) {
+  return dim3((a.items + kCkptWarps * kItems - 1) / (kCkptWarps * kItems));
 }
 
-template <typename T>
+template <typename T, int LAYOUT>
 int launch_pack(const PackArgs& a, int act, cudaStream_t stream) {
-  auto k = act == kActNone ? pack_kernel<T, kActNone> : act == kActErf ? pack_kernel<T, kActErf> : pack_kernel<T, kActTanh>;
-  return launch_pdl(k, dim3(ckpt_grid(a.rows, a.cols)), dim3(kCkptThreads), 0, stream, a);
+  auto k = act == kActNone ? pack_kernel<T, kActNone, LAYOUT>
+                           : act == kActErf ? pack_kernel<T, kActErf, LAYOUT> : pack_kernel<T, kActTanh, LAYOUT>;
+  return launch_pdl(k, ckpt_grid(a), dim3(kCkptThreads), 0, stream, a);
 }
-template <typename T>
+template <typename T, int LAYOUT>
 int launch_unpack(const UnpackArgs& a, int act, cudaStream_t stream) {
-  auto k = act == kActNone ? unpack_kernel<T, kActNone> : act == kActErf ? unpack_kernel<T, kActErf> : unpack_kernel<T, kActTanh>;
-  return launch_pdl(k, dim3(ckpt_grid(a.rows, a.cols)), dim3(kCkptThreads), 0, stream, a);
+  const bool y = a.y != nullptr;
+  auto k = act == kActNone  ? unpack_kernel<T, kActNone, false, LAYOUT>
+           : act == kActErf ? (y ? unpack_kernel<T, kActErf, true, LAYOUT> : unpack_kernel<T, kActErf, false, LAYOUT>)
+                            : (y ? unpack_kernel<T, kActTanh, true, LAYOUT> : unpack_kernel<T, kActTanh, false, LAYOUT>);
+  return launch_pdl(k, ckpt_grid(a), dim3(kCkptThreads), 0, stream, a);
+}
+
+// Slices of a call.  Dense rows of whole blocks follow each other without a gap in every
+// buffer, so they are taken as one long row.
+template <typename A>
+bool cut(A& a, int64_t ld) {
+  if (a.cols % kCkptBlock == 0 && (ld == a.cols || a.rows == 1)) {
+    a.cols *= a.rows;
+    a.rows = 1;
+  }
+  a.pitch = ckpt_pitch(a.cols);
+  a.nscales = ckpt_scales(a.cols);
+  const int64_t slices = (a.cols + kSlice - 1) / kSlice;
+  if (slices > UINT32_MAX / 2 / a.rows) return false;
+  a.slices = static_cast<uint32_t>(slices);
+  a.items = static_cast<uint32_t>(slices * a.rows);
+  return true;
 }
 
 adasum_status_t check_shape(int64_t rows, int64_t cols, int dtype) {
@@ -121,7 +243,7 @@ adasum_status_t check_shape(int64_t rows, int64_t cols, int dtype) {
   return ADASUM_OK;
 }
 
-adasum_status_t pack(const PackArgs& a, int dtype, int act, cudaStream_t stream) {
+adasum_status_t pack(PackArgs a, int dtype, int act, cudaStream_t stream) {
   if (adasum_status_t st = check_shape(a.rows, a.cols, dtype)) return st;
   if (a.rows == 0) return ADASUM_OK;
   if (a.x == nullptr || a.codes == nullptr || a.scales == nullptr || (act != kActNone && a.y == nullptr) ||
@@ -135,12 +257,15 @@ adasum_status_t pack(const PackArgs& a, int dtype, int act, cudaStream_t stream)
   set.write(a.y, a.rows * a.cols * e);
   if (set.conflict()) return ADASUM_ERR_ALIAS;
   const double n = static_cast<double>(a.rows) * a.cols;
+  const bool vec = is_aligned(a.x, 16) && is_aligned(a.y, 16) && a.ld * e % 16 == 0 && (act == kActNone || a.cols * e % 16 == 0);
+  if (!cut(a, a.ld)) return ADASUM_ERR_UNSUPPORTED;
   return counted_launch(stream, act ? "gelu_checkpoint" : "checkpoint_pack", n * (e + 1 + (act ? e : 0)), [&] {
-    return dtype == kBF16 ? launch_pack<bf16>(a, act, stream) : launch_pack<float>(a, act, stream);
+    if (dtype == kBF16) return vec ? launch_pack<bf16, kVec>(a, act, stream) : launch_pack<bf16, kStrided>(a, act, stream);
+    return vec ? launch_pack<float, kVec>(a, act, stream) : launch_pack<float, kStrided>(a, act, stream);
   });
 }
 
-adasum_status_t unpack(const UnpackArgs& a, int dtype, int act, cudaStream_t stream) {
+adasum_status_t unpack(UnpackArgs a, int dtype, int act, cudaStream_t stream) {
   if (adasum_status_t st = check_shape(a.rows, a.cols, dtype)) return st;
   if (a.rows == 0) return ADASUM_OK;
   if (a.codes == nullptr || a.scales == nullptr || a.out == nullptr || !is_aligned(a.codes, 16) ||
@@ -155,9 +280,13 @@ adasum_status_t unpack(const UnpackArgs& a, int dtype, int act, cudaStream_t str
   set.write(a.y, a.rows * a.cols * e);
   if (set.conflict()) return ADASUM_ERR_ALIAS;
   const double n = static_cast<double>(a.rows) * a.cols;
+  const bool vec = is_aligned(a.out, 16) && is_aligned(a.y, 16) && a.cols * e % 16 == 0 &&
+                   (act == kActNone || (is_aligned(a.dy, 16) && a.ld_dy * e % 16 == 0));
+  if (!cut(a, act == kActNone ? a.cols : a.ld_dy)) return ADASUM_ERR_UNSUPPORTED;
   return counted_launch(stream, act ? "gelu_grad_checkpoint" : "checkpoint_unpack",
                         n * (1 + e + (act ? e : 0) + (a.y ? e : 0)), [&] {
-    return dtype == kBF16 ? launch_unpack<bf16>(a, act, stream) : launch_unpack<float>(a, act, stream);
+    if (dtype == kBF16) return vec ? launch_unpack<bf16, kVec>(a, act, stream) : launch_unpack<bf16, kStrided>(a, act, stream);
+    return vec ? launch_unpack<float, kVec>(a, act, stream) : launch_unpack<float, kStrided>(a, act, stream);
   });
 }
 
@@ -171,14 +300,14 @@ extern "C" {
 adasum_status_t adasum_checkpoint_pack(const void* x, int64_t rows, int64_t cols, int64_t ld, adasum_dtype_t dtype,
                                        int8_t* codes, float* scales, adasum_stream_t stream) {
   EntryScope scope("adasum_checkpoint_pack");
-  return pack(PackArgs{x, rows, cols, ld, codes, scales, nullptr}, dtype, kActNone,
+  return pack(PackArgs{x, rows, cols, ld, codes, scales, nullptr, 0, 0, 0, 0}, dtype, kActNone,
               reinterpret_cast<cudaStream_t>(stream));
 }
 
 adasum_status_t adasum_checkpoint_unpack(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
                                          adasum_dtype_t dtype, void* out, adasum_stream_t stream) {
   EntryScope scope("adasum_checkpoint_unpack");
-  return unpack(UnpackArgs{codes, scales, rows, cols, nullptr, 0, out, nullptr}, dtype, kActNone,
+  return unpack(UnpackArgs{codes, scales, rows, cols, nullptr, 0, out, nullptr, 0, 0, 0, 0}, dtype, kActNone,
                 reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -186,7 +315,7 @@ adasum_status_t adasum_gelu_checkpointed(const void* x, int64_t rows, int64_t co
                                          int tanh_form, void* y, int8_t* codes, float* scales,
                                          adasum_stream_t stream) {
   EntryScope scope("adasum_gelu_checkpointed");
-  return pack(PackArgs{x, rows, cols, ld, codes, scales, y}, dtype, tanh_form ? kActTanh : kActErf,
+  return pack(PackArgs{x, rows, cols, ld, codes, scales, y, 0, 0, 0, 0}, dtype, tanh_form ? kActTanh : kActErf,
               reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -195,7 +324,7 @@ adasum_status_t adasum_gelu_checkpointed_backward(const void* grad_out, int64_t 
                                                   adasum_dtype_t dtype, int tanh_form, void* grad_x, void* y,
                                                   adasum_stream_t stream) {
   EntryScope scope("adasum_gelu_checkpointed_backward");
-  return unpack(UnpackArgs{codes, scales, rows, cols, grad_out, ld_grad, grad_x, y}, dtype,
+  return unpack(UnpackArgs{codes, scales, rows, cols, grad_out, ld_grad, grad_x, y, 0, 0, 0, 0}, dtype,
                 tanh_form ? kActTanh : kActErf, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -7,7 +7,8 @@
 namespace adasum {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kSlice = 256;        // columns of a warp's eight per lane
+constexpr int kNormCtasPerSm = 2;  // of the persistent grids
 
 struct NormArgs {
   const void* x;
@@ -21,6 +22,14 @@ struct NormArgs {
   float* rstd;         // may be null
   int8_t* codes;       // null: no checkpoint
   float* scales;
+};
+
+// Rows of worker k are [off[k], off[k+1]) and belong to CTAs [cta_off[k], cta_off[k+1]),
+// `rows_per_cta` each.
+struct WorkerRows {
+  int K, rows_per_cta;
+  int64_t off[kMaxK + 1];
+  int cta_off[kMaxK + 1];
 };
 
 struct NormGradArgs {
@@ -38,146 +47,412 @@ struct NormGradArgs {
   int weight_dtype;
   void* dx;
   void* y;             // null: not wanted
+  float* partials;     // [CTA][weight, bias][cols]; null: parameters' gradients not wanted
 };
 
 struct ParamGradArgs {
-  void* dw[kMaxK];
+  const float* partials;
+  int64_t cols;
+  int dtype, accumulate;
+  void* dw[kMaxK];     // null: not wanted
   void* db[kMaxK];
-  int64_t off[kMaxK + 1];
-  int K;
-  int dtype, accumulate, want_w, want_b;
+  int cta_off[kMaxK + 1];
 };
 
-__device__ float block_sum(float v, float* red) {
-  v = warp_sum(v);
+// A row is shared by a team of W warps, each holding NV slices of 256 columns in registers
+// (slice j * W + w for warp w), so that a row is read once.  A CTA holds TEAMS teams.
+template <int W, int NV>
+struct Team {
+  static constexpr int kWarps = W < 8 ? 8 : W;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kTeams = kWarps / W;
+  static constexpr int kCols = W * NV * kSlice;
+  // one team's barrier (a CTA of one team uses the CTA's)
+  static __device__ __forceinline__ void sync(int team) {
+    if constexpr (kTeams == 1) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
+  }
+};
+
+// The weight and bias of a CTA's columns as floats in shared memory, 1 and 0 where absent.
+template <int COLS, int THREADS>
+__device__ __forceinline__ void stage_params(float* w, float* b, const void* weight, const void* bias, int dtype,
+                                             int64_t cols) {
+  for (int c = threadIdx.x; c < COLS; c += THREADS) {
+    if (w) w[c] = c < cols && weight ? load_any(weight, dtype, c) : 1.f;
+    if (b) b[c] = c < cols && bias ? load_any(bias, dtype, c) : 0.f;
+  }
+}
+
+// Layer norm.  Mean and variance of a row from registers, the variance about the mean; with
+// several warps a row, each has the mean and the sum of squares about it of its own columns
+// and one exchange joins them: with n_w columns, mean m_w and sum of squares S_w,
+//     mean = sum n_w m_w / n,   S = sum S_w + n_w (m_w - mean)^2.
+// Bound by the bytes of x and y; the next row is on its way while one is worked on.
+template <typename T, int LAYOUT, int W, int NV, bool KEEP>
+__global__ void __launch_bounds__(Team<W, NV>::kThreads) norm_kernel(const NormArgs a) {
+  using TM = Team<W, NV>;
+  pdl_enter();
+  extern __shared__ __align__(16) float sm[];
+  float *ws = sm, *bs = sm + TM::kCols;
+  __shared__ float2 ex[2][TM::kTeams][W];
+  stage_params<TM::kCols, TM::kThreads>(ws, bs, a.weight, a.bias, a.weight_dtype, a.cols);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / W, w = warp % W;
+  const float inv_n = 1.f / static_cast<float>(a.cols);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * TM::kTeams;
+  const int64_t pitch = ckpt_pitch(a.cols), nscales = ckpt_scales(a.cols);
+  auto left_of = [&](int j) { return a.cols - (j * W + w) * kSlice; };
+  Raw8<T> next[NV];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      next[j] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld + (j * W + w) * kSlice,
+                                 row < a.rows ? left_of(j) : 0, lane);
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * TM::kTeams + team;
+  fetch(row);
+  for (int it = 0; row < a.rows; row += step, it ^= 1) {
+    Raw8<T> r[NV];
+    float sum = 0.f, count = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      r[j] = next[j];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += raw_value<T>(r[j], e);
+      count += static_cast<float>(max(static_cast<int64_t>(0), min(left_of(j), static_cast<int64_t>(kSlice))));
+    }
+    fetch(row + step);
+    sum = warp_sum(sum);
+    float mean = W == 1 ? sum * inv_n : (count > 0.f ? sum / count : 0.f);
+    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int64_t left = left_of(j);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = raw_value<T>(r[j], e) - mean;
+        if (left >= kSlice || lane_col<LAYOUT>(lane, e) < left) sq = __fmaf_rn(d, d, sq);
+      }
+    }
+    sq = warp_sum(sq);
+    if constexpr (W > 1) {
+      if (lane == 0) ex[it][team][w] = make_float2(mean, sq);
+      TM::sync(team);
+      float total = 0.f;
+      auto columns = [&](int i) {  // of warp i
+        float n = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          n += static_cast<float>(max(static_cast<int64_t>(0), min(a.cols - (j * W + i) * kSlice, static_cast<int64_t>(kSlice))));
+        return n;
+      };
+      float2 v[W];
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        v[i] = ex[it][team][i];
+        total = __fmaf_rn(columns(i), v[i].x, total);
+      }
+      mean = total * inv_n;
+      sq = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        const float d = v[i].x - mean;
+        sq += __fmaf_rn(columns(i) * d, d, v[i].y);
+      }
+    }
+    const float rstd = 1.f / sqrtf(__fmaf_rn(sq, inv_n, a.eps));
+    if (w == 0 && lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c0 = (j * W + w) * kSlice;
+      const int64_t left = left_of(j);
+      if (left <= 0) break;
+      float h[8], wv[8], bv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = (raw_value<T>(r[j], e) - mean) * rstd;
+      if constexpr (KEEP) {
+        if (left < kSlice) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (lane_col<LAYOUT>(lane, e) >= left) h[e] = 0.f;
+        }
+        CkptScale sc[2];
+        ckpt_scales8<LAYOUT>(h, sc);
+        store_codes8<LAYOUT>(a.codes + row * pitch + c0, left, lane, ckpt_codes<LAYOUT>(h, sc));
+        store_scales<LAYOUT>(a.scales + row * nscales + c0 / kCkptBlock, left, lane, sc);
+      }
+      lds8<LAYOUT>(ws + c0, lane, wv);
+      lds8<LAYOUT>(bs + c0, lane, bv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn(h[e], wv[e], bv[e]);
+      store8<T, LAYOUT>(static_cast<T*>(a.y) + row * a.cols + c0, left, lane, h);
+    }
+  }
+}
+
+// The gradient.  With g = dy w and h the normalised row,
+//     dx = rstd (g - mean(g) - h mean(g h)),   dw += dy h,   db += dy:
+// one read of dy and x (or of h's codes), two sums per row, and the parameters' sums of a
+// CTA's rows in registers, joined over its teams at the end and written as the CTA's partial.
+// A CTA's rows all belong to one worker.  Bound by the bytes of dy, x and dx.
+template <typename T, int LAYOUT, int W, int NV, bool KEPT>
+__global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? 2 : 1) norm_grad_kernel(const NormGradArgs a,
+                                                                         const __grid_constant__ WorkerRows rows) {
+  using TM = Team<W, NV>;
+  pdl_enter();
+  extern __shared__ __align__(16) float sm[];  // weight, bias; at the end the teams' sums
+  float *ws = sm, *bs = sm + TM::kCols;
+  __shared__ float2 ex[2][TM::kTeams][W];
+  stage_params<TM::kCols, TM::kThreads>(ws, KEPT ? bs : nullptr, a.weight, a.bias, a.weight_dtype, a.cols);
   __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < kNormThreads / 32; ++i) s += red[i];
-  return s;
-}
-
-// One CTA per row; the row is read three times (the second and third from cache).
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const NormArgs a) {
-  pdl_enter();
-  __shared__ float red[kNormThreads / 32];
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(a.x) + row * a.ld;
-  T* y = static_cast<T*>(a.y) + row * a.cols;
-  float s = 0.f;
-  for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) s += widen(x[c]);
-  const float mean = block_sum(s, red) / static_cast<float>(a.cols);
-  float v = 0.f;
-  for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-    const float d = widen(x[c]) - mean;
-    v = __fmaf_rn(d, d, v);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / W, w = warp % W;
+  const float inv_n = 1.f / static_cast<float>(a.cols);
+  const int64_t pitch = ckpt_pitch(a.cols), nscales = ckpt_scales(a.cols);
+  int k = 0;
+  for (int hi = rows.K; hi - k > 1;) {
+    const int m = (k + hi) >> 1;
+    if (rows.cta_off[m] <= static_cast<int>(blockIdx.x)) k = m;
+    else hi = m;
   }
-  const float rstd = 1.f / sqrtf(block_sum(v, red) / static_cast<float>(a.cols) + a.eps);
-  for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-    const float h = (widen(x[c]) - mean) * rstd;
-    const float w = a.weight ? load_any(a.weight, a.weight_dtype, c) : 1.f;
-    const float b = a.bias ? load_any(a.bias, a.weight_dtype, c) : 0.f;
-    y[c] = narrow<T>(__fmaf_rn(h, w, b));
-  }
-  if (threadIdx.x == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
-  if (a.codes == nullptr) return;
-  const int lane = threadIdx.x & 31;
-  for (int64_t blk = threadIdx.x >> 5; blk < ckpt_scales(a.cols); blk += kNormThreads / 32) {
-    float h[4], top = 0.f;
-    bool bad = false;
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = blk * kCkptBlock + e * 32 + lane;
-      h[e] = c < a.cols ? (widen(x[c]) - mean) * rstd : 0.f;
-      bad |= !isfinite(h[e]);
-      top = fmaxf(top, fabsf(h[e]));
+  const int64_t r0 = rows.off[k] + static_cast<int64_t>(blockIdx.x - rows.cta_off[k]) * rows.rows_per_cta;
+  const int64_t r1 = min(r0 + rows.rows_per_cta, rows.off[k + 1]);
+  auto left_of = [&](int j) { return a.cols - (j * W + w) * kSlice; };
+  float dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[j][e] = db[j][e] = 0.f;
+  struct Row {
+    Raw8<T> dy[NV], x[KEPT ? 1 : NV];
+    uint2 q[KEPT ? NV : 1];
+    float scale[KEPT ? NV : 1][2];
+    float mean, rstd;
+  } next;
+  auto fetch = [&](int64_t row) {
+    const bool in = row < r1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c0 = (j * W + w) * kSlice;
+      const int64_t left = in ? left_of(j) : 0;
+      next.dy[j] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left, lane);
+      if constexpr (KEPT) {
+        next.q[j] = load_codes8<LAYOUT>(a.codes + row * pitch + c0, left, lane);
+        const float* s = a.scales + row * nscales + c0 / kCkptBlock;
+        if constexpr (LAYOUT == kVec) {
+          next.scale[j][0] = lane * 8 < left ? s[lane >> 4] : 0.f;
+          next.scale[j][1] = next.scale[j][0];
+        } else {
+          next.scale[j][0] = left > 0 ? s[0] : 0.f;
+          next.scale[j][1] = left > kCkptBlock ? s[1] : 0.f;
+        }
+      } else {
+        next.x[j] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld_x + c0, left, lane);
+      }
     }
-    const CkptScale sc = ckpt_scale(warp_max(top), __any_sync(0xFFFFFFFFu, bad));
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = blk * kCkptBlock + e * 32 + lane;
-      if (c < a.cols) a.codes[row * ckpt_pitch(a.cols) + c] = static_cast<int8_t>(ckpt_code(h[e], sc.inv));
+    next.mean = !KEPT && in ? a.mean[row] : 0.f;
+    next.rstd = in ? a.rstd[row] : 0.f;
+  };
+  int64_t row = r0 + team;
+  fetch(row);
+  for (int it = 0; row < r1; row += TM::kTeams, it ^= 1) {
+    const Row cur = next;
+    fetch(row + TM::kTeams);
+    float sg = 0.f, sgh = 0.f;
+    auto row_h = [&](int j, float (&h)[8]) {
+      if constexpr (KEPT) {
+        ckpt_values8(cur.q[j], cur.scale[j][0], cur.scale[j][1], h);
+      } else {
+        const int64_t left = left_of(j);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = (raw_value<T>(cur.x[j], e) - cur.mean) * cur.rstd;
+        if (left < kSlice) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (lane_col<LAYOUT>(lane, e) >= left) h[e] = 0.f;
+        }
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float h[8], wv[8];
+      row_h(j, h);
+      lds8<LAYOUT>(ws + (j * W + w) * kSlice, lane, wv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = raw_value<T>(cur.dy[j], e), g = d * wv[e];
+        sg += g;
+        sgh = __fmaf_rn(g, h[e], sgh);
+        dw[j][e] = __fmaf_rn(d, h[e], dw[j][e]);
+        db[j][e] += d;
+      }
     }
-    if (lane == 0) a.scales[row * ckpt_scales(a.cols) + blk] = sc.scale;
+    sg = warp_sum(sg);
+    sgh = warp_sum(sgh);
+    if constexpr (W > 1) {
+      if (lane == 0) ex[it][team][w] = make_float2(sg, sgh);
+      TM::sync(team);
+      sg = sgh = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        sg += ex[it][team][i].x;
+        sgh += ex[it][team][i].y;
+      }
+    }
+    const float mg = sg * inv_n * cur.rstd, mgh = sgh * inv_n * cur.rstd;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c0 = (j * W + w) * kSlice;
+      const int64_t left = left_of(j);
+      if (left <= 0) break;
+      float h[8], wv[8], v[8];
+      row_h(j, h);
+      lds8<LAYOUT>(ws + c0, lane, wv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = __fmaf_rn(raw_value<T>(cur.dy[j], e) * wv[e], cur.rstd, -mg) - h[e] * mgh;
+      store8<T, LAYOUT>(static_cast<T*>(a.dx) + row * a.cols + c0, left, lane, v);
+      if (KEPT && a.y != nullptr) {
+        float bv[8];
+        lds8<LAYOUT>(bs + c0, lane, bv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __fmaf_rn(h[e], wv[e], bv[e]);
+        store8<T, LAYOUT>(static_cast<T*>(a.y) + row * a.cols + c0, left, lane, v);
+      }
+    }
   }
-}
-
-// h of one element, from x or from the checkpoint.
-template <typename T>
-__device__ float norm_h(const NormGradArgs& a, int64_t row, int64_t c) {
-  if (a.codes != nullptr)
-    return ckpt_value(a.codes[row * ckpt_pitch(a.cols) + c], a.scales[row * ckpt_scales(a.cols) + c / kCkptBlock]);
-  return (widen(static_cast<const T*>(a.x)[row * a.ld_x + c]) - a.mean[row]) * a.rstd[row];
-}
-
-// grad_x: one CTA per row.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(const NormGradArgs a) {
-  pdl_enter();
-  __shared__ float red[kNormThreads / 32];
-  const int64_t row = blockIdx.x;
-  const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy;
-  float sg = 0.f, sgh = 0.f;
-  for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-    const float g = widen(dy[c]) * (a.weight ? load_any(a.weight, a.weight_dtype, c) : 1.f);
-    sg += g;
-    sgh = __fmaf_rn(g, norm_h<T>(a, row, c), sgh);
-  }
-  const float mg = block_sum(sg, red) / static_cast<float>(a.cols);
-  const float mgh = block_sum(sgh, red) / static_cast<float>(a.cols);
-  const float rstd = a.rstd[row];
-  for (int64_t c = threadIdx.x; c < a.cols; c += kNormThreads) {
-    const float w = a.weight ? load_any(a.weight, a.weight_dtype, c) : 1.f;
-    const float h = norm_h<T>(a, row, c);
-    static_cast<T*>(a.dx)[row * a.cols + c] = narrow<T>(rstd * (widen(dy[c]) * w - mg - h * mgh));
-    if (a.y != nullptr) {
-      const float b = a.bias ? load_any(a.bias, a.weight_dtype, c) : 0.f;
-      static_cast<T*>(a.y)[row * a.cols + c] = narrow<T>(__fmaf_rn(h, w, b));
+  if (a.partials == nullptr) return;
+  float* out = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+  if constexpr (TM::kTeams == 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c0 = (j * W + w) * kSlice;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = c0 + lane_col<LAYOUT>(lane, e);
+        if (c >= a.cols) continue;
+        out[c] = dw[j][e];
+        out[a.cols + c] = db[j][e];
+      }
+    }
+  } else {
+    __syncthreads();
+    float* mine = sm + team * 2 * TM::kCols;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      sts8<LAYOUT>(mine + (j * W + w) * kSlice, lane, dw[j]);
+      sts8<LAYOUT>(mine + TM::kCols + (j * W + w) * kSlice, lane, db[j]);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * TM::kCols; i += TM::kThreads) {
+      const int c = i % TM::kCols;
+      if (c >= a.cols) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int t = 0; t < TM::kTeams; ++t) s += sm[t * 2 * TM::kCols + i];
+      out[(i / TM::kCols) * a.cols + c] = s;
     }
   }
 }
 
-// Parameter gradients: 32 columns of one worker per CTA, eight rows at a time.
-template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_params_kernel(const NormGradArgs a,
-                                                                  const __grid_constant__ ParamGradArgs p) {
+// Joins the CTAs' partials of one worker: 32 columns per CTA, eight partials at a time.
+__global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant__ ParamGradArgs p) {
   pdl_enter();
-  __shared__ float red[2][8][32];
+  __shared__ float red[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = blockIdx.y;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  float sw = 0.f, sb = 0.f;
-  if (c < a.cols)
-    for (int64_t row = p.off[k] + warp; row < p.off[k + 1]; row += 8) {
-      const float d = widen(static_cast<const T*>(a.dy)[row * a.ld_dy + c]);
-      sw = __fmaf_rn(d, norm_h<T>(a, row, c), sw);
-      sb += d;
-    }
-  red[0][warp][lane] = sw;
-  red[1][warp][lane] = sb;
-  __syncthreads();
-  if (warp >= 2 || c >= a.cols || !(warp ? p.want_b : p.want_w)) return;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane;  // weight columns, then bias columns
   float s = 0.f;
-  for (int i = 0; i < 8; ++i) s += red[warp][i][lane];
-  void* out = warp ? p.db[k] : p.dw[k];
+  if (i < 2 * p.cols) {
+#pragma unroll 4
+    for (int c = p.cta_off[k] + warp; c < p.cta_off[k + 1]; c += 8) s += p.partials[c * 2 * p.cols + i];
+  }
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp > 0 || i >= 2 * p.cols) return;
+  void* out = i < p.cols ? p.dw[k] : p.db[k];
+  if (out == nullptr) return;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) s += red[j][lane];
+  const int64_t c = i < p.cols ? i : i - p.cols;
   if (p.accumulate) s += load_any(out, p.dtype, c);
   store_any(out, p.dtype, c, s);
 }
 
-template <typename T>
+// Allows a kernel its shared memory where that is more than the default.
+int allow_smem(const void* kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ? 0
+                            : static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                    static_cast<int>(bytes)));
+}
+
+template <typename T, int LAYOUT, int W, int NV>
+int launch_norm_as(const NormArgs& a, cudaStream_t stream) {
+  using TM = Team<W, NV>;
+  const size_t smem = 2 * TM::kCols * sizeof(float);
+  auto kernel = a.codes ? norm_kernel<T, LAYOUT, W, NV, true> : norm_kernel<T, LAYOUT, W, NV, false>;
+  if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem)) return rc;
+  const int64_t need = (a.rows + TM::kTeams - 1) / TM::kTeams;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(4) * sm_count()));
+  return launch_pdl(kernel, dim3(grid), dim3(TM::kThreads), smem, stream, a);
+}
+// The smallest team that holds a row: up to four slices a warp, then more warps.
+template <typename T, int LAYOUT>
 int launch_norm(const NormArgs& a, cudaStream_t stream) {
-  return launch_pdl(norm_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(kNormThreads), 0, stream, a);
+  const int64_t slices = (a.cols + kSlice - 1) / kSlice;
+  if (slices <= 1) return launch_norm_as<T, LAYOUT, 1, 1>(a, stream);
+  if (slices <= 2) return launch_norm_as<T, LAYOUT, 1, 2>(a, stream);
+  if (slices <= 4) return launch_norm_as<T, LAYOUT, 1, 4>(a, stream);
+  if (slices <= 8) return launch_norm_as<T, LAYOUT, 2, 4>(a, stream);
+  if (slices <= 16) return launch_norm_as<T, LAYOUT, 4, 4>(a, stream);
+  if (slices <= 32) return launch_norm_as<T, LAYOUT, 8, 4>(a, stream);
+  return launch_norm_as<T, LAYOUT, 16, 4>(a, stream);
 }
-template <typename T>
-int launch_norm_grad(const NormGradArgs& a, cudaStream_t stream) {
-  return launch_pdl(norm_grad_kernel<T>, dim3(static_cast<unsigned>(a.rows)), dim3(kNormThreads), 0, stream, a);
+
+template <typename T, int LAYOUT, int W, int NV>
+int launch_norm_grad_as(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
+  using TM = Team<W, NV>;
+  const size_t smem = (TM::kTeams == 1 ? 1 : TM::kTeams) * 2 * TM::kCols * sizeof(float);
+  auto kernel = a.codes ? norm_grad_kernel<T, LAYOUT, W, NV, true> : norm_grad_kernel<T, LAYOUT, W, NV, false>;
+  if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem)) return rc;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(rows.cta_off[rows.K])), dim3(TM::kThreads), smem, stream, a, rows);
 }
-template <typename T>
-int launch_norm_params(const NormGradArgs& a, const ParamGradArgs& p, cudaStream_t stream) {
-  return launch_pdl(norm_params_kernel<T>, dim3(static_cast<unsigned>((a.cols + 31) / 32), p.K), dim3(kNormThreads), 0,
-                    stream, a, p);
+// Teams of the gradient kernel: two slices a warp, since each costs 16 registers of sums.
+int grad_teams(int64_t cols) {
+  const int64_t slices = (cols + kSlice - 1) / kSlice;
+  return slices <= 2 ? 8 : slices <= 4 ? 4 : slices <= 8 ? 2 : 1;
+}
+template <typename T, int LAYOUT>
+int launch_norm_grad(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
+  const int64_t slices = (a.cols + kSlice - 1) / kSlice;
+  if (slices <= 1) return launch_norm_grad_as<T, LAYOUT, 1, 1>(a, rows, stream);
+  if (slices <= 2) return launch_norm_grad_as<T, LAYOUT, 1, 2>(a, rows, stream);
+  if (slices <= 4) return launch_norm_grad_as<T, LAYOUT, 2, 2>(a, rows, stream);
+  if (slices <= 8) return launch_norm_grad_as<T, LAYOUT, 4, 2>(a, rows, stream);
+  if (slices <= 16) return launch_norm_grad_as<T, LAYOUT, 8, 2>(a, rows, stream);
+  if (slices <= 32) return launch_norm_grad_as<T, LAYOUT, 16, 2>(a, rows, stream);
+  return launch_norm_grad_as<T, LAYOUT, 16, 4>(a, rows, stream);
+}
+
+// Deals the workers' rows to at most about `target` CTAs, none of them to two workers.
+void deal_rows(WorkerRows& r, const int64_t* offs, int K, int teams, int target) {
+  r.K = K;
+  for (int k = 0; k <= K; ++k) r.off[k] = offs[k];
+  const int64_t rows = offs[K];
+  int64_t per = std::max<int64_t>(teams, (rows + target - 1) / target);
+  for (;;) {
+    per = (per + teams - 1) / teams * teams;
+    int64_t ctas = 0;
+    for (int k = 0; k < K; ++k) {
+      ctas += (offs[k + 1] - offs[k] + per - 1) / per;
+      r.cta_off[k + 1] = static_cast<int>(ctas);
+    }
+    if (ctas <= target || per >= rows) break;
+    per += std::max<int64_t>(1, per / 16);
+  }
+  r.rows_per_cta = static_cast<int>(std::min<int64_t>(per, INT32_MAX));
 }
 
 // Size and type checks shared by the norm entry points.
@@ -206,6 +481,7 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
   const int64_t need = adasum_layer_norm_backward_scratch_bytes(a.rows, a.cols, K);
   if (want && need > 0 && (scratch == nullptr || scratch_bytes < need || !is_aligned(scratch, 256)))
     return ADASUM_ERR_INVALID_ARG;
+  WorkerRows rows = {};
   ParamGradArgs p = {};
   BufferSet set;
   set.read(a.dy, span_bytes(a.rows, a.cols, a.ld_dy, e));
@@ -223,7 +499,6 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
   set.write(a.y, a.rows * a.cols * e);
   if (want) set.write(scratch, need);
   for (int k = 0; k < K; ++k) {
-    p.off[k + 1] = offs[k + 1];
     if (dw != nullptr) {
       if (dw[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
       set.write(p.dw[k] = dw[k], a.cols * ge);
@@ -234,21 +509,27 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
     }
   }
   if (set.conflict()) return ADASUM_ERR_ALIAS;
-  p.K = K;
-  p.dtype = grad_dtype;
-  p.accumulate = accumulate != 0;
-  p.want_w = dw != nullptr;
-  p.want_b = db != nullptr;
   const double n = static_cast<double>(a.rows) * a.cols;
+  deal_rows(rows, offs, K, grad_teams(a.cols), kNormCtasPerSm * sm_count());
+  const bool vec = is_aligned(a.dy, 16) && is_aligned(a.dx, 16) && is_aligned(a.y, 16) && a.ld_dy * e % 16 == 0 &&
+                   a.cols * e % 16 == 0 && (kept || (is_aligned(a.x, 16) && a.ld_x * e % 16 == 0));
+  a.partials = want ? static_cast<float*>(scratch) : nullptr;
   if (a.rows > 0)
     if (adasum_status_t st = counted_launch(stream, kept ? "norm_grad_checkpoint" : "norm_grad",
-                                            n * (kept ? 2 * e + 1 : 3 * e), [&] {
-          return dtype == kBF16 ? launch_norm_grad<bf16>(a, stream) : launch_norm_grad<float>(a, stream);
+                                            n * (kept ? 2 * e + 1 + (a.y ? e : 0) : 3 * e), [&] {
+          if (dtype == kBF16)
+            return vec ? launch_norm_grad<bf16, kVec>(a, rows, stream) : launch_norm_grad<bf16, kStrided>(a, rows, stream);
+          return vec ? launch_norm_grad<float, kVec>(a, rows, stream) : launch_norm_grad<float, kStrided>(a, rows, stream);
         }))
       return st;
   if (!want) return ADASUM_OK;
+  p.partials = a.partials;
+  p.cols = a.cols;
+  p.dtype = grad_dtype;
+  p.accumulate = accumulate != 0;
+  std::copy(rows.cta_off, rows.cta_off + K + 1, p.cta_off);
   return counted_launch(stream, "norm_params", 0.0, [&] {
-    return dtype == kBF16 ? launch_norm_params<bf16>(a, p, stream) : launch_norm_params<float>(a, p, stream);
+    return launch_pdl(norm_params_kernel, dim3(static_cast<unsigned>((2 * a.cols + 31) / 32), K), dim3(256), 0, stream, p);
   });
 }
 
@@ -281,17 +562,19 @@ adasum_status_t adasum_layer_norm(const void* x, int64_t rows, int64_t cols, int
   set.write(scales, rows * ckpt_scales(cols) * 4);
   if (set.conflict()) return ADASUM_ERR_ALIAS;
   const NormArgs a = {x, rows, cols, ld, weight, bias, static_cast<int>(weight_dtype), eps, y, mean, rstd, codes, scales};
+  const bool vec = is_aligned(x, 16) && is_aligned(y, 16) && ld * e % 16 == 0 && cols * e % 16 == 0;
   const double n = static_cast<double>(rows) * cols;
   return counted_launch(stream, codes ? "norm_checkpoint" : "norm", n * (2 * e + (codes ? 1 : 0)), [&] {
-    return dtype == ADASUM_BF16 ? launch_norm<bf16>(a, stream) : launch_norm<float>(a, stream);
+    if (dtype == ADASUM_BF16) return vec ? launch_norm<bf16, kVec>(a, stream) : launch_norm<bf16, kStrided>(a, stream);
+    return vec ? launch_norm<float, kVec>(a, stream) : launch_norm<float, kStrided>(a, stream);
   });
 }
 
 int64_t adasum_layer_norm_backward_scratch_bytes(int64_t rows, int64_t cols, int K) {
-  (void)rows;
-  (void)cols;
-  (void)K;
-  return 0;
+  if (rows <= 0 || cols <= 0 || K <= 0) return 0;
+  // one partial per CTA: the persistent grid, or one CTA for every worker
+  const int64_t ctas = std::min<int64_t>(rows, kNormCtasPerSm * sm_count() + static_cast<int64_t>(K));
+  return (ctas * 2 * cols * 4 + 255) / 256 * 256;
 }
 
 adasum_status_t adasum_layer_norm_backward(const void* grad_out, int64_t ld_grad, const void* x, int64_t ld_x,
