@@ -278,27 +278,45 @@ __device__ __forceinline__ void store_codes8(int8_t* p, int64_t left, int lane, 
   }
 }
 
-// Scales of the (one or two) blocks that a lane's eight of 256 columns lie in, from all the
-// lanes' values; columns past the row's end hold 0.  kVec: a block is half a warp; kStrided:
-// a block is four values of every lane.
+// Largest magnitudes of the (one or two) blocks that a lane's eight of 256 columns lie in,
+// from all the lanes' values (NaN if there is one); columns past the row's end hold 0.
+// kVec: a block is half a warp; kStrided: a block is four values of every lane.
 template <int LAYOUT>
-__device__ __forceinline__ void ckpt_scales8(const float (&v)[8], CkptScale (&s)[2]) {
-  const float inf = __int_as_float(0x7F800000);
-  float top[2];
+__device__ __forceinline__ void block_tops(const float (&v)[8], float (&top)[2]) {
   top[0] = max_abs_nan(max_abs_nan(v[0], v[1], v[2]), v[3], v[3]);
   top[1] = max_abs_nan(max_abs_nan(v[4], v[5], v[6]), v[7], v[7]);
   if constexpr (LAYOUT == kVec) {
     top[0] = max_nan(top[0], top[1]);
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) top[0] = max_nan(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], d));
-    s[0] = s[1] = ckpt_scale(top[0], !(top[0] < inf));
+    top[1] = top[0];
   } else {
+    // (magnitudes as integers are ordered like the values, with NaN above infinity)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      // (magnitudes as integers are ordered like the values, with NaN above infinity)
+    for (int b = 0; b < 2; ++b)
       top[b] = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top[b])));
-      s[b] = ckpt_scale(top[b], !(top[b] < inf));
-    }
+  }
+}
+
+// Scales of the blocks of N slices of 256 columns, from block_tops.  The two quotients cost
+// more than the codes of a lane's eight values, so each lane computes those of one slice
+// (and, with kStrided, one block) and the others take them from it.
+template <int LAYOUT, int N>
+__device__ __forceinline__ void block_scales(const float (&top)[N][2], int lane, CkptScale (&s)[N][2]) {
+  constexpr int kJobs = LAYOUT == kVec ? N : 2 * N;
+  static_assert(kJobs <= 16, "one lane of a half warp per scale");
+  float mine = top[0][0];
+#pragma unroll
+  for (int j = 1; j < kJobs; ++j)
+    if ((lane & 15) == j) mine = LAYOUT == kVec ? top[j][0] : top[j >> 1][j & 1];
+  const CkptScale r = ckpt_scale(mine, !(mine < __int_as_float(0x7F800000)));
+#pragma unroll
+  for (int j = 0; j < kJobs; ++j) {
+    const int from = (lane & 16) | j;
+    CkptScale& to = LAYOUT == kVec ? s[j][0] : s[j >> 1][j & 1];
+    to.scale = __shfl_sync(0xFFFFFFFFu, r.scale, from);
+    to.inv = __shfl_sync(0xFFFFFFFFu, r.inv, from);
+    if (LAYOUT == kVec) s[j][1] = to;
   }
 }
 // Stores the scales of 256 columns, of which `left` exist, at p.

@@ -112,36 +112,52 @@ struct UnpackArgs {
 // before it works on the first.  Bound by bytes: each value is read and written once.
 struct Slice {
   int64_t row, c0;
+  __device__ __forceinline__ Slice(uint32_t item, uint32_t slices) {
+    const uint32_t r = item / slices;
+    row = r;
+    c0 = static_cast<int64_t>(item - r * slices) * kSlice;
+  }
+  __device__ __forceinline__ void next(int64_t cols) {
+    c0 += kSlice;
+    if (c0 >= cols) {
+      c0 = 0;
+      ++row;
+    }
+  }
 };
-__device__ __forceinline__ Slice slice_of(uint32_t item, uint32_t slices) {
-  const uint32_t row = item / slices;
-  return {static_cast<int64_t>(row), static_cast<int64_t>(item - row * slices) * kSlice};
-}
 
 template <typename T, int ACT, int LAYOUT>
 __global__ void __launch_bounds__(kCkptThreads) pack_kernel(const PackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
+  if (first >= a.items) return;
+  const Slice begin(first, a.slices);
   Raw8<T> r[kItems];
+  Slice s = begin;
+#pragma unroll
+  for (int i = 0; i < kItems; ++i, s.next(a.cols))
+    r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.row * a.ld + s.c0, first + i < a.items ? a.cols - s.c0 : 0, lane);
+  float top[kItems][2];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
-    if (first + i >= a.items) break;
-    const Slice s = slice_of(first + i, a.slices);
-    r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.row * a.ld + s.c0, a.cols - s.c0, lane);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = raw_value<T>(r[i], e);
+    block_tops<LAYOUT>(v, top[i]);
   }
+  CkptScale sc[kItems][2];
+  block_scales<LAYOUT, kItems>(top, lane, sc);
+  s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
+  for (int i = 0; i < kItems; ++i, s.next(a.cols)) {
     if (first + i >= a.items) break;
-    const Slice s = slice_of(first + i, a.slices);
     const int64_t left = a.cols - s.c0;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = raw_value<T>(r[i], e);
-    CkptScale sc[2];
-    ckpt_scales8<LAYOUT>(v, sc);
-    store_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, left, lane, ckpt_codes<LAYOUT>(v, sc));
-    store_scales<LAYOUT>(a.scales + s.row * a.nscales + s.c0 / kCkptBlock, left, lane, sc);
+    store_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, left, lane, ckpt_codes<LAYOUT>(v, sc[i]));
+    store_scales<LAYOUT>(a.scales + s.row * a.nscales + s.c0 / kCkptBlock, left, lane, sc[i]);
     if constexpr (ACT != kActNone) {
       float y[8];
 #pragma unroll
@@ -162,20 +178,21 @@ __global__ void __launch_bounds__(kCkptThreads) unpack_kernel(const UnpackArgs a
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
+  if (first >= a.items) return;
+  const Slice begin(first, a.slices);
   uint2 q[kItems];
   Raw8<T> r[kItems];
+  Slice s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    if (first + i >= a.items) break;
-    const Slice s = slice_of(first + i, a.slices);
-    q[i] = load_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, a.cols - s.c0, lane);
-    if constexpr (ACT != kActNone)
-      r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.row * a.ld_dy + s.c0, a.cols - s.c0, lane);
+  for (int i = 0; i < kItems; ++i, s.next(a.cols)) {
+    const int64_t left = first + i < a.items ? a.cols - s.c0 : 0;
+    q[i] = load_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, left, lane);
+    if constexpr (ACT != kActNone) r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.row * a.ld_dy + s.c0, left, lane);
   }
+  s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
+  for (int i = 0; i < kItems; ++i, s.next(a.cols)) {
     if (first + i >= a.items) break;
-    const Slice s = slice_of(first + i, a.slices);
     const int64_t left = a.cols - s.c0, at = s.row * a.cols + s.c0;
     float v[8];
     ckpt_values<LAYOUT>(q[i], a.scales + s.row * a.nscales + s.c0 / kCkptBlock, left, lane, v);

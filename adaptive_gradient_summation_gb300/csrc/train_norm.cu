@@ -8,6 +8,15 @@ namespace adasum {
 namespace {
 
 constexpr int kSlice = 256;        // columns of a warp's eight per lane
+#ifndef NV_F
+#define NV_F 4
+#endif
+#ifndef CTA_F
+#define CTA_F 4
+#endif
+#ifndef OCC_F
+#define OCC_F 1
+#endif
 constexpr int kNormCtasPerSm = 2;  // of the persistent grids
 
 struct NormArgs {
@@ -90,7 +99,7 @@ __device__ __forceinline__ void stage_params(float* w, float* b, const void* wei
 //     mean = sum n_w m_w / n,   S = sum S_w + n_w (m_w - mean)^2.
 // Bound by the bytes of x and y; the next row is on its way while one is worked on.
 template <typename T, int LAYOUT, int W, int NV, bool KEEP>
-__global__ void __launch_bounds__(Team<W, NV>::kThreads) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? OCC_F : 1) norm_kernel(const NormArgs a) {
   using TM = Team<W, NV>;
   pdl_enter();
   extern __shared__ __align__(16) float sm[];
@@ -166,24 +175,36 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads) norm_kernel(const NormA
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
+    auto row_h = [&](int j, float (&h)[8]) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[e] = (raw_value<T>(r[j], e) - mean) * rstd;
+      if (KEEP && left_of(j) < kSlice) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (lane_col<LAYOUT>(lane, e) >= left_of(j)) h[e] = 0.f;
+      }
+    };
+    CkptScale sc[KEEP ? NV : 1][2];
+    if constexpr (KEEP) {
+      float top[NV][2];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float h[8];
+        row_h(j, h);
+        block_tops<LAYOUT>(h, top[j]);
+      }
+      block_scales<LAYOUT, NV>(top, lane, sc);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c0 = (j * W + w) * kSlice;
       const int64_t left = left_of(j);
       if (left <= 0) break;
       float h[8], wv[8], bv[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = (raw_value<T>(r[j], e) - mean) * rstd;
+row_h(j, h);
       if constexpr (KEEP) {
-        if (left < kSlice) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (lane_col<LAYOUT>(lane, e) >= left) h[e] = 0.f;
-        }
-        CkptScale sc[2];
-        ckpt_scales8<LAYOUT>(h, sc);
-        store_codes8<LAYOUT>(a.codes + row * pitch + c0, left, lane, ckpt_codes<LAYOUT>(h, sc));
-        store_scales<LAYOUT>(a.scales + row * nscales + c0 / kCkptBlock, left, lane, sc);
+        store_codes8<LAYOUT>(a.codes + row * pitch + c0, left, lane, ckpt_codes<LAYOUT>(h, sc[j]));
+        store_scales<LAYOUT>(a.scales + row * nscales + c0 / kCkptBlock, left, lane, sc[j]);
       }
       lds8<LAYOUT>(ws + c0, lane, wv);
       lds8<LAYOUT>(bs + c0, lane, bv);
@@ -395,13 +416,14 @@ int launch_norm_as(const NormArgs& a, cudaStream_t stream) {
   auto kernel = a.codes ? norm_kernel<T, LAYOUT, W, NV, true> : norm_kernel<T, LAYOUT, W, NV, false>;
   if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem)) return rc;
   const int64_t need = (a.rows + TM::kTeams - 1) / TM::kTeams;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(4) * sm_count()));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(CTA_F) * sm_count()));
   return launch_pdl(kernel, dim3(grid), dim3(TM::kThreads), smem, stream, a);
 }
 // The smallest team that holds a row: up to four slices a warp, then more warps.
 template <typename T, int LAYOUT>
 int launch_norm(const NormArgs& a, cudaStream_t stream) {
   const int64_t slices = (a.cols + kSlice - 1) / kSlice;
+#if NV_F == 4
   if (slices <= 1) return launch_norm_as<T, LAYOUT, 1, 1>(a, stream);
   if (slices <= 2) return launch_norm_as<T, LAYOUT, 1, 2>(a, stream);
   if (slices <= 4) return launch_norm_as<T, LAYOUT, 1, 4>(a, stream);
@@ -409,6 +431,23 @@ int launch_norm(const NormArgs& a, cudaStream_t stream) {
   if (slices <= 16) return launch_norm_as<T, LAYOUT, 4, 4>(a, stream);
   if (slices <= 32) return launch_norm_as<T, LAYOUT, 8, 4>(a, stream);
   return launch_norm_as<T, LAYOUT, 16, 4>(a, stream);
+#elif NV_F == 2
+  if (slices <= 1) return launch_norm_as<T, LAYOUT, 1, 1>(a, stream);
+  if (slices <= 2) return launch_norm_as<T, LAYOUT, 1, 2>(a, stream);
+  if (slices <= 4) return launch_norm_as<T, LAYOUT, 2, 2>(a, stream);
+  if (slices <= 8) return launch_norm_as<T, LAYOUT, 4, 2>(a, stream);
+  if (slices <= 16) return launch_norm_as<T, LAYOUT, 8, 2>(a, stream);
+  if (slices <= 32) return launch_norm_as<T, LAYOUT, 16, 2>(a, stream);
+  return launch_norm_as<T, LAYOUT, 16, 4>(a, stream);
+#else
+  if (slices <= 1) return launch_norm_as<T, LAYOUT, 1, 1>(a, stream);
+  if (slices <= 2) return launch_norm_as<T, LAYOUT, 2, 1>(a, stream);
+  if (slices <= 4) return launch_norm_as<T, LAYOUT, 4, 1>(a, stream);
+  if (slices <= 8) return launch_norm_as<T, LAYOUT, 8, 1>(a, stream);
+  if (slices <= 16) return launch_norm_as<T, LAYOUT, 8, 2>(a, stream);
+  if (slices <= 32) return launch_norm_as<T, LAYOUT, 16, 2>(a, stream);
+  return launch_norm_as<T, LAYOUT, 16, 4>(a, stream);
+#endif
 }
 
 template <typename T, int LAYOUT, int W, int NV>

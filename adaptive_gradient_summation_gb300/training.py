@@ -17,7 +17,7 @@ on that stream, so calls on several streams may overlap and may be captured.
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
 from typing import NamedTuple
 
 import torch
@@ -29,6 +29,12 @@ __all__ = ["Checkpoint", "checkpoint_pack", "checkpoint_unpack", "embedding", "e
            "layer_norm_checkpointed", "layer_norm_checkpointed_backward"]
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
+_DEVICES = [torch.device("cuda", i) for i in range(128)]
+_TOKEN_BYTES = {torch.int32: 4, torch.int64: 8}
+# A small call is bound by the host, so the checks below use torch's cheapest accessors:
+# on a Grace host torch.cuda.current_stream() takes 2.0 us, the raw handle 0.08 us.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 #: Columns per scale of a checkpoint.
 BLOCK = 128
 
@@ -45,42 +51,39 @@ class Checkpoint(NamedTuple):
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-class _On:
-    """Makes a device and a stream current where they are not yet."""
-
-    def __init__(self, device, stream):
-        self.stack = []
-        if device.index != torch.cuda.current_device():
-            self.stack.append(torch.cuda.device(device))
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.stack.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for s in self.stack:
-            s.__enter__()
-
-    def __exit__(self, *exc):
-        while self.stack:
-            self.stack.pop().__exit__(*exc)
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a device or a stream has to be made current before the launch."""
+    return stream is not None or index != torch.cuda.current_device()
 
 
-def _float_tensor(t, what: str) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what} must be a tensor, got {type(t).__name__}")
-    if t.dtype not in _CODE:
-        raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
-    if t.device.type != "cuda":
+def _there(index: int, stream, call, *args, **more):
+    """`call` again, with device `index` and `stream` current."""
+    if stream is None:
+        with torch.cuda.device(index):
+            return call(*args, **more)
+    if stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return call(*args, **more)
+
+
+def _code(t, what: str) -> int:
+    """The type code of a float32 or bfloat16 CUDA tensor."""
+    try:
+        code = _CODE[t.dtype]
+    except (AttributeError, KeyError):
+        raise TypeError(f"{what} must be a float32 or bfloat16 tensor, got {getattr(t, 'dtype', type(t).__name__)}") from None
+    if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    return t
+    return code
 
 
 def _rows(t: torch.Tensor, what: str):
     """(rows, cols, row stride) of an activation whose leading dimensions flatten."""
-    if t.dim() < 1 or t.shape[-1] == 0:
+    shape = t.shape
+    if len(shape) < 1 or shape[-1] == 0:
         raise ValueError(f"{what} must have a last dimension of at least one column")
-    cols = t.shape[-1]
+    cols = shape[-1]
     if t.is_contiguous():
         return t.numel() // cols, cols, cols
     if t.numel() == 0:
@@ -88,7 +91,7 @@ def _rows(t: torch.Tensor, what: str):
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what} must have its columns next to each other")
     n, ld = 1, None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if ld is None:
@@ -102,90 +105,93 @@ def _rows(t: torch.Tensor, what: str):
     return n, cols, ld
 
 
-def _same(t: torch.Tensor, like: torch.Tensor, what: str) -> None:
-    if t.dtype != like.dtype or t.device != like.device or t.shape != like.shape:
-        raise ValueError(f"{what} must have shape {tuple(like.shape)}, {like.dtype}, on {like.device}")
-
-
-def _output(out, like: torch.Tensor, shape, what: str = "out") -> torch.Tensor:
+def _output(out, shape, dtype, index: int) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-    if (not isinstance(out, torch.Tensor) or out.dtype != like.dtype or out.device != like.device
+        return torch.empty(shape, dtype=dtype, device=_DEVICES[index])
+    if (not isinstance(out, torch.Tensor) or out.dtype != dtype or out.get_device() != index
             or out.shape != torch.Size(shape) or not out.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous {like.dtype} tensor of shape {tuple(shape)} on {like.device}")
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
     return out
 
 
-def _parameter(p, cols: int, device, what: str):
-    """(pointer, dtype) of a weight or bias; None is allowed."""
-    if p is None:
-        return None, None
-    _float_tensor(p, what)
-    if p.device != device or p.numel() != cols or not p.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous tensor of {cols} elements on {device}")
-    return p.data_ptr(), p.dtype
+def _like(t: torch.Tensor) -> torch.Tensor:
+    """A new dense tensor of t's shape, type and device."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _parameters(weight, bias, cols: int, device):
-    w, wt = _parameter(weight, cols, device, "weight")
-    b, bt = _parameter(bias, cols, device, "bias")
-    if wt is not None and bt is not None and wt != bt:
-        raise ValueError("weight and bias must share their dtype")
-    return w, b, _CODE[wt or bt or torch.float32]
+def _parameters(weight, bias, cols: int, index: int):
+    """(weight's pointer, bias's, the code of their type); either may be None."""
+    w = b = code = None
+    if weight is not None:
+        code = _code(weight, "weight")
+        if weight.get_device() != index or weight.numel() != cols or not weight.is_contiguous():
+            raise ValueError(f"weight must be a contiguous tensor of {cols} elements on cuda:{index}")
+        w = weight.data_ptr()
+    if bias is not None:
+        c = _code(bias, "bias")
+        if bias.get_device() != index or bias.numel() != cols or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous tensor of {cols} elements on cuda:{index}")
+        if code is not None and c != code:
+            raise ValueError("weight and bias must share their dtype")
+        b, code = bias.data_ptr(), c
+    return w, b, code or 0
 
 
-def _statistic(t, rows: int, device, what: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != device or t.numel() != rows \
+def _statistic(t, rows: int, index: int, what: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.get_device() != index or t.numel() != rows \
             or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous float32 tensor of {rows} elements on {device}")
+        raise ValueError(f"{what} must be a contiguous float32 tensor of {rows} elements on cuda:{index}")
     return t.data_ptr()
 
 
 def _workers(worker_offsets, rows: int):
-    """(ctypes array of K+1 offsets, K)."""
+    """(K+1 offsets, K)."""
     if worker_offsets is None:
-        return (ctypes.c_int64 * 2)(0, rows), 1
-    if isinstance(worker_offsets, torch.Tensor):
-        worker_offsets = worker_offsets.tolist()
-    offs = [int(o) for o in worker_offsets]
+        return array("q", (0, rows)), 1
+    offs = array("q", worker_offsets.tolist() if isinstance(worker_offsets, torch.Tensor) else worker_offsets)
     if len(offs) < 2 or offs[-1] != rows:
         raise ValueError(f"worker_offsets must be K+1 offsets ending at the row count {rows}")
-    return (ctypes.c_int64 * len(offs))(*offs), len(offs) - 1
+    return offs, len(offs) - 1
 
 
-def _gradients(grads, K: int, numel: int, device, dtype, shape, what: str):
-    """(list of K tensors, ctypes array of their pointers, their dtype); None allocates."""
+def _gradients(grads, K: int, numel: int, index: int, dtype, shape, what: str):
+    """(list of K tensors, their pointers, the code of their type); None allocates them."""
     if grads is None:
-        grads = list(torch.empty((K, *shape), dtype=dtype, device=device).unbind(0))
+        grads = list(torch.empty((K, *shape), dtype=dtype, device=_DEVICES[index]).unbind(0))
     elif isinstance(grads, torch.Tensor):
         grads = [grads] if K == 1 and grads.numel() == numel else list(grads.unbind(0))
     else:
         grads = list(grads)
     if len(grads) != K:
         raise ValueError(f"{what} must be one tensor for each of the {K} workers, got {len(grads)}")
+    code = _code(grads[0], what)
     dtype = grads[0].dtype
+    ptrs = array("Q")
     for g in grads:
-        _float_tensor(g, what)
-        if g.dtype != dtype or g.device != device or g.numel() != numel or not g.is_contiguous():
-            raise ValueError(f"{what} must be contiguous tensors of {numel} elements and one dtype on {device}")
-    return grads, (ctypes.c_void_p * K)(*[g.data_ptr() for g in grads]), dtype
+        if not isinstance(g, torch.Tensor) or g.dtype != dtype or g.get_device() != index or g.numel() != numel \
+                or not g.is_contiguous():
+            raise ValueError(f"{what} must be contiguous tensors of {numel} elements and one dtype on cuda:{index}")
+        ptrs.append(g.data_ptr())
+    return grads, ptrs, code
 
 
-def _current_stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _address(a) -> int | None:
+    """Of an array's elements; the library copies them before a call returns."""
+    return None if a is None else a.buffer_info()[0]
 
 
-def _tokens(tokens, device, what: str = "tokens") -> int:
-    if not isinstance(tokens, torch.Tensor) or tokens.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"{what} must be an int32 or int64 tensor")
-    if tokens.device != device or not tokens.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous tensor on {device}")
-    return tokens.element_size()
+def _tokens(tokens, index: int) -> int:
+    width = _TOKEN_BYTES.get(getattr(tokens, "dtype", None))
+    if width is None:
+        raise TypeError("tokens must be an int32 or int64 tensor")
+    if tokens.get_device() != index or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous tensor on cuda:{index}")
+    return width
 
 
-def _scratch(nbytes: int, device):
+def _scratch(nbytes: int, index: int):
     """Scratch memory of one call, from torch's allocator on the current stream."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes > 0 else None
+    return torch.empty(nbytes, dtype=torch.uint8, device=_DEVICES[index]) if nbytes > 0 else None
 
 
 def _ptr(t):
@@ -200,17 +206,18 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0, 
     """``scale * table[tokens]`` (``adasum_embedding``), of shape ``(*tokens.shape, cols)`` in
     the table's dtype.  A token outside the table (the -1 that marks padding) gives zeros.
     tokens: int32 or int64."""
-    _float_tensor(table, "table")
+    code, index = _code(table, "table"), table.get_device()
     if table.dim() != 2 or table.shape[1] == 0 or not table.is_contiguous():
         raise ValueError("table must be a contiguous matrix")
-    device = table.device
-    width = _tokens(tokens, device)
-    with _On(device, stream):
-        out = _output(out, table, (*tokens.shape, table.shape[1]))
-        st = load_library().adasum_embedding(
-            table.data_ptr(), table.shape[0], table.shape[1], _CODE[table.dtype], tokens.data_ptr(), width,
-            tokens.numel(), float(scale), out.data_ptr(), _current_stream(device))
-    check(st, "adasum_embedding")
+    width = _tokens(tokens, index)
+    if _elsewhere(index, stream):
+        return _there(index, stream, embedding, table, tokens, scale=scale, out=out)
+    rows, cols = table.shape
+    out = _output(out, (*tokens.shape, cols), table.dtype, index)
+    st = load_library().adasum_embedding(table.data_ptr(), rows, cols, code, tokens.data_ptr(), width, tokens.numel(),
+                                         float(scale), out.data_ptr(), _raw_stream(index))
+    if st:
+        check(st, "adasum_embedding")
     return out
 
 
@@ -226,9 +233,8 @@ def embedding_backward(grad_output: torch.Tensor, tokens: torch.Tensor, num_rows
     grad_output's), overwritten whole, or with ``accumulate`` added to.  Tokens outside the
     table and ``padding_idx`` get no gradient.
     """
-    _float_tensor(grad_output, "grad_output")
-    device = grad_output.device
-    width = _tokens(tokens, device)
+    code, index = _code(grad_output, "grad_output"), grad_output.get_device()
+    width = _tokens(tokens, index)
     rows, cols, ld = _rows(grad_output, "grad_output")
     if grad_output.shape[:-1] != tokens.shape:
         raise ValueError(f"grad_output must have shape {(*tokens.shape, cols)}")
@@ -236,49 +242,43 @@ def embedding_backward(grad_output: torch.Tensor, tokens: torch.Tensor, num_rows
         raise ValueError("num_rows must not be negative")
     if grads is None and accumulate:
         raise ValueError("accumulate needs grads to add to")
+    if _elsewhere(index, stream):
+        return _there(index, stream, embedding_backward, grad_output, tokens, num_rows, scale=scale,
+                      worker_offsets=worker_offsets, padding_idx=padding_idx, grads=grads, accumulate=accumulate)
     offs, K = _workers(worker_offsets, rows)
+    grads, ptrs, gcode = _gradients(grads, K, num_rows * cols, index, grad_output.dtype, (num_rows, cols), "grads")
     lib = load_library()
-    with _On(device, stream):
-        grads, ptrs, gtype = _gradients(grads, K, num_rows * cols, device, grad_output.dtype, (num_rows, cols), "grads")
-        nbytes = lib.adasum_embedding_backward_scratch_bytes(rows, cols, K)
-        scratch = _scratch(nbytes, device)
-        st = lib.adasum_embedding_backward(
-            grad_output.data_ptr(), cols, ld, _CODE[grad_output.dtype], tokens.data_ptr(), width, offs, K, num_rows,
-            float(scale), -1 if padding_idx is None else int(padding_idx), ptrs, _CODE[gtype], bool(accumulate),
-            _ptr(scratch), nbytes, _current_stream(device))
-    check(st, "adasum_embedding_backward")
+    nbytes = lib.adasum_embedding_backward_scratch_bytes(rows, cols, K)
+    scratch = _scratch(nbytes, index)
+    st = lib.adasum_embedding_backward(
+        grad_output.data_ptr(), cols, ld, code, tokens.data_ptr(), width, _address(offs), K, num_rows, float(scale),
+        -1 if padding_idx is None else padding_idx, _address(ptrs), gcode, bool(accumulate), _ptr(scratch), nbytes,
+        _raw_stream(index))
+    if st:
+        check(st, "adasum_embedding_backward")
     return grads
 
 
 # ---------------------------------------------------------------------------- layer norm
 
 
-def _norm_forward(x, weight, bias, eps, out, stream, kept: bool):
-    _float_tensor(x, "x")
-    device = x.device
-    rows, cols, ld = _rows(x, "x")
-    w, b, wcode = _parameters(weight, bias, cols, device)
-    with _On(device, stream):
-        y = _output(out, x, x.shape)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-        if kept:
-            mean, saved = None, _new_checkpoint(x, rows, cols)
-            codes, scales = saved.codes.data_ptr(), saved.scales.data_ptr()
-        else:
-            mean, codes, scales = torch.empty_like(rstd), None, None
-            saved = mean
-        st = load_library().adasum_layer_norm(
-            x.data_ptr(), rows, cols, ld, _CODE[x.dtype], w, b, wcode, float(eps), y.data_ptr(), _ptr(mean),
-            rstd.data_ptr(), codes, scales, _current_stream(device))
-    check(st, "adasum_layer_norm")
-    return y, saved, rstd
-
-
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
                eps: float = 1e-5, out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
     """Layer norm over the last dimension (``adasum_layer_norm``): ``(y, mean, rstd)``, the
     last two in float32, for :func:`layer_norm_backward`."""
-    return _norm_forward(x, weight, bias, eps, out, stream, False)
+    code, index = _code(x, "x"), x.get_device()
+    rows, cols, ld = _rows(x, "x")
+    w, b, wcode = _parameters(weight, bias, cols, index)
+    if _elsewhere(index, stream):
+        return _there(index, stream, layer_norm, x, weight, bias, eps=eps, out=out)
+    y = _like(x) if out is None else _output(out, x.shape, x.dtype, index)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean = torch.empty_like(rstd)
+    st = load_library().adasum_layer_norm(x.data_ptr(), rows, cols, ld, code, w, b, wcode, float(eps), y.data_ptr(),
+                                          mean.data_ptr(), rstd.data_ptr(), None, None, _raw_stream(index))
+    if st:
+        check(st, "adasum_layer_norm")
+    return y, mean, rstd
 
 
 def layer_norm_checkpointed(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
@@ -286,22 +286,37 @@ def layer_norm_checkpointed(x: torch.Tensor, weight: torch.Tensor | None = None,
                             stream: torch.cuda.Stream | None = None):
     """Layer norm that keeps ``h = (x - mean) rstd`` in 8 bits: ``(y, checkpoint, rstd)``, for
     :func:`layer_norm_checkpointed_backward`; neither x nor y has to be kept."""
-    return _norm_forward(x, weight, bias, eps, out, stream, True)
+    code, index = _code(x, "x"), x.get_device()
+    rows, cols, ld = _rows(x, "x")
+    w, b, wcode = _parameters(weight, bias, cols, index)
+    if _elsewhere(index, stream):
+        return _there(index, stream, layer_norm_checkpointed, x, weight, bias, eps=eps, out=out)
+    y = _like(x) if out is None else _output(out, x.shape, x.dtype, index)
+    kept = _new_checkpoint(x, rows, cols)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    st = load_library().adasum_layer_norm(x.data_ptr(), rows, cols, ld, code, w, b, wcode, float(eps), y.data_ptr(), None,
+                                          rstd.data_ptr(), kept.codes.data_ptr(), kept.scales.data_ptr(),
+                                          _raw_stream(index))
+    if st:
+        check(st, "adasum_layer_norm")
+    return y, kept, rstd
 
 
-def _norm_gradients(lib, grad_weights, grad_biases, wanted, K, cols, device, dtype, rows, accumulate):
-    if accumulate and (grad_weights is None or grad_biases is None) and wanted:
-        raise ValueError("accumulate needs grad_weights and grad_biases to add to")
+def _norm_gradients(grad_weights, grad_biases, weight, wanted, accumulate, K, rows, cols, index):
+    """(weights' gradients, their pointers, biases', pointers, code, scratch bytes, scratch)."""
     if not wanted:
         if grad_weights is not None or grad_biases is not None:
             raise ValueError("grad_weights and grad_biases are not written with parameter_grads=False")
         return None, None, None, None, 0, 0, None
-    dw, dwp, dt = _gradients(grad_weights, K, cols, device, dtype, (cols,), "grad_weights")
-    db, dbp, bt = _gradients(grad_biases, K, cols, device, dt, (cols,), "grad_biases")
-    if dt != bt:
+    if accumulate and (grad_weights is None or grad_biases is None):
+        raise ValueError("accumulate needs grad_weights and grad_biases to add to")
+    dtype = torch.float32 if weight is None else weight.dtype
+    dw, dwp, code = _gradients(grad_weights, K, cols, index, dtype, (cols,), "grad_weights")
+    db, dbp, bcode = _gradients(grad_biases, K, cols, index, dw[0].dtype, (cols,), "grad_biases")
+    if code != bcode:
         raise ValueError("grad_weights and grad_biases must share their dtype")
-    nbytes = lib.adasum_layer_norm_backward_scratch_bytes(rows, cols, K)
-    return dw, dwp, db, dbp, _CODE[dt], nbytes, _scratch(nbytes, device)
+    nbytes = load_library().adasum_layer_norm_backward_scratch_bytes(rows, cols, K)
+    return dw, dwp, db, dbp, code, nbytes, _scratch(nbytes, index)
 
 
 def layer_norm_backward(grad_output: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -314,25 +329,27 @@ def layer_norm_backward(grad_output: torch.Tensor, x: torch.Tensor, mean: torch.
     allocates them, in weight's dtype, else float32), overwritten, or with ``accumulate``
     added to; returned as lists.  ``parameter_grads=False`` leaves them out (None).
     """
-    _float_tensor(grad_output, "grad_output")
-    _float_tensor(x, "x")
-    device = x.device
-    _same(grad_output, x, "grad_output")
+    code, index = _code(x, "x"), x.get_device()
+    if _code(grad_output, "grad_output") != code or grad_output.get_device() != index or grad_output.shape != x.shape:
+        raise ValueError(f"grad_output must have shape {tuple(x.shape)}, {x.dtype}, on cuda:{index}")
     rows, cols, ld_x = _rows(x, "x")
     ld_g = _rows(grad_output, "grad_output")[2]
-    w, _, wcode = _parameters(weight, None, cols, device)
-    mean_p, rstd_p = _statistic(mean, rows, device, "mean"), _statistic(rstd, rows, device, "rstd")
+    w, _, wcode = _parameters(weight, None, cols, index)
+    mean_p, rstd_p = _statistic(mean, rows, index, "mean"), _statistic(rstd, rows, index, "rstd")
+    if _elsewhere(index, stream):
+        return _there(index, stream, layer_norm_backward, grad_output, x, mean, rstd, weight,
+                      worker_offsets=worker_offsets, grad_weights=grad_weights, grad_biases=grad_biases,
+                      accumulate=accumulate, parameter_grads=parameter_grads)
     offs, K = _workers(worker_offsets, rows)
-    lib = load_library()
-    with _On(device, stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
-        dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(
-            lib, grad_weights, grad_biases, parameter_grads, K, cols, device,
-            torch.float32 if weight is None else weight.dtype, rows, accumulate)
-        st = lib.adasum_layer_norm_backward(
-            grad_output.data_ptr(), ld_g, x.data_ptr(), ld_x, mean_p, rstd_p, cols, _CODE[x.dtype], w, wcode, offs, K,
-            dx.data_ptr(), dwp, dbp, gcode, bool(accumulate), _ptr(scratch), nbytes, _current_stream(device))
-    check(st, "adasum_layer_norm_backward")
+    dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(grad_weights, grad_biases, weight, parameter_grads,
+                                                               accumulate, K, rows, cols, index)
+    dx = _like(x)
+    st = load_library().adasum_layer_norm_backward(
+        grad_output.data_ptr(), ld_g, x.data_ptr(), ld_x, mean_p, rstd_p, cols, code, w, wcode, _address(offs), K,
+        dx.data_ptr(), _address(dwp), _address(dbp), gcode, bool(accumulate), _ptr(scratch), nbytes,
+        _raw_stream(index))
+    if st:
+        check(st, "adasum_layer_norm_backward")
     return dx, dw, db
 
 
@@ -344,24 +361,25 @@ def layer_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Chec
     """``(grad_x, grad_weights, grad_biases)`` of layer norm from the 8-bit checkpoint of h
     (``adasum_layer_norm_backward_checkpointed``); with ``with_output`` also the output again,
     as a fourth.  bias is used for the output only.  The rest as in :func:`layer_norm_backward`."""
-    _float_tensor(grad_output, "grad_output")
-    device = grad_output.device
+    code, index = _code(grad_output, "grad_output"), grad_output.get_device()
     rows, cols, ld_g = _rows(grad_output, "grad_output")
-    codes, scales = _check_checkpoint(checkpoint, device, grad_output)
-    w, b, wcode = _parameters(weight, bias, cols, device)
-    rstd_p = _statistic(rstd, rows, device, "rstd")
+    codes, scales = _check_checkpoint(checkpoint, index, grad_output)
+    w, b, wcode = _parameters(weight, bias, cols, index)
+    rstd_p = _statistic(rstd, rows, index, "rstd")
+    if _elsewhere(index, stream):
+        return _there(index, stream, layer_norm_checkpointed_backward, grad_output, checkpoint, rstd, weight, bias,
+                      worker_offsets=worker_offsets, grad_weights=grad_weights, grad_biases=grad_biases,
+                      accumulate=accumulate, parameter_grads=parameter_grads, with_output=with_output)
     offs, K = _workers(worker_offsets, rows)
-    lib = load_library()
-    with _On(device, stream):
-        dx = torch.empty(grad_output.shape, dtype=grad_output.dtype, device=device)
-        y = torch.empty_like(dx) if with_output else None
-        dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(
-            lib, grad_weights, grad_biases, parameter_grads, K, cols, device,
-            torch.float32 if weight is None else weight.dtype, rows, accumulate)
-        st = lib.adasum_layer_norm_backward_checkpointed(
-            grad_output.data_ptr(), ld_g, codes, scales, rstd_p, cols, _CODE[grad_output.dtype], w, b, wcode, offs, K,
-            dx.data_ptr(), _ptr(y), dwp, dbp, gcode, bool(accumulate), _ptr(scratch), nbytes, _current_stream(device))
-    check(st, "adasum_layer_norm_backward_checkpointed")
+    dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(grad_weights, grad_biases, weight, parameter_grads,
+                                                               accumulate, K, rows, cols, index)
+    dx = _like(grad_output)
+    y = torch.empty_like(dx) if with_output else None
+    st = load_library().adasum_layer_norm_backward_checkpointed(
+        grad_output.data_ptr(), ld_g, codes, scales, rstd_p, cols, code, w, b, wcode, _address(offs), K, dx.data_ptr(),
+        _ptr(y), _address(dwp), _address(dbp), gcode, bool(accumulate), _ptr(scratch), nbytes, _raw_stream(index))
+    if st:
+        check(st, "adasum_layer_norm_backward_checkpointed")
     return (dx, dw, db, y) if with_output else (dx, dw, db)
 
 
@@ -369,43 +387,44 @@ def layer_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Chec
 
 
 def _new_checkpoint(x, rows: int, cols: int) -> Checkpoint:
-    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=x.device)
-    scales = torch.empty((rows, (cols + BLOCK - 1) // BLOCK), dtype=torch.float32, device=x.device)
+    device = x.device
+    codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device)
+    scales = torch.empty((rows, (cols + BLOCK - 1) // BLOCK), dtype=torch.float32, device=device)
     return Checkpoint(codes, scales, x.shape, x.dtype)
 
 
-def _check_checkpoint(kept: Checkpoint, device, like: torch.Tensor | None = None):
+def _check_checkpoint(kept: Checkpoint, index: int, like: torch.Tensor | None = None):
     """(pointer of the codes, pointer of the scales)."""
     if not isinstance(kept, Checkpoint):
         raise TypeError("checkpoint must be a Checkpoint")
-    if like is not None and (kept.shape != like.shape or kept.dtype != like.dtype):
-        raise ValueError(f"grad_output must be like the activation: {tuple(kept.shape)}, {kept.dtype}")
-    cols = kept.shape[-1]
+    codes, scales, shape, dtype = kept
+    if like is not None and (shape != like.shape or dtype != like.dtype):
+        raise ValueError(f"grad_output must be like the activation: {tuple(shape)}, {dtype}")
+    cols = shape[-1]
     rows = 1
-    for s in kept.shape[:-1]:
+    for s in shape[:-1]:
         rows *= s
-    codes, scales = kept.codes, kept.scales
-    if codes.dtype != torch.int8 or codes.device != device or not codes.is_contiguous() \
+    if codes.dtype != torch.int8 or codes.get_device() != index or not codes.is_contiguous() \
             or codes.shape != (rows, (cols + 15) // 16 * 16):
-        raise ValueError(f"checkpoint codes do not belong to an activation of shape {tuple(kept.shape)} on {device}")
-    if scales.dtype != torch.float32 or scales.device != device or not scales.is_contiguous() \
+        raise ValueError(f"checkpoint codes do not belong to an activation of shape {tuple(shape)} on cuda:{index}")
+    if scales.dtype != torch.float32 or scales.get_device() != index or not scales.is_contiguous() \
             or scales.shape != (rows, (cols + BLOCK - 1) // BLOCK):
-        raise ValueError(f"checkpoint scales do not belong to an activation of shape {tuple(kept.shape)} on {device}")
+        raise ValueError(f"checkpoint scales do not belong to an activation of shape {tuple(shape)} on cuda:{index}")
     return codes.data_ptr(), scales.data_ptr()
 
 
 def checkpoint_pack(x: torch.Tensor, *, stream: torch.cuda.Stream | None = None) -> Checkpoint:
     """An activation in 8 bits (``adasum_checkpoint_pack``): blocks of 128 columns, each with
     the scale max|x| / 127.  A block holding a NaN or an infinity comes back as NaN."""
-    _float_tensor(x, "x")
-    device = x.device
+    code, index = _code(x, "x"), x.get_device()
     rows, cols, ld = _rows(x, "x")
-    with _On(device, stream):
-        kept = _new_checkpoint(x, rows, cols)
-        st = load_library().adasum_checkpoint_pack(
-            x.data_ptr(), rows, cols, ld, _CODE[x.dtype], kept.codes.data_ptr(), kept.scales.data_ptr(),
-            _current_stream(device))
-    check(st, "adasum_checkpoint_pack")
+    if _elsewhere(index, stream):
+        return _there(index, stream, checkpoint_pack, x)
+    kept = _new_checkpoint(x, rows, cols)
+    st = load_library().adasum_checkpoint_pack(x.data_ptr(), rows, cols, ld, code, kept.codes.data_ptr(),
+                                               kept.scales.data_ptr(), _raw_stream(index))
+    if st:
+        check(st, "adasum_checkpoint_pack")
     return kept
 
 
@@ -415,22 +434,20 @@ def checkpoint_unpack(checkpoint: Checkpoint, *, dtype: torch.dtype | None = Non
     shape and its dtype (or ``dtype``)."""
     if not isinstance(checkpoint, Checkpoint):
         raise TypeError("checkpoint must be a Checkpoint")
-    device = checkpoint.codes.device
-    if device.type != "cuda":
-        raise ValueError("checkpoint must be on a CUDA device")
-    codes, scales = _check_checkpoint(checkpoint, device)
+    if not checkpoint.codes.is_cuda:
+        raise ValueError("checkpoint must hold CUDA tensors")
+    index = checkpoint.codes.get_device()
+    codes, scales = _check_checkpoint(checkpoint, index)
     dtype = checkpoint.dtype if dtype is None else dtype
     if dtype not in _CODE:
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    rows, cols = checkpoint.codes.shape[0], checkpoint.shape[-1]
-    with _On(device, stream):
-        if out is None:
-            out = torch.empty(checkpoint.shape, dtype=dtype, device=device)
-        elif out.dtype != dtype or out.device != device or out.shape != checkpoint.shape or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(checkpoint.shape)} on {device}")
-        st = load_library().adasum_checkpoint_unpack(codes, scales, rows, cols, _CODE[dtype], out.data_ptr(),
-                                                     _current_stream(device))
-    check(st, "adasum_checkpoint_unpack")
+    if _elsewhere(index, stream):
+        return _there(index, stream, checkpoint_unpack, checkpoint, dtype=dtype, out=out)
+    out = _output(out, checkpoint.shape, dtype, index)
+    st = load_library().adasum_checkpoint_unpack(codes, scales, checkpoint.codes.shape[0], checkpoint.shape[-1],
+                                                 _CODE[dtype], out.data_ptr(), _raw_stream(index))
+    if st:
+        check(st, "adasum_checkpoint_unpack")
     return out
 
 
@@ -438,16 +455,16 @@ def gelu_checkpointed(x: torch.Tensor, *, tanh: bool = False, out: torch.Tensor 
                       stream: torch.cuda.Stream | None = None):
     """``(gelu(x), checkpoint of x)`` in one pass (``adasum_gelu_checkpointed``); ``tanh``
     selects the tanh form."""
-    _float_tensor(x, "x")
-    device = x.device
+    code, index = _code(x, "x"), x.get_device()
     rows, cols, ld = _rows(x, "x")
-    with _On(device, stream):
-        y = _output(out, x, x.shape)
-        kept = _new_checkpoint(x, rows, cols)
-        st = load_library().adasum_gelu_checkpointed(
-            x.data_ptr(), rows, cols, ld, _CODE[x.dtype], bool(tanh), y.data_ptr(), kept.codes.data_ptr(),
-            kept.scales.data_ptr(), _current_stream(device))
-    check(st, "adasum_gelu_checkpointed")
+    if _elsewhere(index, stream):
+        return _there(index, stream, gelu_checkpointed, x, tanh=tanh, out=out)
+    y = _like(x) if out is None else _output(out, x.shape, x.dtype, index)
+    kept = _new_checkpoint(x, rows, cols)
+    st = load_library().adasum_gelu_checkpointed(x.data_ptr(), rows, cols, ld, code, bool(tanh), y.data_ptr(),
+                                                 kept.codes.data_ptr(), kept.scales.data_ptr(), _raw_stream(index))
+    if st:
+        check(st, "adasum_gelu_checkpointed")
     return y, kept
 
 
@@ -456,15 +473,16 @@ def gelu_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Checkpoint
     """``grad_output * gelu'(x)`` for the x that the checkpoint stands for
     (``adasum_gelu_checkpointed_backward``); with ``with_output`` the pair of that and gelu(x),
     so that the forward pass's output need not be kept."""
-    _float_tensor(grad_output, "grad_output")
-    device = grad_output.device
+    code, index = _code(grad_output, "grad_output"), grad_output.get_device()
     rows, cols, ld = _rows(grad_output, "grad_output")
-    codes, scales = _check_checkpoint(checkpoint, device, grad_output)
-    with _On(device, stream):
-        dx = torch.empty(grad_output.shape, dtype=grad_output.dtype, device=device)
-        y = torch.empty_like(dx) if with_output else None
-        st = load_library().adasum_gelu_checkpointed_backward(
-            grad_output.data_ptr(), ld, codes, scales, rows, cols, _CODE[grad_output.dtype], bool(tanh),
-            dx.data_ptr(), _ptr(y), _current_stream(device))
-    check(st, "adasum_gelu_checkpointed_backward")
+    codes, scales = _check_checkpoint(checkpoint, index, grad_output)
+    if _elsewhere(index, stream):
+        return _there(index, stream, gelu_checkpointed_backward, grad_output, checkpoint, tanh=tanh,
+                      with_output=with_output)
+    dx = _like(grad_output)
+    y = torch.empty_like(dx) if with_output else None
+    st = load_library().adasum_gelu_checkpointed_backward(grad_output.data_ptr(), ld, codes, scales, rows, cols, code,
+                                                          bool(tanh), dx.data_ptr(), _ptr(y), _raw_stream(index))
+    if st:
+        check(st, "adasum_gelu_checkpointed_backward")
     return (dx, y) if with_output else dx
