@@ -117,10 +117,22 @@ __device__ __forceinline__ float raw_value(const Raw8<T>& r, int e) {
   else return __uint_as_float(r.w[e]);
 }
 
+// The eight values as pairs.
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, F2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2(raw_value<T>(r, 2 * i), raw_value<T>(r, 2 * i + 1));
+}
+
+// Columns of a slice that starts at c0, at most 256, none past the row's end.
+__device__ __forceinline__ int slice_left(int64_t cols, int64_t c0) {
+  return static_cast<int>(max(static_cast<int64_t>(0), min(cols - c0, static_cast<int64_t>(256))));
+}
+
 // Loads the values of 256 columns starting at p, of which `left` exist (others are 0).
 // KEEP: the data will be read again (default: streaming).
 template <typename T, int LAYOUT, bool KEEP = false>
-__device__ __forceinline__ Raw8<T> load8(const T* p, int64_t left, int lane) {
+__device__ __forceinline__ Raw8<T> load8(const T* p, int left, int lane) {
   Raw8<T> r;
   if (LAYOUT == kVec && lane * 8 + 8 <= left) {
     const uint4* q = reinterpret_cast<const uint4*>(p + lane * 8);
@@ -146,29 +158,6 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int64_t left, int lane) {
   return r;
 }
 
-// Eight floats of a lane in shared memory, the columns of its layout.
-template <int LAYOUT>
-__device__ __forceinline__ void lds8(const float* p, int lane, float (&v)[8]) {
-  if constexpr (LAYOUT == kVec) {
-    const float4 a = reinterpret_cast<const float4*>(p)[lane * 2], b = reinterpret_cast<const float4*>(p)[lane * 2 + 1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = p[e * 32 + lane];
-  }
-}
-template <int LAYOUT>
-__device__ __forceinline__ void sts8(float* p, int lane, const float (&v)[8]) {
-  if constexpr (LAYOUT == kVec) {
-    reinterpret_cast<float4*>(p)[lane * 2] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[lane * 2 + 1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e * 32 + lane] = v[e];
-  }
-}
-
 __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
@@ -176,7 +165,7 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
 
 // Stores eight values of 256 columns starting at p, of which `left` exist.
 template <typename T, int LAYOUT>
-__device__ __forceinline__ void store8(T* p, int64_t left, int lane, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* p, int left, int lane, const float (&v)[8]) {
   if (LAYOUT == kVec && lane * 8 + 8 <= left) {
     uint4* q = reinterpret_cast<uint4*>(p + lane * 8);
     if constexpr (sizeof(T) == 2) {
@@ -192,6 +181,38 @@ __device__ __forceinline__ void store8(T* p, int64_t left, int lane, const float
     const int c = lane_col<LAYOUT>(lane, e);
     if (c < left) p[c] = narrow<T>(v[e]);
   }
+}
+
+template <typename T, int LAYOUT>
+__device__ __forceinline__ void store8(T* p, int left, int lane, const F2 (&v)[4]) {
+  float s[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = parts(v[i]);
+    s[2 * i] = x.x;
+    s[2 * i + 1] = x.y;
+  }
+  store8<T, LAYOUT>(p, left, lane, s);
+}
+
+// Floats of 256 columns in shared memory: first values 0..3 of every lane, then 4..7, so
+// that a warp's 16-byte accesses meet no bank twice.  `smem_col` is the column of place i.
+template <int LAYOUT>
+__device__ __forceinline__ int smem_col(int i) {
+  const int r = i & 255;
+  return (i & ~255) + lane_col<LAYOUT>((r >> 2) & 31, (r >> 7) * 4 + (r & 3));
+}
+__device__ __forceinline__ void lds8(const float* p, int lane, F2 (&v)[4]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[lane], b = reinterpret_cast<const float4*>(p)[32 + lane];
+  v[0] = f2(a.x, a.y);
+  v[1] = f2(a.z, a.w);
+  v[2] = f2(b.x, b.y);
+  v[3] = f2(b.z, b.w);
+}
+__device__ __forceinline__ void sts8(float* p, int lane, const F2 (&v)[4]) {
+  const float2 a = parts(v[0]), b = parts(v[1]), c = parts(v[2]), d = parts(v[3]);
+  reinterpret_cast<float4*>(p)[lane] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4*>(p)[32 + lane] = make_float4(c.x, c.y, d.x, d.y);
 }
 
 // ------------------------------------------------------------------- 8-bit checkpoints
@@ -220,13 +241,13 @@ __device__ __forceinline__ CkptScale ckpt_scale(float top, bool bad) {
 // The codes of eight values (two words, in the order of the values): the sum's low byte of
 // each.  (The products are scalar: a packed product and sum were measured to be contracted
 // to a fused one, which rounds differently next to ties.)
-__device__ __forceinline__ uint2 ckpt_codes8(const float (&v)[8], float inv_lo, float inv_hi) {
+__device__ __forceinline__ uint2 ckpt_codes8(const F2 (&v)[4], float inv_lo, float inv_hi) {
   uint32_t b[8];
   const F2 magic = f2(12582912.f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float k = i < 2 ? inv_lo : inv_hi;
-    const float2 s = parts(add2(f2(__fmul_rn(v[2 * i], k), __fmul_rn(v[2 * i + 1], k)), magic));
+    const float2 x = parts(v[i]), s = parts(add2(f2(__fmul_rn(x.x, k), __fmul_rn(x.y, k)), magic));
     b[2 * i] = __float_as_uint(s.x);
     b[2 * i + 1] = __float_as_uint(s.y);
   }
@@ -235,7 +256,7 @@ __device__ __forceinline__ uint2 ckpt_codes8(const float (&v)[8], float inv_lo, 
 }
 // The values of eight codes: a code plus 128 becomes the low byte of 2^23 as a float, and
 // the rest is exact up to the product with the scale.
-__device__ __forceinline__ void ckpt_values8(uint2 q, float lo_scale, float hi_scale, float (&v)[8]) {
+__device__ __forceinline__ void ckpt_values8(uint2 q, float lo_scale, float hi_scale, F2 (&v)[4]) {
   const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};
   const F2 bias = f2(-8388736.f);
 #pragma unroll
@@ -243,16 +264,14 @@ __device__ __forceinline__ void ckpt_values8(uint2 q, float lo_scale, float hi_s
     const uint32_t x = w[i >> 1];
     const float lo = __uint_as_float(__byte_perm(x, 0x4B000000u, i & 1 ? 0x7442 : 0x7440));
     const float hi = __uint_as_float(__byte_perm(x, 0x4B000000u, i & 1 ? 0x7443 : 0x7441));
-    const float2 s = parts(mul2(add2(f2(lo, hi), bias), f2(i < 2 ? lo_scale : hi_scale)));
-    v[2 * i] = s.x;
-    v[2 * i + 1] = s.y;
+    v[i] = mul2(add2(f2(lo, hi), bias), f2(i < 2 ? lo_scale : hi_scale));
   }
 }
 
 // Codes of 256 columns, the same columns per lane as the values'; rows of codes start on
 // 16-byte boundaries whatever the layout of the values.
 template <int LAYOUT>
-__device__ __forceinline__ uint2 load_codes8(const int8_t* p, int64_t left, int lane) {
+__device__ __forceinline__ uint2 load_codes8(const int8_t* p, int left, int lane) {
   if constexpr (LAYOUT == kVec) {  // (rows of codes are padded to 16, so a begun eight is always there)
     return lane * 8 < left ? __ldcs(reinterpret_cast<const uint2*>(p) + lane) : make_uint2(0u, 0u);
   } else {
@@ -266,7 +285,7 @@ __device__ __forceinline__ uint2 load_codes8(const int8_t* p, int64_t left, int 
   }
 }
 template <int LAYOUT>
-__device__ __forceinline__ void store_codes8(int8_t* p, int64_t left, int lane, uint2 q) {
+__device__ __forceinline__ void store_codes8(int8_t* p, int left, int lane, uint2 q) {
   if constexpr (LAYOUT == kVec) {
     if (lane * 8 < left) __stcs(reinterpret_cast<uint2*>(p) + lane, q);
   } else {
@@ -282,9 +301,10 @@ __device__ __forceinline__ void store_codes8(int8_t* p, int64_t left, int lane, 
 // from all the lanes' values (NaN if there is one); columns past the row's end hold 0.
 // kVec: a block is half a warp; kStrided: a block is four values of every lane.
 template <int LAYOUT>
-__device__ __forceinline__ void block_tops(const float (&v)[8], float (&top)[2]) {
-  top[0] = max_abs_nan(max_abs_nan(v[0], v[1], v[2]), v[3], v[3]);
-  top[1] = max_abs_nan(max_abs_nan(v[4], v[5], v[6]), v[7], v[7]);
+__device__ __forceinline__ void block_tops(const F2 (&v)[4], float (&top)[2]) {
+  const float2 a = parts(v[0]), b = parts(v[1]), c = parts(v[2]), d = parts(v[3]);
+  top[0] = max_abs_nan(max_abs_nan(a.x, a.y, b.x), b.y, b.y);
+  top[1] = max_abs_nan(max_abs_nan(c.x, c.y, d.x), d.y, d.y);
   if constexpr (LAYOUT == kVec) {
     top[0] = max_nan(top[0], top[1]);
 #pragma unroll
@@ -321,7 +341,7 @@ __device__ __forceinline__ void block_scales(const float (&top)[N][2], int lane,
 }
 // Stores the scales of 256 columns, of which `left` exist, at p.
 template <int LAYOUT>
-__device__ __forceinline__ void store_scales(float* p, int64_t left, int lane, const CkptScale (&s)[2]) {
+__device__ __forceinline__ void store_scales(float* p, int left, int lane, const CkptScale (&s)[2]) {
   if constexpr (LAYOUT == kVec) {
     if ((lane & 15) == 0 && lane * 8 < left) p[lane >> 4] = s[0].scale;
   } else {
@@ -332,12 +352,12 @@ __device__ __forceinline__ void store_scales(float* p, int64_t left, int lane, c
   }
 }
 template <int LAYOUT>
-__device__ __forceinline__ uint2 ckpt_codes(const float (&v)[8], const CkptScale (&s)[2]) {
+__device__ __forceinline__ uint2 ckpt_codes(const F2 (&v)[4], const CkptScale (&s)[2]) {
   return ckpt_codes8(v, s[0].inv, LAYOUT == kVec ? s[0].inv : s[1].inv);
 }
 // Values of 256 columns' codes, of which `left` columns exist; p: their scales.
 template <int LAYOUT>
-__device__ __forceinline__ void ckpt_values(uint2 q, const float* p, int64_t left, int lane, float (&v)[8]) {
+__device__ __forceinline__ void ckpt_values(uint2 q, const float* p, int left, int lane, F2 (&v)[4]) {
   if constexpr (LAYOUT == kVec) {
     const float s = lane * 8 < left ? p[lane >> 4] : 0.f;
     ckpt_values8(q, s, s, v);

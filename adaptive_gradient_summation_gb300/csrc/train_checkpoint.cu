@@ -35,11 +35,11 @@ __device__ __forceinline__ F2 exp2_2(F2 x) {
 
 // gelu of two values, and its slope.
 //
-// Erf form: with a = |x|, the upper tail of the normal distribution is
-//     q = 1/2 erfc(a / sqrt 2) = 1/2 (a1 t + ... + a5 t^5) exp(-a^2 / 2),
-//     t = 1 / (1 + p a / sqrt 2)
+// Erf form: with b = |x|, the upper tail of the normal distribution is
+//     q = 1/2 erfc(b / sqrt 2) = 1/2 (a1 t + ... + a5 t^5) exp(-b^2 / 2),
+//     t = 1 / (1 + p b / sqrt 2)
 // (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26; the error of erf is
-// below 1.5e-7).  gelu = max(x, 0) - a q; slope = Phi + x phi, where the density phi takes
+// below 1.5e-7).  gelu = max(x, 0) - b q; slope = Phi + x phi, where the density phi takes
 // the same exponential.  Two special-function operations and about a dozen others per value,
 // where the library's erf and exp would be bound by instruction issue.
 // Tanh form: 1/2 (1 + tanh u) is the logistic function of 2 u, s = 1 / (1 + exp(-2 u));
@@ -50,19 +50,16 @@ template <int ACT, bool VALUE, bool SLOPE>
 __device__ __forceinline__ void gelu2(F2 x, F2& value, F2& slope) {
   const float2 xs = parts(x);
   if constexpr (ACT == kActErf) {
-    // (|x| beyond 16 has q = 0; the bound keeps 0 * infinity out)
-    const F2 a = f2(min_nan(fabsf(xs.x), 16.f), min_nan(fabsf(xs.y), 16.f));
-    const F2 t = rcp2(fma2(a, f2(0.3275911f * 0.70710678118f), f2(1.f)));
+    // a = -|x|; beyond 16 q is 0, and the bound keeps 0 * infinity out
+    const F2 a = f2(max_nan(-fabsf(xs.x), -16.f), max_nan(-fabsf(xs.y), -16.f));
+    const F2 t = rcp2(fma2(a, f2(-0.3275911f * 0.70710678118f), f2(1.f)));
     const F2 e = exp2_2(mul2(mul2(a, a), f2(-0.72134752044f)));
     F2 p = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
     p = fma2(p, t, f2(0.5f * 1.421413741f));
     p = fma2(p, t, f2(0.5f * -0.284496736f));
     p = fma2(p, t, f2(0.5f * 0.254829592f));
     const F2 q = mul2(mul2(p, t), e);
-    if constexpr (VALUE) {
-      const float2 as = parts(a);
-      value = fma2(f2(-as.x, -as.y), q, f2(max_nan(xs.x, 0.f), max_nan(xs.y, 0.f)));
-    }
+    if constexpr (VALUE) value = fma2(a, q, f2(max_nan(xs.x, 0.f), max_nan(xs.y, 0.f)));
     if constexpr (SLOPE) {
       const float2 qs = parts(q);
       const F2 phi = add2(f2(copysignf(0.5f - qs.x, xs.x), copysignf(0.5f - qs.y, xs.y)), f2(0.5f));
@@ -110,20 +107,37 @@ struct UnpackArgs {
 
 // A warp takes kItems slices of 256 columns, of one row or of several, and loads them all
 // before it works on the first.  Bound by bytes: each value is read and written once.
-struct Slice {
-  int64_t row, c0;
-  __device__ __forceinline__ Slice(uint32_t item, uint32_t slices) {
-    const uint32_t r = item / slices;
-    row = r;
-    c0 = static_cast<int64_t>(item - r * slices) * kSlice;
+//
+// Where a warp is, as offsets into the buffers, so that going on costs additions only.
+struct Cursor {
+  int64_t in, out, codes, scales;  // the strided input, a dense output, codes, scales
+  int64_t c0, cols;
+  template <typename A>
+  __device__ __forceinline__ Cursor(const A& a, int64_t ld, uint32_t item) {
+    const int64_t row = item / a.slices;
+    c0 = static_cast<int64_t>(item - static_cast<uint32_t>(row) * a.slices) * kSlice;
+    cols = a.cols;
+    in = row * ld + c0;
+    out = row * a.cols + c0;
+    codes = row * a.pitch + c0;
+    scales = row * a.nscales + c0 / kCkptBlock;
   }
-  __device__ __forceinline__ void next(int64_t cols) {
+  template <typename A>
+  __device__ __forceinline__ void next(const A& a, int64_t ld) {
     c0 += kSlice;
+    in += kSlice;
+    out += kSlice;
+    codes += kSlice;
+    scales += kSlice / kCkptBlock;
     if (c0 >= cols) {
+      in += ld - c0;
+      out += cols - c0;
+      codes += a.pitch - c0;
+      scales += a.nscales - c0 / kCkptBlock;
       c0 = 0;
-      ++row;
     }
   }
+  __device__ __forceinline__ int left() const { return static_cast<int>(min(cols - c0, static_cast<int64_t>(kSlice))); }
 };
 
 template <typename T, int ACT, int LAYOUT>
@@ -132,43 +146,34 @@ __global__ void __launch_bounds__(kCkptThreads) pack_kernel(const PackArgs a) {
   const int lane = threadIdx.x & 31;
   const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
   if (first >= a.items) return;
-  const Slice begin(first, a.slices);
-  Raw8<T> r[kItems];
-  Slice s = begin;
+  const int n = min(a.items - first, static_cast<uint32_t>(kItems));
+  const Cursor begin(a, a.ld, first);
+  F2 v[kItems][4];
+  {
+    Raw8<T> r[kItems];
+    Cursor s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i, s.next(a.cols))
-    r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.row * a.ld + s.c0, first + i < a.items ? a.cols - s.c0 : 0, lane);
+    for (int i = 0; i < kItems; ++i, s.next(a, a.ld))
+      r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.in, i < n ? s.left() : 0, lane);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) unpack8<T>(r[i], v[i]);
+  }
   float top[kItems][2];
 #pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = raw_value<T>(r[i], e);
-    block_tops<LAYOUT>(v, top[i]);
-  }
+  for (int i = 0; i < kItems; ++i) block_tops<LAYOUT>(v[i], top[i]);
   CkptScale sc[kItems][2];
   block_scales<LAYOUT, kItems>(top, lane, sc);
-  s = begin;
+  Cursor s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i, s.next(a.cols)) {
-    if (first + i >= a.items) break;
-    const int64_t left = a.cols - s.c0;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = raw_value<T>(r[i], e);
-    store_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, left, lane, ckpt_codes<LAYOUT>(v, sc[i]));
-    store_scales<LAYOUT>(a.scales + s.row * a.nscales + s.c0 / kCkptBlock, left, lane, sc[i]);
+  for (int i = 0; i < kItems; ++i, s.next(a, a.ld)) {
+    if (i >= n) break;
+    store_codes8<LAYOUT>(a.codes + s.codes, s.left(), lane, ckpt_codes<LAYOUT>(v[i], sc[i]));
+    store_scales<LAYOUT>(a.scales + s.scales, s.left(), lane, sc[i]);
     if constexpr (ACT != kActNone) {
-      float y[8];
+      F2 unused;
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        F2 value, slope;
-        gelu2<ACT, true, false>(f2(v[e], v[e + 1]), value, slope);
-        const float2 p = parts(value);
-        y[e] = p.x;
-        y[e + 1] = p.y;
-      }
-      store8<T, LAYOUT>(static_cast<T*>(a.y) + s.row * a.cols + s.c0, left, lane, y);
+      for (int e = 0; e < 4; ++e) gelu2<ACT, true, false>(v[i][e], v[i][e], unused);
+      store8<T, LAYOUT>(static_cast<T*>(a.y) + s.out, s.left(), lane, v[i]);
     }
   }
 }
@@ -179,41 +184,36 @@ __global__ void __launch_bounds__(kCkptThreads) unpack_kernel(const UnpackArgs a
   const int lane = threadIdx.x & 31;
   const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
   if (first >= a.items) return;
-  const Slice begin(first, a.slices);
+  const int n = min(a.items - first, static_cast<uint32_t>(kItems));
+  const Cursor begin(a, a.ld_dy, first);
   uint2 q[kItems];
   Raw8<T> r[kItems];
-  Slice s = begin;
+  Cursor s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i, s.next(a.cols)) {
-    const int64_t left = first + i < a.items ? a.cols - s.c0 : 0;
-    q[i] = load_codes8<LAYOUT>(a.codes + s.row * a.pitch + s.c0, left, lane);
-    if constexpr (ACT != kActNone) r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.row * a.ld_dy + s.c0, left, lane);
+  for (int i = 0; i < kItems; ++i, s.next(a, a.ld_dy)) {
+    const int left = i < n ? s.left() : 0;
+    q[i] = load_codes8<LAYOUT>(a.codes + s.codes, left, lane);
+    if constexpr (ACT != kActNone) r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.in, left, lane);
   }
   s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i, s.next(a.cols)) {
-    if (first + i >= a.items) break;
-    const int64_t left = a.cols - s.c0, at = s.row * a.cols + s.c0;
-    float v[8];
-    ckpt_values<LAYOUT>(q[i], a.scales + s.row * a.nscales + s.c0 / kCkptBlock, left, lane, v);
+  for (int i = 0; i < kItems; ++i, s.next(a, a.ld_dy)) {
+    if (i >= n) break;
+    const int left = s.left();
+    F2 v[4];
+    ckpt_values<LAYOUT>(q[i], a.scales + s.scales, left, lane, v);
     if constexpr (ACT != kActNone) {
-      float y[8];
+      F2 dy[4], y[4];
+      unpack8<T>(r[i], dy);
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        F2 value, slope;
-        gelu2<ACT, AGAIN, true>(f2(v[e], v[e + 1]), value, slope);
-        const float2 d = parts(mul2(slope, f2(raw_value<T>(r[i], e), raw_value<T>(r[i], e + 1))));
-        v[e] = d.x;
-        v[e + 1] = d.y;
-        if constexpr (AGAIN) {
-          const float2 p = parts(value);
-          y[e] = p.x;
-          y[e + 1] = p.y;
-        }
+      for (int e = 0; e < 4; ++e) {
+        F2 slope;
+        gelu2<ACT, AGAIN, true>(v[e], y[e], slope);
+        v[e] = mul2(slope, dy[e]);
       }
-      if constexpr (AGAIN) store8<T, LAYOUT>(static_cast<T*>(a.y) + at, left, lane, y);
+      if constexpr (AGAIN) store8<T, LAYOUT>(static_cast<T*>(a.y) + s.out, left, lane, y);
     }
-    store8<T, LAYOUT>(static_cast<T*>(a.out) + at, left, lane, v);
+    store8<T, LAYOUT>(static_cast<T*>(a.out) + s.out, left, lane, v);
   }
 }
 

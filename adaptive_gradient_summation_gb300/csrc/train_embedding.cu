@@ -2,11 +2,12 @@
 //
 // The gradient of a table row is the sum of the rows of grad_out whose token it is.  The
 // tokens of each worker are sorted (stably, so that equal tokens stay in their order) and
-// the sorted list is cut into chunks of equal length, whatever the tokens: one warp sums
-// the runs of equal tokens inside one chunk over 256 columns.  A run that lies inside its
-// chunk goes straight to the gradient; the pieces of a run that crosses chunks go to
-// scratch memory and are joined in order by a last kernel.  So a token that makes up most
-// of the batch costs no more than any other, and every sum has a fixed order.
+// the sorted list is cut into chunks of equal length, whatever the tokens: one CTA sums the
+// runs of equal tokens inside one chunk over 256 columns, its warps taking equal parts.  A
+// run that lies inside the chunk goes straight to the gradient; the pieces of a run that
+// crosses chunks go to scratch memory and are joined in order by a last kernel.  So a token
+// that makes up most of the batch costs no more than any other, and every sum has a fixed
+// order.  Workers of at most 256 tokens are one chunk each, which the CTAs sort themselves.
 #include "adasum_host.h"
 #include "adasum_launch.h"
 #include "adasum_train.cuh"
@@ -51,13 +52,13 @@ __global__ void __launch_bounds__(kEmbThreads) lookup_kernel(const LookupArgs a)
   const int64_t left = a.cols - c0;
   Raw8<T> r[kLookupVecs];
 #pragma unroll
-  for (int j = 0; j < kLookupVecs; ++j) r[j] = load8<T, LAYOUT, true>(src + j * kSlice, there ? left - j * kSlice : 0, lane);
+  for (int j = 0; j < kLookupVecs; ++j) r[j] = load8<T, LAYOUT, true>(src + j * kSlice, there ? slice_left(left, j * kSlice) : 0, lane);
 #pragma unroll
   for (int j = 0; j < kLookupVecs; ++j) {
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = there ? a.scale * raw_value<T>(r[j], e) : 0.f;
-    store8<T, LAYOUT>(dst + j * kSlice, left - j * kSlice, lane, v);
+    store8<T, LAYOUT>(dst + j * kSlice, slice_left(left, j * kSlice), lane, v);
   }
 }
 
@@ -70,13 +71,16 @@ constexpr int kSortMost = kSortThreads * kSortItems;      // tokens one CTA sort
 constexpr int kDigits = 256;
 constexpr int kMostPasses = 4;
 
-// Tokens per chunk: 32, or 8 when that leaves too few warps to cover the memory's latency
-// (a warp reads its chunk's rows eight at a time).
-int chunk_tokens(int64_t n, int64_t cols) {
-  const int64_t slices = (cols + kSlice - 1) / kSlice;
-  return n * slices >= 32 * 4096 ? 32 : 8;
+constexpr int kSelfSort = kEmbThreads;                    // tokens of a worker that the summing CTAs sort
+
+// Tokens per warp of a chunk: few enough that the warps cover the memory's latency (about
+// 32 per SM), at most 32; workers of at most kSelfSort tokens are one chunk.
+int warp_tokens(int64_t n, int64_t most, int64_t cols) {
+  if (most <= kSelfSort) return most <= 8 * kEmbWarps ? 8 : most <= 16 * kEmbWarps ? 16 : 32;
+  const int64_t work = n * ((cols + kSlice - 1) / kSlice);
+  return work >= 32 * 4864 ? 32 : work >= 16 * 4864 ? 16 : 8;
 }
-int64_t chunk_bound(int64_t n, int64_t cols, int K) { return n / chunk_tokens(n, cols) + K; }
+int64_t chunk_bound(int64_t n, int K) { return n / (8 * kEmbWarps) + K; }
 int64_t tile_bound(int64_t n, int K) { return n / kSortMost + K; }
 
 // Regions of the scratch memory.
@@ -93,8 +97,8 @@ struct Scratch {
     for (int i = 0; i < 2; ++i) pos[i] = take(4 * n);
     hist = take(4 * kMostPasses * kDigits * tile_bound(n, K));
     count = take(4);
-    list = take(4 * chunk_bound(n, cols, K));
-    partials = take(8 * cols * chunk_bound(n, cols, K));
+    list = take(4 * chunk_bound(n, K));
+    partials = take(8 * cols * chunk_bound(n, K));
     total = at;
   }
 };
@@ -123,11 +127,13 @@ struct SortArgs {
 struct TableGradArgs {
   const void* dy;
   int64_t cols, ld;
+  const void* tokens;       // for CTAs that sort themselves
+  int64_t padding_idx;
+  int token_bytes;
   int num_rows;
   float scale;
-  int grad_dtype, accumulate;
-  int K, chunk, slices;
-  int64_t nchunks;
+  int accumulate;
+  int K, part, slices;      // tokens per warp of a chunk
   const int *keys, *pos;
   int *count, *list;
   float* partials;          // [chunk][head, tail][cols]
@@ -166,7 +172,8 @@ __device__ __forceinline__ void fill_share(const SortArgs& a, int cta) {
 }
 
 // Key of token i: the token, or num_rows (sorted last, not summed) when it gets no gradient.
-__device__ __forceinline__ int token_key(const SortArgs& a, int64_t i) {
+template <typename A>
+__device__ __forceinline__ int token_key(const A& a, int64_t i) {
   const int64_t t = load_token(a.tokens, a.token_bytes, i);
   return t >= 0 && t < a.num_rows && t != a.padding_idx ? static_cast<int>(t) : a.num_rows;
 }
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kSortThreads) table_count_kernel(const __grid_
   pdl_enter();
   __shared__ int hist[kDigits];
   const int tile = blockIdx.x;
-  if (tile >= a.ntiles) return fill_share(a, tile - a.ntiles);
+  if (tile >= a.ntiles) return fill_share(a, tile - a.ntiles);  // (every CTA, when there is nothing to count)
   if (tile == 0 && threadIdx.x == 0) *a.join_count = 0;
   const int k = worker_of(a.tile_off, a.K, tile);
   const int64_t lo = a.off[k] + static_cast<int64_t>(tile - a.tile_off[k]) * kSortMost;
@@ -363,79 +370,224 @@ __global__ void __launch_bounds__(kSortThreads) table_scatter_kernel(const __gri
   }
 }
 
-// Writes scale * acc to (or adds it to) 256 columns of a gradient's row.
-template <typename G, int LAYOUT>
-__device__ __forceinline__ void put_row(const TableGradArgs& a, int k, int row, int64_t c0, int lane, const float (&acc)[8]) {
-  G* out = static_cast<G*>(a.grads[k]) + row * a.cols + c0;
-  float v[8];
-  if (a.accumulate) {
-    const Raw8<G> old = load8<G, LAYOUT>(out, a.cols - c0, lane);
+// Writes scale * acc to 256 columns of a gradient's row; ADD: added to `old`, its values.
+template <typename G, int LAYOUT, bool ADD>
+__device__ __forceinline__ void put_row(G* out, float scale, int left, int lane, const F2 (&acc)[4], const Raw8<G>& old) {
+  F2 v[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(raw_value<G>(old, e), __fmul_rn(a.scale, acc[e]));
-  } else {
+  for (int i = 0; i < 4; ++i) v[i] = mul2(acc[i], f2(scale));
+  if constexpr (ADD) {
+    F2 o[4];
+    unpack8<G>(old, o);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = a.scale * acc[e];
+    for (int i = 0; i < 4; ++i) {
+      // (scalar sums: a packed product and sum would be contracted)
+      const float2 x = parts(o[i]), y = parts(v[i]);
+      v[i] = f2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+    }
   }
-  store8<G, LAYOUT>(out, a.cols - c0, lane, v);
+  store8<G, LAYOUT>(out, left, lane, v);
 }
 
-// Sums inside one chunk of sorted tokens, 256 columns per warp; rows are loaded eight at a
-// time.  Bound by grad_out's bytes (each read once) and the gradient rows written.
-template <typename T, typename G, int LAYOUT>
+__device__ __forceinline__ void add8(F2 (&acc)[4], const F2 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = add2(acc[i], v[i]);
+}
+
+// What a warp found at the ends of its part of a chunk.
+enum Ends : int {
+  kHead = 1,   // its first run began earlier
+  kSpan = 2,   // ... and does not end here either
+  kTail = 4,   // its last run begins here and does not end here
+};
+
+// Sums inside one chunk of sorted tokens, 256 columns per CTA and a part of the chunk per
+// warp.  kVec: a lane copies its 16 or 32 bytes of the next rows to shared memory ahead of
+// their use (8 or 4 rows, 4 KiB a warp), which takes no registers and no exchange between
+// lanes; kStrided: the next row is held in registers.  Runs that cross warps are joined
+// through shared memory, runs that cross chunks leave their pieces in scratch memory.
+// Bound by grad_out's bytes (each read once) and the gradient rows written.
+template <typename T, typename G, bool ADD>
+struct SumSmem {
+  static constexpr int kAhead = 16 / sizeof(T);  // rows on their way
+  static constexpr int kVecs = sizeof(T) / 2, kOldVecs = sizeof(G) / 2;  // 16-byte vectors of a lane's eight
+  union {
+    struct {
+      uint4 dy[kEmbWarps][kAhead][kVecs][32];
+      uint4 old[ADD ? kEmbWarps : 1][ADD ? kAhead : 1][kOldVecs][ADD ? 32 : 1];  // gradient rows to be added to
+    } ring;
+    float piece[kEmbWarps][2][kSlice];
+    int unsorted[kSelfSort];
+  };
+};
+template <typename T, typename G, int LAYOUT, bool SORT, bool ADD>
 __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_constant__ TableGradArgs a) {
   pdl_enter();
-  constexpr int B = 8;
-  const int lane = threadIdx.x & 31;
-  const uint32_t item = blockIdx.x * kEmbWarps + (threadIdx.x >> 5);
-  const int64_t chunk = item / static_cast<uint32_t>(a.slices);
-  if (chunk >= a.nchunks) return;
-  const int64_t c0 = (item - chunk * a.slices) * kSlice;
-  const int k = worker_of(a.chunk_off, a.K, chunk);
-  const int64_t first = a.off[k], last = a.off[k + 1], lo = first + (chunk - a.chunk_off[k]) * a.chunk;
-  const int m = static_cast<int>(min(static_cast<int64_t>(a.chunk), last - lo));
-  int key = a.num_rows, pos = 0;
+  using Smem = SumSmem<T, G, ADD>;
+  constexpr int kVecs = Smem::kVecs, kAhead = Smem::kAhead;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  __shared__ int ends[kEmbWarps], tail_key[kEmbWarps];
+  __shared__ int own_keys[SORT ? kSelfSort : 1], own_pos[SORT ? kSelfSort : 1];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const uint32_t chunk = blockIdx.x / static_cast<uint32_t>(a.slices);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - chunk * a.slices) * kSlice;
+  const int left = slice_left(a.cols, c0);
+  const int k = worker_of(a.chunk_off, a.K, static_cast<int>(chunk));
+  const int64_t first = a.off[k], last = a.off[k + 1];
+  const int *keys = a.keys, *pos = a.pos;
+  int64_t base = 0;  // index of keys[0]
+  if constexpr (SORT) {
+    // a token's place is the number of smaller keys and of equal ones before it
+    const int n = static_cast<int>(last - first), i = threadIdx.x;
+    const int mine = i < n ? token_key(a, first + i) : 0;
+    sm.unsorted[i] = i < n ? mine : INT32_MAX;
+    __syncthreads();
+    int place = 0;
+    for (int j = 0; j < n; j += 4) {
+      const int4 q = *reinterpret_cast<const int4*>(&sm.unsorted[j]);
+      place += (q.x < mine + (j < i)) + (q.y < mine + (j + 1 < i)) + (q.z < mine + (j + 2 < i)) + (q.w < mine + (j + 3 < i));
+    }
+    if (i < n) {  // (the ring takes the place of the unsorted keys after the barrier)
+      own_keys[place] = mine;
+      own_pos[place] = static_cast<int>(first) + i;
+    }
+    __syncthreads();
+    keys = own_keys;
+    pos = own_pos;
+    base = first;
+  }
+  const int64_t lo = first + (static_cast<int64_t>(chunk - a.chunk_off[k]) * kEmbWarps + w) * a.part;
+  const int m = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.part), last - lo)));
+  int key = a.num_rows, at = 0, before = a.num_rows, after = a.num_rows;
   if (lane < m) {
-    key = a.keys[lo + lane];
-    pos = a.pos[lo + lane];
+    key = keys[lo - base + lane];
+    at = pos[lo - base + lane];
   }
-  int cur = __shfl_sync(0xFFFFFFFFu, key, 0);
-  if (cur == a.num_rows) return;  // nothing but tokens without a gradient
-  bool head = lo > first && a.keys[lo - 1] == cur;
-  const int next = lo + m < last ? a.keys[lo + m] : a.num_rows;
-  float acc[8];
+  if (m > 0 && lo > first) before = keys[lo - base - 1];
+  if (m > 0 && lo + m < last) after = keys[lo - base + m];
+  // tokens without a gradient are sorted last
+  const int n = __popc(__ballot_sync(0xFFFFFFFFu, key != a.num_rows));
+  const T* dy = static_cast<const T*>(a.dy) + c0;
+  G* grad = static_cast<G*>(a.grads[k]) + c0;
+  const int earlier = __shfl_up_sync(0xFFFFFFFFu, key, 1);
+  const bool begins = lane == 0 ? before != key : earlier != key;  // this lane's token begins a run
+  const unsigned starts = __ballot_sync(0xFFFFFFFFu, begins && key != a.num_rows);
+  Raw8<T> held;
+  Raw8<G> held_old;
+  auto copy = [&](int i) {  // row i of the part, and the gradient row of a run that begins there
+    const int p = __shfl_sync(0xFFFFFFFFu, at, i & 31), q = __shfl_sync(0xFFFFFFFFu, key, i & 31);
+    const T* row = dy + static_cast<int64_t>(p) * a.ld;
+    const bool old = ADD && i < n && (starts >> i & 1);
+    if constexpr (LAYOUT == kVec) {
+      if (i < n) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  auto piece = [&](int slot) {
-    store8<float, LAYOUT>(a.partials + (chunk * 2 + slot) * a.cols + c0, a.cols - c0, lane, acc);
-  };
-  for (int i0 = 0; i0 < m; i0 += B) {
-    Raw8<T> r[B];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int p = __shfl_sync(0xFFFFFFFFu, pos, (i0 + b) & 31), q = __shfl_sync(0xFFFFFFFFu, key, (i0 + b) & 31);
-      r[b] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + p * a.ld + c0, i0 + b < m && q != a.num_rows ? a.cols - c0 : 0, lane);
-    }
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      if (i0 + b >= m) break;
-      const int q = __shfl_sync(0xFFFFFFFFu, key, i0 + b);
-      if (q != cur) {
-        if (head) piece(0);
-        else if (cur != a.num_rows) put_row<G, LAYOUT>(a, k, cur, c0, lane, acc);
-        cur = q;
-        head = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        for (int v = 0; v < kVecs; ++v) {
+          const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(T));
+          const int bytes = max(0, min(16, (left - c) * static_cast<int>(sizeof(T))));
+          cp_async16(smem_addr(&sm.ring.dy[w][i % kAhead][v][lane]), row + (bytes > 0 ? c : 0), bytes);
+        }
       }
+      if (old) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += raw_value<T>(r[b], e);
+        for (int v = 0; v < Smem::kOldVecs; ++v) {
+          const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(G));
+          const int bytes = max(0, min(16, (left - c) * static_cast<int>(sizeof(G))));
+          cp_async16(smem_addr(&sm.ring.old[w][i % kAhead][v][lane]), grad + q * a.cols + (bytes > 0 ? c : 0), bytes);
+        }
+      }
+      cp_async_commit();
+    } else {
+      held = load8<T, LAYOUT>(row, i < n ? left : 0, lane);
+      if constexpr (ADD) held_old = load8<G, LAYOUT>(grad + q * a.cols, old ? left : 0, lane);
+    }
+  };
+  // a lane's eight values from its 16-byte vectors
+  auto gather = [&](auto& r, const auto& from) {
+#pragma unroll
+    for (int v = 0; v < static_cast<int>(sizeof(r.w) / 16); ++v) {
+      const uint4 x = from[v][lane];
+      r.w[4 * v] = x.x;
+      r.w[4 * v + 1] = x.y;
+      r.w[4 * v + 2] = x.z;
+      r.w[4 * v + 3] = x.w;
+    }
+  };
+  constexpr int kLead = LAYOUT == kVec ? kAhead : 1;
+  for (int i = 0; i < kLead; ++i) copy(i);
+  F2 acc[4], head[4];
+  Raw8<G> old = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = head[i] = f2(0.f);
+  int cur = __shfl_sync(0xFFFFFFFFu, key, 0), found = 0;
+  bool from_before = n > 0 && before == cur;
+  for (int i = 0;; ++i) {
+    const int q = i < n ? __shfl_sync(0xFFFFFFFFu, key, i & 31) : -1;
+    if (q != cur || i == n) {  // the run `cur` ends in this part, or the part ends
+      if (n == 0) break;
+      const bool goes_on = i == n && i == m && after == cur;
+      if (from_before) {
+        found |= goes_on ? kHead | kSpan : kHead;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) head[e] = acc[e];
+      } else if (goes_on) {
+        found |= kTail;
+      } else {
+        put_row<G, LAYOUT, ADD>(grad + cur * a.cols, a.scale, left, lane, acc, old);
+      }
+      if (i == n) break;
+      cur = q;
+      from_before = false;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = f2(0.f);
+    }
+    F2 v[4];
+    if constexpr (LAYOUT == kVec) {
+      cp_async_wait<kAhead - 1>();
+      Raw8<T> r;
+      gather(r, sm.ring.dy[w][i % kAhead]);
+      unpack8<T>(r, v);
+      if constexpr (ADD)
+        if (starts >> i & 1) gather(old, sm.ring.old[w][i % kAhead]);
+    } else {
+      unpack8<T>(held, v);
+      if constexpr (ADD)
+        if (starts >> i & 1) old = held_old;
+    }
+    add8(acc, v);
+    copy(i + kLead);
+  }
+  // runs that cross warps
+  const int64_t chunk_end = lo + static_cast<int64_t>(kEmbWarps - w) * a.part;
+  if constexpr (LAYOUT == kVec) cp_async_wait<0>();
+  if (lane == 0) {
+    ends[w] = found;
+    tail_key[w] = cur;
+  }
+  if (!__syncthreads_or(found)) return;
+  if (found & kHead) sts8(sm.piece[w][0], lane, head);
+  if (found & kTail) sts8(sm.piece[w][1], lane, acc);
+  __syncthreads();
+  for (int slot = 0; slot < 2; ++slot) {
+    // slot 0: the run that enters the chunk (warp 0's head); slot 1: a run that begins here
+    if (!(ends[w] & (slot ? kTail : kHead)) || (slot == 0 && w > 0)) continue;
+    lds8(sm.piece[w][slot], lane, acc);
+    bool open = slot == 1 || (ends[w] & kSpan);
+    int j = w + 1;
+    for (; open && j < kEmbWarps && (ends[j] & kHead); ++j) {
+      F2 v[4];
+      lds8(sm.piece[j][0], lane, v);
+      add8(acc, v);
+      open = ends[j] & kSpan;
+    }
+    open = open && j == kEmbWarps && chunk_end < last;
+    if (slot == 0 || open) {
+      store8<float, LAYOUT>(a.partials + (static_cast<int64_t>(chunk) * 2 + slot) * a.cols + c0, left, lane, acc);
+      if (slot == 1 && c0 == 0 && lane == 0) a.list[atomicAdd(a.count, 1)] = static_cast<int>(chunk);
+    } else {
+      put_row<G, LAYOUT, ADD>(grad + tail_key[w] * a.cols, a.scale, left, lane, acc, old);
     }
   }
-  if (cur == a.num_rows) return;
-  const bool tail = next == cur;
-  if (!head && !tail) return put_row<G, LAYOUT>(a, k, cur, c0, lane, acc);
-  piece(head ? 0 : 1);
-  if (!head && c0 == 0 && lane == 0) a.list[atomicAdd(a.count, 1)] = static_cast<int>(chunk);
 }
 
 // Joins the pieces of the runs that cross chunks: one CTA per run and 256 columns, its
@@ -443,52 +595,58 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
 template <typename G, int LAYOUT>
 __global__ void __launch_bounds__(kEmbThreads) table_join_kernel(const __grid_constant__ TableGradArgs a) {
   pdl_enter();
-  constexpr int B = 8;
+  constexpr int B = 4;
   __shared__ float part[kEmbWarps][kSlice];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t items = static_cast<int64_t>(*a.count) * a.slices;
+  const int64_t span = static_cast<int64_t>(a.part) * kEmbWarps;
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t chunk = a.list[item / a.slices], c0 = item % a.slices * kSlice;
+    const int chunk = a.list[item / a.slices];
+    const int64_t c0 = item % a.slices * kSlice;
+    const int left = slice_left(a.cols, c0);
     const int k = worker_of(a.chunk_off, a.K, chunk);
-    const int64_t first = a.off[k], last = a.off[k + 1];
-    const int64_t after = first + (chunk + 1 - a.chunk_off[k]) * a.chunk;  // start of the next chunk
+    const int64_t last = a.off[k + 1];
+    const int64_t after = a.off[k] + (chunk + 1 - a.chunk_off[k]) * span;  // start of the next chunk
     const int key = a.keys[after];
-    // how many chunks begin inside the run: the last such beginning, by bisection
-    int64_t lo = 0, hi = (last - after + a.chunk - 1) / a.chunk;  // keys[after + lo * chunk] == key, that of hi is not
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (a.keys[after + mid * a.chunk] == key) lo = mid;
-      else hi = mid;
+    // the chunk's own tail, and the heads of the following chunks that begin inside the run
+    int64_t pieces = 1;
+    for (;;) {
+      const int64_t i = after + (pieces - 1 + lane) * span;
+      const unsigned in = __ballot_sync(0xFFFFFFFFu, i < last && a.keys[i] == key);
+      pieces += __popc(in);
+      if (in != 0xFFFFFFFFu) break;
     }
-    const int64_t pieces = lo + 2;  // the chunk's own tail, and the heads of the following ones
     const int64_t p0 = pieces * w / kEmbWarps, p1 = pieces * (w + 1) / kEmbWarps;
-    float acc[8];
+    F2 acc[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[e] = f2(0.f);
     for (int64_t i0 = p0; i0 < p1; i0 += B) {
       Raw8<float> r[B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const int64_t i = i0 + b;
         const float* p = a.partials + ((chunk + i) * 2 + (i == 0 ? 1 : 0)) * a.cols + c0;
-        r[b] = load8<float, LAYOUT>(p, i < p1 ? a.cols - c0 : 0, lane);
+        r[b] = load8<float, LAYOUT>(p, i < p1 ? left : 0, lane);
       }
 #pragma unroll
-      for (int b = 0; b < B; ++b)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += raw_value<float>(r[b], e);
+      for (int b = 0; b < B; ++b) {
+        F2 v[4];
+        unpack8<float>(r[b], v);
+        add8(acc, v);
+      }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) part[w][e * 32 + lane] = acc[e];
+    sts8(part[w], lane, acc);
     __syncthreads();
     if (w == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        acc[e] = part[0][e * 32 + lane];
-#pragma unroll
-        for (int i = 1; i < kEmbWarps; ++i) acc[e] += part[i][e * 32 + lane];
+      for (int i = 1; i < kEmbWarps; ++i) {
+        F2 v[4];
+        lds8(part[i], lane, v);
+        add8(acc, v);
       }
-      put_row<G, LAYOUT>(a, k, key, c0, lane, acc);
+      G* out = static_cast<G*>(a.grads[k]) + key * a.cols + c0;
+      if (a.accumulate) put_row<G, LAYOUT, true>(out, a.scale, left, lane, acc, load8<G, LAYOUT>(out, left, lane));
+      else put_row<G, LAYOUT, false>(out, a.scale, left, lane, acc, Raw8<G>{});
     }
     __syncthreads();
   }
@@ -498,10 +656,20 @@ template <typename T>
 int launch_lookup(const LookupArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
   return launch_pdl(vec ? lookup_kernel<T, kVec> : lookup_kernel<T, kStrided>, dim3(grid), dim3(kEmbThreads), 0, stream, a);
 }
+template <typename T, typename G, bool ADD>
+int launch_sum_as(const TableGradArgs& a, bool vec, bool sort, unsigned grid, cudaStream_t stream) {
+  auto kernel = vec ? (sort ? table_sum_kernel<T, G, kVec, true, ADD> : table_sum_kernel<T, G, kVec, false, ADD>)
+                    : (sort ? table_sum_kernel<T, G, kStrided, true, ADD> : table_sum_kernel<T, G, kStrided, false, ADD>);
+  constexpr size_t smem = sizeof(SumSmem<T, G, ADD>);
+  if (smem > 40 * 1024)  // (with the static part, more than the default 48 KiB)
+    if (cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); rc != cudaSuccess)
+      return static_cast<int>(rc);
+  return launch_pdl(kernel, dim3(grid), dim3(kEmbThreads), smem, stream, a);
+}
 template <typename T, typename G>
-int launch_sum(const TableGradArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
-  return launch_pdl(vec ? table_sum_kernel<T, G, kVec> : table_sum_kernel<T, G, kStrided>, dim3(grid), dim3(kEmbThreads), 0,
-                    stream, a);
+int launch_sum(const TableGradArgs& a, bool vec, bool sort, unsigned grid, cudaStream_t stream) {
+  return a.accumulate ? launch_sum_as<T, G, true>(a, vec, sort, grid, stream)
+                      : launch_sum_as<T, G, false>(a, vec, sort, grid, stream);
 }
 template <typename G>
 int launch_join(const TableGradArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
@@ -572,7 +740,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   if (adasum_status_t st = check_worker_offsets(worker_offsets, K)) return st;
   const int64_t n = worker_offsets[K];
   if (cols > INT32_MAX || n >= INT32_MAX || num_rows >= INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
-  if (chunk_bound(n, cols, K) * ((cols + kSlice - 1) / kSlice) > UINT32_MAX - kEmbWarps) return ADASUM_ERR_UNSUPPORTED;
+  if (chunk_bound(n, K) * ((cols + kSlice - 1) / kSlice) > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
   if (num_rows == 0) return ADASUM_OK;
   if (grads == nullptr || (n > 0 && (grad_out == nullptr || tokens == nullptr || ld < cols)))
     return ADASUM_ERR_INVALID_ARG;
@@ -586,24 +754,22 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   set.read(grad_out, span_bytes(n, cols, ld, e));
   set.read(tokens, n * token_bytes);
   set.write(scratch, need);
-  bool vec = is_aligned(grad_out, 16) && ld * e % 16 == 0 && cols * ge % 16 == 0 && cols % 4 == 0;
+  bool vec = is_aligned(grad_out, 16) && ld * e % 16 == 0 && cols * ge % 16 == 0 && cols * e % 16 == 0;
   int64_t most = 0;
-  const int chunk = chunk_tokens(n, cols);
+  for (int k = 0; k < K; ++k) most = std::max(most, worker_offsets[k + 1] - worker_offsets[k]);
+  a.part = warp_tokens(n, most, cols);
+  const int64_t span = static_cast<int64_t>(a.part) * kEmbWarps;
   for (int k = 0; k < K; ++k) {
     if (grads[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
     set.write(grads[k], num_rows * cols * ge);
     vec = vec && is_aligned(grads[k], 16);
     const int64_t nk = worker_offsets[k + 1] - worker_offsets[k];
-    most = std::max(most, nk);
     s.fill[k] = a.grads[k] = grads[k];
     s.off[k + 1] = a.off[k + 1] = worker_offsets[k + 1];
     s.tile_off[k + 1] = s.tile_off[k] + static_cast<int>((nk + kSortMost - 1) / kSortMost);
-    a.chunk_off[k + 1] = a.chunk_off[k] + static_cast<int>((nk + chunk - 1) / chunk);
+    a.chunk_off[k + 1] = a.chunk_off[k] + static_cast<int>((nk + span - 1) / span);
   }
   if (set.conflict()) return ADASUM_ERR_ALIAS;
-  const Scratch at(std::max<int64_t>(n, 0), cols, K);
-  char* base = static_cast<char*>(scratch);
-  auto ints = [&](int64_t offset) { return n > 0 ? reinterpret_cast<int*>(base + offset) : nullptr; };
   if (n == 0) {  // nothing to sum: zero the gradients, or leave them
     if (accumulate) return ADASUM_OK;
     for (int k = 0; k < K; ++k)
@@ -611,36 +777,46 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
         return ADASUM_ERR_CUDA;
     return ADASUM_OK;
   }
+  const Scratch at(n, cols, K);
+  char* base = static_cast<char*>(scratch);
+  auto ints = [&](int64_t offset) { return reinterpret_cast<int*>(base + offset); };
   // digits: as few passes of at most 8 bits as the keys 0..num_rows need
   int bits = 1;
   while ((num_rows >> bits) != 0) ++bits;
-  s.tokens = tokens;
-  s.token_bytes = token_bytes;
-  s.num_rows = static_cast<int>(num_rows);
-  s.padding_idx = padding_idx;
-  s.K = K;
+  s.tokens = a.tokens = tokens;
+  s.token_bytes = a.token_bytes = token_bytes;
+  s.num_rows = a.num_rows = static_cast<int>(num_rows);
+  s.padding_idx = a.padding_idx = padding_idx;
+  s.K = a.K = K;
   s.passes = (bits + 7) / 8;
   s.bits = (bits + s.passes - 1) / s.passes;
-  s.ntiles = s.tile_off[K];
   s.hist = ints(at.hist);
   s.join_count = ints(at.count);
   s.fill_bytes = accumulate ? 0 : num_rows * cols * ge;
   const int64_t fill_vecs = static_cast<int64_t>(K) * (s.fill_bytes / 16);
   s.fill_ctas = accumulate ? 0 : static_cast<int>(std::min<int64_t>(2 * sm_count(), 1 + fill_vecs / kSortThreads));
-  const int sorters = most <= kSortMost ? K : s.ntiles;
+  const bool self_sort = most <= kSelfSort;
   const double fill = static_cast<double>(K) * s.fill_bytes;
   int out = 0;  // which half of the key and position buffers holds the result
-  if (most <= kSortMost) {
+  if (self_sort) {  // only the zeroing, by the sort kernel with no worker to sort for
+    s.ntiles = 0;
+    if (!accumulate)
+      if (adasum_status_t st = counted_launch(stream, "table_fill", fill, [&] {
+            return launch_pdl(table_count_kernel, dim3(s.fill_ctas), dim3(kSortThreads), 0, stream, s);
+          }))
+        return st;
+  } else if (most <= kSortMost) {
     s.keys = ints(at.keys[0]);
     s.pos = ints(at.pos[0]);
     if (adasum_status_t st = counted_launch(stream, "table_sort", fill, [&] {
           if (int rc = allow_smem(reinterpret_cast<const void*>(table_sort_kernel), 0)) return rc;
-          return launch_pdl(table_sort_kernel, dim3(sorters + s.fill_ctas), dim3(kSortThreads), sizeof(SortSmem), stream, s);
+          return launch_pdl(table_sort_kernel, dim3(K + s.fill_ctas), dim3(kSortThreads), sizeof(SortSmem), stream, s);
         }))
       return st;
   } else {
+    s.ntiles = s.tile_off[K];
     if (adasum_status_t st = counted_launch(stream, "table_count", fill, [&] {
-          return launch_pdl(table_count_kernel, dim3(sorters + s.fill_ctas), dim3(kSortThreads), 0, stream, s);
+          return launch_pdl(table_count_kernel, dim3(s.ntiles + s.fill_ctas), dim3(kSortThreads), 0, stream, s);
         }))
       return st;
     for (s.pass = 0; s.pass < s.passes; ++s.pass) {
@@ -652,7 +828,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
       s.pos = ints(at.pos[out]);
       if (adasum_status_t st = counted_launch(stream, "table_scatter", 0.0, [&] {
             if (int rc = allow_smem(reinterpret_cast<const void*>(table_scatter_kernel), 1)) return rc;
-            return launch_pdl(table_scatter_kernel, dim3(sorters), dim3(kSortThreads), sizeof(SortSmem), stream, s);
+            return launch_pdl(table_scatter_kernel, dim3(s.ntiles), dim3(kSortThreads), sizeof(SortSmem), stream, s);
           }))
         return st;
     }
@@ -660,28 +836,26 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   a.dy = grad_out;
   a.cols = cols;
   a.ld = ld;
-  a.num_rows = static_cast<int>(num_rows);
   a.scale = scale;
-  a.grad_dtype = static_cast<int>(grad_dtype);
   a.accumulate = accumulate != 0;
-  a.K = K;
-  a.chunk = chunk;
   a.slices = static_cast<int>((cols + kSlice - 1) / kSlice);
-  a.nchunks = a.chunk_off[K];
   a.keys = ints(at.keys[out]);
   a.pos = ints(at.pos[out]);
   a.count = ints(at.count);
   a.list = ints(at.list);
   a.partials = reinterpret_cast<float*>(base + at.partials);
-  const int64_t grid = (a.nchunks * a.slices + kEmbWarps - 1) / kEmbWarps;
-  const unsigned g = static_cast<unsigned>(grid);
+  const int64_t items = static_cast<int64_t>(a.chunk_off[K]) * a.slices;
+  const unsigned grid = static_cast<unsigned>(items);
   if (adasum_status_t st = counted_launch(stream, "table_sum", static_cast<double>(n) * (cols * e + 8), [&] {
         if (dtype == ADASUM_BF16)
-          return grad_dtype == ADASUM_BF16 ? launch_sum<bf16, bf16>(a, vec, g, stream) : launch_sum<bf16, float>(a, vec, g, stream);
-        return grad_dtype == ADASUM_BF16 ? launch_sum<float, bf16>(a, vec, g, stream) : launch_sum<float, float>(a, vec, g, stream);
+          return grad_dtype == ADASUM_BF16 ? launch_sum<bf16, bf16>(a, vec, self_sort, grid, stream)
+                                           : launch_sum<bf16, float>(a, vec, self_sort, grid, stream);
+        return grad_dtype == ADASUM_BF16 ? launch_sum<float, bf16>(a, vec, self_sort, grid, stream)
+                                         : launch_sum<float, float>(a, vec, self_sort, grid, stream);
       }))
     return st;
-  const unsigned joiners = static_cast<unsigned>(std::min<int64_t>(a.nchunks * a.slices, 4 * static_cast<int64_t>(sm_count())));
+  if (most <= span) return ADASUM_OK;  // no worker has a second chunk, so no run crosses chunks
+  const unsigned joiners = static_cast<unsigned>(std::min<int64_t>(items, 4 * static_cast<int64_t>(sm_count())));
   return counted_launch(stream, "table_join", 0.0, [&] {
     return grad_dtype == ADASUM_BF16 ? launch_join<bf16>(a, vec, joiners, stream) : launch_join<float>(a, vec, joiners, stream);
   });

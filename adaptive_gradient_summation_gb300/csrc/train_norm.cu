@@ -8,15 +8,6 @@ namespace adasum {
 namespace {
 
 constexpr int kSlice = 256;        // columns of a warp's eight per lane
-#ifndef NV_F
-#define NV_F 4
-#endif
-#ifndef CTA_F
-#define CTA_F 4
-#endif
-#ifndef OCC_F
-#define OCC_F 1
-#endif
 constexpr int kNormCtasPerSm = 2;  // of the persistent grids
 
 struct NormArgs {
@@ -84,12 +75,31 @@ struct Team {
 };
 
 // The weight and bias of a CTA's columns as floats in shared memory, 1 and 0 where absent.
-template <int COLS, int THREADS>
+template <int LAYOUT, int COLS, int THREADS>
 __device__ __forceinline__ void stage_params(float* w, float* b, const void* weight, const void* bias, int dtype,
                                              int64_t cols) {
-  for (int c = threadIdx.x; c < COLS; c += THREADS) {
-    if (w) w[c] = c < cols && weight ? load_any(weight, dtype, c) : 1.f;
-    if (b) b[c] = c < cols && bias ? load_any(bias, dtype, c) : 0.f;
+  for (int i = threadIdx.x; i < COLS; i += THREADS) {
+    const int c = smem_col<LAYOUT>(i);
+    if (w) w[i] = c < cols && weight ? load_any(weight, dtype, c) : 1.f;
+    if (b) b[i] = c < cols && bias ? load_any(bias, dtype, c) : 0.f;
+  }
+}
+
+__device__ __forceinline__ float sum_parts(F2 x) {
+  const float2 p = parts(x);
+  return p.x + p.y;
+}
+
+// Zeroes the columns past the row's end in the slice where it lies.
+template <int LAYOUT>
+__device__ __forceinline__ void clear_past(F2 (&v)[4], int left, int lane) {
+  if (left >= kSlice) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 p = parts(v[i]);
+    if (lane_col<LAYOUT>(lane, 2 * i) >= left) p.x = 0.f;
+    if (lane_col<LAYOUT>(lane, 2 * i + 1) >= left) p.y = 0.f;
+    v[i] = f2(p.x, p.y);
   }
 }
 
@@ -99,75 +109,80 @@ __device__ __forceinline__ void stage_params(float* w, float* b, const void* wei
 //     mean = sum n_w m_w / n,   S = sum S_w + n_w (m_w - mean)^2.
 // Bound by the bytes of x and y; the next row is on its way while one is worked on.
 template <typename T, int LAYOUT, int W, int NV, bool KEEP>
-__global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? OCC_F : 1) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm : 1) norm_kernel(const NormArgs a) {
   using TM = Team<W, NV>;
   pdl_enter();
   extern __shared__ __align__(16) float sm[];
   float *ws = sm, *bs = sm + TM::kCols;
   __shared__ float2 ex[2][TM::kTeams][W];
-  stage_params<TM::kCols, TM::kThreads>(ws, bs, a.weight, a.bias, a.weight_dtype, a.cols);
+  stage_params<LAYOUT, TM::kCols, TM::kThreads>(ws, bs, a.weight, a.bias, a.weight_dtype, a.cols);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / W, w = warp % W;
   const float inv_n = 1.f / static_cast<float>(a.cols);
   const int64_t step = static_cast<int64_t>(gridDim.x) * TM::kTeams;
   const int64_t pitch = ckpt_pitch(a.cols), nscales = ckpt_scales(a.cols);
-  auto left_of = [&](int j) { return a.cols - (j * W + w) * kSlice; };
+  int left[NV], count = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) count += left[j] = slice_left(a.cols, (j * W + w) * kSlice);
+  const float inv_count = count > 0 ? 1.f / static_cast<float>(count) : 0.f;
   Raw8<T> next[NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       next[j] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld + (j * W + w) * kSlice,
-                                 row < a.rows ? left_of(j) : 0, lane);
+                                 row < a.rows ? left[j] : 0, lane);
   };
   int64_t row = static_cast<int64_t>(blockIdx.x) * TM::kTeams + team;
   fetch(row);
   for (int it = 0; row < a.rows; row += step, it ^= 1) {
-    Raw8<T> r[NV];
-    float sum = 0.f, count = 0.f;
+    F2 v[NV][4], acc = f2(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      r[j] = next[j];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += raw_value<T>(r[j], e);
-      count += static_cast<float>(max(static_cast<int64_t>(0), min(left_of(j), static_cast<int64_t>(kSlice))));
-    }
+    for (int j = 0; j < NV; ++j) unpack8<T>(next[j], v[j]);
     fetch(row + step);
-    sum = warp_sum(sum);
-    float mean = W == 1 ? sum * inv_n : (count > 0.f ? sum / count : 0.f);
-    float sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc = add2(acc, v[j][i]);
+    float mean = warp_sum(sum_parts(acc)) * (W == 1 ? inv_n : inv_count);
+    acc = f2(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int64_t left = left_of(j);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = raw_value<T>(r[j], e) - mean;
-        if (left >= kSlice || lane_col<LAYOUT>(lane, e) < left) sq = __fmaf_rn(d, d, sq);
-      }
+      for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], f2(-mean));
+      clear_past<LAYOUT>(v[j], left[j], lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc = fma2(v[j][i], v[j][i], acc);
     }
-    sq = warp_sum(sq);
+    float sq = warp_sum(sum_parts(acc));
     if constexpr (W > 1) {
       if (lane == 0) ex[it][team][w] = make_float2(mean, sq);
       TM::sync(team);
-      float total = 0.f;
       auto columns = [&](int i) {  // of warp i
-        float n = 0.f;
+        int n = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          n += static_cast<float>(max(static_cast<int64_t>(0), min(a.cols - (j * W + i) * kSlice, static_cast<int64_t>(kSlice))));
-        return n;
+        for (int j = 0; j < NV; ++j) n += slice_left(a.cols, (j * W + i) * kSlice);
+        return static_cast<float>(n);
       };
-      float2 v[W];
+      const float mine = mean;
+      float total = 0.f;
+      float2 p[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        v[i] = ex[it][team][i];
-        total = __fmaf_rn(columns(i), v[i].x, total);
+        p[i] = ex[it][team][i];
+        total = __fmaf_rn(columns(i), p[i].x, total);
       }
       mean = total * inv_n;
       sq = 0.f;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const float d = v[i].x - mean;
-        sq += __fmaf_rn(columns(i) * d, d, v[i].y);
+        const float d = p[i].x - mean;
+        sq += __fmaf_rn(columns(i) * d, d, p[i].y);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], f2(mine - mean));
+        if (KEEP) clear_past<LAYOUT>(v[j], left[j], lane);
       }
     }
     const float rstd = 1.f / sqrtf(__fmaf_rn(sq, inv_n, a.eps));
@@ -175,45 +190,52 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? OCC_F : 1) nor
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
     }
-    auto row_h = [&](int j, float (&h)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = (raw_value<T>(r[j], e) - mean) * rstd;
-      if (KEEP && left_of(j) < kSlice) {
+    for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (lane_col<LAYOUT>(lane, e) >= left_of(j)) h[e] = 0.f;
-      }
-    };
+      for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], f2(rstd));
     CkptScale sc[KEEP ? NV : 1][2];
     if constexpr (KEEP) {
       float top[NV][2];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        float h[8];
-        row_h(j, h);
-        block_tops<LAYOUT>(h, top[j]);
-      }
+      for (int j = 0; j < NV; ++j) block_tops<LAYOUT>(v[j], top[j]);
       block_scales<LAYOUT, NV>(top, lane, sc);
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c0 = (j * W + w) * kSlice;
-      const int64_t left = left_of(j);
-      if (left <= 0) break;
-      float h[8], wv[8], bv[8];
-row_h(j, h);
+      if (left[j] <= 0) break;
       if constexpr (KEEP) {
-        store_codes8<LAYOUT>(a.codes + row * pitch + c0, left, lane, ckpt_codes<LAYOUT>(h, sc[j]));
-        store_scales<LAYOUT>(a.scales + row * nscales + c0 / kCkptBlock, left, lane, sc[j]);
+        store_codes8<LAYOUT>(a.codes + row * pitch + c0, left[j], lane, ckpt_codes<LAYOUT>(v[j], sc[j]));
+        store_scales<LAYOUT>(a.scales + row * nscales + c0 / kCkptBlock, left[j], lane, sc[j]);
       }
-      lds8<LAYOUT>(ws + c0, lane, wv);
-      lds8<LAYOUT>(bs + c0, lane, bv);
+      F2 wv[4], bv[4];
+      lds8(ws + c0, lane, wv);
+      lds8(bs + c0, lane, bv);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = __fmaf_rn(h[e], wv[e], bv[e]);
-      store8<T, LAYOUT>(static_cast<T*>(a.y) + row * a.cols + c0, left, lane, h);
+      for (int i = 0; i < 4; ++i) v[j][i] = fma2(v[j][i], wv[i], bv[i]);
+      store8<T, LAYOUT>(static_cast<T*>(a.y) + row * a.cols + c0, left[j], lane, v[j]);
     }
   }
 }
+
+// Rows of dy and x (or of h's codes) on their way to the gradient kernel.  kVec: a lane
+// copies the bytes that it will use itself to shared memory, kStages rows ahead, so that the
+// copies take no registers and need no barrier.  kStrided: no row ahead.
+template <typename T, int NV, bool KEPT>
+struct RowCopy {
+  static constexpr int kVecs = sizeof(T) / 2;  // 16-byte vectors of a lane's eight
+  uint4 dy[NV][kVecs][32];
+  uint4 x[KEPT ? 1 : NV][KEPT ? 1 : kVecs][KEPT ? 1 : 32];
+  uint2 q[KEPT ? NV : 1][KEPT ? 32 : 1];
+};
+template <typename T, int W, int NV>
+struct GradShape {
+  static constexpr int kStages = W * NV > 32 && sizeof(T) == 4 ? 1 : 2;
+  // g and h of the row are computed twice instead of kept in registers
+  static constexpr bool kTwice = NV > 2;
+  static constexpr int kCtas = W < 16 ? kNormCtasPerSm : 1;
+};
 
 // The gradient.  With g = dy w and h the normalised row,
 //     dx = rstd (g - mean(g) - h mean(g h)),   dw += dy h,   db += dy:
@@ -221,14 +243,18 @@ row_h(j, h);
 // CTA's rows in registers, joined over its teams at the end and written as the CTA's partial.
 // A CTA's rows all belong to one worker.  Bound by the bytes of dy, x and dx.
 template <typename T, int LAYOUT, int W, int NV, bool KEPT>
-__global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? 2 : 1) norm_grad_kernel(const NormGradArgs a,
-                                                                         const __grid_constant__ WorkerRows rows) {
+__global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kCtas)
+    norm_grad_kernel(const NormGradArgs a, const __grid_constant__ WorkerRows rows) {
   using TM = Team<W, NV>;
+  using Copy = RowCopy<T, NV, KEPT>;
+  constexpr int S = GradShape<T, W, NV>::kStages;
+  constexpr bool kTwice = GradShape<T, W, NV>::kTwice;
   pdl_enter();
-  extern __shared__ __align__(16) float sm[];  // weight, bias; at the end the teams' sums
+  extern __shared__ __align__(16) float sm[];  // weight, bias (KEPT), copies; at the end the teams' sums
   float *ws = sm, *bs = sm + TM::kCols;
+  Copy* copies = reinterpret_cast<Copy*>(sm + (KEPT ? 2 : 1) * TM::kCols);
   __shared__ float2 ex[2][TM::kTeams][W];
-  stage_params<TM::kCols, TM::kThreads>(ws, KEPT ? bs : nullptr, a.weight, a.bias, a.weight_dtype, a.cols);
+  stage_params<LAYOUT, TM::kCols, TM::kThreads>(ws, KEPT ? bs : nullptr, a.weight, a.bias, a.weight_dtype, a.cols);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / W, w = warp % W;
   const float inv_n = 1.f / static_cast<float>(a.cols);
@@ -241,78 +267,121 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? 2 : 1) norm_gr
   }
   const int64_t r0 = rows.off[k] + static_cast<int64_t>(blockIdx.x - rows.cta_off[k]) * rows.rows_per_cta;
   const int64_t r1 = min(r0 + rows.rows_per_cta, rows.off[k + 1]);
-  auto left_of = [&](int j) { return a.cols - (j * W + w) * kSlice; };
-  float dw[NV][8], db[NV][8];
+  int left[NV];
+  F2 dw[NV][4], db[NV][4];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    left[j] = slice_left(a.cols, (j * W + w) * kSlice);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[j][e] = db[j][e] = 0.f;
-  struct Row {
-    Raw8<T> dy[NV], x[KEPT ? 1 : NV];
-    uint2 q[KEPT ? NV : 1];
-    float scale[KEPT ? NV : 1][2];
-    float mean, rstd;
-  } next;
-  auto fetch = [&](int64_t row) {
-    const bool in = row < r1;
+    for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = f2(0.f);
+  }
+  auto issue = [&](int64_t row, int stage) {
+    if constexpr (LAYOUT == kVec) {
+      if (row < r1) {
+        Copy& c = copies[stage * TM::kWarps + warp];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c0 = (j * W + w) * kSlice;
-      const int64_t left = in ? left_of(j) : 0;
-      next.dy[j] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left, lane);
-      if constexpr (KEPT) {
-        next.q[j] = load_codes8<LAYOUT>(a.codes + row * pitch + c0, left, lane);
-        const float* s = a.scales + row * nscales + c0 / kCkptBlock;
-        if constexpr (LAYOUT == kVec) {
-          next.scale[j][0] = lane * 8 < left ? s[lane >> 4] : 0.f;
-          next.scale[j][1] = next.scale[j][0];
-        } else {
-          next.scale[j][0] = left > 0 ? s[0] : 0.f;
-          next.scale[j][1] = left > kCkptBlock ? s[1] : 0.f;
+        for (int j = 0; j < NV; ++j) {
+          const int c0 = (j * W + w) * kSlice;
+          const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy + c0;
+#pragma unroll
+          for (int v = 0; v < Copy::kVecs; ++v) {
+            const int at = lane * 8 + v * 16 / static_cast<int>(sizeof(T));
+            const int bytes = max(0, min(16, (left[j] - at) * static_cast<int>(sizeof(T))));
+            const int from = bytes > 0 ? at : 0;
+            cp_async16(smem_addr(&c.dy[j][v][lane]), dy + from, bytes);
+            if constexpr (!KEPT) {
+              const T* x = static_cast<const T*>(a.x) + row * a.ld_x + c0;
+              cp_async16(smem_addr(&c.x[j][v][lane]), x + from, bytes);
+            }
+          }
+          if constexpr (KEPT) {  // (rows of codes are padded, so a begun eight is always there)
+            const bool in = lane * 8 < left[j];
+            cp_async8(smem_addr(&c.q[j][lane]), a.codes + row * pitch + c0 + (in ? lane * 8 : 0), in ? 8 : 0);
+          }
         }
-      } else {
-        next.x[j] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld_x + c0, left, lane);
       }
+      cp_async_commit();
     }
-    next.mean = !KEPT && in ? a.mean[row] : 0.f;
-    next.rstd = in ? a.rstd[row] : 0.f;
+  };
+  // dy and h of slice j of the row
+  auto take = [&](int64_t row, int stage, int j, float mean, float rstd, float s0, float s1, F2 (&dy)[4], F2 (&h)[4]) {
+    const int c0 = (j * W + w) * kSlice;
+    if constexpr (LAYOUT == kVec) {
+      const Copy& c = copies[stage * TM::kWarps + warp];
+      auto raw = [&](const uint4 (&v)[Copy::kVecs][32], F2 (&to)[4]) {
+        Raw8<T> r;
+#pragma unroll
+        for (int i = 0; i < Copy::kVecs; ++i) {
+          const uint4 u = v[i][lane];
+          r.w[4 * i] = u.x;
+          r.w[4 * i + 1] = u.y;
+          r.w[4 * i + 2] = u.z;
+          r.w[4 * i + 3] = u.w;
+        }
+        unpack8<T>(r, to);
+      };
+      raw(c.dy[j], dy);
+      if constexpr (KEPT) ckpt_values8(c.q[j][lane], s0, s1, h);
+      else raw(c.x[j], h);
+    } else {
+      unpack8<T>(load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left[j], lane), dy);
+      if constexpr (KEPT) ckpt_values8(load_codes8<LAYOUT>(a.codes + row * pitch + c0, left[j], lane), s0, s1, h);
+      else unpack8<T>(load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld_x + c0, left[j], lane), h);
+    }
+    if constexpr (!KEPT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = mul2(add2(h[i], f2(-mean)), f2(rstd));
+      clear_past<LAYOUT>(h, left[j], lane);
+    }
   };
   int64_t row = r0 + team;
-  fetch(row);
-  for (int it = 0; row < r1; row += TM::kTeams, it ^= 1) {
-    const Row cur = next;
-    fetch(row + TM::kTeams);
-    float sg = 0.f, sgh = 0.f;
-    auto row_h = [&](int j, float (&h)[8]) {
-      if constexpr (KEPT) {
-        ckpt_values8(cur.q[j], cur.scale[j][0], cur.scale[j][1], h);
-      } else {
-        const int64_t left = left_of(j);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = (raw_value<T>(cur.x[j], e) - cur.mean) * cur.rstd;
-        if (left < kSlice) {
+  for (int s = 0; s < S; ++s) issue(row + s * TM::kTeams, s);
+  struct Stats {
+    float mean, rstd, scale[KEPT ? NV : 1][2];
+  } next;
+  auto stats = [&](int64_t row) {
+    const bool in = row < r1;
+    next.mean = !KEPT && in ? a.mean[row] : 0.f;
+    next.rstd = in ? a.rstd[row] : 0.f;
+    if constexpr (KEPT) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (lane_col<LAYOUT>(lane, e) >= left) h[e] = 0.f;
+      for (int j = 0; j < NV; ++j) {
+        const int n = in ? left[j] : 0;
+        const float* s = a.scales + row * nscales + (j * W + w) * (kSlice / kCkptBlock);
+        if constexpr (LAYOUT == kVec) {
+          next.scale[j][0] = next.scale[j][1] = lane * 8 < n ? s[lane >> 4] : 0.f;
+        } else {
+          next.scale[j][0] = n > 0 ? s[0] : 0.f;
+          next.scale[j][1] = n > kCkptBlock ? s[1] : 0.f;
         }
       }
-    };
+    }
+  };
+  stats(row);
+  int stage = 0;
+  for (int it = 0; row < r1; row += TM::kTeams, it ^= 1, stage = stage + 1 == S ? 0 : stage + 1) {
+    const Stats cur = next;
+    stats(row + TM::kTeams);
+    if constexpr (LAYOUT == kVec) cp_async_wait<S - 1>();
+    F2 g[kTwice ? 1 : NV][4], h[kTwice ? 1 : NV][4], sg2 = f2(0.f), sgh2 = f2(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float h[8], wv[8];
-      row_h(j, h);
-      lds8<LAYOUT>(ws + (j * W + w) * kSlice, lane, wv);
+      const int at = kTwice ? 0 : j;
+      take(row, stage, j, cur.mean, cur.rstd, cur.scale[KEPT ? j : 0][0], cur.scale[KEPT ? j : 0][1], g[at], h[at]);
+      F2 wv[4];
+      lds8(ws + (j * W + w) * kSlice, lane, wv);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = raw_value<T>(cur.dy[j], e), g = d * wv[e];
-        sg += g;
-        sgh = __fmaf_rn(g, h[e], sgh);
-        dw[j][e] = __fmaf_rn(d, h[e], dw[j][e]);
-        db[j][e] += d;
+      for (int i = 0; i < 4; ++i) {
+        dw[j][i] = fma2(g[at][i], h[at][i], dw[j][i]);
+        db[j][i] = add2(g[at][i], db[j][i]);
+        g[at][i] = mul2(g[at][i], wv[i]);
+        sg2 = add2(sg2, g[at][i]);
+        sgh2 = fma2(g[at][i], h[at][i], sgh2);
       }
     }
-    sg = warp_sum(sg);
-    sgh = warp_sum(sgh);
+    if constexpr (!kTwice) issue(row + S * TM::kTeams, stage);
+    float sg = warp_sum(sum_parts(sg2)), sgh = warp_sum(sum_parts(sgh2));
     if constexpr (W > 1) {
       if (lane == 0) ex[it][team][w] = make_float2(sg, sgh);
       TM::sync(team);
@@ -323,27 +392,30 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? 2 : 1) norm_gr
         sgh += ex[it][team][i].y;
       }
     }
-    const float mg = sg * inv_n * cur.rstd, mgh = sgh * inv_n * cur.rstd;
+    const F2 mg = f2(-sg * inv_n * cur.rstd), mgh = f2(-sgh * inv_n * cur.rstd), r = f2(cur.rstd);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c0 = (j * W + w) * kSlice;
-      const int64_t left = left_of(j);
-      if (left <= 0) break;
-      float h[8], wv[8], v[8];
-      row_h(j, h);
-      lds8<LAYOUT>(ws + c0, lane, wv);
+      const int c0 = (j * W + w) * kSlice, at = kTwice ? 0 : j;
+      if (left[j] <= 0) break;
+      F2 wv[4];
+      if (kTwice || (KEPT && a.y != nullptr)) lds8(ws + c0, lane, wv);
+      if constexpr (kTwice) {
+        take(row, stage, j, cur.mean, cur.rstd, cur.scale[KEPT ? j : 0][0], cur.scale[KEPT ? j : 0][1], g[0], h[0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = __fmaf_rn(raw_value<T>(cur.dy[j], e) * wv[e], cur.rstd, -mg) - h[e] * mgh;
-      store8<T, LAYOUT>(static_cast<T*>(a.dx) + row * a.cols + c0, left, lane, v);
+        for (int i = 0; i < 4; ++i) g[0][i] = mul2(g[0][i], wv[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[at][i] = fma2(h[at][i], mgh, fma2(g[at][i], r, mg));
+      store8<T, LAYOUT>(static_cast<T*>(a.dx) + row * a.cols + c0, left[j], lane, g[at]);
       if (KEPT && a.y != nullptr) {
-        float bv[8];
-        lds8<LAYOUT>(bs + c0, lane, bv);
+        F2 bv[4];
+        lds8(bs + c0, lane, bv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __fmaf_rn(h[e], wv[e], bv[e]);
-        store8<T, LAYOUT>(static_cast<T*>(a.y) + row * a.cols + c0, left, lane, v);
+        for (int i = 0; i < 4; ++i) h[at][i] = fma2(h[at][i], wv[i], bv[i]);
+        store8<T, LAYOUT>(static_cast<T*>(a.y) + row * a.cols + c0, left[j], lane, h[at]);
       }
     }
+    if constexpr (kTwice) issue(row + S * TM::kTeams, stage);
   }
   if (a.partials == nullptr) return;
   float* out = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
@@ -352,24 +424,31 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? 2 : 1) norm_gr
     for (int j = 0; j < NV; ++j) {
       const int c0 = (j * W + w) * kSlice;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = c0 + lane_col<LAYOUT>(lane, e);
-        if (c >= a.cols) continue;
-        out[c] = dw[j][e];
-        out[a.cols + c] = db[j][e];
+      for (int i = 0; i < 4; ++i) {
+        const float2 pw = parts(dw[j][i]), pb = parts(db[j][i]);
+        const int c = lane_col<LAYOUT>(lane, 2 * i), d = lane_col<LAYOUT>(lane, 2 * i + 1);
+        if (c < left[j]) {
+          out[c0 + c] = pw.x;
+          out[a.cols + c0 + c] = pb.x;
+        }
+        if (d < left[j]) {
+          out[c0 + d] = pw.y;
+          out[a.cols + c0 + d] = pb.y;
+        }
       }
     }
   } else {
+    if constexpr (LAYOUT == kVec) cp_async_wait<0>();
     __syncthreads();
     float* mine = sm + team * 2 * TM::kCols;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      sts8<LAYOUT>(mine + (j * W + w) * kSlice, lane, dw[j]);
-      sts8<LAYOUT>(mine + TM::kCols + (j * W + w) * kSlice, lane, db[j]);
+      sts8(mine + (j * W + w) * kSlice, lane, dw[j]);
+      sts8(mine + TM::kCols + (j * W + w) * kSlice, lane, db[j]);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * TM::kCols; i += TM::kThreads) {
-      const int c = i % TM::kCols;
+      const int c = smem_col<LAYOUT>(i % TM::kCols);
       if (c >= a.cols) continue;
       float s = 0.f;
 #pragma unroll
@@ -404,7 +483,7 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant_
 
 // Allows a kernel its shared memory where that is more than the default.
 int allow_smem(const void* kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ? 0
+  return bytes <= 40 * 1024 ? 0  // (48 KiB, less the static part)
                             : static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                     static_cast<int>(bytes)));
 }
@@ -416,14 +495,13 @@ int launch_norm_as(const NormArgs& a, cudaStream_t stream) {
   auto kernel = a.codes ? norm_kernel<T, LAYOUT, W, NV, true> : norm_kernel<T, LAYOUT, W, NV, false>;
   if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem)) return rc;
   const int64_t need = (a.rows + TM::kTeams - 1) / TM::kTeams;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(CTA_F) * sm_count()));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(kNormCtasPerSm) * sm_count()));
   return launch_pdl(kernel, dim3(grid), dim3(TM::kThreads), smem, stream, a);
 }
 // The smallest team that holds a row: up to four slices a warp, then more warps.
 template <typename T, int LAYOUT>
 int launch_norm(const NormArgs& a, cudaStream_t stream) {
   const int64_t slices = (a.cols + kSlice - 1) / kSlice;
-#if NV_F == 4
   if (slices <= 1) return launch_norm_as<T, LAYOUT, 1, 1>(a, stream);
   if (slices <= 2) return launch_norm_as<T, LAYOUT, 1, 2>(a, stream);
   if (slices <= 4) return launch_norm_as<T, LAYOUT, 1, 4>(a, stream);
@@ -431,30 +509,16 @@ int launch_norm(const NormArgs& a, cudaStream_t stream) {
   if (slices <= 16) return launch_norm_as<T, LAYOUT, 4, 4>(a, stream);
   if (slices <= 32) return launch_norm_as<T, LAYOUT, 8, 4>(a, stream);
   return launch_norm_as<T, LAYOUT, 16, 4>(a, stream);
-#elif NV_F == 2
-  if (slices <= 1) return launch_norm_as<T, LAYOUT, 1, 1>(a, stream);
-  if (slices <= 2) return launch_norm_as<T, LAYOUT, 1, 2>(a, stream);
-  if (slices <= 4) return launch_norm_as<T, LAYOUT, 2, 2>(a, stream);
-  if (slices <= 8) return launch_norm_as<T, LAYOUT, 4, 2>(a, stream);
-  if (slices <= 16) return launch_norm_as<T, LAYOUT, 8, 2>(a, stream);
-  if (slices <= 32) return launch_norm_as<T, LAYOUT, 16, 2>(a, stream);
-  return launch_norm_as<T, LAYOUT, 16, 4>(a, stream);
-#else
-  if (slices <= 1) return launch_norm_as<T, LAYOUT, 1, 1>(a, stream);
-  if (slices <= 2) return launch_norm_as<T, LAYOUT, 2, 1>(a, stream);
-  if (slices <= 4) return launch_norm_as<T, LAYOUT, 4, 1>(a, stream);
-  if (slices <= 8) return launch_norm_as<T, LAYOUT, 8, 1>(a, stream);
-  if (slices <= 16) return launch_norm_as<T, LAYOUT, 8, 2>(a, stream);
-  if (slices <= 32) return launch_norm_as<T, LAYOUT, 16, 2>(a, stream);
-  return launch_norm_as<T, LAYOUT, 16, 4>(a, stream);
-#endif
 }
 
-template <typename T, int LAYOUT, int W, int NV>
+template <typename T, int LAYOUT, int W, int NV, bool KEPT>
 int launch_norm_grad_as(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
   using TM = Team<W, NV>;
-  const size_t smem = (TM::kTeams == 1 ? 1 : TM::kTeams) * 2 * TM::kCols * sizeof(float);
-  auto kernel = a.codes ? norm_grad_kernel<T, LAYOUT, W, NV, true> : norm_grad_kernel<T, LAYOUT, W, NV, false>;
+  const size_t work = (KEPT ? 2 : 1) * TM::kCols * sizeof(float) +
+                      (LAYOUT == kVec ? GradShape<T, W, NV>::kStages * TM::kWarps * sizeof(RowCopy<T, NV, KEPT>) : 0);
+  const size_t sums = TM::kTeams == 1 ? 0 : TM::kTeams * 2 * TM::kCols * sizeof(float);
+  const size_t smem = std::max(work, sums);
+  auto kernel = norm_grad_kernel<T, LAYOUT, W, NV, KEPT>;
   if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem)) return rc;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(rows.cta_off[rows.K])), dim3(TM::kThreads), smem, stream, a, rows);
 }
@@ -463,16 +527,21 @@ int grad_teams(int64_t cols) {
   const int64_t slices = (cols + kSlice - 1) / kSlice;
   return slices <= 2 ? 8 : slices <= 4 ? 4 : slices <= 8 ? 2 : 1;
 }
+template <typename T, int LAYOUT, bool KEPT>
+int launch_norm_grad_kept(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
+  const int64_t slices = (a.cols + kSlice - 1) / kSlice;
+  if (slices <= 1) return launch_norm_grad_as<T, LAYOUT, 1, 1, KEPT>(a, rows, stream);
+  if (slices <= 2) return launch_norm_grad_as<T, LAYOUT, 1, 2, KEPT>(a, rows, stream);
+  if (slices <= 4) return launch_norm_grad_as<T, LAYOUT, 2, 2, KEPT>(a, rows, stream);
+  if (slices <= 8) return launch_norm_grad_as<T, LAYOUT, 4, 2, KEPT>(a, rows, stream);
+  if (slices <= 16) return launch_norm_grad_as<T, LAYOUT, 8, 2, KEPT>(a, rows, stream);
+  if (slices <= 32) return launch_norm_grad_as<T, LAYOUT, 16, 2, KEPT>(a, rows, stream);
+  return launch_norm_grad_as<T, LAYOUT, 16, 4, KEPT>(a, rows, stream);
+}
 template <typename T, int LAYOUT>
 int launch_norm_grad(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
-  const int64_t slices = (a.cols + kSlice - 1) / kSlice;
-  if (slices <= 1) return launch_norm_grad_as<T, LAYOUT, 1, 1>(a, rows, stream);
-  if (slices <= 2) return launch_norm_grad_as<T, LAYOUT, 1, 2>(a, rows, stream);
-  if (slices <= 4) return launch_norm_grad_as<T, LAYOUT, 2, 2>(a, rows, stream);
-  if (slices <= 8) return launch_norm_grad_as<T, LAYOUT, 4, 2>(a, rows, stream);
-  if (slices <= 16) return launch_norm_grad_as<T, LAYOUT, 8, 2>(a, rows, stream);
-  if (slices <= 32) return launch_norm_grad_as<T, LAYOUT, 16, 2>(a, rows, stream);
-  return launch_norm_grad_as<T, LAYOUT, 16, 4>(a, rows, stream);
+  return a.codes ? launch_norm_grad_kept<T, LAYOUT, true>(a, rows, stream)
+                 : launch_norm_grad_kept<T, LAYOUT, false>(a, rows, stream);
 }
 
 // Deals the workers' rows to at most about `target` CTAs, none of them to two workers.
