@@ -99,4 +99,21 @@ inline int sm_count() {
   return known[dev];
 }
 
+// Allows a kernel `bytes` of dynamic shared memory where that is (with its static part) more
+// than the default 48 KiB; asked of the runtime once per device.  `known` belongs to the
+// kernel and its size.
+struct SmemAllowed {
+  bool on[64] = {};
+};
+template <typename Kernel>
+int allow_smem(Kernel* kernel, size_t bytes, SmemAllowed& known) {
+  if (bytes <= 40 * 1024) return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return static_cast<int>(cudaErrorInvalidDevice);
+  if (dev >= 0 && dev < 64 && known.on[dev]) return 0;
+  const cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (rc == cudaSuccess && dev >= 0 && dev < 64) known.on[dev] = true;
+  return static_cast<int>(rc);
+}
+
 }  // namespace adasum

@@ -124,6 +124,19 @@ __device__ __forceinline__ void unpack8(const Raw8<T>& r, F2 (&v)[4]) {
   for (int i = 0; i < 4; ++i) v[i] = f2(raw_value<T>(r, 2 * i), raw_value<T>(r, 2 * i + 1));
 }
 
+// A lane's eight values from its 16-byte vectors in shared memory.
+template <typename T>
+__device__ __forceinline__ void gather8(Raw8<T>& r, const uint4 (&from)[sizeof(T) / 2][32], int lane) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
+    const uint4 x = from[i][lane];
+    r.w[4 * i] = x.x;
+    r.w[4 * i + 1] = x.y;
+    r.w[4 * i + 2] = x.z;
+    r.w[4 * i + 3] = x.w;
+  }
+}
+
 // Columns of a slice that starts at c0, at most 256, none past the row's end.
 __device__ __forceinline__ int slice_left(int64_t cols, int64_t c0) {
   return static_cast<int>(max(static_cast<int64_t>(0), min(cols - c0, static_cast<int64_t>(256))));

@@ -109,52 +109,64 @@ struct UnpackArgs {
 // before it works on the first.  Bound by bytes: each value is read and written once.
 //
 // Where a warp is, as offsets into the buffers, so that going on costs additions only.
+// DENSE: everything is one long row, and all offsets are the same.
+template <bool DENSE>
 struct Cursor {
-  int64_t in, out, codes, scales;  // the strided input, a dense output, codes, scales
   int64_t c0, cols;
+  int64_t in, out, codes, scales;  // the strided input, a dense output, codes, scales
   template <typename A>
   __device__ __forceinline__ Cursor(const A& a, int64_t ld, uint32_t item) {
-    const int64_t row = item / a.slices;
-    c0 = static_cast<int64_t>(item - static_cast<uint32_t>(row) * a.slices) * kSlice;
     cols = a.cols;
-    in = row * ld + c0;
-    out = row * a.cols + c0;
-    codes = row * a.pitch + c0;
-    scales = row * a.nscales + c0 / kCkptBlock;
+    if constexpr (DENSE) {
+      c0 = static_cast<int64_t>(item) * kSlice;
+    } else {
+      const int64_t row = item / a.slices;
+      c0 = static_cast<int64_t>(item - static_cast<uint32_t>(row) * a.slices) * kSlice;
+      in = row * ld + c0;
+      out = row * a.cols + c0;
+      codes = row * a.pitch + c0;
+      scales = row * a.nscales + c0 / kCkptBlock;
+    }
   }
   template <typename A>
   __device__ __forceinline__ void next(const A& a, int64_t ld) {
     c0 += kSlice;
-    in += kSlice;
-    out += kSlice;
-    codes += kSlice;
-    scales += kSlice / kCkptBlock;
-    if (c0 >= cols) {
-      in += ld - c0;
-      out += cols - c0;
-      codes += a.pitch - c0;
-      scales += a.nscales - c0 / kCkptBlock;
-      c0 = 0;
+    if constexpr (!DENSE) {
+      in += kSlice;
+      out += kSlice;
+      codes += kSlice;
+      scales += kSlice / kCkptBlock;
+      if (c0 >= cols) {
+        in += ld - c0;
+        out += cols - c0;
+        codes += a.pitch - c0;
+        scales += a.nscales - c0 / kCkptBlock;
+        c0 = 0;
+      }
     }
   }
+  __device__ __forceinline__ int64_t at_in() const { return DENSE ? c0 : in; }
+  __device__ __forceinline__ int64_t at_out() const { return DENSE ? c0 : out; }
+  __device__ __forceinline__ int64_t at_codes() const { return DENSE ? c0 : codes; }
+  __device__ __forceinline__ int64_t at_scales() const { return DENSE ? c0 / kCkptBlock : scales; }
   __device__ __forceinline__ int left() const { return static_cast<int>(min(cols - c0, static_cast<int64_t>(kSlice))); }
 };
 
-template <typename T, int ACT, int LAYOUT>
-__global__ void __launch_bounds__(kCkptThreads) pack_kernel(const PackArgs a) {
+template <typename T, int ACT, int LAYOUT, bool DENSE>
+__global__ void __launch_bounds__(kCkptThreads, sizeof(T) == 2 ? 4 : 3) pack_kernel(const PackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
   if (first >= a.items) return;
   const int n = min(a.items - first, static_cast<uint32_t>(kItems));
-  const Cursor begin(a, a.ld, first);
+  const Cursor<DENSE> begin(a, a.ld, first);
   F2 v[kItems][4];
   {
     Raw8<T> r[kItems];
-    Cursor s = begin;
+    Cursor<DENSE> s = begin;
 #pragma unroll
     for (int i = 0; i < kItems; ++i, s.next(a, a.ld))
-      r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.in, i < n ? s.left() : 0, lane);
+      r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.at_in(), i < n ? s.left() : 0, lane);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) unpack8<T>(r[i], v[i]);
   }
@@ -163,37 +175,37 @@ __global__ void __launch_bounds__(kCkptThreads) pack_kernel(const PackArgs a) {
   for (int i = 0; i < kItems; ++i) block_tops<LAYOUT>(v[i], top[i]);
   CkptScale sc[kItems][2];
   block_scales<LAYOUT, kItems>(top, lane, sc);
-  Cursor s = begin;
+  Cursor<DENSE> s = begin;
 #pragma unroll
   for (int i = 0; i < kItems; ++i, s.next(a, a.ld)) {
     if (i >= n) break;
-    store_codes8<LAYOUT>(a.codes + s.codes, s.left(), lane, ckpt_codes<LAYOUT>(v[i], sc[i]));
-    store_scales<LAYOUT>(a.scales + s.scales, s.left(), lane, sc[i]);
+    store_codes8<LAYOUT>(a.codes + s.at_codes(), s.left(), lane, ckpt_codes<LAYOUT>(v[i], sc[i]));
+    store_scales<LAYOUT>(a.scales + s.at_scales(), s.left(), lane, sc[i]);
     if constexpr (ACT != kActNone) {
       F2 unused;
 #pragma unroll
       for (int e = 0; e < 4; ++e) gelu2<ACT, true, false>(v[i][e], v[i][e], unused);
-      store8<T, LAYOUT>(static_cast<T*>(a.y) + s.out, s.left(), lane, v[i]);
+      store8<T, LAYOUT>(static_cast<T*>(a.y) + s.at_out(), s.left(), lane, v[i]);
     }
   }
 }
 
-template <typename T, int ACT, bool AGAIN, int LAYOUT>
+template <typename T, int ACT, bool AGAIN, int LAYOUT, bool DENSE>
 __global__ void __launch_bounds__(kCkptThreads) unpack_kernel(const UnpackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
   const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
   if (first >= a.items) return;
   const int n = min(a.items - first, static_cast<uint32_t>(kItems));
-  const Cursor begin(a, a.ld_dy, first);
+  const Cursor<DENSE> begin(a, a.ld_dy, first);
   uint2 q[kItems];
   Raw8<T> r[kItems];
-  Cursor s = begin;
+  Cursor<DENSE> s = begin;
 #pragma unroll
   for (int i = 0; i < kItems; ++i, s.next(a, a.ld_dy)) {
     const int left = i < n ? s.left() : 0;
-    q[i] = load_codes8<LAYOUT>(a.codes + s.codes, left, lane);
-    if constexpr (ACT != kActNone) r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.in, left, lane);
+    q[i] = load_codes8<LAYOUT>(a.codes + s.at_codes(), left, lane);
+    if constexpr (ACT != kActNone) r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.at_in(), left, lane);
   }
   s = begin;
 #pragma unroll
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(kCkptThreads) unpack_kernel(const UnpackArgs a
     if (i >= n) break;
     const int left = s.left();
     F2 v[4];
-    ckpt_values<LAYOUT>(q[i], a.scales + s.scales, left, lane, v);
+    ckpt_values<LAYOUT>(q[i], a.scales + s.at_scales(), left, lane, v);
     if constexpr (ACT != kActNone) {
       F2 dy[4], y[4];
       unpack8<T>(r[i], dy);
@@ -211,9 +223,9 @@ __global__ void __launch_bounds__(kCkptThreads) unpack_kernel(const UnpackArgs a
         gelu2<ACT, AGAIN, true>(v[e], y[e], slope);
         v[e] = mul2(slope, dy[e]);
       }
-      if constexpr (AGAIN) store8<T, LAYOUT>(static_cast<T*>(a.y) + s.out, left, lane, y);
+      if constexpr (AGAIN) store8<T, LAYOUT>(static_cast<T*>(a.y) + s.at_out(), left, lane, y);
     }
-    store8<T, LAYOUT>(static_cast<T*>(a.out) + s.out, left, lane, v);
+    store8<T, LAYOUT>(static_cast<T*>(a.out) + s.at_out(), left, lane, v);
   }
 }
 
@@ -222,18 +234,20 @@ dim3 ckpt_grid(const A& a) {
   return dim3((a.items + kCkptWarps * kItems - 1) / (kCkptWarps * kItems));
 }
 
-template <typename T, int LAYOUT>
+template <typename T, int LAYOUT, bool DENSE>
 int launch_pack(const PackArgs& a, int act, cudaStream_t stream) {
-  auto k = act == kActNone ? pack_kernel<T, kActNone, LAYOUT>
-                           : act == kActErf ? pack_kernel<T, kActErf, LAYOUT> : pack_kernel<T, kActTanh, LAYOUT>;
+  auto k = act == kActNone  ? pack_kernel<T, kActNone, LAYOUT, DENSE>
+           : act == kActErf ? pack_kernel<T, kActErf, LAYOUT, DENSE>
+                            : pack_kernel<T, kActTanh, LAYOUT, DENSE>;
   return launch_pdl(k, ckpt_grid(a), dim3(kCkptThreads), 0, stream, a);
 }
-template <typename T, int LAYOUT>
+template <typename T, int LAYOUT, bool DENSE>
 int launch_unpack(const UnpackArgs& a, int act, cudaStream_t stream) {
   const bool y = a.y != nullptr;
-  auto k = act == kActNone  ? unpack_kernel<T, kActNone, false, LAYOUT>
-           : act == kActErf ? (y ? unpack_kernel<T, kActErf, true, LAYOUT> : unpack_kernel<T, kActErf, false, LAYOUT>)
-                            : (y ? unpack_kernel<T, kActTanh, true, LAYOUT> : unpack_kernel<T, kActTanh, false, LAYOUT>);
+  auto k = act == kActNone ? unpack_kernel<T, kActNone, false, LAYOUT, DENSE>
+           : act == kActErf
+               ? (y ? unpack_kernel<T, kActErf, true, LAYOUT, DENSE> : unpack_kernel<T, kActErf, false, LAYOUT, DENSE>)
+               : (y ? unpack_kernel<T, kActTanh, true, LAYOUT, DENSE> : unpack_kernel<T, kActTanh, false, LAYOUT, DENSE>);
   return launch_pdl(k, ckpt_grid(a), dim3(kCkptThreads), 0, stream, a);
 }
 
@@ -277,8 +291,12 @@ adasum_status_t pack(PackArgs a, int dtype, int act, cudaStream_t stream) {
   const bool vec = is_aligned(a.x, 16) && is_aligned(a.y, 16) && a.ld * e % 16 == 0 && (act == kActNone || a.cols * e % 16 == 0);
   if (!cut(a, a.ld)) return ADASUM_ERR_UNSUPPORTED;
   return counted_launch(stream, act ? "gelu_checkpoint" : "checkpoint_pack", n * (e + 1 + (act ? e : 0)), [&] {
-    if (dtype == kBF16) return vec ? launch_pack<bf16, kVec>(a, act, stream) : launch_pack<bf16, kStrided>(a, act, stream);
-    return vec ? launch_pack<float, kVec>(a, act, stream) : launch_pack<float, kStrided>(a, act, stream);
+    const bool dense = a.rows == 1;
+    if (dtype == kBF16)
+      return !vec ? launch_pack<bf16, kStrided, false>(a, act, stream)
+                  : dense ? launch_pack<bf16, kVec, true>(a, act, stream) : launch_pack<bf16, kVec, false>(a, act, stream);
+    return !vec ? launch_pack<float, kStrided, false>(a, act, stream)
+                : dense ? launch_pack<float, kVec, true>(a, act, stream) : launch_pack<float, kVec, false>(a, act, stream);
   });
 }
 
@@ -302,8 +320,12 @@ adasum_status_t unpack(UnpackArgs a, int dtype, int act, cudaStream_t stream) {
   if (!cut(a, act == kActNone ? a.cols : a.ld_dy)) return ADASUM_ERR_UNSUPPORTED;
   return counted_launch(stream, act ? "gelu_grad_checkpoint" : "checkpoint_unpack",
                         n * (1 + e + (act ? e : 0) + (a.y ? e : 0)), [&] {
-    if (dtype == kBF16) return vec ? launch_unpack<bf16, kVec>(a, act, stream) : launch_unpack<bf16, kStrided>(a, act, stream);
-    return vec ? launch_unpack<float, kVec>(a, act, stream) : launch_unpack<float, kStrided>(a, act, stream);
+    const bool dense = a.rows == 1;
+    if (dtype == kBF16)
+      return !vec ? launch_unpack<bf16, kStrided, false>(a, act, stream)
+                  : dense ? launch_unpack<bf16, kVec, true>(a, act, stream) : launch_unpack<bf16, kVec, false>(a, act, stream);
+    return !vec ? launch_unpack<float, kStrided, false>(a, act, stream)
+                : dense ? launch_unpack<float, kVec, true>(a, act, stream) : launch_unpack<float, kVec, false>(a, act, stream);
   });
 }
 

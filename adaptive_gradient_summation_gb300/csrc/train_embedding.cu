@@ -64,24 +64,24 @@ __global__ void __launch_bounds__(kEmbThreads) lookup_kernel(const LookupArgs a)
 
 // ------------------------------------------------------------------- the table's gradient
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = 8;                             // tokens per thread
-constexpr int kSortMost = kSortThreads * kSortItems;      // tokens one CTA sorts by itself
+constexpr int kSortThreads = 1024, kSortItems = 8;        // of the CTA that sorts a worker's tokens
+constexpr int kSortMost = kSortThreads * kSortItems;      // tokens it takes
+constexpr int kTileThreads = 256, kTileItems = 8;         // of a tile of the multi-CTA sort
+constexpr int kTile = kTileThreads * kTileItems;
 constexpr int kDigits = 256;
 constexpr int kMostPasses = 4;
-
-constexpr int kSelfSort = kEmbThreads;                    // tokens of a worker that the summing CTAs sort
+constexpr int kSelfSort = kEmbThreads;  // tokens of a worker that the summing CTAs sort themselves
+constexpr int kSelfPart = 4;            // ... and of a warp then
 
 // Tokens per warp of a chunk: few enough that the warps cover the memory's latency (about
-// 32 per SM), at most 32; workers of at most kSelfSort tokens are one chunk.
+// 32 per SM), at most 32.
 int warp_tokens(int64_t n, int64_t most, int64_t cols) {
-  if (most <= kSelfSort) return most <= 8 * kEmbWarps ? 8 : most <= 16 * kEmbWarps ? 16 : 32;
+  if (most <= kSelfSort) return kSelfPart;
   const int64_t work = n * ((cols + kSlice - 1) / kSlice);
   return work >= 32 * 4864 ? 32 : work >= 16 * 4864 ? 16 : 8;
 }
-int64_t chunk_bound(int64_t n, int K) { return n / (8 * kEmbWarps) + K; }
-int64_t tile_bound(int64_t n, int K) { return n / kSortMost + K; }
+int64_t chunk_bound(int64_t n, int K) { return n / (kSelfPart * kEmbWarps) + K; }
+int64_t tile_bound(int64_t n, int K) { return n / kTile + K; }
 
 // Regions of the scratch memory.
 struct Scratch {
@@ -178,29 +178,36 @@ __device__ __forceinline__ int token_key(const A& a, int64_t i) {
   return t >= 0 && t < a.num_rows && t != a.padding_idx ? static_cast<int>(t) : a.num_rows;
 }
 
+template <int THREADS, int ITEMS>
 struct SortSmem {
-  int hist[kSortWarps][kDigits];  // then: where a warp's keys of a digit go
+  static constexpr int kWarps = THREADS / 32, kParts = THREADS / kDigits;
+  int hist[kWarps][kDigits];      // then: where a warp's keys of a digit go
+  int part[kParts][kDigits];      // counts of a digit in the warps of a part
   int scan[kDigits / 32];
-  int key[kSortMost], pos[kSortMost];
+  int key[THREADS * ITEMS], pos[THREADS * ITEMS];
 };
 
-// Ranks a CTA's keys by one digit.  Item j of lane l of warp w is number (w * kSortItems +
-// j) * 32 + l of `n`; after the call, item j goes to place s.hist[w][digit] + rank[j] of the
-// CTA's keys in the digit's order, equal digits staying in their order.  Returns, to thread
+// Ranks a CTA's keys by one digit.  Item j of lane l of warp w is number (w * ITEMS + j) * 32
+// + l of `n`; after the call, item j goes to place s.hist[w][digit] + rank[j] of the CTA's
+// keys in the digit's order, equal digits staying in their order.  Returns, to thread
 // d < kDigits, the number of keys of digit d and of smaller digits.
 struct DigitCount {
   int here, before;
 };
-__device__ __forceinline__ DigitCount block_rank(SortSmem& s, const int (&key)[kSortItems], int (&rank)[kSortItems],
-                                                int n, int shift, int bits) {
+template <int THREADS, int ITEMS>
+__device__ __forceinline__ DigitCount block_rank(SortSmem<THREADS, ITEMS>& s, const int (&key)[ITEMS],
+                                                int (&rank)[ITEMS], int n, int shift, int bits) {
+  constexpr int kRows = 8;  // warps of a part
+  static_assert(THREADS / 32 == kRows * (THREADS / kDigits), "eight warps per 256 threads");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int mask = (1 << bits) - 1;
-  for (int d = lane; d < kDigits; d += 32) s.hist[w][d] = 0;
+#pragma unroll
+  for (int i = 0; i < kDigits / 32; ++i) s.hist[w][i * 32 + lane] = 0;
   __syncwarp();
 #pragma unroll
-  for (int j = 0; j < kSortItems; ++j) {
-    if (w * kSortItems * 32 + j * 32 >= n) break;  // (uniform over the warp)
-    const bool in = w * kSortItems * 32 + j * 32 + lane < n;
+  for (int j = 0; j < ITEMS; ++j) {
+    if ((w * ITEMS + j) * 32 >= n) break;  // (uniform over the warp)
+    const bool in = (w * ITEMS + j) * 32 + lane < n;
     const int d = in ? (key[j] >> shift) & mask : kDigits;
     const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
     const int before = __popc(same & ((1u << lane) - 1u));
@@ -212,33 +219,41 @@ __device__ __forceinline__ DigitCount block_rank(SortSmem& s, const int (&key)[k
     rank[j] = base + before;
   }
   __syncthreads();
-  DigitCount c = {0, 0};
-  if (threadIdx.x < kDigits) {
-    int sum = 0;
-#pragma unroll 8
-    for (int i = 0; i < kSortWarps; ++i) {
-      const int v = s.hist[i][threadIdx.x];
-      s.hist[i][threadIdx.x] = sum;
-      sum += v;
-    }
-    int incl = sum;
+  // digit d of the eight warps of part p, by thread p * 256 + d
+  const int d = threadIdx.x & (kDigits - 1), p = threadIdx.x / kDigits;
+  int row[kRows], sum = 0;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += up;
-    }
-    if (lane == 31) s.scan[w] = incl;
-    c.here = sum;
-    c.before = incl - sum;
+  for (int i = 0; i < kRows; ++i) row[i] = s.hist[p * kRows + i][d];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int v = row[i];
+    row[i] = sum;
+    sum += v;
   }
+  s.part[p][d] = sum;
   __syncthreads();
-  if (threadIdx.x < kDigits) {
-    for (int i = 0; i < w; ++i) c.before += s.scan[i];
-#pragma unroll 8
-    for (int i = 0; i < kSortWarps; ++i) s.hist[i][threadIdx.x] += c.before;
+  int total = 0, mine = 0;
+#pragma unroll
+  for (int i = 0; i < THREADS / kDigits; ++i) {
+    if (i == p) mine = total;
+    total += s.part[i][d];
   }
+  int incl = total;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, incl, i);
+    if (lane >= i) incl += up;
+  }
+  if (p == 0 && lane == 31) s.scan[w] = incl;
   __syncthreads();
-  return c;
+  int before = incl - total;
+#pragma unroll
+  for (int i = 0; i < kDigits / 32; ++i)
+    if (i < d / 32) before += s.scan[i];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) s.hist[p * kRows + i][d] = row[i] + mine + before;
+  __syncthreads();
+  return {total, before};
 }
 
 // Up to kSortMost tokens per worker: one CTA sorts a worker's in shared memory, all passes;
@@ -246,7 +261,7 @@ __device__ __forceinline__ DigitCount block_rank(SortSmem& s, const int (&key)[k
 __global__ void __launch_bounds__(kSortThreads) table_sort_kernel(const __grid_constant__ SortArgs a) {
   pdl_enter();
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  SortSmem& s = *reinterpret_cast<SortSmem*>(smem_raw);
+  auto& s = *reinterpret_cast<SortSmem<kSortThreads, kSortItems>*>(smem_raw);
   const int k = blockIdx.x;
   if (k >= a.K) return fill_share(a, k - a.K);
   if (k == 0 && threadIdx.x == 0) *a.join_count = 0;
@@ -263,7 +278,7 @@ __global__ void __launch_bounds__(kSortThreads) table_sort_kernel(const __grid_c
   }
   for (int pass = 0; pass < a.passes; ++pass) {
     const int shift = pass * a.bits;
-    block_rank(s, key, rank, n, shift, a.bits);
+    block_rank<kSortThreads, kSortItems>(s, key, rank, n, shift, a.bits);
 #pragma unroll
     for (int j = 0; j < kSortItems; ++j) {
       const int i = (w * kSortItems + j) * 32 + lane;
@@ -291,81 +306,82 @@ __global__ void __launch_bounds__(kSortThreads) table_sort_kernel(const __grid_c
   }
 }
 
-// More tokens: tiles of kSortMost.  First the digit counts of every tile (and the zeroing),
-__global__ void __launch_bounds__(kSortThreads) table_count_kernel(const __grid_constant__ SortArgs a) {
+// More tokens: tiles of kTile.  First the digit counts of every tile (and the zeroing),
+__global__ void __launch_bounds__(kTileThreads) table_count_kernel(const __grid_constant__ SortArgs a) {
   pdl_enter();
+  static_assert(kTileThreads == kDigits, "a thread per digit");
   __shared__ int hist[kDigits];
   const int tile = blockIdx.x;
   if (tile >= a.ntiles) return fill_share(a, tile - a.ntiles);  // (every CTA, when there is nothing to count)
   if (tile == 0 && threadIdx.x == 0) *a.join_count = 0;
   const int k = worker_of(a.tile_off, a.K, tile);
-  const int64_t lo = a.off[k] + static_cast<int64_t>(tile - a.tile_off[k]) * kSortMost;
-  const int n = static_cast<int>(min(a.off[k + 1] - lo, static_cast<int64_t>(kSortMost)));
-  if (threadIdx.x < kDigits) {
-    hist[threadIdx.x] = 0;
-    for (int p = 1; p < a.passes; ++p) a.hist[(static_cast<int64_t>(p) * a.ntiles + tile) * kDigits + threadIdx.x] = 0;
+  const int64_t lo = a.off[k] + static_cast<int64_t>(tile - a.tile_off[k]) * kTile;
+  const int n = static_cast<int>(min(a.off[k + 1] - lo, static_cast<int64_t>(kTile)));
+  hist[threadIdx.x] = 0;
+  for (int p = 1; p < a.passes; ++p) a.hist[(static_cast<int64_t>(p) * a.ntiles + tile) * kDigits + threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kTileItems; ++j) {
+    const int i = j * kTileThreads + threadIdx.x;
+    if (i < n) atomicAdd(&hist[token_key(a, lo + i) & ((1 << a.bits) - 1)], 1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kSortThreads) atomicAdd(&hist[token_key(a, lo + i) & ((1 << a.bits) - 1)], 1);
-  __syncthreads();
-  if (threadIdx.x < kDigits) a.hist[static_cast<int64_t>(tile) * kDigits + threadIdx.x] = hist[threadIdx.x];
+  a.hist[static_cast<int64_t>(tile) * kDigits + threadIdx.x] = hist[threadIdx.x];
 }
 
 // then one pass per digit: a tile's keys of digit d go after the worker's keys of smaller
 // digits and those of digit d in earlier tiles; on the way the next digit is counted in the
 // tiles that the keys arrive in.
-__global__ void __launch_bounds__(kSortThreads) table_scatter_kernel(const __grid_constant__ SortArgs a) {
+__global__ void __launch_bounds__(kTileThreads) table_scatter_kernel(const __grid_constant__ SortArgs a) {
   pdl_enter();
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  SortSmem& s = *reinterpret_cast<SortSmem*>(smem_raw);
+  __shared__ SortSmem<kTileThreads, kTileItems> s;
   const int tile = blockIdx.x, k = worker_of(a.tile_off, a.K, tile);
-  const int64_t base = a.off[k], lo = base + static_cast<int64_t>(tile - a.tile_off[k]) * kSortMost;
-  const int n = static_cast<int>(min(a.off[k + 1] - lo, static_cast<int64_t>(kSortMost)));
+  const int64_t base = a.off[k], lo = base + static_cast<int64_t>(tile - a.tile_off[k]) * kTile;
+  const int n = static_cast<int>(min(a.off[k + 1] - lo, static_cast<int64_t>(kTile)));
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, mask = (1 << a.bits) - 1;
-  int key[kSortItems], pos[kSortItems], rank[kSortItems];
+  int key[kTileItems], pos[kTileItems], rank[kTileItems];
 #pragma unroll
-  for (int j = 0; j < kSortItems; ++j) {
-    const int i = (w * kSortItems + j) * 32 + lane;
+  for (int j = 0; j < kTileItems; ++j) {
+    const int i = (w * kTileItems + j) * 32 + lane;
     key[j] = pos[j] = rank[j] = 0;
     if (i < n) {
       key[j] = a.keys_in ? a.keys_in[lo + i] : token_key(a, lo + i);
       pos[j] = a.keys_in ? a.pos_in[lo + i] : static_cast<int>(lo + i);
     }
   }
-  const DigitCount c = block_rank(s, key, rank, n, a.shift, a.bits);
-  // place of this tile's digit d in the worker's order, minus its place in the tile's
-  if (threadIdx.x < kDigits) {
-    const int* h = a.hist + static_cast<int64_t>(a.pass) * a.ntiles * kDigits + threadIdx.x;
-    int earlier = 0, total = 0;
-#pragma unroll 4
-    for (int t = a.tile_off[k]; t < a.tile_off[k + 1]; ++t) {
-      const int v = h[static_cast<int64_t>(t) * kDigits];
-      if (t < tile) earlier += v;
-      total += v;
-    }
-    int incl = total;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int up = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += up;
-    }
-    if (lane == 31) s.scan[w] = incl;
-    s.key[threadIdx.x] = incl - total + earlier - c.before;
+  // (thread d: digit d of the worker's tiles)
+  const int* h = a.hist + static_cast<int64_t>(a.pass) * a.ntiles * kDigits + threadIdx.x;
+  int earlier = 0, total = 0;
+#pragma unroll 8
+  for (int t = a.tile_off[k]; t < a.tile_off[k + 1]; ++t) {
+    const int v = h[static_cast<int64_t>(t) * kDigits];
+    if (t < tile) earlier += v;
+    total += v;
   }
+  const DigitCount c = block_rank<kTileThreads, kTileItems>(s, key, rank, n, a.shift, a.bits);
+  // place of this tile's digit d in the worker's order, minus its place in the tile's
+  int incl = total;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, incl, i);
+    if (lane >= i) incl += up;
+  }
+  if (lane == 31) s.scan[w] = incl;
   __syncthreads();
-  if (threadIdx.x < kDigits)
-    for (int i = 0; i < w; ++i) s.key[threadIdx.x] += s.scan[i];
+  int place = incl - total + earlier - c.before;
+  for (int i = 0; i < w; ++i) place += s.scan[i];
+  s.key[threadIdx.x] = place;
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < kSortItems; ++j) {
-    const int i = (w * kSortItems + j) * 32 + lane;
+  for (int j = 0; j < kTileItems; ++j) {
+    const int i = (w * kTileItems + j) * 32 + lane;
     if (i >= n) continue;
     const int d = (key[j] >> a.shift) & mask;
     const int to = s.hist[w][d] + rank[j] + s.key[d];
     a.keys[base + to] = key[j];
     a.pos[base + to] = pos[j];
     if (a.pass + 1 < a.passes)
-      atomicAdd(&a.hist[(static_cast<int64_t>(a.pass + 1) * a.ntiles + a.tile_off[k] + to / kSortMost) * kDigits +
+      atomicAdd(&a.hist[(static_cast<int64_t>(a.pass + 1) * a.ntiles + a.tile_off[k] + to / kTile) * kDigits +
                         ((key[j] >> (a.shift + a.bits)) & mask)], 1);
   }
 }
@@ -401,191 +417,236 @@ enum Ends : int {
   kTail = 4,   // its last run begins here and does not end here
 };
 
-// Sums inside one chunk of sorted tokens, 256 columns per CTA and a part of the chunk per
-// warp.  kVec: a lane copies its 16 or 32 bytes of the next rows to shared memory ahead of
-// their use (8 or 4 rows, 4 KiB a warp), which takes no registers and no exchange between
-// lanes; kStrided: the next row is held in registers.  Runs that cross warps are joined
-// through shared memory, runs that cross chunks leave their pieces in scratch memory.
+// Sums inside one chunk of sorted tokens, NV * 256 columns per CTA and a part of the chunk
+// per warp.  kVec: a lane copies its 16-byte pieces of the next rows to shared memory ahead of
+// their use (4 or 8 KiB a warp), which takes no registers and no exchange between lanes;
+// kStrided: the next row is held in registers.  Runs that cross warps are joined through
+// shared memory, runs that cross chunks leave their pieces in scratch memory.
+// SORT: the CTA sorts its worker's few tokens itself, and a warp takes the runs that begin in
+// its part to their end, so that nothing is left to join.
 // Bound by grad_out's bytes (each read once) and the gradient rows written.
-template <typename T, typename G, bool ADD>
+template <typename T, typename G, int NV, bool ADD>
 struct SumSmem {
   static constexpr int kAhead = 16 / sizeof(T);  // rows on their way
   static constexpr int kVecs = sizeof(T) / 2, kOldVecs = sizeof(G) / 2;  // 16-byte vectors of a lane's eight
   union {
     struct {
-      uint4 dy[kEmbWarps][kAhead][kVecs][32];
-      uint4 old[ADD ? kEmbWarps : 1][ADD ? kAhead : 1][kOldVecs][ADD ? 32 : 1];  // gradient rows to be added to
+      uint4 dy[kEmbWarps][kAhead][NV][kVecs][32];
+      uint4 old[ADD ? kEmbWarps : 1][ADD ? kAhead : 1][NV][kOldVecs][32];  // gradient rows to be added to
     } ring;
-    float piece[kEmbWarps][2][kSlice];
-    int unsorted[kSelfSort];
+    float piece[kEmbWarps][2][NV * kSlice];
+    uint32_t unsorted[kSelfSort];
   };
 };
-template <typename T, typename G, int LAYOUT, bool SORT, bool ADD>
+template <typename T, typename G, int LAYOUT, int NV, bool SORT, bool ADD>
 __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_constant__ TableGradArgs a) {
   pdl_enter();
-  using Smem = SumSmem<T, G, ADD>;
+  using Smem = SumSmem<T, G, NV, ADD>;
   constexpr int kVecs = Smem::kVecs, kAhead = Smem::kAhead;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   __shared__ int ends[kEmbWarps], tail_key[kEmbWarps];
   __shared__ int own_keys[SORT ? kSelfSort : 1], own_pos[SORT ? kSelfSort : 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const uint32_t chunk = blockIdx.x / static_cast<uint32_t>(a.slices);
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x - chunk * a.slices) * kSlice;
-  const int left = slice_left(a.cols, c0);
+  const int slices = a.slices / NV;
+  const uint32_t chunk = blockIdx.x / static_cast<uint32_t>(slices);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - chunk * slices) * (NV * kSlice);
+  int left[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) left[j] = slice_left(a.cols, c0 + j * kSlice);
   const int k = worker_of(a.chunk_off, a.K, static_cast<int>(chunk));
   const int64_t first = a.off[k], last = a.off[k + 1];
-  const int *keys = a.keys, *pos = a.pos;
-  int64_t base = 0;  // index of keys[0]
+  int64_t lo = first + (static_cast<int64_t>(chunk - a.chunk_off[k]) * kEmbWarps + w) * a.part;
+  int m = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.part), last - lo)));
+  // the part's n tokens with a gradient: the sorted keys and rows of SORT's are read from
+  // shared memory, others are held one per lane
+  int n, key = a.num_rows, at = 0, before = a.num_rows, after = a.num_rows, skip = 0;
   if constexpr (SORT) {
-    // a token's place is the number of smaller keys and of equal ones before it
-    const int n = static_cast<int>(last - first), i = threadIdx.x;
-    const int mine = i < n ? token_key(a, first + i) : 0;
-    sm.unsorted[i] = i < n ? mine : INT32_MAX;
+    // a token's place is the number of smaller (key, index) pairs; `ways` threads count it
+    const int total = static_cast<int>(last - first);
+    const uint32_t i = threadIdx.x;
+    const uint32_t word = static_cast<int>(i) < total ? static_cast<uint32_t>(token_key(a, first + i)) << 8 | i : 0xFFFFFFFFu;
+    sm.unsorted[i] = word;
     __syncthreads();
+    int ways = 1;
+    while (ways < 32 && 2 * ways * total <= kEmbThreads) ways *= 2;
+    const int mine = threadIdx.x / ways;
+    const uint32_t me = mine < total ? sm.unsorted[mine] : 0u;
     int place = 0;
-    for (int j = 0; j < n; j += 4) {
-      const int4 q = *reinterpret_cast<const int4*>(&sm.unsorted[j]);
-      place += (q.x < mine + (j < i)) + (q.y < mine + (j + 1 < i)) + (q.z < mine + (j + 2 < i)) + (q.w < mine + (j + 3 < i));
+    for (int j = threadIdx.x % ways; 4 * j < total; j += ways) {
+      const uint4 q = reinterpret_cast<const uint4*>(sm.unsorted)[j];
+      place += (q.x < me) + (q.y < me) + (q.z < me) + (q.w < me);
     }
-    if (i < n) {  // (the ring takes the place of the unsorted keys after the barrier)
-      own_keys[place] = mine;
-      own_pos[place] = static_cast<int>(first) + i;
+    for (int d = ways / 2; d > 0; d /= 2) place += __shfl_xor_sync(0xFFFFFFFFu, place, d);
+    if (mine < total && threadIdx.x % ways == 0) {
+      own_keys[place] = static_cast<int>(me >> 8);
+      own_pos[place] = static_cast<int>(first) + static_cast<int>(me & 255u);
     }
     __syncthreads();
-    keys = own_keys;
-    pos = own_pos;
-    base = first;
+    const int from = static_cast<int>(lo - first);
+    while (skip < m && from + skip > 0 && own_keys[from + skip] == own_keys[from + skip - 1]) ++skip;
+    if (skip == m) return;  // no run begins here
+    int end = from + m;
+    while (end < total && own_keys[end] == own_keys[end - 1]) ++end;
+    skip += from;  // the runs are [skip, end)
+    while (end > skip && own_keys[end - 1] == a.num_rows) --end;  // tokens without a gradient are last
+    n = end - skip;
+  } else {
+    if (lane < m) {
+      key = a.keys[lo + lane];
+      at = a.pos[lo + lane];
+    }
+    if (m > 0 && lo > first) before = a.keys[lo - 1];
+    if (m > 0 && lo + m < last) after = a.keys[lo + m];
+    n = __popc(__ballot_sync(0xFFFFFFFFu, key != a.num_rows));
   }
-  const int64_t lo = first + (static_cast<int64_t>(chunk - a.chunk_off[k]) * kEmbWarps + w) * a.part;
-  const int m = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.part), last - lo)));
-  int key = a.num_rows, at = 0, before = a.num_rows, after = a.num_rows;
-  if (lane < m) {
-    key = keys[lo - base + lane];
-    at = pos[lo - base + lane];
-  }
-  if (m > 0 && lo > first) before = keys[lo - base - 1];
-  if (m > 0 && lo + m < last) after = keys[lo - base + m];
-  // tokens without a gradient are sorted last
-  const int n = __popc(__ballot_sync(0xFFFFFFFFu, key != a.num_rows));
+  auto key_of = [&](int i) { return SORT ? own_keys[skip + min(i, n - 1)] : __shfl_sync(0xFFFFFFFFu, key, i & 31); };
+  auto row_of = [&](int i) { return SORT ? own_pos[skip + min(i, n - 1)] : __shfl_sync(0xFFFFFFFFu, at, i & 31); };
+  if (SORT && n == 0) return;
   const T* dy = static_cast<const T*>(a.dy) + c0;
   G* grad = static_cast<G*>(a.grads[k]) + c0;
-  const int earlier = __shfl_up_sync(0xFFFFFFFFu, key, 1);
-  const bool begins = lane == 0 ? before != key : earlier != key;  // this lane's token begins a run
-  const unsigned starts = __ballot_sync(0xFFFFFFFFu, begins && key != a.num_rows);
-  Raw8<T> held;
-  Raw8<G> held_old;
+  Raw8<T> held[NV];
+  Raw8<G> held_old[NV];
+  int copied = -1;  // key of the last row whose copy was begun (rows below n only)
+  if (!SORT && n > 0 && before == __shfl_sync(0xFFFFFFFFu, key, 0)) copied = before;  // (that run's row is not added to here)
   auto copy = [&](int i) {  // row i of the part, and the gradient row of a run that begins there
-    const int p = __shfl_sync(0xFFFFFFFFu, at, i & 31), q = __shfl_sync(0xFFFFFFFFu, key, i & 31);
+    const int p = row_of(i), q = key_of(i);
     const T* row = dy + static_cast<int64_t>(p) * a.ld;
-    const bool old = ADD && i < n && (starts >> i & 1);
+    const G* old = grad + q * a.cols;
+    const bool begins = ADD && i < n && q != copied;
+    if (i < n) copied = q;
     if constexpr (LAYOUT == kVec) {
-      if (i < n) {
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
-          const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(T));
-          const int bytes = max(0, min(16, (left - c) * static_cast<int>(sizeof(T))));
-          cp_async16(smem_addr(&sm.ring.dy[w][i % kAhead][v][lane]), row + (bytes > 0 ? c : 0), bytes);
+      for (int j = 0; j < NV; ++j) {
+        if (i < n) {
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) {
+            const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(T));
+            const int bytes = max(0, min(16, (left[j] - c) * static_cast<int>(sizeof(T))));
+            cp_async16(smem_addr(&sm.ring.dy[w][i % kAhead][j][v][lane]), row + (bytes > 0 ? j * kSlice + c : 0), bytes);
+          }
         }
-      }
-      if (old) {
+        if (begins) {
 #pragma unroll
-        for (int v = 0; v < Smem::kOldVecs; ++v) {
-          const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(G));
-          const int bytes = max(0, min(16, (left - c) * static_cast<int>(sizeof(G))));
-          cp_async16(smem_addr(&sm.ring.old[w][i % kAhead][v][lane]), grad + q * a.cols + (bytes > 0 ? c : 0), bytes);
+          for (int v = 0; v < Smem::kOldVecs; ++v) {
+            const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(G));
+            const int bytes = max(0, min(16, (left[j] - c) * static_cast<int>(sizeof(G))));
+            cp_async16(smem_addr(&sm.ring.old[w][i % kAhead][j][v][lane]), old + (bytes > 0 ? j * kSlice + c : 0), bytes);
+          }
         }
       }
       cp_async_commit();
     } else {
-      held = load8<T, LAYOUT>(row, i < n ? left : 0, lane);
-      if constexpr (ADD) held_old = load8<G, LAYOUT>(grad + q * a.cols, old ? left : 0, lane);
-    }
-  };
-  // a lane's eight values from its 16-byte vectors
-  auto gather = [&](auto& r, const auto& from) {
 #pragma unroll
-    for (int v = 0; v < static_cast<int>(sizeof(r.w) / 16); ++v) {
-      const uint4 x = from[v][lane];
-      r.w[4 * v] = x.x;
-      r.w[4 * v + 1] = x.y;
-      r.w[4 * v + 2] = x.z;
-      r.w[4 * v + 3] = x.w;
+      for (int j = 0; j < NV; ++j) {
+        held[j] = load8<T, LAYOUT>(row + j * kSlice, i < n ? left[j] : 0, lane);
+        if constexpr (ADD) held_old[j] = load8<G, LAYOUT>(old + j * kSlice, begins ? left[j] : 0, lane);
+      }
     }
   };
   constexpr int kLead = LAYOUT == kVec ? kAhead : 1;
   for (int i = 0; i < kLead; ++i) copy(i);
-  F2 acc[4], head[4];
-  Raw8<G> old = {};
+  F2 acc[NV][4], head[SORT ? 1 : NV][4];
+  Raw8<G> old[NV] = {};
+  auto clear = [&](auto& v) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = head[i] = f2(0.f);
-  int cur = __shfl_sync(0xFFFFFFFFu, key, 0), found = 0;
-  bool from_before = n > 0 && before == cur;
+    for (auto& x : v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = f2(0.f);
+  };
+  clear(acc);
+  if constexpr (!SORT) clear(head);
+  auto put = [&](int row) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      put_row<G, LAYOUT, ADD>(grad + row * a.cols + j * kSlice, a.scale, left[j], lane, acc[j], old[j]);
+  };
+  int cur = n > 0 ? key_of(0) : -1, found = 0;
+  bool from_before = !SORT && n > 0 && before == cur, fresh = !from_before;
   for (int i = 0;; ++i) {
-    const int q = i < n ? __shfl_sync(0xFFFFFFFFu, key, i & 31) : -1;
+    const int q = i < n ? key_of(i) : -1;
     if (q != cur || i == n) {  // the run `cur` ends in this part, or the part ends
       if (n == 0) break;
-      const bool goes_on = i == n && i == m && after == cur;
+      const bool goes_on = !SORT && i == n && i == m && after == cur;
       if (from_before) {
         found |= goes_on ? kHead | kSpan : kHead;
+        if constexpr (!SORT) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) head[e] = acc[e];
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) head[j][e] = acc[j][e];
+        }
       } else if (goes_on) {
         found |= kTail;
       } else {
-        put_row<G, LAYOUT, ADD>(grad + cur * a.cols, a.scale, left, lane, acc, old);
+        put(cur);
       }
       if (i == n) break;
       cur = q;
       from_before = false;
+      fresh = true;
+      clear(acc);
+    }
+    if constexpr (LAYOUT == kVec) cp_async_wait<kAhead - 1>();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = f2(0.f);
+    for (int j = 0; j < NV; ++j) {
+      F2 v[4];
+      if constexpr (LAYOUT == kVec) {
+        Raw8<T> r;
+        gather8<T>(r, sm.ring.dy[w][i % kAhead][j], lane);
+        unpack8<T>(r, v);
+        if constexpr (ADD)
+          if (fresh) gather8<G>(old[j], sm.ring.old[w][i % kAhead][j], lane);
+      } else {
+        unpack8<T>(held[j], v);
+        if constexpr (ADD)
+          if (fresh) old[j] = held_old[j];
+      }
+      add8(acc[j], v);
     }
-    F2 v[4];
-    if constexpr (LAYOUT == kVec) {
-      cp_async_wait<kAhead - 1>();
-      Raw8<T> r;
-      gather(r, sm.ring.dy[w][i % kAhead]);
-      unpack8<T>(r, v);
-      if constexpr (ADD)
-        if (starts >> i & 1) gather(old, sm.ring.old[w][i % kAhead]);
-    } else {
-      unpack8<T>(held, v);
-      if constexpr (ADD)
-        if (starts >> i & 1) old = held_old;
-    }
-    add8(acc, v);
+    fresh = false;
     copy(i + kLead);
   }
-  // runs that cross warps
-  const int64_t chunk_end = lo + static_cast<int64_t>(kEmbWarps - w) * a.part;
-  if constexpr (LAYOUT == kVec) cp_async_wait<0>();
-  if (lane == 0) {
-    ends[w] = found;
-    tail_key[w] = cur;
-  }
-  if (!__syncthreads_or(found)) return;
-  if (found & kHead) sts8(sm.piece[w][0], lane, head);
-  if (found & kTail) sts8(sm.piece[w][1], lane, acc);
-  __syncthreads();
-  for (int slot = 0; slot < 2; ++slot) {
-    // slot 0: the run that enters the chunk (warp 0's head); slot 1: a run that begins here
-    if (!(ends[w] & (slot ? kTail : kHead)) || (slot == 0 && w > 0)) continue;
-    lds8(sm.piece[w][slot], lane, acc);
-    bool open = slot == 1 || (ends[w] & kSpan);
-    int j = w + 1;
-    for (; open && j < kEmbWarps && (ends[j] & kHead); ++j) {
-      F2 v[4];
-      lds8(sm.piece[j][0], lane, v);
-      add8(acc, v);
-      open = ends[j] & kSpan;
+  if constexpr (!SORT) {
+    // runs that cross warps
+    const int64_t chunk_end = lo + static_cast<int64_t>(kEmbWarps - w) * a.part;
+    if constexpr (LAYOUT == kVec) cp_async_wait<0>();
+    if (lane == 0) {
+      ends[w] = found;
+      tail_key[w] = cur;
     }
-    open = open && j == kEmbWarps && chunk_end < last;
-    if (slot == 0 || open) {
-      store8<float, LAYOUT>(a.partials + (static_cast<int64_t>(chunk) * 2 + slot) * a.cols + c0, left, lane, acc);
-      if (slot == 1 && c0 == 0 && lane == 0) a.list[atomicAdd(a.count, 1)] = static_cast<int>(chunk);
-    } else {
-      put_row<G, LAYOUT, ADD>(grad + tail_key[w] * a.cols, a.scale, left, lane, acc, old);
+    if (!__syncthreads_or(found)) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (found & kHead) sts8(sm.piece[w][0] + j * kSlice, lane, head[j]);
+      if (found & kTail) sts8(sm.piece[w][1] + j * kSlice, lane, acc[j]);
+    }
+    __syncthreads();
+    for (int slot = 0; slot < 2; ++slot) {
+      // slot 0: the run that enters the chunk (warp 0's head); slot 1: a run that begins here
+      if (!(ends[w] & (slot ? kTail : kHead)) || (slot == 0 && w > 0)) continue;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) lds8(sm.piece[w][slot] + j * kSlice, lane, acc[j]);
+      bool open = slot == 1 || (ends[w] & kSpan);
+      int u = w + 1;
+      for (; open && u < kEmbWarps && (ends[u] & kHead); ++u) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          F2 v[4];
+          lds8(sm.piece[u][0] + j * kSlice, lane, v);
+          add8(acc[j], v);
+        }
+        open = ends[u] & kSpan;
+      }
+      open = open && u == kEmbWarps && chunk_end < last;
+      if (slot == 0 || open) {
+        float* p = a.partials + (static_cast<int64_t>(chunk) * 2 + slot) * a.cols + c0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) store8<float, LAYOUT>(p + j * kSlice, left[j], lane, acc[j]);
+        if (slot == 1 && c0 == 0 && lane == 0) a.list[atomicAdd(a.count, 1)] = static_cast<int>(chunk);
+      } else {
+        put(tail_key[w]);
+      }
     }
   }
 }
@@ -656,36 +717,34 @@ template <typename T>
 int launch_lookup(const LookupArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
   return launch_pdl(vec ? lookup_kernel<T, kVec> : lookup_kernel<T, kStrided>, dim3(grid), dim3(kEmbThreads), 0, stream, a);
 }
-template <typename T, typename G, bool ADD>
-int launch_sum_as(const TableGradArgs& a, bool vec, bool sort, unsigned grid, cudaStream_t stream) {
-  auto kernel = vec ? (sort ? table_sum_kernel<T, G, kVec, true, ADD> : table_sum_kernel<T, G, kVec, false, ADD>)
-                    : (sort ? table_sum_kernel<T, G, kStrided, true, ADD> : table_sum_kernel<T, G, kStrided, false, ADD>);
-  constexpr size_t smem = sizeof(SumSmem<T, G, ADD>);
-  if (smem > 40 * 1024)  // (with the static part, more than the default 48 KiB)
-    if (cudaError_t rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); rc != cudaSuccess)
-      return static_cast<int>(rc);
-  return launch_pdl(kernel, dim3(grid), dim3(kEmbThreads), smem, stream, a);
+template <typename T, typename G, int LAYOUT, int NV, bool SORT, bool ADD>
+int launch_sum_as(const TableGradArgs& a, cudaStream_t stream) {
+  auto kernel = table_sum_kernel<T, G, LAYOUT, NV, SORT, ADD>;
+  constexpr size_t smem = sizeof(SumSmem<T, G, NV, ADD>);
+  static SmemAllowed allowed;
+  if (int rc = allow_smem(kernel, smem, allowed)) return rc;
+  TableGradArgs b = a;
+  b.slices = (a.slices + NV - 1) / NV * NV;
+  const unsigned grid = static_cast<unsigned>(a.chunk_off[a.K]) * static_cast<unsigned>(b.slices / NV);
+  return launch_pdl(kernel, dim3(grid), dim3(kEmbThreads), smem, stream, b);
+}
+// Two slices a warp halve what a token costs besides its bytes; with few tokens, or gradient
+// rows on their way as well, one slice leaves more warps.
+template <typename T, typename G, int LAYOUT>
+int launch_sum_layout(const TableGradArgs& a, bool sort, bool wide, cudaStream_t stream) {
+  if (a.accumulate)
+    return sort ? launch_sum_as<T, G, LAYOUT, 1, true, true>(a, stream) : launch_sum_as<T, G, LAYOUT, 1, false, true>(a, stream);
+  if (sort) return launch_sum_as<T, G, LAYOUT, 1, true, false>(a, stream);
+  return wide ? launch_sum_as<T, G, LAYOUT, 2, false, false>(a, stream) : launch_sum_as<T, G, LAYOUT, 1, false, false>(a, stream);
 }
 template <typename T, typename G>
-int launch_sum(const TableGradArgs& a, bool vec, bool sort, unsigned grid, cudaStream_t stream) {
-  return a.accumulate ? launch_sum_as<T, G, true>(a, vec, sort, grid, stream)
-                      : launch_sum_as<T, G, false>(a, vec, sort, grid, stream);
+int launch_sum(const TableGradArgs& a, bool vec, bool sort, bool wide, cudaStream_t stream) {
+  return vec ? launch_sum_layout<T, G, kVec>(a, sort, wide, stream) : launch_sum_layout<T, G, kStrided>(a, sort, wide, stream);
 }
 template <typename G>
 int launch_join(const TableGradArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
   return launch_pdl(vec ? table_join_kernel<G, kVec> : table_join_kernel<G, kStrided>, dim3(grid), dim3(kEmbThreads), 0,
                     stream, a);
-}
-
-// Allows a sort kernel its shared memory (once per device and kernel).
-int allow_smem(const void* kernel, int which) {
-  static bool done[2][64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return static_cast<int>(cudaErrorInvalidDevice);
-  if (dev >= 0 && dev < 64 && done[which][dev]) return 0;
-  const int rc = static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)));
-  if (rc == 0 && dev >= 0 && dev < 64) done[which][dev] = true;
-  return rc;
 }
 
 }  // namespace
@@ -757,7 +816,8 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   bool vec = is_aligned(grad_out, 16) && ld * e % 16 == 0 && cols * ge % 16 == 0 && cols * e % 16 == 0;
   int64_t most = 0;
   for (int k = 0; k < K; ++k) most = std::max(most, worker_offsets[k + 1] - worker_offsets[k]);
-  a.part = warp_tokens(n, most, cols);
+  // (a key and an index share 32 bits where a CTA sorts by itself)
+  a.part = warp_tokens(n, num_rows < (1 << 23) ? most : INT64_MAX, cols);
   const int64_t span = static_cast<int64_t>(a.part) * kEmbWarps;
   for (int k = 0; k < K; ++k) {
     if (grads[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
@@ -766,7 +826,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
     const int64_t nk = worker_offsets[k + 1] - worker_offsets[k];
     s.fill[k] = a.grads[k] = grads[k];
     s.off[k + 1] = a.off[k + 1] = worker_offsets[k + 1];
-    s.tile_off[k + 1] = s.tile_off[k] + static_cast<int>((nk + kSortMost - 1) / kSortMost);
+    s.tile_off[k + 1] = s.tile_off[k] + static_cast<int>((nk + kTile - 1) / kTile);
     a.chunk_off[k + 1] = a.chunk_off[k] + static_cast<int>((nk + span - 1) / span);
   }
   if (set.conflict()) return ADASUM_ERR_ALIAS;
@@ -794,29 +854,32 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   s.join_count = ints(at.count);
   s.fill_bytes = accumulate ? 0 : num_rows * cols * ge;
   const int64_t fill_vecs = static_cast<int64_t>(K) * (s.fill_bytes / 16);
-  s.fill_ctas = accumulate ? 0 : static_cast<int>(std::min<int64_t>(2 * sm_count(), 1 + fill_vecs / kSortThreads));
-  const bool self_sort = most <= kSelfSort;
+  const bool self_sort = a.part == kSelfPart;
+  const int fill_threads = !self_sort && most <= kSortMost ? kSortThreads : kTileThreads;
+  s.fill_ctas = accumulate ? 0 : static_cast<int>(std::min<int64_t>(2048 / fill_threads * sm_count(), 1 + fill_vecs / fill_threads));
   const double fill = static_cast<double>(K) * s.fill_bytes;
   int out = 0;  // which half of the key and position buffers holds the result
   if (self_sort) {  // only the zeroing, by the sort kernel with no worker to sort for
     s.ntiles = 0;
     if (!accumulate)
       if (adasum_status_t st = counted_launch(stream, "table_fill", fill, [&] {
-            return launch_pdl(table_count_kernel, dim3(s.fill_ctas), dim3(kSortThreads), 0, stream, s);
+            return launch_pdl(table_count_kernel, dim3(s.fill_ctas), dim3(kTileThreads), 0, stream, s);
           }))
         return st;
   } else if (most <= kSortMost) {
     s.keys = ints(at.keys[0]);
     s.pos = ints(at.pos[0]);
     if (adasum_status_t st = counted_launch(stream, "table_sort", fill, [&] {
-          if (int rc = allow_smem(reinterpret_cast<const void*>(table_sort_kernel), 0)) return rc;
-          return launch_pdl(table_sort_kernel, dim3(K + s.fill_ctas), dim3(kSortThreads), sizeof(SortSmem), stream, s);
+          static SmemAllowed allowed;
+          constexpr size_t smem = sizeof(SortSmem<kSortThreads, kSortItems>);
+          if (int rc = allow_smem(table_sort_kernel, smem, allowed)) return rc;
+          return launch_pdl(table_sort_kernel, dim3(K + s.fill_ctas), dim3(kSortThreads), smem, stream, s);
         }))
       return st;
   } else {
     s.ntiles = s.tile_off[K];
     if (adasum_status_t st = counted_launch(stream, "table_count", fill, [&] {
-          return launch_pdl(table_count_kernel, dim3(s.ntiles + s.fill_ctas), dim3(kSortThreads), 0, stream, s);
+          return launch_pdl(table_count_kernel, dim3(s.ntiles + s.fill_ctas), dim3(kTileThreads), 0, stream, s);
         }))
       return st;
     for (s.pass = 0; s.pass < s.passes; ++s.pass) {
@@ -827,8 +890,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
       s.keys = ints(at.keys[out]);
       s.pos = ints(at.pos[out]);
       if (adasum_status_t st = counted_launch(stream, "table_scatter", 0.0, [&] {
-            if (int rc = allow_smem(reinterpret_cast<const void*>(table_scatter_kernel), 1)) return rc;
-            return launch_pdl(table_scatter_kernel, dim3(s.ntiles), dim3(kSortThreads), sizeof(SortSmem), stream, s);
+            return launch_pdl(table_scatter_kernel, dim3(s.ntiles), dim3(kTileThreads), 0, stream, s);
           }))
         return st;
     }
@@ -845,16 +907,16 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   a.list = ints(at.list);
   a.partials = reinterpret_cast<float*>(base + at.partials);
   const int64_t items = static_cast<int64_t>(a.chunk_off[K]) * a.slices;
-  const unsigned grid = static_cast<unsigned>(items);
+  const bool wide = a.slices >= 2 && n * a.slices >= 16 * 4864;
   if (adasum_status_t st = counted_launch(stream, "table_sum", static_cast<double>(n) * (cols * e + 8), [&] {
         if (dtype == ADASUM_BF16)
-          return grad_dtype == ADASUM_BF16 ? launch_sum<bf16, bf16>(a, vec, self_sort, grid, stream)
-                                           : launch_sum<bf16, float>(a, vec, self_sort, grid, stream);
-        return grad_dtype == ADASUM_BF16 ? launch_sum<float, bf16>(a, vec, self_sort, grid, stream)
-                                         : launch_sum<float, float>(a, vec, self_sort, grid, stream);
+          return grad_dtype == ADASUM_BF16 ? launch_sum<bf16, bf16>(a, vec, self_sort, wide, stream)
+                                           : launch_sum<bf16, float>(a, vec, self_sort, wide, stream);
+        return grad_dtype == ADASUM_BF16 ? launch_sum<float, bf16>(a, vec, self_sort, wide, stream)
+                                         : launch_sum<float, float>(a, vec, self_sort, wide, stream);
       }))
     return st;
-  if (most <= span) return ADASUM_OK;  // no worker has a second chunk, so no run crosses chunks
+  if (self_sort || most <= span) return ADASUM_OK;  // no run crosses chunks
   const unsigned joiners = static_cast<unsigned>(std::min<int64_t>(items, 4 * static_cast<int64_t>(sm_count())));
   return counted_launch(stream, "table_join", 0.0, [&] {
     return grad_dtype == ADASUM_BF16 ? launch_join<bf16>(a, vec, joiners, stream) : launch_join<float>(a, vec, joiners, stream);

@@ -310,14 +310,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
       const Copy& c = copies[stage * TM::kWarps + warp];
       auto raw = [&](const uint4 (&v)[Copy::kVecs][32], F2 (&to)[4]) {
         Raw8<T> r;
-#pragma unroll
-        for (int i = 0; i < Copy::kVecs; ++i) {
-          const uint4 u = v[i][lane];
-          r.w[4 * i] = u.x;
-          r.w[4 * i + 1] = u.y;
-          r.w[4 * i + 2] = u.z;
-          r.w[4 * i + 3] = u.w;
-        }
+        gather8<T>(r, v, lane);
         unpack8<T>(r, to);
       };
       raw(c.dy[j], dy);
@@ -481,19 +474,13 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant_
   store_any(out, p.dtype, c, s);
 }
 
-// Allows a kernel its shared memory where that is more than the default.
-int allow_smem(const void* kernel, size_t bytes) {
-  return bytes <= 40 * 1024 ? 0  // (48 KiB, less the static part)
-                            : static_cast<int>(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                                    static_cast<int>(bytes)));
-}
-
 template <typename T, int LAYOUT, int W, int NV>
 int launch_norm_as(const NormArgs& a, cudaStream_t stream) {
   using TM = Team<W, NV>;
   const size_t smem = 2 * TM::kCols * sizeof(float);
+  static SmemAllowed allowed[2];
   auto kernel = a.codes ? norm_kernel<T, LAYOUT, W, NV, true> : norm_kernel<T, LAYOUT, W, NV, false>;
-  if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem)) return rc;
+  if (int rc = allow_smem(kernel, smem, allowed[a.codes != nullptr])) return rc;
   const int64_t need = (a.rows + TM::kTeams - 1) / TM::kTeams;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(kNormCtasPerSm) * sm_count()));
   return launch_pdl(kernel, dim3(grid), dim3(TM::kThreads), smem, stream, a);
@@ -518,8 +505,9 @@ int launch_norm_grad_as(const NormGradArgs& a, const WorkerRows& rows, cudaStrea
                       (LAYOUT == kVec ? GradShape<T, W, NV>::kStages * TM::kWarps * sizeof(RowCopy<T, NV, KEPT>) : 0);
   const size_t sums = TM::kTeams == 1 ? 0 : TM::kTeams * 2 * TM::kCols * sizeof(float);
   const size_t smem = std::max(work, sums);
+  static SmemAllowed allowed;
   auto kernel = norm_grad_kernel<T, LAYOUT, W, NV, KEPT>;
-  if (int rc = allow_smem(reinterpret_cast<const void*>(kernel), smem)) return rc;
+  if (int rc = allow_smem(kernel, smem, allowed)) return rc;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(rows.cta_off[rows.K])), dim3(TM::kThreads), smem, stream, a, rows);
 }
 // Teams of the gradient kernel: two slices a warp, since each costs 16 registers of sums.

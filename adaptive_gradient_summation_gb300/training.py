@@ -67,15 +67,15 @@ def _there(index: int, stream, call, *args, **more):
         return call(*args, **more)
 
 
-def _code(t, what: str) -> int:
-    """The type code of a float32 or bfloat16 CUDA tensor."""
+def _kind(t, what: str):
+    """(type code, device index) of a float32 or bfloat16 CUDA tensor."""
     try:
-        code = _CODE[t.dtype]
+        code, index = _CODE[t.dtype], t.get_device()
     except (AttributeError, KeyError):
         raise TypeError(f"{what} must be a float32 or bfloat16 tensor, got {getattr(t, 'dtype', type(t).__name__)}") from None
-    if not t.is_cuda:
+    if index < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
-    return code
+    return code, index
 
 
 def _rows(t: torch.Tensor, what: str):
@@ -114,26 +114,21 @@ def _output(out, shape, dtype, index: int) -> torch.Tensor:
     return out
 
 
-def _like(t: torch.Tensor) -> torch.Tensor:
-    """A new dense tensor of t's shape, type and device."""
-    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
-
-
 def _parameters(weight, bias, cols: int, index: int):
     """(weight's pointer, bias's, the code of their type); either may be None."""
     w = b = code = None
     if weight is not None:
-        code = _code(weight, "weight")
-        if weight.get_device() != index or weight.numel() != cols or not weight.is_contiguous():
+        code, at = _kind(weight, "weight")
+        if at != index or weight.numel() != cols or not weight.is_contiguous():
             raise ValueError(f"weight must be a contiguous tensor of {cols} elements on cuda:{index}")
         w = weight.data_ptr()
     if bias is not None:
-        c = _code(bias, "bias")
-        if bias.get_device() != index or bias.numel() != cols or not bias.is_contiguous():
+        other, at = _kind(bias, "bias")
+        if at != index or bias.numel() != cols or not bias.is_contiguous():
             raise ValueError(f"bias must be a contiguous tensor of {cols} elements on cuda:{index}")
-        if code is not None and c != code:
+        if code is not None and other != code:
             raise ValueError("weight and bias must share their dtype")
-        b, code = bias.data_ptr(), c
+        b, code = bias.data_ptr(), other
     return w, b, code or 0
 
 
@@ -155,24 +150,23 @@ def _workers(worker_offsets, rows: int):
 
 
 def _gradients(grads, K: int, numel: int, index: int, dtype, shape, what: str):
-    """(list of K tensors, their pointers, the code of their type); None allocates them."""
+    """(list of K tensors, their pointers, their type); None allocates them."""
     if grads is None:
-        grads = list(torch.empty((K, *shape), dtype=dtype, device=_DEVICES[index]).unbind(0))
+        grads = torch.empty((K, *shape), dtype=dtype, device=_DEVICES[index]).unbind(0)
     elif isinstance(grads, torch.Tensor):
-        grads = [grads] if K == 1 and grads.numel() == numel else list(grads.unbind(0))
-    else:
-        grads = list(grads)
+        grads = (grads,) if K == 1 and grads.numel() == numel else grads.unbind(0)
+    grads = list(grads)
     if len(grads) != K:
         raise ValueError(f"{what} must be one tensor for each of the {K} workers, got {len(grads)}")
-    code = _code(grads[0], what)
+    _kind(grads[0], what)
     dtype = grads[0].dtype
     ptrs = array("Q")
+    add = ptrs.append
     for g in grads:
-        if not isinstance(g, torch.Tensor) or g.dtype != dtype or g.get_device() != index or g.numel() != numel \
-                or not g.is_contiguous():
+        if g.dtype is not dtype or g.get_device() != index or g.numel() != numel or not g.is_contiguous():
             raise ValueError(f"{what} must be contiguous tensors of {numel} elements and one dtype on cuda:{index}")
-        ptrs.append(g.data_ptr())
-    return grads, ptrs, code
+        add(g.data_ptr())
+    return grads, ptrs, dtype
 
 
 def _address(a) -> int | None:
@@ -206,7 +200,7 @@ def embedding(table: torch.Tensor, tokens: torch.Tensor, *, scale: float = 1.0, 
     """``scale * table[tokens]`` (``adasum_embedding``), of shape ``(*tokens.shape, cols)`` in
     the table's dtype.  A token outside the table (the -1 that marks padding) gives zeros.
     tokens: int32 or int64."""
-    code, index = _code(table, "table"), table.get_device()
+    code, index = _kind(table, "table")
     if table.dim() != 2 or table.shape[1] == 0 or not table.is_contiguous():
         raise ValueError("table must be a contiguous matrix")
     width = _tokens(tokens, index)
@@ -233,7 +227,7 @@ def embedding_backward(grad_output: torch.Tensor, tokens: torch.Tensor, num_rows
     grad_output's), overwritten whole, or with ``accumulate`` added to.  Tokens outside the
     table and ``padding_idx`` get no gradient.
     """
-    code, index = _code(grad_output, "grad_output"), grad_output.get_device()
+    code, index = _kind(grad_output, "grad_output")
     width = _tokens(tokens, index)
     rows, cols, ld = _rows(grad_output, "grad_output")
     if grad_output.shape[:-1] != tokens.shape:
@@ -246,13 +240,13 @@ def embedding_backward(grad_output: torch.Tensor, tokens: torch.Tensor, num_rows
         return _there(index, stream, embedding_backward, grad_output, tokens, num_rows, scale=scale,
                       worker_offsets=worker_offsets, padding_idx=padding_idx, grads=grads, accumulate=accumulate)
     offs, K = _workers(worker_offsets, rows)
-    grads, ptrs, gcode = _gradients(grads, K, num_rows * cols, index, grad_output.dtype, (num_rows, cols), "grads")
+    grads, ptrs, gtype = _gradients(grads, K, num_rows * cols, index, grad_output.dtype, (num_rows, cols), "grads")
     lib = load_library()
     nbytes = lib.adasum_embedding_backward_scratch_bytes(rows, cols, K)
     scratch = _scratch(nbytes, index)
     st = lib.adasum_embedding_backward(
         grad_output.data_ptr(), cols, ld, code, tokens.data_ptr(), width, _address(offs), K, num_rows, float(scale),
-        -1 if padding_idx is None else padding_idx, _address(ptrs), gcode, bool(accumulate), _ptr(scratch), nbytes,
+        -1 if padding_idx is None else padding_idx, _address(ptrs), _CODE[gtype], bool(accumulate), _ptr(scratch), nbytes,
         _raw_stream(index))
     if st:
         check(st, "adasum_embedding_backward")
@@ -266,14 +260,15 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
                eps: float = 1e-5, out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
     """Layer norm over the last dimension (``adasum_layer_norm``): ``(y, mean, rstd)``, the
     last two in float32, for :func:`layer_norm_backward`."""
-    code, index = _code(x, "x"), x.get_device()
+    code, index = _kind(x, "x")
     rows, cols, ld = _rows(x, "x")
     w, b, wcode = _parameters(weight, bias, cols, index)
     if _elsewhere(index, stream):
         return _there(index, stream, layer_norm, x, weight, bias, eps=eps, out=out)
-    y = _like(x) if out is None else _output(out, x.shape, x.dtype, index)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    mean = torch.empty_like(rstd)
+    y = _output(out, x.shape, x.dtype, index)
+    lead = x.shape[:-1]
+    mean = torch.empty(lead, dtype=torch.float32, device=_DEVICES[index])
+    rstd = torch.empty(lead, dtype=torch.float32, device=_DEVICES[index])
     st = load_library().adasum_layer_norm(x.data_ptr(), rows, cols, ld, code, w, b, wcode, float(eps), y.data_ptr(),
                                           mean.data_ptr(), rstd.data_ptr(), None, None, _raw_stream(index))
     if st:
@@ -286,14 +281,14 @@ def layer_norm_checkpointed(x: torch.Tensor, weight: torch.Tensor | None = None,
                             stream: torch.cuda.Stream | None = None):
     """Layer norm that keeps ``h = (x - mean) rstd`` in 8 bits: ``(y, checkpoint, rstd)``, for
     :func:`layer_norm_checkpointed_backward`; neither x nor y has to be kept."""
-    code, index = _code(x, "x"), x.get_device()
+    code, index = _kind(x, "x")
     rows, cols, ld = _rows(x, "x")
     w, b, wcode = _parameters(weight, bias, cols, index)
     if _elsewhere(index, stream):
         return _there(index, stream, layer_norm_checkpointed, x, weight, bias, eps=eps, out=out)
-    y = _like(x) if out is None else _output(out, x.shape, x.dtype, index)
+    y = _output(out, x.shape, x.dtype, index)
     kept = _new_checkpoint(x, rows, cols)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=_DEVICES[index])
     st = load_library().adasum_layer_norm(x.data_ptr(), rows, cols, ld, code, w, b, wcode, float(eps), y.data_ptr(), None,
                                           rstd.data_ptr(), kept.codes.data_ptr(), kept.scales.data_ptr(),
                                           _raw_stream(index))
@@ -311,12 +306,12 @@ def _norm_gradients(grad_weights, grad_biases, weight, wanted, accumulate, K, ro
     if accumulate and (grad_weights is None or grad_biases is None):
         raise ValueError("accumulate needs grad_weights and grad_biases to add to")
     dtype = torch.float32 if weight is None else weight.dtype
-    dw, dwp, code = _gradients(grad_weights, K, cols, index, dtype, (cols,), "grad_weights")
-    db, dbp, bcode = _gradients(grad_biases, K, cols, index, dw[0].dtype, (cols,), "grad_biases")
-    if code != bcode:
+    dw, dwp, dtype = _gradients(grad_weights, K, cols, index, dtype, (cols,), "grad_weights")
+    db, dbp, other = _gradients(grad_biases, K, cols, index, dtype, (cols,), "grad_biases")
+    if other is not dtype:
         raise ValueError("grad_weights and grad_biases must share their dtype")
     nbytes = load_library().adasum_layer_norm_backward_scratch_bytes(rows, cols, K)
-    return dw, dwp, db, dbp, code, nbytes, _scratch(nbytes, index)
+    return dw, dwp, db, dbp, _CODE[dtype], nbytes, _scratch(nbytes, index)
 
 
 def layer_norm_backward(grad_output: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
@@ -329,8 +324,8 @@ def layer_norm_backward(grad_output: torch.Tensor, x: torch.Tensor, mean: torch.
     allocates them, in weight's dtype, else float32), overwritten, or with ``accumulate``
     added to; returned as lists.  ``parameter_grads=False`` leaves them out (None).
     """
-    code, index = _code(x, "x"), x.get_device()
-    if _code(grad_output, "grad_output") != code or grad_output.get_device() != index or grad_output.shape != x.shape:
+    code, index = _kind(x, "x")
+    if _kind(grad_output, "grad_output") != (code, index) or grad_output.shape != x.shape:
         raise ValueError(f"grad_output must have shape {tuple(x.shape)}, {x.dtype}, on cuda:{index}")
     rows, cols, ld_x = _rows(x, "x")
     ld_g = _rows(grad_output, "grad_output")[2]
@@ -343,7 +338,7 @@ def layer_norm_backward(grad_output: torch.Tensor, x: torch.Tensor, mean: torch.
     offs, K = _workers(worker_offsets, rows)
     dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(grad_weights, grad_biases, weight, parameter_grads,
                                                                accumulate, K, rows, cols, index)
-    dx = _like(x)
+    dx = _output(None, x.shape, x.dtype, index)
     st = load_library().adasum_layer_norm_backward(
         grad_output.data_ptr(), ld_g, x.data_ptr(), ld_x, mean_p, rstd_p, cols, code, w, wcode, _address(offs), K,
         dx.data_ptr(), _address(dwp), _address(dbp), gcode, bool(accumulate), _ptr(scratch), nbytes,
@@ -361,7 +356,7 @@ def layer_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Chec
     """``(grad_x, grad_weights, grad_biases)`` of layer norm from the 8-bit checkpoint of h
     (``adasum_layer_norm_backward_checkpointed``); with ``with_output`` also the output again,
     as a fourth.  bias is used for the output only.  The rest as in :func:`layer_norm_backward`."""
-    code, index = _code(grad_output, "grad_output"), grad_output.get_device()
+    code, index = _kind(grad_output, "grad_output")
     rows, cols, ld_g = _rows(grad_output, "grad_output")
     codes, scales = _check_checkpoint(checkpoint, index, grad_output)
     w, b, wcode = _parameters(weight, bias, cols, index)
@@ -373,8 +368,8 @@ def layer_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Chec
     offs, K = _workers(worker_offsets, rows)
     dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(grad_weights, grad_biases, weight, parameter_grads,
                                                                accumulate, K, rows, cols, index)
-    dx = _like(grad_output)
-    y = torch.empty_like(dx) if with_output else None
+    dx = _output(None, grad_output.shape, grad_output.dtype, index)
+    y = _output(None, dx.shape, dx.dtype, index) if with_output else None
     st = load_library().adasum_layer_norm_backward_checkpointed(
         grad_output.data_ptr(), ld_g, codes, scales, rstd_p, cols, code, w, b, wcode, _address(offs), K, dx.data_ptr(),
         _ptr(y), _address(dwp), _address(dbp), gcode, bool(accumulate), _ptr(scratch), nbytes, _raw_stream(index))
@@ -416,7 +411,7 @@ def _check_checkpoint(kept: Checkpoint, index: int, like: torch.Tensor | None = 
 def checkpoint_pack(x: torch.Tensor, *, stream: torch.cuda.Stream | None = None) -> Checkpoint:
     """An activation in 8 bits (``adasum_checkpoint_pack``): blocks of 128 columns, each with
     the scale max|x| / 127.  A block holding a NaN or an infinity comes back as NaN."""
-    code, index = _code(x, "x"), x.get_device()
+    code, index = _kind(x, "x")
     rows, cols, ld = _rows(x, "x")
     if _elsewhere(index, stream):
         return _there(index, stream, checkpoint_pack, x)
@@ -455,11 +450,11 @@ def gelu_checkpointed(x: torch.Tensor, *, tanh: bool = False, out: torch.Tensor 
                       stream: torch.cuda.Stream | None = None):
     """``(gelu(x), checkpoint of x)`` in one pass (``adasum_gelu_checkpointed``); ``tanh``
     selects the tanh form."""
-    code, index = _code(x, "x"), x.get_device()
+    code, index = _kind(x, "x")
     rows, cols, ld = _rows(x, "x")
     if _elsewhere(index, stream):
         return _there(index, stream, gelu_checkpointed, x, tanh=tanh, out=out)
-    y = _like(x) if out is None else _output(out, x.shape, x.dtype, index)
+    y = _output(out, x.shape, x.dtype, index)
     kept = _new_checkpoint(x, rows, cols)
     st = load_library().adasum_gelu_checkpointed(x.data_ptr(), rows, cols, ld, code, bool(tanh), y.data_ptr(),
                                                  kept.codes.data_ptr(), kept.scales.data_ptr(), _raw_stream(index))
@@ -473,14 +468,14 @@ def gelu_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Checkpoint
     """``grad_output * gelu'(x)`` for the x that the checkpoint stands for
     (``adasum_gelu_checkpointed_backward``); with ``with_output`` the pair of that and gelu(x),
     so that the forward pass's output need not be kept."""
-    code, index = _code(grad_output, "grad_output"), grad_output.get_device()
+    code, index = _kind(grad_output, "grad_output")
     rows, cols, ld = _rows(grad_output, "grad_output")
     codes, scales = _check_checkpoint(checkpoint, index, grad_output)
     if _elsewhere(index, stream):
         return _there(index, stream, gelu_checkpointed_backward, grad_output, checkpoint, tanh=tanh,
                       with_output=with_output)
-    dx = _like(grad_output)
-    y = torch.empty_like(dx) if with_output else None
+    dx = _output(None, grad_output.shape, grad_output.dtype, index)
+    y = _output(None, dx.shape, dx.dtype, index) if with_output else None
     st = load_library().adasum_gelu_checkpointed_backward(grad_output.data_ptr(), ld, codes, scales, rows, cols, code,
                                                           bool(tanh), dx.data_ptr(), _ptr(y), _raw_stream(index))
     if st:
