@@ -159,14 +159,23 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int left, int lane) {
     }
     return r;
   }
+  auto element = [&](int e) -> uint32_t {
+    const int c = lane_col<LAYOUT>(lane, e);
+    if constexpr (sizeof(T) == 2) return reinterpret_cast<const uint16_t*>(p)[c];
+    else return reinterpret_cast<const uint32_t*>(p)[c];
+  };
+  uint32_t v[8];
+  if (LAYOUT == kStrided && left >= 256) {  // (uniform over the warp: no check per element)
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T)) * 2; ++i) r.w[i] = 0u;
+    for (int e = 0; e < 8; ++e) v[e] = element(e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = lane_col<LAYOUT>(lane, e) < left ? element(e) : 0u;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int c = lane_col<LAYOUT>(lane, e);
-    if (c >= left) continue;
-    if constexpr (sizeof(T) == 2) r.w[e >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[c]) << (16 * (e & 1));
-    else r.w[e] = reinterpret_cast<const uint32_t*>(p)[c];
+    if constexpr (sizeof(T) == 4) r.w[e] = v[e];
+    else if (e & 1) r.w[e >> 1] = __byte_perm(v[e - 1], v[e], 0x5410);
   }
   return r;
 }
@@ -189,11 +198,17 @@ __device__ __forceinline__ void store8(T* p, int left, int lane, const float (&v
     }
     return;
   }
+  if (LAYOUT == kStrided && left >= 256) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[lane_col<LAYOUT>(lane, e)] = narrow<T>(v[e]);
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int c = lane_col<LAYOUT>(lane, e);
     if (c < left) p[c] = narrow<T>(v[e]);
   }
+}
 }
 
 template <typename T, int LAYOUT>
@@ -288,13 +303,19 @@ __device__ __forceinline__ uint2 load_codes8(const int8_t* p, int left, int lane
   if constexpr (LAYOUT == kVec) {  // (rows of codes are padded to 16, so a begun eight is always there)
     return lane * 8 < left ? __ldcs(reinterpret_cast<const uint2*>(p) + lane) : make_uint2(0u, 0u);
   } else {
-    uint32_t w[2] = {0u, 0u};
+    uint32_t v[8];
+    if (left >= 256) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = lane_col<LAYOUT>(lane, e);
-      if (c < left) w[e >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(p[c])) << (8 * (e & 3));
+      for (int e = 0; e < 8; ++e) v[e] = static_cast<uint8_t>(p[lane_col<LAYOUT>(lane, e)]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = lane_col<LAYOUT>(lane, e);
+        v[e] = c < left ? static_cast<uint8_t>(p[c]) : 0u;
+      }
     }
-    return make_uint2(w[0], w[1]);
+    return make_uint2(__byte_perm(__byte_perm(v[0], v[1], 0x0040), __byte_perm(v[2], v[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(v[4], v[5], 0x0040), __byte_perm(v[6], v[7], 0x0040), 0x5410));
   }
 }
 template <int LAYOUT>

@@ -417,43 +417,40 @@ enum Ends : int {
   kTail = 4,   // its last run begins here and does not end here
 };
 
-// Sums inside one chunk of sorted tokens, NV * 256 columns per CTA and a part of the chunk
-// per warp.  kVec: a lane copies its 16-byte pieces of the next rows to shared memory ahead of
-// their use (4 or 8 KiB a warp), which takes no registers and no exchange between lanes;
-// kStrided: the next row is held in registers.  Runs that cross warps are joined through
+// Sums inside one chunk of sorted tokens, 256 columns per CTA and a part of the chunk per
+// warp.  kVec: a lane copies its 16 or 32 bytes of the next rows to shared memory ahead of
+// their use (8 or 4 rows, 4 KiB a warp), which takes no registers and no exchange between
+// lanes; kStrided: the next row is held in registers.  Runs that cross warps are joined through
 // shared memory, runs that cross chunks leave their pieces in scratch memory.
 // SORT: the CTA sorts its worker's few tokens itself, and a warp takes the runs that begin in
 // its part to their end, so that nothing is left to join.
 // Bound by grad_out's bytes (each read once) and the gradient rows written.
-template <typename T, typename G, int NV, bool ADD>
+template <typename T, typename G, bool ADD>
 struct SumSmem {
   static constexpr int kAhead = 16 / sizeof(T);  // rows on their way
   static constexpr int kVecs = sizeof(T) / 2, kOldVecs = sizeof(G) / 2;  // 16-byte vectors of a lane's eight
   union {
     struct {
-      uint4 dy[kEmbWarps][kAhead][NV][kVecs][32];
-      uint4 old[ADD ? kEmbWarps : 1][ADD ? kAhead : 1][NV][kOldVecs][32];  // gradient rows to be added to
+      uint4 dy[kEmbWarps][kAhead][kVecs][32];
+      uint4 old[ADD ? kEmbWarps : 1][ADD ? kAhead : 1][kOldVecs][32];  // gradient rows to be added to
     } ring;
-    float piece[kEmbWarps][2][NV * kSlice];
+    float piece[kEmbWarps][2][kSlice];
     uint32_t unsorted[kSelfSort];
   };
 };
-template <typename T, typename G, int LAYOUT, int NV, bool SORT, bool ADD>
+template <typename T, typename G, int LAYOUT, bool SORT, bool ADD>
 __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_constant__ TableGradArgs a) {
   pdl_enter();
-  using Smem = SumSmem<T, G, NV, ADD>;
+  using Smem = SumSmem<T, G, ADD>;
   constexpr int kVecs = Smem::kVecs, kAhead = Smem::kAhead;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   __shared__ int ends[kEmbWarps], tail_key[kEmbWarps];
   __shared__ int own_keys[SORT ? kSelfSort : 1], own_pos[SORT ? kSelfSort : 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int slices = a.slices / NV;
-  const uint32_t chunk = blockIdx.x / static_cast<uint32_t>(slices);
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x - chunk * slices) * (NV * kSlice);
-  int left[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) left[j] = slice_left(a.cols, c0 + j * kSlice);
+  const uint32_t chunk = blockIdx.x / static_cast<uint32_t>(a.slices);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x - chunk * a.slices) * kSlice;
+  const int left = slice_left(a.cols, c0), cols = static_cast<int>(a.cols);
   const int k = worker_of(a.chunk_off, a.K, static_cast<int>(chunk));
   const int64_t first = a.off[k], last = a.off[k + 1];
   int64_t lo = first + (static_cast<int64_t>(chunk - a.chunk_off[k]) * kEmbWarps + w) * a.part;
@@ -505,61 +502,62 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
   if (SORT && n == 0) return;
   const T* dy = static_cast<const T*>(a.dy) + c0;
   G* grad = static_cast<G*>(a.grads[k]) + c0;
-  Raw8<T> held[NV];
-  Raw8<G> held_old[NV];
+  // kVec: where the lane's pieces of a row lie (in 16-byte units from dy; the host keeps them
+  // within 32 bits) and their bytes
+  const uint32_t ld16 = static_cast<uint32_t>(a.ld * static_cast<int>(sizeof(T)) / 16);
+  const uint32_t at16 = static_cast<uint32_t>(at) * ld16;
+  int bytes[kVecs], old_bytes[Smem::kOldVecs];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v)
+    bytes[v] = max(0, min(16, left * static_cast<int>(sizeof(T)) - (lane * kVecs + v) * 16));
+#pragma unroll
+  for (int v = 0; v < Smem::kOldVecs; ++v)
+    old_bytes[v] = max(0, min(16, left * static_cast<int>(sizeof(G)) - (lane * Smem::kOldVecs + v) * 16));
+  Raw8<T> held;
+  Raw8<G> held_old;
   int copied = -1;  // key of the last row whose copy was begun (rows below n only)
   if (!SORT && n > 0 && before == __shfl_sync(0xFFFFFFFFu, key, 0)) copied = before;  // (that run's row is not added to here)
   auto copy = [&](int i) {  // row i of the part, and the gradient row of a run that begins there
-    const int p = row_of(i), q = key_of(i);
-    const T* row = dy + static_cast<int64_t>(p) * a.ld;
-    const G* old = grad + q * a.cols;
-    const bool begins = ADD && i < n && q != copied;
-    if (i < n) copied = q;
+    bool begins = false;
+    int q = 0;
+    if constexpr (ADD) {
+      q = key_of(i);
+      begins = i < n && q != copied;
+      if (i < n) copied = q;
+    }
     if constexpr (LAYOUT == kVec) {
+      const uint32_t p16 = SORT ? static_cast<uint32_t>(row_of(i)) * ld16 : __shfl_sync(0xFFFFFFFFu, at16, i & 31);
+      const uint4* row = reinterpret_cast<const uint4*>(dy) + p16;
+      if (i < n) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        if (i < n) {
+        for (int v = 0; v < kVecs; ++v)
+          cp_async16(smem_addr(&sm.ring.dy[w][i % kAhead][v][lane]), bytes[v] > 0 ? row + lane * kVecs + v : row, bytes[v]);
+      }
+      if (begins) {
+        const G* old = grad + static_cast<int64_t>(q) * cols;
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) {
-            const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(T));
-            const int bytes = max(0, min(16, (left[j] - c) * static_cast<int>(sizeof(T))));
-            cp_async16(smem_addr(&sm.ring.dy[w][i % kAhead][j][v][lane]), row + (bytes > 0 ? j * kSlice + c : 0), bytes);
-          }
-        }
-        if (begins) {
-#pragma unroll
-          for (int v = 0; v < Smem::kOldVecs; ++v) {
-            const int c = lane * 8 + v * 16 / static_cast<int>(sizeof(G));
-            const int bytes = max(0, min(16, (left[j] - c) * static_cast<int>(sizeof(G))));
-            cp_async16(smem_addr(&sm.ring.old[w][i % kAhead][j][v][lane]), old + (bytes > 0 ? j * kSlice + c : 0), bytes);
-          }
-        }
+        for (int v = 0; v < Smem::kOldVecs; ++v)
+          cp_async16(smem_addr(&sm.ring.old[w][i % kAhead][v][lane]),
+                     old + (old_bytes[v] > 0 ? (lane * Smem::kOldVecs + v) * 16 / static_cast<int>(sizeof(G)) : 0), old_bytes[v]);
       }
       cp_async_commit();
     } else {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        held[j] = load8<T, LAYOUT>(row + j * kSlice, i < n ? left[j] : 0, lane);
-        if constexpr (ADD) held_old[j] = load8<G, LAYOUT>(old + j * kSlice, begins ? left[j] : 0, lane);
-      }
+      held = load8<T, LAYOUT>(dy + static_cast<int64_t>(row_of(i)) * a.ld, i < n ? left : 0, lane);
+      if constexpr (ADD) held_old = load8<G, LAYOUT>(grad + static_cast<int64_t>(q) * cols, begins ? left : 0, lane);
     }
   };
   constexpr int kLead = LAYOUT == kVec ? kAhead : 1;
   for (int i = 0; i < kLead; ++i) copy(i);
-  F2 acc[NV][4], head[SORT ? 1 : NV][4];
-  Raw8<G> old[NV] = {};
-  auto clear = [&](auto& v) {
+  F2 acc[4], head[4];
+  Raw8<G> old = {};
+  auto clear = [&](F2 (&v)[4]) {
 #pragma unroll
-    for (auto& x : v)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = f2(0.f);
+    for (int e = 0; e < 4; ++e) v[e] = f2(0.f);
   };
   clear(acc);
-  if constexpr (!SORT) clear(head);
+  clear(head);
   auto put = [&](int row) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      put_row<G, LAYOUT, ADD>(grad + row * a.cols + j * kSlice, a.scale, left[j], lane, acc[j], old[j]);
+    put_row<G, LAYOUT, ADD>(grad + static_cast<int64_t>(row) * cols, a.scale, left, lane, acc, old);
   };
   int cur = n > 0 ? key_of(0) : -1, found = 0;
   bool from_before = !SORT && n > 0 && before == cur, fresh = !from_before;
@@ -570,12 +568,8 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
       const bool goes_on = !SORT && i == n && i == m && after == cur;
       if (from_before) {
         found |= goes_on ? kHead | kSpan : kHead;
-        if constexpr (!SORT) {
 #pragma unroll
-          for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) head[j][e] = acc[j][e];
-        }
+        for (int e = 0; e < 4; ++e) head[e] = acc[e];
       } else if (goes_on) {
         found |= kTail;
       } else {
@@ -587,24 +581,21 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
       fresh = true;
       clear(acc);
     }
-    if constexpr (LAYOUT == kVec) cp_async_wait<kAhead - 1>();
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      F2 v[4];
-      if constexpr (LAYOUT == kVec) {
-        Raw8<T> r;
-        gather8<T>(r, sm.ring.dy[w][i % kAhead][j], lane);
-        unpack8<T>(r, v);
-        if constexpr (ADD)
-          if (fresh) gather8<G>(old[j], sm.ring.old[w][i % kAhead][j], lane);
-      } else {
-        unpack8<T>(held[j], v);
-        if constexpr (ADD)
-          if (fresh) old[j] = held_old[j];
-      }
-      add8(acc[j], v);
+    F2 v[4];
+    if constexpr (LAYOUT == kVec) {
+      cp_async_wait<kAhead - 1>();
+      Raw8<T> r;
+      gather8<T>(r, sm.ring.dy[w][i % kAhead], lane);
+      unpack8<T>(r, v);
+      if constexpr (ADD)
+        if (fresh) gather8<G>(old, sm.ring.old[w][i % kAhead], lane);
+    } else {
+      unpack8<T>(held, v);
+      if constexpr (ADD)
+        if (fresh) old = held_old;
     }
     fresh = false;
+    add8(acc, v);
     copy(i + kLead);
   }
   if constexpr (!SORT) {
@@ -616,33 +607,24 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
       tail_key[w] = cur;
     }
     if (!__syncthreads_or(found)) return;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (found & kHead) sts8(sm.piece[w][0] + j * kSlice, lane, head[j]);
-      if (found & kTail) sts8(sm.piece[w][1] + j * kSlice, lane, acc[j]);
-    }
+    if (found & kHead) sts8(sm.piece[w][0], lane, head);
+    if (found & kTail) sts8(sm.piece[w][1], lane, acc);
     __syncthreads();
     for (int slot = 0; slot < 2; ++slot) {
       // slot 0: the run that enters the chunk (warp 0's head); slot 1: a run that begins here
       if (!(ends[w] & (slot ? kTail : kHead)) || (slot == 0 && w > 0)) continue;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) lds8(sm.piece[w][slot] + j * kSlice, lane, acc[j]);
+      lds8(sm.piece[w][slot], lane, acc);
       bool open = slot == 1 || (ends[w] & kSpan);
       int u = w + 1;
       for (; open && u < kEmbWarps && (ends[u] & kHead); ++u) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          F2 v[4];
-          lds8(sm.piece[u][0] + j * kSlice, lane, v);
-          add8(acc[j], v);
-        }
+        F2 v[4];
+        lds8(sm.piece[u][0], lane, v);
+        add8(acc, v);
         open = ends[u] & kSpan;
       }
       open = open && u == kEmbWarps && chunk_end < last;
       if (slot == 0 || open) {
-        float* p = a.partials + (static_cast<int64_t>(chunk) * 2 + slot) * a.cols + c0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) store8<float, LAYOUT>(p + j * kSlice, left[j], lane, acc[j]);
+        store8<float, LAYOUT>(a.partials + (static_cast<int64_t>(chunk) * 2 + slot) * a.cols + c0, left, lane, acc);
         if (slot == 1 && c0 == 0 && lane == 0) a.list[atomicAdd(a.count, 1)] = static_cast<int>(chunk);
       } else {
         put(tail_key[w]);
@@ -717,29 +699,23 @@ template <typename T>
 int launch_lookup(const LookupArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
   return launch_pdl(vec ? lookup_kernel<T, kVec> : lookup_kernel<T, kStrided>, dim3(grid), dim3(kEmbThreads), 0, stream, a);
 }
-template <typename T, typename G, int LAYOUT, int NV, bool SORT, bool ADD>
-int launch_sum_as(const TableGradArgs& a, cudaStream_t stream) {
-  auto kernel = table_sum_kernel<T, G, LAYOUT, NV, SORT, ADD>;
-  constexpr size_t smem = sizeof(SumSmem<T, G, NV, ADD>);
+template <typename T, typename G, int LAYOUT, bool SORT, bool ADD>
+int launch_sum_as(const TableGradArgs& a, unsigned grid, cudaStream_t stream) {
+  auto kernel = table_sum_kernel<T, G, LAYOUT, SORT, ADD>;
+  constexpr size_t smem = sizeof(SumSmem<T, G, ADD>);
   static SmemAllowed allowed;
   if (int rc = allow_smem(kernel, smem, allowed)) return rc;
-  TableGradArgs b = a;
-  b.slices = (a.slices + NV - 1) / NV * NV;
-  const unsigned grid = static_cast<unsigned>(a.chunk_off[a.K]) * static_cast<unsigned>(b.slices / NV);
-  return launch_pdl(kernel, dim3(grid), dim3(kEmbThreads), smem, stream, b);
+  return launch_pdl(kernel, dim3(grid), dim3(kEmbThreads), smem, stream, a);
 }
-// Two slices a warp halve what a token costs besides its bytes; with few tokens, or gradient
-// rows on their way as well, one slice leaves more warps.
 template <typename T, typename G, int LAYOUT>
-int launch_sum_layout(const TableGradArgs& a, bool sort, bool wide, cudaStream_t stream) {
+int launch_sum_layout(const TableGradArgs& a, bool sort, unsigned grid, cudaStream_t stream) {
   if (a.accumulate)
-    return sort ? launch_sum_as<T, G, LAYOUT, 1, true, true>(a, stream) : launch_sum_as<T, G, LAYOUT, 1, false, true>(a, stream);
-  if (sort) return launch_sum_as<T, G, LAYOUT, 1, true, false>(a, stream);
-  return wide ? launch_sum_as<T, G, LAYOUT, 2, false, false>(a, stream) : launch_sum_as<T, G, LAYOUT, 1, false, false>(a, stream);
+    return sort ? launch_sum_as<T, G, LAYOUT, true, true>(a, grid, stream) : launch_sum_as<T, G, LAYOUT, false, true>(a, grid, stream);
+  return sort ? launch_sum_as<T, G, LAYOUT, true, false>(a, grid, stream) : launch_sum_as<T, G, LAYOUT, false, false>(a, grid, stream);
 }
 template <typename T, typename G>
-int launch_sum(const TableGradArgs& a, bool vec, bool sort, bool wide, cudaStream_t stream) {
-  return vec ? launch_sum_layout<T, G, kVec>(a, sort, wide, stream) : launch_sum_layout<T, G, kStrided>(a, sort, wide, stream);
+int launch_sum(const TableGradArgs& a, bool vec, bool sort, unsigned grid, cudaStream_t stream) {
+  return vec ? launch_sum_layout<T, G, kVec>(a, sort, grid, stream) : launch_sum_layout<T, G, kStrided>(a, sort, grid, stream);
 }
 template <typename G>
 int launch_join(const TableGradArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
@@ -813,7 +789,9 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   set.read(grad_out, span_bytes(n, cols, ld, e));
   set.read(tokens, n * token_bytes);
   set.write(scratch, need);
-  bool vec = is_aligned(grad_out, 16) && ld * e % 16 == 0 && cols * ge % 16 == 0 && cols * e % 16 == 0;
+  // (rows of grad_out are addressed by 32 bits of 16-byte units)
+  bool vec = is_aligned(grad_out, 16) && ld * e % 16 == 0 && cols * ge % 16 == 0 && cols * e % 16 == 0 &&
+             span_bytes(n, cols, ld, e) < (int64_t(16) << 32);
   int64_t most = 0;
   for (int k = 0; k < K; ++k) most = std::max(most, worker_offsets[k + 1] - worker_offsets[k]);
   // (a key and an index share 32 bits where a CTA sorts by itself)
@@ -907,13 +885,13 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   a.list = ints(at.list);
   a.partials = reinterpret_cast<float*>(base + at.partials);
   const int64_t items = static_cast<int64_t>(a.chunk_off[K]) * a.slices;
-  const bool wide = a.slices >= 2 && n * a.slices >= 16 * 4864;
+  const unsigned grid = static_cast<unsigned>(items);
   if (adasum_status_t st = counted_launch(stream, "table_sum", static_cast<double>(n) * (cols * e + 8), [&] {
         if (dtype == ADASUM_BF16)
-          return grad_dtype == ADASUM_BF16 ? launch_sum<bf16, bf16>(a, vec, self_sort, wide, stream)
-                                           : launch_sum<bf16, float>(a, vec, self_sort, wide, stream);
-        return grad_dtype == ADASUM_BF16 ? launch_sum<float, bf16>(a, vec, self_sort, wide, stream)
-                                         : launch_sum<float, float>(a, vec, self_sort, wide, stream);
+          return grad_dtype == ADASUM_BF16 ? launch_sum<bf16, bf16>(a, vec, self_sort, grid, stream)
+                                           : launch_sum<bf16, float>(a, vec, self_sort, grid, stream);
+        return grad_dtype == ADASUM_BF16 ? launch_sum<float, bf16>(a, vec, self_sort, grid, stream)
+                                         : launch_sum<float, float>(a, vec, self_sort, grid, stream);
       }))
     return st;
   if (self_sort || most <= span) return ADASUM_OK;  // no run crosses chunks
