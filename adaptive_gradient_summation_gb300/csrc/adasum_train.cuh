@@ -209,7 +209,6 @@ __device__ __forceinline__ void store8(T* p, int left, int lane, const float (&v
     if (c < left) p[c] = narrow<T>(v[e]);
   }
 }
-}
 
 template <typename T, int LAYOUT>
 __device__ __forceinline__ void store8(T* p, int left, int lane, const F2 (&v)[4]) {
