@@ -94,15 +94,19 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 
 // ------------------------------------------------------------- eight columns of a lane
 
-// A warp covers 256 columns of a row at a time, eight per lane.  kVec: lane l holds the
-// neighbouring columns 8 l .. 8 l + 7, moved as 16-byte vectors; it needs rows that start
-// on 16-byte boundaries.  kStrided: lane l holds columns l, l + 32, ..., l + 224, moved one
-// by one but coalesced over the lanes; for every other address.
-enum Layout : int { kStrided = 0, kVec = 1 };
+// A warp covers 256 columns of a row at a time, eight per lane, as 8 / N pieces of N
+// neighbouring columns: piece i of lane l holds columns (32 i + l) N .. (32 i + l) N + N - 1,
+// so that a warp's access to a piece is contiguous.  N = 8 for bf16 and 4 for fp32 make
+// pieces of 16 bytes (fp32 as eight neighbours a lane, two accesses with gaps, measured 35
+// against 30 us for a lookup of 32768 x 1024); N = 4 also serves bf16 beside fp32 in one
+// kernel.  They need rows that start on a piece's boundary; N = 1 takes every address.
+enum Layout : int { kStrided = 1, kVec4 = 4, kVec8 = 8 };
+template <typename T>
+constexpr int kWide = sizeof(T) == 2 ? kVec8 : kVec4;
 
-template <int LAYOUT>
+template <int N>
 __device__ __forceinline__ int lane_col(int lane, int e) {
-  return LAYOUT == kVec ? lane * 8 + e : e * 32 + lane;
+  return (e / N * 32 + lane) * N + e % N;
 }
 
 // Raw bits of a lane's eight values.
@@ -124,19 +128,6 @@ __device__ __forceinline__ void unpack8(const Raw8<T>& r, F2 (&v)[4]) {
   for (int i = 0; i < 4; ++i) v[i] = f2(raw_value<T>(r, 2 * i), raw_value<T>(r, 2 * i + 1));
 }
 
-// A lane's eight values from its 16-byte vectors in shared memory.
-template <typename T>
-__device__ __forceinline__ void gather8(Raw8<T>& r, const uint4 (&from)[sizeof(T) / 2][32], int lane) {
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
-    const uint4 x = from[i][lane];
-    r.w[4 * i] = x.x;
-    r.w[4 * i + 1] = x.y;
-    r.w[4 * i + 2] = x.z;
-    r.w[4 * i + 3] = x.w;
-  }
-}
-
 // Columns of a slice that starts at c0, at most 256, none past the row's end.
 __device__ __forceinline__ int slice_left(int64_t cols, int64_t c0) {
   return static_cast<int>(max(static_cast<int64_t>(0), min(cols - c0, static_cast<int64_t>(256))));
@@ -144,41 +135,91 @@ __device__ __forceinline__ int slice_left(int64_t cols, int64_t c0) {
 
 // Loads the values of 256 columns starting at p, of which `left` exist (others are 0).
 // KEEP: the data will be read again (default: streaming).
-template <typename T, int LAYOUT, bool KEEP = false>
+template <typename T, int N, bool KEEP = false>
 __device__ __forceinline__ Raw8<T> load8(const T* p, int left, int lane) {
+  constexpr int kWords = N * static_cast<int>(sizeof(T)) / 4;  // of a piece
   Raw8<T> r;
-  if (LAYOUT == kVec && lane * 8 + 8 <= left) {
-    const uint4* q = reinterpret_cast<const uint4*>(p + lane * 8);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i) {
-      const uint4 v = KEEP ? __ldg(q + i) : __ldcs(q + i);
-      r.w[4 * i] = v.x;
-      r.w[4 * i + 1] = v.y;
-      r.w[4 * i + 2] = v.z;
-      r.w[4 * i + 3] = v.w;
-    }
-    return r;
-  }
-  auto element = [&](int e) -> uint32_t {
-    const int c = lane_col<LAYOUT>(lane, e);
+  auto element = [&](int c) -> uint32_t {
     if constexpr (sizeof(T) == 2) return reinterpret_cast<const uint16_t*>(p)[c];
     else return reinterpret_cast<const uint32_t*>(p)[c];
   };
-  uint32_t v[8];
-  if (LAYOUT == kStrided && left >= 256) {  // (uniform over the warp: no check per element)
+  if constexpr (N == kStrided) {
+    uint32_t v[8];
+    if (left >= 256) {  // (uniform over the warp: no check per element)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = element(e);
+      for (int e = 0; e < 8; ++e) v[e] = element(lane_col<N>(lane, e));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = lane_col<N>(lane, e) < left ? element(lane_col<N>(lane, e)) : 0u;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (sizeof(T) == 4) r.w[e] = v[e];
+      else if (e & 1) r.w[e >> 1] = __byte_perm(v[e - 1], v[e], 0x5410);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = lane_col<LAYOUT>(lane, e) < left ? element(e) : 0u;
-  }
+    for (int i = 0; i < 8 / N; ++i) {
+      const int c = lane_col<N>(lane, i * N);
+      uint32_t* w = r.w + i * kWords;
+      if (c + N <= left) {
+        if constexpr (kWords == 4) {
+          const uint4* q = reinterpret_cast<const uint4*>(p + c);
+          const uint4 v = KEEP ? __ldg(q) : __ldcs(q);
+          w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+          static_assert(kWords == 2 || kWords == 4, "pieces of 8 or 16 bytes");
+          const uint2* q = reinterpret_cast<const uint2*>(p + c);
+          const uint2 v = KEEP ? __ldg(q) : __ldcs(q);
+          w[0] = v.x, w[1] = v.y;
+        }
+      } else {
+        uint32_t v[N];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if constexpr (sizeof(T) == 4) r.w[e] = v[e];
-    else if (e & 1) r.w[e >> 1] = __byte_perm(v[e - 1], v[e], 0x5410);
+        for (int e = 0; e < N; ++e) v[e] = c + e < left ? element(c + e) : 0u;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          if constexpr (sizeof(T) == 4) w[e] = v[e];
+          else if (e & 1) w[e >> 1] = __byte_perm(v[e - 1], v[e], 0x5410);
+        }
+      }
+    }
   }
   return r;
 }
+
+// 256 columns on their way through shared memory.  A lane copies the pieces that it will use
+// itself, so that nothing has to be exchanged: `copy` starts it (past the row's end come
+// zeros), `take` reads them once cp_async_wait has returned.
+template <typename T, int N>
+struct alignas(16) LaneSlot {
+  static constexpr int kBytes = N * static_cast<int>(sizeof(T)), kWords = kBytes / 4;  // of a piece
+  uint32_t w[8 / N][32][kWords];
+  __device__ __forceinline__ void copy(const T* p, int left, int lane) {
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) {
+      const int c = lane_col<N>(lane, i * N);
+      const int bytes = max(0, min(kBytes, (left - c) * static_cast<int>(sizeof(T))));
+      const T* from = p + (bytes > 0 ? c : 0);
+      if constexpr (kBytes == 16) cp_async16(smem_addr(w[i][lane]), from, bytes);
+      else cp_async_small<kBytes>(smem_addr(w[i][lane]), from, bytes);
+    }
+  }
+  __device__ __forceinline__ Raw8<T> take(int lane) const {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < 8 / N; ++i) {
+      if constexpr (kWords == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(w[i][lane]);
+        r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(w[i][lane]);
+        r.w[2 * i] = v.x, r.w[2 * i + 1] = v.y;
+      }
+    }
+    return r;
+  }
+};
 
 __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
@@ -186,27 +227,36 @@ __device__ __forceinline__ uint32_t pack2_bf16(float lo, float hi) {
 }
 
 // Stores eight values of 256 columns starting at p, of which `left` exist.
-template <typename T, int LAYOUT>
+template <typename T, int N>
 __device__ __forceinline__ void store8(T* p, int left, int lane, const float (&v)[8]) {
-  if (LAYOUT == kVec && lane * 8 + 8 <= left) {
-    uint4* q = reinterpret_cast<uint4*>(p + lane * 8);
-    if constexpr (sizeof(T) == 2) {
-      __stcs(q, make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7])));
-    } else {
-      __stcs(reinterpret_cast<float4*>(q), make_float4(v[0], v[1], v[2], v[3]));
-      __stcs(reinterpret_cast<float4*>(q) + 1, make_float4(v[4], v[5], v[6], v[7]));
+  if constexpr (N == kStrided) {
+    if (left >= 256) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[lane_col<N>(lane, e)] = narrow<T>(v[e]);
+      return;
     }
-    return;
-  }
-  if (LAYOUT == kStrided && left >= 256) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[lane_col<LAYOUT>(lane, e)] = narrow<T>(v[e]);
-    return;
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = lane_col<LAYOUT>(lane, e);
-    if (c < left) p[c] = narrow<T>(v[e]);
+  for (int i = 0; i < 8 / N; ++i) {
+    const int c = lane_col<N>(lane, i * N);
+    const float* x = v + i * N;
+    if constexpr (N > 1) {
+      if (c + N <= left) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int e = 0; e < N; e += 4) __stcs(reinterpret_cast<float4*>(p + c + e), make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]));
+        } else if constexpr (N == 8) {
+          __stcs(reinterpret_cast<uint4*>(p + c), make_uint4(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]),
+                                                             pack2_bf16(x[4], x[5]), pack2_bf16(x[6], x[7])));
+        } else {
+          __stcs(reinterpret_cast<uint2*>(p + c), make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3])));
+        }
+        continue;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (c + e < left) p[c + e] = narrow<T>(x[e]);
   }
 }
 
@@ -296,20 +346,23 @@ __device__ __forceinline__ void ckpt_values8(uint2 q, float lo_scale, float hi_s
 }
 
 // Codes of 256 columns, the same columns per lane as the values'; rows of codes start on
-// 16-byte boundaries whatever the layout of the values.
-template <int LAYOUT>
+// 16-byte boundaries, and are padded to them, so that a begun piece is always there.
+template <int N>
 __device__ __forceinline__ uint2 load_codes8(const int8_t* p, int left, int lane) {
-  if constexpr (LAYOUT == kVec) {  // (rows of codes are padded to 16, so a begun eight is always there)
+  if constexpr (N == kVec8) {
     return lane * 8 < left ? __ldcs(reinterpret_cast<const uint2*>(p) + lane) : make_uint2(0u, 0u);
+  } else if constexpr (N == kVec4) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + lane;
+    return make_uint2(lane * 4 < left ? __ldcs(q) : 0u, 128 + lane * 4 < left ? __ldcs(q + 32) : 0u);
   } else {
     uint32_t v[8];
     if (left >= 256) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = static_cast<uint8_t>(p[lane_col<LAYOUT>(lane, e)]);
+      for (int e = 0; e < 8; ++e) v[e] = static_cast<uint8_t>(p[lane_col<N>(lane, e)]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int c = lane_col<LAYOUT>(lane, e);
+        const int c = lane_col<N>(lane, e);
         v[e] = c < left ? static_cast<uint8_t>(p[c]) : 0u;
       }
     }
@@ -317,14 +370,18 @@ __device__ __forceinline__ uint2 load_codes8(const int8_t* p, int left, int lane
                       __byte_perm(__byte_perm(v[4], v[5], 0x0040), __byte_perm(v[6], v[7], 0x0040), 0x5410));
   }
 }
-template <int LAYOUT>
+template <int N>
 __device__ __forceinline__ void store_codes8(int8_t* p, int left, int lane, uint2 q) {
-  if constexpr (LAYOUT == kVec) {
+  if constexpr (N == kVec8) {
     if (lane * 8 < left) __stcs(reinterpret_cast<uint2*>(p) + lane, q);
+  } else if constexpr (N == kVec4) {
+    uint32_t* to = reinterpret_cast<uint32_t*>(p) + lane;
+    if (lane * 4 < left) __stcs(to, q.x);
+    if (128 + lane * 4 < left) __stcs(to + 32, q.y);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = lane_col<LAYOUT>(lane, e);
+      const int c = lane_col<N>(lane, e);
       if (c < left) p[c] = static_cast<int8_t>(((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 0xFFu);
     }
   }
@@ -332,13 +389,13 @@ __device__ __forceinline__ void store_codes8(int8_t* p, int left, int lane, uint
 
 // Largest magnitudes of the (one or two) blocks that a lane's eight of 256 columns lie in,
 // from all the lanes' values (NaN if there is one); columns past the row's end hold 0.
-// kVec: a block is half a warp; kStrided: a block is four values of every lane.
+// N = 8: a block is half a warp; otherwise it is four values of every lane.
 template <int LAYOUT>
 __device__ __forceinline__ void block_tops(const F2 (&v)[4], float (&top)[2]) {
   const float2 a = parts(v[0]), b = parts(v[1]), c = parts(v[2]), d = parts(v[3]);
   top[0] = max_abs_nan(max_abs_nan(a.x, a.y, b.x), b.y, b.y);
   top[1] = max_abs_nan(max_abs_nan(c.x, c.y, d.x), d.y, d.y);
-  if constexpr (LAYOUT == kVec) {
+  if constexpr (LAYOUT == kVec8) {
     top[0] = max_nan(top[0], top[1]);
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) top[0] = max_nan(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], d));
@@ -353,29 +410,29 @@ __device__ __forceinline__ void block_tops(const F2 (&v)[4], float (&top)[2]) {
 
 // Scales of the blocks of N slices of 256 columns, from block_tops.  The two quotients cost
 // more than the codes of a lane's eight values, so each lane computes those of one slice
-// (and, with kStrided, one block) and the others take them from it.
+// (and one block) and the others take them from it.
 template <int LAYOUT, int N>
 __device__ __forceinline__ void block_scales(const float (&top)[N][2], int lane, CkptScale (&s)[N][2]) {
-  constexpr int kJobs = LAYOUT == kVec ? N : 2 * N;
+  constexpr int kJobs = LAYOUT == kVec8 ? N : 2 * N;
   static_assert(kJobs <= 16, "one lane of a half warp per scale");
   float mine = top[0][0];
 #pragma unroll
   for (int j = 1; j < kJobs; ++j)
-    if ((lane & 15) == j) mine = LAYOUT == kVec ? top[j][0] : top[j >> 1][j & 1];
+    if ((lane & 15) == j) mine = LAYOUT == kVec8 ? top[j][0] : top[j >> 1][j & 1];
   const CkptScale r = ckpt_scale(mine, !(mine < __int_as_float(0x7F800000)));
 #pragma unroll
   for (int j = 0; j < kJobs; ++j) {
     const int from = (lane & 16) | j;
-    CkptScale& to = LAYOUT == kVec ? s[j][0] : s[j >> 1][j & 1];
+    CkptScale& to = LAYOUT == kVec8 ? s[j][0] : s[j >> 1][j & 1];
     to.scale = __shfl_sync(0xFFFFFFFFu, r.scale, from);
     to.inv = __shfl_sync(0xFFFFFFFFu, r.inv, from);
-    if (LAYOUT == kVec) s[j][1] = to;
+    if (LAYOUT == kVec8) s[j][1] = to;
   }
 }
 // Stores the scales of 256 columns, of which `left` exist, at p.
 template <int LAYOUT>
 __device__ __forceinline__ void store_scales(float* p, int left, int lane, const CkptScale (&s)[2]) {
-  if constexpr (LAYOUT == kVec) {
+  if constexpr (LAYOUT == kVec8) {
     if ((lane & 15) == 0 && lane * 8 < left) p[lane >> 4] = s[0].scale;
   } else {
     if (lane == 0) {
@@ -386,12 +443,12 @@ __device__ __forceinline__ void store_scales(float* p, int left, int lane, const
 }
 template <int LAYOUT>
 __device__ __forceinline__ uint2 ckpt_codes(const F2 (&v)[4], const CkptScale (&s)[2]) {
-  return ckpt_codes8(v, s[0].inv, LAYOUT == kVec ? s[0].inv : s[1].inv);
+  return ckpt_codes8(v, s[0].inv, LAYOUT == kVec8 ? s[0].inv : s[1].inv);
 }
 // Values of 256 columns' codes, of which `left` columns exist; p: their scales.
 template <int LAYOUT>
 __device__ __forceinline__ void ckpt_values(uint2 q, const float* p, int left, int lane, F2 (&v)[4]) {
-  if constexpr (LAYOUT == kVec) {
+  if constexpr (LAYOUT == kVec8) {
     const float s = lane * 8 < left ? p[lane >> 4] : 0.f;
     ckpt_values8(q, s, s, v);
   } else {

@@ -294,9 +294,9 @@ adasum_status_t pack(PackArgs a, int dtype, int act, cudaStream_t stream) {
     const bool dense = a.rows == 1;
     if (dtype == kBF16)
       return !vec ? launch_pack<bf16, kStrided, false>(a, act, stream)
-                  : dense ? launch_pack<bf16, kVec, true>(a, act, stream) : launch_pack<bf16, kVec, false>(a, act, stream);
+                  : dense ? launch_pack<bf16, kVec8, true>(a, act, stream) : launch_pack<bf16, kVec8, false>(a, act, stream);
     return !vec ? launch_pack<float, kStrided, false>(a, act, stream)
-                : dense ? launch_pack<float, kVec, true>(a, act, stream) : launch_pack<float, kVec, false>(a, act, stream);
+                : dense ? launch_pack<float, kVec4, true>(a, act, stream) : launch_pack<float, kVec4, false>(a, act, stream);
   });
 }
 
@@ -323,9 +323,9 @@ adasum_status_t unpack(UnpackArgs a, int dtype, int act, cudaStream_t stream) {
     const bool dense = a.rows == 1;
     if (dtype == kBF16)
       return !vec ? launch_unpack<bf16, kStrided, false>(a, act, stream)
-                  : dense ? launch_unpack<bf16, kVec, true>(a, act, stream) : launch_unpack<bf16, kVec, false>(a, act, stream);
+                  : dense ? launch_unpack<bf16, kVec8, true>(a, act, stream) : launch_unpack<bf16, kVec8, false>(a, act, stream);
     return !vec ? launch_unpack<float, kStrided, false>(a, act, stream)
-                : dense ? launch_unpack<float, kVec, true>(a, act, stream) : launch_unpack<float, kVec, false>(a, act, stream);
+                : dense ? launch_unpack<float, kVec4, true>(a, act, stream) : launch_unpack<float, kVec4, false>(a, act, stream);
   });
 }
 

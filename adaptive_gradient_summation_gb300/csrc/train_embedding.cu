@@ -418,21 +418,23 @@ enum Ends : int {
 };
 
 // Sums inside one chunk of sorted tokens, 256 columns per CTA and a part of the chunk per
-// warp.  kVec: a lane copies its 16 or 32 bytes of the next rows to shared memory ahead of
-// their use (8 or 4 rows, 4 KiB a warp), which takes no registers and no exchange between
-// lanes; kStrided: the next row is held in registers.  Runs that cross warps are joined through
+// warp.  A lane copies its pieces of the next rows to shared memory ahead of their use (8 or
+// 4 rows, 4 KiB a warp), which takes no registers and no exchange between lanes (N = 1: the
+// next row is held in registers).  Runs that cross warps are joined through
 // shared memory, runs that cross chunks leave their pieces in scratch memory.
 // SORT: the CTA sorts its worker's few tokens itself, and a warp takes the runs that begin in
 // its part to their end, so that nothing is left to join.
 // Bound by grad_out's bytes (each read once) and the gradient rows written.
-template <typename T, typename G, bool ADD>
+template <typename T, typename G, int LAYOUT, bool ADD>
 struct SumSmem {
   static constexpr int kAhead = 16 / sizeof(T);  // rows on their way
-  static constexpr int kVecs = sizeof(T) / 2, kOldVecs = sizeof(G) / 2;  // 16-byte vectors of a lane's eight
+  static constexpr int kRing = LAYOUT != kStrided ? kEmbWarps : 1, kOld = LAYOUT != kStrided && ADD ? kEmbWarps : 1;
+  using Slot = LaneSlot<T, LAYOUT != kStrided ? LAYOUT : kWide<T>>;
+  using OldSlot = LaneSlot<G, LAYOUT != kStrided ? LAYOUT : kWide<G>>;
   union {
     struct {
-      uint4 dy[kEmbWarps][kAhead][kVecs][32];
-      uint4 old[ADD ? kEmbWarps : 1][ADD ? kAhead : 1][kOldVecs][32];  // gradient rows to be added to
+      Slot dy[kRing][kAhead];
+      OldSlot old[kOld][kAhead];  // gradient rows to be added to
     } ring;
     float piece[kEmbWarps][2][kSlice];
     uint32_t unsorted[kSelfSort];
@@ -441,8 +443,8 @@ struct SumSmem {
 template <typename T, typename G, int LAYOUT, bool SORT, bool ADD>
 __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_constant__ TableGradArgs a) {
   pdl_enter();
-  using Smem = SumSmem<T, G, ADD>;
-  constexpr int kVecs = Smem::kVecs, kAhead = Smem::kAhead;
+  using Smem = SumSmem<T, G, LAYOUT, ADD>;
+  constexpr int kAhead = Smem::kAhead;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   __shared__ int ends[kEmbWarps], tail_key[kEmbWarps];
@@ -502,17 +504,9 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
   if (SORT && n == 0) return;
   const T* dy = static_cast<const T*>(a.dy) + c0;
   G* grad = static_cast<G*>(a.grads[k]) + c0;
-  // kVec: where the lane's pieces of a row lie (in 16-byte units from dy; the host keeps them
-  // within 32 bits) and their bytes
-  const uint32_t ld16 = static_cast<uint32_t>(a.ld * static_cast<int>(sizeof(T)) / 16);
-  const uint32_t at16 = static_cast<uint32_t>(at) * ld16;
-  int bytes[kVecs], old_bytes[Smem::kOldVecs];
-#pragma unroll
-  for (int v = 0; v < kVecs; ++v)
-    bytes[v] = max(0, min(16, left * static_cast<int>(sizeof(T)) - (lane * kVecs + v) * 16));
-#pragma unroll
-  for (int v = 0; v < Smem::kOldVecs; ++v)
-    old_bytes[v] = max(0, min(16, left * static_cast<int>(sizeof(G)) - (lane * Smem::kOldVecs + v) * 16));
+  // where a row lies, in units of 8 bytes from dy (the host keeps them within 32 bits; N > 1)
+  const uint32_t ld8 = static_cast<uint32_t>(a.ld * static_cast<int>(sizeof(T)) / 8);
+  const uint32_t at8 = static_cast<uint32_t>(at) * ld8;
   Raw8<T> held;
   Raw8<G> held_old;
   int copied = -1;  // key of the last row whose copy was begun (rows below n only)
@@ -525,28 +519,17 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
       begins = i < n && q != copied;
       if (i < n) copied = q;
     }
-    if constexpr (LAYOUT == kVec) {
-      const uint32_t p16 = SORT ? static_cast<uint32_t>(row_of(i)) * ld16 : __shfl_sync(0xFFFFFFFFu, at16, i & 31);
-      const uint4* row = reinterpret_cast<const uint4*>(dy) + p16;
-      if (i < n) {
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-          cp_async16(smem_addr(&sm.ring.dy[w][i % kAhead][v][lane]), bytes[v] > 0 ? row + lane * kVecs + v : row, bytes[v]);
-      }
-      if (begins) {
-        const G* old = grad + static_cast<int64_t>(q) * cols;
-#pragma unroll
-        for (int v = 0; v < Smem::kOldVecs; ++v)
-          cp_async16(smem_addr(&sm.ring.old[w][i % kAhead][v][lane]),
-                     old + (old_bytes[v] > 0 ? (lane * Smem::kOldVecs + v) * 16 / static_cast<int>(sizeof(G)) : 0), old_bytes[v]);
-      }
+    if constexpr (LAYOUT != kStrided) {
+      const uint32_t p8 = SORT ? static_cast<uint32_t>(row_of(i)) * ld8 : __shfl_sync(0xFFFFFFFFu, at8, i & 31);
+      if (i < n) sm.ring.dy[w][i % kAhead].copy(reinterpret_cast<const T*>(reinterpret_cast<const uint2*>(dy) + p8), left, lane);
+      if (begins) sm.ring.old[w][i % kAhead].copy(grad + static_cast<int64_t>(q) * cols, left, lane);
       cp_async_commit();
     } else {
       held = load8<T, LAYOUT>(dy + static_cast<int64_t>(row_of(i)) * a.ld, i < n ? left : 0, lane);
       if constexpr (ADD) held_old = load8<G, LAYOUT>(grad + static_cast<int64_t>(q) * cols, begins ? left : 0, lane);
     }
   };
-  constexpr int kLead = LAYOUT == kVec ? kAhead : 1;
+  constexpr int kLead = LAYOUT != kStrided ? kAhead : 1;
   for (int i = 0; i < kLead; ++i) copy(i);
   F2 acc[4], head[4];
   Raw8<G> old = {};
@@ -582,13 +565,11 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
       clear(acc);
     }
     F2 v[4];
-    if constexpr (LAYOUT == kVec) {
+    if constexpr (LAYOUT != kStrided) {
       cp_async_wait<kAhead - 1>();
-      Raw8<T> r;
-      gather8<T>(r, sm.ring.dy[w][i % kAhead], lane);
-      unpack8<T>(r, v);
+      unpack8<T>(sm.ring.dy[w][i % kAhead].take(lane), v);
       if constexpr (ADD)
-        if (fresh) gather8<G>(old, sm.ring.old[w][i % kAhead], lane);
+        if (fresh) old = sm.ring.old[w][i % kAhead].take(lane);
     } else {
       unpack8<T>(held, v);
       if constexpr (ADD)
@@ -601,7 +582,7 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
   if constexpr (!SORT) {
     // runs that cross warps
     const int64_t chunk_end = lo + static_cast<int64_t>(kEmbWarps - w) * a.part;
-    if constexpr (LAYOUT == kVec) cp_async_wait<0>();
+    if constexpr (LAYOUT != kStrided) cp_async_wait<0>();
     if (lane == 0) {
       ends[w] = found;
       tail_key[w] = cur;
@@ -697,12 +678,12 @@ __global__ void __launch_bounds__(kEmbThreads) table_join_kernel(const __grid_co
 
 template <typename T>
 int launch_lookup(const LookupArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
-  return launch_pdl(vec ? lookup_kernel<T, kVec> : lookup_kernel<T, kStrided>, dim3(grid), dim3(kEmbThreads), 0, stream, a);
+  return launch_pdl(vec ? lookup_kernel<T, kWide<T>> : lookup_kernel<T, kStrided>, dim3(grid), dim3(kEmbThreads), 0, stream, a);
 }
 template <typename T, typename G, int LAYOUT, bool SORT, bool ADD>
 int launch_sum_as(const TableGradArgs& a, unsigned grid, cudaStream_t stream) {
   auto kernel = table_sum_kernel<T, G, LAYOUT, SORT, ADD>;
-  constexpr size_t smem = sizeof(SumSmem<T, G, ADD>);
+  constexpr size_t smem = sizeof(SumSmem<T, G, LAYOUT, ADD>);
   static SmemAllowed allowed;
   if (int rc = allow_smem(kernel, smem, allowed)) return rc;
   return launch_pdl(kernel, dim3(grid), dim3(kEmbThreads), smem, stream, a);
@@ -715,11 +696,12 @@ int launch_sum_layout(const TableGradArgs& a, bool sort, unsigned grid, cudaStre
 }
 template <typename T, typename G>
 int launch_sum(const TableGradArgs& a, bool vec, bool sort, unsigned grid, cudaStream_t stream) {
-  return vec ? launch_sum_layout<T, G, kVec>(a, sort, grid, stream) : launch_sum_layout<T, G, kStrided>(a, sort, grid, stream);
+  constexpr int kBoth = sizeof(T) + sizeof(G) == 4 ? kVec8 : kVec4;
+  return vec ? launch_sum_layout<T, G, kBoth>(a, sort, grid, stream) : launch_sum_layout<T, G, kStrided>(a, sort, grid, stream);
 }
 template <typename G>
 int launch_join(const TableGradArgs& a, bool vec, unsigned grid, cudaStream_t stream) {
-  return launch_pdl(vec ? table_join_kernel<G, kVec> : table_join_kernel<G, kStrided>, dim3(grid), dim3(kEmbThreads), 0,
+  return launch_pdl(vec ? table_join_kernel<G, kVec4> : table_join_kernel<G, kStrided>, dim3(grid), dim3(kEmbThreads), 0,
                     stream, a);
 }
 
@@ -789,9 +771,11 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   set.read(grad_out, span_bytes(n, cols, ld, e));
   set.read(tokens, n * token_bytes);
   set.write(scratch, need);
-  // (rows of grad_out are addressed by 32 bits of 16-byte units)
-  bool vec = is_aligned(grad_out, 16) && ld * e % 16 == 0 && cols * ge % 16 == 0 && cols * e % 16 == 0 &&
-             span_bytes(n, cols, ld, e) < (int64_t(16) << 32);
+  // vectors: pieces of eight columns where both types are bf16, else of four, on their own
+  // boundaries (and rows of grad_out addressed by 32 bits of 8-byte units)
+  const int piece = e + ge == 4 ? 8 : 4;
+  bool vec = is_aligned(grad_out, piece * e) && ld % piece == 0 && cols % piece == 0 &&
+             span_bytes(n, cols, ld, e) < (int64_t(8) << 32);
   int64_t most = 0;
   for (int k = 0; k < K; ++k) most = std::max(most, worker_offsets[k + 1] - worker_offsets[k]);
   // (a key and an index share 32 bits where a CTA sorts by itself)
@@ -800,7 +784,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   for (int k = 0; k < K; ++k) {
     if (grads[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
     set.write(grads[k], num_rows * cols * ge);
-    vec = vec && is_aligned(grads[k], 16);
+    vec = vec && is_aligned(grads[k], piece * ge);
     const int64_t nk = worker_offsets[k + 1] - worker_offsets[k];
     s.fill[k] = a.grads[k] = grads[k];
     s.off[k + 1] = a.off[k + 1] = worker_offsets[k + 1];

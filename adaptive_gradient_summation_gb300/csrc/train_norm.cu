@@ -219,15 +219,17 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
   }
 }
 
-// Rows of dy and x (or of h's codes) on their way to the gradient kernel.  kVec: a lane
-// copies the bytes that it will use itself to shared memory, kStages rows ahead, so that the
-// copies take no registers and need no barrier.  kStrided: no row ahead.
-template <typename T, int NV, bool KEPT>
+// Rows of dy and x (or of h's codes) on their way to the gradient kernel, one warp's part.
+// A lane copies the bytes that it will use itself, kStages rows ahead, so that the copies take
+// no registers and need no barrier (N = 1: no row ahead).
+template <typename T, int N, int NV, bool KEPT>
 struct RowCopy {
-  static constexpr int kVecs = sizeof(T) / 2;  // 16-byte vectors of a lane's eight
-  uint4 dy[NV][kVecs][32];
-  uint4 x[KEPT ? 1 : NV][KEPT ? 1 : kVecs][KEPT ? 1 : 32];
-  uint2 q[KEPT ? NV : 1][KEPT ? 32 : 1];
+  LaneSlot<T, N> dy[NV], x[NV];
+};
+template <typename T, int N, int NV>
+struct RowCopy<T, N, NV, true> {
+  LaneSlot<T, N> dy[NV];
+  alignas(8) uint32_t q[NV][8 / N][32][N == kVec8 ? 2 : 1];  // codes
 };
 template <typename T, int W, int NV>
 struct GradShape {
@@ -246,7 +248,7 @@ template <typename T, int LAYOUT, int W, int NV, bool KEPT>
 __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kCtas)
     norm_grad_kernel(const NormGradArgs a, const __grid_constant__ WorkerRows rows) {
   using TM = Team<W, NV>;
-  using Copy = RowCopy<T, NV, KEPT>;
+  using Copy = RowCopy<T, LAYOUT, NV, KEPT>;
   constexpr int S = GradShape<T, W, NV>::kStages;
   constexpr bool kTwice = GradShape<T, W, NV>::kTwice;
   pdl_enter();
@@ -276,27 +278,22 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
     for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = f2(0.f);
   }
   auto issue = [&](int64_t row, int stage) {
-    if constexpr (LAYOUT == kVec) {
+    if constexpr (LAYOUT != kStrided) {
       if (row < r1) {
         Copy& c = copies[stage * TM::kWarps + warp];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           const int c0 = (j * W + w) * kSlice;
-          const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy + c0;
+          c.dy[j].copy(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left[j], lane);
+          if constexpr (!KEPT) {
+            c.x[j].copy(static_cast<const T*>(a.x) + row * a.ld_x + c0, left[j], lane);
+          } else {  // (rows of codes are padded, so a begun piece is always there)
 #pragma unroll
-          for (int v = 0; v < Copy::kVecs; ++v) {
-            const int at = lane * 8 + v * 16 / static_cast<int>(sizeof(T));
-            const int bytes = max(0, min(16, (left[j] - at) * static_cast<int>(sizeof(T))));
-            const int from = bytes > 0 ? at : 0;
-            cp_async16(smem_addr(&c.dy[j][v][lane]), dy + from, bytes);
-            if constexpr (!KEPT) {
-              const T* x = static_cast<const T*>(a.x) + row * a.ld_x + c0;
-              cp_async16(smem_addr(&c.x[j][v][lane]), x + from, bytes);
+            for (int i = 0; i < 8 / LAYOUT; ++i) {
+              const int at = lane_col<LAYOUT>(lane, i * LAYOUT);
+              const bool in = at < left[j];
+              cp_async_small<LAYOUT>(smem_addr(c.q[j][i][lane]), a.codes + row * pitch + c0 + (in ? at : 0), in ? LAYOUT : 0);
             }
-          }
-          if constexpr (KEPT) {  // (rows of codes are padded, so a begun eight is always there)
-            const bool in = lane * 8 < left[j];
-            cp_async8(smem_addr(&c.q[j][lane]), a.codes + row * pitch + c0 + (in ? lane * 8 : 0), in ? 8 : 0);
           }
         }
       }
@@ -306,16 +303,12 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
   // dy and h of slice j of the row
   auto take = [&](int64_t row, int stage, int j, float mean, float rstd, float s0, float s1, F2 (&dy)[4], F2 (&h)[4]) {
     const int c0 = (j * W + w) * kSlice;
-    if constexpr (LAYOUT == kVec) {
+    if constexpr (LAYOUT != kStrided) {
       const Copy& c = copies[stage * TM::kWarps + warp];
-      auto raw = [&](const uint4 (&v)[Copy::kVecs][32], F2 (&to)[4]) {
-        Raw8<T> r;
-        gather8<T>(r, v, lane);
-        unpack8<T>(r, to);
-      };
-      raw(c.dy[j], dy);
-      if constexpr (KEPT) ckpt_values8(c.q[j][lane], s0, s1, h);
-      else raw(c.x[j], h);
+      unpack8<T>(c.dy[j].take(lane), dy);
+      if constexpr (!KEPT) unpack8<T>(c.x[j].take(lane), h);
+      else if constexpr (LAYOUT == kVec8) ckpt_values8(*reinterpret_cast<const uint2*>(c.q[j][0][lane]), s0, s1, h);
+      else ckpt_values8(make_uint2(c.q[j][0][lane][0], c.q[j][1][lane][0]), s0, s1, h);
     } else {
       unpack8<T>(load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left[j], lane), dy);
       if constexpr (KEPT) ckpt_values8(load_codes8<LAYOUT>(a.codes + row * pitch + c0, left[j], lane), s0, s1, h);
@@ -342,7 +335,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
       for (int j = 0; j < NV; ++j) {
         const int n = in ? left[j] : 0;
         const float* s = a.scales + row * nscales + (j * W + w) * (kSlice / kCkptBlock);
-        if constexpr (LAYOUT == kVec) {
+        if constexpr (LAYOUT == kVec8) {
           next.scale[j][0] = next.scale[j][1] = lane * 8 < n ? s[lane >> 4] : 0.f;
         } else {
           next.scale[j][0] = n > 0 ? s[0] : 0.f;
@@ -356,7 +349,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
   for (int it = 0; row < r1; row += TM::kTeams, it ^= 1, stage = stage + 1 == S ? 0 : stage + 1) {
     const Stats cur = next;
     stats(row + TM::kTeams);
-    if constexpr (LAYOUT == kVec) cp_async_wait<S - 1>();
+    if constexpr (LAYOUT != kStrided) cp_async_wait<S - 1>();
     F2 g[kTwice ? 1 : NV][4], h[kTwice ? 1 : NV][4], sg2 = f2(0.f), sgh2 = f2(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -431,7 +424,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
       }
     }
   } else {
-    if constexpr (LAYOUT == kVec) cp_async_wait<0>();
+    if constexpr (LAYOUT != kStrided) cp_async_wait<0>();
     __syncthreads();
     float* mine = sm + team * 2 * TM::kCols;
 #pragma unroll
@@ -502,7 +495,7 @@ template <typename T, int LAYOUT, int W, int NV, bool KEPT>
 int launch_norm_grad_as(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
   using TM = Team<W, NV>;
   const size_t work = (KEPT ? 2 : 1) * TM::kCols * sizeof(float) +
-                      (LAYOUT == kVec ? GradShape<T, W, NV>::kStages * TM::kWarps * sizeof(RowCopy<T, NV, KEPT>) : 0);
+                      (LAYOUT != kStrided ? GradShape<T, W, NV>::kStages * TM::kWarps * sizeof(RowCopy<T, LAYOUT, NV, KEPT>) : 0);
   const size_t sums = TM::kTeams == 1 ? 0 : TM::kTeams * 2 * TM::kCols * sizeof(float);
   const size_t smem = std::max(work, sums);
   static SmemAllowed allowed;
@@ -614,8 +607,8 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
     if (adasum_status_t st = counted_launch(stream, kept ? "norm_grad_checkpoint" : "norm_grad",
                                             n * (kept ? 2 * e + 1 + (a.y ? e : 0) : 3 * e), [&] {
           if (dtype == kBF16)
-            return vec ? launch_norm_grad<bf16, kVec>(a, rows, stream) : launch_norm_grad<bf16, kStrided>(a, rows, stream);
-          return vec ? launch_norm_grad<float, kVec>(a, rows, stream) : launch_norm_grad<float, kStrided>(a, rows, stream);
+            return vec ? launch_norm_grad<bf16, kVec8>(a, rows, stream) : launch_norm_grad<bf16, kStrided>(a, rows, stream);
+          return vec ? launch_norm_grad<float, kVec4>(a, rows, stream) : launch_norm_grad<float, kStrided>(a, rows, stream);
         }))
       return st;
   if (!want) return ADASUM_OK;
@@ -661,8 +654,8 @@ adasum_status_t adasum_layer_norm(const void* x, int64_t rows, int64_t cols, int
   const bool vec = is_aligned(x, 16) && is_aligned(y, 16) && ld * e % 16 == 0 && cols * e % 16 == 0;
   const double n = static_cast<double>(rows) * cols;
   return counted_launch(stream, codes ? "norm_checkpoint" : "norm", n * (2 * e + (codes ? 1 : 0)), [&] {
-    if (dtype == ADASUM_BF16) return vec ? launch_norm<bf16, kVec>(a, stream) : launch_norm<bf16, kStrided>(a, stream);
-    return vec ? launch_norm<float, kVec>(a, stream) : launch_norm<float, kStrided>(a, stream);
+    if (dtype == ADASUM_BF16) return vec ? launch_norm<bf16, kVec8>(a, stream) : launch_norm<bf16, kStrided>(a, stream);
+    return vec ? launch_norm<float, kVec4>(a, stream) : launch_norm<float, kStrided>(a, stream);
   });
 }
 
