@@ -90,8 +90,8 @@ struct PackArgs {
   int8_t* codes;
   float* scales;
   void* y;  // the activation's output (kActNone: null)
-  int64_t pitch, nscales;   // of a row's codes and scales
-  uint32_t slices, items;   // slices of 256 columns in a row, in all
+  int64_t pitch, nscales;  // of a row's codes and scales
+  uint32_t groups;         // warps that share a row
 };
 struct UnpackArgs {
   const int8_t* codes;
@@ -102,71 +102,47 @@ struct UnpackArgs {
   void* out;       // the values (kActNone) or grad_x
   void* y;         // the activation again; null: not wanted
   int64_t pitch, nscales;
-  uint32_t slices, items;
+  uint32_t groups;
 };
 
-// A warp takes kItems slices of 256 columns, of one row or of several, and loads them all
-// before it works on the first.  Bound by bytes: each value is read and written once.
-//
-// Where a warp is, as offsets into the buffers, so that going on costs additions only.
-// DENSE: everything is one long row, and all offsets are the same.
-template <bool DENSE>
-struct Cursor {
-  int64_t c0, cols;
-  int64_t in, out, codes, scales;  // the strided input, a dense output, codes, scales
+// A warp takes kItems slices of 256 columns and loads them all before it works on the first:
+// ROW neighbouring ones of each of kItems / ROW rows, so that a slice's place is the warp's
+// plus a few constants.  Bound by bytes: each value is read and written once.
+template <int ROW>
+struct Place {
+  int64_t row, c0;
+  int rows, cols;  // that exist from here on, as far as the warp goes
   template <typename A>
-  __device__ __forceinline__ Cursor(const A& a, int64_t ld, uint32_t item) {
-    cols = a.cols;
-    if constexpr (DENSE) {
-      c0 = static_cast<int64_t>(item) * kSlice;
-    } else {
-      const int64_t row = item / a.slices;
-      c0 = static_cast<int64_t>(item - static_cast<uint32_t>(row) * a.slices) * kSlice;
-      in = row * ld + c0;
-      out = row * a.cols + c0;
-      codes = row * a.pitch + c0;
-      scales = row * a.nscales + c0 / kCkptBlock;
-    }
+  __device__ __forceinline__ Place(const A& a) {
+    const uint32_t warp = blockIdx.x * kCkptWarps + (threadIdx.x >> 5), block = warp / a.groups;
+    row = static_cast<int64_t>(block) * (kItems / ROW);
+    c0 = static_cast<int64_t>(warp - block * a.groups) * (ROW * kSlice);
+    rows = static_cast<int>(max(static_cast<int64_t>(0), min(a.rows - row, static_cast<int64_t>(kItems))));
+    cols = static_cast<int>(min(a.cols - c0, static_cast<int64_t>(ROW * kSlice)));
   }
-  template <typename A>
-  __device__ __forceinline__ void next(const A& a, int64_t ld) {
-    c0 += kSlice;
-    if constexpr (!DENSE) {
-      in += kSlice;
-      out += kSlice;
-      codes += kSlice;
-      scales += kSlice / kCkptBlock;
-      if (c0 >= cols) {
-        in += ld - c0;
-        out += cols - c0;
-        codes += a.pitch - c0;
-        scales += a.nscales - c0 / kCkptBlock;
-        c0 = 0;
-      }
-    }
+  // of slice i: its columns that exist, and its offset from the warp's place in a matrix
+  // whose rows are ld apart
+  __device__ __forceinline__ int left(int i) const {
+    return i / ROW < rows ? max(0, min(cols - i % ROW * kSlice, kSlice)) : 0;
   }
-  __device__ __forceinline__ int64_t at_in() const { return DENSE ? c0 : in; }
-  __device__ __forceinline__ int64_t at_out() const { return DENSE ? c0 : out; }
-  __device__ __forceinline__ int64_t at_codes() const { return DENSE ? c0 : codes; }
-  __device__ __forceinline__ int64_t at_scales() const { return DENSE ? c0 / kCkptBlock : scales; }
-  __device__ __forceinline__ int left() const { return static_cast<int>(min(cols - c0, static_cast<int64_t>(kSlice))); }
+  __device__ __forceinline__ static int64_t step(int i, int64_t ld) { return i / ROW * ld + i % ROW * kSlice; }
+  __device__ __forceinline__ static int64_t scale_step(int i, int64_t n) {
+    return i / ROW * n + i % ROW * (kSlice / kCkptBlock);
+  }
 };
 
-template <typename T, int ACT, int LAYOUT, bool DENSE>
+template <typename T, int ACT, int LAYOUT, int ROW>
 __global__ void __launch_bounds__(kCkptThreads, sizeof(T) == 2 ? 4 : 3) pack_kernel(const PackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
-  if (first >= a.items) return;
-  const int n = min(a.items - first, static_cast<uint32_t>(kItems));
-  const Cursor<DENSE> begin(a, a.ld, first);
+  const Place<ROW> at(a);
+  if (at.rows == 0) return;
   F2 v[kItems][4];
   {
+    const T* x = static_cast<const T*>(a.x) + at.row * a.ld + at.c0;
     Raw8<T> r[kItems];
-    Cursor<DENSE> s = begin;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i, s.next(a, a.ld))
-      r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + s.at_in(), i < n ? s.left() : 0, lane);
+    for (int i = 0; i < kItems; ++i) r[i] = load8<T, LAYOUT>(x + at.step(i, a.ld), at.left(i), lane);
 #pragma unroll
     for (int i = 0; i < kItems; ++i) unpack8<T>(r[i], v[i]);
   }
@@ -175,97 +151,115 @@ __global__ void __launch_bounds__(kCkptThreads, sizeof(T) == 2 ? 4 : 3) pack_ker
   for (int i = 0; i < kItems; ++i) block_tops<LAYOUT>(v[i], top[i]);
   CkptScale sc[kItems][2];
   block_scales<LAYOUT, kItems>(top, lane, sc);
-  Cursor<DENSE> s = begin;
+  int8_t* codes = a.codes + at.row * a.pitch + at.c0;
+  float* scales = a.scales + at.row * a.nscales + at.c0 / kCkptBlock;
+  T* y = static_cast<T*>(a.y) + at.row * a.cols + at.c0;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i, s.next(a, a.ld)) {
-    if (i >= n) break;
-    store_codes8<LAYOUT>(a.codes + s.at_codes(), s.left(), lane, ckpt_codes<LAYOUT>(v[i], sc[i]));
-    store_scales<LAYOUT>(a.scales + s.at_scales(), s.left(), lane, sc[i]);
+  for (int i = 0; i < kItems; ++i) {
+    const int left = at.left(i);
+    if (left <= 0) continue;
+    store_codes8<LAYOUT>(codes + at.step(i, a.pitch), left, lane, ckpt_codes<LAYOUT>(v[i], sc[i]));
+    store_scales<LAYOUT>(scales + at.scale_step(i, a.nscales), left, lane, sc[i]);
     if constexpr (ACT != kActNone) {
       F2 unused;
 #pragma unroll
       for (int e = 0; e < 4; ++e) gelu2<ACT, true, false>(v[i][e], v[i][e], unused);
-      store8<T, LAYOUT>(static_cast<T*>(a.y) + s.at_out(), s.left(), lane, v[i]);
+      store8<T, LAYOUT>(y + at.step(i, a.cols), left, lane, v[i]);
     }
   }
 }
 
-template <typename T, int ACT, bool AGAIN, int LAYOUT, bool DENSE>
-__global__ void __launch_bounds__(kCkptThreads) unpack_kernel(const UnpackArgs a) {
+template <typename T, int ACT, bool AGAIN, int LAYOUT, int ROW>
+__global__ void __launch_bounds__(kCkptThreads, 4) unpack_kernel(const UnpackArgs a) {
   pdl_enter();
   const int lane = threadIdx.x & 31;
-  const uint32_t first = (blockIdx.x * kCkptWarps + (threadIdx.x >> 5)) * kItems;
-  if (first >= a.items) return;
-  const int n = min(a.items - first, static_cast<uint32_t>(kItems));
-  const Cursor<DENSE> begin(a, a.ld_dy, first);
+  const Place<ROW> at(a);
+  if (at.rows == 0) return;
+  const int8_t* codes = a.codes + at.row * a.pitch + at.c0;
+  const float* scales = a.scales + at.row * a.nscales + at.c0 / kCkptBlock;
+  const T* dy = static_cast<const T*>(a.dy) + at.row * a.ld_dy + at.c0;
   uint2 q[kItems];
   Raw8<T> r[kItems];
-  Cursor<DENSE> s = begin;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i, s.next(a, a.ld_dy)) {
-    const int left = i < n ? s.left() : 0;
-    q[i] = load_codes8<LAYOUT>(a.codes + s.at_codes(), left, lane);
-    if constexpr (ACT != kActNone) r[i] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + s.at_in(), left, lane);
+  for (int i = 0; i < kItems; ++i) {
+    q[i] = load_codes8<LAYOUT>(codes + at.step(i, a.pitch), at.left(i), lane);
+    if constexpr (ACT != kActNone) r[i] = load8<T, LAYOUT>(dy + at.step(i, a.ld_dy), at.left(i), lane);
   }
-  s = begin;
+  T* out = static_cast<T*>(a.out) + at.row * a.cols + at.c0;
+  T* again = static_cast<T*>(a.y) + at.row * a.cols + at.c0;
 #pragma unroll
-  for (int i = 0; i < kItems; ++i, s.next(a, a.ld_dy)) {
-    if (i >= n) break;
-    const int left = s.left();
+  for (int i = 0; i < kItems; ++i) {
+    const int left = at.left(i);
+    if (left <= 0) continue;
     F2 v[4];
-    ckpt_values<LAYOUT>(q[i], a.scales + s.at_scales(), left, lane, v);
+    ckpt_values<LAYOUT>(q[i], scales + at.scale_step(i, a.nscales), left, lane, v);
     if constexpr (ACT != kActNone) {
-      F2 dy[4], y[4];
-      unpack8<T>(r[i], dy);
+      F2 d[4], y[4];
+      unpack8<T>(r[i], d);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         F2 slope;
         gelu2<ACT, AGAIN, true>(v[e], y[e], slope);
-        v[e] = mul2(slope, dy[e]);
+        v[e] = mul2(slope, d[e]);
       }
-      if constexpr (AGAIN) store8<T, LAYOUT>(static_cast<T*>(a.y) + s.at_out(), left, lane, y);
+      if constexpr (AGAIN) store8<T, LAYOUT>(again + at.step(i, a.cols), left, lane, y);
     }
-    store8<T, LAYOUT>(static_cast<T*>(a.out) + s.at_out(), left, lane, v);
+    store8<T, LAYOUT>(out + at.step(i, a.cols), left, lane, v);
   }
 }
 
+// Slices of a warp that lie in one row.
 template <typename A>
-dim3 ckpt_grid(const A& a) {
-  return dim3((a.items + kCkptWarps * kItems - 1) / (kCkptWarps * kItems));
+int slices_per_row(const A& a) {
+  return a.cols <= kSlice ? 1 : a.cols <= 2 * kSlice ? 2 : 4;
 }
 
-template <typename T, int LAYOUT, bool DENSE>
-int launch_pack(const PackArgs& a, int act, cudaStream_t stream) {
-  auto k = act == kActNone  ? pack_kernel<T, kActNone, LAYOUT, DENSE>
-           : act == kActErf ? pack_kernel<T, kActErf, LAYOUT, DENSE>
-                            : pack_kernel<T, kActTanh, LAYOUT, DENSE>;
-  return launch_pdl(k, ckpt_grid(a), dim3(kCkptThreads), 0, stream, a);
+template <typename T, int LAYOUT, int ROW>
+int launch_pack_as(const PackArgs& a, int act, unsigned grid, cudaStream_t stream) {
+  auto k = act == kActNone  ? pack_kernel<T, kActNone, LAYOUT, ROW>
+           : act == kActErf ? pack_kernel<T, kActErf, LAYOUT, ROW>
+                            : pack_kernel<T, kActTanh, LAYOUT, ROW>;
+  return launch_pdl(k, dim3(grid), dim3(kCkptThreads), 0, stream, a);
 }
-template <typename T, int LAYOUT, bool DENSE>
-int launch_unpack(const UnpackArgs& a, int act, cudaStream_t stream) {
+template <typename T, int LAYOUT>
+int launch_pack(const PackArgs& a, int act, unsigned grid, cudaStream_t stream) {
+  const int row = slices_per_row(a);
+  if (row == 1) return launch_pack_as<T, LAYOUT, 1>(a, act, grid, stream);
+  if (row == 2) return launch_pack_as<T, LAYOUT, 2>(a, act, grid, stream);
+  return launch_pack_as<T, LAYOUT, 4>(a, act, grid, stream);
+}
+template <typename T, int LAYOUT, int ROW>
+int launch_unpack_as(const UnpackArgs& a, int act, unsigned grid, cudaStream_t stream) {
   const bool y = a.y != nullptr;
-  auto k = act == kActNone ? unpack_kernel<T, kActNone, false, LAYOUT, DENSE>
-           : act == kActErf
-               ? (y ? unpack_kernel<T, kActErf, true, LAYOUT, DENSE> : unpack_kernel<T, kActErf, false, LAYOUT, DENSE>)
-               : (y ? unpack_kernel<T, kActTanh, true, LAYOUT, DENSE> : unpack_kernel<T, kActTanh, false, LAYOUT, DENSE>);
-  return launch_pdl(k, ckpt_grid(a), dim3(kCkptThreads), 0, stream, a);
+  auto k = act == kActNone  ? unpack_kernel<T, kActNone, false, LAYOUT, ROW>
+           : act == kActErf ? (y ? unpack_kernel<T, kActErf, true, LAYOUT, ROW> : unpack_kernel<T, kActErf, false, LAYOUT, ROW>)
+                            : (y ? unpack_kernel<T, kActTanh, true, LAYOUT, ROW> : unpack_kernel<T, kActTanh, false, LAYOUT, ROW>);
+  return launch_pdl(k, dim3(grid), dim3(kCkptThreads), 0, stream, a);
+}
+template <typename T, int LAYOUT>
+int launch_unpack(const UnpackArgs& a, int act, unsigned grid, cudaStream_t stream) {
+  const int row = slices_per_row(a);
+  if (row == 1) return launch_unpack_as<T, LAYOUT, 1>(a, act, grid, stream);
+  if (row == 2) return launch_unpack_as<T, LAYOUT, 2>(a, act, grid, stream);
+  return launch_unpack_as<T, LAYOUT, 4>(a, act, grid, stream);
 }
 
-// Slices of a call.  Dense rows of whole blocks follow each other without a gap in every
-// buffer, so they are taken as one long row.
+// Deals a call's slices to warps; the grid, or 0 when there are too many.  Dense rows of whole
+// blocks follow each other without a gap in every buffer, so they are taken as one long row.
 template <typename A>
-bool cut(A& a, int64_t ld) {
+unsigned deal(A& a, int64_t ld) {
   if (a.cols % kCkptBlock == 0 && (ld == a.cols || a.rows == 1)) {
     a.cols *= a.rows;
     a.rows = 1;
   }
   a.pitch = ckpt_pitch(a.cols);
   a.nscales = ckpt_scales(a.cols);
-  const int64_t slices = (a.cols + kSlice - 1) / kSlice;
-  if (slices > UINT32_MAX / 2 / a.rows) return false;
-  a.slices = static_cast<uint32_t>(slices);
-  a.items = static_cast<uint32_t>(slices * a.rows);
-  return true;
+  const int row = slices_per_row(a);
+  const int64_t groups = (a.cols + row * kSlice - 1) / (row * kSlice);
+  const int64_t blocks = (a.rows + kItems / row - 1) / (kItems / row);
+  if (groups > INT32_MAX / blocks) return 0;
+  a.groups = static_cast<uint32_t>(groups);
+  return static_cast<unsigned>((groups * blocks + kCkptWarps - 1) / kCkptWarps);
 }
 
 adasum_status_t check_shape(int64_t rows, int64_t cols, int dtype) {
@@ -289,14 +283,12 @@ adasum_status_t pack(PackArgs a, int dtype, int act, cudaStream_t stream) {
   if (set.conflict()) return ADASUM_ERR_ALIAS;
   const double n = static_cast<double>(a.rows) * a.cols;
   const bool vec = is_aligned(a.x, 16) && is_aligned(a.y, 16) && a.ld * e % 16 == 0 && (act == kActNone || a.cols * e % 16 == 0);
-  if (!cut(a, a.ld)) return ADASUM_ERR_UNSUPPORTED;
+  const unsigned grid = deal(a, a.ld);
+  if (grid == 0) return ADASUM_ERR_UNSUPPORTED;
   return counted_launch(stream, act ? "gelu_checkpoint" : "checkpoint_pack", n * (e + 1 + (act ? e : 0)), [&] {
-    const bool dense = a.rows == 1;
     if (dtype == kBF16)
-      return !vec ? launch_pack<bf16, kStrided, false>(a, act, stream)
-                  : dense ? launch_pack<bf16, kVec8, true>(a, act, stream) : launch_pack<bf16, kVec8, false>(a, act, stream);
-    return !vec ? launch_pack<float, kStrided, false>(a, act, stream)
-                : dense ? launch_pack<float, kVec4, true>(a, act, stream) : launch_pack<float, kVec4, false>(a, act, stream);
+      return vec ? launch_pack<bf16, kVec8>(a, act, grid, stream) : launch_pack<bf16, kStrided>(a, act, grid, stream);
+    return vec ? launch_pack<float, kVec4>(a, act, grid, stream) : launch_pack<float, kStrided>(a, act, grid, stream);
   });
 }
 
@@ -317,15 +309,13 @@ adasum_status_t unpack(UnpackArgs a, int dtype, int act, cudaStream_t stream) {
   const double n = static_cast<double>(a.rows) * a.cols;
   const bool vec = is_aligned(a.out, 16) && is_aligned(a.y, 16) && a.cols * e % 16 == 0 &&
                    (act == kActNone || (is_aligned(a.dy, 16) && a.ld_dy * e % 16 == 0));
-  if (!cut(a, act == kActNone ? a.cols : a.ld_dy)) return ADASUM_ERR_UNSUPPORTED;
+  const unsigned grid = deal(a, act == kActNone ? a.cols : a.ld_dy);
+  if (grid == 0) return ADASUM_ERR_UNSUPPORTED;
   return counted_launch(stream, act ? "gelu_grad_checkpoint" : "checkpoint_unpack",
                         n * (1 + e + (act ? e : 0) + (a.y ? e : 0)), [&] {
-    const bool dense = a.rows == 1;
     if (dtype == kBF16)
-      return !vec ? launch_unpack<bf16, kStrided, false>(a, act, stream)
-                  : dense ? launch_unpack<bf16, kVec8, true>(a, act, stream) : launch_unpack<bf16, kVec8, false>(a, act, stream);
-    return !vec ? launch_unpack<float, kStrided, false>(a, act, stream)
-                : dense ? launch_unpack<float, kVec4, true>(a, act, stream) : launch_unpack<float, kVec4, false>(a, act, stream);
+      return vec ? launch_unpack<bf16, kVec8>(a, act, grid, stream) : launch_unpack<bf16, kStrided>(a, act, grid, stream);
+    return vec ? launch_unpack<float, kVec4>(a, act, grid, stream) : launch_unpack<float, kStrided>(a, act, grid, stream);
   });
 }
 
@@ -339,14 +329,14 @@ extern "C" {
 adasum_status_t adasum_checkpoint_pack(const void* x, int64_t rows, int64_t cols, int64_t ld, adasum_dtype_t dtype,
                                        int8_t* codes, float* scales, adasum_stream_t stream) {
   EntryScope scope("adasum_checkpoint_pack");
-  return pack(PackArgs{x, rows, cols, ld, codes, scales, nullptr, 0, 0, 0, 0}, dtype, kActNone,
+  return pack(PackArgs{x, rows, cols, ld, codes, scales, nullptr, 0, 0, 0}, dtype, kActNone,
               reinterpret_cast<cudaStream_t>(stream));
 }
 
 adasum_status_t adasum_checkpoint_unpack(const int8_t* codes, const float* scales, int64_t rows, int64_t cols,
                                          adasum_dtype_t dtype, void* out, adasum_stream_t stream) {
   EntryScope scope("adasum_checkpoint_unpack");
-  return unpack(UnpackArgs{codes, scales, rows, cols, nullptr, 0, out, nullptr, 0, 0, 0, 0}, dtype, kActNone,
+  return unpack(UnpackArgs{codes, scales, rows, cols, nullptr, 0, out, nullptr, 0, 0, 0}, dtype, kActNone,
                 reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -354,7 +344,7 @@ adasum_status_t adasum_gelu_checkpointed(const void* x, int64_t rows, int64_t co
                                          int tanh_form, void* y, int8_t* codes, float* scales,
                                          adasum_stream_t stream) {
   EntryScope scope("adasum_gelu_checkpointed");
-  return pack(PackArgs{x, rows, cols, ld, codes, scales, y, 0, 0, 0, 0}, dtype, tanh_form ? kActTanh : kActErf,
+  return pack(PackArgs{x, rows, cols, ld, codes, scales, y, 0, 0, 0}, dtype, tanh_form ? kActTanh : kActErf,
               reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -363,7 +353,7 @@ adasum_status_t adasum_gelu_checkpointed_backward(const void* grad_out, int64_t 
                                                   adasum_dtype_t dtype, int tanh_form, void* grad_x, void* y,
                                                   adasum_stream_t stream) {
   EntryScope scope("adasum_gelu_checkpointed_backward");
-  return unpack(UnpackArgs{codes, scales, rows, cols, grad_out, ld_grad, grad_x, y, 0, 0, 0, 0}, dtype,
+  return unpack(UnpackArgs{codes, scales, rows, cols, grad_out, ld_grad, grad_x, y, 0, 0, 0}, dtype,
                 tanh_form ? kActTanh : kActErf, reinterpret_cast<cudaStream_t>(stream));
 }
 
