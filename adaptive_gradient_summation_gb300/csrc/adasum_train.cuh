@@ -109,23 +109,25 @@ __device__ __forceinline__ int lane_col(int lane, int e) {
   return (e / N * 32 + lane) * N + e % N;
 }
 
-// Raw bits of a lane's eight values.
-template <typename T>
+// Raw bits of a lane's eight values; with N = 1 a word each, so that bf16 loads need not have
+// arrived to be held (packing them on arrival made a prefetch of the next row wait for them).
+template <typename T, int N>
 struct Raw8 {
-  uint32_t w[sizeof(T) * 2];
+  uint32_t w[N == kStrided ? 8 : sizeof(T) * 2];
 };
 
-template <typename T>
-__device__ __forceinline__ float raw_value(const Raw8<T>& r, int e) {
-  if constexpr (sizeof(T) == 2) return __uint_as_float(e & 1 ? r.w[e >> 1] & 0xFFFF0000u : r.w[e >> 1] << 16);
-  else return __uint_as_float(r.w[e]);
+template <typename T, int N>
+__device__ __forceinline__ float raw_value(const Raw8<T, N>& r, int e) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(r.w[e]);
+  else if constexpr (N == kStrided) return __uint_as_float(r.w[e] << 16);
+  else return __uint_as_float(e & 1 ? r.w[e >> 1] & 0xFFFF0000u : r.w[e >> 1] << 16);
 }
 
 // The eight values as pairs.
-template <typename T>
-__device__ __forceinline__ void unpack8(const Raw8<T>& r, F2 (&v)[4]) {
+template <typename T, int N>
+__device__ __forceinline__ void unpack8(const Raw8<T, N>& r, F2 (&v)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = f2(raw_value<T>(r, 2 * i), raw_value<T>(r, 2 * i + 1));
+  for (int i = 0; i < 4; ++i) v[i] = f2(raw_value<T, N>(r, 2 * i), raw_value<T, N>(r, 2 * i + 1));
 }
 
 // Columns of a slice that starts at c0, at most 256, none past the row's end.
@@ -136,26 +138,20 @@ __device__ __forceinline__ int slice_left(int64_t cols, int64_t c0) {
 // Loads the values of 256 columns starting at p, of which `left` exist (others are 0).
 // KEEP: the data will be read again (default: streaming).
 template <typename T, int N, bool KEEP = false>
-__device__ __forceinline__ Raw8<T> load8(const T* p, int left, int lane) {
+__device__ __forceinline__ Raw8<T, N> load8(const T* p, int left, int lane) {
   constexpr int kWords = N * static_cast<int>(sizeof(T)) / 4;  // of a piece
-  Raw8<T> r;
+  Raw8<T, N> r;
   auto element = [&](int c) -> uint32_t {
     if constexpr (sizeof(T) == 2) return reinterpret_cast<const uint16_t*>(p)[c];
     else return reinterpret_cast<const uint32_t*>(p)[c];
   };
   if constexpr (N == kStrided) {
-    uint32_t v[8];
     if (left >= 256) {  // (uniform over the warp: no check per element)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = element(lane_col<N>(lane, e));
+      for (int e = 0; e < 8; ++e) r.w[e] = element(lane_col<N>(lane, e));
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = lane_col<N>(lane, e) < left ? element(lane_col<N>(lane, e)) : 0u;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (sizeof(T) == 4) r.w[e] = v[e];
-      else if (e & 1) r.w[e >> 1] = __byte_perm(v[e - 1], v[e], 0x5410);
+      for (int e = 0; e < 8; ++e) r.w[e] = lane_col<N>(lane, e) < left ? element(lane_col<N>(lane, e)) : 0u;
     }
   } else {
 #pragma unroll
@@ -205,8 +201,8 @@ struct alignas(16) LaneSlot {
       else cp_async_small<kBytes>(smem_addr(w[i][lane]), from, bytes);
     }
   }
-  __device__ __forceinline__ Raw8<T> take(int lane) const {
-    Raw8<T> r;
+  __device__ __forceinline__ Raw8<T, N> take(int lane) const {
+    Raw8<T, N> r;
 #pragma unroll
     for (int i = 0; i < 8 / N; ++i) {
       if constexpr (kWords == 4) {

@@ -140,11 +140,11 @@ __global__ void __launch_bounds__(kCkptThreads, sizeof(T) == 2 ? 4 : 3) pack_ker
   F2 v[kItems][4];
   {
     const T* x = static_cast<const T*>(a.x) + at.row * a.ld + at.c0;
-    Raw8<T> r[kItems];
+    Raw8<T, LAYOUT> r[kItems];
 #pragma unroll
     for (int i = 0; i < kItems; ++i) r[i] = load8<T, LAYOUT>(x + at.step(i, a.ld), at.left(i), lane);
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) unpack8<T>(r[i], v[i]);
+    for (int i = 0; i < kItems; ++i) unpack8<T, LAYOUT>(r[i], v[i]);
   }
   float top[kItems][2];
 #pragma unroll
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kCkptThreads, 4) unpack_kernel(const UnpackArg
   const float* scales = a.scales + at.row * a.nscales + at.c0 / kCkptBlock;
   const T* dy = static_cast<const T*>(a.dy) + at.row * a.ld_dy + at.c0;
   uint2 q[kItems];
-  Raw8<T> r[kItems];
+  Raw8<T, LAYOUT> r[kItems];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
     q[i] = load_codes8<LAYOUT>(codes + at.step(i, a.pitch), at.left(i), lane);
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kCkptThreads, 4) unpack_kernel(const UnpackArg
     ckpt_values<LAYOUT>(q[i], scales + at.scale_step(i, a.nscales), left, lane, v);
     if constexpr (ACT != kActNone) {
       F2 d[4], y[4];
-      unpack8<T>(r[i], d);
+      unpack8<T, LAYOUT>(r[i], d);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         F2 slope;

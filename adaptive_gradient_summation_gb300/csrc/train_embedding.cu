@@ -50,14 +50,14 @@ __global__ void __launch_bounds__(kEmbThreads) lookup_kernel(const LookupArgs a)
   const T* src = static_cast<const T*>(a.table) + (there ? t : 0) * a.cols + c0;
   T* dst = static_cast<T*>(a.out) + static_cast<int64_t>(i) * a.cols + c0;
   const int64_t left = a.cols - c0;
-  Raw8<T> r[kLookupVecs];
+  Raw8<T, LAYOUT> r[kLookupVecs];
 #pragma unroll
   for (int j = 0; j < kLookupVecs; ++j) r[j] = load8<T, LAYOUT, true>(src + j * kSlice, there ? slice_left(left, j * kSlice) : 0, lane);
 #pragma unroll
   for (int j = 0; j < kLookupVecs; ++j) {
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = there ? a.scale * raw_value<T>(r[j], e) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = there ? a.scale * raw_value<T, LAYOUT>(r[j], e) : 0.f;
     store8<T, LAYOUT>(dst + j * kSlice, slice_left(left, j * kSlice), lane, v);
   }
 }
@@ -388,13 +388,13 @@ __global__ void __launch_bounds__(kTileThreads) table_scatter_kernel(const __gri
 
 // Writes scale * acc to 256 columns of a gradient's row; ADD: added to `old`, its values.
 template <typename G, int LAYOUT, bool ADD>
-__device__ __forceinline__ void put_row(G* out, float scale, int left, int lane, const F2 (&acc)[4], const Raw8<G>& old) {
+__device__ __forceinline__ void put_row(G* out, float scale, int left, int lane, const F2 (&acc)[4], const Raw8<G, LAYOUT>& old) {
   F2 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = mul2(acc[i], f2(scale));
   if constexpr (ADD) {
     F2 o[4];
-    unpack8<G>(old, o);
+    unpack8<G, LAYOUT>(old, o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // (scalar sums: a packed product and sum would be contracted)
@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
   // where a row lies, in units of 8 bytes from dy (the host keeps them within 32 bits; N > 1)
   const uint32_t ld8 = static_cast<uint32_t>(a.ld * static_cast<int>(sizeof(T)) / 8);
   const uint32_t at8 = static_cast<uint32_t>(at) * ld8;
-  Raw8<T> held;
-  Raw8<G> held_old;
+  Raw8<T, LAYOUT> held;
+  Raw8<G, LAYOUT> held_old;
   int copied = -1;  // key of the last row whose copy was begun (rows below n only)
   if (!SORT && n > 0 && before == __shfl_sync(0xFFFFFFFFu, key, 0)) copied = before;  // (that run's row is not added to here)
   auto copy = [&](int i) {  // row i of the part, and the gradient row of a run that begins there
@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
   constexpr int kLead = LAYOUT != kStrided ? kAhead : 1;
   for (int i = 0; i < kLead; ++i) copy(i);
   F2 acc[4], head[4];
-  Raw8<G> old = {};
+  Raw8<G, LAYOUT> old = {};
   auto clear = [&](F2 (&v)[4]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = f2(0.f);
@@ -567,11 +567,11 @@ __global__ void __launch_bounds__(kEmbThreads) table_sum_kernel(const __grid_con
     F2 v[4];
     if constexpr (LAYOUT != kStrided) {
       cp_async_wait<kAhead - 1>();
-      unpack8<T>(sm.ring.dy[w][i % kAhead].take(lane), v);
+      unpack8<T, LAYOUT>(sm.ring.dy[w][i % kAhead].take(lane), v);
       if constexpr (ADD)
         if (fresh) old = sm.ring.old[w][i % kAhead].take(lane);
     } else {
-      unpack8<T>(held, v);
+      unpack8<T, LAYOUT>(held, v);
       if constexpr (ADD)
         if (fresh) old = held_old;
     }
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kEmbThreads) table_join_kernel(const __grid_co
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = f2(0.f);
     for (int64_t i0 = p0; i0 < p1; i0 += B) {
-      Raw8<float> r[B];
+      Raw8<float, LAYOUT> r[B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         const int64_t i = i0 + b;
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kEmbThreads) table_join_kernel(const __grid_co
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         F2 v[4];
-        unpack8<float>(r[b], v);
+        unpack8<float, LAYOUT>(r[b], v);
         add8(acc, v);
       }
     }
@@ -670,7 +670,7 @@ __global__ void __launch_bounds__(kEmbThreads) table_join_kernel(const __grid_co
       }
       G* out = static_cast<G*>(a.grads[k]) + key * a.cols + c0;
       if (a.accumulate) put_row<G, LAYOUT, true>(out, a.scale, left, lane, acc, load8<G, LAYOUT>(out, left, lane));
-      else put_row<G, LAYOUT, false>(out, a.scale, left, lane, acc, Raw8<G>{});
+      else put_row<G, LAYOUT, false>(out, a.scale, left, lane, acc, Raw8<G, LAYOUT>{});
     }
     __syncthreads();
   }

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
 #pragma unroll
   for (int j = 0; j < NV; ++j) count += left[j] = slice_left(a.cols, (j * W + w) * kSlice);
   const float inv_count = count > 0 ? 1.f / static_cast<float>(count) : 0.f;
-  Raw8<T> next[NV];
+  Raw8<T, LAYOUT> next[NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
   for (int it = 0; row < a.rows; row += step, it ^= 1) {
     F2 v[NV][4], acc = f2(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) unpack8<T>(next[j], v[j]);
+    for (int j = 0; j < NV; ++j) unpack8<T, LAYOUT>(next[j], v[j]);
     fetch(row + step);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
@@ -305,14 +305,14 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
     const int c0 = (j * W + w) * kSlice;
     if constexpr (LAYOUT != kStrided) {
       const Copy& c = copies[stage * TM::kWarps + warp];
-      unpack8<T>(c.dy[j].take(lane), dy);
-      if constexpr (!KEPT) unpack8<T>(c.x[j].take(lane), h);
+      unpack8<T, LAYOUT>(c.dy[j].take(lane), dy);
+      if constexpr (!KEPT) unpack8<T, LAYOUT>(c.x[j].take(lane), h);
       else if constexpr (LAYOUT == kVec8) ckpt_values8(*reinterpret_cast<const uint2*>(c.q[j][0][lane]), s0, s1, h);
       else ckpt_values8(make_uint2(c.q[j][0][lane][0], c.q[j][1][lane][0]), s0, s1, h);
     } else {
-      unpack8<T>(load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left[j], lane), dy);
+      unpack8<T, LAYOUT>(load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left[j], lane), dy);
       if constexpr (KEPT) ckpt_values8(load_codes8<LAYOUT>(a.codes + row * pitch + c0, left[j], lane), s0, s1, h);
-      else unpack8<T>(load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld_x + c0, left[j], lane), h);
+      else unpack8<T, LAYOUT>(load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld_x + c0, left[j], lane), h);
     }
     if constexpr (!KEPT) {
 #pragma unroll
