@@ -300,9 +300,18 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
       cp_async_commit();
     }
   };
-  // dy and h of slice j of the row
-  auto take = [&](int64_t row, int stage, int j, float mean, float rstd, float s0, float s1, F2 (&dy)[4], F2 (&h)[4]) {
+  // dy and h of slice j of the row; N = 1: from `raw`, loaded by `load_raw`
+  struct Raw {
+    Raw8<T, LAYOUT> dy[LAYOUT != kStrided ? 1 : NV], x[LAYOUT != kStrided || KEPT ? 1 : NV];
+    uint2 q[LAYOUT == kStrided && KEPT ? NV : 1];
+  } raw;
+  auto load_raw = [&](int64_t row, int j) {
     const int c0 = (j * W + w) * kSlice;
+    raw.dy[j] = load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left[j], lane);
+    if constexpr (KEPT) raw.q[j] = load_codes8<LAYOUT>(a.codes + row * pitch + c0, left[j], lane);
+    else raw.x[j] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld_x + c0, left[j], lane);
+  };
+  auto take = [&](int stage, int j, float mean, float rstd, float s0, float s1, F2 (&dy)[4], F2 (&h)[4]) {
     if constexpr (LAYOUT != kStrided) {
       const Copy& c = copies[stage * TM::kWarps + warp];
       unpack8<T, LAYOUT>(c.dy[j].take(lane), dy);
@@ -310,9 +319,9 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
       else if constexpr (LAYOUT == kVec8) ckpt_values8(*reinterpret_cast<const uint2*>(c.q[j][0][lane]), s0, s1, h);
       else ckpt_values8(make_uint2(c.q[j][0][lane][0], c.q[j][1][lane][0]), s0, s1, h);
     } else {
-      unpack8<T, LAYOUT>(load8<T, LAYOUT>(static_cast<const T*>(a.dy) + row * a.ld_dy + c0, left[j], lane), dy);
-      if constexpr (KEPT) ckpt_values8(load_codes8<LAYOUT>(a.codes + row * pitch + c0, left[j], lane), s0, s1, h);
-      else unpack8<T, LAYOUT>(load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld_x + c0, left[j], lane), h);
+      unpack8<T, LAYOUT>(raw.dy[j], dy);
+      if constexpr (KEPT) ckpt_values8(raw.q[j], s0, s1, h);
+      else unpack8<T, LAYOUT>(raw.x[j], h);
     }
     if constexpr (!KEPT) {
 #pragma unroll
@@ -349,12 +358,17 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
   for (int it = 0; row < r1; row += TM::kTeams, it ^= 1, stage = stage + 1 == S ? 0 : stage + 1) {
     const Stats cur = next;
     stats(row + TM::kTeams);
-    if constexpr (LAYOUT != kStrided) cp_async_wait<S - 1>();
+    if constexpr (LAYOUT != kStrided) {
+      cp_async_wait<S - 1>();
+    } else {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) load_raw(row, j);
+    }
     F2 g[kTwice ? 1 : NV][4], h[kTwice ? 1 : NV][4], sg2 = f2(0.f), sgh2 = f2(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int at = kTwice ? 0 : j;
-      take(row, stage, j, cur.mean, cur.rstd, cur.scale[KEPT ? j : 0][0], cur.scale[KEPT ? j : 0][1], g[at], h[at]);
+      take(stage, j, cur.mean, cur.rstd, cur.scale[KEPT ? j : 0][0], cur.scale[KEPT ? j : 0][1], g[at], h[at]);
       F2 wv[4];
       lds8(ws + (j * W + w) * kSlice, lane, wv);
 #pragma unroll
@@ -386,7 +400,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
       F2 wv[4];
       if (kTwice || (KEPT && a.y != nullptr)) lds8(ws + c0, lane, wv);
       if constexpr (kTwice) {
-        take(row, stage, j, cur.mean, cur.rstd, cur.scale[KEPT ? j : 0][0], cur.scale[KEPT ? j : 0][1], g[0], h[0]);
+        take(stage, j, cur.mean, cur.rstd, cur.scale[KEPT ? j : 0][0], cur.scale[KEPT ? j : 0][1], g[0], h[0]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) g[0][i] = mul2(g[0][i], wv[i]);
       }
