@@ -6,6 +6,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -42,7 +43,8 @@ inline bool valid_dtype(int dt) { return dt == kF32 || dt == kBF16; }
 inline int64_t dtype_bytes(int dt) { return dt == kBF16 ? 2 : 4; }
 inline bool is_aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
-// Buffers of one call.  `conflict` tells whether a written one overlaps any other.
+// Buffers of one call, each with the size of its elements.  `bad`: one does not start on an
+// element's boundary; `conflict`: a written one overlaps another.
 struct BufferSet {
   static constexpr int kMost = 2 * kMaxK + 16;
   struct Range {
@@ -50,12 +52,14 @@ struct BufferSet {
     bool written;
   } r[kMost];
   int n = 0;
+  bool bad = false;
 
-  void read(const void* p, int64_t bytes) { add(p, bytes, false); }
-  void write(const void* p, int64_t bytes) { add(p, bytes, true); }
-  void add(const void* p, int64_t bytes, bool written) {
+  void read(const void* p, int64_t bytes, int64_t elem) { add(p, bytes, elem, false); }
+  void write(const void* p, int64_t bytes, int64_t elem) { add(p, bytes, elem, true); }
+  void add(const void* p, int64_t bytes, int64_t elem, bool written) {
     if (p == nullptr || bytes <= 0) return;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    bad = bad || (lo & static_cast<uintptr_t>(elem - 1)) != 0;
     r[n++] = Range{lo, lo + static_cast<uintptr_t>(bytes), written};
   }
   bool conflict() {
@@ -68,9 +72,13 @@ struct BufferSet {
     }
     return false;
   }
+  adasum_status_t check() { return bad ? ADASUM_ERR_INVALID_ARG : conflict() ? ADASUM_ERR_ALIAS : ADASUM_OK; }
 };
 
-// Bytes a strided input of `rows` rows spans.
+// Whether rows `ld` apart can be addressed, and the bytes a strided input of them spans.
+inline bool valid_ld(int64_t rows, int64_t cols, int64_t ld) {
+  return ld >= cols && (rows <= 1 || ld <= INT64_MAX / 16 / rows);
+}
 inline int64_t span_bytes(int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
   return rows > 0 ? ((rows - 1) * ld + cols) * elem : 0;
 }
@@ -87,16 +95,16 @@ inline adasum_status_t check_worker_offsets(const int64_t* offs, int K) {
 
 // SMs of the current device (asked once per device).
 inline int sm_count() {
-  static int known[64] = {};
+  static std::atomic<int> known[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 152;
   if (dev < 0 || dev >= 64) dev = 0;
-  if (known[dev] == 0) {
-    int n = 0;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    known[dev] = n;
+    known[dev].store(n, std::memory_order_relaxed);
   }
-  return known[dev];
+  return n;
 }
 
 // Allows a kernel `bytes` of dynamic shared memory where that is (with its static part) more

@@ -272,15 +272,15 @@ adasum_status_t pack(PackArgs a, int dtype, int act, cudaStream_t stream) {
   if (adasum_status_t st = check_shape(a.rows, a.cols, dtype)) return st;
   if (a.rows == 0) return ADASUM_OK;
   if (a.x == nullptr || a.codes == nullptr || a.scales == nullptr || (act != kActNone && a.y == nullptr) ||
-      a.ld < a.cols || !is_aligned(a.codes, 16))
+      !valid_ld(a.rows, a.cols, a.ld) || !is_aligned(a.codes, 16))
     return ADASUM_ERR_INVALID_ARG;
   const int64_t e = dtype_bytes(dtype);
   BufferSet set;
-  set.read(a.x, span_bytes(a.rows, a.cols, a.ld, e));
-  set.write(a.codes, a.rows * ckpt_pitch(a.cols));
-  set.write(a.scales, a.rows * ckpt_scales(a.cols) * 4);
-  set.write(a.y, a.rows * a.cols * e);
-  if (set.conflict()) return ADASUM_ERR_ALIAS;
+  set.read(a.x, span_bytes(a.rows, a.cols, a.ld, e), e);
+  set.write(a.codes, a.rows * ckpt_pitch(a.cols), 16);
+  set.write(a.scales, a.rows * ckpt_scales(a.cols) * 4, 4);
+  set.write(a.y, a.rows * a.cols * e, e);
+  if (adasum_status_t st = set.check()) return st;
   const double n = static_cast<double>(a.rows) * a.cols;
   const bool vec = is_aligned(a.x, 16) && is_aligned(a.y, 16) && a.ld * e % 16 == 0 && (act == kActNone || a.cols * e % 16 == 0);
   const unsigned grid = deal(a, a.ld);
@@ -296,16 +296,16 @@ adasum_status_t unpack(UnpackArgs a, int dtype, int act, cudaStream_t stream) {
   if (adasum_status_t st = check_shape(a.rows, a.cols, dtype)) return st;
   if (a.rows == 0) return ADASUM_OK;
   if (a.codes == nullptr || a.scales == nullptr || a.out == nullptr || !is_aligned(a.codes, 16) ||
-      (act != kActNone && (a.dy == nullptr || a.ld_dy < a.cols)))
+      (act != kActNone && (a.dy == nullptr || !valid_ld(a.rows, a.cols, a.ld_dy))))
     return ADASUM_ERR_INVALID_ARG;
   const int64_t e = dtype_bytes(dtype);
   BufferSet set;
-  set.read(a.codes, a.rows * ckpt_pitch(a.cols));
-  set.read(a.scales, a.rows * ckpt_scales(a.cols) * 4);
-  if (act != kActNone) set.read(a.dy, span_bytes(a.rows, a.cols, a.ld_dy, e));
-  set.write(a.out, a.rows * a.cols * e);
-  set.write(a.y, a.rows * a.cols * e);
-  if (set.conflict()) return ADASUM_ERR_ALIAS;
+  set.read(a.codes, a.rows * ckpt_pitch(a.cols), 16);
+  set.read(a.scales, a.rows * ckpt_scales(a.cols) * 4, 4);
+  if (act != kActNone) set.read(a.dy, span_bytes(a.rows, a.cols, a.ld_dy, e), e);
+  set.write(a.out, a.rows * a.cols * e, e);
+  set.write(a.y, a.rows * a.cols * e, e);
+  if (adasum_status_t st = set.check()) return st;
   const double n = static_cast<double>(a.rows) * a.cols;
   const bool vec = is_aligned(a.out, 16) && is_aligned(a.y, 16) && a.cols * e % 16 == 0 &&
                    (act == kActNone || (is_aligned(a.dy, 16) && a.ld_dy * e % 16 == 0));

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kEmbThreads) lookup_kernel(const LookupArgs a)
 
 constexpr int kSortThreads = 1024, kSortItems = 8;        // of the CTA that sorts a worker's tokens
 constexpr int kSortMost = kSortThreads * kSortItems;      // tokens it takes
-constexpr int kTileThreads = 256, kTileItems = 8;         // of a tile of the multi-CTA sort
+constexpr int kTileThreads = 256, kTileItems = 4;         // of a tile of the multi-CTA sort
 constexpr int kTile = kTileThreads * kTileItems;
 constexpr int kDigits = 256;
 constexpr int kMostPasses = 4;
@@ -719,15 +719,16 @@ adasum_status_t adasum_embedding(const void* table, int64_t num_rows, int64_t co
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (!valid_dtype(dtype) || num_rows < 0 || cols < 1 || n < 0 || (token_bytes != 4 && token_bytes != 8))
     return ADASUM_ERR_INVALID_ARG;
-  if (cols > INT32_MAX || n > INT32_MAX || num_rows > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
+  if (cols > INT32_MAX || n > INT32_MAX || num_rows > INT32_MAX || num_rows > INT64_MAX / 8 / cols)
+    return ADASUM_ERR_UNSUPPORTED;
   if (n == 0) return ADASUM_OK;
   if ((table == nullptr && num_rows > 0) || tokens == nullptr || out == nullptr) return ADASUM_ERR_INVALID_ARG;
   const int64_t e = dtype_bytes(dtype);
   BufferSet set;
-  set.read(table, num_rows * cols * e);
-  set.read(tokens, n * token_bytes);
-  set.write(out, n * cols * e);
-  if (set.conflict()) return ADASUM_ERR_ALIAS;
+  set.read(table, num_rows * cols * e, e);
+  set.read(tokens, n * token_bytes, token_bytes);
+  set.write(out, n * cols * e, e);
+  if (adasum_status_t st = set.check()) return st;
   const int parts = static_cast<int>((cols + kLookupVecs * kSlice - 1) / (kLookupVecs * kSlice));
   if (n * parts > UINT32_MAX - kEmbWarps) return ADASUM_ERR_UNSUPPORTED;
   const int64_t grid = (n * parts + kEmbWarps - 1) / kEmbWarps;
@@ -756,10 +757,11 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
     return ADASUM_ERR_INVALID_ARG;
   if (adasum_status_t st = check_worker_offsets(worker_offsets, K)) return st;
   const int64_t n = worker_offsets[K];
-  if (cols > INT32_MAX || n >= INT32_MAX || num_rows >= INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
+  if (cols > INT32_MAX || n >= INT32_MAX || num_rows >= INT32_MAX || num_rows > INT64_MAX / 8 / cols)
+    return ADASUM_ERR_UNSUPPORTED;
   if (chunk_bound(n, K) * ((cols + kSlice - 1) / kSlice) > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
   if (num_rows == 0) return ADASUM_OK;
-  if (grads == nullptr || (n > 0 && (grad_out == nullptr || tokens == nullptr || ld < cols)))
+  if (grads == nullptr || (n > 0 && (grad_out == nullptr || tokens == nullptr || !valid_ld(n, cols, ld))))
     return ADASUM_ERR_INVALID_ARG;
   const int64_t need = adasum_embedding_backward_scratch_bytes(n, cols, K);
   if (need > 0 && (scratch == nullptr || scratch_bytes < need || !is_aligned(scratch, 256)))
@@ -768,9 +770,9 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   SortArgs s = {};
   TableGradArgs a = {};
   BufferSet set;
-  set.read(grad_out, span_bytes(n, cols, ld, e));
-  set.read(tokens, n * token_bytes);
-  set.write(scratch, need);
+  set.read(grad_out, span_bytes(n, cols, ld, e), e);
+  set.read(tokens, n * token_bytes, token_bytes);
+  set.write(scratch, need, 256);
   // vectors: pieces of eight columns where both types are bf16, else of four, on their own
   // boundaries (and rows of grad_out addressed by 32 bits of 8-byte units)
   const int piece = e + ge == 4 ? 8 : 4;
@@ -783,7 +785,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   const int64_t span = static_cast<int64_t>(a.part) * kEmbWarps;
   for (int k = 0; k < K; ++k) {
     if (grads[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
-    set.write(grads[k], num_rows * cols * ge);
+    set.write(grads[k], num_rows * cols * ge, ge);
     vec = vec && is_aligned(grads[k], piece * ge);
     const int64_t nk = worker_offsets[k + 1] - worker_offsets[k];
     s.fill[k] = a.grads[k] = grads[k];
@@ -791,7 +793,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
     s.tile_off[k + 1] = s.tile_off[k] + static_cast<int>((nk + kTile - 1) / kTile);
     a.chunk_off[k + 1] = a.chunk_off[k] + static_cast<int>((nk + span - 1) / span);
   }
-  if (set.conflict()) return ADASUM_ERR_ALIAS;
+  if (adasum_status_t st = set.check()) return st;
   if (n == 0) {  // nothing to sum: zero the gradients, or leave them
     if (accumulate) return ADASUM_OK;
     for (int k = 0; k < K; ++k)

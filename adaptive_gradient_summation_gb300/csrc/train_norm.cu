@@ -578,7 +578,7 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
   if (a.rows > 0) {
     if (a.dy == nullptr || a.rstd == nullptr || a.dx == nullptr) return ADASUM_ERR_INVALID_ARG;
     if (kept ? a.scales == nullptr : (a.x == nullptr || a.mean == nullptr)) return ADASUM_ERR_INVALID_ARG;
-    if (a.ld_dy < a.cols || (!kept && a.ld_x < a.cols) || (kept && !is_aligned(a.codes, 16)))
+    if (!valid_ld(a.rows, a.cols, a.ld_dy) || (!kept && !valid_ld(a.rows, a.cols, a.ld_x)) || (kept && !is_aligned(a.codes, 16)))
       return ADASUM_ERR_INVALID_ARG;
   }
   const int64_t need = adasum_layer_norm_backward_scratch_bytes(a.rows, a.cols, K);
@@ -587,31 +587,31 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
   WorkerRows rows = {};
   ParamGradArgs p = {};
   BufferSet set;
-  set.read(a.dy, span_bytes(a.rows, a.cols, a.ld_dy, e));
+  set.read(a.dy, span_bytes(a.rows, a.cols, a.ld_dy, e), e);
   if (kept) {
-    set.read(a.codes, a.rows * ckpt_pitch(a.cols));
-    set.read(a.scales, a.rows * ckpt_scales(a.cols) * 4);
+    set.read(a.codes, a.rows * ckpt_pitch(a.cols), 16);
+    set.read(a.scales, a.rows * ckpt_scales(a.cols) * 4, 4);
   } else {
-    set.read(a.x, span_bytes(a.rows, a.cols, a.ld_x, e));
-    set.read(a.mean, a.rows * 4);
+    set.read(a.x, span_bytes(a.rows, a.cols, a.ld_x, e), e);
+    set.read(a.mean, a.rows * 4, 4);
   }
-  set.read(a.rstd, a.rows * 4);
-  set.read(a.weight, a.cols * we);
-  set.read(a.bias, a.cols * we);
-  set.write(a.dx, a.rows * a.cols * e);
-  set.write(a.y, a.rows * a.cols * e);
-  if (want) set.write(scratch, need);
+  set.read(a.rstd, a.rows * 4, 4);
+  set.read(a.weight, a.cols * we, we);
+  set.read(a.bias, a.cols * we, we);
+  set.write(a.dx, a.rows * a.cols * e, e);
+  set.write(a.y, a.rows * a.cols * e, e);
+  if (want) set.write(scratch, need, 256);
   for (int k = 0; k < K; ++k) {
     if (dw != nullptr) {
       if (dw[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
-      set.write(p.dw[k] = dw[k], a.cols * ge);
+      set.write(p.dw[k] = dw[k], a.cols * ge, ge);
     }
     if (db != nullptr) {
       if (db[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
-      set.write(p.db[k] = db[k], a.cols * ge);
+      set.write(p.db[k] = db[k], a.cols * ge, ge);
     }
   }
-  if (set.conflict()) return ADASUM_ERR_ALIAS;
+  if (adasum_status_t st = set.check()) return st;
   const double n = static_cast<double>(a.rows) * a.cols;
   deal_rows(rows, offs, K, grad_teams(a.cols), kNormCtasPerSm * sm_count());
   const bool vec = is_aligned(a.dy, 16) && is_aligned(a.dx, 16) && is_aligned(a.y, 16) && a.ld_dy * e % 16 == 0 &&
@@ -652,18 +652,18 @@ adasum_status_t adasum_layer_norm(const void* x, int64_t rows, int64_t cols, int
   if (adasum_status_t st = check_norm(rows, cols, dtype, weight_dtype)) return st;
   if ((codes == nullptr) != (scales == nullptr) || !(eps >= 0.f)) return ADASUM_ERR_INVALID_ARG;
   if (rows == 0) return ADASUM_OK;
-  if (x == nullptr || y == nullptr || ld < cols || !is_aligned(codes, 16)) return ADASUM_ERR_INVALID_ARG;
+  if (x == nullptr || y == nullptr || !valid_ld(rows, cols, ld) || !is_aligned(codes, 16)) return ADASUM_ERR_INVALID_ARG;
   const int64_t e = dtype_bytes(dtype), we = dtype_bytes(weight_dtype);
   BufferSet set;
-  set.read(x, span_bytes(rows, cols, ld, e));
-  set.read(weight, cols * we);
-  set.read(bias, cols * we);
-  set.write(y, rows * cols * e);
-  set.write(mean, rows * 4);
-  set.write(rstd, rows * 4);
-  set.write(codes, rows * ckpt_pitch(cols));
-  set.write(scales, rows * ckpt_scales(cols) * 4);
-  if (set.conflict()) return ADASUM_ERR_ALIAS;
+  set.read(x, span_bytes(rows, cols, ld, e), e);
+  set.read(weight, cols * we, we);
+  set.read(bias, cols * we, we);
+  set.write(y, rows * cols * e, e);
+  set.write(mean, rows * 4, 4);
+  set.write(rstd, rows * 4, 4);
+  set.write(codes, rows * ckpt_pitch(cols), 16);
+  set.write(scales, rows * ckpt_scales(cols) * 4, 4);
+  if (adasum_status_t st = set.check()) return st;
   const NormArgs a = {x, rows, cols, ld, weight, bias, static_cast<int>(weight_dtype), eps, y, mean, rstd, codes, scales};
   const bool vec = is_aligned(x, 16) && is_aligned(y, 16) && ld * e % 16 == 0 && cols * e % 16 == 0;
   const double n = static_cast<double>(rows) * cols;

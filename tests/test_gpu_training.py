@@ -146,6 +146,31 @@ def test_table_gradient_runs(native, kind, n):
     check_table_gradient(rows, cols, offs, BF16, FP32, False, tokens, seed=n)
 
 
+@pytest.mark.parametrize("n", [50, 300, 5000, 9000])
+@pytest.mark.parametrize("rows,cols", [(1 << 23, 2), ((1 << 24) + 5, 1)])
+def test_table_gradient_many_rows(native, rows, cols, n):
+    """Tokens of 24 and 25 bits: more digits to sort by, and no 32-bit word for a token and its
+    place."""
+    tokens = skewed_tokens(n, rows, seed=n)
+    dy = randn(n, cols, seed=1)
+    for accumulate in (False, True):
+        grad = torch.zeros(rows * cols, device=DEV)
+        ags.embedding_backward(dy, tokens, rows, grads=grad, accumulate=accumulate)
+        want, tol = ref.table_gradient(dy, tokens, rows, 1.0, [0, n], None, None, FP32)[0]
+        close(grad.view(rows, cols), want, tol, "gradient")
+
+
+def test_table_gradient_most_workers(native):
+    """256 workers of 0 to 70 tokens each, a few hundred, and one of thousands."""
+    rows, cols = 37, 40
+    for sizes in ([k % 71 for k in range(256)], [k % 3 * 130 for k in range(256)], [k % 71 for k in range(255)] + [9000]):
+        offs = [0]
+        for s in sizes:
+            offs.append(offs[-1] + s)
+        tokens = skewed_tokens(offs[-1], rows, seed=len(set(sizes)))
+        check_table_gradient(rows, cols, offs, BF16, FP32, True, tokens)
+
+
 def test_table_gradient_order_of_tokens(native):
     """Sorting is stable and sums are fixed: equal calls give equal bits, and tokens permuted
     within a worker change the sums by roundings only."""
@@ -835,6 +860,8 @@ def test_refusals_of_the_c_entry(native):
     if need > 0:
         scratch = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
         assert emb() == BAD and emb(s=p(scratch), sb=need - 1) == BAD and emb(s=p(scratch) + 8, sb=need) == BAD
+    assert norm(x=p(x) + 2) == BAD and norm(m=p(st) + 1) == BAD and norm(ld=1 << 62) == BAD
+    assert back(g=p(x) + 1) == BAD and back(dx=p(out) + 2) == BAD and emb(t=p(st) + 2) == BAD
     assert lib.adasum_embedding(p(x), 6, 64, 0, p(st), 8, -1, 1.0, p(out), None) == BAD
     assert lib.adasum_embedding(p(x), 6, 64, 0, p(st), 8, 1 << 40, 1.0, p(out), None) == BIG
     assert lib.adasum_checkpoint_pack(p(x), 6, 64, 64, 0, p(i8) + 8, p(st), None) == BAD
