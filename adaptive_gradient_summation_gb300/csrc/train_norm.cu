@@ -108,7 +108,7 @@ __device__ __forceinline__ void clear_past(F2 (&v)[4], int left, int lane) {
 // and one exchange joins them: with n_w columns, mean m_w and sum of squares S_w,
 //     mean = sum n_w m_w / n,   S = sum S_w + n_w (m_w - mean)^2.
 // Bound by the bytes of x and y; the next row is on its way while one is worked on.
-template <typename T, int LAYOUT, int W, int NV, bool KEEP>
+template <typename T, int LAYOUT, int W, int NV, bool KEEP, bool FULL>
 __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm : 1) norm_kernel(const NormArgs a) {
   using TM = Team<W, NV>;
   pdl_enter();
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
   const int64_t pitch = ckpt_pitch(a.cols), nscales = ckpt_scales(a.cols);
   int left[NV], count = 0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) count += left[j] = slice_left(a.cols, (j * W + w) * kSlice);
+  for (int j = 0; j < NV; ++j) count += left[j] = FULL ? kSlice : slice_left(a.cols, (j * W + w) * kSlice);
   const float inv_count = count > 0 ? 1.f / static_cast<float>(count) : 0.f;
   Raw8<T, LAYOUT> next[NV];
   auto fetch = [&](int64_t row) {
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
       auto columns = [&](int i) {  // of warp i
         int n = 0;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) n += slice_left(a.cols, (j * W + i) * kSlice);
+        for (int j = 0; j < NV; ++j) n += FULL ? kSlice : slice_left(a.cols, (j * W + i) * kSlice);
         return static_cast<float>(n);
       };
       const float mine = mean;
@@ -244,7 +244,7 @@ struct GradShape {
 // one read of dy and x (or of h's codes), two sums per row, and the parameters' sums of a
 // CTA's rows in registers, joined over its teams at the end and written as the CTA's partial.
 // A CTA's rows all belong to one worker.  Bound by the bytes of dy, x and dx.
-template <typename T, int LAYOUT, int W, int NV, bool KEPT>
+template <typename T, int LAYOUT, int W, int NV, bool KEPT, bool FULL>
 __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kCtas)
     norm_grad_kernel(const NormGradArgs a, const __grid_constant__ WorkerRows rows) {
   using TM = Team<W, NV>;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
   F2 dw[NV][4], db[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    left[j] = slice_left(a.cols, (j * W + w) * kSlice);
+    left[j] = FULL ? kSlice : slice_left(a.cols, (j * W + w) * kSlice);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[j][i] = db[j][i] = f2(0.f);
   }
@@ -485,9 +485,12 @@ template <typename T, int LAYOUT, int W, int NV>
 int launch_norm_as(const NormArgs& a, cudaStream_t stream) {
   using TM = Team<W, NV>;
   const size_t smem = 2 * TM::kCols * sizeof(float);
-  static SmemAllowed allowed[2];
-  auto kernel = a.codes ? norm_kernel<T, LAYOUT, W, NV, true> : norm_kernel<T, LAYOUT, W, NV, false>;
-  if (int rc = allow_smem(kernel, smem, allowed[a.codes != nullptr])) return rc;
+  static SmemAllowed allowed[2][2];
+  const bool full = LAYOUT != kStrided && a.cols == TM::kCols, keep = a.codes != nullptr;
+  constexpr bool kCan = LAYOUT != kStrided;
+  auto kernel = full ? (keep ? norm_kernel<T, LAYOUT, W, NV, true, kCan> : norm_kernel<T, LAYOUT, W, NV, false, kCan>)
+                     : (keep ? norm_kernel<T, LAYOUT, W, NV, true, false> : norm_kernel<T, LAYOUT, W, NV, false, false>);
+  if (int rc = allow_smem(kernel, smem, allowed[full][keep])) return rc;
   const int64_t need = (a.rows + TM::kTeams - 1) / TM::kTeams;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(need, static_cast<int64_t>(kNormCtasPerSm) * sm_count()));
   return launch_pdl(kernel, dim3(grid), dim3(TM::kThreads), smem, stream, a);
@@ -512,9 +515,11 @@ int launch_norm_grad_as(const NormGradArgs& a, const WorkerRows& rows, cudaStrea
                       (LAYOUT != kStrided ? GradShape<T, W, NV>::kStages * TM::kWarps * sizeof(RowCopy<T, LAYOUT, NV, KEPT>) : 0);
   const size_t sums = TM::kTeams == 1 ? 0 : TM::kTeams * 2 * TM::kCols * sizeof(float);
   const size_t smem = std::max(work, sums);
-  static SmemAllowed allowed;
-  auto kernel = norm_grad_kernel<T, LAYOUT, W, NV, KEPT>;
-  if (int rc = allow_smem(kernel, smem, allowed)) return rc;
+  static SmemAllowed allowed[2];
+  constexpr bool kCan = LAYOUT != kStrided;
+  const bool full = kCan && a.cols == TM::kCols;
+  auto kernel = full ? norm_grad_kernel<T, LAYOUT, W, NV, KEPT, kCan> : norm_grad_kernel<T, LAYOUT, W, NV, KEPT, false>;
+  if (int rc = allow_smem(kernel, smem, allowed[full])) return rc;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(rows.cta_off[rows.K])), dim3(TM::kThreads), smem, stream, a, rows);
 }
 // Teams of the gradient kernel: two slices a warp, since each costs 16 registers of sums.
