@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kSlice = 256;        // columns of a warp's eight per lane
 constexpr int kNormCtasPerSm = 2;  // of the persistent grids
+constexpr int kGradCluster = 8;    // CTAs of a worker when the gradient runs as one launch
 
 struct NormArgs {
   const void* x;
@@ -47,7 +48,8 @@ struct NormGradArgs {
   int weight_dtype;
   void* dx;
   void* y;             // null: not wanted
-  float* partials;     // [CTA][weight, bias][cols]; null: parameters' gradients not wanted
+  float* partials;     // [CTA][weight, bias][cols]; null: parameters' gradients not wanted, or
+  int cluster;         // joined by a cluster of this many CTAs per worker (0: no)
 };
 
 struct ParamGradArgs {
@@ -73,6 +75,14 @@ struct Team {
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(W * 32) : "memory");
   }
 };
+
+// Writes (or adds) one sum of a worker's weight (bias: its bias) gradient.
+__device__ __forceinline__ void put_param(const ParamGradArgs& p, int k, bool bias, int64_t c, float s) {
+  void* out = bias ? p.db[k] : p.dw[k];
+  if (out == nullptr || c >= p.cols) return;
+  if (p.accumulate) s += load_any(out, p.dtype, c);
+  store_any(out, p.dtype, c, s);
+}
 
 // The weight and bias of a CTA's columns as floats in shared memory, 1 and 0 where absent.
 template <int LAYOUT, int COLS, int THREADS>
@@ -246,7 +256,8 @@ struct GradShape {
 // A CTA's rows all belong to one worker.  Bound by the bytes of dy, x and dx.
 template <typename T, int LAYOUT, int W, int NV, bool KEPT, bool FULL>
 __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kCtas)
-    norm_grad_kernel(const NormGradArgs a, const __grid_constant__ WorkerRows rows) {
+    norm_grad_kernel(const NormGradArgs a, const __grid_constant__ WorkerRows rows,
+                     const __grid_constant__ ParamGradArgs params) {
   using TM = Team<W, NV>;
   using Copy = RowCopy<T, LAYOUT, NV, KEPT>;
   constexpr int S = GradShape<T, W, NV>::kStages;
@@ -262,13 +273,21 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
   const float inv_n = 1.f / static_cast<float>(a.cols);
   const int64_t pitch = ckpt_pitch(a.cols), nscales = ckpt_scales(a.cols);
   int k = 0;
-  for (int hi = rows.K; hi - k > 1;) {
-    const int m = (k + hi) >> 1;
-    if (rows.cta_off[m] <= static_cast<int>(blockIdx.x)) k = m;
-    else hi = m;
+  int64_t r0, r1;
+  if (a.cluster) {
+    k = blockIdx.x / a.cluster;
+    const int64_t per = (rows.off[k + 1] - rows.off[k] + a.cluster - 1) / a.cluster;
+    r0 = rows.off[k] + static_cast<int64_t>(blockIdx.x - k * a.cluster) * per;
+    r1 = min(r0 + per, rows.off[k + 1]);
+  } else {
+    for (int hi = rows.K; hi - k > 1;) {
+      const int m = (k + hi) >> 1;
+      if (rows.cta_off[m] <= static_cast<int>(blockIdx.x)) k = m;
+      else hi = m;
+    }
+    r0 = rows.off[k] + static_cast<int64_t>(blockIdx.x - rows.cta_off[k]) * rows.rows_per_cta;
+    r1 = min(r0 + rows.rows_per_cta, rows.off[k + 1]);
   }
-  const int64_t r0 = rows.off[k] + static_cast<int64_t>(blockIdx.x - rows.cta_off[k]) * rows.rows_per_cta;
-  const int64_t r1 = min(r0 + rows.rows_per_cta, rows.off[k + 1]);
   int left[NV];
   F2 dw[NV][4], db[NV][4];
 #pragma unroll
@@ -417,45 +436,41 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kC
     }
     if constexpr (kTwice) issue(row + S * TM::kTeams, stage);
   }
-  if (a.partials == nullptr) return;
-  float* out = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-  if constexpr (TM::kTeams == 1) {
+  if (a.partials == nullptr && a.cluster == 0) return;
+  // the teams' sums in shared memory, the first team's place taking their total
+  if constexpr (LAYOUT != kStrided) cp_async_wait<0>();
+  __syncthreads();
+  float* mine = sm + team * 2 * TM::kCols;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c0 = (j * W + w) * kSlice;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 pw = parts(dw[j][i]), pb = parts(db[j][i]);
-        const int c = lane_col<LAYOUT>(lane, 2 * i), d = lane_col<LAYOUT>(lane, 2 * i + 1);
-        if (c < left[j]) {
-          out[c0 + c] = pw.x;
-          out[a.cols + c0 + c] = pb.x;
-        }
-        if (d < left[j]) {
-          out[c0 + d] = pw.y;
-          out[a.cols + c0 + d] = pb.y;
-        }
-      }
-    }
-  } else {
-    if constexpr (LAYOUT != kStrided) cp_async_wait<0>();
-    __syncthreads();
-    float* mine = sm + team * 2 * TM::kCols;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      sts8(mine + (j * W + w) * kSlice, lane, dw[j]);
-      sts8(mine + TM::kCols + (j * W + w) * kSlice, lane, db[j]);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * TM::kCols; i += TM::kThreads) {
-      const int c = smem_col<LAYOUT>(i % TM::kCols);
-      if (c >= a.cols) continue;
-      float s = 0.f;
-#pragma unroll
-      for (int t = 0; t < TM::kTeams; ++t) s += sm[t * 2 * TM::kCols + i];
-      out[(i / TM::kCols) * a.cols + c] = s;
-    }
+  for (int j = 0; j < NV; ++j) {
+    sts8(mine + (j * W + w) * kSlice, lane, dw[j]);
+    sts8(mine + TM::kCols + (j * W + w) * kSlice, lane, db[j]);
   }
+  __syncthreads();
+  float* out = a.cluster ? nullptr : a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+  for (int i = threadIdx.x; i < 2 * TM::kCols; i += TM::kThreads) {
+    const int c = smem_col<LAYOUT>(i % TM::kCols);
+    float s = sm[i];
+#pragma unroll
+    for (int t = 1; t < TM::kTeams; ++t) s += sm[t * 2 * TM::kCols + i];
+    if (a.cluster) sm[i] = s;
+    else if (c < a.cols) out[(i / TM::kCols) * a.cols + c] = s;
+  }
+  if (a.cluster == 0) return;
+  // few rows: the worker's CTAs are one cluster, and each adds its share of the columns over
+  // them, in their order
+  cluster_sync_all();
+  const int share = 2 * TM::kCols / kGradCluster, rank = static_cast<int>(cluster_ctarank());
+  for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += TM::kThreads) {
+    const int c = smem_col<LAYOUT>(i % TM::kCols);
+    float v[kGradCluster], s = 0.f;
+#pragma unroll
+    for (int r = 0; r < kGradCluster; ++r) v[r] = *map_rank(sm + i, r);
+#pragma unroll
+    for (int r = 0; r < kGradCluster; ++r) s += v[r];
+    put_param(params, k, i >= TM::kCols, c, s);
+  }
+  cluster_sync_all();  // the others may still read this CTA's sums
 }
 
 // Joins the CTAs' partials of one worker: 32 columns per CTA, eight partials at a time.
@@ -472,13 +487,9 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant_
   red[warp][lane] = s;
   __syncthreads();
   if (warp > 0 || i >= 2 * p.cols) return;
-  void* out = i < p.cols ? p.dw[k] : p.db[k];
-  if (out == nullptr) return;
 #pragma unroll
   for (int j = 1; j < 8; ++j) s += red[j][lane];
-  const int64_t c = i < p.cols ? i : i - p.cols;
-  if (p.accumulate) s += load_any(out, p.dtype, c);
-  store_any(out, p.dtype, c, s);
+  put_param(p, k, i >= p.cols, i < p.cols ? i : i - p.cols, s);
 }
 
 template <typename T, int LAYOUT, int W, int NV>
@@ -509,18 +520,21 @@ int launch_norm(const NormArgs& a, cudaStream_t stream) {
 }
 
 template <typename T, int LAYOUT, int W, int NV, bool KEPT>
-int launch_norm_grad_as(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
+int launch_norm_grad_as(const NormGradArgs& a, const WorkerRows& rows, const ParamGradArgs& params, cudaStream_t stream) {
   using TM = Team<W, NV>;
   const size_t work = (KEPT ? 2 : 1) * TM::kCols * sizeof(float) +
                       (LAYOUT != kStrided ? GradShape<T, W, NV>::kStages * TM::kWarps * sizeof(RowCopy<T, LAYOUT, NV, KEPT>) : 0);
-  const size_t sums = TM::kTeams == 1 ? 0 : TM::kTeams * 2 * TM::kCols * sizeof(float);
+  const size_t sums = TM::kTeams * 2 * TM::kCols * sizeof(float);
   const size_t smem = std::max(work, sums);
   static SmemAllowed allowed[2];
   constexpr bool kCan = LAYOUT != kStrided;
   const bool full = kCan && a.cols == TM::kCols;
   auto kernel = full ? norm_grad_kernel<T, LAYOUT, W, NV, KEPT, kCan> : norm_grad_kernel<T, LAYOUT, W, NV, KEPT, false>;
   if (int rc = allow_smem(kernel, smem, allowed[full])) return rc;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(rows.cta_off[rows.K])), dim3(TM::kThreads), smem, stream, a, rows);
+  if (a.cluster)
+    return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(rows.K * a.cluster)), dim3(TM::kThreads), a.cluster, smem,
+                              stream, a, rows, params);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(rows.cta_off[rows.K])), dim3(TM::kThreads), smem, stream, a, rows, params);
 }
 // Teams of the gradient kernel: two slices a warp, since each costs 16 registers of sums.
 int grad_teams(int64_t cols) {
@@ -528,20 +542,33 @@ int grad_teams(int64_t cols) {
   return slices <= 2 ? 8 : slices <= 4 ? 4 : slices <= 8 ? 2 : 1;
 }
 template <typename T, int LAYOUT, bool KEPT>
-int launch_norm_grad_kept(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
+int launch_norm_grad_kept(const NormGradArgs& a, const WorkerRows& rows, const ParamGradArgs& p, cudaStream_t stream) {
   const int64_t slices = (a.cols + kSlice - 1) / kSlice;
-  if (slices <= 1) return launch_norm_grad_as<T, LAYOUT, 1, 1, KEPT>(a, rows, stream);
-  if (slices <= 2) return launch_norm_grad_as<T, LAYOUT, 1, 2, KEPT>(a, rows, stream);
-  if (slices <= 4) return launch_norm_grad_as<T, LAYOUT, 2, 2, KEPT>(a, rows, stream);
-  if (slices <= 8) return launch_norm_grad_as<T, LAYOUT, 4, 2, KEPT>(a, rows, stream);
-  if (slices <= 16) return launch_norm_grad_as<T, LAYOUT, 8, 2, KEPT>(a, rows, stream);
-  if (slices <= 32) return launch_norm_grad_as<T, LAYOUT, 16, 2, KEPT>(a, rows, stream);
-  return launch_norm_grad_as<T, LAYOUT, 16, 4, KEPT>(a, rows, stream);
+  if (slices <= 1) return launch_norm_grad_as<T, LAYOUT, 1, 1, KEPT>(a, rows, p, stream);
+  if (slices <= 2) return launch_norm_grad_as<T, LAYOUT, 1, 2, KEPT>(a, rows, p, stream);
+  if (slices <= 4) return launch_norm_grad_as<T, LAYOUT, 2, 2, KEPT>(a, rows, p, stream);
+  if (slices <= 8) return launch_norm_grad_as<T, LAYOUT, 4, 2, KEPT>(a, rows, p, stream);
+  if (slices <= 16) return launch_norm_grad_as<T, LAYOUT, 8, 2, KEPT>(a, rows, p, stream);
+  if (slices <= 32) return launch_norm_grad_as<T, LAYOUT, 16, 2, KEPT>(a, rows, p, stream);
+  return launch_norm_grad_as<T, LAYOUT, 16, 4, KEPT>(a, rows, p, stream);
 }
 template <typename T, int LAYOUT>
-int launch_norm_grad(const NormGradArgs& a, const WorkerRows& rows, cudaStream_t stream) {
-  return a.codes ? launch_norm_grad_kept<T, LAYOUT, true>(a, rows, stream)
-                 : launch_norm_grad_kept<T, LAYOUT, false>(a, rows, stream);
+int launch_norm_grad(const NormGradArgs& a, const WorkerRows& rows, const ParamGradArgs& p, cudaStream_t stream) {
+  return a.codes ? launch_norm_grad_kept<T, LAYOUT, true>(a, rows, p, stream)
+                 : launch_norm_grad_kept<T, LAYOUT, false>(a, rows, p, stream);
+}
+
+// Whether the gradient's sums are joined by clusters in the same launch.  That saves the host
+// a launch, the scratch memory and its size: 10 us of 50 for a call through the binding.  The
+// device takes longer, since a worker's rows have eight CTAs only: 1 us of 5 at 4 rows a team
+// (128 x 1024 bf16, replayed from a graph), 2 of 6 at 8, 5 of 6 at 16 and 10 of 9 at 32.  So
+// up to 16 rows a team for the worker with the most.
+bool one_launch(const int64_t* offs, int K, int64_t cols) {
+  if (K > 32) return false;
+  const int64_t most = static_cast<int64_t>(16) * kGradCluster * grad_teams(cols);
+  for (int k = 0; k < K; ++k)
+    if (offs[k + 1] - offs[k] > most) return false;
+  return true;
 }
 
 // Deals the workers' rows to at most about `target` CTAs, none of them to two workers.
@@ -586,7 +613,7 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
     if (!valid_ld(a.rows, a.cols, a.ld_dy) || (!kept && !valid_ld(a.rows, a.cols, a.ld_x)) || (kept && !is_aligned(a.codes, 16)))
       return ADASUM_ERR_INVALID_ARG;
   }
-  const int64_t need = adasum_layer_norm_backward_scratch_bytes(a.rows, a.cols, K);
+  const int64_t need = adasum_layer_norm_backward_scratch_bytes(offs, K, a.cols);
   if (want && need > 0 && (scratch == nullptr || scratch_bytes < need || !is_aligned(scratch, 256)))
     return ADASUM_ERR_INVALID_ARG;
   WorkerRows rows = {};
@@ -619,22 +646,24 @@ adasum_status_t norm_backward(NormGradArgs a, int dtype, const int64_t* offs, in
   if (adasum_status_t st = set.check()) return st;
   const double n = static_cast<double>(a.rows) * a.cols;
   deal_rows(rows, offs, K, grad_teams(a.cols), kNormCtasPerSm * sm_count());
+  p.cols = a.cols;
+  p.dtype = grad_dtype;
+  p.accumulate = accumulate != 0;
+  const bool joined = want && a.rows > 0 && one_launch(offs, K, a.cols);
+  a.cluster = joined ? kGradCluster : 0;
   const bool vec = is_aligned(a.dy, 16) && is_aligned(a.dx, 16) && is_aligned(a.y, 16) && a.ld_dy * e % 16 == 0 &&
                    a.cols * e % 16 == 0 && (kept || (is_aligned(a.x, 16) && a.ld_x * e % 16 == 0));
-  a.partials = want ? static_cast<float*>(scratch) : nullptr;
+  a.partials = want && !joined ? static_cast<float*>(scratch) : nullptr;
   if (a.rows > 0)
     if (adasum_status_t st = counted_launch(stream, kept ? "norm_grad_checkpoint" : "norm_grad",
                                             n * (kept ? 2 * e + 1 + (a.y ? e : 0) : 3 * e), [&] {
           if (dtype == kBF16)
-            return vec ? launch_norm_grad<bf16, kVec8>(a, rows, stream) : launch_norm_grad<bf16, kStrided>(a, rows, stream);
-          return vec ? launch_norm_grad<float, kVec4>(a, rows, stream) : launch_norm_grad<float, kStrided>(a, rows, stream);
+            return vec ? launch_norm_grad<bf16, kVec8>(a, rows, p, stream) : launch_norm_grad<bf16, kStrided>(a, rows, p, stream);
+          return vec ? launch_norm_grad<float, kVec4>(a, rows, p, stream) : launch_norm_grad<float, kStrided>(a, rows, p, stream);
         }))
       return st;
-  if (!want) return ADASUM_OK;
+  if (!want || joined) return ADASUM_OK;
   p.partials = a.partials;
-  p.cols = a.cols;
-  p.dtype = grad_dtype;
-  p.accumulate = accumulate != 0;
   std::copy(rows.cta_off, rows.cta_off + K + 1, p.cta_off);
   return counted_launch(stream, "norm_params", 0.0, [&] {
     return launch_pdl(norm_params_kernel, dim3(static_cast<unsigned>((2 * a.cols + 31) / 32), K), dim3(256), 0, stream, p);
@@ -678,8 +707,10 @@ adasum_status_t adasum_layer_norm(const void* x, int64_t rows, int64_t cols, int
   });
 }
 
-int64_t adasum_layer_norm_backward_scratch_bytes(int64_t rows, int64_t cols, int K) {
-  if (rows <= 0 || cols <= 0 || K <= 0) return 0;
+int64_t adasum_layer_norm_backward_scratch_bytes(const int64_t* worker_offsets, int K, int64_t cols) {
+  if (check_worker_offsets(worker_offsets, K) || cols <= 0 || cols > ADASUM_NORM_MAX_COLS) return 0;
+  const int64_t rows = worker_offsets[K];
+  if (rows == 0 || one_launch(worker_offsets, K, cols)) return 0;
   // one partial per CTA: the persistent grid, or one CTA for every worker
   const int64_t ctas = std::min<int64_t>(rows, kNormCtasPerSm * sm_count() + static_cast<int64_t>(K));
   return (ctas * 2 * cols * 4 + 255) / 256 * 256;

@@ -304,7 +304,7 @@ def layer_norm_checkpointed(x: torch.Tensor, weight: torch.Tensor | None = None,
     return y, kept, rstd
 
 
-def _norm_gradients(grad_weights, grad_biases, weight, wanted, accumulate, K, rows, cols, index):
+def _norm_gradients(grad_weights, grad_biases, weight, wanted, accumulate, offs, K, cols, index):
     """(weights' gradients, their pointers, biases', pointers, code, scratch bytes, scratch)."""
     if not wanted:
         if grad_weights is not None or grad_biases is not None:
@@ -317,7 +317,7 @@ def _norm_gradients(grad_weights, grad_biases, weight, wanted, accumulate, K, ro
     db, dbp, other = _gradients(grad_biases, K, cols, index, dtype, (cols,), "grad_biases")
     if other is not dtype:
         raise ValueError("grad_weights and grad_biases must share their dtype")
-    nbytes = load_library().adasum_layer_norm_backward_scratch_bytes(rows, cols, K)
+    nbytes = load_library().adasum_layer_norm_backward_scratch_bytes(_address(offs), K, cols)
     return dw, dwp, db, dbp, _CODE[dtype], nbytes, _scratch(nbytes, index)
 
 
@@ -344,7 +344,7 @@ def layer_norm_backward(grad_output: torch.Tensor, x: torch.Tensor, mean: torch.
                       accumulate=accumulate, parameter_grads=parameter_grads)
     offs, K = _workers(worker_offsets, rows)
     dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(grad_weights, grad_biases, weight, parameter_grads,
-                                                               accumulate, K, rows, cols, index)
+                                                               accumulate, offs, K, cols, index)
     dx = _output(None, x.shape, x.dtype, index)
     st = load_library().adasum_layer_norm_backward(
         grad_output.data_ptr(), ld_g, x.data_ptr(), ld_x, mean_p, rstd_p, cols, code, w, wcode, _address(offs), K,
@@ -374,7 +374,7 @@ def layer_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Chec
                       accumulate=accumulate, parameter_grads=parameter_grads, with_output=with_output)
     offs, K = _workers(worker_offsets, rows)
     dw, dwp, db, dbp, gcode, nbytes, scratch = _norm_gradients(grad_weights, grad_biases, weight, parameter_grads,
-                                                               accumulate, K, rows, cols, index)
+                                                               accumulate, offs, K, cols, index)
     dx = _output(None, grad_output.shape, grad_output.dtype, index)
     y = _output(None, dx.shape, dx.dtype, index) if with_output else None
     st = load_library().adasum_layer_norm_backward_checkpointed(

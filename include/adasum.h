@@ -400,8 +400,8 @@ ADASUM_API adasum_status_t adasum_layer_norm(const void *x, int64_t rows, int64_
  *   grad_x        rows x cols elements of dtype
  *   grad_weights, grad_biases  host arrays of K device pointers to cols elements of
  *                 grad_dtype; either may be NULL: not wanted
- *   scratch       adasum_layer_norm_backward_scratch_bytes(rows, cols, K); may be NULL
- *                 when neither gradient is wanted
+ *   scratch       adasum_layer_norm_backward_scratch_bytes(worker_offsets, K, cols); may be
+ *                 NULL when that is 0 (few rows) or neither gradient is wanted
  */
 ADASUM_API adasum_status_t adasum_layer_norm_backward(
     const void *grad_out, int64_t ld_grad, const void *x, int64_t ld_x, const float *mean,
@@ -409,7 +409,8 @@ ADASUM_API adasum_status_t adasum_layer_norm_backward(
     adasum_dtype_t weight_dtype, const int64_t *worker_offsets, int K, void *grad_x,
     void *const *grad_weights, void *const *grad_biases, adasum_dtype_t grad_dtype,
     int accumulate, void *scratch, int64_t scratch_bytes, adasum_stream_t stream);
-ADASUM_API int64_t adasum_layer_norm_backward_scratch_bytes(int64_t rows, int64_t cols, int K);
+ADASUM_API int64_t adasum_layer_norm_backward_scratch_bytes(const int64_t *worker_offsets, int K,
+                                                            int64_t cols);
 
 /*
  * adasum_layer_norm_backward_checkpointed -- the same from the 8-bit checkpoint of h that

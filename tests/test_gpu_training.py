@@ -337,6 +337,55 @@ def test_norm_gradient_many_rows(native, offs, kept):
     assert all(torch.equal(p, q) for p, q in zip([got[0][0]] + got[0][1] + got[0][2], [got[1][0]] + got[1][1] + got[1][2]))
 
 
+@pytest.mark.parametrize("kept", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(2100, 100), (2100, 512), (1100, 1000), (1100, 1001), (600, 2056), (300, 4104),
+                                       (270, 8192), (265, 16383)])
+def test_norm_gradient_long(native, rows, cols, dtype, kept):
+    """Enough rows for the sums to be joined by a second kernel, at every width of team, two of
+    the three workers' parts beginning inside a CTA's rows."""
+    x, dy, (w, b) = activations(rows, cols, dtype, 5), randn(rows, cols, seed=3, dtype=dtype), params(cols, FP32, 9)
+    offs = [0, rows // 3, rows // 3 + 1, rows]
+    old = randn(2, 3, cols, seed=11)
+    dw, db = list(old[0].clone().unbind(0)), list(old[1].clone().unbind(0))
+    more = dict(worker_offsets=offs, grad_weights=dw, grad_biases=db, accumulate=True)
+    if kept:
+        _, ckpt, rstd = ags.layer_norm_checkpointed(x, w, b)
+        h = ref.unpacked(ckpt.codes, ckpt.scales, cols)
+        h_tol = u * h.abs()
+        dx = ags.layer_norm_checkpointed_backward(dy, ckpt, rstd, w, **more)[0]
+    else:
+        _, mean, rstd = ags.layer_norm(x, w, b)
+        h = (x.to(F8) - mean.to(F8)[:, None]) * rstd.to(F8)[:, None]
+        h_tol = 3 * u * (x.to(F8).abs() + mean.to(F8).abs()[:, None]) * rstd.to(F8)[:, None] + 2 * u * h.abs()
+        dx = ags.layer_norm_backward(dy, x, mean, rstd, w, **more)[0]
+    want_x, want_w, want_b = ref.norm_gradient(dy, h, h_tol, rstd, w, offs, old[0], old[1], FP32)
+    close(dx, *want_x, "dx")
+    for k in range(3):
+        close(dw[k], *want_w[k], f"dw of worker {k}")
+        close(db[k], *want_b[k], f"db of worker {k}")
+
+
+def test_scratch_is_checked(native):
+    """Scratch memory that is missing, too small, not aligned or part of an input."""
+    import ctypes
+    lib, rows, cols = ags.load_library(), 3000, 64
+    x, stat, out = randn(rows, cols, seed=1), torch.ones(rows, device=DEV), torch.empty(rows, cols, device=DEV)
+    g = torch.empty(cols, device=DEV)
+    offs, grads = (ctypes.c_int64 * 2)(0, rows), (ctypes.c_void_p * 1)(g.data_ptr())
+    need = lib.adasum_layer_norm_backward_scratch_bytes(offs, 1, cols)
+    scratch = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
+    call = lambda s, n: lib.adasum_layer_norm_backward(  # noqa: E731
+        x.data_ptr(), cols, x.data_ptr(), cols, stat.data_ptr(), stat.data_ptr(), cols, 0, None, 0, offs, 1, out.data_ptr(),
+        grads, None, 0, 0, s, n, None)
+    before = ags.launch_count()
+    assert need > 0 and call(None, need) == 1 and call(scratch.data_ptr(), need - 1) == 1
+    assert call(scratch.data_ptr() + 8, need) == 1 and call(x.data_ptr(), need) == 3
+    assert ags.launch_count() == before
+    assert call(scratch.data_ptr(), need) == 0
+    torch.cuda.synchronize()
+
+
 def test_norm_without_rows(native):
     x = torch.empty(0, 40, device=DEV)
     w, b = params(40, FP32, 1)
@@ -849,7 +898,7 @@ def test_refusals_of_the_c_entry(native):
     assert back(g=None) == BAD and back(m=None) == BAD and back(r=None) == BAD and back(dx=None) == BAD
     assert back(o=None) == BAD and back(K=0) == BAD and back(K=257) == BIG and back(lg=1) == BAD and back(lx=1) == BAD
     assert back(dw=null) == BAD and back(gd=7) == BAD and back(dx=p(x)) == ALIAS
-    need = lib.adasum_layer_norm_backward_scratch_bytes(6, 64, 1)
+    need = lib.adasum_layer_norm_backward_scratch_bytes(offs, 1, 64)
     if need > 0:
         scratch = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
         assert back(dw=grads) == BAD and back(dw=grads, sc=p(scratch), sb=need - 1) == BAD
