@@ -70,7 +70,7 @@ SIGNATURES = {
     "adasum_embedding": (ctypes.c_int, [_P, _I64, _I64, _I, _P, _I, _I64, _F, _P, _P]),
     "adasum_embedding_backward": (ctypes.c_int, [_P, _I64, _I64, _I, _P, _I, _P, _I, _I64, _F, _I64,
                                                  _P, _I, _I, _P, _I64, _P]),
-    "adasum_embedding_backward_scratch_bytes": (ctypes.c_int64, [_I64, _I64, _I]),
+    "adasum_embedding_backward_scratch_bytes": (ctypes.c_int64, [_P, _I, _I64, _I64]),
     "adasum_layer_norm": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _P, _P, _I, _F, _P, _P, _P, _P, _P, _P]),
     "adasum_layer_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I64, _I, _P, _I, _P, _I,
                                                   _P, _P, _P, _I, _I, _P, _I64, _P]),

@@ -73,14 +73,21 @@ constexpr int kMostPasses = 4;
 constexpr int kSelfSort = kEmbThreads;  // tokens of a worker that the summing CTAs sort themselves
 constexpr int kSelfPart = 4;            // ... and of a warp then
 
+// Whether the summing CTAs sort their worker's tokens themselves: few tokens for each, and a
+// token and its place in 32 bits.
+bool self_sorted(const int64_t* offs, int K, int64_t num_rows) {
+  for (int k = 0; k < K; ++k)
+    if (offs[k + 1] - offs[k] > kSelfSort) return false;
+  return num_rows < (1 << 23);
+}
+
 // Tokens per warp of a chunk: few enough that the warps cover the memory's latency (about
 // 32 per SM), at most 32.
-int warp_tokens(int64_t n, int64_t most, int64_t cols) {
-  if (most <= kSelfSort) return kSelfPart;
+int warp_tokens(int64_t n, int64_t cols) {
   const int64_t work = n * ((cols + kSlice - 1) / kSlice);
   return work >= 32 * 4864 ? 32 : work >= 16 * 4864 ? 16 : 8;
 }
-int64_t chunk_bound(int64_t n, int K) { return n / (kSelfPart * kEmbWarps) + K; }
+int64_t chunk_bound(int64_t n, int K) { return n / (8 * kEmbWarps) + K; }
 int64_t tile_bound(int64_t n, int K) { return n / kTile + K; }
 
 // Regions of the scratch memory.
@@ -740,9 +747,10 @@ adasum_status_t adasum_embedding(const void* table, int64_t num_rows, int64_t co
   });
 }
 
-int64_t adasum_embedding_backward_scratch_bytes(int64_t n, int64_t cols, int K) {
-  if (n <= 0 || cols <= 0 || K <= 0) return 0;
-  return Scratch(n, cols, K).total;
+int64_t adasum_embedding_backward_scratch_bytes(const int64_t* worker_offsets, int K, int64_t num_rows, int64_t cols) {
+  if (check_worker_offsets(worker_offsets, K) || num_rows <= 0 || cols <= 0) return 0;
+  const int64_t n = worker_offsets[K];
+  return n == 0 || self_sorted(worker_offsets, K, num_rows) ? 0 : Scratch(n, cols, K).total;
 }
 
 adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, int64_t ld, adasum_dtype_t dtype,
@@ -759,11 +767,11 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   const int64_t n = worker_offsets[K];
   if (cols > INT32_MAX || n >= INT32_MAX || num_rows >= INT32_MAX || num_rows > INT64_MAX / 8 / cols)
     return ADASUM_ERR_UNSUPPORTED;
-  if (chunk_bound(n, K) * ((cols + kSlice - 1) / kSlice) > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
+  if ((n / (kSelfPart * kEmbWarps) + K) * ((cols + kSlice - 1) / kSlice) > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
   if (num_rows == 0) return ADASUM_OK;
   if (grads == nullptr || (n > 0 && (grad_out == nullptr || tokens == nullptr || !valid_ld(n, cols, ld))))
     return ADASUM_ERR_INVALID_ARG;
-  const int64_t need = adasum_embedding_backward_scratch_bytes(n, cols, K);
+  const int64_t need = adasum_embedding_backward_scratch_bytes(worker_offsets, K, num_rows, cols);
   if (need > 0 && (scratch == nullptr || scratch_bytes < need || !is_aligned(scratch, 256)))
     return ADASUM_ERR_INVALID_ARG;
   const int64_t e = dtype_bytes(dtype), ge = dtype_bytes(grad_dtype);
@@ -780,8 +788,8 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
              span_bytes(n, cols, ld, e) < (int64_t(8) << 32);
   int64_t most = 0;
   for (int k = 0; k < K; ++k) most = std::max(most, worker_offsets[k + 1] - worker_offsets[k]);
-  // (a key and an index share 32 bits where a CTA sorts by itself)
-  a.part = warp_tokens(n, num_rows < (1 << 23) ? most : INT64_MAX, cols);
+  const bool self_sort = self_sorted(worker_offsets, K, num_rows);
+  a.part = self_sort ? kSelfPart : warp_tokens(n, cols);
   const int64_t span = static_cast<int64_t>(a.part) * kEmbWarps;
   for (int k = 0; k < K; ++k) {
     if (grads[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
@@ -802,8 +810,8 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
     return ADASUM_OK;
   }
   const Scratch at(n, cols, K);
-  char* base = static_cast<char*>(scratch);
-  auto ints = [&](int64_t offset) { return reinterpret_cast<int*>(base + offset); };
+  char* base = need > 0 ? static_cast<char*>(scratch) : nullptr;
+  auto ints = [&](int64_t offset) { return base ? reinterpret_cast<int*>(base + offset) : nullptr; };
   // digits: as few passes of at most 8 bits as the keys 0..num_rows need
   int bits = 1;
   while ((num_rows >> bits) != 0) ++bits;
@@ -818,7 +826,6 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   s.join_count = ints(at.count);
   s.fill_bytes = accumulate ? 0 : num_rows * cols * ge;
   const int64_t fill_vecs = static_cast<int64_t>(K) * (s.fill_bytes / 16);
-  const bool self_sort = a.part == kSelfPart;
   const int fill_threads = !self_sort && most <= kSortMost ? kSortThreads : kTileThreads;
   s.fill_ctas = accumulate ? 0 : static_cast<int>(std::min<int64_t>(2048 / fill_threads * sm_count(), 1 + fill_vecs / fill_threads));
   const double fill = static_cast<double>(K) * s.fill_bytes;
@@ -869,7 +876,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
   a.pos = ints(at.pos[out]);
   a.count = ints(at.count);
   a.list = ints(at.list);
-  a.partials = reinterpret_cast<float*>(base + at.partials);
+  a.partials = base ? reinterpret_cast<float*>(base + at.partials) : nullptr;
   const int64_t items = static_cast<int64_t>(a.chunk_off[K]) * a.slices;
   const unsigned grid = static_cast<unsigned>(items);
   if (adasum_status_t st = counted_launch(stream, "table_sum", static_cast<double>(n) * (cols * e + 8), [&] {

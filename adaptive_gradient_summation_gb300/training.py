@@ -249,7 +249,7 @@ def embedding_backward(grad_output: torch.Tensor, tokens: torch.Tensor, num_rows
     offs, K = _workers(worker_offsets, rows)
     grads, ptrs, gtype = _gradients(grads, K, num_rows * cols, index, grad_output.dtype, (num_rows, cols), "grads")
     lib = load_library()
-    nbytes = lib.adasum_embedding_backward_scratch_bytes(rows, cols, K)
+    nbytes = lib.adasum_embedding_backward_scratch_bytes(_address(offs), K, num_rows, cols)
     scratch = _scratch(nbytes, index)
     st = lib.adasum_embedding_backward(
         grad_output.data_ptr(), cols, ld, code, tokens.data_ptr(), width, _address(offs), K, num_rows, float(scale),

@@ -362,7 +362,8 @@ ADASUM_API adasum_status_t adasum_embedding(const void *table, int64_t num_rows,
  *   padding_idx   a token that gets no gradient (any value outside [0, num_rows): none);
  *                 tokens outside the table get none either
  *   grads         host array of K device pointers, num_rows x cols elements of grad_dtype
- *   scratch       adasum_embedding_backward_scratch_bytes(worker_offsets[K], cols, K)
+ *   scratch       adasum_embedding_backward_scratch_bytes(worker_offsets, K, num_rows,
+ *                 cols); may be NULL when that is 0 (few tokens)
  * 1 <= K <= ADASUM_MAX_K; fewer than 2^31 tokens and table rows, else
  * ADASUM_ERR_UNSUPPORTED.
  */
@@ -371,7 +372,8 @@ ADASUM_API adasum_status_t adasum_embedding_backward(
     int token_bytes, const int64_t *worker_offsets, int K, int64_t num_rows, float scale,
     int64_t padding_idx, void *const *grads, adasum_dtype_t grad_dtype, int accumulate,
     void *scratch, int64_t scratch_bytes, adasum_stream_t stream);
-ADASUM_API int64_t adasum_embedding_backward_scratch_bytes(int64_t n, int64_t cols, int K);
+ADASUM_API int64_t adasum_embedding_backward_scratch_bytes(const int64_t *worker_offsets, int K,
+                                                           int64_t num_rows, int64_t cols);
 
 /*
  * adasum_layer_norm -- per row: mean and variance over the columns, rstd =

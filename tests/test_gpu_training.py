@@ -384,6 +384,17 @@ def test_scratch_is_checked(native):
     assert ags.launch_count() == before
     assert call(scratch.data_ptr(), need) == 0
     torch.cuda.synchronize()
+    tokens = torch.zeros(rows, dtype=torch.int32, device=DEV)
+    need = lib.adasum_embedding_backward_scratch_bytes(offs, 1, 1, cols)
+    scratch = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
+    call = lambda s, n: lib.adasum_embedding_backward(  # noqa: E731
+        x.data_ptr(), cols, cols, 0, tokens.data_ptr(), 4, offs, 1, 1, 1.0, -1, grads, 0, 0, s, n, None)
+    before = ags.launch_count()
+    assert need > 0 and call(None, need) == 1 and call(scratch.data_ptr(), need - 1) == 1
+    assert call(scratch.data_ptr() + 8, need) == 1 and call(x.data_ptr(), need) == 3
+    assert ags.launch_count() == before
+    assert call(scratch.data_ptr(), need) == 0
+    torch.cuda.synchronize()
 
 
 def test_norm_without_rows(native):
@@ -898,17 +909,8 @@ def test_refusals_of_the_c_entry(native):
     assert back(g=None) == BAD and back(m=None) == BAD and back(r=None) == BAD and back(dx=None) == BAD
     assert back(o=None) == BAD and back(K=0) == BAD and back(K=257) == BIG and back(lg=1) == BAD and back(lx=1) == BAD
     assert back(dw=null) == BAD and back(gd=7) == BAD and back(dx=p(x)) == ALIAS
-    need = lib.adasum_layer_norm_backward_scratch_bytes(offs, 1, 64)
-    if need > 0:
-        scratch = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
-        assert back(dw=grads) == BAD and back(dw=grads, sc=p(scratch), sb=need - 1) == BAD
-        assert back(dw=grads, sc=p(scratch) + 8, sb=need) == BAD and back(dw=grads, sc=p(x), sb=need) == ALIAS
     assert emb(g=None) == BAD and emb(t=None) == BAD and emb(tb=2) == BAD and emb(grads=None) == BAD
     assert emb(grads=null) == BAD and emb(rows=-1) == BAD and emb(cols=0) == BAD and emb(K=300) == BIG
-    need = lib.adasum_embedding_backward_scratch_bytes(6, 64, 1)
-    if need > 0:
-        scratch = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
-        assert emb() == BAD and emb(s=p(scratch), sb=need - 1) == BAD and emb(s=p(scratch) + 8, sb=need) == BAD
     assert norm(x=p(x) + 2) == BAD and norm(m=p(st) + 1) == BAD and norm(ld=1 << 62) == BAD
     assert back(g=p(x) + 1) == BAD and back(dx=p(out) + 2) == BAD and emb(t=p(st) + 2) == BAD
     assert lib.adasum_embedding(p(x), 6, 64, 0, p(st), 8, -1, 1.0, p(out), None) == BAD
