@@ -169,7 +169,7 @@ __device__ __forceinline__ Raw8<T, N> load8(const T* p, int left, int lane) {
           const uint2 v = KEEP ? __ldg(q) : __ldcs(q);
           w[0] = v.x, w[1] = v.y;
         }
-      } else {
+      } else if (c < left) {
         uint32_t v[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = c + e < left ? element(c + e) : 0u;
@@ -178,6 +178,9 @@ __device__ __forceinline__ Raw8<T, N> load8(const T* p, int left, int lane) {
           if constexpr (sizeof(T) == 4) w[e] = v[e];
           else if (e & 1) w[e >> 1] = __byte_perm(v[e - 1], v[e], 0x5410);
         }
+      } else {  // (most lanes of a narrow row)
+#pragma unroll
+        for (int e = 0; e < kWords; ++e) w[e] = 0u;
       }
     }
   }
@@ -249,6 +252,7 @@ __device__ __forceinline__ void store8(T* p, int left, int lane, const float (&v
         }
         continue;
       }
+      if (c >= left) continue;
     }
 #pragma unroll
     for (int e = 0; e < N; ++e)

@@ -63,6 +63,11 @@ struct ParamGradArgs {
 
 // A row is shared by a team of W warps, each holding NV slices of 256 columns in registers
 // (slice j * W + w for warp w), so that a row is read once.  A CTA holds TEAMS teams.
+// A warp that has a whole row of one or two slices to itself takes kRows rows at a time, so
+// that their sums over the lanes, chains of shuffles, run side by side.
+template <int W, int NV>
+constexpr int kRows = W == 1 && NV <= 2 ? 4 / NV : 1;
+
 template <int W, int NV>
 struct Team {
   static constexpr int kWarps = W < 8 ? 8 : W;
@@ -93,6 +98,15 @@ __device__ __forceinline__ void stage_params(float* w, float* b, const void* wei
     if (w) w[i] = c < cols && weight ? load_any(weight, dtype, c) : 1.f;
     if (b) b[i] = c < cols && bias ? load_any(bias, dtype, c) : 0.f;
   }
+}
+
+// Sums over the lanes of several values side by side.
+template <int R>
+__device__ __forceinline__ void warp_sums(float (&v)[R]) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xFFFFFFFFu, v[r], d);
 }
 
 __device__ __forceinline__ float sum_parts(F2 x) {
@@ -135,37 +149,53 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
 #pragma unroll
   for (int j = 0; j < NV; ++j) count += left[j] = FULL ? kSlice : slice_left(a.cols, (j * W + w) * kSlice);
   const float inv_count = count > 0 ? 1.f / static_cast<float>(count) : 0.f;
-  Raw8<T, LAYOUT> next[NV];
+  constexpr int R = kRows<W, NV>;
+  Raw8<T, LAYOUT> next[R][NV];
   auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      next[j] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld + (j * W + w) * kSlice,
-                                 row < a.rows ? left[j] : 0, lane);
+    for (int r = 0; r < R; ++r, row += step)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        next[r][j] = load8<T, LAYOUT>(static_cast<const T*>(a.x) + row * a.ld + (j * W + w) * kSlice,
+                                      row < a.rows ? left[j] : 0, lane);
   };
   int64_t row = static_cast<int64_t>(blockIdx.x) * TM::kTeams + team;
   fetch(row);
-  for (int it = 0; row < a.rows; row += step, it ^= 1) {
-    F2 v[NV][4], acc = f2(0.f);
+  for (int it = 0; row < a.rows; row += R * step, it ^= 1) {
+    F2 v[R][NV][4];
+    float mean[R], sq[R], rstd[R];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) unpack8<T, LAYOUT>(next[j], v[j]);
-    fetch(row + step);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NV; ++j) unpack8<T, LAYOUT>(next[r][j], v[r][j]);
+    fetch(row + R * step);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc = add2(acc, v[j][i]);
-    float mean = warp_sum(sum_parts(acc)) * (W == 1 ? inv_n : inv_count);
-    acc = f2(0.f);
+    for (int r = 0; r < R; ++r) {
+      F2 acc = f2(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+      for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], f2(-mean));
-      clear_past<LAYOUT>(v[j], left[j], lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc = fma2(v[j][i], v[j][i], acc);
+        for (int i = 0; i < 4; ++i) acc = add2(acc, v[r][j][i]);
+      mean[r] = sum_parts(acc);
     }
-    float sq = warp_sum(sum_parts(acc));
+    warp_sums(mean);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] *= W == 1 ? inv_n : inv_count;
+      F2 acc = f2(0.f);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[r][j][i] = add2(v[r][j][i], f2(-mean[r]));
+        clear_past<LAYOUT>(v[r][j], left[j], lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = fma2(v[r][j][i], v[r][j][i], acc);
+      }
+      sq[r] = sum_parts(acc);
+    }
+    warp_sums(sq);
     if constexpr (W > 1) {
-      if (lane == 0) ex[it][team][w] = make_float2(mean, sq);
+      if (lane == 0) ex[it][team][w] = make_float2(mean[0], sq[0]);
       TM::sync(team);
       auto columns = [&](int i) {  // of warp i
         int n = 0;
@@ -173,7 +203,7 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
         for (int j = 0; j < NV; ++j) n += FULL ? kSlice : slice_left(a.cols, (j * W + i) * kSlice);
         return static_cast<float>(n);
       };
-      const float mine = mean;
+      const float mine = mean[0];
       float total = 0.f;
       float2 p[W];
 #pragma unroll
@@ -181,50 +211,61 @@ __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm
         p[i] = ex[it][team][i];
         total = __fmaf_rn(columns(i), p[i].x, total);
       }
-      mean = total * inv_n;
-      sq = 0.f;
+      mean[0] = total * inv_n;
+      sq[0] = 0.f;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const float d = p[i].x - mean;
-        sq += __fmaf_rn(columns(i) * d, d, p[i].y);
+        const float d = p[i].x - mean[0];
+        sq[0] += __fmaf_rn(columns(i) * d, d, p[i].y);
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[j][i] = add2(v[j][i], f2(mine - mean));
-        if (KEEP) clear_past<LAYOUT>(v[j], left[j], lane);
+        for (int i = 0; i < 4; ++i) v[0][j][i] = add2(v[0][j][i], f2(mine - mean[0]));
+        if (KEEP) clear_past<LAYOUT>(v[0][j], left[j], lane);
       }
     }
-    const float rstd = 1.f / sqrtf(__fmaf_rn(sq, inv_n, a.eps));
-    if (w == 0 && lane == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+    float top[KEEP ? R * NV : 1][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      rstd[r] = 1.f / sqrtf(__fmaf_rn(sq[r], inv_n, a.eps));
+      if (w == 0 && lane == 0 && row + r * step < a.rows) {
+        if (a.mean) a.mean[row + r * step] = mean[r];
+        if (a.rstd) a.rstd[row + r * step] = rstd[r];
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[r][j][i] = mul2(v[r][j][i], f2(rstd[r]));
+        if constexpr (KEEP) block_tops<LAYOUT>(v[r][j], top[r * NV + j]);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = mul2(v[j][i], f2(rstd));
-    CkptScale sc[KEEP ? NV : 1][2];
-    if constexpr (KEEP) {
-      float top[NV][2];
-#pragma unroll
-      for (int j = 0; j < NV; ++j) block_tops<LAYOUT>(v[j], top[j]);
-      block_scales<LAYOUT, NV>(top, lane, sc);
-    }
+    CkptScale sc[KEEP ? R * NV : 1][2];
+    if constexpr (KEEP) block_scales<LAYOUT, R * NV>(top, lane, sc);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c0 = (j * W + w) * kSlice;
       if (left[j] <= 0) break;
       if constexpr (KEEP) {
-        store_codes8<LAYOUT>(a.codes + row * pitch + c0, left[j], lane, ckpt_codes<LAYOUT>(v[j], sc[j]));
-        store_scales<LAYOUT>(a.scales + row * nscales + c0 / kCkptBlock, left[j], lane, sc[j]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const int64_t at = row + r * step;
+          if (R > 1 && at >= a.rows) break;
+          store_codes8<LAYOUT>(a.codes + at * pitch + c0, left[j], lane, ckpt_codes<LAYOUT>(v[r][j], sc[r * NV + j]));
+          store_scales<LAYOUT>(a.scales + at * nscales + c0 / kCkptBlock, left[j], lane, sc[r * NV + j]);
+        }
       }
       F2 wv[4], bv[4];
       lds8(ws + c0, lane, wv);
       lds8(bs + c0, lane, bv);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[j][i] = fma2(v[j][i], wv[i], bv[i]);
-      store8<T, LAYOUT>(static_cast<T*>(a.y) + row * a.cols + c0, left[j], lane, v[j]);
+      for (int r = 0; r < R; ++r) {
+        const int64_t at = row + r * step;
+        if (R > 1 && at >= a.rows) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[r][j][i] = fma2(v[r][j][i], wv[i], bv[i]);
+        store8<T, LAYOUT>(static_cast<T*>(a.y) + at * a.cols + c0, left[j], lane, v[r][j]);
+      }
     }
   }
 }
