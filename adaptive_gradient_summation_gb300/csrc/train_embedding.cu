@@ -73,6 +73,7 @@ constexpr int kSortThreads = 1024, kSortItems = 4;
 constexpr int kSortMost = kSortThreads * kSortItems;
 constexpr int kTileThreads = 256, kTileItems = 4;         // of a tile of the multi-CTA sort
 constexpr int kTile = kTileThreads * kTileItems;
+constexpr int kScanTiles = 64;  // of a worker, above which a kernel of its own sums the tiles' counts
 constexpr int kDigits = 256;
 constexpr int kMostPasses = 4;
 constexpr int kSelfSort = kEmbThreads;  // tokens of a worker that the summing CTAs sort themselves
@@ -103,7 +104,7 @@ int64_t tile_bound(int64_t n, int K) { return n / kTile + K; }
 
 // Regions of the scratch memory.
 struct Scratch {
-  int64_t keys[2], pos[2], hist, count, list, partials, total;
+  int64_t keys[2], pos[2], hist, totals, count, list, partials, total;
   Scratch(int64_t n, int64_t cols, int K) {
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -114,6 +115,7 @@ struct Scratch {
     for (int i = 0; i < 2; ++i) keys[i] = take(4 * n);
     for (int i = 0; i < 2; ++i) pos[i] = take(4 * n);
     hist = take(4 * kMostPasses * kDigits * tile_bound(n, K));
+    totals = take(4 * kDigits * static_cast<int64_t>(K));
     count = take(4);
     list = take(4 * chunk_bound(n, K));
     partials = take(8 * cols * chunk_bound(n, K));
@@ -134,6 +136,7 @@ struct SortArgs {
   const int *keys_in, *pos_in;   // null in the first pass: the tokens
   int *keys, *pos;
   int* hist;           // [passes][ntiles][kDigits]
+  int* totals;         // [K][kDigits]: null, or hist holds the counts of a worker's earlier tiles
   int* join_count;
   void* fill[kMaxK];   // gradients to be zeroed
   int64_t fill_bytes;  // of each (0: accumulate)
@@ -360,6 +363,47 @@ __global__ void __launch_bounds__(kTileThreads) table_count_kernel(const __grid_
   a.hist[static_cast<int64_t>(tile) * kDigits + threadIdx.x] = hist[threadIdx.x];
 }
 
+// then, where a worker has many tiles, before each pass the counts of its earlier tiles in
+// place of a tile's own, and their totals: 32 digits of a worker per CTA, its tiles in as many
+// parts as a CTA has warps, each read twice (sums, then prefixes).  Without it every tile of a
+// pass reads the counts of all the worker's tiles, which is less where they are few and grows
+// with their square.  Gradient of 50304 rows x 8 columns added, tokens of one worker, without
+// and with: 65536 47.6 and 47.6 us, 131072 87 and 76, 1048576 431 and 228, 4194304 3100 and
+// 799; 16 workers of 65536 each, 64 columns, 261 and 252.
+__global__ void __launch_bounds__(kSortThreads) table_scan_kernel(const __grid_constant__ SortArgs a) {
+  pdl_enter();
+  constexpr int kParts = kSortThreads / 32;
+  __shared__ int part[kParts][32];
+  const int k = blockIdx.x / (kDigits / 32), lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int d = blockIdx.x % (kDigits / 32) * 32 + lane;
+  const int64_t first = a.tile_off[k], tiles = a.tile_off[k + 1] - first;
+  const int64_t t0 = first + tiles * w / kParts, t1 = first + tiles * (w + 1) / kParts;
+  int* h = a.hist + static_cast<int64_t>(a.pass) * a.ntiles * kDigits + d;
+  int sum = 0;
+#pragma unroll 8
+  for (int64_t t = t0; t < t1; ++t) sum += h[t * kDigits];
+  part[w][lane] = sum;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll 8
+  for (int i = 0; i < kParts; ++i) {
+    const int v = part[i][lane];
+    if (i < w) before += v;
+    total += v;
+  }
+  if (w == 0) a.totals[k * kDigits + d] = total;
+  for (int64_t t = t0; t < t1; t += 8) {
+    int v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = t + i < t1 ? h[(t + i) * kDigits] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (t + i < t1) h[(t + i) * kDigits] = before;
+      before += v[i];
+    }
+  }
+}
+
 // then one pass per digit: a tile's keys of digit d go after the worker's keys of smaller
 // digits and those of digit d in earlier tiles; on the way the next digit is counted in the
 // tiles that the keys arrive in.  Each pass zeroes its part of the gradients beside.
@@ -385,11 +429,16 @@ __global__ void __launch_bounds__(kTileThreads) table_scatter_kernel(const __gri
   // (thread d: digit d of the worker's tiles)
   const int* h = a.hist + static_cast<int64_t>(a.pass) * a.ntiles * kDigits + threadIdx.x;
   int earlier = 0, total = 0;
+  if (a.totals) {
+    earlier = h[static_cast<int64_t>(tile) * kDigits];
+    total = a.totals[k * kDigits + threadIdx.x];
+  } else {
 #pragma unroll 8
-  for (int t = a.tile_off[k]; t < a.tile_off[k + 1]; ++t) {
-    const int v = h[static_cast<int64_t>(t) * kDigits];
-    if (t < tile) earlier += v;
-    total += v;
+    for (int t = a.tile_off[k]; t < a.tile_off[k + 1]; ++t) {
+      const int v = h[static_cast<int64_t>(t) * kDigits];
+      if (t < tile) earlier += v;
+      total += v;
+    }
   }
   const DigitCount c = block_rank<kTileThreads, kTileItems>(s, key, rank, n, a.shift, a.bits);
   // place of this tile's digit d in the worker's order, minus its place in the tile's
@@ -880,6 +929,7 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
       return st;
   } else {
     s.ntiles = s.tile_off[K];
+    s.totals = most > static_cast<int64_t>(kScanTiles) * kTile ? ints(at.totals) : nullptr;
     if (adasum_status_t st = counted_launch(stream, "table_count", 0.0, [&] {
           return launch_pdl(table_count_kernel, dim3(s.ntiles), dim3(kTileThreads), 0, stream, s);
         }))
@@ -891,6 +941,11 @@ adasum_status_t adasum_embedding_backward(const void* grad_out, int64_t cols, in
       s.pos_in = s.pass > 0 ? ints(at.pos[1 - out]) : nullptr;
       s.keys = ints(at.keys[out]);
       s.pos = ints(at.pos[out]);
+      if (s.totals)
+        if (adasum_status_t st = counted_launch(stream, "table_scan", 0.0, [&] {
+              return launch_pdl(table_scan_kernel, dim3(static_cast<unsigned>(K * (kDigits / 32))), dim3(kSortThreads), 0, stream, s);
+            }))
+          return st;
       s.fill_first = pieces * s.pass / s.passes;
       const int64_t share = pieces * (s.pass + 1) / s.passes - s.fill_first;
       if (adasum_status_t st = counted_launch(stream, "table_scatter", fill / s.passes, [&] {
