@@ -99,7 +99,7 @@ int warp_tokens(int64_t n, int64_t cols) {
   const int64_t work = n * ((cols + kSlice - 1) / kSlice);
   return work >= 150000 ? 32 : work >= 50000 ? 16 : 8;
 }
-int64_t chunk_bound(int64_t n, int K) { return n / (8 * kEmbWarps) + K; }
+int64_t chunk_bound(int64_t n, int64_t cols, int K) { return n / (warp_tokens(n, cols) * kEmbWarps) + K; }
 int64_t tile_bound(int64_t n, int K) { return n / kTile + K; }
 
 // Regions of the scratch memory.
@@ -117,8 +117,8 @@ struct Scratch {
     hist = take(4 * kMostPasses * kDigits * tile_bound(n, K));
     totals = take(4 * kDigits * static_cast<int64_t>(K));
     count = take(4);
-    list = take(4 * chunk_bound(n, K));
-    partials = take(8 * cols * chunk_bound(n, K));
+    list = take(4 * chunk_bound(n, cols, K));
+    partials = take(8 * cols * chunk_bound(n, cols, K));
     total = at;
   }
 };
