@@ -6,8 +6,15 @@
 // runs of equal tokens inside one chunk over 256 columns, its warps taking equal parts.  A
 // run that lies inside the chunk goes straight to the gradient; the pieces of a run that
 // crosses chunks go to scratch memory and are joined in order by a last kernel.  So a token
-// that makes up most of the batch costs no more than any other, and every sum has a fixed
-// order.  Workers of at most 256 tokens are one chunk each, which the CTAs sort themselves.
+// that makes up most of the batch costs no more than any other (65536 equal tokens x 1024
+// columns, added, 78 us in a graph, 65536 different ones 93), and every sum has a fixed order.
+// Where all workers have at most 256 tokens the CTAs sort themselves and a warp takes a run to
+// its end: there one token for all costs more (256 equal tokens x 1024 columns 62 us in a graph,
+// 256 different ones 11).
+//
+// Times in the comments are those of one launch between two events (the library's profiler; 4
+// to 6 us of it are the launch), unless they are said to be of a call in a graph of many or of a
+// pass, a call among others through the Python binding.
 #include "adasum_host.h"
 #include "adasum_launch.h"
 #include "adasum_train.cuh"
@@ -37,7 +44,7 @@ __device__ __forceinline__ int64_t load_token(const void* tokens, int bytes, int
 // out = scale * table[token], 0 where a token is not in the table.  One warp copies up to 1024
 // columns of one token's row, four 16-byte vectors per lane in flight; rows that repeat come
 // from L2.  Bound by the output's bytes: 65536 tokens x 2048 bf16 of a table of 50304 rows in
-// 57 us (268 MB written; two vectors in flight 59.6), 8 tokens in 6.
+// 57 us, 52 of them the kernel's (268 MB written; two vectors in flight 59.6), 8 tokens in 6.
 constexpr int kLookupVecs = 4;
 template <typename T, int LAYOUT>
 __global__ void __launch_bounds__(kEmbThreads) lookup_kernel(const LookupArgs a) {
@@ -77,13 +84,13 @@ constexpr int kScanTiles = 64;  // of a worker, above which a kernel of its own 
 constexpr int kDigits = 256;
 constexpr int kMostPasses = 4;
 constexpr int kSelfSort = kEmbThreads;  // tokens of a worker that the summing CTAs sort themselves
-constexpr int kSelfPart = 4;            // ... and of a warp then (8: 128 tokens 5.7 us, not 4.4)
+constexpr int kSelfPart = 4;            // ... and of a warp then (8: 128 tokens 5.7 us in a graph, not 4.4)
 
 // Whether the summing CTAs sort their worker's tokens themselves: few tokens for each, and a
 // token and its place in 32 bits.  That is one launch and no scratch memory, though every CTA
 // of a worker repeats the sort.  In a graph, against sorting in a kernel before: one worker x
 // 1024 columns, 128 tokens 4.4 and 11.0 us, 256 tokens 7.4 and 13.4; 256 x 4096 columns 9.0
-// and 14.2; through the binding 18.7 and 29.1.  (The sort is by counting, quadratic in the
+// and 14.2; a pass of 128 tokens 18.7 and 29.1.  (The sort is by counting, quadratic in the
 // tokens, so it ends where a thread no longer has a token each.)
 bool self_sorted(const int64_t* offs, int K, int64_t num_rows) {
   for (int k = 0; k < K; ++k)
@@ -92,8 +99,8 @@ bool self_sorted(const int64_t* offs, int K, int64_t num_rows) {
 }
 
 // Tokens per warp of a chunk, by the tokens times slices there are: few enough that the warps
-// cover the memory's latency, and not so few that what a warp does once weighs.  The whole
-// gradient with 8, 16 and 32: 8192 tokens x 1024 columns 29.8, 31.4, 34.5 us; 65536 x 256
+// cover the memory's latency, and not so few that what a warp does once weighs.  Added, in a
+// graph, with 8, 16 and 32: 8192 tokens x 1024 columns 29.8, 31.4, 34.5 us; 65536 x 256
 // 42.6, 36.5, 40.6; 20000 x 1024 36.3, 33.5, 39.5; 65536 x 1024 85.4, 68.1, 65.0.
 int warp_tokens(int64_t n, int64_t cols) {
   const int64_t work = n * ((cols + kSlice - 1) / kSlice);
@@ -180,7 +187,7 @@ __device__ __forceinline__ int worker_of(const A* off, int K, I i) {
 // Many CTAs that each write one piece and leave, so that pieces are written nearly in their
 // order, reach 7.6 TB/s on 1 GB; a grid that stays and strides, whose CTAs drift apart, 6.4.
 // (Beside the sort of 16 workers x 4096 tokens 4, 8, 16, 32 vectors: 159, 137, 135, 137 us;
-// beside that of 8192 tokens, one table of 30522 x 1024: 26.1, 26.3, 30.8, 33.4.)
+// the whole gradient of 8192 tokens, one table of 30522 x 1024, in a graph: 26.1, 26.3, 30.8, 33.4.)
 constexpr int kFillVecs = 8;
 __device__ __forceinline__ void fill_piece(const SortArgs& a, int64_t piece) {
   const int k = static_cast<int>(piece / a.fill_pieces);
@@ -367,8 +374,8 @@ __global__ void __launch_bounds__(kTileThreads) table_count_kernel(const __grid_
 // place of a tile's own, and their totals: 32 digits of a worker per CTA, its tiles in as many
 // parts as a CTA has warps, each read twice (sums, then prefixes).  Without it every tile of a
 // pass reads the counts of all the worker's tiles, which is less where they are few and grows
-// with their square.  Gradient of 50304 rows x 8 columns added, tokens of one worker, without
-// and with: 65536 47.6 and 47.6 us, 131072 87 and 76, 1048576 431 and 228, 4194304 3100 and
+// with their square.  Gradient of 50304 rows x 8 columns added, tokens of one worker, one call
+// in a graph, without and with: 65536 47.6 and 47.6 us, 131072 87 and 76, 1048576 431 and 228, 4194304 3100 and
 // 799; 16 workers of 65536 each, 64 columns, 261 and 252.
 __global__ void __launch_bounds__(kSortThreads) table_scan_kernel(const __grid_constant__ SortArgs a) {
   pdl_enter();
@@ -509,7 +516,8 @@ enum Ends : int {
 // The bytes are grad_out's, read once, and the gradient rows written; bound by the issue of
 // instructions (73% of its slots), since with tokens spread over the table most runs are one
 // or two rows, and a row costs its key, its place and a store besides the sum: 65536 rows x
-// 1024 bf16 of 16 workers 41 us after the sort (135 MB read), 128 rows with their sort 12.
+// 1024 bf16 of 16 workers 41 us after the sort (135 MB read), 128 rows with their sort 12 (in a
+// graph 4.4).
 // (Two slices a warp measured slower.)
 template <typename T, typename G, int LAYOUT, bool ADD>
 struct SumSmem {

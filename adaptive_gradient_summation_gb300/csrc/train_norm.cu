@@ -1,5 +1,9 @@
 // train_norm.cu -- layer norm, its gradient with the per-worker reduction of the
 // parameters' gradients, and both with the normalised activation kept in 8 bits.
+//
+// Times in the comments are those of one launch between two events (the library's profiler; 4
+// to 6 us of it are the launch), unless they are said to be of a call in a graph of many or of a
+// pass, a call among others through the Python binding.
 #include "adasum_host.h"
 #include "adasum_launch.h"
 #include "adasum_train.cuh"
@@ -64,11 +68,11 @@ struct ParamGradArgs {
 // A row is shared by a team of W warps, each holding NV slices of 256 columns in registers
 // (slice j * W + w for warp w), so that a row is read once.  A CTA holds TEAMS teams.
 // A warp that has a whole row of one or two slices to itself takes kRows rows at a time, so
-// that their sums over the lanes, chains of shuffles, run side by side: 393216 rows x 128 bf16
-// in 104 us against 186 one at a time, 196608 x 256 in 40 against 58, 98304 x 512 in 36
-// against 41.  (The gradient has its parameters' sums in registers too; two rows at a time
-// gained 120 -> 97 us at 128 columns and lost at 512 and beside the checkpoint, so it takes
-// one.)
+// that their sums over the lanes, chains of shuffles, run side by side: a pass over 393216 rows
+// x 128 bf16 in 104 us against 186 one at a time, 196608 x 256 in 40 against 58, 98304 x 512 in
+// 35 against 41.  The gradient, which has its parameters' sums in registers too, takes one row
+// at every width: two lost at 512 columns and beside the checkpoint.  (At 128 columns without
+// it they gained, 120 -> 97 us a pass; that form does not exist.)
 template <int W, int NV>
 constexpr int kRows = W == 1 && NV <= 2 ? 4 / NV : 1;
 
@@ -562,8 +566,8 @@ int launch_norm_as(const NormArgs& a, cudaStream_t stream) {
 // The smallest team that holds a row: up to four slices a warp, then more warps.  (Two slices a
 // warp: 65536 x 2048 bf16 109 us against 90, with the checkpoint 132 against 113, as a row's
 // sums over the lanes and its exchange between warps are then spread over fewer bytes.)
-// Above 8192 columns a CTA of 16 warps has an SM to itself and one row on its way: 16384
-// columns run at 4.3 TB/s, the gradient, whose sums do not all stay in registers, at 3.4.
+// Above 8192 columns a CTA of 16 warps has an SM to itself and one row on its way: passes over
+// 16384 columns run at 4.3 TB/s, the gradient's, whose sums do not all stay in registers, at 3.4.
 template <typename T, int LAYOUT>
 int launch_norm(const NormArgs& a, cudaStream_t stream) {
   const int64_t slices = (a.cols + kSlice - 1) / kSlice;
@@ -617,7 +621,7 @@ int launch_norm_grad(const NormGradArgs& a, const WorkerRows& rows, const ParamG
 }
 
 // Whether the gradient's sums are joined by clusters in the same launch.  That saves the host
-// a launch, the scratch memory and its size: 10 us of 50 for a call through the binding.  The
+// a launch, the scratch memory and its size: 10 us of a pass of 50.  The
 // device takes longer, since a worker's rows have eight CTAs only: 1 us of 5 at 4 rows a team
 // (128 x 1024 bf16, replayed from a graph), 2 of 6 at 8, 5 of 6 at 16 and 10 of 9 at 32.  So
 // up to 16 rows a team for the worker with the most.

@@ -13,7 +13,9 @@ include/adasum.h: inputs are CUDA tensors, float32 or bfloat16, the types of act
 parameters and parameter gradients being independent of each other; their columns have to
 be next to each other, while rows may be strided.  Outputs are dense.  Calls are
 asynchronous on the current (or given) stream; scratch memory comes from torch's allocator
-on that stream, so calls on several streams may overlap and may be captured.
+on that stream, so calls on several streams may overlap and may be captured.  Nothing is
+recorded for autograd: outputs do not require gradients even where an input does, and the
+caller makes the backward calls (for instance from a ``torch.autograd.Function``).
 """
 from __future__ import annotations
 
@@ -232,7 +234,8 @@ def embedding_backward(grad_output: torch.Tensor, tokens: torch.Tensor, num_rows
     worker_offsets: K+1 offsets into the flattened tokens (None: one worker).  grads: K
     contiguous tensors of num_rows * cols elements (of any one dtype; None allocates them in
     grad_output's), overwritten whole, or with ``accumulate`` added to.  Tokens outside the
-    table and ``padding_idx`` get no gradient.
+    table and ``padding_idx`` get no gradient; ``padding_idx`` is the token itself, so a
+    negative one is no row of the table and masks nothing (it does not count from the end).
     """
     code, index = _kind(grad_output, "grad_output")
     width = _tokens(tokens, index)
