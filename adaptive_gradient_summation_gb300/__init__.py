@@ -27,13 +27,14 @@ from ._native import AdasumError, KernelStat, Status, check, library_path, load_
 from .training import (Checkpoint, checkpoint_pack, checkpoint_unpack, embedding, embedding_backward,
                        gelu_checkpointed, gelu_checkpointed_backward, layer_norm, layer_norm_backward,
                        layer_norm_checkpointed, layer_norm_checkpointed_backward)
+from .updates import NEWTON_SCHULZ, muon_step, orthogonalize
 
 __all__ = ["reduce", "pair", "pair_noalloc", "reduce_momentum_sgd", "local_momentum_reduce", "reduce_from_host", "AdasumError",
            "Status", "load_library", "library_path", "get_last_error", "release_workspace",
            "launch_count", "recomputed_segments", "profile_enable", "profile_collect", "version",
            "Checkpoint", "checkpoint_pack", "checkpoint_unpack", "embedding", "embedding_backward",
            "gelu_checkpointed", "gelu_checkpointed_backward", "layer_norm", "layer_norm_backward",
-           "layer_norm_checkpointed", "layer_norm_checkpointed_backward"]
+           "layer_norm_checkpointed", "layer_norm_checkpointed_backward", "NEWTON_SCHULZ", "muon_step", "orthogonalize"]
 
 _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}
 

@@ -81,6 +81,10 @@ SIGNATURES = {
     "adasum_checkpoint_unpack": (ctypes.c_int, [_P, _P, _I64, _I64, _I, _P, _P]),
     "adasum_gelu_checkpointed": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P]),
     "adasum_gelu_checkpointed_backward": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I64, _I, _I, _P, _P, _P]),
+    "adasum_orthogonalize": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _I, _I, _P, _F, _P, _P, _I64, _P]),
+    "adasum_orthogonalize_scratch_bytes": (ctypes.c_int64, [_I64, _I64, _I64, _I]),
+    "adasum_muon_step": (ctypes.c_int, [_P, _I, _P, _P, _P, _I, _P, _P, _F, _F, _I, _F, _I, _I, _P, _F, _P, _I64, _P]),
+    "adasum_muon_step_scratch_bytes": (ctypes.c_int64, [_P, _P, _I]),
     "adasum_get_last_error": (ctypes.c_int, []),
     "adasum_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "adasum_release_workspace": (ctypes.c_int, []),

@@ -1419,11 +1419,15 @@ adasum_status_t adasum_get_last_error(void) {
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return ADASUM_ERR_CUDA;
   Workspace& ws = workspace_for(device);
-  if (ws.d_error == nullptr) return ADASUM_OK;
-  int h = 0;
-  if (cudaMemcpy(&h, ws.d_error, sizeof h, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(ws.d_error, 0, sizeof h) != cudaSuccess)
-    return ADASUM_ERR_CUDA;
+  int h = take_update_error();
+  if (h < 0) return ADASUM_ERR_CUDA;
+  if (ws.d_error != nullptr) {
+    int w = 0;
+    if (cudaMemcpy(&w, ws.d_error, sizeof w, cudaMemcpyDeviceToHost) != cudaSuccess ||
+        cudaMemset(ws.d_error, 0, sizeof w) != cudaSuccess)
+      return ADASUM_ERR_CUDA;
+    h |= w;
+  }
   if (h & kErrBounds) return ADASUM_ERR_BOUNDS;
   return h ? ADASUM_ERR_TIMEOUT : ADASUM_OK;
 }

@@ -78,6 +78,18 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
       : "memory");
 }
 
+// ------------------------------------------------------------------ counts in global memory
+
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+// (after what this thread has written, and what others wrote before a barrier it was at)
+__device__ __forceinline__ void add_release(int* p, int v) {
+  asm volatile("fence.acq_rel.gpu;\n red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
 // ------------------------------------------------------------------ dependent launch
 
 // First statement of every kernel of a call's chain.  The kernels are launched with

@@ -1,0 +1,955 @@
+// train_muon.cu -- orthogonalised updates: the Newton-Schulz iteration on the tensor cores,
+// and the step of momentum, iteration and weights that follows the combine.
+//
+// With X = G / |G| (m x n, m <= n; a taller matrix is laid out transposed) every step is
+//     A = X X',   B = b A + c A A,   X <- a X + B X,
+// three products, the first two of which are symmetric: only tiles that touch the lower
+// triangle are computed, and written to both places.
+//
+// Precision.  Operands are fp16, kept times a power of two so that what is far below a
+// matrix's largest values stays in the normal range; products accumulate in fp32.
+// Each step multiplies small singular values by a (3.4 in the usual iteration), and with them
+// the rounding errors of X that point into their directions: after five steps one rounding of
+// X to bf16 is 1e-2 to 1e-1 of the result's norm, to fp16 2e-3 to 2e-2 (random, power-law and
+// low-rank spectra).  So
+//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits), a product is three
+//     products of them (the fourth, of the low parts, is below 2^-22): off by 5e-7 to 5e-6,
+//     where fp32 throughout is off by 2e-6 to 2e-5;
+//   bf16 results: products of the high parts alone, but X itself in both parts for the term
+//     a X, where the growing errors would come from; the last two steps, whose errors no
+//     longer grow, take the rounded X there too, so that value and slope of the polynomial
+//     fit each other.  Off by 1.4e-3 at most, as much as the result's rounding to bf16.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <vector>
+
+#include "adasum_host.h"
+#include "adasum_launch.h"
+#include "adasum_train.cuh"
+#include "adasum_umma.cuh"
+
+namespace adasum {
+namespace {
+
+constexpr int kMaxBatch = 256;                    // matrices of one launch
+constexpr int64_t kChunkBytes = int64_t(1) << 30;  // scratch of a chunk of equal matrices, about
+constexpr float kScaleX = 8192.f, kScaleA = 8192.f, kScaleB = 4096.f;
+
+// What a wait that ran out leaves (adasum_get_last_error).
+__device__ int g_error;
+constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
+
+// ------------------------------------------------------------------ momentum and norms
+
+// Where a matrix's elements are: 2 * start + (1: transposed).
+struct Places {
+  int64_t at[kMaxBatch];
+};
+
+struct SourceArgs {
+  const void* x;       // the matrices, or the gradient
+  float* momentum;     // null: no momentum
+  int dtype;
+  int64_t rows, cols, ld;  // of a matrix as the caller has it, if not transposed
+  float mu;
+  int nesterov;
+  float* partials;     // [matrix][chunk][3]
+  int* ready;          // per matrix, to be zeroed
+  int chunks;
+  int64_t per_chunk;
+  float eps;
+  __half *hi, *lo;     // the first X
+  int64_t m, n, ldx;
+};
+
+// Sums of squares in three ranges, so that no magnitude that fp32 holds is lost: of the
+// values, of the values times 2^-64, and times 2^64.
+struct Squares {
+  float mid = 0.f, big = 0.f, small = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    mid = __fmaf_rn(x, x, mid);
+    const float b = x * 0x1p-64f, s = x * 0x1p64f;
+    big = __fmaf_rn(b, b, big);
+    small = __fmaf_rn(s, s, small);
+  }
+};
+
+// v <- mu v + g (with momentum), and the sums of squares of the update, per chunk.  Bound by
+// bytes.
+__global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const __grid_constant__ Places places) {
+  pdl_enter();
+  __shared__ float red[3][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t start = places.at[blockIdx.y] >> 1;
+  const int64_t lo = blockIdx.x * a.per_chunk, hi = min(lo + a.per_chunk, a.rows * a.cols);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.ready[blockIdx.y] = 0;
+  Squares s;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
+    int64_t at = start + i;
+    if (a.ld != a.cols) at = start + i / a.cols * a.ld + i % a.cols;
+    float u = load_any(a.x, a.dtype, at);
+    if (a.momentum) {
+      const float v = __fmaf_rn(a.mu, a.momentum[at], u);
+      a.momentum[at] = v;
+      u = a.nesterov ? __fmaf_rn(a.mu, v, u) : v;
+    }
+    s.add(u);
+  }
+  s.mid = warp_sum(s.mid);
+  s.big = warp_sum(s.big);
+  s.small = warp_sum(s.small);
+  if (lane == 0) red[0][warp] = s.mid, red[1][warp] = s.big, red[2][warp] = s.small;
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += red[threadIdx.x][i];
+    a.partials[(static_cast<int64_t>(blockIdx.y) * a.chunks + blockIdx.x) * 3 + threadIdx.x] = t;
+  }
+}
+
+__device__ __forceinline__ void split_store(__half* hi, __half* lo, int64_t at, float x) {
+  const __half h = __float2half_rn(x);
+  hi[at] = h;
+  lo[at] = __float2half_rn(x - __half2float(h));
+}
+
+// X = update / (|update| + eps), times kScaleX, as sums of two fp16; 64 x 64 tiles.
+__global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, const __grid_constant__ Places places) {
+  pdl_enter();
+  __shared__ float tile[64][65];
+  __shared__ float factors[2];
+  const int64_t place = places.at[blockIdx.z], start = place >> 1;
+  const bool transposed = place & 1;
+  if (threadIdx.x < 32) {
+    const float* p = a.partials + static_cast<int64_t>(blockIdx.z) * a.chunks * 3;
+    float s[3] = {0.f, 0.f, 0.f};
+    for (int i = threadIdx.x; i < a.chunks; i += 32)
+      for (int j = 0; j < 3; ++j) s[j] += p[i * 3 + j];
+    for (int j = 0; j < 3; ++j) s[j] = warp_sum(s[j]);
+    if (threadIdx.x == 0) {
+      // (the middle range between 2^-80 and 2^100; NaN takes the first branch's last case)
+      float pre = 1.f, norm;
+      if (s[0] > 0x1p100f) pre = 0x1p-64f, norm = sqrtf(s[1]) + a.eps * 0x1p-64f;
+      else if (s[0] < 0x1p-80f) pre = 0x1p64f, norm = sqrtf(s[2]) + a.eps * 0x1p64f;
+      else norm = sqrtf(s[0]) + a.eps;
+      factors[0] = pre;
+      factors[1] = norm > 0.f || norm != norm ? kScaleX / norm : 0.f;
+    }
+  }
+  __syncthreads();
+  const float pre = factors[0], factor = factors[1];
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  // rows and columns as the caller has them
+  const int64_t rows = transposed ? a.n : a.m, cols = transposed ? a.m : a.n;
+  const int64_t ld = a.momentum || a.ld == a.cols ? cols : a.ld;
+  const int64_t r0 = static_cast<int64_t>(transposed ? blockIdx.x : blockIdx.y) * 64;
+  const int64_t c0 = static_cast<int64_t>(transposed ? blockIdx.y : blockIdx.x) * 64;
+  for (int r = ty; r < 64; r += 4) {
+    if (r0 + r >= rows || c0 + tx >= cols) continue;
+    const int64_t at = start + (r0 + r) * ld + c0 + tx;
+    float u;
+    if (a.momentum) {
+      u = a.momentum[at];
+      if (a.nesterov) u = __fmaf_rn(a.mu, u, load_any(a.x, a.dtype, at));
+    } else {
+      u = load_any(a.x, a.dtype, at);
+    }
+    u = u * pre * factor;
+    if (transposed) tile[r][tx] = u;
+    else split_store(a.hi, a.lo, (static_cast<int64_t>(blockIdx.z) * a.m + r0 + r) * a.ldx + c0 + tx, u);
+  }
+  if (!transposed) return;
+  __syncthreads();
+  for (int c = ty; c < 64; c += 4)
+    if (c0 + c < cols && r0 + tx < rows)
+      split_store(a.hi, a.lo, (static_cast<int64_t>(blockIdx.z) * a.m + c0 + c) * a.ldx + r0 + tx, tile[tx][c]);
+}
+
+// ------------------------------------------------------------------------- products
+
+constexpr int kEpilogueWarps = 8;
+constexpr int kFlowThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kPitch = 33;  // floats between rows of a warp's 32 x 32 block in shared memory
+
+// What the iteration of equal matrices needs: the operands' maps (boxes of 64 x 64) and places,
+// the tiles of a product, where the results go.
+struct FlowArgs {
+  CUtensorMap x_map[2][2], a_map[2], b_map[2];  // [buffer][part], [part]
+  __half *x[2][2], *a[2], *b[2];
+  int64_t ldx, lda;
+  int m, n, batch, steps;
+  int col_tiles[2], tiles[2];  // of A and B (lower triangle), of X
+  int* ready;                  // per matrix: warps that have written their part of a tile
+  int last;                    // 1: results to `dest`, 2: weights there are moved
+  void* dest;
+  int dest_dtype;
+  float keep, step[2];         // weights: w <- keep w - step x (of a matrix as it is, transposed)
+  float coefficients[3 * ADASUM_NEWTON_SCHULZ_MAX_STEPS];
+};
+
+// Tiles are 128 * CTAS x NT: CTAS = 2 CTAs (a cluster) share one, each with 128 of its rows, and
+// each copies its rows of the left operand and its half of the columns of the right one.
+// TERMS = 3: products of sums of two parts.  Their accumulators: the high parts' product in runs
+// of kRun along the depth, each drained and added in fp32 registers, since the tensor cores cut
+// sums off towards zero (one run of 4096 left 1.4e-5 of 4 matrices of 1024 x 4096 after five
+// steps); beside it, for the whole depth, the two products with a low part.
+template <int CTAS, int NT, int TERMS>
+struct FlowShape {
+  static constexpr int kHeight = 128 * CTAS;
+  static constexpr int kParts = TERMS == 3 ? 2 : 1;
+  static constexpr int kQRows = NT / CTAS;                           // of the right operand, of one CTA
+  static constexpr int kPBytes = 128 * 128, kQBytes = kQRows * 128;  // of one part: 64 along the depth
+  static constexpr int kStageBytes = kParts * (kPBytes + kQBytes);
+  static constexpr int kStages = 196608 / kStageBytes < 6 ? 196608 / kStageBytes : 6;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * 32 * kPitch * 4;
+  static_assert(kSmem + 1024 <= 232448, "with the barriers, a CTA's shared memory");
+  static constexpr int kBuffers = NT == 256 && TERMS == 3 ? 1 : 2;  // accumulators of the high parts
+  static constexpr int kCross = kBuffers * NT;                       // column of the others'
+  static constexpr int kUsed = kCross + (TERMS == 3 ? NT : 0);
+  static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static constexpr int kRun = TERMS == 3 ? 8 : 1 << 30;  // stages of 64
+  static constexpr int kBlocks = NT / 64;                // of 32 x 32, of an epilogue warp
+};
+
+// Row tile r of a symmetric product has the column tiles up to the diagonal.
+__host__ __device__ constexpr int sym_tiles(int r, int height, int nt) { return (r * height + height - 1) / nt + 1; }
+
+enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
+
+struct Tile {
+  int step, kind, matrix, row, col;  // row and column of the result where it starts
+};
+
+// All steps of the iteration in one launch of co-resident CTAs.  The tiles (128 x NT of one
+// product of one matrix) of all products lie in one sequence, product after product, and CTAs
+// take them in turn.  A tile needs its matrix's previous product whole, and nothing else: a
+// count per matrix of what has been written tells.  Every tile waits only for tiles before it
+// in the sequence, which CTAs take in order, so all waits end; and where there are several
+// matrices the products of one fill the SMs while another's last tiles finish.
+// A warp copies (TMA), a thread issues the products, eight warps take finished accumulators
+// out of TMEM.
+template <int CTAS, int NT, int TERMS>
+__global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_constant__ FlowArgs a, const __grid_constant__ Places places) {
+  using S = FlowShape<CTAS, NT, TERMS>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], cross_empty;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int stop;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], kEpilogueWarps * CTAS);
+    mbar_init(&cross_empty, kEpilogueWarps * CTAS);
+    mbar_fence_init();
+    stop = 0;
+  }
+  if (warp == 1) tmem_alloc<S::kCols, CTAS>(&tmem_slot);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CTAS > 1) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;  // of this cluster's tiles
+  const int per_step = a.batch * (2 * a.tiles[0] + a.tiles[1]), total = a.steps * per_step;
+  auto give_up = [&] {
+    if (!stop) atomicOr(&g_error, 2);
+    stop = 1;
+    return false;
+  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait_pair<CTAS>(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait_pair<CTAS>(bar, parity))
+      if (stop || clock64() - t0 > kWaitCycles) return give_up();
+    return true;
+  };
+  // until the products of its matrix before this tile's are written
+  auto wait_ready = [&](const Tile& t) {
+    const int need = kEpilogueWarps * CTAS * (t.step * (2 * a.tiles[0] + a.tiles[1]) + t.kind * a.tiles[0]);
+    if (load_acquire(a.ready + t.matrix) >= need) return true;
+    const long long t0 = clock64();
+    while (load_acquire(a.ready + t.matrix) < need) {
+      if (stop || clock64() - t0 > kWaitCycles) return give_up();
+      __nanosleep(32);
+    }
+    return true;
+  };
+  auto locate = [&](int t) {
+    Tile w;
+    w.step = t / per_step;
+    int r = t - w.step * per_step;
+    const int sym = a.batch * a.tiles[0];
+    w.kind = r < sym ? kGram : r < 2 * sym ? kPoly : kApply;
+    r -= w.kind * sym;
+    if (w.kind == kApply) {
+      w.matrix = r / a.tiles[1];
+      r -= w.matrix * a.tiles[1];
+      const int i = r / a.col_tiles[1];
+      w.row = i * S::kHeight;
+      w.col = (r - i * a.col_tiles[1]) * NT;
+    } else {
+      w.matrix = r / a.tiles[0];
+      r -= w.matrix * a.tiles[0];
+      int i = 0;
+      for (int n; r >= (n = min(sym_tiles(i, S::kHeight, NT), a.col_tiles[0])); ++i) r -= n;
+      w.row = i * S::kHeight;
+      w.col = r * NT;
+    }
+    return w;
+  };
+  auto depth = [&](const Tile& t) { return (((t.kind == kGram ? a.n : a.m)) + 63) / 64; };
+  int issued = 0;  // whole stages whose copies this thread began
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      for (int at = first; ok && at < total; at += stride) {
+        const Tile t = locate(at);
+        if (!(ok = wait_ready(t))) break;
+        fence_proxy_async();
+        const int ks = depth(t);
+        const CUtensorMap* p = t.kind == kGram ? a.x_map[t.step & 1] : t.kind == kPoly ? a.a_map : a.b_map;
+        const CUtensorMap* q = t.kind == kPoly ? a.a_map : a.x_map[t.step & 1];
+        for (int k = 0; k < ks; ++k, ++issued) {
+          const int s = issued % S::kStages;
+          if (!(ok = wait(&empty[s], ((issued / S::kStages) & 1) ^ 1))) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * S::kStageBytes);
+          const uint32_t bar = first_of_pair<CTAS>(smem_addr(&full[s]));
+          uint32_t to = smem_addr(stages) + s * S::kStageBytes;
+#pragma unroll
+          for (int part = 0; part < S::kParts; ++part)
+#pragma unroll
+            for (int h = 0; h < 2; ++h, to += 8192) tma_load3<CTAS>(to, p + part, bar, k * 64, t.row + rank * 128 + h * 64, t.matrix);
+#pragma unroll
+          for (int part = 0; part < S::kParts; ++part)
+#pragma unroll
+            for (int h = 0; h < S::kQRows / 64; ++h, to += 8192) {
+              const int c = t.col + rank * S::kQRows + h * 64;
+              tma_load3<CTAS>(to, q + part, bar, t.kind == kApply ? c : k * 64, t.kind == kApply ? k * 64 : c, t.matrix);
+            }
+        }
+      }
+      // every stage consumed: no arrival is on its way to a CTA that has left
+      for (int i = max(0, issued - S::kStages); ok && i < issued; ++i) ok = wait(&empty[i % S::kStages], (i / S::kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int it = 0, acc = 0, tiles = 0;
+      bool ok = true;
+      for (int at = first; ok && at < total; at += stride, ++tiles) {
+        const Tile t = locate(at);
+        const int ks = depth(t);
+        const bool mn = t.kind == kApply;
+        const uint32_t idesc = mn ? umma_idesc(CTAS, NT, true) : umma_idesc(CTAS, NT, false);
+        const uint64_t q_block = mn ? 8192 : 16, q_step = mn ? 128 : 2;
+        for (int k = 0; k < ks; ++k, ++it) {
+          const int s = it % S::kStages, buffer = acc % S::kBuffers;
+          const bool fresh = k % S::kRun == 0;  // the first of a run
+          if (!(ok = wait(&full[s], (it / S::kStages) & 1))) break;
+          tc_fence_after();
+          const uint32_t base = smem_addr(stages) + s * S::kStageBytes, qbase = base + S::kParts * S::kPBytes;
+          auto multiply = [&](int p_part, int q_part, uint32_t d, bool clear) {
+            const uint64_t p = umma_desc(base + p_part * S::kPBytes, 16), q = umma_desc(qbase + q_part * S::kQBytes, q_block);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) umma_f16<CTAS>(d, p + e * 2, q + e * q_step, idesc, !clear || e > 0);
+          };
+          if constexpr (TERMS == 3) {  // (these while the last run is drained)
+            if (k == 0) {
+              if (!(ok = wait(&cross_empty, (tiles & 1) ^ 1))) break;
+              tc_fence_after();
+            }
+            multiply(0, 1, tmem + S::kCross, k == 0);
+            multiply(1, 0, tmem + S::kCross, false);
+          }
+          if (fresh) {
+            if (!(ok = wait(&acc_empty[buffer], ((acc / S::kBuffers) & 1) ^ 1))) break;
+            tc_fence_after();
+          }
+          multiply(0, 0, tmem + buffer * NT, fresh);
+          umma_commit<CTAS>(&empty[s]);
+          if (k + 1 == ks || (k + 1) % S::kRun == 0) {
+            umma_commit<CTAS>(&acc_full[buffer]);
+            ++acc;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    float* block = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes) + (warp - 2) * 32 * kPitch;
+    const int sub = lane >> 2, oct = (lane & 3) * 8;  // of eight rows and four groups of columns
+    int acc = 0;
+    for (int at = first; at < total; at += stride) {
+      const Tile t = locate(at);
+      const bool apply = t.kind == kApply, last_step = t.step + 1 == a.steps;
+      // parts of X in the linear term of this step and of the next (the file's comment)
+      const int in_parts = TERMS == 3 || (apply && t.step + 2 < a.steps) ? 2 : 1;
+      const int out_parts = TERMS == 3 || (apply && t.step + 3 < a.steps) ? 2 : 1;
+      const float c_a = a.coefficients[3 * t.step], c_b = a.coefficients[3 * t.step + 1], c_c = a.coefficients[3 * t.step + 2];
+      const float scale = t.kind == kGram   ? kScaleA / (kScaleX * kScaleX)
+                          : t.kind == kPoly ? c_c * (kScaleB / (kScaleA * kScaleA))
+                                            : 1.f / kScaleB;
+      const float in_scale = apply ? c_a : c_b * (kScaleB / kScaleA);
+      __half* const* in = apply ? a.x[t.step & 1] : a.a;
+      __half* const* out = apply ? a.x[(t.step & 1) ^ 1] : t.kind == kGram ? a.a : a.b;
+      const int64_t ld = apply ? a.ldx : a.lda, base = static_cast<int64_t>(t.matrix) * a.m * ld;
+      const int cols = apply ? a.n : a.m, i0 = t.row + rank * 128 + quarter * 32;
+      auto column = [&](int k) { return t.col + (half + 2 * k) * 32; };
+      auto there = [&](int k) { return i0 < a.m && column(k) < cols && (apply || column(k) <= i0); };
+      // what is added, of block k: four rows' eight columns of each lane
+      struct Added {
+        uint4 part[2][4];
+      };
+      auto fetch = [&](int k, Added& f) {
+        if (t.kind == kGram || k >= S::kBlocks || !there(k)) return;
+        const int c = column(k) + oct;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = i0 + r * 8 + sub;
+          const int64_t from = base + i * ld + c;
+          const bool on = i < a.m && c < cols;
+          f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(in[0] + from)) : make_uint4(0, 0, 0, 0);
+          f.part[1][r] = on && in_parts == 2 ? __ldcg(reinterpret_cast<const uint4*>(in[1] + from)) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      auto finish = [&](int k, const float (&v)[32], const Added& f) {
+        const int j0 = column(k);
+        __syncwarp();  // the last block has been read
+#pragma unroll
+        for (int c = 0; c < 32; ++c) block[lane * kPitch + c] = v[c];
+        __syncwarp();
+        auto put = [&](int64_t to, const float (&x)[8]) {
+          uint4 h, l;
+          uint32_t* hw = &h.x;
+          uint32_t* lw = &l.x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 p = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+            const float2 w = __half22float2(p);
+            const __half2 rest = __floats2half2_rn(x[2 * e] - w.x, x[2 * e + 1] - w.y);
+            hw[e] = *reinterpret_cast<const uint32_t*>(&p);
+            lw[e] = *reinterpret_cast<const uint32_t*>(&rest);
+          }
+          *reinterpret_cast<uint4*>(out[0] + to) = h;
+          if (out_parts == 2) *reinterpret_cast<uint4*>(out[1] + to) = l;
+        };
+        const bool mirror = !apply && j0 < i0, final = apply && last_step;
+        // (a row's last eight columns may reach into its padding)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = i0 + r * 8 + sub;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = block[(r * 8 + sub) * kPitch + oct + e] * scale;
+          if (t.kind != kGram) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const uint32_t* w = &f.part[part][r].x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(w + e));
+                x[2 * e] = __fmaf_rn(in_scale, y.x, x[2 * e]);
+                x[2 * e + 1] = __fmaf_rn(in_scale, y.y, x[2 * e + 1]);
+              }
+            }
+          }
+          if (mirror || final) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) block[(r * 8 + sub) * kPitch + oct + e] = x[e];
+          }
+          if (!final && i < a.m && j0 + oct < cols) put(base + i * ld + j0 + oct, x);
+        }
+        if (mirror) {
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = j0 + r * 8 + sub;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = block[(oct + e) * kPitch + r * 8 + sub];
+            if (j < cols && i0 + oct < a.m) put(base + j * ld + i0 + oct, x);
+          }
+        }
+        if (final) {
+          __syncwarp();
+          const int64_t place = places.at[t.matrix], start = place >> 1;
+          const bool transposed = place & 1;
+          const float step = a.step[transposed];
+#pragma unroll 8
+          for (int r = 0; r < 32; ++r) {
+            const int i = i0 + (transposed ? lane : r), j = j0 + (transposed ? r : lane);
+            if (i >= a.m || j >= cols) continue;
+            const float x = (transposed ? block[lane * kPitch + r] : block[r * kPitch + lane]) * (1.f / kScaleX);
+            const int64_t to = start + (transposed ? static_cast<int64_t>(j) * a.m + i : static_cast<int64_t>(i) * cols + j);
+            if (a.last == 2) {
+              float* w = static_cast<float*>(a.dest) + to;
+              *w = __fmaf_rn(-step, x, a.keep * *w);
+            } else {
+              store_any(a.dest, a.dest_dtype, to, x);
+            }
+          }
+        }
+      };
+      bool ok = true;
+      if (lane == 0) ok = wait_ready(t);
+      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
+      auto release = [&](uint64_t* bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at<CTAS>(first_of_pair<CTAS>(smem_addr(bar)));
+      };
+      if constexpr (TERMS == 1) {
+        const int buffer = acc % S::kBuffers;
+        Added now, next;
+        fetch(0, next);
+        if (!wait(&acc_full[buffer], (acc / S::kBuffers) & 1)) break;
+        ++acc;
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = 0; k < S::kBlocks; ++k) {
+          now = next;
+          fetch(k + 1, next);
+          if (!there(k)) continue;
+          float v[32];
+          tmem_load32(from + buffer * NT + k * 64, v);
+          finish(k, v, now);
+        }
+        release(&acc_empty[buffer]);
+      } else {
+        float v[S::kBlocks][32];
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[k][c] = 0.f;
+        const int ks = depth(t);
+        for (int run = 0; ok && run < ks; run += S::kRun, ++acc) {
+          const int buffer = acc % S::kBuffers;
+          if (!(ok = wait(&acc_full[buffer], (acc / S::kBuffers) & 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k) {
+            if (!there(k)) continue;
+            tmem_add16(from + buffer * NT + k * 64, v[k]);
+            tmem_add16(from + buffer * NT + k * 64 + 16, v[k] + 16);
+          }
+          release(&acc_empty[buffer]);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k) {
+          if (!there(k)) continue;
+          tmem_add16(from + S::kCross + k * 64, v[k]);
+          tmem_add16(from + S::kCross + k * 64 + 16, v[k] + 16);
+        }
+        release(&cross_empty);
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k) {
+          if (!there(k)) continue;
+          Added f;
+          fetch(k, f);
+          finish(k, v[k], f);
+        }
+      }
+      // what this warp wrote is there, for others' copies too
+      if (!(apply && last_step)) {
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) add_release(a.ready + t.matrix, 1);
+      }
+    }
+  }
+  if (warp == 0 && lane == 0 && stop) {  // copies still in flight
+    for (int i = max(0, issued - S::kStages); rank == 0 && i < issued; ++i) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&full[i % S::kStages], (i / S::kStages) & 1) && clock64() - t0 < kWaitCycles) {
+      }
+    }
+    const long long t0 = clock64();  // (a pair's second CTA cannot see its copies' barrier)
+    while (clock64() - t0 < kWaitCycles / 1000) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CTAS > 1) cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_free<S::kCols, CTAS>(tmem);
+}
+
+// ----------------------------------------------------------------------- host side
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return f;
+}
+
+// Boxes of 64 x 64 of `batch` matrices of rows x cols fp16, their rows ld apart.
+bool make_map(CUtensorMap* map, const __half* p, int64_t rows, int64_t cols, int64_t ld, int64_t batch) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * 2};
+  const cuuint32_t box[3] = {64, 64, 1}, ones[3] = {1, 1, 1};
+  return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides, box, ones,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Matrices of one shape m x n (m <= n) that are iterated together, and where their parts lie
+// in the scratch memory.
+struct ScratchMap {
+  int64_t m, n, ldx, lda;
+  int64_t x[2][2], a[2], b[2], partials, ready, bytes;
+  int chunks;
+  int64_t per_chunk;
+  ScratchMap(int64_t m_, int64_t n_, int64_t batch, bool fine) : m(m_), n(n_), ldx(round_up(n_, 8)), lda(round_up(m_, 8)) {
+    int64_t at = 0;
+    auto take = [&](int64_t count) {
+      const int64_t here = at;
+      at += round_up(count, 256);
+      return here;
+    };
+    for (int i = 0; i < 2; ++i)
+      for (int part = 0; part < 2; ++part) x[i][part] = take(batch * m * ldx * 2);
+    for (int part = 0; part < 2; ++part) {
+      a[part] = part == 0 || fine ? take(batch * m * lda * 2) : 0;
+      b[part] = part == 0 || fine ? take(batch * m * lda * 2) : 0;
+    }
+    per_chunk = 16384;
+    while ((m * n + per_chunk - 1) / per_chunk > 1024) per_chunk *= 2;
+    chunks = static_cast<int>((m * n + per_chunk - 1) / per_chunk);
+    partials = take(batch * chunks * 3 * 4);
+    ready = take(batch * 4);
+    bytes = at;
+  }
+};
+// Matrices of a chunk: what about a gigabyte of scratch holds, as even as possible.
+int64_t chunk_of(int64_t m, int64_t n, int64_t count, bool fine) {
+  const int64_t one = ScratchMap(m, n, 1, fine).bytes;
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxBatch, kChunkBytes / one));
+  const int64_t chunks = (count + most - 1) / most;
+  return (count + chunks - 1) / chunks;
+}
+
+struct Iteration {
+  int steps;
+  const float* coefficients;
+  float eps;
+};
+struct Result {
+  int last;  // as in FlowArgs
+  void* dest;
+  int dtype;
+  float keep, step[2];
+};
+
+int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
+  const int64_t row_tiles = (rows + height - 1) / height, col_tiles = (cols + nt - 1) / nt;
+  if (!sym) return row_tiles * col_tiles;
+  int64_t tiles = 0;
+  for (int64_t r = 0; r < row_tiles; ++r) tiles += std::min<int64_t>(sym_tiles(static_cast<int>(r), height, nt), col_tiles);
+  return tiles;
+}
+// CTAs and columns of a tile: those whose waves over the SMs take least.  A tile costs its
+// columns and about 32 columns' time beside them; single CTAs copy half as much again for
+// the same product.
+struct TileSize {
+  int ctas, nt;
+};
+TileSize tile_size(int64_t m, int64_t n, int64_t batch) {
+  TileSize best = {2, 256};
+  double least = 1e300;
+  for (const TileSize s : {TileSize{2, 256}, TileSize{1, 128}, TileSize{1, 64}}) {
+    const int64_t units = sm_count() / s.ctas;
+    auto waves = [&](int64_t tiles) { return static_cast<double>((tiles * batch + units - 1) / units); };
+    const int64_t sym = count_tiles(m, m, 128 * s.ctas, s.nt, true), gen = count_tiles(m, n, 128 * s.ctas, s.nt, false);
+    const double cost = (waves(sym) * static_cast<double>(n + m) + waves(gen) * static_cast<double>(m)) * (s.nt + 32) * (s.ctas == 2 ? 1.0 : 1.5);
+    if (cost < least) least = cost, best = s;
+  }
+  return best;
+}
+
+template <int CTAS, int NT, int TERMS>
+int launch_flow_as(FlowArgs& a, const Places& places, cudaStream_t stream) {
+  using S = FlowShape<CTAS, NT, TERMS>;
+  static SmemAllowed allowed;
+  if (int rc = allow_smem(flow_kernel<CTAS, NT, TERMS>, S::kSmem, allowed)) return rc;
+  a.col_tiles[0] = (a.m + NT - 1) / NT;
+  a.col_tiles[1] = (a.n + NT - 1) / NT;
+  a.tiles[0] = static_cast<int>(count_tiles(a.m, a.m, S::kHeight, NT, true));
+  a.tiles[1] = static_cast<int>(count_tiles(a.m, a.n, S::kHeight, NT, false));
+  const int64_t most = static_cast<int64_t>(a.batch) * std::max(a.tiles[0], a.tiles[1]);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, sm_count() / CTAS) * CTAS));
+  cfg.blockDim = dim3(kFlowThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;  // (all CTAs resident, as they wait for each other)
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CTAS > 1 ? 2 : 1;
+  return static_cast<int>(cudaLaunchKernelEx(&cfg, flow_kernel<CTAS, NT, TERMS>, static_cast<const FlowArgs&>(a), places));
+}
+template <int TERMS>
+int launch_flow(FlowArgs& a, const Places& places, TileSize s, cudaStream_t stream) {
+  if (s.ctas == 2) return launch_flow_as<2, 256, TERMS>(a, places, stream);
+  if (s.nt == 128) return launch_flow_as<1, 128, TERMS>(a, places, stream);
+  return launch_flow_as<1, 64, TERMS>(a, places, stream);
+}
+
+// Iterates `batch` matrices of one shape, which are at `from`; the results go to `places`.
+adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places, int64_t m, int64_t n, int batch, bool fine,
+                        const Iteration& it, const Result& res, char* scratch, cudaStream_t stream) {
+  const ScratchMap l(m, n, batch, fine);
+  FlowArgs f = {};
+  bool ok = true;
+  for (int part = 0; part < 2; ++part) {
+    for (int i = 0; i < 2; ++i) {
+      f.x[i][part] = reinterpret_cast<__half*>(scratch + l.x[i][part]);
+      ok = ok && make_map(&f.x_map[i][part], f.x[i][part], m, n, l.ldx, batch);
+    }
+    if (part > 0 && !fine) continue;
+    f.a[part] = reinterpret_cast<__half*>(scratch + l.a[part]);
+    f.b[part] = reinterpret_cast<__half*>(scratch + l.b[part]);
+    ok = ok && make_map(&f.a_map[part], f.a[part], m, m, l.lda, batch) && make_map(&f.b_map[part], f.b[part], m, m, l.lda, batch);
+  }
+  if (!ok) return ADASUM_ERR_CUDA;
+  f.ldx = l.ldx;
+  f.lda = l.lda;
+  f.m = static_cast<int>(m);
+  f.n = static_cast<int>(n);
+  f.batch = batch;
+  f.steps = it.steps;
+  f.ready = reinterpret_cast<int*>(scratch + l.ready);
+  f.last = res.last;
+  f.dest = res.dest;
+  f.dest_dtype = res.dtype;
+  f.keep = res.keep;
+  std::copy(res.step, res.step + 2, f.step);
+  std::copy(it.coefficients, it.coefficients + 3 * it.steps, f.coefficients);
+  src.partials = reinterpret_cast<float*>(scratch + l.partials);
+  src.ready = f.ready;
+  src.chunks = l.chunks;
+  src.per_chunk = l.per_chunk;
+  src.eps = it.eps;
+  src.hi = f.x[0][0];
+  src.lo = f.x[0][1];
+  src.m = m;
+  src.n = n;
+  src.ldx = l.ldx;
+  const double elements = static_cast<double>(m) * n * batch, e = dtype_bytes(src.dtype);
+  adasum_status_t st = counted_launch(stream, "update_squares", elements * (e + (src.momentum ? 8 : 0)), [&] {
+    return launch_pdl(squares_kernel, dim3(l.chunks, batch), dim3(256), 0, stream, src, from);
+  });
+  if (st) return st;
+  st = counted_launch(stream, "update_normalize", elements * (e + (src.momentum ? 4 : 0) + 4), [&] {
+    return launch_pdl(normalize_kernel, dim3(static_cast<unsigned>((n + 63) / 64), static_cast<unsigned>((m + 63) / 64), batch),
+                      dim3(256), 0, stream, src, from);
+  });
+  if (st) return st;
+  const TileSize size = tile_size(m, n, batch);
+  return counted_launch(stream, fine ? "update_iterate3" : "update_iterate", 0.0, [&] {
+    return fine ? launch_flow<3>(f, places, size, stream) : launch_flow<1>(f, places, size, stream);
+  });
+}
+
+adasum_status_t check_iteration(int steps, const float* coefficients, float eps) {
+  if (steps < 1 || coefficients == nullptr || !(eps >= 0.f)) return ADASUM_ERR_INVALID_ARG;
+  if (steps > ADASUM_NEWTON_SCHULZ_MAX_STEPS) return ADASUM_ERR_UNSUPPORTED;
+  for (int i = 0; i < 3 * steps; ++i)
+    if (!std::isfinite(coefficients[i])) return ADASUM_ERR_INVALID_ARG;
+  return ADASUM_OK;
+}
+
+// Matrices whose shapes agree once the taller ones are transposed; `members` in their order.
+struct Group {
+  int64_t m, n;
+  std::vector<int> members;
+};
+std::vector<Group> group_shapes(const int64_t* rows, const int64_t* cols, int L) {
+  std::vector<int> order;
+  for (int s = 0; s < L; ++s)
+    if (rows[s] > 0 && cols[s] > 0) order.push_back(s);
+  auto m = [&](int s) { return std::min(rows[s], cols[s]); };
+  auto n = [&](int s) { return std::max(rows[s], cols[s]); };
+  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return m(a) != m(b) ? m(a) > m(b) : n(a) > n(b); });
+  std::vector<Group> groups;
+  for (int s : order) {
+    if (groups.empty() || groups.back().m != m(s) || groups.back().n != n(s)) groups.push_back(Group{m(s), n(s), {}});
+    groups.back().members.push_back(s);
+  }
+  return groups;
+}
+
+bool fits(int64_t rows, int64_t cols) { return rows <= ADASUM_NEWTON_SCHULZ_MAX_DIM && cols <= ADASUM_NEWTON_SCHULZ_MAX_DIM; }
+
+}  // namespace
+
+int take_update_error() {
+  int h = 0;
+  const int zero = 0;
+  if (cudaMemcpyFromSymbol(&h, g_error, sizeof h) != cudaSuccess) return -1;
+  if (h != 0 && cudaMemcpyToSymbol(g_error, &zero, sizeof zero) != cudaSuccess) return -1;
+  return h;
+}
+
+}  // namespace adasum
+
+using namespace adasum;
+
+extern "C" {
+
+int64_t adasum_orthogonalize_scratch_bytes(int64_t batch, int64_t rows, int64_t cols, adasum_dtype_t dtype) {
+  if (batch < 1 || rows < 1 || cols < 1 || !fits(rows, cols)) return 0;
+  const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
+  const bool fine = dtype == ADASUM_F32;
+  return ScratchMap(m, n, chunk_of(m, n, batch, fine), fine).bytes;
+}
+
+adasum_status_t adasum_orthogonalize(const void* x, int64_t batch, int64_t rows, int64_t cols, int64_t batch_stride, int64_t ld,
+                                     adasum_dtype_t dtype, int steps, const float* coefficients, float eps, void* out,
+                                     void* scratch, int64_t scratch_bytes, adasum_stream_t stream_) {
+  EntryScope scope("adasum_orthogonalize");
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (batch < 0 || rows < 0 || cols < 0 || !valid_dtype(dtype)) return ADASUM_ERR_INVALID_ARG;
+  if (adasum_status_t st = check_iteration(steps, coefficients, eps)) return st;
+  if (!fits(rows, cols)) return ADASUM_ERR_UNSUPPORTED;
+  if (batch == 0 || rows == 0 || cols == 0) return ADASUM_OK;
+  const int64_t e = dtype_bytes(dtype);
+  if (x == nullptr || out == nullptr || !valid_ld(rows, cols, ld) || (batch > 1 && batch_stride < (rows - 1) * ld + cols))
+    return ADASUM_ERR_INVALID_ARG;
+  if (batch > INT64_MAX / 64 / (rows * cols) || (batch > 1 && batch_stride > INT64_MAX / 64 / batch)) return ADASUM_ERR_UNSUPPORTED;
+  const int64_t need = adasum_orthogonalize_scratch_bytes(batch, rows, cols, dtype);
+  if (scratch == nullptr || scratch_bytes < need || !is_aligned(scratch, 256)) return ADASUM_ERR_INVALID_ARG;
+  BufferSet set;
+  set.read(x, ((batch - 1) * batch_stride + (rows - 1) * ld + cols) * e, e);
+  set.write(out, batch * rows * cols * e, e);
+  set.write(scratch, need, 256);
+  if (adasum_status_t st = set.check()) return st;
+  if (encode_tiled() == nullptr) return ADASUM_ERR_CUDA;
+  const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
+  const bool fine = dtype == ADASUM_F32, transposed = rows > cols;
+  const int64_t chunk = chunk_of(m, n, batch, fine);
+  for (int64_t b0 = 0; b0 < batch; b0 += chunk) {
+    const int count = static_cast<int>(std::min(chunk, batch - b0));
+    Places from = {}, to = {};
+    for (int i = 0; i < count; ++i) {
+      from.at[i] = 2 * i * batch_stride + transposed;
+      to.at[i] = 2 * i * rows * cols + transposed;
+    }
+    SourceArgs src = {};
+    src.x = static_cast<const char*>(x) + b0 * batch_stride * e;
+    src.dtype = dtype;
+    src.rows = rows;
+    src.cols = cols;
+    src.ld = ld;
+    Result res = {1, static_cast<char*>(out) + b0 * rows * cols * e, static_cast<int>(dtype), 0.f, {0.f, 0.f}};
+    if (adasum_status_t st = iterate(src, from, to, m, n, count, fine, {steps, coefficients, eps}, res, static_cast<char*>(scratch), stream))
+      return st;
+  }
+  return ADASUM_OK;
+}
+
+int64_t adasum_muon_step_scratch_bytes(const int64_t* rows, const int64_t* cols, int L) {
+  if (rows == nullptr || cols == nullptr || L < 1) return 0;
+  for (int s = 0; s < L; ++s)
+    if (!fits(rows[s], cols[s])) return 0;
+  try {
+    int64_t most = 0;
+    for (const Group& g : group_shapes(rows, cols, L))
+      most = std::max(most, ScratchMap(g.m, g.n, chunk_of(g.m, g.n, static_cast<int64_t>(g.members.size()), true), true).bytes);
+    return most;
+  } catch (...) {  // (out of host memory)
+    return -1;
+  }
+}
+
+adasum_status_t adasum_muon_step(const void* grad, adasum_dtype_t dtype, const int64_t* seg_offsets, const int64_t* rows,
+                                 const int64_t* cols, int L, float* master_w, float* momentum, float lr, float mu, int nesterov,
+                                 float weight_decay, adasum_muon_scale_t scale, int steps, const float* coefficients, float eps,
+                                 void* scratch, int64_t scratch_bytes, adasum_stream_t stream_) {
+  EntryScope scope("adasum_muon_step");
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (L < 0 || seg_offsets == nullptr || !valid_dtype(dtype) || scale < ADASUM_MUON_SCALE_NONE || scale > ADASUM_MUON_SCALE_RMS)
+    return ADASUM_ERR_INVALID_ARG;
+  if (adasum_status_t st = check_iteration(steps, coefficients, eps)) return st;
+  if (seg_offsets[0] != 0 || (L > 0 && (rows == nullptr || cols == nullptr))) return ADASUM_ERR_INVALID_ARG;
+  for (int s = 0; s < L; ++s) {
+    if (seg_offsets[s + 1] < seg_offsets[s] || rows[s] < 0 || cols[s] < 0) return ADASUM_ERR_INVALID_ARG;
+    if (rows[s] == 0 || cols[s] == 0) continue;
+    if (!fits(rows[s], cols[s])) return ADASUM_ERR_UNSUPPORTED;
+    if (rows[s] * cols[s] != seg_offsets[s + 1] - seg_offsets[s]) return ADASUM_ERR_INVALID_ARG;
+  }
+  const int64_t N = seg_offsets[L];
+  if (N > INT64_MAX / 64) return ADASUM_ERR_UNSUPPORTED;
+  const int64_t need = adasum_muon_step_scratch_bytes(rows, cols, L);
+  if (need < 0) return ADASUM_ERR_NO_MEMORY;
+  if (need == 0) return ADASUM_OK;  // no matrices
+  if (grad == nullptr || master_w == nullptr || momentum == nullptr || scratch == nullptr || scratch_bytes < need ||
+      !is_aligned(scratch, 256))
+    return ADASUM_ERR_INVALID_ARG;
+  const int64_t e = dtype_bytes(dtype);
+  BufferSet set;
+  set.read(grad, N * e, e);
+  set.write(master_w, N * 4, 4);
+  set.write(momentum, N * 4, 4);
+  set.write(scratch, need, 256);
+  if (adasum_status_t st = set.check()) return st;
+  if (encode_tiled() == nullptr) return ADASUM_ERR_CUDA;
+  try {
+    for (const Group& g : group_shapes(rows, cols, L)) {
+      const int64_t all = static_cast<int64_t>(g.members.size()), chunk = chunk_of(g.m, g.n, all, true);
+      for (int64_t b0 = 0; b0 < all; b0 += chunk) {
+        const int count = static_cast<int>(std::min(chunk, all - b0));
+        Places places = {};
+        for (int i = 0; i < count; ++i) {
+          const int s = g.members[b0 + i];
+          places.at[i] = 2 * seg_offsets[s] + (rows[s] > cols[s]);
+        }
+        SourceArgs src = {};
+        src.x = grad;
+        src.momentum = momentum;
+        src.dtype = dtype;
+        src.rows = g.m;
+        src.cols = src.ld = g.n;
+        src.mu = mu;
+        src.nesterov = nesterov != 0;
+        // the step of a wide matrix (rows <= cols), and of a tall one
+        const double wide = scale == ADASUM_MUON_SCALE_RMS ? 0.2 * std::sqrt(static_cast<double>(g.n)) : 1.0;
+        const double tall = scale == ADASUM_MUON_SCALE_SPECTRAL ? std::sqrt(static_cast<double>(g.n) / static_cast<double>(g.m)) : wide;
+        const Result res = {2, master_w, kF32, static_cast<float>(1.0 - static_cast<double>(lr) * weight_decay),
+                            {static_cast<float>(lr * wide), static_cast<float>(lr * tall)}};
+        if (adasum_status_t st = iterate(src, places, places, g.m, g.n, count, true, {steps, coefficients, eps}, res,
+                                         static_cast<char*>(scratch), stream))
+          return st;
+      }
+    }
+  } catch (...) {
+    return ADASUM_ERR_NO_MEMORY;
+  }
+  return ADASUM_OK;
+}
+
+}  // extern "C"

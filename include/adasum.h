@@ -469,6 +469,78 @@ ADASUM_API adasum_status_t adasum_gelu_checkpointed_backward(
     int64_t cols, adasum_dtype_t dtype, int tanh_form, void *grad_x, void *y,
     adasum_stream_t stream);
 
+/* ---- Orthogonalised updates ------------------------------------------------------- */
+
+/*
+ * The update of a matrix G of rows x cols by its nearly orthogonal factor, as the Muon
+ * optimiser takes it: X = G / (|G| + eps) with the Frobenius norm, then for every step, with
+ * that step's coefficients (a, b, c),
+ *     A = X X',   X <- a X + (b A + c A A) X
+ * (for rows > cols the same of the transposed matrix).  Every singular value s of X becomes
+ * a s + b s^3 + c s^5; coefficients are the caller's, and have to keep the singular values
+ * below 2.8, else the result is infinite or NaN.
+ *
+ * All products run on the tensor cores with fp16 operands and fp32 sums.  fp32 results:
+ * every operand is the sum of two fp16 numbers; the result is as far from the exact one as
+ * if all were computed in fp32, or nearer.  bf16 results: single fp16 operands, the linear
+ * term from two; the result is within about 2e-3 of the exact one's norm before its rounding.
+ * NaN and infinities in a matrix make all of it NaN; a matrix of zeros stays zero.
+ *
+ * The conventions of the training operators above hold (scratch memory from the caller, any
+ * stream, capture).
+ */
+/* Longest side of a matrix, and most steps. */
+#define ADASUM_NEWTON_SCHULZ_MAX_DIM 65536
+#define ADASUM_NEWTON_SCHULZ_MAX_STEPS 64
+
+/*
+ * adasum_orthogonalize -- the iteration on `batch` matrices of rows x cols elements of dtype.
+ *   x             element (i, r, c) at i * batch_stride + r * ld + c
+ *   coefficients  host array of 3 * steps floats, (a, b, c) of every step
+ *   out           batch x rows x cols elements of dtype, dense
+ *   scratch       adasum_orthogonalize_scratch_bytes(batch, rows, cols, dtype): some ten bytes
+ *                 an element, but of at most about a gigabyte's matrices at a time
+ */
+ADASUM_API adasum_status_t adasum_orthogonalize(const void *x, int64_t batch, int64_t rows,
+                                                int64_t cols, int64_t batch_stride, int64_t ld,
+                                                adasum_dtype_t dtype, int steps,
+                                                const float *coefficients, float eps, void *out,
+                                                void *scratch, int64_t scratch_bytes,
+                                                adasum_stream_t stream);
+ADASUM_API int64_t adasum_orthogonalize_scratch_bytes(int64_t batch, int64_t rows, int64_t cols,
+                                                      adasum_dtype_t dtype);
+
+/* Factor of the learning rate for a matrix of rows x cols. */
+typedef enum {
+  ADASUM_MUON_SCALE_NONE = 0,     /* 1 */
+  ADASUM_MUON_SCALE_SPECTRAL = 1, /* sqrt(max(1, rows / cols)) */
+  ADASUM_MUON_SCALE_RMS = 2       /* 0.2 sqrt(max(rows, cols)) */
+} adasum_muon_scale_t;
+
+/*
+ * adasum_muon_step -- the step of a flat vector's matrices after the combine: for every
+ * segment that is a matrix,
+ *     v <- mu v + g,   u = g + mu v (nesterov) or v,
+ *     w <- (1 - lr weight_decay) w - lr s X(u)
+ * with X from the iteration above in fp32 accuracy and the factor s of `scale`.
+ *   grad          N = seg_offsets[L] elements of dtype (for instance adasum_reduce's out)
+ *   seg_offsets   host array of L+1 offsets, as adasum_reduce takes them
+ *   rows, cols    host arrays of L sizes: segment s is a row-major matrix of rows[s] x cols[s]
+ *                 = its length; 0: not a matrix, its weights and momentum are not touched
+ *   master_w, momentum  N floats each, updated in place
+ *   coefficients  host array of 3 * steps floats
+ *   scratch       adasum_muon_step_scratch_bytes(rows, cols, L) (-1: out of host memory)
+ */
+ADASUM_API adasum_status_t adasum_muon_step(const void *grad, adasum_dtype_t dtype,
+                                            const int64_t *seg_offsets, const int64_t *rows,
+                                            const int64_t *cols, int L, float *master_w,
+                                            float *momentum, float lr, float mu, int nesterov,
+                                            float weight_decay, adasum_muon_scale_t scale,
+                                            int steps, const float *coefficients, float eps,
+                                            void *scratch, int64_t scratch_bytes,
+                                            adasum_stream_t stream);
+ADASUM_API int64_t adasum_muon_step_scratch_bytes(const int64_t *rows, const int64_t *cols, int L);
+
 /* ---- Instrumentation (used by the benchmark; not needed for normal use) ---------- */
 
 /*
