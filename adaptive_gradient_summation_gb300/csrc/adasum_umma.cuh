@@ -11,6 +11,15 @@
 
 namespace adasum {
 
+// True in one lane of a whole warp, always the same.  (Instructions of one thread issued under
+// `lane == 0` instead cost the copying and multiplying warps about twice the time: the compiler
+// does not see that their operands are uniform.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------------ tiled copies
 
 // CTAS = 2: a pair of CTAs on neighbouring SMs (a cluster of two) works on one product of twice
@@ -84,8 +93,8 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 16 columns, added to v.
-__device__ __forceinline__ void tmem_add16(uint32_t addr, float* v) {
+// 16 columns, times `gain`, added to v.
+__device__ __forceinline__ void tmem_add16(uint32_t addr, float* v, float gain) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
@@ -95,7 +104,7 @@ __device__ __forceinline__ void tmem_add16(uint32_t addr, float* v) {
       : "r"(addr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i] = __fmaf_rn(__uint_as_float(r[i]), gain, v[i]);
 }
 
 // ------------------------------------------------------------------- matrix products

@@ -12,7 +12,8 @@
 // the rounding errors of X that point into their directions: after five steps one rounding of
 // X to bf16 is 1e-2 to 1e-1 of the result's norm, to fp16 2e-3 to 2e-2 (random, power-law and
 // low-rank spectra).  So
-//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits), a product is three
+//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits; X in fp32 for the term a X,
+//     where the growing errors come from), a product is three
 //     products of them (the fourth, of the low parts, is below 2^-22): off by 5e-7 to 5e-6,
 //     where fp32 throughout is off by 2e-6 to 2e-5;
 //   bf16 results: products of the high parts alone, but X itself in both parts for the term
@@ -60,7 +61,9 @@ struct SourceArgs {
   int chunks;
   int64_t per_chunk;
   float eps;
+  bool vec;            // x and momentum lie on 16-byte boundaries
   __half *hi, *lo;     // the first X
+  float* full;         // null: not wanted
   int64_t m, n, ldx;
 };
 
@@ -76,26 +79,94 @@ struct Squares {
   }
 };
 
+// Eight neighbouring elements from element `at` on, of which `count` exist (others 0); vec: they
+// lie on a 16-byte boundary (and are all there).
+__device__ __forceinline__ void load_eight(const void* p, int dtype, int64_t at, int count, bool vec, float (&v)[8]) {
+  if (vec) {
+    if (dtype == kBF16) {
+      const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(p) + at));
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+    } else {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at) + 1);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < count ? load_any(p, dtype, at + e) : 0.f;
+  }
+}
+// Of floats that this kernel may have written.
+__device__ __forceinline__ void load_eight_own(const float* p, int count, bool vec, float (&v)[8]) {
+  if (vec) {
+    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < count ? p[e] : 0.f;
+  }
+}
+__device__ __forceinline__ void store_eight(float* p, int count, bool vec, const float (&v)[8]) {
+  if (vec) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < count) p[e] = v[e];
+  }
+}
+// The high parts of eight values as fp16, and what is left of them.
+__device__ __forceinline__ void split_eight(const float (&x)[8], uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 p = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+    const float2 w = __half22float2(p);
+    const __half2 rest = __floats2half2_rn(x[2 * e] - w.x, x[2 * e + 1] - w.y);
+    h[e] = *reinterpret_cast<const uint32_t*>(&p);
+    l[e] = *reinterpret_cast<const uint32_t*>(&rest);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 // v <- mu v + g (with momentum), and the sums of squares of the update, per chunk.  Bound by
 // bytes.
 __global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const __grid_constant__ Places places) {
   pdl_enter();
   __shared__ float red[3][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t start = places.at[blockIdx.y] >> 1;
-  const int64_t lo = blockIdx.x * a.per_chunk, hi = min(lo + a.per_chunk, a.rows * a.cols);
+  const int64_t start = places.at[blockIdx.y] >> 1, size = a.rows * a.cols;
+  const int64_t lo = blockIdx.x * a.per_chunk, hi = min(lo + a.per_chunk, size);
+  const bool dense = a.ld == a.cols, vec = a.vec && start % 8 == 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) a.ready[blockIdx.y] = 0;
   Squares s;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
-    int64_t at = start + i;
-    if (a.ld != a.cols) at = start + i / a.cols * a.ld + i % a.cols;
-    float u = load_any(a.x, a.dtype, at);
-    if (a.momentum) {
-      const float v = __fmaf_rn(a.mu, a.momentum[at], u);
-      a.momentum[at] = v;
-      u = a.nesterov ? __fmaf_rn(a.mu, v, u) : v;
+  if (dense) {
+#pragma unroll 2
+    for (int64_t i = lo + threadIdx.x * 8; i < hi; i += 2048) {
+      const int count = static_cast<int>(min(hi - i, static_cast<int64_t>(8)));
+      const bool whole = vec && count == 8;
+      float u[8];
+      load_eight(a.x, a.dtype, start + i, count, whole, u);
+      if (a.momentum) {
+        float v[8];
+        load_eight_own(a.momentum + start + i, count, whole, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = __fmaf_rn(a.mu, v[e], u[e]);
+          u[e] = a.nesterov ? __fmaf_rn(a.mu, v[e], u[e]) : v[e];
+        }
+        store_eight(a.momentum + start + i, count, whole, v);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < count) s.add(u[e]);
     }
-    s.add(u);
+  } else {
+    for (int64_t i = lo + threadIdx.x; i < hi; i += 256) s.add(load_any(a.x, a.dtype, start + i / a.cols * a.ld + i % a.cols));
   }
   s.mid = warp_sum(s.mid);
   s.big = warp_sum(s.big);
@@ -110,13 +181,8 @@ __global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const 
   }
 }
 
-__device__ __forceinline__ void split_store(__half* hi, __half* lo, int64_t at, float x) {
-  const __half h = __float2half_rn(x);
-  hi[at] = h;
-  lo[at] = __float2half_rn(x - __half2float(h));
-}
-
-// X = update / (|update| + eps), times kScaleX, as sums of two fp16; 64 x 64 tiles.
+// X = update / (|update| + eps), times kScaleX, in its parts; 64 x 64 tiles, eight neighbours a
+// thread on both sides.  Bound by bytes.
 __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, const __grid_constant__ Places places) {
   pdl_enter();
   __shared__ float tile[64][65];
@@ -130,7 +196,7 @@ __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, cons
       for (int j = 0; j < 3; ++j) s[j] += p[i * 3 + j];
     for (int j = 0; j < 3; ++j) s[j] = warp_sum(s[j]);
     if (threadIdx.x == 0) {
-      // (the middle range between 2^-80 and 2^100; NaN takes the first branch's last case)
+      // (the middle range between 2^-80 and 2^100; NaN takes the last branch)
       float pre = 1.f, norm;
       if (s[0] > 0x1p100f) pre = 0x1p-64f, norm = sqrtf(s[1]) + a.eps * 0x1p-64f;
       else if (s[0] < 0x1p-80f) pre = 0x1p64f, norm = sqrtf(s[2]) + a.eps * 0x1p64f;
@@ -141,31 +207,58 @@ __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, cons
   }
   __syncthreads();
   const float pre = factors[0], factor = factors[1];
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const int at8 = (threadIdx.x & 7) * 8, line = threadIdx.x >> 3;
   // rows and columns as the caller has them
   const int64_t rows = transposed ? a.n : a.m, cols = transposed ? a.m : a.n;
   const int64_t ld = a.momentum || a.ld == a.cols ? cols : a.ld;
   const int64_t r0 = static_cast<int64_t>(transposed ? blockIdx.x : blockIdx.y) * 64;
   const int64_t c0 = static_cast<int64_t>(transposed ? blockIdx.y : blockIdx.x) * 64;
-  for (int r = ty; r < 64; r += 4) {
-    if (r0 + r >= rows || c0 + tx >= cols) continue;
-    const int64_t at = start + (r0 + r) * ld + c0 + tx;
-    float u;
+  const bool vec = a.vec && start % 8 == 0 && ld % 8 == 0;
+  auto put = [&](int64_t i, int64_t j, const float (&x)[8]) {  // (a row's last eight may reach into its padding)
+    const int64_t to = (static_cast<int64_t>(blockIdx.z) * a.m + i) * a.ldx + j;
+    uint4 h, l;
+    split_eight(x, h, l);
+    *reinterpret_cast<uint4*>(a.hi + to) = h;
+    *reinterpret_cast<uint4*>(a.lo + to) = l;
+    if (a.full) store_eight(a.full + to, 8, true, x);
+  };
+#pragma unroll
+  for (int r = line; r < 64; r += 32) {
+    if (r0 + r >= rows || c0 + at8 >= cols) continue;
+    const int count = static_cast<int>(min(cols - c0 - at8, static_cast<int64_t>(8)));
+    const int64_t at = start + (r0 + r) * ld + c0 + at8;
+    const bool whole = vec && count == 8;
+    float u[8];
     if (a.momentum) {
-      u = a.momentum[at];
-      if (a.nesterov) u = __fmaf_rn(a.mu, u, load_any(a.x, a.dtype, at));
+      load_eight_own(a.momentum + at, count, whole, u);
+      if (a.nesterov) {
+        float g[8];
+        load_eight(a.x, a.dtype, at, count, whole, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = __fmaf_rn(a.mu, u[e], g[e]);
+      }
     } else {
-      u = load_any(a.x, a.dtype, at);
+      load_eight(a.x, a.dtype, at, count, whole, u);
     }
-    u = u * pre * factor;
-    if (transposed) tile[r][tx] = u;
-    else split_store(a.hi, a.lo, (static_cast<int64_t>(blockIdx.z) * a.m + r0 + r) * a.ldx + c0 + tx, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = u[e] * pre * factor;
+    if (transposed) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tile[r][at8 + e] = u[e];
+    } else {
+      put(r0 + r, c0 + at8, u);
+    }
   }
   if (!transposed) return;
   __syncthreads();
-  for (int c = ty; c < 64; c += 4)
-    if (c0 + c < cols && r0 + tx < rows)
-      split_store(a.hi, a.lo, (static_cast<int64_t>(blockIdx.z) * a.m + c0 + c) * a.ldx + r0 + tx, tile[tx][c]);
+#pragma unroll
+  for (int c = line; c < 64; c += 32) {
+    if (c0 + c >= cols || r0 + at8 >= rows) continue;
+    float u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = tile[at8 + e][c];
+    put(c0 + c, r0 + at8, u);
+  }
 }
 
 // ------------------------------------------------------------------------- products
@@ -179,13 +272,14 @@ constexpr int kPitch = 33;  // floats between rows of a warp's 32 x 32 block in 
 struct FlowArgs {
   CUtensorMap x_map[2][2], a_map[2], b_map[2];  // [buffer][part], [part]
   __half *x[2][2], *a[2], *b[2];
+  float* full;                 // X in fp32 (TERMS = 3), replaced element by element
   int64_t ldx, lda;
   int m, n, batch, steps;
   int col_tiles[2], tiles[2];  // of A and B (lower triangle), of X
   int* ready;                  // per matrix: warps that have written their part of a tile
   int last;                    // 1: results to `dest`, 2: weights there are moved
   void* dest;
-  int dest_dtype;
+  int dest_dtype, dest_vec;    // on a 16-byte boundary
   float keep, step[2];         // weights: w <- keep w - step x (of a matrix as it is, transposed)
   float coefficients[3 * ADASUM_NEWTON_SCHULZ_MAX_STEPS];
 };
@@ -206,16 +300,22 @@ struct FlowShape {
   static constexpr int kStages = 196608 / kStageBytes < 6 ? 196608 / kStageBytes : 6;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * 32 * kPitch * 4;
   static_assert(kSmem + 1024 <= 232448, "with the barriers, a CTA's shared memory");
-  static constexpr int kBuffers = NT == 256 && TERMS == 3 ? 1 : 2;  // accumulators of the high parts
+  static constexpr int kBuffers = 2;                                   // accumulators of the high parts
   static constexpr int kCross = kBuffers * NT;                       // column of the others'
   static constexpr int kUsed = kCross + (TERMS == 3 ? NT : 0);
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static constexpr int kRun = TERMS == 3 ? 8 : 1 << 30;  // stages of 64
+  static constexpr int kRun = TERMS == 3 ? 2 : 1 << 30;  // stages of 64
   static constexpr int kBlocks = NT / 64;                // of 32 x 32, of an epilogue warp
 };
 
 // Row tile r of a symmetric product has the column tiles up to the diagonal.
 __host__ __device__ constexpr int sym_tiles(int r, int height, int nt) { return (r * height + height - 1) / nt + 1; }
+
+// Average loss of a sum to one cut-off at fp32's 24 bits: half a unit of the last place, which is
+// 2^-23 / x of a value x in [1, 2), and that 0.72 * 2^-23 on average over the logarithm of x.
+// Sums grow in proportion to their terms so far, so k cut-offs take (k + 1) / 2 of them; 4 of
+// products of depth 16 make a stage.
+constexpr float kCutOff = 4.3e-8f;
 
 enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
 
@@ -235,10 +335,11 @@ template <int CTAS, int NT, int TERMS>
 __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_constant__ FlowArgs a, const __grid_constant__ Places places) {
   using S = FlowShape<CTAS, NT, TERMS>;
   extern __shared__ uint8_t raw[];
-  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], cross_empty;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int stop;
+  __shared__ int copied;  // tiles whose operands this CTA has found ready
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
@@ -246,6 +347,7 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
     mbar_init(&cross_empty, kEpilogueWarps * CTAS);
     mbar_fence_init();
     stop = 0;
+    copied = 0;
   }
   if (warp == 1) tmem_alloc<S::kCols, CTAS>(&tmem_slot);
   tc_fence_before();
@@ -303,20 +405,24 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
     return w;
   };
   auto depth = [&](const Tile& t) { return (((t.kind == kGram ? a.n : a.m)) + 63) / 64; };
-  int issued = 0;  // whole stages whose copies this thread began
+  auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+  int issued = 0;  // whole stages whose copies this warp began
   if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      for (int at = first; ok && at < total; at += stride) {
-        const Tile t = locate(at);
-        if (!(ok = wait_ready(t))) break;
-        fence_proxy_async();
-        const int ks = depth(t);
-        const CUtensorMap* p = t.kind == kGram ? a.x_map[t.step & 1] : t.kind == kPoly ? a.a_map : a.b_map;
-        const CUtensorMap* q = t.kind == kPoly ? a.a_map : a.x_map[t.step & 1];
-        for (int k = 0; k < ks; ++k, ++issued) {
-          const int s = issued % S::kStages;
-          if (!(ok = wait(&empty[s], ((issued / S::kStages) & 1) ^ 1))) break;
+    bool ok = true;
+    int tiles = 0;
+    for (int at = first; ok && at < total; at += stride) {
+      const Tile t = locate(at);
+      if (!(ok = __all_sync(0xFFFFFFFFu, wait_ready(t)))) break;
+      ++tiles;
+      if (elect_one()) store_release_cta(&copied, tiles);
+      fence_proxy_async();
+      const int ks = depth(t);
+      const CUtensorMap* p = t.kind == kGram ? a.x_map[t.step & 1] : t.kind == kPoly ? a.a_map : a.b_map;
+      const CUtensorMap* q = t.kind == kPoly ? a.a_map : a.x_map[t.step & 1];
+      for (int k = 0; k < ks; ++k, ++issued) {
+        const int s = issued % S::kStages;
+        if (!(ok = all_wait(&empty[s], ((issued / S::kStages) & 1) ^ 1))) break;
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * S::kStageBytes);
           const uint32_t bar = first_of_pair<CTAS>(smem_addr(&full[s]));
           uint32_t to = smem_addr(stages) + s * S::kStageBytes;
@@ -332,13 +438,13 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
               tma_load3<CTAS>(to, q + part, bar, t.kind == kApply ? c : k * 64, t.kind == kApply ? k * 64 : c, t.matrix);
             }
         }
+        __syncwarp();
       }
-      // every stage consumed: no arrival is on its way to a CTA that has left
-      for (int i = max(0, issued - S::kStages); ok && i < issued; ++i) ok = wait(&empty[i % S::kStages], (i / S::kStages) & 1);
     }
-    __syncwarp();
+    // every stage consumed: no arrival is on its way to a CTA that has left
+    for (int i = max(0, issued - S::kStages); ok && i < issued; ++i) ok = all_wait(&empty[i % S::kStages], (i / S::kStages) & 1);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int it = 0, acc = 0, tiles = 0;
       bool ok = true;
       for (int at = first; ok && at < total; at += stride, ++tiles) {
@@ -350,7 +456,8 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
         for (int k = 0; k < ks; ++k, ++it) {
           const int s = it % S::kStages, buffer = acc % S::kBuffers;
           const bool fresh = k % S::kRun == 0;  // the first of a run
-          if (!(ok = wait(&full[s], (it / S::kStages) & 1))) break;
+          const bool done = k + 1 == ks || (k + 1) % S::kRun == 0;
+          if (!(ok = all_wait(&full[s], (it / S::kStages) & 1))) break;
           tc_fence_after();
           const uint32_t base = smem_addr(stages) + s * S::kStageBytes, qbase = base + S::kParts * S::kPBytes;
           auto multiply = [&](int p_part, int q_part, uint32_t d, bool clear) {
@@ -360,44 +467,49 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
           };
           if constexpr (TERMS == 3) {  // (these while the last run is drained)
             if (k == 0) {
-              if (!(ok = wait(&cross_empty, (tiles & 1) ^ 1))) break;
+              if (!(ok = all_wait(&cross_empty, (tiles & 1) ^ 1))) break;
               tc_fence_after();
             }
-            multiply(0, 1, tmem + S::kCross, k == 0);
-            multiply(1, 0, tmem + S::kCross, false);
+            if (elect_one()) {
+              multiply(0, 1, tmem + S::kCross, k == 0);
+              multiply(1, 0, tmem + S::kCross, false);
+            }
+            __syncwarp();
           }
           if (fresh) {
-            if (!(ok = wait(&acc_empty[buffer], ((acc / S::kBuffers) & 1) ^ 1))) break;
+            if (!(ok = all_wait(&acc_empty[buffer], ((acc / S::kBuffers) & 1) ^ 1))) break;
             tc_fence_after();
           }
-          multiply(0, 0, tmem + buffer * NT, fresh);
-          umma_commit<CTAS>(&empty[s]);
-          if (k + 1 == ks || (k + 1) % S::kRun == 0) {
-            umma_commit<CTAS>(&acc_full[buffer]);
-            ++acc;
+          if (elect_one()) {
+            multiply(0, 0, tmem + buffer * NT, fresh);
+            umma_commit<CTAS>(&empty[s]);
+            if (done) umma_commit<CTAS>(&acc_full[buffer]);
           }
+          __syncwarp();
+          if (done) ++acc;
         }
       }
     }
-    __syncwarp();
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     float* block = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes) + (warp - 2) * 32 * kPitch;
     const int sub = lane >> 2, oct = (lane & 3) * 8;  // of eight rows and four groups of columns
-    int acc = 0;
-    for (int at = first; at < total; at += stride) {
+    int acc = 0, tiles = 0;
+    for (int at = first; at < total; at += stride, ++tiles) {
       const Tile t = locate(at);
       const bool apply = t.kind == kApply, last_step = t.step + 1 == a.steps;
-      // parts of X in the linear term of this step and of the next (the file's comment)
-      const int in_parts = TERMS == 3 || (apply && t.step + 2 < a.steps) ? 2 : 1;
+      // (TERMS = 1) parts of X in the linear term of this step and of the next
+      const int in_parts = apply && t.step + 2 < a.steps ? 2 : 1;
       const int out_parts = TERMS == 3 || (apply && t.step + 3 < a.steps) ? 2 : 1;
       const float c_a = a.coefficients[3 * t.step], c_b = a.coefficients[3 * t.step + 1], c_c = a.coefficients[3 * t.step + 2];
       const float scale = t.kind == kGram   ? kScaleA / (kScaleX * kScaleX)
                           : t.kind == kPoly ? c_c * (kScaleB / (kScaleA * kScaleA))
                                             : 1.f / kScaleB;
       const float in_scale = apply ? c_a : c_b * (kScaleB / kScaleA);
-      __half* const* in = apply ? a.x[t.step & 1] : a.a;
-      __half* const* out = apply ? a.x[(t.step & 1) ^ 1] : t.kind == kGram ? a.a : a.b;
+      const bool even = (t.step & 1) == 0;
+      const __half *in0 = apply ? (even ? a.x[0][0] : a.x[1][0]) : a.a[0], *in1 = apply ? (even ? a.x[0][1] : a.x[1][1]) : a.a[1];
+      __half *out0 = apply ? (even ? a.x[1][0] : a.x[0][0]) : t.kind == kGram ? a.a[0] : a.b[0];
+      __half *out1 = apply ? (even ? a.x[1][1] : a.x[0][1]) : t.kind == kGram ? a.a[1] : a.b[1];
       const int64_t ld = apply ? a.ldx : a.lda, base = static_cast<int64_t>(t.matrix) * a.m * ld;
       const int cols = apply ? a.n : a.m, i0 = t.row + rank * 128 + quarter * 32;
       auto column = [&](int k) { return t.col + (half + 2 * k) * 32; };
@@ -414,8 +526,14 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
           const int i = i0 + r * 8 + sub;
           const int64_t from = base + i * ld + c;
           const bool on = i < a.m && c < cols;
-          f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(in[0] + from)) : make_uint4(0, 0, 0, 0);
-          f.part[1][r] = on && in_parts == 2 ? __ldcg(reinterpret_cast<const uint4*>(in[1] + from)) : make_uint4(0, 0, 0, 0);
+          const uint4 none = make_uint4(0, 0, 0, 0);
+          if (TERMS == 3 && apply) {  // fp32
+            f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(a.full + from)) : none;
+            f.part[1][r] = on ? __ldcg(reinterpret_cast<const uint4*>(a.full + from) + 1) : none;
+          } else {
+            f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(in0 + from)) : none;
+            f.part[1][r] = on && (TERMS == 3 || in_parts == 2) ? __ldcg(reinterpret_cast<const uint4*>(in1 + from)) : none;
+          }
         }
       };
       auto finish = [&](int k, const float (&v)[32], const Added& f) {
@@ -426,19 +544,40 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
         __syncwarp();
         auto put = [&](int64_t to, const float (&x)[8]) {
           uint4 h, l;
-          uint32_t* hw = &h.x;
-          uint32_t* lw = &l.x;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2 p = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
-            const float2 w = __half22float2(p);
-            const __half2 rest = __floats2half2_rn(x[2 * e] - w.x, x[2 * e + 1] - w.y);
-            hw[e] = *reinterpret_cast<const uint32_t*>(&p);
-            lw[e] = *reinterpret_cast<const uint32_t*>(&rest);
-          }
-          *reinterpret_cast<uint4*>(out[0] + to) = h;
-          if (out_parts == 2) *reinterpret_cast<uint4*>(out[1] + to) = l;
+          split_eight(x, h, l);
+          *reinterpret_cast<uint4*>(out0 + to) = h;
+          if (out_parts == 2) *reinterpret_cast<uint4*>(out1 + to) = l;
         };
+        // eight neighbours of the result's row (or column, if it is stored transposed) `line`
+        auto put_last = [&](int line, int first, int lines, int length, const float (&x)[8]) {
+          if (line >= lines || first >= length) return;
+          const int64_t place = places.at[t.matrix], to = (place >> 1) + static_cast<int64_t>(line) * length + first;
+          const int count = min(8, length - first);
+          const bool whole = a.dest_vec && length % 8 == 0 && (place >> 1) % 8 == 0;
+          float y[8];
+          if (a.last == 2) {
+            float* w = static_cast<float*>(a.dest) + to;
+            const float step = a.step[place & 1] * (1.f / kScaleX);
+            load_eight_own(w, count, whole, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __fmaf_rn(-step, x[e], a.keep * y[e]);
+            store_eight(w, count, whole, y);
+            return;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = x[e] * (1.f / kScaleX);
+          if (a.dest_dtype == kF32) {
+            store_eight(static_cast<float*>(a.dest) + to, count, whole, y);
+          } else if (whole) {
+            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dest) + to) =
+                make_uint4(pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (e < count) static_cast<bf16*>(a.dest)[to + e] = narrow<bf16>(y[e]);
+          }
+        };
+        const bool transposed = apply && last_step && (places.at[t.matrix] & 1);
         const bool mirror = !apply && j0 < i0, final = apply && last_step;
         // (a row's last eight columns may reach into its padding)
 #pragma unroll
@@ -447,7 +586,13 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
           float x[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = block[(r * 8 + sub) * kPitch + oct + e] * scale;
-          if (t.kind != kGram) {
+          if (TERMS == 3 && apply) {
+            const float y[8] = {__uint_as_float(f.part[0][r].x), __uint_as_float(f.part[0][r].y), __uint_as_float(f.part[0][r].z),
+                                __uint_as_float(f.part[0][r].w), __uint_as_float(f.part[1][r].x), __uint_as_float(f.part[1][r].y),
+                                __uint_as_float(f.part[1][r].z), __uint_as_float(f.part[1][r].w)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __fmaf_rn(in_scale, y[e], x[e]);
+          } else if (t.kind != kGram) {
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
               const uint32_t* w = &f.part[part][r].x;
@@ -459,13 +604,18 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
               }
             }
           }
-          if (mirror || final) {
+          if (mirror || transposed) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) block[(r * 8 + sub) * kPitch + oct + e] = x[e];
           }
-          if (!final && i < a.m && j0 + oct < cols) put(base + i * ld + j0 + oct, x);
+          if (final) {
+            if (!transposed) put_last(i, j0 + oct, a.m, cols, x);
+          } else if (i < a.m && j0 + oct < cols) {
+            put(base + i * ld + j0 + oct, x);
+            if (TERMS == 3 && apply) store_eight(a.full + base + i * ld + j0 + oct, 8, true, x);
+          }
         }
-        if (mirror) {
+        if (mirror || transposed) {
           __syncwarp();
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -473,32 +623,20 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = block[(oct + e) * kPitch + r * 8 + sub];
-            if (j < cols && i0 + oct < a.m) put(base + j * ld + i0 + oct, x);
-          }
-        }
-        if (final) {
-          __syncwarp();
-          const int64_t place = places.at[t.matrix], start = place >> 1;
-          const bool transposed = place & 1;
-          const float step = a.step[transposed];
-#pragma unroll 8
-          for (int r = 0; r < 32; ++r) {
-            const int i = i0 + (transposed ? lane : r), j = j0 + (transposed ? r : lane);
-            if (i >= a.m || j >= cols) continue;
-            const float x = (transposed ? block[lane * kPitch + r] : block[r * kPitch + lane]) * (1.f / kScaleX);
-            const int64_t to = start + (transposed ? static_cast<int64_t>(j) * a.m + i : static_cast<int64_t>(i) * cols + j);
-            if (a.last == 2) {
-              float* w = static_cast<float*>(a.dest) + to;
-              *w = __fmaf_rn(-step, x, a.keep * *w);
-            } else {
-              store_any(a.dest, a.dest_dtype, to, x);
-            }
+            if (transposed) put_last(j, i0 + oct, cols, a.m, x);
+            else if (j < cols && i0 + oct < a.m) put(base + j * ld + i0 + oct, x);
           }
         }
       };
+      // (the copying warp has seen this tile's matrix ready; what it saw is visible after that)
       bool ok = true;
-      if (lane == 0) ok = wait_ready(t);
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
+      const long long t0 = clock64();
+      while (load_acquire_cta(&copied) <= tiles)
+        if (stop || clock64() - t0 > kWaitCycles) {
+          ok = give_up();
+          break;
+        }
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
       auto release = [&](uint64_t* bar) {
         tc_fence_before();
@@ -533,11 +671,13 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
           const int buffer = acc % S::kBuffers;
           if (!(ok = wait(&acc_full[buffer], (acc / S::kBuffers) & 1))) break;
           tc_fence_after();
+          // what a run of sums cut off towards zero loses on average (FlowShape)
+          const float gain = 1.f + kCutOff * (2 * min(ks - run, S::kRun) + 0.5f);
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k) {
             if (!there(k)) continue;
-            tmem_add16(from + buffer * NT + k * 64, v[k]);
-            tmem_add16(from + buffer * NT + k * 64 + 16, v[k] + 16);
+            tmem_add16(from + buffer * NT + k * 64, v[k], gain);
+            tmem_add16(from + buffer * NT + k * 64 + 16, v[k] + 16, gain);
           }
           release(&acc_empty[buffer]);
         }
@@ -545,8 +685,8 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k) {
           if (!there(k)) continue;
-          tmem_add16(from + S::kCross + k * 64, v[k]);
-          tmem_add16(from + S::kCross + k * 64 + 16, v[k] + 16);
+          tmem_add16(from + S::kCross + k * 64, v[k], 1.f);
+          tmem_add16(from + S::kCross + k * 64 + 16, v[k] + 16, 1.f);
         }
         release(&cross_empty);
 #pragma unroll
@@ -617,7 +757,7 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 // in the scratch memory.
 struct ScratchMap {
   int64_t m, n, ldx, lda;
-  int64_t x[2][2], a[2], b[2], partials, ready, bytes;
+  int64_t x[2][2], full, a[2], b[2], partials, ready, bytes;
   int chunks;
   int64_t per_chunk;
   ScratchMap(int64_t m_, int64_t n_, int64_t batch, bool fine) : m(m_), n(n_), ldx(round_up(n_, 8)), lda(round_up(m_, 8)) {
@@ -629,6 +769,7 @@ struct ScratchMap {
     };
     for (int i = 0; i < 2; ++i)
       for (int part = 0; part < 2; ++part) x[i][part] = take(batch * m * ldx * 2);
+    full = fine ? take(batch * m * ldx * 4) : 0;
     for (int part = 0; part < 2; ++part) {
       a[part] = part == 0 || fine ? take(batch * m * lda * 2) : 0;
       b[part] = part == 0 || fine ? take(batch * m * lda * 2) : 0;
@@ -674,10 +815,10 @@ int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
 struct TileSize {
   int ctas, nt;
 };
-TileSize tile_size(int64_t m, int64_t n, int64_t batch) {
-  TileSize best = {2, 256};
+TileSize tile_size(int64_t m, int64_t n, int64_t batch, bool fine) {
+  TileSize best = {2, fine ? 128 : 256};
   double least = 1e300;
-  for (const TileSize s : {TileSize{2, 256}, TileSize{1, 128}, TileSize{1, 64}}) {
+  for (const TileSize s : {TileSize{2, fine ? 128 : 256}, TileSize{1, 128}, TileSize{1, 64}}) {
     const int64_t units = sm_count() / s.ctas;
     auto waves = [&](int64_t tiles) { return static_cast<double>((tiles * batch + units - 1) / units); };
     const int64_t sym = count_tiles(m, m, 128 * s.ctas, s.nt, true), gen = count_tiles(m, n, 128 * s.ctas, s.nt, false);
@@ -714,7 +855,7 @@ int launch_flow_as(FlowArgs& a, const Places& places, cudaStream_t stream) {
 }
 template <int TERMS>
 int launch_flow(FlowArgs& a, const Places& places, TileSize s, cudaStream_t stream) {
-  if (s.ctas == 2) return launch_flow_as<2, 256, TERMS>(a, places, stream);
+  if (s.ctas == 2) return launch_flow_as<2, TERMS == 3 ? 128 : 256, TERMS>(a, places, stream);
   if (s.nt == 128) return launch_flow_as<1, 128, TERMS>(a, places, stream);
   return launch_flow_as<1, 64, TERMS>(a, places, stream);
 }
@@ -736,6 +877,7 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
     ok = ok && make_map(&f.a_map[part], f.a[part], m, m, l.lda, batch) && make_map(&f.b_map[part], f.b[part], m, m, l.lda, batch);
   }
   if (!ok) return ADASUM_ERR_CUDA;
+  f.full = fine ? reinterpret_cast<float*>(scratch + l.full) : nullptr;
   f.ldx = l.ldx;
   f.lda = l.lda;
   f.m = static_cast<int>(m);
@@ -746,6 +888,7 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
   f.last = res.last;
   f.dest = res.dest;
   f.dest_dtype = res.dtype;
+  f.dest_vec = is_aligned(res.dest, 16);
   f.keep = res.keep;
   std::copy(res.step, res.step + 2, f.step);
   std::copy(it.coefficients, it.coefficients + 3 * it.steps, f.coefficients);
@@ -754,6 +897,8 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
   src.chunks = l.chunks;
   src.per_chunk = l.per_chunk;
   src.eps = it.eps;
+  src.vec = is_aligned(src.x, 16) && is_aligned(src.momentum, 16);
+  src.full = f.full;
   src.hi = f.x[0][0];
   src.lo = f.x[0][1];
   src.m = m;
@@ -769,7 +914,7 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
                       dim3(256), 0, stream, src, from);
   });
   if (st) return st;
-  const TileSize size = tile_size(m, n, batch);
+  const TileSize size = tile_size(m, n, batch, fine);
   return counted_launch(stream, fine ? "update_iterate3" : "update_iterate", 0.0, [&] {
     return fine ? launch_flow<3>(f, places, size, stream) : launch_flow<1>(f, places, size, stream);
   });
