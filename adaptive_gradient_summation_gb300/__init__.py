@@ -26,7 +26,8 @@ import torch
 from ._native import AdasumError, KernelStat, Status, check, library_path, load_library
 from .training import (Checkpoint, checkpoint_pack, checkpoint_unpack, embedding, embedding_backward,
                        gelu_checkpointed, gelu_checkpointed_backward, layer_norm, layer_norm_backward,
-                       layer_norm_checkpointed, layer_norm_checkpointed_backward)
+                       layer_norm_checkpointed, layer_norm_checkpointed_backward, relative_position_bias,
+                       relative_position_bias_backward, rms_norm, rms_norm_backward, rms_norm_checkpointed, rms_norm_checkpointed_backward)
 from .updates import NEWTON_SCHULZ, muon_step, orthogonalize
 
 __all__ = ["reduce", "pair", "pair_noalloc", "reduce_momentum_sgd", "local_momentum_reduce", "reduce_from_host", "AdasumError",
@@ -34,7 +35,9 @@ __all__ = ["reduce", "pair", "pair_noalloc", "reduce_momentum_sgd", "local_momen
            "launch_count", "recomputed_segments", "profile_enable", "profile_collect", "version",
            "Checkpoint", "checkpoint_pack", "checkpoint_unpack", "embedding", "embedding_backward",
            "gelu_checkpointed", "gelu_checkpointed_backward", "layer_norm", "layer_norm_backward",
-           "layer_norm_checkpointed", "layer_norm_checkpointed_backward", "NEWTON_SCHULZ", "muon_step", "orthogonalize"]
+           "layer_norm_checkpointed", "layer_norm_checkpointed_backward", "NEWTON_SCHULZ", "muon_step", "orthogonalize",
+           "relative_position_bias", "relative_position_bias_backward", "rms_norm", "rms_norm_backward", "rms_norm_checkpointed",
+           "rms_norm_checkpointed_backward"]
 
 _DTYPE_CODE = {torch.float32: 0, torch.bfloat16: 1}
 

@@ -36,10 +36,11 @@ TEST_FLAGS = ["-DADASUM_TEST_HOOKS", "-DADASUM_BOUNDS_CHECK"]
 
 SOURCES = ["adasum_api.cu", "launch_f32.cu", "launch_bf16.cu", "launch_f64.cu",
            "launch_onchip.cu", "adasum_noalloc.cu", "train_embedding.cu", "train_norm.cu",
-           "train_checkpoint.cu", "train_muon.cu"]
+           "train_checkpoint.cu", "train_muon.cu", "train_rms.cu", "train_rms_grad.cu", "train_rms_sum_grad.cu",
+           "train_bias.cu"]
 HEADERS = ["adasum_internal.h", "adasum_kernels.cuh", "adasum_ptx.cuh",
            "adasum_onchip.cuh", "adasum_launch.h", "adasum_pair.cuh", "adasum_host.h",
-           "adasum_train.cuh", "adasum_umma.cuh"]
+           "adasum_train.cuh", "adasum_umma.cuh", "adasum_norm.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -77,10 +77,21 @@ SIGNATURES = {
     "adasum_layer_norm_backward_scratch_bytes": (ctypes.c_int64, [_P, _I, _I64]),
     "adasum_layer_norm_backward_checkpointed": (ctypes.c_int, [
         _P, _I64, _P, _P, _P, _I64, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _I64, _P]),
+    "adasum_rms_norm": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _P, _I64, _P, _P, _I, _F, _P, _P, _P, _P, _P]),
+    "adasum_rms_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I, _P, _I, _P, _I64, _P, _I, _P, _P, _I, _I, _P,
+                                                _I64, _P]),
+    "adasum_rms_norm_backward_scratch_bytes": (ctypes.c_int64, [_P, _I, _I64]),
+    "adasum_rms_norm_backward_checkpointed": (ctypes.c_int, [_P, _I64, _P, _P, _P, _I64, _I, _P, _I, _P, _I64, _P, _I, _P, _P,
+                                                             _P, _I, _I, _P, _I64, _P]),
     "adasum_checkpoint_pack": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _P, _P, _P]),
     "adasum_checkpoint_unpack": (ctypes.c_int, [_P, _P, _I64, _I64, _I, _P, _P]),
     "adasum_gelu_checkpointed": (ctypes.c_int, [_P, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P]),
     "adasum_gelu_checkpointed_backward": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _I64, _I, _I, _P, _P, _P]),
+    "adasum_relative_position_bias": (ctypes.c_int, [_P, _I, _I64, _I, _I, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64,
+                                                     _I, _P, _P]),
+    "adasum_relative_position_bias_backward": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _I64, _I, _I, _I, _I64, _I64, _P,
+                                                              _I, _P, _I, _I, _P, _I64, _P]),
+    "adasum_relative_position_bias_backward_scratch_bytes": (ctypes.c_int64, [_P, _I, _I64, _I64, _I64, _I]),
     "adasum_orthogonalize": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _I, _I, _P, _F, _P, _P, _I64, _P]),
     "adasum_orthogonalize_scratch_bytes": (ctypes.c_int64, [_I64, _I64, _I64, _I]),
     "adasum_muon_step": (ctypes.c_int, [_P, _I, _P, _P, _P, _I, _P, _P, _F, _F, _I, _F, _I, _I, _P, _F, _P, _I64, _P]),

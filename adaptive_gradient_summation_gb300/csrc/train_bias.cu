@@ -1,0 +1,585 @@
+// train_bias.cu -- the learned relative position bias of attention scores by buckets, and the
+// gradient of its table per worker.
+//
+// Times in the comments are those of one launch between two events (the library's profiler; 4
+// to 6 us of it are the launch), unless they are said to be of a pass, a call among others
+// through the Python binding.
+#include <cmath>
+#include <vector>
+
+#include "adasum_host.h"
+#include "adasum_launch.h"
+#include "adasum_train.cuh"
+
+namespace adasum {
+namespace {
+
+constexpr int kMaxBuckets = ADASUM_BIAS_MAX_BUCKETS;
+constexpr int kBiasThreads = 256, kBiasWarps = 8;
+
+// Buckets of one direction: distance d belongs to the last j with border[j] <= d.
+struct Buckets {
+  int n;               // of one direction
+  int both;            // keys ahead have n of their own, after the others; else all are in bucket 0
+  int64_t border[kMaxBuckets];
+};
+
+// `rel`: key's position less the query's.
+__device__ __forceinline__ int bucket_of(const Buckets& b, int64_t rel) {
+  int64_t d = rel < 0 ? -rel : b.both ? rel : 0;
+  int lo = 0, hi = b.n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (b.border[m] <= d) lo = m;
+    else hi = m;
+  }
+  return b.both && rel > 0 ? b.n + lo : lo;
+}
+
+// ------------------------------------------------------------------------------ forward
+
+struct BiasArgs {
+  const void* table;
+  int table_dtype;
+  int64_t heads, batch, queries, keys, offset;
+  const void* scores;  // null: the bias alone
+  int64_t stride_b, stride_h, stride_q;
+  void* out;
+  int row_groups;      // of a CTA's warps, four rows each; the others take other sequences
+  int64_t per_cta;     // sequences
+  Buckets buckets;
+};
+
+// E keys a lane: neighbours (16 bytes, VEC) or 32 apart.  A CTA has up to 32 rows of one head
+// and a warp's 32 E keys; the biases that occur there, one for each diagonal, go through shared
+// memory (a word of padding every 32, so that lanes 4 or 8 apart meet no bank twice) into the
+// registers of a warp's four rows, which serve all its sequences.  Bound by the bytes of the
+// scores.  BIASFIGURES
+template <typename T, int E, bool VEC, bool SCORES>
+__global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constant__ BiasArgs a) {
+  pdl_enter();
+  __shared__ float lut[(32 * E + 32) * 33 / 32 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t tiles = (a.keys + 32 * E - 1) / (32 * E);
+  const int64_t k0 = blockIdx.x % tiles * (32 * E), h = blockIdx.y;
+  const int rows = 4 * a.row_groups;
+  const int64_t q0 = blockIdx.x / tiles * rows;
+  // lut[i]: of key k0 + i - (rows - 1) against query q0
+  const int64_t rel0 = k0 - (rows - 1) - q0 - a.offset;
+  for (int i = threadIdx.x; i < 32 * E + rows - 1; i += kBiasThreads)
+    lut[i + (i >> 5)] = load_any(a.table, a.table_dtype, bucket_of(a.buckets, rel0 + i) * a.heads + h);
+  __syncthreads();
+  const int group = warp % a.row_groups, first = warp / a.row_groups, step = kBiasWarps / a.row_groups;
+  float bias[4][E];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = (VEC ? lane * E + e : lane + 32 * e) + rows - 1 - (group * 4 + r);
+      bias[r][e] = lut[i + (i >> 5)];
+    }
+  const int64_t q = q0 + group * 4, k = k0 + (VEC ? lane * E : lane);
+  const int64_t b0 = blockIdx.z * a.per_cta, b1 = min(b0 + a.per_cta, a.batch);
+  const int left = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(4), a.queries - q)));
+#pragma unroll 2
+  for (int64_t b = b0 + first; b < b1; b += step) {
+    const T* from = static_cast<const T*>(a.scores) + b * a.stride_b + h * a.stride_h + q * a.stride_q + k;
+    T* to = static_cast<T*>(a.out) + ((b * a.heads + h) * a.queries + q) * a.keys + k;
+    if constexpr (VEC) {
+      uint4 x[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (SCORES && r < left && k < a.keys) x[r] = __ldcs(reinterpret_cast<const uint4*>(from + r * a.stride_q));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r >= left || k >= a.keys) continue;
+        float v[E];
+        const uint32_t* w = &x[r].x;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float s = 0.f;
+          if constexpr (SCORES) {
+            if constexpr (sizeof(T) == 4) s = __uint_as_float(w[e]);
+            else s = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+          }
+          v[e] = SCORES ? s + bias[r][e] : bias[r][e];
+        }
+        uint4 y;
+        if constexpr (sizeof(T) == 4)
+          y = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        else
+          y = make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[E - 4], v[E - 3]), pack2_bf16(v[E - 2], v[E - 1]));
+        __stcs(reinterpret_cast<uint4*>(to + r * a.keys), y);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r >= left) break;
+        T x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (SCORES && k + 32 * e < a.keys) x[e] = from[r * a.stride_q + 32 * e];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (k + 32 * e < a.keys) to[r * a.keys + 32 * e] = narrow<T>(SCORES ? widen(x[e]) + bias[r][e] : bias[r][e]);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- gradient
+
+constexpr int kBiasRows = 256;  // at most, of a warp
+constexpr int kBiasKeys = 256;  // of a warp, eight a lane
+
+struct BiasGradArgs {
+  const void* d;
+  int64_t stride_b, stride_h, stride_q;
+  int64_t heads, queries, keys, offset;
+  int rows;            // of a unit
+  int row_units, key_units, batch_units, per_unit;  // units of one worker and head; sequences of a unit
+  int groups;          // CTAs of one worker and head, eight units each
+  float* partials;     // [worker, head][group][bucket]; null: one group, the gradient is written
+  int total;           // buckets of both directions
+  Buckets buckets;
+  int64_t off[kMaxK + 1];
+};
+struct BiasOut {
+  void* grads[kMaxK];
+  int dtype, accumulate;
+  int64_t heads;
+  int total, groups;
+  const float* partials;
+};
+
+__device__ __forceinline__ void put_bucket(const BiasOut& o, int k, int64_t h, int bucket, float s) {
+  const int64_t at = bucket * o.heads + h;
+  if (o.accumulate) s += load_any(o.grads[k], o.dtype, at);
+  store_any(o.grads[k], o.dtype, at, s);
+}
+
+// A bucket's sum runs over whole diagonals.  A warp has a unit: 256 neighbouring keys, eight a
+// lane, up to 256 queries, some sequences of one worker.  It goes down the queries with the
+// running sums of 256 diagonals in registers: from one query to the next a diagonal moves on
+// by one key, so the sums move by one register (or lane), the last lane's leaves the window and
+// a new one begins.  The diagonals' sums end in shared memory and are added up per bucket, in
+// an order that depends on the sizes alone.  One read of the gradients, an addition a value.
+// GRADFIGURES
+// VEC: a lane's eight keys are neighbours on 16-byte boundaries; else they are 32 apart.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kBiasThreads, 4) bias_grad_kernel(const __grid_constant__ BiasGradArgs a, const __grid_constant__ BiasOut o) {
+  pdl_enter();
+  __shared__ float diagonals[kBiasWarps][kBiasRows + kBiasKeys];
+  __shared__ float sums[kBiasWarps][kMaxBuckets];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t h = blockIdx.y;
+  const int k = blockIdx.z;
+  const int units = a.row_units * a.key_units * a.batch_units;
+  const int unit = blockIdx.x * kBiasWarps + warp;
+  float* mine = diagonals[warp];
+  for (int b = lane; b < a.total; b += 32) sums[warp][b] = 0.f;
+  const int64_t b0 = a.off[k] + static_cast<int64_t>(unit / (a.row_units * a.key_units)) * a.per_unit;
+  const int nb = unit < units ? static_cast<int>(max(static_cast<int64_t>(0), min(a.off[k + 1] - b0, static_cast<int64_t>(a.per_unit)))) : 0;
+  if (nb > 0) {
+    const int r = unit % (a.row_units * a.key_units);
+    const int64_t q0 = static_cast<int64_t>(r / a.key_units) * a.rows, k0 = static_cast<int64_t>(r % a.key_units) * kBiasKeys;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.queries - q0));
+    const int width = static_cast<int>(min(static_cast<int64_t>(kBiasKeys), a.keys - k0));
+    const T* p = static_cast<const T*>(a.d) + b0 * a.stride_b + h * a.stride_h + q0 * a.stride_q + k0;
+    const int64_t back = a.stride_q - (nb - 1) * a.stride_b;
+    const int count = rows * nb;  // rows of 256 keys, sequence by sequence, query by query
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+    struct Row {
+      uint32_t w[VEC ? sizeof(T) * 2 : 8];
+    } row[kAhead];
+    int next_b = 0, next = 0;
+    auto fetch = [&](Row& f) {
+      if (next >= count) return;
+      if constexpr (VEC) {
+        constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes
+        const T* at = p + lane * 8;
+        if (lane * 8 + 8 <= width) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const uint4 x = __ldcs(reinterpret_cast<const uint4*>(at) + i);
+            f.w[4 * i] = x.x, f.w[4 * i + 1] = x.y, f.w[4 * i + 2] = x.z, f.w[4 * i + 3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = lane * 8 + e < width ? widen(at[e]) : 0.f;
+            if constexpr (sizeof(T) == 4) f.w[e] = __float_as_uint(x);
+            else f.w[e >> 1] = e & 1 ? f.w[e >> 1] | (__float_as_uint(x) & 0xFFFF0000u) : __float_as_uint(x) >> 16;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.w[e] = lane + 32 * e < width ? __float_as_uint(widen(p[lane + 32 * e])) : 0u;
+      }
+      ++next;
+      if (++next_b == nb) next_b = 0, p += back;
+      else p += a.stride_b;
+    };
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    int b = 0, done = 0;  // sequences of this query, queries
+    // slot of the diagonal that key i of the window is on, at the last of the unit's queries
+    auto take = [&](const Row& f) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (!VEC || sizeof(T) == 4) acc[e] += __uint_as_float(f.w[e]);
+        else acc[e] += __uint_as_float(e & 1 ? f.w[e >> 1] & 0xFFFF0000u : f.w[e >> 1] << 16);
+      }
+      if (++b < nb) return;
+      b = 0;
+      if (++done == rows) return;
+      if constexpr (VEC) {
+        if (lane == 31) mine[kBiasKeys - 1 + rows - done] = acc[7];
+        const float in = __shfl_up_sync(0xFFFFFFFFu, acc[7], 1);
+#pragma unroll
+        for (int e = 7; e > 0; --e) acc[e] = acc[e - 1];
+        acc[0] = lane == 0 ? 0.f : in;
+      } else {
+        if (lane == 31) mine[kBiasKeys - 1 + rows - done] = acc[7];
+        float in[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) in[e] = __shfl_sync(0xFFFFFFFFu, acc[e], (lane + 31) & 31);
+#pragma unroll
+        for (int e = 7; e > 0; --e) acc[e] = lane == 0 ? in[e - 1] : in[e];
+        acc[0] = lane == 0 ? 0.f : in[0];
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(row[i]);
+    for (int at = 0; at < count; at += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (at + i >= count) break;
+        const Row now = row[i];
+        fetch(row[i]);
+        take(now);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine[VEC ? lane * 8 + e : lane + 32 * e] = acc[e];
+    __syncwarp();
+    // mine[i]: key k0 + i against the unit's last query
+    const int64_t rel0 = k0 - (q0 + rows - 1) - a.offset;
+    const int slots = kBiasKeys + rows - 1;
+    const int n = a.buckets.n;
+    auto range = [&](int bucket, int& lo, int& hi) {  // slots of a bucket
+      const bool ahead = bucket >= n;
+      const int j = ahead ? bucket - n : bucket;
+      const int64_t near = a.buckets.border[j], far = j + 1 < n ? a.buckets.border[j + 1] : INT64_MAX;
+      int64_t first, last;  // of the relative positions, and one past it
+      if (ahead) first = max(near, static_cast<int64_t>(1)), last = far;
+      else first = far == INT64_MAX ? INT64_MIN : 1 - far, last = 1 - near;
+      if (!a.buckets.both && j == 0) last = INT64_MAX;
+      auto slot = [&](int64_t rel) {
+        return rel <= rel0 ? 0 : rel >= rel0 + slots ? slots : static_cast<int>(rel - rel0);
+      };
+      lo = slot(first);
+      hi = slot(last);
+    };
+    // short buckets by a lane each, long ones by the warp
+    constexpr int kShort = 16;
+    for (int c = 0; c < a.total; c += 32) {
+      int lo = 0, hi = 0;
+      if (c + lane < a.total) range(c + lane, lo, hi);
+      float s = 0.f;
+      if (hi - lo <= kShort)
+        for (int i = lo; i < hi; ++i) s += mine[i];
+      unsigned longs = __ballot_sync(0xFFFFFFFFu, hi - lo > kShort);
+      for (; longs; longs &= longs - 1) {
+        const int from = __ffs(longs) - 1;
+        const int l = __shfl_sync(0xFFFFFFFFu, lo, from), e = __shfl_sync(0xFFFFFFFFu, hi, from);
+        float v = 0.f;
+        for (int i = l + lane; i < e; i += 32) v += mine[i];
+        v = warp_sum(v);
+        if (lane == from) s = v;
+      }
+      if (c + lane < a.total) sums[warp][c + lane] = s;
+    }
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < a.total; b += kBiasThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBiasWarps; ++w) s += sums[w][b];
+    if (a.partials == nullptr) put_bucket(o, k, h, b, s);
+    else a.partials[((k * a.heads + h) * a.groups + blockIdx.x) * a.total + b] = s;
+  }
+}
+
+// Adds the CTAs' sums of one worker and head, in their order within eight rows of them.
+__global__ void __launch_bounds__(256) bias_join_kernel(const __grid_constant__ BiasOut o) {
+  pdl_enter();
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = blockIdx.z;
+  const int64_t h = blockIdx.y;
+  const int b = blockIdx.x * 32 + lane;
+  const float* p = o.partials + (k * o.heads + h) * o.groups * static_cast<int64_t>(o.total);
+  float s = 0.f;
+  if (b < o.total) {
+#pragma unroll 4
+    for (int g = warp; g < o.groups; g += 8) s += p[static_cast<int64_t>(g) * o.total + b];
+  }
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp > 0 || b >= o.total) return;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) s += red[j][lane];
+  put_bucket(o, k, h, b, s);
+}
+
+// ----------------------------------------------------------------------------- host side
+
+// base^power times what is there, in whole numbers of any length.
+void multiply(std::vector<uint32_t>& x, uint64_t by) {
+  const uint64_t parts[2] = {by & 0xFFFFFFFFu, by >> 32};
+  std::vector<uint32_t> out(x.size() + 3, 0u);
+  for (int h = 0; h < 2; ++h) {
+    uint64_t carry = 0;
+    for (size_t i = 0; i < x.size() || carry; ++i) {
+      const uint64_t v = out[i + h] + carry + (i < x.size() ? parts[h] * x[i] : 0);
+      out[i + h] = static_cast<uint32_t>(v);
+      carry = v >> 32;
+    }
+  }
+  while (out.size() > 1 && out.back() == 0) out.pop_back();
+  x.swap(out);
+}
+std::vector<uint32_t> power_product(uint64_t a, int i, uint64_t b, int j) {  // a^i b^j
+  std::vector<uint32_t> x(1, 1u);
+  for (; i > 0; --i) multiply(x, a);
+  for (; j > 0; --j) multiply(x, b);
+  return x;
+}
+bool at_least(const std::vector<uint32_t>& a, const std::vector<uint32_t>& b) {
+  if (a.size() != b.size()) return a.size() > b.size();
+  for (size_t i = a.size(); i-- > 0;)
+    if (a[i] != b[i]) return a[i] > b[i];
+  return true;
+}
+
+// The borders of one direction.  Bucket e + i begins at the smallest d with
+// (n - e) ln(d / e) >= i ln(D / e): where d is not plainly on one side, (d / e)^(n - e) is
+// compared with (D / e)^i in whole numbers, d^(n - e) e^i with D^i e^(n - e).
+void borders(Buckets& b, int64_t max_distance) {
+  const int e = b.n / 2, p = b.n - e;
+  for (int j = 0; j <= e; ++j) b.border[j] = j;
+  for (int i = 1; i < p; ++i) {
+    const double x = e * std::exp(std::log(static_cast<double>(max_distance) / e) * i / p);
+    int64_t d = std::llround(x);
+    if (std::fabs(x - static_cast<double>(d)) < 1e-9 * x) {
+      if (!at_least(power_product(d, p, e, i), power_product(max_distance, i, e, p))) ++d;
+    } else {
+      d = static_cast<int64_t>(std::ceil(x));
+    }
+    b.border[e + i] = d;
+  }
+}
+
+// Fills the buckets of a call; what is wrong with it.
+adasum_status_t make_buckets(Buckets& b, int buckets, int both, int64_t max_distance) {
+  if (buckets > kMaxBuckets || max_distance > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
+  if (buckets < 1 || (both && buckets % 2)) return ADASUM_ERR_INVALID_ARG;
+  b.both = both != 0;
+  b.n = both ? buckets / 2 : buckets;
+  if (b.n < 2 || max_distance <= b.n / 2) return ADASUM_ERR_INVALID_ARG;
+  try {
+    borders(b, max_distance);
+  } catch (...) {  // (out of host memory)
+    return ADASUM_ERR_NO_MEMORY;
+  }
+  return ADASUM_OK;
+}
+
+adasum_status_t check_sizes(int64_t heads, int64_t batch, int64_t queries, int64_t keys, int64_t offset) {
+  if (heads < 0 || batch < 0 || queries < 0 || keys < 0) return ADASUM_ERR_INVALID_ARG;
+  constexpr int64_t kFar = int64_t(1) << 61;
+  if (heads > 65535 || queries > INT32_MAX || keys > INT32_MAX || offset > kFar || offset < -kFar) return ADASUM_ERR_UNSUPPORTED;
+  if (batch > 0 && heads > 0 && queries > 0 && keys > 0 && batch > INT64_MAX / 16 / heads / queries / keys)
+    return ADASUM_ERR_UNSUPPORTED;
+  return ADASUM_OK;
+}
+// Elements that strided scores reach over; -1: strides that overlap or cannot be addressed.
+int64_t span_of(int64_t batch, int64_t heads, int64_t queries, int64_t keys, int64_t sb, int64_t sh, int64_t sq) {
+  if ((queries > 1 && sq < keys) || (heads > 1 && sh < 0) || (batch > 1 && sb < 0)) return -1;
+  auto far = [](int64_t count, int64_t stride) { return count > 1 && stride > INT64_MAX / 64 / count; };
+  if (far(batch, sb) || far(heads, sh) || far(queries, sq)) return -1;
+  return (batch > 1 ? (batch - 1) * sb : 0) + (heads > 1 ? (heads - 1) * sh : 0) + (queries > 1 ? (queries - 1) * sq : 0) + keys;
+}
+
+template <typename T, bool SCORES>
+int launch_bias(const BiasArgs& a, bool vec, dim3 grid, cudaStream_t stream) {
+  constexpr int E = 16 / sizeof(T);
+  return launch_pdl(vec ? bias_kernel<T, E, true, SCORES> : bias_kernel<T, E, false, SCORES>, grid, dim3(kBiasThreads), 0, stream, a);
+}
+
+// Units of one worker and head, and how they are dealt.
+struct GradPlan {
+  int rows, row_units, key_units, batch_units, per_unit, groups;
+};
+GradPlan plan_grad(const int64_t* offs, int K, int64_t heads, int64_t queries, int64_t keys) {
+  GradPlan g = {};
+  int64_t most = 1;
+  for (int k = 0; k < K; ++k) most = std::max(most, offs[k + 1] - offs[k]);
+  // At most 16 sequences a unit, so that no running sum gets long.  Then queries: the fewer
+  // rows, the more warps share the work, down to 32 rows; enough is six CTAs an SM.
+  g.per_unit = static_cast<int>(std::min<int64_t>(most, 16));
+  const int64_t batch_units = (most + g.per_unit - 1) / g.per_unit, key_units = (keys + kBiasKeys - 1) / kBiasKeys;
+  const int64_t enough = static_cast<int64_t>(6) * kBiasWarps * sm_count();
+  g.rows = kBiasRows;
+  while (g.rows > 32 && K * heads * batch_units * key_units * ((queries + g.rows - 1) / g.rows) < enough) g.rows /= 2;
+  g.row_units = static_cast<int>((queries + g.rows - 1) / g.rows);
+  g.key_units = static_cast<int>(key_units);
+  g.batch_units = static_cast<int>(std::min<int64_t>(batch_units, INT32_MAX));
+  const int64_t units = static_cast<int64_t>(g.row_units) * key_units * batch_units;
+  g.groups = units > (int64_t(1) << 30) ? -1 : static_cast<int>((units + kBiasWarps - 1) / kBiasWarps);
+  return g;
+}
+
+}  // namespace
+}  // namespace adasum
+
+using namespace adasum;
+
+extern "C" {
+
+adasum_status_t adasum_relative_position_bias(const void* table, int buckets, int64_t heads, adasum_dtype_t table_dtype,
+                                              int bidirectional, int64_t max_distance, int64_t offset, int64_t queries,
+                                              int64_t keys, const void* scores, int64_t batch, int64_t stride_b,
+                                              int64_t stride_h, int64_t stride_q, adasum_dtype_t dtype, void* out,
+                                              adasum_stream_t stream_) {
+  EntryScope scope("adasum_relative_position_bias");
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!valid_dtype(table_dtype) || (scores != nullptr && !valid_dtype(dtype))) return ADASUM_ERR_INVALID_ARG;
+  if (scores == nullptr) batch = 1, dtype = table_dtype;
+  if (adasum_status_t st = check_sizes(heads, batch, queries, keys, offset)) return st;
+  BiasArgs a = {};
+  if (adasum_status_t st = make_buckets(a.buckets, buckets, bidirectional, max_distance)) return st;
+  if (heads == 0 || batch == 0 || queries == 0 || keys == 0) return ADASUM_OK;
+  if (table == nullptr || out == nullptr) return ADASUM_ERR_INVALID_ARG;
+  const int64_t e = dtype_bytes(dtype), te = dtype_bytes(table_dtype), n = heads * queries * keys;
+  const int64_t span = scores ? span_of(batch, heads, queries, keys, stride_b, stride_h, stride_q) : 0;
+  if (span < 0) return ADASUM_ERR_INVALID_ARG;
+  const bool dense = (queries == 1 || stride_q == keys) && (heads == 1 || stride_h == queries * keys) && (batch == 1 || stride_b == n);
+  BufferSet set;
+  set.read(table, buckets * heads * te, te);
+  if (scores != nullptr && !(scores == out && dense)) set.read(scores, span * e, e);
+  set.write(out, batch * n * e, e);
+  if (adasum_status_t st = set.check()) return st;
+  a.table = table;
+  a.table_dtype = table_dtype;
+  a.heads = heads;
+  a.batch = batch;
+  a.queries = queries;
+  a.keys = keys;
+  a.offset = offset;
+  a.scores = scores;
+  a.stride_b = stride_b;
+  a.stride_h = stride_h;
+  a.stride_q = stride_q;
+  a.out = out;
+  a.row_groups = queries > 16 ? 8 : queries > 8 ? 4 : queries > 4 ? 2 : 1;
+  const int64_t width = 32 * (16 / e), tiles = (keys + width - 1) / width, rows = 4 * a.row_groups;
+  const int64_t x = tiles * ((queries + rows - 1) / rows), step = kBiasWarps / a.row_groups;
+  if (x > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
+  // sequences of a CTA: as many as leave eight CTAs an SM, so that the biases serve many of them
+  int64_t parts = std::max<int64_t>(1, std::min<int64_t>((batch + step - 1) / step, static_cast<int64_t>(8) * sm_count() / (x * heads)));
+  parts = std::max(parts, (batch + (int64_t(1) << 16) - 1) >> 16);
+  a.per_cta = (batch + parts - 1) / parts;
+  parts = (batch + a.per_cta - 1) / a.per_cta;
+  if (parts > 65535) return ADASUM_ERR_UNSUPPORTED;
+  const bool vec = is_aligned(out, 16) && keys * e % 16 == 0 &&
+                   (scores == nullptr || (is_aligned(scores, 16) && (queries == 1 || stride_q * e % 16 == 0) &&
+                                          (heads == 1 || stride_h * e % 16 == 0) && (batch == 1 || stride_b * e % 16 == 0)));
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(heads), static_cast<unsigned>(parts));
+  return counted_launch(stream, scores ? "position_bias_add" : "position_bias", static_cast<double>(batch) * n * e * (scores ? 2 : 1), [&] {
+    if (dtype == ADASUM_BF16) return scores ? launch_bias<bf16, true>(a, vec, grid, stream) : launch_bias<bf16, false>(a, vec, grid, stream);
+    return scores ? launch_bias<float, true>(a, vec, grid, stream) : launch_bias<float, false>(a, vec, grid, stream);
+  });
+}
+
+int64_t adasum_relative_position_bias_backward_scratch_bytes(const int64_t* worker_offsets, int K, int64_t heads,
+                                                             int64_t queries, int64_t keys, int buckets) {
+  if (check_worker_offsets(worker_offsets, K) || buckets < 1 || buckets > kMaxBuckets) return 0;
+  if (check_sizes(heads, worker_offsets[K], queries, keys, 0) || heads == 0 || worker_offsets[K] == 0 || queries == 0 || keys == 0) return 0;
+  const GradPlan g = plan_grad(worker_offsets, K, heads, queries, keys);
+  return g.groups <= 1 ? 0 : (static_cast<int64_t>(K) * heads * g.groups * buckets * 4 + 255) / 256 * 256;
+}
+
+adasum_status_t adasum_relative_position_bias_backward(const void* grad_scores, int64_t heads, int64_t queries, int64_t keys,
+                                                       int64_t stride_b, int64_t stride_h, int64_t stride_q,
+                                                       adasum_dtype_t dtype, int buckets, int bidirectional,
+                                                       int64_t max_distance, int64_t offset, const int64_t* worker_offsets,
+                                                       int K, void* const* grads, adasum_dtype_t grad_dtype, int accumulate,
+                                                       void* scratch, int64_t scratch_bytes, adasum_stream_t stream_) {
+  EntryScope scope("adasum_relative_position_bias_backward");
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (adasum_status_t st = check_worker_offsets(worker_offsets, K)) return st;
+  if (!valid_dtype(dtype) || !valid_dtype(grad_dtype) || grads == nullptr) return ADASUM_ERR_INVALID_ARG;
+  const int64_t batch = worker_offsets[K];
+  if (adasum_status_t st = check_sizes(heads, batch, queries, keys, offset)) return st;
+  BiasGradArgs a = {};
+  BiasOut o = {};
+  if (adasum_status_t st = make_buckets(a.buckets, buckets, bidirectional, max_distance)) return st;
+  if (heads == 0) return ADASUM_OK;
+  const int64_t e = dtype_bytes(dtype), ge = dtype_bytes(grad_dtype);
+  const bool some = batch > 0 && queries > 0 && keys > 0;
+  const int64_t span = some ? span_of(batch, heads, queries, keys, stride_b, stride_h, stride_q) : 0;
+  if (span < 0 || (some && grad_scores == nullptr)) return ADASUM_ERR_INVALID_ARG;
+  const int64_t need = adasum_relative_position_bias_backward_scratch_bytes(worker_offsets, K, heads, queries, keys, buckets);
+  if (need > 0 && (scratch == nullptr || scratch_bytes < need || !is_aligned(scratch, 256))) return ADASUM_ERR_INVALID_ARG;
+  BufferSet set;
+  set.read(grad_scores, span * e, e);
+  if (need > 0) set.write(scratch, need, 256);
+  for (int k = 0; k < K; ++k) {
+    if (grads[k] == nullptr) return ADASUM_ERR_INVALID_ARG;
+    set.write(o.grads[k] = grads[k], buckets * heads * ge, ge);
+  }
+  if (adasum_status_t st = set.check()) return st;
+  if (!some && accumulate) return ADASUM_OK;
+  const GradPlan g = plan_grad(worker_offsets, K, heads, some ? queries : 1, some ? keys : 1);
+  if (g.groups < 0) return ADASUM_ERR_UNSUPPORTED;
+  a.d = grad_scores;
+  a.stride_b = stride_b;
+  a.stride_h = stride_h;
+  a.stride_q = stride_q;
+  a.heads = heads;
+  a.queries = queries;
+  a.keys = keys;
+  a.offset = offset;
+  a.rows = g.rows;
+  a.row_units = g.row_units;
+  a.key_units = g.key_units;
+  a.batch_units = some ? g.batch_units : 0;  // (no units: every sum is zero)
+  a.per_unit = g.per_unit;
+  a.groups = some ? g.groups : 1;
+  a.partials = a.groups > 1 ? static_cast<float*>(scratch) : nullptr;
+  a.total = buckets;
+  std::copy(worker_offsets, worker_offsets + K + 1, a.off);
+  o.dtype = grad_dtype;
+  o.accumulate = accumulate != 0;
+  o.heads = heads;
+  o.total = buckets;
+  o.groups = a.groups;
+  o.partials = a.partials;
+  const bool vec = is_aligned(grad_scores, 16) && (queries <= 1 || stride_q * e % 16 == 0) && (heads == 1 || stride_h * e % 16 == 0) &&
+                   (batch <= 1 || stride_b * e % 16 == 0);
+  const dim3 grid(static_cast<unsigned>(a.groups), static_cast<unsigned>(heads), static_cast<unsigned>(K));
+  adasum_status_t st = counted_launch(stream, "position_bias_grad", static_cast<double>(batch) * heads * queries * keys * e, [&] {
+    if (dtype == ADASUM_BF16)
+      return launch_pdl(vec ? bias_grad_kernel<bf16, true> : bias_grad_kernel<bf16, false>, grid, dim3(kBiasThreads), 0, stream, a, o);
+    return launch_pdl(vec ? bias_grad_kernel<float, true> : bias_grad_kernel<float, false>, grid, dim3(kBiasThreads), 0, stream, a, o);
+  });
+  if (st || a.partials == nullptr) return st;
+  return counted_launch(stream, "position_bias_join", 0.0, [&] {
+    return launch_pdl(bias_join_kernel, dim3(static_cast<unsigned>((buckets + 31) / 32), static_cast<unsigned>(heads), static_cast<unsigned>(K)),
+                      dim3(256), 0, stream, o);
+  });
+}
+
+}  // extern "C"

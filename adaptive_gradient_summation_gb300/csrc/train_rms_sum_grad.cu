@@ -1,0 +1,11 @@
+// train_rms_sum_grad.cu -- the gradient of the root-mean-square norm with the gradient that
+// reaches its input past it (kernels: adasum_norm.cuh).
+#include "adasum_norm.cuh"
+
+namespace adasum {
+
+int launch_rms_sum_grad(const NormGradArgs& a, int dtype, bool vec, const WorkerRows& rows, const ParamGradArgs& p, cudaStream_t stream) {
+  return launch_norm_grad_of<kRmsSum>(a, dtype, vec, rows, p, stream);
+}
+
+}  // namespace adasum

@@ -1,4 +1,5 @@
 """Operators of the training step around the Adasum combine: token embeddings, layer norm,
+root-mean-square norm with the residual's addition, the relative position bias of attention scores,
 and activations kept in 8 bits between the forward and the backward pass.
 
 Parameter gradients come per worker.  The rows of a call (all leading dimensions of a
@@ -29,7 +30,9 @@ from ._native import check, load_library
 
 __all__ = ["Checkpoint", "checkpoint_pack", "checkpoint_unpack", "embedding", "embedding_backward",
            "gelu_checkpointed", "gelu_checkpointed_backward", "layer_norm", "layer_norm_backward",
-           "layer_norm_checkpointed", "layer_norm_checkpointed_backward"]
+           "layer_norm_checkpointed", "layer_norm_checkpointed_backward", "relative_position_bias",
+           "relative_position_bias_backward", "rms_norm", "rms_norm_backward",
+           "rms_norm_checkpointed", "rms_norm_checkpointed_backward"]
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
 _DEVICES = [torch.device("cuda", i) for i in range(128)]
@@ -386,6 +389,216 @@ def layer_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Chec
     if st:
         check(st, "adasum_layer_norm_backward_checkpointed")
     return (dx, dw, db, y) if with_output else (dx, dw, db)
+
+
+# ------------------------------------------------------------------ root-mean-square norm
+
+
+def _like(t, x, code: int, index: int, what: str):
+    """(pointer, row stride) of an optional tensor like x; (None, 0) without one."""
+    if t is None:
+        return None, 0
+    if _kind(t, what) != (code, index) or t.shape != x.shape:
+        raise ValueError(f"{what} must have shape {tuple(x.shape)}, {x.dtype}, on cuda:{index}")
+    return t.data_ptr(), _rows(t, what)[2]
+
+
+def _rms_forward(call, keep: bool, x, weight, residual, eps, out, stream):
+    code, index = _kind(x, "x")
+    rows, cols, ld = _rows(x, "x")
+    w, _, wcode = _parameters(weight, None, cols, index)
+    residual_p, ld_r = _like(residual, x, code, index, "residual")
+    if _elsewhere(index, stream):
+        return _there(index, stream, call, x, weight, residual=residual, eps=eps, out=out)
+    y = _output(out, x.shape, x.dtype, index)
+    total = None if residual is None else torch.empty(x.shape, dtype=x.dtype, device=_DEVICES[index])
+    kept = _new_checkpoint(x, rows, cols) if keep else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=_DEVICES[index])
+    st = load_library().adasum_rms_norm(x.data_ptr(), rows, cols, ld, code, residual_p, ld_r, _ptr(total), w, wcode, float(eps),
+                                        y.data_ptr(), rstd.data_ptr(), kept.codes.data_ptr() if keep else None,
+                                        kept.scales.data_ptr() if keep else None, _raw_stream(index))
+    if st:
+        check(st, "adasum_rms_norm")
+    return (y,) + ((total,) if residual is not None else ()) + ((kept,) if keep else ()) + (rstd,)
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """Root-mean-square norm over the last dimension, with the residual's addition
+    (``adasum_rms_norm``): ``(y, rstd)``, or with a residual ``(y, total, rstd)``, where total
+    is ``x + residual`` in x's dtype, which is normalised and goes on as the next residual."""
+    return _rms_forward(rms_norm, False, x, weight, residual, eps, out, stream)
+
+
+def rms_norm_checkpointed(x: torch.Tensor, weight: torch.Tensor | None = None, *, residual: torch.Tensor | None = None,
+                          eps: float = 1e-6, out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """The same, keeping ``h = total * rstd`` in 8 bits: ``(y, checkpoint, rstd)``, or with a
+    residual ``(y, total, checkpoint, rstd)``, for :func:`rms_norm_checkpointed_backward`."""
+    return _rms_forward(rms_norm_checkpointed, True, x, weight, residual, eps, out, stream)
+
+
+def _weight_gradients(grad_weights, weight, wanted, accumulate, offs, K, cols, index):
+    """(weights' gradients, their pointers, code, scratch bytes, scratch)."""
+    if not wanted:
+        if grad_weights is not None:
+            raise ValueError("grad_weights is not written with parameter_grads=False")
+        return None, None, 0, 0, None
+    if accumulate and grad_weights is None:
+        raise ValueError("accumulate needs grad_weights to add to")
+    dw, dwp, dtype = _gradients(grad_weights, K, cols, index, torch.float32 if weight is None else weight.dtype, (cols,),
+                                "grad_weights")
+    nbytes = load_library().adasum_rms_norm_backward_scratch_bytes(_address(offs), K, cols)
+    return dw, dwp, _CODE[dtype], nbytes, _scratch(nbytes, index)
+
+
+def rms_norm_backward(grad_output: torch.Tensor, x: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor | None = None, *,
+                      grad_residual: torch.Tensor | None = None, worker_offsets=None, grad_weights=None,
+                      accumulate: bool = False, parameter_grads: bool = True, stream: torch.cuda.Stream | None = None):
+    """``(grad_x, grad_weights)`` of the root-mean-square norm (``adasum_rms_norm_backward``).
+
+    x: what was normalised (with a residual, the total).  grad_residual: the gradient that
+    reaches the total past the norm, which is added; grad_x is then the gradient of the forward
+    call's x and of its residual alike.  grad_weights: K contiguous tensors of cols elements (one dtype;
+    None allocates them, in weight's dtype, else float32), overwritten, or with ``accumulate``
+    added to; returned as a list.  ``parameter_grads=False`` leaves them out (None).
+    """
+    code, index = _kind(x, "x")
+    grad_p, ld_g = _like(grad_output, x, code, index, "grad_output")
+    rows, cols, ld_x = _rows(x, "x")
+    past_p, ld_p = _like(grad_residual, x, code, index, "grad_residual")
+    w, _, wcode = _parameters(weight, None, cols, index)
+    rstd_p = _statistic(rstd, rows, index, "rstd")
+    if _elsewhere(index, stream):
+        return _there(index, stream, rms_norm_backward, grad_output, x, rstd, weight, grad_residual=grad_residual,
+                      worker_offsets=worker_offsets, grad_weights=grad_weights, accumulate=accumulate,
+                      parameter_grads=parameter_grads)
+    offs, K = _workers(worker_offsets, rows)
+    dw, dwp, gcode, nbytes, scratch = _weight_gradients(grad_weights, weight, parameter_grads, accumulate, offs, K, cols, index)
+    dx = _output(None, x.shape, x.dtype, index)
+    st = load_library().adasum_rms_norm_backward(
+        grad_p, ld_g, x.data_ptr(), ld_x, rstd_p, cols, code, w, wcode, past_p, ld_p, _address(offs), K, dx.data_ptr(),
+        _address(dwp), gcode, bool(accumulate), _ptr(scratch), nbytes, _raw_stream(index))
+    if st:
+        check(st, "adasum_rms_norm_backward")
+    return dx, dw
+
+
+def rms_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Checkpoint, rstd: torch.Tensor,
+                                   weight: torch.Tensor | None = None, *, grad_residual: torch.Tensor | None = None,
+                                   worker_offsets=None, grad_weights=None, accumulate: bool = False,
+                                   parameter_grads: bool = True, with_output: bool = False,
+                                   stream: torch.cuda.Stream | None = None):
+    """``(grad_x, grad_weights)`` of the root-mean-square norm from the 8-bit checkpoint of h
+    (``adasum_rms_norm_backward_checkpointed``); with ``with_output`` also the output again, as
+    a third.  The rest as in :func:`rms_norm_backward`."""
+    code, index = _kind(grad_output, "grad_output")
+    rows, cols, ld_g = _rows(grad_output, "grad_output")
+    codes, scales = _check_checkpoint(checkpoint, index, grad_output)
+    past_p, ld_p = _like(grad_residual, grad_output, code, index, "grad_residual")
+    w, _, wcode = _parameters(weight, None, cols, index)
+    rstd_p = _statistic(rstd, rows, index, "rstd")
+    if _elsewhere(index, stream):
+        return _there(index, stream, rms_norm_checkpointed_backward, grad_output, checkpoint, rstd, weight,
+                      grad_residual=grad_residual, worker_offsets=worker_offsets, grad_weights=grad_weights,
+                      accumulate=accumulate, parameter_grads=parameter_grads, with_output=with_output)
+    offs, K = _workers(worker_offsets, rows)
+    dw, dwp, gcode, nbytes, scratch = _weight_gradients(grad_weights, weight, parameter_grads, accumulate, offs, K, cols, index)
+    dx = _output(None, grad_output.shape, grad_output.dtype, index)
+    y = _output(None, dx.shape, dx.dtype, index) if with_output else None
+    st = load_library().adasum_rms_norm_backward_checkpointed(
+        grad_output.data_ptr(), ld_g, codes, scales, rstd_p, cols, code, w, wcode, past_p, ld_p, _address(offs), K,
+        dx.data_ptr(), _ptr(y), _address(dwp), gcode, bool(accumulate), _ptr(scratch), nbytes, _raw_stream(index))
+    if st:
+        check(st, "adasum_rms_norm_backward_checkpointed")
+    return (dx, dw, y) if with_output else (dx, dw)
+
+
+# ------------------------------------------------------------------ relative position bias
+
+
+def _scores(t: torch.Tensor, what: str):
+    """The shape (batch, heads, queries, keys) of a tensor, and its first three strides."""
+    if t.dim() != 4:
+        raise ValueError(f"{what} must have shape (batch, heads, queries, keys)")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{what} must have its keys next to each other")
+    if t.numel() and any(size > 1 and stride < 1 for size, stride in zip(t.shape, t.stride())):
+        raise ValueError(f"{what} must not repeat elements")
+    return t.shape, t.stride()[:3]
+
+
+def relative_position_bias(table: torch.Tensor, queries: int, keys: int, *, bidirectional: bool = True, max_distance: int = 128,
+                           offset: int = 0, scores: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                           stream: torch.cuda.Stream | None = None) -> torch.Tensor:
+    """The learned bias of attention scores by the relative position of query and key, in
+    buckets (``adasum_relative_position_bias``): ``scores + bias`` in scores' shape and dtype, or
+    without scores the bias, of shape (heads, queries, keys) in the table's dtype.
+
+    table: (buckets, heads).  Key j stands ``j - i - offset`` from query i; offset counts the
+    keys before the first query's own (for one new token: the keys in the cache).  Near distances have
+    a bucket each, farther ones share buckets that grow up to max_distance.  bidirectional: half
+    of the buckets for keys ahead; otherwise those take bucket 0.  scores: (batch, heads,
+    queries, keys), their keys next to each other; out may be scores itself if it is contiguous.
+    """
+    tcode, index = _kind(table, "table")
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous matrix")
+    buckets, heads = table.shape
+    if queries < 0 or keys < 0:
+        raise ValueError("queries and keys must not be negative")
+    code, batch, strides, p = tcode, 1, (0, 0, 0), None
+    if scores is not None:
+        code, at = _kind(scores, "scores")
+        shape, strides = _scores(scores, "scores")
+        if at != index or shape[1:] != (heads, queries, keys):
+            raise ValueError(f"scores must have shape (batch, {heads}, {queries}, {keys}), on cuda:{index}")
+        batch = shape[0]
+        p = scores.data_ptr() or table.data_ptr()  # (an empty batch is no call for the bias alone)
+    if _elsewhere(index, stream):
+        return _there(index, stream, relative_position_bias, table, queries, keys, bidirectional=bidirectional,
+                      max_distance=max_distance, offset=offset, scores=scores, out=out)
+    like = table if scores is None else scores
+    out = _output(out, (heads, queries, keys) if scores is None else scores.shape, like.dtype, index)
+    st = load_library().adasum_relative_position_bias(
+        table.data_ptr(), buckets, heads, tcode, bool(bidirectional), max_distance, offset, queries, keys, p, batch, *strides, code,
+        out.data_ptr(), _raw_stream(index))
+    if st:
+        check(st, "adasum_relative_position_bias")
+    return out
+
+
+def relative_position_bias_backward(grad_scores: torch.Tensor, num_buckets: int, *, bidirectional: bool = True,
+                                    max_distance: int = 128, offset: int = 0, worker_offsets=None, grads=None,
+                                    accumulate: bool = False, stream: torch.cuda.Stream | None = None) -> list:
+    """The gradient of the bias' table, per worker (``adasum_relative_position_bias_backward``):
+    a list of K tensors of shape (num_buckets, heads).
+
+    grad_scores: (batch, heads, queries, keys); every value counts, so masked ones have to be zero.
+    worker_offsets: K+1 offsets into the batch (None: one worker).  grads: K contiguous tensors
+    of num_buckets * heads elements (of any one dtype; None allocates them in grad_scores'),
+    overwritten, or with ``accumulate`` added to.
+    """
+    code, index = _kind(grad_scores, "grad_scores")
+    (batch, heads, queries, keys), strides = _scores(grad_scores, "grad_scores")
+    if num_buckets < 1:
+        raise ValueError("num_buckets must be positive")
+    if grads is None and accumulate:
+        raise ValueError("accumulate needs grads to add to")
+    if _elsewhere(index, stream):
+        return _there(index, stream, relative_position_bias_backward, grad_scores, num_buckets, bidirectional=bidirectional,
+                      max_distance=max_distance, offset=offset, worker_offsets=worker_offsets, grads=grads,
+                      accumulate=accumulate)
+    offs, K = _workers(worker_offsets, batch)
+    grads, ptrs, gtype = _gradients(grads, K, num_buckets * heads, index, grad_scores.dtype, (num_buckets, heads), "grads")
+    lib = load_library()
+    nbytes = lib.adasum_relative_position_bias_backward_scratch_bytes(_address(offs), K, heads, queries, keys, num_buckets)
+    scratch = _scratch(nbytes, index)
+    st = lib.adasum_relative_position_bias_backward(
+        grad_scores.data_ptr(), heads, queries, keys, *strides, code, num_buckets, bool(bidirectional), max_distance, offset,
+        _address(offs), K, _address(ptrs), _CODE[gtype], bool(accumulate), _ptr(scratch), nbytes, _raw_stream(index))
+    if st:
+        check(st, "adasum_relative_position_bias_backward")
+    return grads
 
 
 # --------------------------------------------------------------------- 8-bit checkpoints

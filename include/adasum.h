@@ -431,6 +431,61 @@ ADASUM_API adasum_status_t adasum_layer_norm_backward_checkpointed(
     int accumulate, void *scratch, int64_t scratch_bytes, adasum_stream_t stream);
 
 /*
+ * adasum_rms_norm -- root-mean-square norm, with the residual's addition: per row
+ * t = x + residual (rounded to dtype; x itself without a residual), rstd =
+ * 1/sqrt(mean(t^2) + eps), h = t rstd, y = h weight.
+ *   x             rows x cols elements of dtype, ld apart; cols <= ADASUM_NORM_MAX_COLS
+ *   residual      NULL, or rows x cols elements of dtype, ld_residual apart
+ *   total         t, rows x cols elements of dtype; NULL exactly if residual is
+ *   weight        cols elements of weight_dtype; NULL: 1
+ *   y             rows x cols elements of dtype
+ *   rstd          rows floats for the backward pass, or NULL
+ *   codes, scales both NULL, or the 8-bit checkpoint of h (adasum_checkpoint_pack's
+ *                 format): with it the backward pass does not need t
+ */
+ADASUM_API adasum_status_t adasum_rms_norm(const void *x, int64_t rows, int64_t cols, int64_t ld,
+                                           adasum_dtype_t dtype, const void *residual,
+                                           int64_t ld_residual, void *total, const void *weight,
+                                           adasum_dtype_t weight_dtype, float eps, void *y,
+                                           float *rstd, int8_t *codes, float *scales,
+                                           adasum_stream_t stream);
+
+/*
+ * adasum_rms_norm_backward -- with h = x rstd (x: what was normalised, so t) and
+ * g = grad_out * weight,
+ *     grad_x = grad_residual + rstd (g - h mean(g h)),
+ *     grad_weights[k] = sum of grad_out h over worker k's rows.
+ *   grad_residual NULL, or rows x cols elements of dtype, ld_residual apart: the gradient
+ *                 that reaches t past the norm.  grad_x is then the gradient of the forward
+ *                 pass's x and of its residual alike
+ *   grad_weights  host array of K device pointers to cols elements of grad_dtype; NULL: not
+ *                 wanted
+ *   scratch       adasum_rms_norm_backward_scratch_bytes(worker_offsets, K, cols); may be
+ *                 NULL when that is 0 (few rows) or the weights' gradients are not wanted
+ */
+ADASUM_API adasum_status_t adasum_rms_norm_backward(
+    const void *grad_out, int64_t ld_grad, const void *x, int64_t ld_x, const float *rstd,
+    int64_t cols, adasum_dtype_t dtype, const void *weight, adasum_dtype_t weight_dtype,
+    const void *grad_residual, int64_t ld_residual, const int64_t *worker_offsets, int K,
+    void *grad_x, void *const *grad_weights, adasum_dtype_t grad_dtype, int accumulate,
+    void *scratch, int64_t scratch_bytes, adasum_stream_t stream);
+ADASUM_API int64_t adasum_rms_norm_backward_scratch_bytes(const int64_t *worker_offsets, int K,
+                                                          int64_t cols);
+
+/*
+ * adasum_rms_norm_backward_checkpointed -- the same from the 8-bit checkpoint of h.
+ *   y             NULL, or rows x cols elements of dtype: h weight, the forward pass's output
+ *                 again
+ */
+ADASUM_API adasum_status_t adasum_rms_norm_backward_checkpointed(
+    const void *grad_out, int64_t ld_grad, const int8_t *codes, const float *scales,
+    const float *rstd, int64_t cols, adasum_dtype_t dtype, const void *weight,
+    adasum_dtype_t weight_dtype, const void *grad_residual, int64_t ld_residual,
+    const int64_t *worker_offsets, int K, void *grad_x, void *y, void *const *grad_weights,
+    adasum_dtype_t grad_dtype, int accumulate, void *scratch, int64_t scratch_bytes,
+    adasum_stream_t stream);
+
+/*
  * adasum_checkpoint_pack -- 8-bit checkpoint of an activation.  Every row is cut into
  * blocks of 128 columns (the last may be shorter).  A block with the largest magnitude m
  * gets the scale m / 127 and the codes q = round(x * (127 / m)), ties to even, and stands
@@ -468,6 +523,51 @@ ADASUM_API adasum_status_t adasum_gelu_checkpointed_backward(
     const void *grad_out, int64_t ld_grad, const int8_t *codes, const float *scales, int64_t rows,
     int64_t cols, adasum_dtype_t dtype, int tanh_form, void *grad_x, void *y,
     adasum_stream_t stream);
+
+/*
+ * Relative position bias of attention scores by buckets.  Score (b, h, i, j) of query i and key
+ * j gets table[bucket(j - i - offset)][h].  With `buckets` rows in the table, n = buckets / 2 for
+ * each direction (bidirectional: keys ahead, j > i + offset, take the rows from n on; buckets
+ * is even) or n = buckets (keys ahead all take row 0).  A distance d below e = n / 2 has a row of
+ * its own; beyond, the row is
+ *     e + floor((n - e) ln(d / e) / ln(max_distance / e)),  at most n - 1,
+ * of the exact value (borders that are whole distances belong to the farther row).
+ *   table         buckets x heads elements of table_dtype; 2 <= n, buckets <=
+ *                 ADASUM_BIAS_MAX_BUCKETS, n / 2 < max_distance < 2^31
+ *   offset        keys before the first query's own (queries that follow a cache); |offset| <=
+ *                 2^61
+ *   scores        element (b, h, i, j) at b * stride_b + h * stride_h + i * stride_q + j
+ *
+ * adasum_relative_position_bias -- out = scores + bias, batch x heads x queries x keys elements
+ * of dtype, dense, rounded once; with scores = NULL the bias alone, heads x queries x keys of
+ * table_dtype.  out may be scores itself where that is dense.  heads <= 65535, queries and keys
+ * below 2^31.
+ */
+#define ADASUM_BIAS_MAX_BUCKETS 256
+ADASUM_API adasum_status_t adasum_relative_position_bias(
+    const void *table, int buckets, int64_t heads, adasum_dtype_t table_dtype, int bidirectional,
+    int64_t max_distance, int64_t offset, int64_t queries, int64_t keys, const void *scores,
+    int64_t batch, int64_t stride_b, int64_t stride_h, int64_t stride_q, adasum_dtype_t dtype,
+    void *out, adasum_stream_t stream);
+
+/*
+ * adasum_relative_position_bias_backward -- the gradient of the table, per worker: grads[k] is
+ * buckets x heads, the sums of grad_scores over worker k's sequences (worker_offsets counts
+ * sequences of the batch) and each bucket's queries and keys.  Every value counts, so what
+ * attention has masked must be zero, as a softmax's gradient leaves it.
+ *   grad_scores   worker_offsets[K] sequences, laid out like scores above
+ *   scratch       adasum_relative_position_bias_backward_scratch_bytes(worker_offsets, K,
+ *                 heads, queries, keys, buckets); may be NULL when that is 0
+ */
+ADASUM_API adasum_status_t adasum_relative_position_bias_backward(
+    const void *grad_scores, int64_t heads, int64_t queries, int64_t keys, int64_t stride_b,
+    int64_t stride_h, int64_t stride_q, adasum_dtype_t dtype, int buckets, int bidirectional,
+    int64_t max_distance, int64_t offset, const int64_t *worker_offsets, int K,
+    void *const *grads, adasum_dtype_t grad_dtype, int accumulate, void *scratch,
+    int64_t scratch_bytes, adasum_stream_t stream);
+ADASUM_API int64_t adasum_relative_position_bias_backward_scratch_bytes(
+    const int64_t *worker_offsets, int K, int64_t heads, int64_t queries, int64_t keys,
+    int buckets);
 
 /* ---- Orthogonalised updates ------------------------------------------------------- */
 
