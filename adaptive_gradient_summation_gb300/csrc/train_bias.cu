@@ -167,7 +167,7 @@ __device__ __forceinline__ void put_bucket(const BiasOut& o, int k, int64_t h, i
 // GRADFIGURES
 // VEC: a lane's eight keys are neighbours on 16-byte boundaries; else they are 32 apart.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBiasThreads, 4) bias_grad_kernel(const __grid_constant__ BiasGradArgs a, const __grid_constant__ BiasOut o) {
+__global__ void __launch_bounds__(kBiasThreads, VEC ? 2 : 3) bias_grad_kernel(const __grid_constant__ BiasGradArgs a, const __grid_constant__ BiasOut o) {
   pdl_enter();
   __shared__ float diagonals[kBiasWarps][kBiasRows + kBiasKeys];
   __shared__ float sums[kBiasWarps][kMaxBuckets];
@@ -186,53 +186,73 @@ __global__ void __launch_bounds__(kBiasThreads, 4) bias_grad_kernel(const __grid
     const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.queries - q0));
     const int width = static_cast<int>(min(static_cast<int64_t>(kBiasKeys), a.keys - k0));
     const T* p = static_cast<const T*>(a.d) + b0 * a.stride_b + h * a.stride_h + q0 * a.stride_q + k0;
-    const int64_t back = a.stride_q - (nb - 1) * a.stride_b;
-    const int count = rows * nb;  // rows of 256 keys, sequence by sequence, query by query
-    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+    // rows of 256 keys, query by query, kGroup sequences at a time, two groups on their way
+    constexpr int kGroup = sizeof(T) == 2 && VEC ? 4 : 2;
     struct Row {
       uint32_t w[VEC ? sizeof(T) * 2 : 8];
-    } row[kAhead];
+    };
+    struct Group {
+      Row row[kGroup];
+    } ahead[2];
+    const int per_query = (nb + kGroup - 1) / kGroup, count = rows * per_query;
+    const bool whole = !VEC || lane * 8 + 8 <= width;
+    const T* pb = p + (VEC ? lane * 8 : lane);
+    p = pb;
     int next_b = 0, next = 0;
-    auto fetch = [&](Row& f) {
+    auto fetch = [&](Group& g) {
       if (next >= count) return;
-      if constexpr (VEC) {
-        constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes
-        const T* at = p + lane * 8;
-        if (lane * 8 + 8 <= width) {
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            const uint4 x = __ldcs(reinterpret_cast<const uint4*>(at) + i);
-            f.w[4 * i] = x.x, f.w[4 * i + 1] = x.y, f.w[4 * i + 2] = x.z, f.w[4 * i + 3] = x.w;
+      for (int s = 0; s < kGroup; ++s) {
+        Row& f = g.row[s];
+        const T* at = pb + s * a.stride_b;
+        const bool on = next_b + s < nb;
+        if constexpr (VEC) {
+          constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              const uint4 x = on ? __ldcs(reinterpret_cast<const uint4*>(at) + i) : make_uint4(0u, 0u, 0u, 0u);
+              f.w[4 * i] = x.x, f.w[4 * i + 1] = x.y, f.w[4 * i + 2] = x.z, f.w[4 * i + 3] = x.w;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t x = on && lane * 8 + e < width ? __float_as_uint(widen(at[e])) : 0u;
+              if constexpr (sizeof(T) == 4) f.w[e] = x;
+              else f.w[e >> 1] = e & 1 ? f.w[e >> 1] | x : x >> 16;
+            }
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = lane * 8 + e < width ? widen(at[e]) : 0.f;
-            if constexpr (sizeof(T) == 4) f.w[e] = __float_as_uint(x);
-            else f.w[e >> 1] = e & 1 ? f.w[e >> 1] | (__float_as_uint(x) & 0xFFFF0000u) : __float_as_uint(x) >> 16;
-          }
+          for (int e = 0; e < 8; ++e) f.w[e] = on && lane + 32 * e < width ? __float_as_uint(widen(at[32 * e])) : 0u;
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f.w[e] = lane + 32 * e < width ? __float_as_uint(widen(p[lane + 32 * e])) : 0u;
       }
       ++next;
-      if (++next_b == nb) next_b = 0, p += back;
-      else p += a.stride_b;
+      next_b += kGroup;
+      pb += kGroup * a.stride_b;
+      if (next_b >= nb) next_b = 0, pb = p += a.stride_q;
     };
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    int b = 0, done = 0;  // sequences of this query, queries
+    int groups_left = per_query, done = 0;  // of this query; queries
     // slot of the diagonal that key i of the window is on, at the last of the unit's queries
-    auto take = [&](const Row& f) {
+    auto take = [&](const Group& g) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (!VEC || sizeof(T) == 4) acc[e] += __uint_as_float(f.w[e]);
-        else acc[e] += __uint_as_float(e & 1 ? f.w[e >> 1] & 0xFFFF0000u : f.w[e >> 1] << 16);
+      for (int s = 0; s < kGroup; ++s) {
+        const Row& f = g.row[s];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          F2 x;
+          if constexpr (!VEC || sizeof(T) == 4) x = f2(__uint_as_float(f.w[e]), __uint_as_float(f.w[e + 1]));
+          else x = f2(__uint_as_float(f.w[e >> 1] << 16), __uint_as_float(f.w[e >> 1] & 0xFFFF0000u));
+          const float2 y = parts(add2(f2(acc[e], acc[e + 1]), x));
+          acc[e] = y.x;
+          acc[e + 1] = y.y;
+        }
       }
-      if (++b < nb) return;
-      b = 0;
+      if (--groups_left > 0) return;
+      groups_left = per_query;
       if (++done == rows) return;
       if constexpr (VEC) {
         if (lane == 31) mine[kBiasKeys - 1 + rows - done] = acc[7];
@@ -250,16 +270,16 @@ __global__ void __launch_bounds__(kBiasThreads, 4) bias_grad_kernel(const __grid
         acc[0] = lane == 0 ? 0.f : in[0];
       }
     };
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(row[i]);
-    for (int at = 0; at < count; at += kAhead) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (at + i >= count) break;
-        const Row now = row[i];
-        fetch(row[i]);
-        take(now);
-      }
+    fetch(ahead[0]);
+    fetch(ahead[1]);
+    for (int at = 0; at < count; at += 2) {
+      Group now = ahead[0];
+      fetch(ahead[0]);
+      take(now);
+      if (at + 1 >= count) break;
+      now = ahead[1];
+      fetch(ahead[1]);
+      take(now);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) mine[VEC ? lane * 8 + e : lane + 32 * e] = acc[e];
@@ -427,12 +447,13 @@ GradPlan plan_grad(const int64_t* offs, int K, int64_t heads, int64_t queries, i
   int64_t most = 1;
   for (int k = 0; k < K; ++k) most = std::max(most, offs[k + 1] - offs[k]);
   // At most 16 sequences a unit, so that no running sum gets long.  Then queries: the fewer
-  // rows, the more warps share the work, down to 32 rows; enough is six CTAs an SM.
+  // rows, the more warps share the work, down to 8 rows; enough is two CTAs an SM
+  // (64 x 16 x 512 x 512 bf16 of 16 workers: 99 us, with four 105, with six and 32 rows 140).
   g.per_unit = static_cast<int>(std::min<int64_t>(most, 16));
   const int64_t batch_units = (most + g.per_unit - 1) / g.per_unit, key_units = (keys + kBiasKeys - 1) / kBiasKeys;
-  const int64_t enough = static_cast<int64_t>(6) * kBiasWarps * sm_count();
+  const int64_t enough = static_cast<int64_t>(2) * kBiasWarps * sm_count();
   g.rows = kBiasRows;
-  while (g.rows > 32 && K * heads * batch_units * key_units * ((queries + g.rows - 1) / g.rows) < enough) g.rows /= 2;
+  while (g.rows > 8 && K * heads * batch_units * key_units * ((queries + g.rows - 1) / g.rows) < enough) g.rows /= 2;
   g.row_units = static_cast<int>((queries + g.rows - 1) / g.rows);
   g.key_units = static_cast<int>(key_units);
   g.batch_units = static_cast<int>(std::min<int64_t>(batch_units, INT32_MAX));

@@ -12,8 +12,7 @@
 // the rounding errors of X that point into their directions: after five steps one rounding of
 // X to bf16 is 1e-2 to 1e-1 of the result's norm, to fp16 2e-3 to 2e-2 (random, power-law and
 // low-rank spectra).  So
-//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits; X in fp32 for the term a X,
-//     where the growing errors come from), a product is three
+//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits), a product is three
 //     products of them (the fourth, of the low parts, is below 2^-22): off by 5e-7 to 5e-6,
 //     where fp32 throughout is off by 2e-6 to 2e-5;
 //   bf16 results: products of the high parts alone, but X itself in both parts for the term
@@ -63,7 +62,6 @@ struct SourceArgs {
   float eps;
   bool vec;            // x and momentum lie on 16-byte boundaries
   __half *hi, *lo;     // the first X
-  float* full;         // null: not wanted
   int64_t m, n, ldx;
 };
 
@@ -220,7 +218,6 @@ __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, cons
     split_eight(x, h, l);
     *reinterpret_cast<uint4*>(a.hi + to) = h;
     *reinterpret_cast<uint4*>(a.lo + to) = l;
-    if (a.full) store_eight(a.full + to, 8, true, x);
   };
 #pragma unroll
   for (int r = line; r < 64; r += 32) {
@@ -263,16 +260,28 @@ __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, cons
 
 // ------------------------------------------------------------------------- products
 
-constexpr int kEpilogueWarps = 8;
-constexpr int kFlowThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kPitch = 33;  // floats between rows of a warp's 32 x 32 block in shared memory
+// The warps that take results out of TMEM and write them, in blocks of 32 rows and kCols columns.
+// TERMS = 1: eight with blocks of 32 columns, which have the next block's inputs on their way (16
+// warps with 16 columns: 24 x (4096 x 1024) in 2.47 ms against 1.69).  TERMS = 3: sixteen with 16
+// columns, since a tile's sums are in registers for a while (eight: 8.4 ms against 4.6).
+template <int TERMS>
+struct Epilogue {
+  static constexpr int kWarps = TERMS == 1 ? 8 : 16, kCols = TERMS == 1 ? 32 : 16;
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kGroups = kWarps / 4;               // of warps that share 32 rows
+  static constexpr int kOcts = kCols / 8, kRows = 32 / kOcts, kPasses = kOcts;  // lanes a row, rows at a time
+  static constexpr int kFloats = TERMS == 1 ? 32 * 33 : 32 * 16;  // of a block in shared memory
+  // Place of element (r, c) of the block: no two of a row-wise or column-wise access of a warp
+  // meet a bank (kCols = 16: two of the transposed one).
+  static __device__ __forceinline__ int place(int r, int c) { return TERMS == 1 ? r * 33 + c : r * 16 + (c ^ ((r >> 1) & 15)); }
+};
 
 // What the iteration of equal matrices needs: the operands' maps (boxes of 64 x 64) and places,
 // the tiles of a product, where the results go.
 struct FlowArgs {
   CUtensorMap x_map[2][2], a_map[2], b_map[2];  // [buffer][part], [part]
   __half *x[2][2], *a[2], *b[2];
-  float* full;                 // X in fp32 (TERMS = 3), replaced element by element
+  float *da, *db;              // A's and B's diagonals, times kScaleA and kScaleB
   int64_t ldx, lda;
   int m, n, batch, steps;
   int col_tiles[2], tiles[2];  // of A and B (lower triangle), of X
@@ -298,14 +307,14 @@ struct FlowShape {
   static constexpr int kPBytes = 128 * 128, kQBytes = kQRows * 128;  // of one part: 64 along the depth
   static constexpr int kStageBytes = kParts * (kPBytes + kQBytes);
   static constexpr int kStages = 196608 / kStageBytes < 6 ? 196608 / kStageBytes : 6;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * 32 * kPitch * 4;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + Epilogue<TERMS>::kWarps * Epilogue<TERMS>::kFloats * 4;
   static_assert(kSmem + 1024 <= 232448, "with the barriers, a CTA's shared memory");
-  static constexpr int kBuffers = 2;                                   // accumulators of the high parts
+  static constexpr int kBuffers = NT == 256 && TERMS == 3 ? 1 : 2;  // accumulators of the high parts
   static constexpr int kCross = kBuffers * NT;                       // column of the others'
   static constexpr int kUsed = kCross + (TERMS == 3 ? NT : 0);
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
-  static constexpr int kRun = TERMS == 3 ? 2 : 1 << 30;  // stages of 64
-  static constexpr int kBlocks = NT / 64;                // of 32 x 32, of an epilogue warp
+  static constexpr int kRun = TERMS == 3 ? 8 : 1 << 30;  // stages of 64 along the depth
+  static constexpr int kBlocks = NT / 64;  // of an epilogue warp
 };
 
 // Row tile r of a symmetric product has the column tiles up to the diagonal.
@@ -332,8 +341,9 @@ struct Tile {
 // A warp copies (TMA), a thread issues the products, eight warps take finished accumulators
 // out of TMEM.
 template <int CTAS, int NT, int TERMS>
-__global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_constant__ FlowArgs a, const __grid_constant__ Places places) {
+__global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(const __grid_constant__ FlowArgs a, const __grid_constant__ Places places) {
   using S = FlowShape<CTAS, NT, TERMS>;
+  using E = Epilogue<TERMS>;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], cross_empty;
@@ -343,11 +353,16 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], kEpilogueWarps * CTAS);
-    mbar_init(&cross_empty, kEpilogueWarps * CTAS);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], E::kWarps * CTAS);
+    mbar_init(&cross_empty, E::kWarps * CTAS);
     mbar_fence_init();
     stop = 0;
     copied = 0;
+    for (int i = 0; i < 4; ++i) {  // (of all maps; the second part's are zeros where there is none)
+      if (i & 1 && S::kParts == 1) continue;
+      tma_prefetch_map(&a.x_map[i >> 1][i & 1]);
+      tma_prefetch_map(i >> 1 ? &a.b_map[i & 1] : &a.a_map[i & 1]);
+    }
   }
   if (warp == 1) tmem_alloc<S::kCols, CTAS>(&tmem_slot);
   tc_fence_before();
@@ -372,7 +387,7 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
   };
   // until the products of its matrix before this tile's are written
   auto wait_ready = [&](const Tile& t) {
-    const int need = kEpilogueWarps * CTAS * (t.step * (2 * a.tiles[0] + a.tiles[1]) + t.kind * a.tiles[0]);
+    const int need = E::kWarps * CTAS * (t.step * (2 * a.tiles[0] + a.tiles[1]) + t.kind * a.tiles[0]);
     if (load_acquire(a.ready + t.matrix) >= need) return true;
     const long long t0 = clock64();
     while (load_acquire(a.ready + t.matrix) < need) {
@@ -451,12 +466,12 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
         const Tile t = locate(at);
         const int ks = depth(t);
         const bool mn = t.kind == kApply;
+        const int run = t.kind == kGram ? S::kRun : ks;
         const uint32_t idesc = mn ? umma_idesc(CTAS, NT, true) : umma_idesc(CTAS, NT, false);
         const uint64_t q_block = mn ? 8192 : 16, q_step = mn ? 128 : 2;
         for (int k = 0; k < ks; ++k, ++it) {
           const int s = it % S::kStages, buffer = acc % S::kBuffers;
-          const bool fresh = k % S::kRun == 0;  // the first of a run
-          const bool done = k + 1 == ks || (k + 1) % S::kRun == 0;
+          const bool fresh = k % run == 0, done = k + 1 == ks || (k + 1) % run == 0;
           if (!(ok = all_wait(&full[s], (it / S::kStages) & 1))) break;
           tc_fence_after();
           const uint32_t base = smem_addr(stages) + s * S::kStageBytes, qbase = base + S::kParts * S::kPBytes;
@@ -491,140 +506,155 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
       }
     }
   } else {
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
-    float* block = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes) + (warp - 2) * 32 * kPitch;
-    const int sub = lane >> 2, oct = (lane & 3) * 8;  // of eight rows and four groups of columns
+    const int quarter = warp & 3, group = (warp - 2) >> 2;
+    float* block = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes) + (warp - 2) * E::kFloats;
+    const int sub = lane / E::kOcts, oct = lane % E::kOcts * 8;  // row, of kRows, and the first of eight columns
+    // A's and B's diagonals apart, so that no sum is dominated by one term (the file's comment)
+    constexpr bool kDiagonals = TERMS == 3;
     int acc = 0, tiles = 0;
     for (int at = first; at < total; at += stride, ++tiles) {
       const Tile t = locate(at);
       const bool apply = t.kind == kApply, last_step = t.step + 1 == a.steps;
       // (TERMS = 1) parts of X in the linear term of this step and of the next
-      const int in_parts = apply && t.step + 2 < a.steps ? 2 : 1;
+      const int in_parts = TERMS == 3 || (apply && t.step + 2 < a.steps) ? 2 : 1;
       const int out_parts = TERMS == 3 || (apply && t.step + 3 < a.steps) ? 2 : 1;
       const float c_a = a.coefficients[3 * t.step], c_b = a.coefficients[3 * t.step + 1], c_c = a.coefficients[3 * t.step + 2];
       const float scale = t.kind == kGram   ? kScaleA / (kScaleX * kScaleX)
                           : t.kind == kPoly ? c_c * (kScaleB / (kScaleA * kScaleA))
                                             : 1.f / kScaleB;
-      const float in_scale = apply ? c_a : c_b * (kScaleB / kScaleA);
       const bool even = (t.step & 1) == 0;
       const __half *in0 = apply ? (even ? a.x[0][0] : a.x[1][0]) : a.a[0], *in1 = apply ? (even ? a.x[0][1] : a.x[1][1]) : a.a[1];
       __half *out0 = apply ? (even ? a.x[1][0] : a.x[0][0]) : t.kind == kGram ? a.a[0] : a.b[0];
       __half *out1 = apply ? (even ? a.x[1][1] : a.x[0][1]) : t.kind == kGram ? a.a[1] : a.b[1];
       const int64_t ld = apply ? a.ldx : a.lda, base = static_cast<int64_t>(t.matrix) * a.m * ld;
       const int cols = apply ? a.n : a.m, i0 = t.row + rank * 128 + quarter * 32;
-      auto column = [&](int k) { return t.col + (half + 2 * k) * 32; };
-      auto there = [&](int k) { return i0 < a.m && column(k) < cols && (apply || column(k) <= i0); };
-      // what is added, of block k: four rows' eight columns of each lane
+      const float* diagonal_a = a.da + static_cast<int64_t>(t.matrix) * a.lda;
+      auto column = [&](int k) { return t.col + (group + E::kGroups * k) * E::kCols; };
+      // (of a symmetric result: the lower triangle in squares of 32 x 32)
+      auto there = [&](int k) { return k < S::kBlocks && i0 < a.m && column(k) < cols && (apply || column(k) < i0 + 32); };
+      // What X's row is multiplied with beside the product (kApply), or A's (kPoly: with more for
+      // the column), and A's diagonal there.
+      float of_row[E::kPasses], on_diagonal[E::kPasses];
+      // What is added, of block k: some rows' eight columns of each lane.
       struct Added {
-        uint4 part[2][4];
+        uint4 part[2][E::kPasses];
+        float diagonal;  // kPoly: of A, the lane's column of the block
       };
       auto fetch = [&](int k, Added& f) {
-        if (t.kind == kGram || k >= S::kBlocks || !there(k)) return;
-        const int c = column(k) + oct;
+        if (t.kind == kGram || !there(k)) return;
+        const int c = column(k);
+        if (kDiagonals && !apply) f.diagonal = c + lane % E::kCols < cols ? __ldcg(diagonal_a + c + lane % E::kCols) : 0.f;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = i0 + r * 8 + sub;
-          const int64_t from = base + i * ld + c;
-          const bool on = i < a.m && c < cols;
+        for (int r = 0; r < E::kPasses; ++r) {
+          const int i = i0 + r * E::kRows + sub;
+          const int64_t from = base + i * ld + c + oct;
+          const bool on = i < a.m && c + oct < cols;
           const uint4 none = make_uint4(0, 0, 0, 0);
-          if (TERMS == 3 && apply) {  // fp32
-            f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(a.full + from)) : none;
-            f.part[1][r] = on ? __ldcg(reinterpret_cast<const uint4*>(a.full + from) + 1) : none;
-          } else {
-            f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(in0 + from)) : none;
-            f.part[1][r] = on && (TERMS == 3 || in_parts == 2) ? __ldcg(reinterpret_cast<const uint4*>(in1 + from)) : none;
-          }
+          f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(in0 + from)) : none;
+          f.part[1][r] = on && in_parts == 2 ? __ldcg(reinterpret_cast<const uint4*>(in1 + from)) : none;
         }
       };
-      auto finish = [&](int k, const float (&v)[32], const Added& f) {
+      auto put = [&](int64_t to, const float (&x)[8]) {
+        uint4 h, l;
+        split_eight(x, h, l);
+        *reinterpret_cast<uint4*>(out0 + to) = h;
+        if (out_parts == 2) *reinterpret_cast<uint4*>(out1 + to) = l;
+      };
+      // Eight neighbours of row `line` of the result (or column, if it is stored transposed).
+      auto put_last = [&](int line, int from, int lines, int length, const float (&x)[8]) {
+        if (line >= lines || from >= length) return;
+        const int64_t place = places.at[t.matrix], to = (place >> 1) + static_cast<int64_t>(line) * length + from;
+        const int count = min(8, length - from);
+        const bool whole = a.dest_vec && length % 8 == 0 && (place >> 1) % 8 == 0;
+        float y[8];
+        if (a.last == 2) {
+          float* w = static_cast<float*>(a.dest) + to;
+          const float step = a.step[place & 1] * (1.f / kScaleX);
+          load_eight_own(w, count, whole, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = __fmaf_rn(-step, x[e], a.keep * y[e]);
+          store_eight(w, count, whole, y);
+          return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = x[e] * (1.f / kScaleX);
+        if (a.dest_dtype == kF32) {
+          store_eight(static_cast<float*>(a.dest) + to, count, whole, y);
+        } else if (whole) {
+          *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dest) + to) =
+              make_uint4(pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < count) static_cast<bf16*>(a.dest)[to + e] = narrow<bf16>(y[e]);
+        }
+      };
+      const bool final = apply && last_step, transposed = final && (places.at[t.matrix] & 1);
+      // Block k, whose rows' products the lanes hold.
+      auto finish = [&](int k, const float (&v)[E::kCols], const Added& f) {
         const int j0 = column(k);
+        const bool mirror = !apply && j0 < i0, diagonal = kDiagonals && !apply && !mirror;
         __syncwarp();  // the last block has been read
 #pragma unroll
-        for (int c = 0; c < 32; ++c) block[lane * kPitch + c] = v[c];
+        for (int c = 0; c < E::kCols; ++c) block[E::place(lane, c)] = v[c];
         __syncwarp();
-        auto put = [&](int64_t to, const float (&x)[8]) {
-          uint4 h, l;
-          split_eight(x, h, l);
-          *reinterpret_cast<uint4*>(out0 + to) = h;
-          if (out_parts == 2) *reinterpret_cast<uint4*>(out1 + to) = l;
-        };
-        // eight neighbours of the result's row (or column, if it is stored transposed) `line`
-        auto put_last = [&](int line, int first, int lines, int length, const float (&x)[8]) {
-          if (line >= lines || first >= length) return;
-          const int64_t place = places.at[t.matrix], to = (place >> 1) + static_cast<int64_t>(line) * length + first;
-          const int count = min(8, length - first);
-          const bool whole = a.dest_vec && length % 8 == 0 && (place >> 1) % 8 == 0;
-          float y[8];
-          if (a.last == 2) {
-            float* w = static_cast<float*>(a.dest) + to;
-            const float step = a.step[place & 1] * (1.f / kScaleX);
-            load_eight_own(w, count, whole, y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __fmaf_rn(-step, x[e], a.keep * y[e]);
-            store_eight(w, count, whole, y);
-            return;
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e] * (1.f / kScaleX);
-          if (a.dest_dtype == kF32) {
-            store_eight(static_cast<float*>(a.dest) + to, count, whole, y);
-          } else if (whole) {
-            *reinterpret_cast<uint4*>(static_cast<bf16*>(a.dest) + to) =
-                make_uint4(pack2_bf16(y[0], y[1]), pack2_bf16(y[2], y[3]), pack2_bf16(y[4], y[5]), pack2_bf16(y[6], y[7]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (e < count) static_cast<bf16*>(a.dest)[to + e] = narrow<bf16>(y[e]);
-          }
-        };
-        const bool transposed = apply && last_step && (places.at[t.matrix] & 1);
-        const bool mirror = !apply && j0 < i0, final = apply && last_step;
         // (a row's last eight columns may reach into its padding)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = i0 + r * 8 + sub;
+        for (int r = 0; r < E::kPasses; ++r) {
+          const int row = r * E::kRows + sub, i = i0 + row;
           float x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = block[(r * 8 + sub) * kPitch + oct + e] * scale;
-          if (TERMS == 3 && apply) {
-            const float y[8] = {__uint_as_float(f.part[0][r].x), __uint_as_float(f.part[0][r].y), __uint_as_float(f.part[0][r].z),
-                                __uint_as_float(f.part[0][r].w), __uint_as_float(f.part[1][r].x), __uint_as_float(f.part[1][r].y),
-                                __uint_as_float(f.part[1][r].z), __uint_as_float(f.part[1][r].w)};
+          for (int e = 0; e < 8; ++e) x[e] = block[E::place(row, oct + e)] * scale;
+          if (t.kind != kGram) {
+            float factor[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = __fmaf_rn(in_scale, y[e], x[e]);
-          } else if (t.kind != kGram) {
+            for (int e = 0; e < 8; ++e) factor[e] = of_row[r];
+            if (kDiagonals && !apply) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) factor[e] = __fmaf_rn(scale, __shfl_sync(0xFFFFFFFFu, f.diagonal, oct + e), factor[e]);
+            }
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-              const uint32_t* w = &f.part[part][r].x;
+              const uint32_t w[4] = {f.part[part][r].x, f.part[part][r].y, f.part[part][r].z, f.part[part][r].w};
+              if (part == 1 && in_parts == 1) break;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float2 y = __half22float2(*reinterpret_cast<const __half2*>(w + e));
-                x[2 * e] = __fmaf_rn(in_scale, y.x, x[2 * e]);
-                x[2 * e + 1] = __fmaf_rn(in_scale, y.y, x[2 * e + 1]);
+                x[2 * e] = __fmaf_rn(factor[2 * e], y.x, x[2 * e]);
+                x[2 * e + 1] = __fmaf_rn(factor[2 * e + 1], y.y, x[2 * e + 1]);
               }
             }
           }
+          if (diagonal) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (i == j0 + oct + e && i < a.m) {
+                if (t.kind == kGram) a.da[static_cast<int64_t>(t.matrix) * a.lda + i] = x[e];
+                else a.db[static_cast<int64_t>(t.matrix) * a.lda + i] = __fmaf_rn(of_row[r], on_diagonal[r], x[e]);
+                x[e] = 0.f;
+              }
+          }
           if (mirror || transposed) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) block[(r * 8 + sub) * kPitch + oct + e] = x[e];
+            for (int e = 0; e < 8; ++e) block[E::place(row, oct + e)] = x[e];
           }
           if (final) {
             if (!transposed) put_last(i, j0 + oct, a.m, cols, x);
           } else if (i < a.m && j0 + oct < cols) {
             put(base + i * ld + j0 + oct, x);
-            if (TERMS == 3 && apply) store_eight(a.full + base + i * ld + j0 + oct, 8, true, x);
           }
         }
         if (mirror || transposed) {
           __syncwarp();
+          const int row = (lane & 3) * 8;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = j0 + r * 8 + sub;
+          for (int r = 0; r < E::kCols / 8; ++r) {
+            const int c = r * 8 + (lane >> 2), j = j0 + c;
             float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = block[(oct + e) * kPitch + r * 8 + sub];
-            if (transposed) put_last(j, i0 + oct, cols, a.m, x);
-            else if (j < cols && i0 + oct < a.m) put(base + j * ld + i0 + oct, x);
+            for (int e = 0; e < 8; ++e) x[e] = block[E::place(row + e, c)];
+            if (transposed) put_last(j, i0 + row, cols, a.m, x);
+            else if (j < cols && i0 + row < a.m) put(base + j * ld + i0 + row, x);
           }
         }
       };
@@ -637,68 +667,74 @@ __global__ void __launch_bounds__(kFlowThreads, 1) flow_kernel(const __grid_cons
           break;
         }
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 32;
+      Added next;
+      fetch(0, next);
+#pragma unroll
+      for (int r = 0; r < E::kPasses; ++r) {
+        const int i = i0 + r * E::kRows + sub;
+        on_diagonal[r] = kDiagonals && t.kind == kPoly && i < a.m ? __ldcg(diagonal_a + i) : 0.f;
+        of_row[r] = apply ? c_a + (kDiagonals && i < a.m ? __ldcg(a.db + static_cast<int64_t>(t.matrix) * a.lda + i) : 0.f) * (1.f / kScaleB)
+                          : __fmaf_rn(scale, on_diagonal[r], c_b * (kScaleB / kScaleA));
+      }
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * E::kCols;
       auto release = [&](uint64_t* bar) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_at<CTAS>(first_of_pair<CTAS>(smem_addr(bar)));
       };
-      if constexpr (TERMS == 1) {
+      const int ks = depth(t);
+      constexpr int kStep = E::kGroups * E::kCols;  // columns between a warp's blocks
+      if (TERMS == 3 && t.kind == kGram) {
+        float v[S::kBlocks][E::kCols];
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k)
+#pragma unroll
+          for (int c = 0; c < E::kCols; ++c) v[k][c] = 0.f;
+        for (int run = 0; ok && run < ks; run += S::kRun, ++acc) {
+          const int buffer = acc % S::kBuffers;
+          if (!(ok = wait(&acc_full[buffer], (acc / S::kBuffers) & 1))) break;
+          tc_fence_after();
+          const float gain = 1.f + kCutOff * (2 * min(ks - run, S::kRun) + 0.5f);
+#pragma unroll
+          for (int k = 0; k < S::kBlocks; ++k)
+            if (there(k)) tmem_add<E::kCols>(from + buffer * NT + k * kStep, v[k], gain);
+          release(&acc_empty[buffer]);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k)
+          if (there(k)) tmem_add<E::kCols>(from + S::kCross + k * kStep, v[k], 1.f);
+        release(&cross_empty);
+#pragma unroll
+        for (int k = 0; k < S::kBlocks; ++k)
+          if (there(k)) finish(k, v[k], next);
+      } else {
         const int buffer = acc % S::kBuffers;
-        Added now, next;
-        fetch(0, next);
         if (!wait(&acc_full[buffer], (acc / S::kBuffers) & 1)) break;
         ++acc;
         tc_fence_after();
 #pragma unroll 1
         for (int k = 0; k < S::kBlocks; ++k) {
-          now = next;
+          const Added now = next;
           fetch(k + 1, next);
           if (!there(k)) continue;
-          float v[32];
-          tmem_load32(from + buffer * NT + k * 64, v);
+          float v[E::kCols];
+          if constexpr (TERMS == 1) {
+            tmem_load<E::kCols>(from + buffer * NT + k * kStep, v);
+          } else {
+            const float gain = 1.f + kCutOff * (2 * ks + 0.5f);
+#pragma unroll
+            for (int c = 0; c < E::kCols; ++c) v[c] = 0.f;
+            tmem_add<E::kCols>(from + buffer * NT + k * kStep, v, gain);
+            tmem_add<E::kCols>(from + S::kCross + k * kStep, v, 1.f);
+          }
           finish(k, v, now);
         }
         release(&acc_empty[buffer]);
-      } else {
-        float v[S::kBlocks][32];
-#pragma unroll
-        for (int k = 0; k < S::kBlocks; ++k)
-#pragma unroll
-          for (int c = 0; c < 32; ++c) v[k][c] = 0.f;
-        const int ks = depth(t);
-        for (int run = 0; ok && run < ks; run += S::kRun, ++acc) {
-          const int buffer = acc % S::kBuffers;
-          if (!(ok = wait(&acc_full[buffer], (acc / S::kBuffers) & 1))) break;
-          tc_fence_after();
-          // what a run of sums cut off towards zero loses on average (FlowShape)
-          const float gain = 1.f + kCutOff * (2 * min(ks - run, S::kRun) + 0.5f);
-#pragma unroll
-          for (int k = 0; k < S::kBlocks; ++k) {
-            if (!there(k)) continue;
-            tmem_add16(from + buffer * NT + k * 64, v[k], gain);
-            tmem_add16(from + buffer * NT + k * 64 + 16, v[k] + 16, gain);
-          }
-          release(&acc_empty[buffer]);
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int k = 0; k < S::kBlocks; ++k) {
-          if (!there(k)) continue;
-          tmem_add16(from + S::kCross + k * 64, v[k], 1.f);
-          tmem_add16(from + S::kCross + k * 64 + 16, v[k] + 16, 1.f);
-        }
-        release(&cross_empty);
-#pragma unroll
-        for (int k = 0; k < S::kBlocks; ++k) {
-          if (!there(k)) continue;
-          Added f;
-          fetch(k, f);
-          finish(k, v[k], f);
-        }
+        if constexpr (TERMS == 3) release(&cross_empty);
       }
       // what this warp wrote is there, for others' copies too
-      if (!(apply && last_step)) {
+      if (!final) {
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) add_release(a.ready + t.matrix, 1);
@@ -757,7 +793,7 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 // in the scratch memory.
 struct ScratchMap {
   int64_t m, n, ldx, lda;
-  int64_t x[2][2], full, a[2], b[2], partials, ready, bytes;
+  int64_t x[2][2], a[2], b[2], da, db, partials, ready, bytes;
   int chunks;
   int64_t per_chunk;
   ScratchMap(int64_t m_, int64_t n_, int64_t batch, bool fine) : m(m_), n(n_), ldx(round_up(n_, 8)), lda(round_up(m_, 8)) {
@@ -769,7 +805,6 @@ struct ScratchMap {
     };
     for (int i = 0; i < 2; ++i)
       for (int part = 0; part < 2; ++part) x[i][part] = take(batch * m * ldx * 2);
-    full = fine ? take(batch * m * ldx * 4) : 0;
     for (int part = 0; part < 2; ++part) {
       a[part] = part == 0 || fine ? take(batch * m * lda * 2) : 0;
       b[part] = part == 0 || fine ? take(batch * m * lda * 2) : 0;
@@ -778,6 +813,8 @@ struct ScratchMap {
     while ((m * n + per_chunk - 1) / per_chunk > 1024) per_chunk *= 2;
     chunks = static_cast<int>((m * n + per_chunk - 1) / per_chunk);
     partials = take(batch * chunks * 3 * 4);
+    da = take(batch * lda * 4);
+    db = take(batch * lda * 4);
     ready = take(batch * 4);
     bytes = at;
   }
@@ -815,10 +852,10 @@ int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
 struct TileSize {
   int ctas, nt;
 };
-TileSize tile_size(int64_t m, int64_t n, int64_t batch, bool fine) {
-  TileSize best = {2, fine ? 128 : 256};
+TileSize tile_size(int64_t m, int64_t n, int64_t batch) {
+  TileSize best = {2, 256};
   double least = 1e300;
-  for (const TileSize s : {TileSize{2, fine ? 128 : 256}, TileSize{1, 128}, TileSize{1, 64}}) {
+  for (const TileSize s : {TileSize{2, 256}, TileSize{1, 128}, TileSize{1, 64}}) {
     const int64_t units = sm_count() / s.ctas;
     auto waves = [&](int64_t tiles) { return static_cast<double>((tiles * batch + units - 1) / units); };
     const int64_t sym = count_tiles(m, m, 128 * s.ctas, s.nt, true), gen = count_tiles(m, n, 128 * s.ctas, s.nt, false);
@@ -840,7 +877,7 @@ int launch_flow_as(FlowArgs& a, const Places& places, cudaStream_t stream) {
   const int64_t most = static_cast<int64_t>(a.batch) * std::max(a.tiles[0], a.tiles[1]);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, sm_count() / CTAS) * CTAS));
-  cfg.blockDim = dim3(kFlowThreads);
+  cfg.blockDim = dim3(Epilogue<TERMS>::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -855,7 +892,7 @@ int launch_flow_as(FlowArgs& a, const Places& places, cudaStream_t stream) {
 }
 template <int TERMS>
 int launch_flow(FlowArgs& a, const Places& places, TileSize s, cudaStream_t stream) {
-  if (s.ctas == 2) return launch_flow_as<2, TERMS == 3 ? 128 : 256, TERMS>(a, places, stream);
+  if (s.ctas == 2) return launch_flow_as<2, 256, TERMS>(a, places, stream);
   if (s.nt == 128) return launch_flow_as<1, 128, TERMS>(a, places, stream);
   return launch_flow_as<1, 64, TERMS>(a, places, stream);
 }
@@ -877,7 +914,8 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
     ok = ok && make_map(&f.a_map[part], f.a[part], m, m, l.lda, batch) && make_map(&f.b_map[part], f.b[part], m, m, l.lda, batch);
   }
   if (!ok) return ADASUM_ERR_CUDA;
-  f.full = fine ? reinterpret_cast<float*>(scratch + l.full) : nullptr;
+  f.da = reinterpret_cast<float*>(scratch + l.da);
+  f.db = reinterpret_cast<float*>(scratch + l.db);
   f.ldx = l.ldx;
   f.lda = l.lda;
   f.m = static_cast<int>(m);
@@ -898,7 +936,6 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
   src.per_chunk = l.per_chunk;
   src.eps = it.eps;
   src.vec = is_aligned(src.x, 16) && is_aligned(src.momentum, 16);
-  src.full = f.full;
   src.hi = f.x[0][0];
   src.lo = f.x[0][1];
   src.m = m;
@@ -914,7 +951,7 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
                       dim3(256), 0, stream, src, from);
   });
   if (st) return st;
-  const TileSize size = tile_size(m, n, batch, fine);
+  const TileSize size = tile_size(m, n, batch);
   return counted_launch(stream, fine ? "update_iterate3" : "update_iterate", 0.0, [&] {
     return fine ? launch_flow<3>(f, places, size, stream) : launch_flow<1>(f, places, size, stream);
   });
