@@ -309,10 +309,12 @@ struct FlowShape {
   static constexpr int kStages = 196608 / kStageBytes < 6 ? 196608 / kStageBytes : 6;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + Epilogue<TERMS>::kWarps * Epilogue<TERMS>::kFloats * 4;
   static_assert(kSmem + 1024 <= 232448, "with the barriers, a CTA's shared memory");
-  static constexpr int kBuffers = NT == 256 && TERMS == 3 ? 1 : 2;  // accumulators of the high parts
-  static constexpr int kCross = kBuffers * NT;                       // column of the others'
-  static constexpr int kUsed = kCross + (TERMS == 3 ? NT : 0);
-  static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  // Accumulators.  A product waits for the one before it on the same sums (about 150 cycles, however
+  // narrow it is), so narrow tiles have several sums that take turns, 256 columns in all.
+  static constexpr int kChains = 256 / NT;
+  static constexpr int kBuffers = TERMS == 3 ? 1 : 2;  // of 256 columns
+  static constexpr int kCross = 256;                   // column of the products with a low part
+  static constexpr int kCols = 512;
   static constexpr int kRun = TERMS == 3 ? 8 : 1 << 30;  // stages of 64 along the depth
   static constexpr int kBlocks = NT / 64;  // of an epilogue warp
 };
@@ -325,6 +327,10 @@ __host__ __device__ constexpr int sym_tiles(int r, int height, int nt) { return 
 // Sums grow in proportion to their terms so far, so k cut-offs take (k + 1) / 2 of them; 4 of
 // products of depth 16 make a stage.
 constexpr float kCutOff = 4.3e-8f;
+template <int CHAINS>
+__device__ __forceinline__ float cut_off(int stages) {
+  return 1.f + kCutOff * (2.f / CHAINS * static_cast<float>(stages) + 0.5f);
+}
 
 enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
 
@@ -478,7 +484,8 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
           auto multiply = [&](int p_part, int q_part, uint32_t d, bool clear) {
             const uint64_t p = umma_desc(base + p_part * S::kPBytes, 16), q = umma_desc(qbase + q_part * S::kQBytes, q_block);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) umma_f16<CTAS>(d, p + e * 2, q + e * q_step, idesc, !clear || e > 0);
+            for (int e = 0; e < 4; ++e)
+              umma_f16<CTAS>(d + e % S::kChains * NT, p + e * 2, q + e * q_step, idesc, !clear || e >= S::kChains);
           };
           if constexpr (TERMS == 3) {  // (these while the last run is drained)
             if (k == 0) {
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
             tc_fence_after();
           }
           if (elect_one()) {
-            multiply(0, 0, tmem + buffer * NT, fresh);
+            multiply(0, 0, tmem + buffer * 256, fresh);
             umma_commit<CTAS>(&empty[s]);
             if (done) umma_commit<CTAS>(&acc_full[buffer]);
           }
@@ -694,16 +701,22 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
           const int buffer = acc % S::kBuffers;
           if (!(ok = wait(&acc_full[buffer], (acc / S::kBuffers) & 1))) break;
           tc_fence_after();
-          const float gain = 1.f + kCutOff * (2 * min(ks - run, S::kRun) + 0.5f);
+          const float gain = cut_off<S::kChains>(min(ks - run, S::kRun));
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k)
-            if (there(k)) tmem_add<E::kCols>(from + buffer * NT + k * kStep, v[k], gain);
+            if (there(k)) {
+#pragma unroll
+              for (int c = 0; c < S::kChains; ++c) tmem_add<E::kCols>(from + buffer * 256 + c * NT + k * kStep, v[k], gain);
+            }
           release(&acc_empty[buffer]);
         }
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k)
-          if (there(k)) tmem_add<E::kCols>(from + S::kCross + k * kStep, v[k], 1.f);
+          if (there(k)) {
+#pragma unroll
+            for (int c = 0; c < S::kChains; ++c) tmem_add<E::kCols>(from + S::kCross + c * NT + k * kStep, v[k], 1.f);
+          }
         release(&cross_empty);
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k)
@@ -719,14 +732,17 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
           fetch(k + 1, next);
           if (!there(k)) continue;
           float v[E::kCols];
-          if constexpr (TERMS == 1) {
-            tmem_load<E::kCols>(from + buffer * NT + k * kStep, v);
-          } else {
-            const float gain = 1.f + kCutOff * (2 * ks + 0.5f);
+          const float gain = TERMS == 3 ? cut_off<S::kChains>(ks) : 1.f;
+          tmem_load<E::kCols>(from + buffer * 256 + k * kStep, v);
+          if constexpr (TERMS == 3) {
 #pragma unroll
-            for (int c = 0; c < E::kCols; ++c) v[c] = 0.f;
-            tmem_add<E::kCols>(from + buffer * NT + k * kStep, v, gain);
-            tmem_add<E::kCols>(from + S::kCross + k * kStep, v, 1.f);
+            for (int c = 0; c < E::kCols; ++c) v[c] *= gain;
+          }
+#pragma unroll
+          for (int c = 1; c < S::kChains; ++c) tmem_add<E::kCols>(from + buffer * 256 + c * NT + k * kStep, v, gain);
+          if constexpr (TERMS == 3) {
+#pragma unroll
+            for (int c = 0; c < S::kChains; ++c) tmem_add<E::kCols>(from + S::kCross + c * NT + k * kStep, v, 1.f);
           }
           finish(k, v, now);
         }
