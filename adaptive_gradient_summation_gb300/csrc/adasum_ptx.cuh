@@ -96,7 +96,7 @@ __device__ __forceinline__ void store_release_cta(int* p, int v) {
 }
 // (after what this thread has written, and what others wrote before a barrier it was at)
 __device__ __forceinline__ void add_release(int* p, int v) {
-  asm volatile("fence.acq_rel.gpu;\n red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
 // ------------------------------------------------------------------ dependent launch

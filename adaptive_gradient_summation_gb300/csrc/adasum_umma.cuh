@@ -117,31 +117,32 @@ __device__ __forceinline__ void tmem_add(uint32_t addr, float (&v)[N], float gai
 
 // ------------------------------------------------------------------- matrix products
 
-// Shared-memory operand of 16-bit elements with the 128-byte swizzle that TMA wrote.
+// Shared-memory operand of 16-bit elements with the 128-byte swizzle that TMA wrote, as the two
+// words of its descriptor.
 // K-major: rows of 64 elements along k, 128 bytes apart; 16 along k further: +32 bytes.
 // MN-major: blocks of 64 rows of the product, each 64 k-lines of 128 bytes; 16 along k
 // further: +2048 bytes.  `block`: bytes between two blocks of 64 (MN-major only).
-__device__ __forceinline__ uint64_t umma_desc(uint32_t addr, uint32_t block) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// (Addresses count in units of 16 bytes, and fit the low word's 14 bits.)
+__device__ __forceinline__ uint32_t umma_low(uint32_t addr, uint32_t block) { return (addr >> 4) | ((block >> 4) << 16); }
+constexpr uint32_t kUmmaHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
 // fp16 operands, fp32 accumulator of 128 * ctas x n; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t umma_idesc(int ctas, int n, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 * ctas >> 4) << 24);
 }
+// a, b: low words of the operands' descriptors.
 template <int CTAS>
-__device__ __forceinline__ void umma_f16(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_f16(uint32_t tmem, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
   if constexpr (CTAS == 1)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(kUmmaHigh)
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %4, 0;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(add ? 1u : 0u), "r"(kUmmaHigh)
         : "memory");
 }
 // Arrives on `bar` (CTAS = 2: on both CTAs' at that place) once this thread's products so far

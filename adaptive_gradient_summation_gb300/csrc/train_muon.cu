@@ -116,6 +116,10 @@ __device__ __forceinline__ void store_eight(float* p, int count, bool vec, const
       if (e < count) p[e] = v[e];
   }
 }
+__device__ __forceinline__ uint32_t pack2_half(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
 // The high parts of eight values as fp16, and what is left of them.
 __device__ __forceinline__ void split_eight(const float (&x)[8], uint4& hi, uint4& lo) {
   uint32_t h[4], l[4];
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, cons
 template <int TERMS>
 struct Epilogue {
   static constexpr int kWarps = TERMS == 1 ? 8 : 16, kCols = TERMS == 1 ? 32 : 16;
-  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kThreads = 96 + 32 * kWarps;
   static constexpr int kGroups = kWarps / 4;               // of warps that share 32 rows
   static constexpr int kOcts = kCols / 8, kRows = 32 / kOcts, kPasses = kOcts;  // lanes a row, rows at a time
   static constexpr int kFloats = TERMS == 1 ? 32 * 33 : 32 * 16;  // of a block in shared memory
@@ -276,10 +280,10 @@ struct Epilogue {
   static __device__ __forceinline__ int place(int r, int c) { return TERMS == 1 ? r * 33 + c : r * 16 + (c ^ ((r >> 1) & 15)); }
 };
 
-// What the iteration of equal matrices needs: the operands' maps (boxes of 64 x 64) and places,
+// What the iteration of equal matrices needs: the operands' maps (boxes of 64 x 128 and 64 x 64) and places,
 // the tiles of a product, where the results go.
 struct FlowArgs {
-  CUtensorMap x_map[2][2], a_map[2], b_map[2];  // [buffer][part], [part]
+  CUtensorMap x_tall[2][2], x_square[2][2], a_tall[2], a_square[2], b_tall[2];  // [buffer][part], [part]
   __half *x[2][2], *a[2], *b[2];
   float *da, *db;              // A's and B's diagonals, times kScaleA and kScaleB
   int64_t ldx, lda;
@@ -358,17 +362,12 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
   __shared__ int copied;  // tiles whose operands this CTA has found ready
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 1), mbar_init(&empty[i], 1);
+    for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 2), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], E::kWarps * CTAS);
     mbar_init(&cross_empty, E::kWarps * CTAS);
     mbar_fence_init();
     stop = 0;
     copied = 0;
-    for (int i = 0; i < 4; ++i) {  // (of all maps; the second part's are zeros where there is none)
-      if (i & 1 && S::kParts == 1) continue;
-      tma_prefetch_map(&a.x_map[i >> 1][i & 1]);
-      tma_prefetch_map(i >> 1 ? &a.b_map[i & 1] : &a.a_map[i & 1]);
-    }
   }
   if (warp == 1) tmem_alloc<S::kCols, CTAS>(&tmem_slot);
   tc_fence_before();
@@ -426,92 +425,112 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
     return w;
   };
   auto depth = [&](const Tile& t) { return (((t.kind == kGram ? a.n : a.m)) + 63) / 64; };
-  auto all_wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
-  int issued = 0;  // whole stages whose copies this warp began
-  if (warp == 0) {
-    bool ok = true;
-    int tiles = 0;
-    for (int at = first; ok && at < total; at += stride) {
-      const Tile t = locate(at);
-      if (!(ok = __all_sync(0xFFFFFFFFu, wait_ready(t)))) break;
-      ++tiles;
-      if (elect_one()) store_release_cta(&copied, tiles);
-      fence_proxy_async();
-      const int ks = depth(t);
-      const CUtensorMap* p = t.kind == kGram ? a.x_map[t.step & 1] : t.kind == kPoly ? a.a_map : a.b_map;
-      const CUtensorMap* q = t.kind == kPoly ? a.a_map : a.x_map[t.step & 1];
-      for (int k = 0; k < ks; ++k, ++issued) {
-        const int s = issued % S::kStages;
-        if (!(ok = all_wait(&empty[s], ((issued / S::kStages) & 1) ^ 1))) break;
-        if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], CTAS * S::kStageBytes);
+  // Two warps copy, the left operand's tiles and the right one's: an instruction takes its thread
+  // about 100 cycles, which for both operands was more than narrow tiles' products take.
+  constexpr int kCopyQ = 2 + E::kWarps;
+  int issued = 0;  // whole stages whose copies this thread began
+  if (warp == 0 || warp == kCopyQ) {
+    if (elect_one()) {
+      const bool right = warp == kCopyQ;
+      const uint32_t bytes = CTAS * S::kParts * (right ? S::kQBytes : S::kPBytes);
+      bool ok = true;
+      int tiles = 0, s = 0;
+      uint32_t phase = 1;
+      for (int at = first; ok && at < total; at += stride) {
+        const Tile t = locate(at);
+        if (!(ok = wait_ready(t))) break;
+        if (!right) store_release_cta(&copied, ++tiles);
+        fence_proxy_async();
+        const int ks = depth(t), b = t.step & 1;
+        // (the right operand of kApply has the depth along its rows)
+        const CUtensorMap* map = !right ? (t.kind == kGram ? a.x_tall[b] : t.kind == kPoly ? a.a_tall : a.b_tall)
+                                 : t.kind == kApply ? a.x_square[b]
+                                 : S::kQRows == 128 ? (t.kind == kGram ? a.x_tall[b] : a.a_tall)
+                                                    : (t.kind == kGram ? a.x_square[b] : a.a_square);
+        const int line = right ? t.col + rank * S::kQRows : t.row + rank * 128;
+        for (int k = 0; k < ks; ++k, ++issued) {
+          if (!(ok = wait(&empty[s], phase))) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
           const uint32_t bar = first_of_pair<CTAS>(smem_addr(&full[s]));
-          uint32_t to = smem_addr(stages) + s * S::kStageBytes;
+          uint32_t to = smem_addr(stages) + s * S::kStageBytes + (right ? S::kParts * S::kPBytes : 0);
+          if (!right || (t.kind != kApply && S::kQRows <= 128)) {
 #pragma unroll
-          for (int part = 0; part < S::kParts; ++part)
+            for (int part = 0; part < S::kParts; ++part, to += right ? S::kQBytes : S::kPBytes)
+              tma_load3<CTAS>(to, map + part, bar, k * 64, line, t.matrix);
+          } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h, to += 8192) tma_load3<CTAS>(to, p + part, bar, k * 64, t.row + rank * 128 + h * 64, t.matrix);
+            for (int part = 0; part < S::kParts; ++part)
 #pragma unroll
-          for (int part = 0; part < S::kParts; ++part)
-#pragma unroll
-            for (int h = 0; h < S::kQRows / 64; ++h, to += 8192) {
-              const int c = t.col + rank * S::kQRows + h * 64;
-              tma_load3<CTAS>(to, q + part, bar, t.kind == kApply ? c : k * 64, t.kind == kApply ? k * 64 : c, t.matrix);
-            }
+              for (int h = 0; h < S::kQRows / 64; ++h, to += 8192) tma_load3<CTAS>(to, map + part, bar, line + h * 64, k * 64, t.matrix);
+          }
+          if (++s == S::kStages) s = 0, phase ^= 1;
         }
-        __syncwarp();
+      }
+      // every stage consumed: no arrival is on its way to a CTA that has left
+      for (int i = max(0, issued - S::kStages); ok && i < issued; ++i) ok = wait(&empty[i % S::kStages], (i / S::kStages) & 1);
+      if (!ok && warp == 0) {  // copies still in flight
+        for (int i = max(0, issued - S::kStages); rank == 0 && i < issued; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(&full[i % S::kStages], (i / S::kStages) & 1) && clock64() - t0 < kWaitCycles) {
+          }
+        }
+      }
+      if (!ok) {  // (a pair's second CTA cannot see its copies' barrier)
+        const long long t0 = clock64();
+        while (clock64() - t0 < kWaitCycles / 1000) {
+        }
       }
     }
-    // every stage consumed: no arrival is on its way to a CTA that has left
-    for (int i = max(0, issued - S::kStages); ok && i < issued; ++i) ok = all_wait(&empty[i % S::kStages], (i / S::kStages) & 1);
+    __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0) {
-      int it = 0, acc = 0, tiles = 0;
-      bool ok = true;
+    if (rank == 0 && elect_one()) {
+      int acc = 0, tiles = 0, s = 0;
+      uint32_t phase = 0;
+      bool ok = tmem_slot == 0;  // (all of TMEM is this CTA's, so it begins at 0, which the compiler may know)
       for (int at = first; ok && at < total; at += stride, ++tiles) {
         const Tile t = locate(at);
         const int ks = depth(t);
         const bool mn = t.kind == kApply;
         const int run = t.kind == kGram ? S::kRun : ks;
         const uint32_t idesc = mn ? umma_idesc(CTAS, NT, true) : umma_idesc(CTAS, NT, false);
-        const uint64_t q_block = mn ? 8192 : 16, q_step = mn ? 128 : 2;
-        for (int k = 0; k < ks; ++k, ++it) {
-          const int s = it % S::kStages, buffer = acc % S::kBuffers;
-          const bool fresh = k % run == 0, done = k + 1 == ks || (k + 1) % run == 0;
-          if (!(ok = all_wait(&full[s], (it / S::kStages) & 1))) break;
+        const uint32_t q_block = mn ? 8192 : 16, q_step = mn ? 128 : 2;
+        int in_run = 0;
+        for (int k = 0; k < ks; ++k) {
+          const int buffer = acc % S::kBuffers;
+          if (!(ok = wait(&full[s], phase))) break;
           tc_fence_after();
           const uint32_t base = smem_addr(stages) + s * S::kStageBytes, qbase = base + S::kParts * S::kPBytes;
           auto multiply = [&](int p_part, int q_part, uint32_t d, bool clear) {
-            const uint64_t p = umma_desc(base + p_part * S::kPBytes, 16), q = umma_desc(qbase + q_part * S::kQBytes, q_block);
+            const uint32_t p = umma_low(base + p_part * S::kPBytes, 16), q = umma_low(qbase + q_part * S::kQBytes, q_block);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               umma_f16<CTAS>(d + e % S::kChains * NT, p + e * 2, q + e * q_step, idesc, !clear || e >= S::kChains);
           };
           if constexpr (TERMS == 3) {  // (these while the last run is drained)
             if (k == 0) {
-              if (!(ok = all_wait(&cross_empty, (tiles & 1) ^ 1))) break;
+              if (!(ok = wait(&cross_empty, (tiles & 1) ^ 1))) break;
               tc_fence_after();
             }
-            if (elect_one()) {
-              multiply(0, 1, tmem + S::kCross, k == 0);
-              multiply(1, 0, tmem + S::kCross, false);
-            }
-            __syncwarp();
+            multiply(0, 1, S::kCross, k == 0);
+            multiply(1, 0, S::kCross, false);
           }
-          if (fresh) {
-            if (!(ok = all_wait(&acc_empty[buffer], ((acc / S::kBuffers) & 1) ^ 1))) break;
+          if (in_run == 0) {
+            if (!(ok = wait(&acc_empty[buffer], ((acc / S::kBuffers) & 1) ^ 1))) break;
             tc_fence_after();
           }
-          if (elect_one()) {
-            multiply(0, 0, tmem + buffer * 256, fresh);
-            umma_commit<CTAS>(&empty[s]);
-            if (done) umma_commit<CTAS>(&acc_full[buffer]);
+          multiply(0, 0, buffer * 256, in_run == 0);
+          umma_commit<CTAS>(&empty[s]);
+          if (++in_run == run || k + 1 == ks) {
+            umma_commit<CTAS>(&acc_full[buffer]);
+            ++acc;
+            in_run = 0;
           }
-          __syncwarp();
-          if (done) ++acc;
+          if (++s == S::kStages) s = 0, phase ^= 1;
         }
       }
+      if (!ok) give_up();
     }
+    __syncwarp();
   } else {
     const int quarter = warp & 3, group = (warp - 2) >> 2;
     float* block = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes) + (warp - 2) * E::kFloats;
@@ -563,9 +582,13 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       };
       auto put = [&](int64_t to, const float (&x)[8]) {
         uint4 h, l;
-        split_eight(x, h, l);
+        if (TERMS == 3 || out_parts == 2) {
+          split_eight(x, h, l);
+          *reinterpret_cast<uint4*>(out1 + to) = l;
+        } else {
+          h = make_uint4(pack2_half(x[0], x[1]), pack2_half(x[2], x[3]), pack2_half(x[4], x[5]), pack2_half(x[6], x[7]));
+        }
         *reinterpret_cast<uint4*>(out0 + to) = h;
-        if (out_parts == 2) *reinterpret_cast<uint4*>(out1 + to) = l;
       };
       // Eight neighbours of row `line` of the result (or column, if it is stored transposed).
       auto put_last = [&](int line, int from, int lines, int length, const float (&x)[8]) {
@@ -757,16 +780,6 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       }
     }
   }
-  if (warp == 0 && lane == 0 && stop) {  // copies still in flight
-    for (int i = max(0, issued - S::kStages); rank == 0 && i < issued; ++i) {
-      const long long t0 = clock64();
-      while (!mbar_try_wait(&full[i % S::kStages], (i / S::kStages) & 1) && clock64() - t0 < kWaitCycles) {
-      }
-    }
-    const long long t0 = clock64();  // (a pair's second CTA cannot see its copies' barrier)
-    while (clock64() - t0 < kWaitCycles / 1000) {
-    }
-  }
   tc_fence_before();
   __syncthreads();
   if constexpr (CTAS > 1) cluster_sync_all();
@@ -793,11 +806,11 @@ EncodeTiled encode_tiled() {
   return f;
 }
 
-// Boxes of 64 x 64 of `batch` matrices of rows x cols fp16, their rows ld apart.
-bool make_map(CUtensorMap* map, const __half* p, int64_t rows, int64_t cols, int64_t ld, int64_t batch) {
+// Boxes of 64 x `box_rows` of `batch` matrices of rows x cols fp16, their rows ld apart.
+bool make_map(CUtensorMap* map, const __half* p, int64_t rows, int64_t cols, int64_t ld, int64_t batch, cuuint32_t box_rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(rows) * 2};
-  const cuuint32_t box[3] = {64, 64, 1}, ones[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, box_rows, 1}, ones[3] = {1, 1, 1};
   return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides, box, ones,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -922,12 +935,15 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
   for (int part = 0; part < 2; ++part) {
     for (int i = 0; i < 2; ++i) {
       f.x[i][part] = reinterpret_cast<__half*>(scratch + l.x[i][part]);
-      ok = ok && make_map(&f.x_map[i][part], f.x[i][part], m, n, l.ldx, batch);
+      if (part > 0 && !fine) continue;
+      ok = ok && make_map(&f.x_tall[i][part], f.x[i][part], m, n, l.ldx, batch, 128) &&
+           make_map(&f.x_square[i][part], f.x[i][part], m, n, l.ldx, batch, 64);
     }
     if (part > 0 && !fine) continue;
     f.a[part] = reinterpret_cast<__half*>(scratch + l.a[part]);
     f.b[part] = reinterpret_cast<__half*>(scratch + l.b[part]);
-    ok = ok && make_map(&f.a_map[part], f.a[part], m, m, l.lda, batch) && make_map(&f.b_map[part], f.b[part], m, m, l.lda, batch);
+    ok = ok && make_map(&f.a_tall[part], f.a[part], m, m, l.lda, batch, 128) && make_map(&f.a_square[part], f.a[part], m, m, l.lda, batch, 64) &&
+         make_map(&f.b_tall[part], f.b[part], m, m, l.lda, batch, 128);
   }
   if (!ok) return ADASUM_ERR_CUDA;
   f.da = reinterpret_cast<float*>(scratch + l.da);
