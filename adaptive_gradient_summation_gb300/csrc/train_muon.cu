@@ -57,6 +57,7 @@ struct SourceArgs {
   int nesterov;
   float* partials;     // [matrix][chunk][3]
   int* ready;          // per matrix, to be zeroed
+  int first;           // the first matrix' place among all
   int chunks;
   int64_t per_chunk;
   float eps;
@@ -141,7 +142,7 @@ __global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const 
   pdl_enter();
   __shared__ float red[3][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t start = places.at[blockIdx.y] >> 1, size = a.rows * a.cols;
+  const int64_t start = places.at[a.first + blockIdx.y] >> 1, size = a.rows * a.cols;
   const int64_t lo = blockIdx.x * a.per_chunk, hi = min(lo + a.per_chunk, size);
   const bool dense = a.ld == a.cols, vec = a.vec && start % 8 == 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) a.ready[blockIdx.y] = 0;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, cons
   pdl_enter();
   __shared__ float tile[64][65];
   __shared__ float factors[2];
-  const int64_t place = places.at[blockIdx.z], start = place >> 1;
+  const int64_t place = places.at[a.first + blockIdx.z], start = place >> 1;
   const bool transposed = place & 1;
   if (threadIdx.x < 32) {
     const float* p = a.partials + static_cast<int64_t>(blockIdx.z) * a.chunks * 3;
@@ -280,20 +281,27 @@ struct Epilogue {
   static __device__ __forceinline__ int place(int r, int c) { return TERMS == 1 ? r * 33 + c : r * 16 + (c ^ ((r >> 1) & 15)); }
 };
 
-// What the iteration of equal matrices needs: the operands' maps (boxes of 64 x 128 and 64 x 64) and places,
-// the tiles of a product, where the results go.
-struct FlowArgs {
+// Equal matrices that are iterated: the operands' maps (boxes of 64 x 128 and 64 x 64) and places,
+// the tiles of a product.
+struct FlowGroup {
   CUtensorMap x_tall[2][2], x_square[2][2], a_tall[2], a_square[2], b_tall[2];  // [buffer][part], [part]
   __half *x[2][2], *a[2], *b[2];
   float *da, *db;              // A's and B's diagonals, times kScaleA and kScaleB
   int64_t ldx, lda;
-  int m, n, batch, steps;
+  int m, n, batch, first;      // the first matrix' place among all
   int col_tiles[2], tiles[2];  // of A and B (lower triangle), of X
   int* ready;                  // per matrix: warps that have written their part of a tile
-  int last;                    // 1: results to `dest`, 2: weights there are moved
+  float step[2];               // weights: w <- keep w - step x (of a matrix as it is, transposed)
+};
+constexpr int kMaxGroups = 4;  // of one launch
+// And where the results go.
+struct FlowArgs {
+  FlowGroup group[kMaxGroups];
+  int groups, steps, per_step;  // tiles of a step
+  int last;                     // 1: results to `dest`, 2: weights there are moved
   void* dest;
-  int dest_dtype, dest_vec;    // on a 16-byte boundary
-  float keep, step[2];         // weights: w <- keep w - step x (of a matrix as it is, transposed)
+  int dest_dtype, dest_vec;     // on a 16-byte boundary
+  float keep;
   float coefficients[3 * ADASUM_NEWTON_SCHULZ_MAX_STEPS];
 };
 
@@ -339,7 +347,7 @@ __device__ __forceinline__ float cut_off(int stages) {
 enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
 
 struct Tile {
-  int step, kind, matrix, row, col;  // row and column of the result where it starts
+  int step, kind, group, matrix, row, col;  // row and column of the result where it starts
 };
 
 // All steps of the iteration in one launch of co-resident CTAs.  The tiles (128 x NT of one
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
   const uint32_t tmem = tmem_slot;
   const int rank = CTAS > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;  // of this cluster's tiles
-  const int per_step = a.batch * (2 * a.tiles[0] + a.tiles[1]), total = a.steps * per_step;
+  const int total = a.steps * a.per_step;
   auto give_up = [&] {
     if (!stop) atomicOr(&g_error, 2);
     stop = 1;
@@ -392,10 +400,11 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
   };
   // until the products of its matrix before this tile's are written
   auto wait_ready = [&](const Tile& t) {
-    const int need = E::kWarps * CTAS * (t.step * (2 * a.tiles[0] + a.tiles[1]) + t.kind * a.tiles[0]);
-    if (load_acquire(a.ready + t.matrix) >= need) return true;
+    const FlowGroup& g = a.group[t.group];
+    const int need = E::kWarps * CTAS * (t.step * (2 * g.tiles[0] + g.tiles[1]) + t.kind * g.tiles[0]);
+    if (load_acquire(g.ready + t.matrix) >= need) return true;
     const long long t0 = clock64();
-    while (load_acquire(a.ready + t.matrix) < need) {
+    while (load_acquire(g.ready + t.matrix) < need) {
       if (stop || clock64() - t0 > kWaitCycles) return give_up();
       __nanosleep(32);
     }
@@ -403,28 +412,30 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
   };
   auto locate = [&](int t) {
     Tile w;
-    w.step = t / per_step;
-    int r = t - w.step * per_step;
-    const int sym = a.batch * a.tiles[0];
-    w.kind = r < sym ? kGram : r < 2 * sym ? kPoly : kApply;
-    r -= w.kind * sym;
-    if (w.kind == kApply) {
-      w.matrix = r / a.tiles[1];
-      r -= w.matrix * a.tiles[1];
-      const int i = r / a.col_tiles[1];
-      w.row = i * S::kHeight;
-      w.col = (r - i * a.col_tiles[1]) * NT;
-    } else {
-      w.matrix = r / a.tiles[0];
-      r -= w.matrix * a.tiles[0];
-      int i = 0;
-      for (int n; r >= (n = min(sym_tiles(i, S::kHeight, NT), a.col_tiles[0])); ++i) r -= n;
-      w.row = i * S::kHeight;
-      w.col = r * NT;
+    w.step = t / a.per_step;
+    int r = t - w.step * a.per_step;
+    w.kind = kGram;
+    w.group = 0;
+    for (int n; r >= (n = a.group[w.group].batch * a.group[w.group].tiles[w.kind == kApply]);) {
+      r -= n;
+      if (++w.group == a.groups) w.group = 0, ++w.kind;
     }
+    const FlowGroup& g = a.group[w.group];
+    const int tiles = g.tiles[w.kind == kApply], columns = g.col_tiles[w.kind == kApply];
+    w.matrix = r / tiles;
+    r -= w.matrix * tiles;
+    int i = 0;
+    if (w.kind == kApply) {
+      i = r / columns;
+      r -= i * columns;
+    } else {
+      for (int n; r >= (n = min(sym_tiles(i, S::kHeight, NT), columns)); ++i) r -= n;
+    }
+    w.row = i * S::kHeight;
+    w.col = r * NT;
     return w;
   };
-  auto depth = [&](const Tile& t) { return (((t.kind == kGram ? a.n : a.m)) + 63) / 64; };
+  auto depth = [&](const Tile& t) { return ((t.kind == kGram ? a.group[t.group].n : a.group[t.group].m) + 63) / 64; };
   // Two warps copy, the left operand's tiles and the right one's: an instruction takes its thread
   // about 100 cycles, which for both operands was more than narrow tiles' products take.
   constexpr int kCopyQ = 2 + E::kWarps;
@@ -441,12 +452,13 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
         if (!(ok = wait_ready(t))) break;
         if (!right) store_release_cta(&copied, ++tiles);
         fence_proxy_async();
+        const FlowGroup& g = a.group[t.group];
         const int ks = depth(t), b = t.step & 1;
         // (the right operand of kApply has the depth along its rows)
-        const CUtensorMap* map = !right ? (t.kind == kGram ? a.x_tall[b] : t.kind == kPoly ? a.a_tall : a.b_tall)
-                                 : t.kind == kApply ? a.x_square[b]
-                                 : S::kQRows == 128 ? (t.kind == kGram ? a.x_tall[b] : a.a_tall)
-                                                    : (t.kind == kGram ? a.x_square[b] : a.a_square);
+        const CUtensorMap* map = !right ? (t.kind == kGram ? g.x_tall[b] : t.kind == kPoly ? g.a_tall : g.b_tall)
+                                 : t.kind == kApply ? g.x_square[b]
+                                 : S::kQRows == 128 ? (t.kind == kGram ? g.x_tall[b] : g.a_tall)
+                                                    : (t.kind == kGram ? g.x_square[b] : g.a_square);
         const int line = right ? t.col + rank * S::kQRows : t.row + rank * 128;
         for (int k = 0; k < ks; ++k, ++issued) {
           if (!(ok = wait(&empty[s], phase))) break;
@@ -540,6 +552,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
     int acc = 0, tiles = 0;
     for (int at = first; at < total; at += stride, ++tiles) {
       const Tile t = locate(at);
+      const FlowGroup& g = a.group[t.group];
       const bool apply = t.kind == kApply, last_step = t.step + 1 == a.steps;
       // (TERMS = 1) parts of X in the linear term of this step and of the next
       const int in_parts = TERMS == 3 || (apply && t.step + 2 < a.steps) ? 2 : 1;
@@ -549,15 +562,15 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
                           : t.kind == kPoly ? c_c * (kScaleB / (kScaleA * kScaleA))
                                             : 1.f / kScaleB;
       const bool even = (t.step & 1) == 0;
-      const __half *in0 = apply ? (even ? a.x[0][0] : a.x[1][0]) : a.a[0], *in1 = apply ? (even ? a.x[0][1] : a.x[1][1]) : a.a[1];
-      __half *out0 = apply ? (even ? a.x[1][0] : a.x[0][0]) : t.kind == kGram ? a.a[0] : a.b[0];
-      __half *out1 = apply ? (even ? a.x[1][1] : a.x[0][1]) : t.kind == kGram ? a.a[1] : a.b[1];
-      const int64_t ld = apply ? a.ldx : a.lda, base = static_cast<int64_t>(t.matrix) * a.m * ld;
-      const int cols = apply ? a.n : a.m, i0 = t.row + rank * 128 + quarter * 32;
-      const float* diagonal_a = a.da + static_cast<int64_t>(t.matrix) * a.lda;
+      const __half *in0 = apply ? (even ? g.x[0][0] : g.x[1][0]) : g.a[0], *in1 = apply ? (even ? g.x[0][1] : g.x[1][1]) : g.a[1];
+      __half *out0 = apply ? (even ? g.x[1][0] : g.x[0][0]) : t.kind == kGram ? g.a[0] : g.b[0];
+      __half *out1 = apply ? (even ? g.x[1][1] : g.x[0][1]) : t.kind == kGram ? g.a[1] : g.b[1];
+      const int64_t ld = apply ? g.ldx : g.lda, base = static_cast<int64_t>(t.matrix) * g.m * ld;
+      const int cols = apply ? g.n : g.m, i0 = t.row + rank * 128 + quarter * 32;
+      const float* diagonal_a = g.da + static_cast<int64_t>(t.matrix) * g.lda;
       auto column = [&](int k) { return t.col + (group + E::kGroups * k) * E::kCols; };
       // (of a symmetric result: the lower triangle in squares of 32 x 32)
-      auto there = [&](int k) { return k < S::kBlocks && i0 < a.m && column(k) < cols && (apply || column(k) < i0 + 32); };
+      auto there = [&](int k) { return k < S::kBlocks && i0 < g.m && column(k) < cols && (apply || column(k) < i0 + 32); };
       // What X's row is multiplied with beside the product (kApply), or A's (kPoly: with more for
       // the column), and A's diagonal there.
       float of_row[E::kPasses], on_diagonal[E::kPasses];
@@ -574,7 +587,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
         for (int r = 0; r < E::kPasses; ++r) {
           const int i = i0 + r * E::kRows + sub;
           const int64_t from = base + i * ld + c + oct;
-          const bool on = i < a.m && c + oct < cols;
+          const bool on = i < g.m && c + oct < cols;
           const uint4 none = make_uint4(0, 0, 0, 0);
           f.part[0][r] = on ? __ldcg(reinterpret_cast<const uint4*>(in0 + from)) : none;
           f.part[1][r] = on && in_parts == 2 ? __ldcg(reinterpret_cast<const uint4*>(in1 + from)) : none;
@@ -593,13 +606,13 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       // Eight neighbours of row `line` of the result (or column, if it is stored transposed).
       auto put_last = [&](int line, int from, int lines, int length, const float (&x)[8]) {
         if (line >= lines || from >= length) return;
-        const int64_t place = places.at[t.matrix], to = (place >> 1) + static_cast<int64_t>(line) * length + from;
+        const int64_t place = places.at[g.first + t.matrix], to = (place >> 1) + static_cast<int64_t>(line) * length + from;
         const int count = min(8, length - from);
         const bool whole = a.dest_vec && length % 8 == 0 && (place >> 1) % 8 == 0;
         float y[8];
         if (a.last == 2) {
           float* w = static_cast<float*>(a.dest) + to;
-          const float step = a.step[place & 1] * (1.f / kScaleX);
+          const float step = g.step[place & 1] * (1.f / kScaleX);
           load_eight_own(w, count, whole, y);
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] = __fmaf_rn(-step, x[e], a.keep * y[e]);
@@ -619,7 +632,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
             if (e < count) static_cast<bf16*>(a.dest)[to + e] = narrow<bf16>(y[e]);
         }
       };
-      const bool final = apply && last_step, transposed = final && (places.at[t.matrix] & 1);
+      const bool final = apply && last_step, transposed = final && (places.at[g.first + t.matrix] & 1);
       // Block k, whose rows' products the lanes hold.
       auto finish = [&](int k, const float (&v)[E::kCols], const Added& f) {
         const int j0 = column(k);
@@ -658,9 +671,9 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
           if (diagonal) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (i == j0 + oct + e && i < a.m) {
-                if (t.kind == kGram) a.da[static_cast<int64_t>(t.matrix) * a.lda + i] = x[e];
-                else a.db[static_cast<int64_t>(t.matrix) * a.lda + i] = __fmaf_rn(of_row[r], on_diagonal[r], x[e]);
+              if (i == j0 + oct + e && i < g.m) {
+                if (t.kind == kGram) g.da[static_cast<int64_t>(t.matrix) * g.lda + i] = x[e];
+                else g.db[static_cast<int64_t>(t.matrix) * g.lda + i] = __fmaf_rn(of_row[r], on_diagonal[r], x[e]);
                 x[e] = 0.f;
               }
           }
@@ -669,8 +682,8 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
             for (int e = 0; e < 8; ++e) block[E::place(row, oct + e)] = x[e];
           }
           if (final) {
-            if (!transposed) put_last(i, j0 + oct, a.m, cols, x);
-          } else if (i < a.m && j0 + oct < cols) {
+            if (!transposed) put_last(i, j0 + oct, g.m, cols, x);
+          } else if (i < g.m && j0 + oct < cols) {
             put(base + i * ld + j0 + oct, x);
           }
         }
@@ -683,8 +696,8 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = block[E::place(row + e, c)];
-            if (transposed) put_last(j, i0 + row, cols, a.m, x);
-            else if (j < cols && i0 + row < a.m) put(base + j * ld + i0 + row, x);
+            if (transposed) put_last(j, i0 + row, cols, g.m, x);
+            else if (j < cols && i0 + row < g.m) put(base + j * ld + i0 + row, x);
           }
         }
       };
@@ -702,8 +715,8 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
 #pragma unroll
       for (int r = 0; r < E::kPasses; ++r) {
         const int i = i0 + r * E::kRows + sub;
-        on_diagonal[r] = kDiagonals && t.kind == kPoly && i < a.m ? __ldcg(diagonal_a + i) : 0.f;
-        of_row[r] = apply ? c_a + (kDiagonals && i < a.m ? __ldcg(a.db + static_cast<int64_t>(t.matrix) * a.lda + i) : 0.f) * (1.f / kScaleB)
+        on_diagonal[r] = kDiagonals && t.kind == kPoly && i < g.m ? __ldcg(diagonal_a + i) : 0.f;
+        of_row[r] = apply ? c_a + (kDiagonals && i < g.m ? __ldcg(g.db + static_cast<int64_t>(t.matrix) * g.lda + i) : 0.f) * (1.f / kScaleB)
                           : __fmaf_rn(scale, on_diagonal[r], c_b * (kScaleB / kScaleA));
       }
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * E::kCols;
@@ -776,7 +789,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       if (!final) {
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) add_release(a.ready + t.matrix, 1);
+        if (lane == 0) add_release(g.ready + t.matrix, 1);
       }
     }
   }
@@ -848,12 +861,31 @@ struct ScratchMap {
     bytes = at;
   }
 };
-// Matrices of a chunk: what about a gigabyte of scratch holds, as even as possible.
+// Equal matrices, m x n once the taller ones are transposed, that are iterated in one launch, on
+// their own or with others.
+struct Piece {
+  int64_t m, n;
+  int batch;
+  float step[2];  // as in FlowGroup
+};
+// Matrices of a piece: what about a gigabyte of scratch holds, as even as possible.
 int64_t chunk_of(int64_t m, int64_t n, int64_t count, bool fine) {
   const int64_t one = ScratchMap(m, n, 1, fine).bytes;
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxBatch, kChunkBytes / one));
   const int64_t chunks = (count + most - 1) / most;
   return (count + chunks - 1) / chunks;
+}
+// How many of the pieces from `p` on, up to `end`, one launch takes, and the scratch they need.
+int take_pieces(const Piece* p, const Piece* end, bool fine, int64_t& bytes) {
+  int count = 0, matrices = 0;
+  bytes = 0;
+  for (; p + count < end && count < kMaxGroups; ++count) {
+    const int64_t more = ScratchMap(p[count].m, p[count].n, p[count].batch, fine).bytes;
+    if (count > 0 && (bytes + more > kChunkBytes || matrices + p[count].batch > kMaxBatch)) break;
+    bytes += more;
+    matrices += p[count].batch;
+  }
+  return count;
 }
 
 struct Iteration {
@@ -865,7 +897,7 @@ struct Result {
   int last;  // as in FlowArgs
   void* dest;
   int dtype;
-  float keep, step[2];
+  float keep;
 };
 
 int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
@@ -875,20 +907,30 @@ int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
   for (int64_t r = 0; r < row_tiles; ++r) tiles += std::min<int64_t>(sym_tiles(static_cast<int>(r), height, nt), col_tiles);
   return tiles;
 }
-// CTAs and columns of a tile: those whose waves over the SMs take least.  A tile costs its
-// columns and about 32 columns' time beside them; single CTAs copy half as much again for
-// the same product.
+// CTAs and columns of a tile: those for which the products, one after the other, take least, in
+// cycles as measured: for 64 along the depth an instruction's time (at least 65 each, what its
+// thread takes) and 100; for a tile 5000 and 40 a column until its results are written.
 struct TileSize {
   int ctas, nt;
 };
-TileSize tile_size(int64_t m, int64_t n, int64_t batch) {
+TileSize tile_size(const Piece* p, int pieces, bool fine) {
   TileSize best = {2, 256};
   double least = 1e300;
   for (const TileSize s : {TileSize{2, 256}, TileSize{1, 128}, TileSize{1, 64}}) {
     const int64_t units = sm_count() / s.ctas;
-    auto waves = [&](int64_t tiles) { return static_cast<double>((tiles * batch + units - 1) / units); };
-    const int64_t sym = count_tiles(m, m, 128 * s.ctas, s.nt, true), gen = count_tiles(m, n, 128 * s.ctas, s.nt, false);
-    const double cost = (waves(sym) * static_cast<double>(n + m) + waves(gen) * static_cast<double>(m)) * (s.nt + 32) * (s.ctas == 2 ? 1.0 : 1.5);
+    int64_t sym = 0, gen = 0;
+    double depth[2] = {0.0, 0.0};
+    for (int i = 0; i < pieces; ++i) {
+      sym += p[i].batch * count_tiles(p[i].m, p[i].m, 128 * s.ctas, s.nt, true);
+      gen += p[i].batch * count_tiles(p[i].m, p[i].n, 128 * s.ctas, s.nt, false);
+      depth[0] = std::max(depth[0], static_cast<double>(p[i].n));
+      depth[1] = std::max(depth[1], static_cast<double>(p[i].m));
+    }
+    auto waves = [&](int64_t tiles) { return static_cast<double>((tiles + units - 1) / units); };
+    auto tile = [&](double deep) {
+      return deep / 64.0 * (4 * (fine ? 3 : 1) * std::max(65.0, s.nt / 2.0) + 100.0) + 5000.0 + 40.0 * s.nt;
+    };
+    const double cost = waves(sym) * (tile(depth[0]) + tile(depth[1])) + waves(gen) * tile(depth[1]);
     if (cost < least) least = cost, best = s;
   }
   return best;
@@ -899,11 +941,18 @@ int launch_flow_as(FlowArgs& a, const Places& places, cudaStream_t stream) {
   using S = FlowShape<CTAS, NT, TERMS>;
   static SmemAllowed allowed;
   if (int rc = allow_smem(flow_kernel<CTAS, NT, TERMS>, S::kSmem, allowed)) return rc;
-  a.col_tiles[0] = (a.m + NT - 1) / NT;
-  a.col_tiles[1] = (a.n + NT - 1) / NT;
-  a.tiles[0] = static_cast<int>(count_tiles(a.m, a.m, S::kHeight, NT, true));
-  a.tiles[1] = static_cast<int>(count_tiles(a.m, a.n, S::kHeight, NT, false));
-  const int64_t most = static_cast<int64_t>(a.batch) * std::max(a.tiles[0], a.tiles[1]);
+  int64_t sym = 0, gen = 0;
+  for (int i = 0; i < a.groups; ++i) {
+    FlowGroup& g = a.group[i];
+    g.col_tiles[0] = (g.m + NT - 1) / NT;
+    g.col_tiles[1] = (g.n + NT - 1) / NT;
+    g.tiles[0] = static_cast<int>(count_tiles(g.m, g.m, S::kHeight, NT, true));
+    g.tiles[1] = static_cast<int>(count_tiles(g.m, g.n, S::kHeight, NT, false));
+    sym += static_cast<int64_t>(g.batch) * g.tiles[0];
+    gen += static_cast<int64_t>(g.batch) * g.tiles[1];
+  }
+  const int64_t most = std::max(sym, gen);
+  a.per_step = static_cast<int>(2 * sym + gen);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, sm_count() / CTAS) * CTAS));
   cfg.blockDim = dim3(Epilogue<TERMS>::kThreads);
@@ -926,64 +975,77 @@ int launch_flow(FlowArgs& a, const Places& places, TileSize s, cudaStream_t stre
   return launch_flow_as<1, 64, TERMS>(a, places, stream);
 }
 
-// Iterates `batch` matrices of one shape, which are at `from`; the results go to `places`.
-adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places, int64_t m, int64_t n, int batch, bool fine,
+// Iterates the pieces' matrices, which are at `from`, all in one launch; the results go to `places`.
+adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places, const Piece* pieces, int count, bool fine,
                         const Iteration& it, const Result& res, char* scratch, cudaStream_t stream) {
-  const ScratchMap l(m, n, batch, fine);
   FlowArgs f = {};
-  bool ok = true;
-  for (int part = 0; part < 2; ++part) {
-    for (int i = 0; i < 2; ++i) {
-      f.x[i][part] = reinterpret_cast<__half*>(scratch + l.x[i][part]);
-      if (part > 0 && !fine) continue;
-      ok = ok && make_map(&f.x_tall[i][part], f.x[i][part], m, n, l.ldx, batch, 128) &&
-           make_map(&f.x_square[i][part], f.x[i][part], m, n, l.ldx, batch, 64);
-    }
-    if (part > 0 && !fine) continue;
-    f.a[part] = reinterpret_cast<__half*>(scratch + l.a[part]);
-    f.b[part] = reinterpret_cast<__half*>(scratch + l.b[part]);
-    ok = ok && make_map(&f.a_tall[part], f.a[part], m, m, l.lda, batch, 128) && make_map(&f.a_square[part], f.a[part], m, m, l.lda, batch, 64) &&
-         make_map(&f.b_tall[part], f.b[part], m, m, l.lda, batch, 128);
-  }
-  if (!ok) return ADASUM_ERR_CUDA;
-  f.da = reinterpret_cast<float*>(scratch + l.da);
-  f.db = reinterpret_cast<float*>(scratch + l.db);
-  f.ldx = l.ldx;
-  f.lda = l.lda;
-  f.m = static_cast<int>(m);
-  f.n = static_cast<int>(n);
-  f.batch = batch;
+  f.groups = count;
   f.steps = it.steps;
-  f.ready = reinterpret_cast<int*>(scratch + l.ready);
   f.last = res.last;
   f.dest = res.dest;
   f.dest_dtype = res.dtype;
   f.dest_vec = is_aligned(res.dest, 16);
   f.keep = res.keep;
-  std::copy(res.step, res.step + 2, f.step);
   std::copy(it.coefficients, it.coefficients + 3 * it.steps, f.coefficients);
-  src.partials = reinterpret_cast<float*>(scratch + l.partials);
-  src.ready = f.ready;
-  src.chunks = l.chunks;
-  src.per_chunk = l.per_chunk;
   src.eps = it.eps;
   src.vec = is_aligned(src.x, 16) && is_aligned(src.momentum, 16);
-  src.hi = f.x[0][0];
-  src.lo = f.x[0][1];
-  src.m = m;
-  src.n = n;
-  src.ldx = l.ldx;
-  const double elements = static_cast<double>(m) * n * batch, e = dtype_bytes(src.dtype);
-  adasum_status_t st = counted_launch(stream, "update_squares", elements * (e + (src.momentum ? 8 : 0)), [&] {
-    return launch_pdl(squares_kernel, dim3(l.chunks, batch), dim3(256), 0, stream, src, from);
-  });
-  if (st) return st;
-  st = counted_launch(stream, "update_normalize", elements * (e + (src.momentum ? 4 : 0) + 4), [&] {
-    return launch_pdl(normalize_kernel, dim3(static_cast<unsigned>((n + 63) / 64), static_cast<unsigned>((m + 63) / 64), batch),
-                      dim3(256), 0, stream, src, from);
-  });
-  if (st) return st;
-  const TileSize size = tile_size(m, n, batch);
+  int first = 0;
+  for (int i = 0; i < count; ++i) {
+    const int64_t m = pieces[i].m, n = pieces[i].n;
+    const int batch = pieces[i].batch;
+    const ScratchMap l(m, n, batch, fine);
+    FlowGroup& g = f.group[i];
+    bool ok = true;
+    for (int part = 0; part < 2; ++part) {
+      for (int j = 0; j < 2; ++j) {
+        g.x[j][part] = reinterpret_cast<__half*>(scratch + l.x[j][part]);
+        if (part > 0 && !fine) continue;
+        ok = ok && make_map(&g.x_tall[j][part], g.x[j][part], m, n, l.ldx, batch, 128) &&
+             make_map(&g.x_square[j][part], g.x[j][part], m, n, l.ldx, batch, 64);
+      }
+      if (part > 0 && !fine) continue;
+      g.a[part] = reinterpret_cast<__half*>(scratch + l.a[part]);
+      g.b[part] = reinterpret_cast<__half*>(scratch + l.b[part]);
+      ok = ok && make_map(&g.a_tall[part], g.a[part], m, m, l.lda, batch, 128) &&
+           make_map(&g.a_square[part], g.a[part], m, m, l.lda, batch, 64) && make_map(&g.b_tall[part], g.b[part], m, m, l.lda, batch, 128);
+    }
+    if (!ok) return ADASUM_ERR_CUDA;
+    g.da = reinterpret_cast<float*>(scratch + l.da);
+    g.db = reinterpret_cast<float*>(scratch + l.db);
+    g.ldx = l.ldx;
+    g.lda = l.lda;
+    g.m = static_cast<int>(m);
+    g.n = static_cast<int>(n);
+    g.batch = batch;
+    g.first = src.first = first;
+    g.ready = src.ready = reinterpret_cast<int*>(scratch + l.ready);
+    std::copy(pieces[i].step, pieces[i].step + 2, g.step);
+    src.partials = reinterpret_cast<float*>(scratch + l.partials);
+    src.chunks = l.chunks;
+    src.per_chunk = l.per_chunk;
+    src.hi = g.x[0][0];
+    src.lo = g.x[0][1];
+    src.m = m;
+    src.n = n;
+    src.ldx = l.ldx;
+    if (src.momentum) {  // (dense)
+      src.rows = m;
+      src.cols = src.ld = n;
+    }
+    const double elements = static_cast<double>(m) * n * batch, e = dtype_bytes(src.dtype);
+    adasum_status_t st = counted_launch(stream, "update_squares", elements * (e + (src.momentum ? 8 : 0)), [&] {
+      return launch_pdl(squares_kernel, dim3(l.chunks, batch), dim3(256), 0, stream, src, from);
+    });
+    if (st) return st;
+    st = counted_launch(stream, "update_normalize", elements * (e + (src.momentum ? 4 : 0) + 4), [&] {
+      return launch_pdl(normalize_kernel, dim3(static_cast<unsigned>((n + 63) / 64), static_cast<unsigned>((m + 63) / 64), batch),
+                        dim3(256), 0, stream, src, from);
+    });
+    if (st) return st;
+    first += batch;
+    scratch += l.bytes;
+  }
+  const TileSize size = tile_size(pieces, count, fine);
   return counted_launch(stream, fine ? "update_iterate3" : "update_iterate", 0.0, [&] {
     return fine ? launch_flow<3>(f, places, size, stream) : launch_flow<1>(f, places, size, stream);
   });
@@ -997,24 +1059,26 @@ adasum_status_t check_iteration(int steps, const float* coefficients, float eps)
   return ADASUM_OK;
 }
 
-// Matrices whose shapes agree once the taller ones are transposed; `members` in their order.
-struct Group {
-  int64_t m, n;
-  std::vector<int> members;
+// The matrices of a step, equal shapes together and large ones first, and their pieces.
+struct StepPlan {
+  std::vector<int> order;  // segments
+  std::vector<Piece> pieces;
 };
-std::vector<Group> group_shapes(const int64_t* rows, const int64_t* cols, int L) {
-  std::vector<int> order;
+StepPlan plan_step(const int64_t* rows, const int64_t* cols, int L) {
+  StepPlan plan;
   for (int s = 0; s < L; ++s)
-    if (rows[s] > 0 && cols[s] > 0) order.push_back(s);
+    if (rows[s] > 0 && cols[s] > 0) plan.order.push_back(s);
   auto m = [&](int s) { return std::min(rows[s], cols[s]); };
   auto n = [&](int s) { return std::max(rows[s], cols[s]); };
-  std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return m(a) != m(b) ? m(a) > m(b) : n(a) > n(b); });
-  std::vector<Group> groups;
-  for (int s : order) {
-    if (groups.empty() || groups.back().m != m(s) || groups.back().n != n(s)) groups.push_back(Group{m(s), n(s), {}});
-    groups.back().members.push_back(s);
+  std::stable_sort(plan.order.begin(), plan.order.end(), [&](int a, int b) { return m(a) != m(b) ? m(a) > m(b) : n(a) > n(b); });
+  for (size_t i = 0, j; i < plan.order.size(); i = j) {
+    const int s = plan.order[i];
+    for (j = i + 1; j < plan.order.size() && m(plan.order[j]) == m(s) && n(plan.order[j]) == n(s);) ++j;
+    const int64_t all = static_cast<int64_t>(j - i), chunk = chunk_of(m(s), n(s), all, true);
+    for (int64_t done = 0; done < all; done += chunk)
+      plan.pieces.push_back(Piece{m(s), n(s), static_cast<int>(std::min(chunk, all - done)), {0.f, 0.f}});
   }
-  return groups;
+  return plan;
 }
 
 bool fits(int64_t rows, int64_t cols) { return rows <= ADASUM_NEWTON_SCHULZ_MAX_DIM && cols <= ADASUM_NEWTON_SCHULZ_MAX_DIM; }
@@ -1079,8 +1143,9 @@ adasum_status_t adasum_orthogonalize(const void* x, int64_t batch, int64_t rows,
     src.rows = rows;
     src.cols = cols;
     src.ld = ld;
-    Result res = {1, static_cast<char*>(out) + b0 * rows * cols * e, static_cast<int>(dtype), 0.f, {0.f, 0.f}};
-    if (adasum_status_t st = iterate(src, from, to, m, n, count, fine, {steps, coefficients, eps}, res, static_cast<char*>(scratch), stream))
+    const Result res = {1, static_cast<char*>(out) + b0 * rows * cols * e, static_cast<int>(dtype), 0.f};
+    const Piece piece = {m, n, count, {0.f, 0.f}};
+    if (adasum_status_t st = iterate(src, from, to, &piece, 1, fine, {steps, coefficients, eps}, res, static_cast<char*>(scratch), stream))
       return st;
   }
   return ADASUM_OK;
@@ -1091,9 +1156,12 @@ int64_t adasum_muon_step_scratch_bytes(const int64_t* rows, const int64_t* cols,
   for (int s = 0; s < L; ++s)
     if (!fits(rows[s], cols[s])) return 0;
   try {
-    int64_t most = 0;
-    for (const Group& g : group_shapes(rows, cols, L))
-      most = std::max(most, ScratchMap(g.m, g.n, chunk_of(g.m, g.n, static_cast<int64_t>(g.members.size()), true), true).bytes);
+    const StepPlan plan = plan_step(rows, cols, L);
+    int64_t most = 0, bytes = 0;
+    for (size_t i = 0; i < plan.pieces.size();) {
+      i += take_pieces(plan.pieces.data() + i, plan.pieces.data() + plan.pieces.size(), true, bytes);
+      most = std::max(most, bytes);
+    }
     return most;
   } catch (...) {  // (out of host memory)
     return -1;
@@ -1133,32 +1201,33 @@ adasum_status_t adasum_muon_step(const void* grad, adasum_dtype_t dtype, const i
   if (adasum_status_t st = set.check()) return st;
   if (encode_tiled() == nullptr) return ADASUM_ERR_CUDA;
   try {
-    for (const Group& g : group_shapes(rows, cols, L)) {
-      const int64_t all = static_cast<int64_t>(g.members.size()), chunk = chunk_of(g.m, g.n, all, true);
-      for (int64_t b0 = 0; b0 < all; b0 += chunk) {
-        const int count = static_cast<int>(std::min(chunk, all - b0));
-        Places places = {};
-        for (int i = 0; i < count; ++i) {
-          const int s = g.members[b0 + i];
-          places.at[i] = 2 * seg_offsets[s] + (rows[s] > cols[s]);
-        }
-        SourceArgs src = {};
-        src.x = grad;
-        src.momentum = momentum;
-        src.dtype = dtype;
-        src.rows = g.m;
-        src.cols = src.ld = g.n;
-        src.mu = mu;
-        src.nesterov = nesterov != 0;
-        // the step of a wide matrix (rows <= cols), and of a tall one
-        const double wide = scale == ADASUM_MUON_SCALE_RMS ? 0.2 * std::sqrt(static_cast<double>(g.n)) : 1.0;
-        const double tall = scale == ADASUM_MUON_SCALE_SPECTRAL ? std::sqrt(static_cast<double>(g.n) / static_cast<double>(g.m)) : wide;
-        const Result res = {2, master_w, kF32, static_cast<float>(1.0 - static_cast<double>(lr) * weight_decay),
-                            {static_cast<float>(lr * wide), static_cast<float>(lr * tall)}};
-        if (adasum_status_t st = iterate(src, places, places, g.m, g.n, count, true, {steps, coefficients, eps}, res,
-                                         static_cast<char*>(scratch), stream))
-          return st;
-      }
+    StepPlan plan = plan_step(rows, cols, L);
+    for (Piece& p : plan.pieces) {  // the step of a wide matrix (rows <= cols), and of a tall one
+      const double wide = scale == ADASUM_MUON_SCALE_RMS ? 0.2 * std::sqrt(static_cast<double>(p.n)) : 1.0;
+      const double tall = scale == ADASUM_MUON_SCALE_SPECTRAL ? std::sqrt(static_cast<double>(p.n) / static_cast<double>(p.m)) : wide;
+      p.step[0] = static_cast<float>(lr * wide);
+      p.step[1] = static_cast<float>(lr * tall);
+    }
+    SourceArgs src = {};
+    src.x = grad;
+    src.momentum = momentum;
+    src.dtype = dtype;
+    src.mu = mu;
+    src.nesterov = nesterov != 0;
+    const Result res = {2, master_w, kF32, static_cast<float>(1.0 - static_cast<double>(lr) * weight_decay)};
+    const int* segment = plan.order.data();
+    for (size_t i = 0; i < plan.pieces.size();) {
+      int64_t bytes;
+      const int count = take_pieces(plan.pieces.data() + i, plan.pieces.data() + plan.pieces.size(), true, bytes);
+      Places places = {};
+      int at = 0;
+      for (int k = 0; k < count; ++k)
+        for (int j = 0; j < plan.pieces[i + k].batch; ++j, ++segment)
+          places.at[at++] = 2 * seg_offsets[*segment] + (rows[*segment] > cols[*segment]);
+      if (adasum_status_t st = iterate(src, places, places, plan.pieces.data() + i, count, true, {steps, coefficients, eps}, res,
+                                       static_cast<char*>(scratch), stream))
+        return st;
+      i += count;
     }
   } catch (...) {
     return ADASUM_ERR_NO_MEMORY;
