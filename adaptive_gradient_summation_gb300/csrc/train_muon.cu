@@ -907,30 +907,33 @@ int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
   for (int64_t r = 0; r < row_tiles; ++r) tiles += std::min<int64_t>(sym_tiles(static_cast<int>(r), height, nt), col_tiles);
   return tiles;
 }
-// CTAs and columns of a tile: those for which the products, one after the other, take least, in
-// cycles as measured: for 64 along the depth an instruction's time (at least 65 each, what its
-// thread takes) and 100; for a tile 5000 and 40 a column until its results are written.
+// CTAs and columns of a tile: those for which the products of a step, one after the other, take
+// least.  Wide tiles copy less and multiply faster, narrow ones give more CTAs something to do:
+// in cycles, as fitted to runs of 24 x (1024 x 1024), a tile takes `deep` for 64 along the
+// depth and `end` for its results.  (us of all five steps, by 2 x 256, 128 and 64 columns: 24 x
+// (1024 x 4096) bf16 1619, 2113, 3043, fp32 4559, 4596, 5910; one of 2048 x 2048 297, 262, 376 and
+// 710, 509, 703; one of 256 x 1024 175, 124, 95 and 356, 192, 142.)
 struct TileSize {
   int ctas, nt;
+  double deep[2], end[2];  // of bf16 and fp32 results
 };
 TileSize tile_size(const Piece* p, int pieces, bool fine) {
-  TileSize best = {2, 256};
+  constexpr TileSize kSizes[3] = {
+      {2, 256, {640, 1900}, {11000, 27000}}, {1, 128, {480, 1300}, {7800, 9200}}, {1, 64, {400, 620}, {3400, 8700}}};
+  TileSize best = kSizes[0];
   double least = 1e300;
-  for (const TileSize s : {TileSize{2, 256}, TileSize{1, 128}, TileSize{1, 64}}) {
+  for (const TileSize& s : kSizes) {
     const int64_t units = sm_count() / s.ctas;
-    int64_t sym = 0, gen = 0;
-    double depth[2] = {0.0, 0.0};
+    int64_t sym = 0, gen = 0, deep = 0, low = 0;  // (the deepest of the pieces' products)
     for (int i = 0; i < pieces; ++i) {
       sym += p[i].batch * count_tiles(p[i].m, p[i].m, 128 * s.ctas, s.nt, true);
       gen += p[i].batch * count_tiles(p[i].m, p[i].n, 128 * s.ctas, s.nt, false);
-      depth[0] = std::max(depth[0], static_cast<double>(p[i].n));
-      depth[1] = std::max(depth[1], static_cast<double>(p[i].m));
+      deep = std::max(deep, (p[i].n + 63) / 64);
+      low = std::max(low, (p[i].m + 63) / 64);
     }
     auto waves = [&](int64_t tiles) { return static_cast<double>((tiles + units - 1) / units); };
-    auto tile = [&](double deep) {
-      return deep / 64.0 * (4 * (fine ? 3 : 1) * std::max(65.0, s.nt / 2.0) + 100.0) + 5000.0 + 40.0 * s.nt;
-    };
-    const double cost = waves(sym) * (tile(depth[0]) + tile(depth[1])) + waves(gen) * tile(depth[1]);
+    auto tile = [&](int64_t stages) { return static_cast<double>(stages) * s.deep[fine] + s.end[fine]; };
+    const double cost = waves(sym) * (tile(deep) + tile(low)) + waves(gen) * tile(low);
     if (cost < least) least = cost, best = s;
   }
   return best;
