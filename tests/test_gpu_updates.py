@@ -357,3 +357,17 @@ def test_guards(native, monkeypatch, rows, cols):
         assert (buf[x.numel():] == 7).all()
     torch.cuda.synchronize()
     assert len(guards) == 2 and all((g == 171).all() for g in guards)
+
+
+def test_full_grids_on_two_streams(native):
+    """Calls whose CTAs fill the GPU each, at once: CTAs of one wait for each other."""
+    xs = [updates(16, 512, 640, gen=gen(i)).to(BF16) for i in range(3)]
+    want = [ags.orthogonalize(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [ags.orthogonalize(x, stream=s) for x, s in zip(xs, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    check_status()
