@@ -321,12 +321,11 @@ struct FlowShape {
   static constexpr int kStages = 196608 / kStageBytes < 6 ? 196608 / kStageBytes : 6;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + Epilogue<TERMS>::kWarps * Epilogue<TERMS>::kFloats * 4;
   static_assert(kSmem + 1024 <= 232448, "with the barriers, a CTA's shared memory");
-  // Accumulators.  A product waits for the one before it on the same sums (about 150 cycles, however
-  // narrow it is), so narrow tiles have several sums that take turns, 256 columns in all.
-  static constexpr int kChains = 256 / NT;
-  static constexpr int kBuffers = TERMS == 3 ? 1 : 2;  // of 256 columns
-  static constexpr int kCross = 256;                   // column of the products with a low part
-  static constexpr int kCols = 512;
+  // Two sets of 256 columns, one filled while the other is read.  TERMS = 3: half of a set for the
+  // high parts' product, half for the two others.  A narrower tile's sums take turns: a product
+  // waits for the one before it on the same sums.
+  static constexpr int kSet = 256, kHigh = TERMS == 3 ? 128 : 256, kChains = kHigh / NT, kCols = 512;
+  static_assert(NT <= kHigh, "a set holds a tile");
   static constexpr int kRun = TERMS == 3 ? 8 : 1 << 30;  // stages of 64 along the depth
   static constexpr int kBlocks = NT / 64;  // of an epilogue warp
 };
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
   using E = Epilogue<TERMS>;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-  __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], cross_empty;
+  __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int stop;
   __shared__ int copied;  // tiles whose operands this CTA has found ready
@@ -372,7 +371,6 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) mbar_init(&full[i], 2), mbar_init(&empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], E::kWarps * CTAS);
-    mbar_init(&cross_empty, E::kWarps * CTAS);
     mbar_fence_init();
     stop = 0;
     copied = 0;
@@ -496,10 +494,10 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      int acc = 0, tiles = 0, s = 0;
+      int acc = 0, s = 0;
       uint32_t phase = 0;
       bool ok = tmem_slot == 0;  // (all of TMEM is this CTA's, so it begins at 0, which the compiler may know)
-      for (int at = first; ok && at < total; at += stride, ++tiles) {
+      for (int at = first; ok && at < total; at += stride) {
         const Tile t = locate(at);
         const int ks = depth(t);
         const bool mn = t.kind == kApply;
@@ -508,7 +506,10 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
         const uint32_t q_block = mn ? 8192 : 16, q_step = mn ? 128 : 2;
         int in_run = 0;
         for (int k = 0; k < ks; ++k) {
-          const int buffer = acc % S::kBuffers;
+          if (in_run == 0) {
+            if (!(ok = wait(&acc_empty[acc & 1], ((acc >> 1) & 1) ^ 1))) break;
+            tc_fence_after();
+          }
           if (!(ok = wait(&full[s], phase))) break;
           tc_fence_after();
           const uint32_t base = smem_addr(stages) + s * S::kStageBytes, qbase = base + S::kParts * S::kPBytes;
@@ -518,22 +519,15 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
             for (int e = 0; e < 4; ++e)
               umma_f16<CTAS>(d + e % S::kChains * NT, p + e * 2, q + e * q_step, idesc, !clear || e >= S::kChains);
           };
-          if constexpr (TERMS == 3) {  // (these while the last run is drained)
-            if (k == 0) {
-              if (!(ok = wait(&cross_empty, (tiles & 1) ^ 1))) break;
-              tc_fence_after();
-            }
-            multiply(0, 1, S::kCross, k == 0);
-            multiply(1, 0, S::kCross, false);
+          const uint32_t set = (acc & 1) * S::kSet;
+          multiply(0, 0, set, in_run == 0);
+          if constexpr (TERMS == 3) {
+            multiply(0, 1, set + S::kHigh, in_run == 0);
+            multiply(1, 0, set + S::kHigh, false);
           }
-          if (in_run == 0) {
-            if (!(ok = wait(&acc_empty[buffer], ((acc / S::kBuffers) & 1) ^ 1))) break;
-            tc_fence_after();
-          }
-          multiply(0, 0, buffer * 256, in_run == 0);
           umma_commit<CTAS>(&empty[s]);
           if (++in_run == run || k + 1 == ks) {
-            umma_commit<CTAS>(&acc_full[buffer]);
+            umma_commit<CTAS>(&acc_full[acc & 1]);
             ++acc;
             in_run = 0;
           }
@@ -734,56 +728,51 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
 #pragma unroll
           for (int c = 0; c < E::kCols; ++c) v[k][c] = 0.f;
         for (int run = 0; ok && run < ks; run += S::kRun, ++acc) {
-          const int buffer = acc % S::kBuffers;
-          if (!(ok = wait(&acc_full[buffer], (acc / S::kBuffers) & 1))) break;
+          if (!(ok = wait(&acc_full[acc & 1], (acc >> 1) & 1))) break;
           tc_fence_after();
           const float gain = cut_off<S::kChains>(min(ks - run, S::kRun));
+          const uint32_t set = from + (acc & 1) * S::kSet;
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k)
             if (there(k)) {
 #pragma unroll
-              for (int c = 0; c < S::kChains; ++c) tmem_add<E::kCols>(from + buffer * 256 + c * NT + k * kStep, v[k], gain);
+              for (int c = 0; c < S::kChains; ++c) {
+                tmem_add<E::kCols>(set + c * NT + k * kStep, v[k], gain);
+                tmem_add<E::kCols>(set + S::kHigh + c * NT + k * kStep, v[k], 1.f);
+              }
             }
-          release(&acc_empty[buffer]);
+          release(&acc_empty[acc & 1]);
         }
         if (!ok) break;
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k)
-          if (there(k)) {
-#pragma unroll
-            for (int c = 0; c < S::kChains; ++c) tmem_add<E::kCols>(from + S::kCross + c * NT + k * kStep, v[k], 1.f);
-          }
-        release(&cross_empty);
-#pragma unroll
-        for (int k = 0; k < S::kBlocks; ++k)
           if (there(k)) finish(k, v[k], next);
       } else {
-        const int buffer = acc % S::kBuffers;
-        if (!wait(&acc_full[buffer], (acc / S::kBuffers) & 1)) break;
-        ++acc;
+        if (!wait(&acc_full[acc & 1], (acc >> 1) & 1)) break;
         tc_fence_after();
+        const float gain = TERMS == 3 ? cut_off<S::kChains>(ks) : 1.f;
+        const uint32_t set = from + (acc & 1) * S::kSet;
 #pragma unroll 1
         for (int k = 0; k < S::kBlocks; ++k) {
           const Added now = next;
           fetch(k + 1, next);
           if (!there(k)) continue;
           float v[E::kCols];
-          const float gain = TERMS == 3 ? cut_off<S::kChains>(ks) : 1.f;
-          tmem_load<E::kCols>(from + buffer * 256 + k * kStep, v);
+          tmem_load<E::kCols>(set + k * kStep, v);
           if constexpr (TERMS == 3) {
 #pragma unroll
             for (int c = 0; c < E::kCols; ++c) v[c] *= gain;
           }
 #pragma unroll
-          for (int c = 1; c < S::kChains; ++c) tmem_add<E::kCols>(from + buffer * 256 + c * NT + k * kStep, v, gain);
+          for (int c = 1; c < S::kChains; ++c) tmem_add<E::kCols>(set + c * NT + k * kStep, v, gain);
           if constexpr (TERMS == 3) {
 #pragma unroll
-            for (int c = 0; c < S::kChains; ++c) tmem_add<E::kCols>(from + S::kCross + c * NT + k * kStep, v, 1.f);
+            for (int c = 0; c < S::kChains; ++c) tmem_add<E::kCols>(set + S::kHigh + c * NT + k * kStep, v, 1.f);
           }
           finish(k, v, now);
         }
-        release(&acc_empty[buffer]);
-        if constexpr (TERMS == 3) release(&cross_empty);
+        release(&acc_empty[acc & 1]);
+        ++acc;
       }
       // what this warp wrote is there, for others' copies too
       if (!final) {
@@ -918,8 +907,8 @@ struct TileSize {
   double deep[2], end[2];  // of bf16 and fp32 results
 };
 TileSize tile_size(const Piece* p, int pieces, bool fine) {
-  constexpr TileSize kSizes[3] = {
-      {2, 256, {640, 1900}, {11000, 27000}}, {1, 128, {480, 1300}, {7800, 9200}}, {1, 64, {400, 620}, {3400, 8700}}};
+  const TileSize kSizes[3] = {
+      {2, fine ? 128 : 256, {640, 900}, {11000, 9200}}, {1, 128, {480, 1300}, {7800, 9200}}, {1, 64, {400, 620}, {3400, 8700}}};
   TileSize best = kSizes[0];
   double least = 1e300;
   for (const TileSize& s : kSizes) {
@@ -973,7 +962,7 @@ int launch_flow_as(FlowArgs& a, const Places& places, cudaStream_t stream) {
 }
 template <int TERMS>
 int launch_flow(FlowArgs& a, const Places& places, TileSize s, cudaStream_t stream) {
-  if (s.ctas == 2) return launch_flow_as<2, 256, TERMS>(a, places, stream);
+  if (s.ctas == 2) return launch_flow_as<2, TERMS == 3 ? 128 : 256, TERMS>(a, places, stream);
   if (s.nt == 128) return launch_flow_as<1, 128, TERMS>(a, places, stream);
   return launch_flow_as<1, 64, TERMS>(a, places, stream);
 }
