@@ -897,21 +897,22 @@ int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
   return tiles;
 }
 // CTAs and columns of a tile: those for which the products of a step, one after the other, take
-// least.  Wide tiles copy less and multiply faster, narrow ones give more CTAs something to do:
-// in cycles, as fitted to runs of 24 x (1024 x 1024), a tile takes `deep` for 64 along the
-// depth and `end` for its results.  (us of all five steps, by 2 x 256, 128 and 64 columns: 24 x
-// (1024 x 4096) bf16 1619, 2113, 3043, fp32 4559, 4596, 5910; one of 2048 x 2048 297, 262, 376 and
-// 710, 509, 703; one of 256 x 1024 175, 124, 95 and 356, 192, 142.)
+// least.  Wide tiles copy less for a product, narrow ones give more CTAs something to do: in
+// cycles, about as measured, a tile takes `deep` for 64 along the depth and `end` for its
+// results.  (us of all five steps by 2 x 256, 128 and 64 columns, bf16: 24 x (1024 x 4096) 1622,
+// 2060, 3030, one of 2048 x 2048 296, 259, 371, one of 256 x 1024 187, 127, 93; by 2 x 128, 128 and 64,
+// fp32: 4238, 4203, 5505; 465, 498, 630; 218, 206, 133.)
 struct TileSize {
-  int ctas, nt;
-  double deep[2], end[2];  // of bf16 and fp32 results
+  int ctas, nt, deep, end;
 };
 TileSize tile_size(const Piece* p, int pieces, bool fine) {
-  const TileSize kSizes[3] = {
-      {2, fine ? 128 : 256, {640, 900}, {11000, 9200}}, {1, 128, {480, 1300}, {7800, 9200}}, {1, 64, {400, 620}, {3400, 8700}}};
+  constexpr TileSize kBf16[3] = {{2, 256, 640, 11000}, {1, 128, 480, 7800}, {1, 64, 400, 3400}};
+  constexpr TileSize kFp32[3] = {{2, 128, 850, 14000}, {1, 128, 1000, 12000}, {1, 64, 620, 6600}};
+  const TileSize* const kSizes = fine ? kFp32 : kBf16;
   TileSize best = kSizes[0];
   double least = 1e300;
-  for (const TileSize& s : kSizes) {
+  for (int which = 0; which < 3; ++which) {
+    const TileSize& s = kSizes[which];
     const int64_t units = sm_count() / s.ctas;
     int64_t sym = 0, gen = 0, deep = 0, low = 0;  // (the deepest of the pieces' products)
     for (int i = 0; i < pieces; ++i) {
@@ -921,7 +922,7 @@ TileSize tile_size(const Piece* p, int pieces, bool fine) {
       low = std::max(low, (p[i].m + 63) / 64);
     }
     auto waves = [&](int64_t tiles) { return static_cast<double>((tiles + units - 1) / units); };
-    auto tile = [&](int64_t stages) { return static_cast<double>(stages) * s.deep[fine] + s.end[fine]; };
+    auto tile = [&](int64_t stages) { return static_cast<double>(stages) * s.deep + s.end; };
     const double cost = waves(sym) * (tile(deep) + tile(low)) + waves(gen) * tile(low);
     if (cost < least) least = cost, best = s;
   }
