@@ -164,7 +164,8 @@ __device__ __forceinline__ F2 rounded(F2 x) {
 // worked on, keep coming: 65536 x 2048 bf16 in 90 us, 5.9 TB/s (through shared memory by
 // asynchronous copies, one to three rows ahead, 101 to 105).  Rows that fill their team's
 // columns (FULL) need no test per column: with the checkpoint kept 113 us against 121.
-// The root-mean-square norms have the sum of squares alone, and no bias.  RMSFIGURES
+// The root-mean-square norms have the sum of squares alone, and no bias: 65536 x 2048 bf16 in 93 us,
+// with the residual, two tensors in and two out, 177, 6.1 TB/s, keeping 8 bits too 203, 6.0 TB/s.
 template <typename T, int LAYOUT, int W, int NV, bool KEEP, bool FULL, int NORM>
 __global__ void __launch_bounds__(Team<W, NV>::kThreads, W < 16 ? kNormCtasPerSm : 1) norm_kernel(const NormArgs a) {
   using TM = Team<W, NV>;
@@ -370,7 +371,8 @@ struct GradShape {
 // CTA's rows in registers, joined over its teams at the end and written as the CTA's partial.
 // A CTA's rows all belong to one worker.  Bound by the bytes of dy, x and dx: 65536 x 1024 bf16
 // of 16 workers in 72 us, 5.6 TB/s; from codes, 65536 x 2048 with the output once more, 159 us,
-// 5.9 TB/s.
+// 5.9 TB/s.  The root-mean-square norm has one sum per row and no db, and may add the gradient past
+// the norm: 65536 x 1024 bf16 of 16 workers with it 76 us, 7.1 TB/s.
 template <typename T, int LAYOUT, int W, int NV, bool KEPT, bool FULL, int NORM>
 __global__ void __launch_bounds__(Team<W, NV>::kThreads, GradShape<T, W, NV>::kCtas)
     norm_grad_kernel(const NormGradArgs a, const __grid_constant__ WorkerRows rows,

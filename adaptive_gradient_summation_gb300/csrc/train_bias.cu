@@ -5,6 +5,7 @@
 // to 6 us of it are the launch), unless they are said to be of a pass, a call among others
 // through the Python binding.
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "adasum_host.h"
@@ -54,7 +55,8 @@ struct BiasArgs {
 // and a warp's 32 E keys; the biases that occur there, one for each diagonal, go through shared
 // memory (a word of padding every 32, so that lanes 4 or 8 apart meet no bank twice) into the
 // registers of a warp's four rows, which serve all its sequences.  Bound by the bytes of the
-// scores.  BIASFIGURES
+// scores: 64 x 16 x 512 x 512 bf16 in 188 us, 5.7 TB/s, fp32 337, 6.4 TB/s; 511 x 513 of them bf16, one
+// value a load and store, 376; the bias alone of 16 x 2048 x 2048 fp32 51, 5.3 TB/s.
 template <typename T, int E, bool VEC, bool SCORES>
 __global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constant__ BiasArgs a) {
   pdl_enter();
@@ -130,13 +132,14 @@ __global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constan
 // ----------------------------------------------------------------------------- gradient
 
 constexpr int kBiasRows = 256;  // at most, of a warp
-constexpr int kBiasKeys = 256;  // of a warp, eight a lane
+constexpr int kBiasKeys = 256;  // of a warp at most, eight a lane
+constexpr int kBiasGradCtas = 2;  // of an SM (3 with half as many rows on their way: 140 us against 99)
 
 struct BiasGradArgs {
   const void* d;
   int64_t stride_b, stride_h, stride_q;
   int64_t heads, queries, keys, offset;
-  int rows;            // of a unit
+  int rows, width;     // queries and keys of a unit
   int row_units, key_units, batch_units, per_unit;  // units of one worker and head; sequences of a unit
   int groups;          // CTAs of one worker and head, eight units each
   float* partials;     // [worker, head][group][bucket]; null: one group, the gradient is written
@@ -163,11 +166,14 @@ __device__ __forceinline__ void put_bucket(const BiasOut& o, int k, int64_t h, i
 // running sums of 256 diagonals in registers: from one query to the next a diagonal moves on
 // by one key, so the sums move by one register (or lane), the last lane's leaves the window and
 // a new one begins.  The diagonals' sums end in shared memory and are added up per bucket, in
-// an order that depends on the sizes alone.  One read of the gradients, an addition a value.
-// GRADFIGURES
-// VEC: a lane's eight keys are neighbours on 16-byte boundaries; else they are 32 apart.
+// an order that depends on the sizes alone.  One read of the gradients, an addition a value: bound
+// by bytes, 64 x 16 x 512 x 512 of 16 workers bf16 in 92 us, 5.9 TB/s, fp32 168, 6.4 TB/s.  511 x 513
+// of them bf16 in 161 (loaded value by value, 32 keys apart a lane: 763); one sequence each of 4
+// workers of 16 x 2048 x 2048 in 112 us, 4.8 TB/s.
+// VEC: all rows of keys begin on 16-byte boundaries; else the pieces of 16 bytes that hold them do,
+// and the values move over by less than a lane.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBiasThreads, VEC ? 2 : 3) bias_grad_kernel(const __grid_constant__ BiasGradArgs a, const __grid_constant__ BiasOut o) {
+__global__ void __launch_bounds__(kBiasThreads, kBiasGradCtas) bias_grad_kernel(const __grid_constant__ BiasGradArgs a, const __grid_constant__ BiasOut o) {
   pdl_enter();
   __shared__ float diagonals[kBiasWarps][kBiasRows + kBiasKeys];
   __shared__ float sums[kBiasWarps][kMaxBuckets];
@@ -182,107 +188,140 @@ __global__ void __launch_bounds__(kBiasThreads, VEC ? 2 : 3) bias_grad_kernel(co
   const int nb = unit < units ? static_cast<int>(max(static_cast<int64_t>(0), min(a.off[k + 1] - b0, static_cast<int64_t>(a.per_unit)))) : 0;
   if (nb > 0) {
     const int r = unit % (a.row_units * a.key_units);
-    const int64_t q0 = static_cast<int64_t>(r / a.key_units) * a.rows, k0 = static_cast<int64_t>(r % a.key_units) * kBiasKeys;
+    const int64_t q0 = static_cast<int64_t>(r / a.key_units) * a.rows, k0 = static_cast<int64_t>(r % a.key_units) * a.width;
     const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.queries - q0));
-    const int width = static_cast<int>(min(static_cast<int64_t>(kBiasKeys), a.keys - k0));
+    const int width = static_cast<int>(min(static_cast<int64_t>(a.width), a.keys - k0));
     const T* p = static_cast<const T*>(a.d) + b0 * a.stride_b + h * a.stride_h + q0 * a.stride_q + k0;
-    // rows of 256 keys, query by query, kGroup sequences at a time, two groups on their way
-    constexpr int kGroup = sizeof(T) == 2 && VEC ? 4 : 2;
-    struct Row {
-      uint32_t w[VEC ? sizeof(T) * 2 : 8];
-    };
+    // Rows of keys come in groups, two of them on their way: some sequences' of one query, or, where
+    // there are few sequences (FEW), of some queries.
+    constexpr int kGroup = sizeof(T) == 2 ? 4 : 2, kWords = sizeof(T) * 2;
     struct Group {
-      Row row[kGroup];
+      uint32_t row[kGroup][kWords];
+      int off[VEC ? 1 : kGroup];  // values of a row's first 16 bytes that are before its keys
     } ahead[2];
-    const int per_query = (nb + kGroup - 1) / kGroup, count = rows * per_query;
-    const bool whole = !VEC || lane * 8 + 8 <= width;
-    const T* pb = p + (VEC ? lane * 8 : lane);
-    p = pb;
-    int next_b = 0, next = 0;
-    auto fetch = [&](Group& g) {
-      if (next >= count) return;
+    const int mine_left = max(0, min(8, width - lane * 8));
+    uint32_t mask[kWords];  // of the lane's values that exist
 #pragma unroll
-      for (int s = 0; s < kGroup; ++s) {
-        Row& f = g.row[s];
-        const T* at = pb + s * a.stride_b;
-        const bool on = next_b + s < nb;
-        if constexpr (VEC) {
-          constexpr int kPieces = sizeof(T) / 2;  // of 16 bytes
-          if (whole) {
+    for (int i = 0; i < kWords; ++i) {
+      const int left = sizeof(T) == 4 ? mine_left - i : mine_left - 2 * i;
+      mask[i] = left <= 0 ? 0u : sizeof(T) == 2 && left == 1 ? 0xFFFFu : 0xFFFFFFFFu;
+    }
+    // Pieces of 16 bytes that hold a value of the row (and may hold others').
+    auto load = [&](Group& g, int s, const T* at, bool on) {
+      int off = 0;
+      if constexpr (!VEC) g.off[s] = off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15) / static_cast<int>(sizeof(T));
+      const uint4* from = reinterpret_cast<const uint4*>(at - off) + lane * (kWords / 4);
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-              const uint4 x = on ? __ldcs(reinterpret_cast<const uint4*>(at) + i) : make_uint4(0u, 0u, 0u, 0u);
-              f.w[4 * i] = x.x, f.w[4 * i + 1] = x.y, f.w[4 * i + 2] = x.z, f.w[4 * i + 3] = x.w;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t x = on && lane * 8 + e < width ? __float_as_uint(widen(at[e])) : 0u;
-              if constexpr (sizeof(T) == 4) f.w[e] = x;
-              else f.w[e >> 1] = e & 1 ? f.w[e >> 1] | x : x >> 16;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f.w[e] = on && lane + 32 * e < width ? __float_as_uint(widen(at[32 * e])) : 0u;
-        }
+      for (int i = 0; i < kWords / 4; ++i) {
+        const bool there = on && lane * 8 + i * (16 / static_cast<int>(sizeof(T))) - off < width;
+        const uint4 x = there ? __ldcs(from + i) : make_uint4(0u, 0u, 0u, 0u);
+        g.row[s][4 * i] = x.x, g.row[s][4 * i + 1] = x.y, g.row[s][4 * i + 2] = x.z, g.row[s][4 * i + 3] = x.w;
       }
-      ++next;
-      next_b += kGroup;
-      pb += kGroup * a.stride_b;
-      if (next_b >= nb) next_b = 0, pb = p += a.stride_q;
     };
     float acc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    int groups_left = per_query, done = 0;  // of this query; queries
-    // slot of the diagonal that key i of the window is on, at the last of the unit's queries
-    auto take = [&](const Group& g) {
-#pragma unroll
-      for (int s = 0; s < kGroup; ++s) {
-        const Row& f = g.row[s];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          F2 x;
-          if constexpr (!VEC || sizeof(T) == 4) x = f2(__uint_as_float(f.w[e]), __uint_as_float(f.w[e + 1]));
-          else x = f2(__uint_as_float(f.w[e >> 1] << 16), __uint_as_float(f.w[e >> 1] & 0xFFFF0000u));
-          const float2 y = parts(add2(f2(acc[e], acc[e + 1]), x));
-          acc[e] = y.x;
-          acc[e + 1] = y.y;
-        }
-      }
-      if (--groups_left > 0) return;
-      groups_left = per_query;
-      if (++done == rows) return;
+    auto add = [&](const Group& g, int s) {
+      uint32_t w[kWords];
       if constexpr (VEC) {
-        if (lane == 31) mine[kBiasKeys - 1 + rows - done] = acc[7];
-        const float in = __shfl_up_sync(0xFFFFFFFFu, acc[7], 1);
 #pragma unroll
-        for (int e = 7; e > 0; --e) acc[e] = acc[e - 1];
-        acc[0] = lane == 0 ? 0.f : in;
+        for (int i = 0; i < kWords; ++i) w[i] = g.row[s][i];
       } else {
-        if (lane == 31) mine[kBiasKeys - 1 + rows - done] = acc[7];
-        float in[8];
+        // the lane's words and the next lane's, moved over by `off` values (the same for the warp):
+        // by two words, by one, by half
+        constexpr int kMore = sizeof(T) == 4 ? 3 : 4;
+        const int off = g.off[s], words = sizeof(T) == 4 ? off : off >> 1;
+        uint32_t x[kWords + kMore];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) in[e] = __shfl_sync(0xFFFFFFFFu, acc[e], (lane + 31) & 31);
+        for (int i = 0; i < kWords; ++i) x[i] = g.row[s][i];
 #pragma unroll
-        for (int e = 7; e > 0; --e) acc[e] = lane == 0 ? in[e - 1] : in[e];
-        acc[0] = lane == 0 ? 0.f : in[0];
+        for (int i = 0; i < kMore; ++i) x[kWords + i] = __shfl_down_sync(0xFFFFFFFFu, x[i], 1);
+#pragma unroll
+        for (int i = 0; i < kWords + kMore - 2; ++i) x[i] = words & 2 ? x[i + 2] : x[i];
+#pragma unroll
+        for (int i = 0; i < kWords + kMore - 3; ++i) x[i] = words & 1 ? x[i + 1] : x[i];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = sizeof(T) == 4 ? x[i] : __funnelshift_r(x[i], x[i + 1], off & 1 ? 16 : 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] &= mask[i];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        F2 x;
+        if constexpr (sizeof(T) == 4) x = f2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+        else x = f2(__uint_as_float(w[e >> 1] << 16), __uint_as_float(w[e >> 1] & 0xFFFF0000u));
+        const float2 y = parts(add2(f2(acc[e], acc[e + 1]), x));
+        acc[e] = y.x;
+        acc[e + 1] = y.y;
       }
     };
-    fetch(ahead[0]);
-    fetch(ahead[1]);
-    for (int at = 0; at < count; at += 2) {
-      Group now = ahead[0];
-      fetch(ahead[0]);
-      take(now);
-      if (at + 1 >= count) break;
-      now = ahead[1];
-      fetch(ahead[1]);
-      take(now);
-    }
+    int done = 0;  // queries
+    // On to the next query: a slot is where a diagonal's key stands in the window at the last one.
+    auto next_query = [&] {
+      if (++done == rows) return;
+      if (lane == 31) mine[kBiasKeys - 1 + rows - done] = acc[7];
+      const float in = __shfl_up_sync(0xFFFFFFFFu, acc[7], 1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mine[VEC ? lane * 8 + e : lane + 32 * e] = acc[e];
+      for (int e = 7; e > 0; --e) acc[e] = acc[e - 1];
+      acc[0] = lane == 0 ? 0.f : in;
+    };
+    auto sweep = [&](auto few) {
+      constexpr bool FEW = decltype(few)::value;
+      const int per_query = (nb + kGroup - 1) / kGroup, all = rows * nb;
+      const int count = FEW ? (all + kGroup - 1) / kGroup : rows * per_query;
+      const T* at = p;
+      int ready = 0, row = 0, at_b = 0;  // groups fetched; the next row's (FEW), and sequence
+      auto fetch = [&](Group& g) {
+        if (ready >= count) return;
+        ++ready;
+#pragma unroll
+        for (int s = 0; s < kGroup; ++s) {
+          if constexpr (FEW) {
+            load(g, s, at, row < all);
+            ++row;
+            if (++at_b == nb) at_b = 0, at = p += a.stride_q;
+            else at += a.stride_b;
+          } else {
+            load(g, s, at + s * a.stride_b, at_b + s < nb);
+          }
+        }
+        if constexpr (!FEW) {
+          at_b += kGroup;
+          at += kGroup * a.stride_b;
+          if (at_b >= nb) at_b = 0, at = p += a.stride_q;
+        }
+      };
+      int b = 0, taken = 0;  // of the query's sequences (groups of them); rows (FEW)
+      auto take = [&](const Group& g) {
+#pragma unroll
+        for (int s = 0; s < kGroup; ++s) {
+          if (FEW && taken == all) break;
+          add(g, s);
+          if constexpr (FEW) {
+            ++taken;
+            if (++b == nb) b = 0, next_query();
+          }
+        }
+        if constexpr (!FEW) {
+          if (++b == per_query) b = 0, next_query();
+        }
+      };
+      fetch(ahead[0]);
+      fetch(ahead[1]);
+      for (int i = 0; i < count; i += 2) {
+        Group now = ahead[0];
+        fetch(ahead[0]);
+        take(now);
+        if (i + 1 >= count) break;
+        now = ahead[1];
+        fetch(ahead[1]);
+        take(now);
+      }
+    };
+    if (nb <= 2) sweep(std::true_type{});
+    else sweep(std::false_type{});
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine[lane * 8 + e] = acc[e];
     __syncwarp();
     // mine[i]: key k0 + i against the unit's last query
     const int64_t rel0 = k0 - (q0 + rows - 1) - a.offset;
@@ -440,20 +479,28 @@ int launch_bias(const BiasArgs& a, bool vec, dim3 grid, cudaStream_t stream) {
 
 // Units of one worker and head, and how they are dealt.
 struct GradPlan {
-  int rows, row_units, key_units, batch_units, per_unit, groups;
+  int rows, width, row_units, key_units, batch_units, per_unit, groups;
 };
-GradPlan plan_grad(const int64_t* offs, int K, int64_t heads, int64_t queries, int64_t keys) {
+GradPlan plan_grad(const int64_t* offs, int K, int64_t heads, int64_t queries, int64_t keys, bool vec) {
   GradPlan g = {};
   int64_t most = 1;
   for (int k = 0; k < K; ++k) most = std::max(most, offs[k + 1] - offs[k]);
-  // At most 16 sequences a unit, so that no running sum gets long.  Then queries: the fewer
-  // rows, the more warps share the work, down to 8 rows; enough is two CTAs an SM
-  // (64 x 16 x 512 x 512 bf16 of 16 workers: 99 us, with four 105, with six and 32 rows 140).
+  // At most 16 sequences a unit, so that no running sum gets long; keys in equal parts.  Then
+  // queries, 8 to 256: the number for which the waves of CTAs take least, a unit costing its
+  // groups of rows and about 24 groups' time for its diagonals' sums.
   g.per_unit = static_cast<int>(std::min<int64_t>(most, 16));
-  const int64_t batch_units = (most + g.per_unit - 1) / g.per_unit, key_units = (keys + kBiasKeys - 1) / kBiasKeys;
-  const int64_t enough = static_cast<int64_t>(2) * kBiasWarps * sm_count();
-  g.rows = kBiasRows;
-  while (g.rows > 8 && K * heads * batch_units * key_units * ((queries + g.rows - 1) / g.rows) < enough) g.rows /= 2;
+  const int64_t batch_units = (most + g.per_unit - 1) / g.per_unit, widest = vec ? kBiasKeys : kBiasKeys - 8,
+                key_units = (keys + widest - 1) / widest;  // (room for pieces that begin before the keys)
+  g.width = static_cast<int>(((keys + key_units - 1) / key_units + 7) / 8 * 8);
+  const double per_query = g.per_unit <= 2 ? g.per_unit / 4.0 : (g.per_unit + 3) / 4;
+  const int64_t slots = static_cast<int64_t>(kBiasGradCtas) * sm_count();
+  double least = 1e300;
+  for (int rows = kBiasRows; rows >= 8; rows /= 2) {
+    const int64_t units = (queries + rows - 1) / rows * key_units * batch_units;
+    const int64_t ctas = K * heads * ((units + kBiasWarps - 1) / kBiasWarps);
+    const double cost = static_cast<double>((ctas + slots - 1) / slots) * (static_cast<double>(std::min<int64_t>(rows, queries)) * per_query + 24.0);
+    if (cost < least) least = cost, g.rows = rows;
+  }
   g.row_units = static_cast<int>((queries + g.rows - 1) / g.rows);
   g.key_units = static_cast<int>(key_units);
   g.batch_units = static_cast<int>(std::min<int64_t>(batch_units, INT32_MAX));
@@ -528,8 +575,10 @@ int64_t adasum_relative_position_bias_backward_scratch_bytes(const int64_t* work
                                                              int64_t queries, int64_t keys, int buckets) {
   if (check_worker_offsets(worker_offsets, K) || buckets < 1 || buckets > kMaxBuckets) return 0;
   if (check_sizes(heads, worker_offsets[K], queries, keys, 0) || heads == 0 || worker_offsets[K] == 0 || queries == 0 || keys == 0) return 0;
-  const GradPlan g = plan_grad(worker_offsets, K, heads, queries, keys);
-  return g.groups <= 1 ? 0 : (static_cast<int64_t>(K) * heads * g.groups * buckets * 4 + 255) / 256 * 256;
+  // (whatever the rows' alignment turns out to be)
+  const int64_t groups = std::max(plan_grad(worker_offsets, K, heads, queries, keys, true).groups,
+                                  plan_grad(worker_offsets, K, heads, queries, keys, false).groups);
+  return groups <= 1 ? 0 : (static_cast<int64_t>(K) * heads * groups * buckets * 4 + 255) / 256 * 256;
 }
 
 adasum_status_t adasum_relative_position_bias_backward(const void* grad_scores, int64_t heads, int64_t queries, int64_t keys,
@@ -563,7 +612,9 @@ adasum_status_t adasum_relative_position_bias_backward(const void* grad_scores, 
   }
   if (adasum_status_t st = set.check()) return st;
   if (!some && accumulate) return ADASUM_OK;
-  const GradPlan g = plan_grad(worker_offsets, K, heads, some ? queries : 1, some ? keys : 1);
+  const bool vec = is_aligned(grad_scores, 16) && (queries <= 1 || stride_q * e % 16 == 0) && (heads == 1 || stride_h * e % 16 == 0) &&
+                   (batch <= 1 || stride_b * e % 16 == 0);
+  const GradPlan g = plan_grad(worker_offsets, K, heads, some ? queries : 1, some ? keys : 1, vec);
   if (g.groups < 0) return ADASUM_ERR_UNSUPPORTED;
   a.d = grad_scores;
   a.stride_b = stride_b;
@@ -574,6 +625,7 @@ adasum_status_t adasum_relative_position_bias_backward(const void* grad_scores, 
   a.keys = keys;
   a.offset = offset;
   a.rows = g.rows;
+  a.width = g.width;
   a.row_units = g.row_units;
   a.key_units = g.key_units;
   a.batch_units = some ? g.batch_units : 0;  // (no units: every sum is zero)
@@ -588,8 +640,6 @@ adasum_status_t adasum_relative_position_bias_backward(const void* grad_scores, 
   o.total = buckets;
   o.groups = a.groups;
   o.partials = a.partials;
-  const bool vec = is_aligned(grad_scores, 16) && (queries <= 1 || stride_q * e % 16 == 0) && (heads == 1 || stride_h * e % 16 == 0) &&
-                   (batch <= 1 || stride_b * e % 16 == 0);
   const dim3 grid(static_cast<unsigned>(a.groups), static_cast<unsigned>(heads), static_cast<unsigned>(K));
   adasum_status_t st = counted_launch(stream, "position_bias_grad", static_cast<double>(batch) * heads * queries * keys * e, [&] {
     if (dtype == ADASUM_BF16)
