@@ -12,13 +12,19 @@
 // the rounding errors of X that point into their directions: after five steps one rounding of
 // X to bf16 is 1e-2 to 1e-1 of the result's norm, to fp16 2e-3 to 2e-2 (random, power-law and
 // low-rank spectra).  So
-//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits), a product is three
-//     products of them (the fourth, of the low parts, is below 2^-22): off by 5e-7 to 5e-6,
-//     where fp32 throughout is off by 2e-6 to 2e-5;
-//   bf16 results: products of the high parts alone, but X itself in both parts for the term
-//     a X, where the growing errors would come from; the last two steps, whose errors no
-//     longer grow, take the rounded X there too, so that value and slope of the polynomial
-//     fit each other.  Off by 1.4e-3 at most, as much as the result's rounding to bf16.
+//   bf16 results: products of X, A and B as single fp16 numbers, but X itself as the sum of two
+//     for the term a X, where the growing errors would come from; the last two steps, whose
+//     errors no longer grow, take the rounded X there too, so that value and slope of the
+//     polynomial fit each other.  Off by 1.4e-3 at most, as much as the result's rounding to bf16.
+//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits), a product is three products
+//     of them (the fourth, of the low parts, is below 2^-22).  The diagonals of A and B, which
+//     dominate once the singular values are near 1, are kept apart in fp32:
+//         A A = E E + (d_i + d_j) E + d^2  with A = E + diag(d),   B X = F X + d_i X,
+//     the rest of which is added to the product in fp32.  For the tensor cores cut every partial sum
+//     off towards zero: 64 cut-offs along a depth of 1024 lose 1.4e-6 of a sum that grows
+//     evenly, which is made good by a factor (kCutOff), but up to twice that where one term
+//     outweighs the others.  Off by 5e-7 to 5e-6, fp32 throughout by 2e-6 to 2e-5.  (1024 x 4096 after
+//     five steps: 1.5e-5 without factor and diagonals apart, 1.2e-5 with the factor alone, 1.5e-6.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -305,12 +311,13 @@ struct FlowArgs {
   float coefficients[3 * ADASUM_NEWTON_SCHULZ_MAX_STEPS];
 };
 
+enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
+
 // Tiles are 128 * CTAS x NT: CTAS = 2 CTAs (a cluster) share one, each with 128 of its rows, and
 // each copies its rows of the left operand and its half of the columns of the right one.
-// TERMS = 3: products of sums of two parts.  Their accumulators: the high parts' product in runs
-// of kRun along the depth, each drained and added in fp32 registers, since the tensor cores cut
-// sums off towards zero (one run of 4096 left 1.4e-5 of 4 matrices of 1024 x 4096 after five
-// steps); beside it, for the whole depth, the two products with a low part.
+// TERMS = 3: products of sums of two parts.  Their sums come in runs along the depth, each drained
+// and added in fp32 registers; shorter ones for A = X X', which has squares on its diagonal.
+// (4096 x 4096 in one run: 9.5e-6 off after five steps.)
 template <int CTAS, int NT, int TERMS>
 struct FlowShape {
   static constexpr int kHeight = 128 * CTAS;
@@ -326,7 +333,8 @@ struct FlowShape {
   // waits for the one before it on the same sums.
   static constexpr int kSet = 256, kHigh = TERMS == 3 ? 128 : 256, kChains = kHigh / NT, kCols = 512;
   static_assert(NT <= kHigh, "a set holds a tile");
-  static constexpr int kRun = TERMS == 3 ? 8 : 1 << 30;  // stages of 64 along the depth
+  // stages of 64 along the depth in a run
+  __device__ static int run(int kind) { return TERMS == 1 ? 1 << 30 : kind == kGram ? 8 : 16; }
   static constexpr int kBlocks = NT / 64;  // of an epilogue warp
 };
 
@@ -343,20 +351,24 @@ __device__ __forceinline__ float cut_off(int stages) {
   return 1.f + kCutOff * (2.f / CHAINS * static_cast<float>(stages) + 0.5f);
 }
 
-enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
-
 struct Tile {
   int step, kind, group, matrix, row, col;  // row and column of the result where it starts
 };
 
-// All steps of the iteration in one launch of co-resident CTAs.  The tiles (128 x NT of one
+// All steps of the iteration in one launch of co-resident CTAs.  The tiles (128 CTAS x NT of one
 // product of one matrix) of all products lie in one sequence, product after product, and CTAs
 // take them in turn.  A tile needs its matrix's previous product whole, and nothing else: a
 // count per matrix of what has been written tells.  Every tile waits only for tiles before it
 // in the sequence, which CTAs take in order, so all waits end; and where there are several
-// matrices the products of one fill the SMs while another's last tiles finish.
-// A warp copies (TMA), a thread issues the products, eight warps take finished accumulators
-// out of TMEM.
+// matrices the products of one fill the SMs while another's last tiles finish.  (One launch a
+// product: 24 x (4096 x 1024) bf16 5.3 ms at the time against 2.8, one of 256 x 1024 137 us against 119.)
+// Two warps copy (TMA), a thread issues the products, the others take finished sums out of TMEM.
+// What bounds it: with many large matrices the traffic between L2 and the SMs, about 43 bytes a cycle
+// and SM: 24 x (1024 x 4096) bf16 1.62 ms, 1.1 without the results' reads and writes, at 1.7 PFLOP/s
+// then; fp32 4.2 ms, three times the products.  One matrix of 4096 x 4096 bf16 in 0.94 ms, 1.4 PFLOP/s
+// of the products that count.  Small matrices: the latency of 15 products in series, each about
+// 2.5 thousand cycles until the first operands are there, 2 to 13 thousand of products, 3 of
+// results and 2 until others may read them: one of 256 x 1024 in 93 us, fp32 133.
 template <int CTAS, int NT, int TERMS>
 __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(const __grid_constant__ FlowArgs a, const __grid_constant__ Places places) {
   using S = FlowShape<CTAS, NT, TERMS>;
@@ -501,7 +513,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
         const Tile t = locate(at);
         const int ks = depth(t);
         const bool mn = t.kind == kApply;
-        const int run = t.kind == kGram ? S::kRun : ks;
+        const int run = S::run(t.kind);
         const uint32_t idesc = mn ? umma_idesc(CTAS, NT, true) : umma_idesc(CTAS, NT, false);
         const uint32_t q_block = mn ? 8192 : 16, q_step = mn ? 128 : 2;
         int in_run = 0;
@@ -721,16 +733,17 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       };
       const int ks = depth(t);
       constexpr int kStep = E::kGroups * E::kCols;  // columns between a warp's blocks
-      if (TERMS == 3 && t.kind == kGram) {
+      if (TERMS == 3 && ks > S::run(t.kind)) {
         float v[S::kBlocks][E::kCols];
 #pragma unroll
         for (int k = 0; k < S::kBlocks; ++k)
 #pragma unroll
           for (int c = 0; c < E::kCols; ++c) v[k][c] = 0.f;
-        for (int run = 0; ok && run < ks; run += S::kRun, ++acc) {
+        const int length = S::run(t.kind);
+        for (int run = 0; ok && run < ks; run += length, ++acc) {
           if (!(ok = wait(&acc_full[acc & 1], (acc >> 1) & 1))) break;
           tc_fence_after();
-          const float gain = cut_off<S::kChains>(min(ks - run, S::kRun));
+          const float gain = cut_off<S::kChains>(min(ks - run, length));
           const uint32_t set = from + (acc & 1) * S::kSet;
 #pragma unroll
           for (int k = 0; k < S::kBlocks; ++k)
@@ -745,8 +758,10 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
         }
         if (!ok) break;
 #pragma unroll
-        for (int k = 0; k < S::kBlocks; ++k)
+        for (int k = 0; k < S::kBlocks; ++k) {
           if (there(k)) finish(k, v[k], next);
+          if (t.kind != kGram) fetch(k + 1, next);
+        }
       } else {
         if (!wait(&acc_full[acc & 1], (acc >> 1) & 1)) break;
         tc_fence_after();
