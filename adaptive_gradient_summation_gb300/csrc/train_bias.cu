@@ -51,12 +51,29 @@ struct BiasArgs {
   Buckets buckets;
 };
 
+// Value e of a piece of 16 bytes, and a piece of values rounded and stored.
+template <typename T>
+__device__ __forceinline__ float value_of(const uint4& x, int e) {
+  const uint32_t* w = &x.x;
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+  else return __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+}
+template <typename T, int E>
+__device__ __forceinline__ void put_piece(T* to, const float (&v)[E]) {
+  uint4 y;
+  if constexpr (sizeof(T) == 4)
+    y = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  else
+    y = make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[E - 4], v[E - 3]), pack2_bf16(v[E - 2], v[E - 1]));
+  __stcs(reinterpret_cast<uint4*>(to), y);
+}
+
 // E keys a lane: neighbours (16 bytes, VEC) or 32 apart.  A CTA has up to 32 rows of one head
 // and a warp's 32 E keys; the biases that occur there, one for each diagonal, go through shared
 // memory (a word of padding every 32, so that lanes 4 or 8 apart meet no bank twice) into the
 // registers of a warp's four rows, which serve all its sequences.  Bound by the bytes of the
-// scores: 64 x 16 x 512 x 512 bf16 in 188 us, 5.7 TB/s, fp32 337, 6.4 TB/s; 511 x 513 of them bf16, one
-// value a load and store, 376; the bias alone of 16 x 2048 x 2048 fp32 51, 5.3 TB/s.
+// scores: 64 x 16 x 512 x 512 bf16 in 180 us, 6.0 TB/s, fp32 337, 6.4 TB/s; 511 x 511 of them bf16 behind
+// a stride of 512, one value a load and store, 298; the bias alone of 16 x 2048 x 2048 fp32 51, 5.3 TB/s.
 template <typename T, int E, bool VEC, bool SCORES>
 __global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constant__ BiasArgs a) {
   pdl_enter();
@@ -96,22 +113,9 @@ __global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constan
       for (int r = 0; r < 4; ++r) {
         if (r >= left || k >= a.keys) continue;
         float v[E];
-        const uint32_t* w = &x[r].x;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float s = 0.f;
-          if constexpr (SCORES) {
-            if constexpr (sizeof(T) == 4) s = __uint_as_float(w[e]);
-            else s = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-          }
-          v[e] = SCORES ? s + bias[r][e] : bias[r][e];
-        }
-        uint4 y;
-        if constexpr (sizeof(T) == 4)
-          y = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-        else
-          y = make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[E - 4], v[E - 3]), pack2_bf16(v[E - 2], v[E - 1]));
-        __stcs(reinterpret_cast<uint4*>(to + r * a.keys), y);
+        for (int e = 0; e < E; ++e) v[e] = SCORES ? value_of<T>(x[r], e) + bias[r][e] : bias[r][e];
+        put_piece(to + r * a.keys, v);
       }
     } else {
 #pragma unroll
@@ -124,6 +128,73 @@ __global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constan
 #pragma unroll
         for (int e = 0; e < E; ++e)
           if (k + 32 * e < a.keys) to[r * a.keys + 32 * e] = narrow<T>(SCORES ? widen(x[e]) + bias[r][e] : bias[r][e]);
+      }
+    }
+  }
+}
+
+// Dense scores whose rows are no multiple of 16 bytes, or do not begin on one: the rows of a head
+// and sequence as one run of values, in the pieces of 16 bytes that hold them, E values each, four
+// a thread.  A piece may hold the end of a row and the next row's beginning, and the run's first
+// and last are shared with other heads.  The biases of all diagonals that a CTA's kFlatPieces
+// pieces meet are in shared memory, padded as above.  64 x 16 x 511 x 505 bf16 in 180 us, 5.9 TB/s,
+// 511 x 513 fp32 338, 6.4 TB/s (one value a load and store 293 and 549; rows one by one in pieces
+// shifted by each row's offset 236 and 412).
+constexpr int kFlatPieces = 4 * kBiasThreads, kFlatMaxKeys = 8192;
+// Rows after the first that the pieces of a CTA may reach into, and the diagonals then.
+__host__ __device__ __forceinline__ int flat_rows(int keys, int E) { return (keys - 1 + (kFlatPieces + 1) * E) / keys; }
+__host__ __device__ __forceinline__ int flat_diagonals(int keys, int E) { return keys + flat_rows(keys, E) + E; }
+template <typename T, int E, bool SCORES>
+__global__ void __launch_bounds__(kBiasThreads) bias_flat_kernel(const __grid_constant__ BiasArgs a) {
+  pdl_enter();
+  extern __shared__ float lut[];
+  const int keys = static_cast<int>(a.keys), rows = flat_rows(keys, E);
+  const int64_t size = a.queries * a.keys, h = blockIdx.y, first = static_cast<int64_t>(blockIdx.x) * (kFlatPieces * E);
+  const int64_t q0 = first / keys;
+  const int k0 = static_cast<int>(first - q0 * keys);
+  // lut[i]: of key i - rows against query q0
+  for (int i = threadIdx.x; i < flat_diagonals(keys, E); i += kBiasThreads)
+    lut[i + (i >> 5)] = load_any(a.table, a.table_dtype, bucket_of(a.buckets, i - rows - q0 - a.offset) * a.heads + h);
+  __syncthreads();
+  int key[4], row[4];  // of a piece's first value, were the run to begin on a piece
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = k0 + (threadIdx.x + j * kBiasThreads) * E;
+    row[j] = at / keys;
+    key[j] = at - row[j] * keys;
+  }
+  const int64_t b0 = blockIdx.z * a.per_cta, b1 = min(b0 + a.per_cta, a.batch);
+  for (int64_t b = b0; b < b1; ++b) {
+    T* const to = static_cast<T*>(a.out) + (b * a.heads + h) * size;
+    const T* const from = static_cast<const T*>(a.scores) + (b * a.heads + h) * size;
+    const int before = static_cast<int>(reinterpret_cast<uintptr_t>(to) / sizeof(T) % E);  // others' values in the first piece
+    uint4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t at = first + (threadIdx.x + j * kBiasThreads) * E - before;
+      if (SCORES && at < size) x[j] = __ldcs(reinterpret_cast<const uint4*>(from + at));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t at = first + (threadIdx.x + j * kBiasThreads) * E - before;
+      if (at >= size) break;
+      int k = key[j] - before, i = k - row[j] + rows;
+      while (k < 0) k += keys, i += keys + 1;  // (the key, in the row before)
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float add = lut[i + (i >> 5)];
+        v[e] = SCORES ? value_of<T>(x[j], e) + add : add;
+        const bool ends = ++k == keys;
+        i += ends ? -keys : 1;
+        if (ends) k = 0;
+      }
+      if (at >= 0 && at + E <= size) {
+        put_piece(to + at, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (at + e >= 0 && at + e < size) to[at + e] = narrow<T>(v[e]);
       }
     }
   }
@@ -472,8 +543,12 @@ int64_t span_of(int64_t batch, int64_t heads, int64_t queries, int64_t keys, int
 }
 
 template <typename T, bool SCORES>
-int launch_bias(const BiasArgs& a, bool vec, dim3 grid, cudaStream_t stream) {
+int launch_bias(const BiasArgs& a, bool vec, bool flat, dim3 grid, cudaStream_t stream) {
   constexpr int E = 16 / sizeof(T);
+  if (flat) {
+    const size_t smem = (flat_diagonals(static_cast<int>(a.keys), E) * 33 / 32 + 1) * sizeof(float);  // (below 35 KB)
+    return launch_pdl(bias_flat_kernel<T, E, SCORES>, grid, dim3(kBiasThreads), smem, stream, a);
+  }
   return launch_pdl(vec ? bias_kernel<T, E, true, SCORES> : bias_kernel<T, E, false, SCORES>, grid, dim3(kBiasThreads), 0, stream, a);
 }
 
@@ -552,8 +627,17 @@ adasum_status_t adasum_relative_position_bias(const void* table, int buckets, in
   a.stride_q = stride_q;
   a.out = out;
   a.row_groups = queries > 16 ? 8 : queries > 8 ? 4 : queries > 4 ? 2 : 1;
-  const int64_t width = 32 * (16 / e), tiles = (keys + width - 1) / width, rows = 4 * a.row_groups;
-  const int64_t x = tiles * ((queries + rows - 1) / rows), step = kBiasWarps / a.row_groups;
+  const bool vec = is_aligned(out, 16) && keys * e % 16 == 0 &&
+                   (scores == nullptr || (is_aligned(scores, 16) && (queries == 1 || stride_q * e % 16 == 0) &&
+                                          (heads == 1 || stride_h * e % 16 == 0) && (batch == 1 || stride_b * e % 16 == 0)));
+  // (the biases of a row's diagonals have to serve enough values: bf16, 16 heads of 2047 x 2047 97 us
+  // either way, four sequences of them 196 and 269; one of 4 x 4095 x 8191 450 and 181)
+  const bool flat = !vec && keys <= std::min<int64_t>(kFlatMaxKeys, 2048 * batch) &&
+                    (scores == nullptr || (dense && (reinterpret_cast<uintptr_t>(scores) - reinterpret_cast<uintptr_t>(out)) % 16 == 0));
+  const int64_t piece = 16 / e, width = 32 * piece, tiles = (keys + width - 1) / width, rows = 4 * a.row_groups;
+  const int64_t x = flat ? (queries * keys + piece - 1 + kFlatPieces * piece - 1) / (kFlatPieces * piece)
+                         : tiles * ((queries + rows - 1) / rows);
+  const int64_t step = flat ? 1 : kBiasWarps / a.row_groups;
   if (x > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
   // sequences of a CTA: as many as leave eight CTAs an SM, so that the biases serve many of them
   int64_t parts = std::max<int64_t>(1, std::min<int64_t>((batch + step - 1) / step, static_cast<int64_t>(8) * sm_count() / (x * heads)));
@@ -561,13 +645,10 @@ adasum_status_t adasum_relative_position_bias(const void* table, int buckets, in
   a.per_cta = (batch + parts - 1) / parts;
   parts = (batch + a.per_cta - 1) / a.per_cta;
   if (parts > 65535) return ADASUM_ERR_UNSUPPORTED;
-  const bool vec = is_aligned(out, 16) && keys * e % 16 == 0 &&
-                   (scores == nullptr || (is_aligned(scores, 16) && (queries == 1 || stride_q * e % 16 == 0) &&
-                                          (heads == 1 || stride_h * e % 16 == 0) && (batch == 1 || stride_b * e % 16 == 0)));
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(heads), static_cast<unsigned>(parts));
   return counted_launch(stream, scores ? "position_bias_add" : "position_bias", static_cast<double>(batch) * n * e * (scores ? 2 : 1), [&] {
-    if (dtype == ADASUM_BF16) return scores ? launch_bias<bf16, true>(a, vec, grid, stream) : launch_bias<bf16, false>(a, vec, grid, stream);
-    return scores ? launch_bias<float, true>(a, vec, grid, stream) : launch_bias<float, false>(a, vec, grid, stream);
+    if (dtype == ADASUM_BF16) return scores ? launch_bias<bf16, true>(a, vec, flat, grid, stream) : launch_bias<bf16, false>(a, vec, flat, grid, stream);
+    return scores ? launch_bias<float, true>(a, vec, flat, grid, stream) : launch_bias<float, false>(a, vec, flat, grid, stream);
   });
 }
 

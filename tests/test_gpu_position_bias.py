@@ -261,3 +261,34 @@ def test_refusals(native):
         ags.relative_position_bias(table, 4, 8, scores=buf[1:].view(2, 3, 4, 8), out=buf[:-1].view(2, 3, 4, 8))
     with pytest.raises(ags.AdasumError):
         ags.relative_position_bias_backward(x, 16, grads=[x.view(-1)[:48]])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,heads,queries,keys", [(2, 3, 37, 1), (2, 3, 37, 5), (1, 2, 5, 127), (2, 2, 33, 255), (2, 1, 40, 257),
+                                                      (70, 1, 3, 263), (1, 2, 34, 511), (3, 1, 9, 514),
+                                                      (2, 1, 9000, 1), (2, 2, 3, 8191), (1, 2, 2, 8195)])
+def test_rows_that_begin_anywhere(native, batch, heads, queries, keys, dtype):
+    """Dense scores whose rows are no multiple of 16 bytes, at every offset from a 16-byte
+    boundary, the output at the same one or another, and in place; nothing beside it is written."""
+    table = randn(32, heads, seed=1)
+    size = batch * heads * queries * keys
+    x = randn(batch, heads, queries, keys, seed=2, dtype=dtype, std=3.0)
+    index = more.bucket_matrix(queries, keys, 7, 32, True, 128, DEV)
+    want = x.to(F8) + table.to(F8)[index].permute(2, 0, 1)
+    tol = (u + HALF[dtype]) * want.abs() + TINY
+    for at in range(16 // dtype.itemsize):
+        source = torch.full((size + 32,), math.nan, dtype=dtype, device=DEV)
+        scores = source[at:at + size].view_as(x).copy_(x)
+        for to in (at, at + 16, at + 3):
+            room = torch.full((size + 64,), 77.0, dtype=dtype, device=DEV)
+            got = ags.relative_position_bias(table, queries, keys, offset=7, scores=scores, out=room[to:to + size].view_as(x))
+            close(got, want, tol, f"{at} to {to}")
+            assert (room[:to] == 77).all() and (room[to + size:] == 77).all()
+        assert ags.relative_position_bias(table, queries, keys, offset=7, scores=scores, out=scores) is scores
+        close(scores, want, tol, f"{at} in place")
+        assert torch.isnan(source[:at]).all() and torch.isnan(source[at + size:]).all()
+    alone = torch.full((heads * queries * keys + 16,), 77.0, device=DEV)
+    for at in range(4):
+        got = ags.relative_position_bias(table, queries, keys, offset=7, out=alone[at:at + heads * queries * keys].view(heads, queries, keys))
+        assert torch.equal(got, table[index].permute(2, 0, 1))
+        assert (alone[at + heads * queries * keys:] == 77).all()
