@@ -303,8 +303,9 @@ ADASUM_API adasum_status_t adasum_pair_noalloc(const void *a, const void *b, int
 /* ---- Operators of the training step around the combine ---------------------------- */
 
 /*
- * The operators below are the memory-bound ends of a training step: token embeddings,
- * layer norm, and activations kept in 8 bits between the forward and the backward pass.
+ * The operators below are the memory-bound parts of a training step: token embeddings,
+ * layer and root-mean-square norm, the position bias of attention scores, and activations
+ * kept in 8 bits between the forward and the backward pass.
  * Their parameter gradients are written per worker, into the flat gradient buffers that
  * adasum_reduce takes: the rows of one call are the microbatches of K workers one after
  * the other, worker k's being rows [worker_offsets[k], worker_offsets[k+1]), and
