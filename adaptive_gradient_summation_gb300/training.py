@@ -518,13 +518,14 @@ def rms_norm_checkpointed_backward(grad_output: torch.Tensor, checkpoint: Checkp
 
 def _scores(t: torch.Tensor, what: str):
     """The shape (batch, heads, queries, keys) of a tensor, and its first three strides."""
-    if t.dim() != 4:
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 4:
         raise ValueError(f"{what} must have shape (batch, heads, queries, keys)")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if shape[3] > 1 and strides[3] != 1:
         raise ValueError(f"{what} must have its keys next to each other")
-    if t.numel() and any(size > 1 and stride < 1 for size, stride in zip(t.shape, t.stride())):
+    if 0 in strides and t.numel() and any(size > 1 and stride < 1 for size, stride in zip(shape, strides)):
         raise ValueError(f"{what} must not repeat elements")
-    return t.shape, t.stride()[:3]
+    return shape, strides[:3]
 
 
 def relative_position_bias(table: torch.Tensor, queries: int, keys: int, *, bidirectional: bool = True, max_distance: int = 128,

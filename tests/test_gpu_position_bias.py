@@ -292,3 +292,17 @@ def test_rows_that_begin_anywhere(native, batch, heads, queries, keys, dtype):
         got = ags.relative_position_bias(table, queries, keys, offset=7, out=alone[at:at + heads * queries * keys].view(heads, queries, keys))
         assert torch.equal(got, table[index].permute(2, 0, 1))
         assert (alone[at + heads * queries * keys:] == 77).all()
+
+
+@pytest.mark.parametrize("buckets,both,distance", [(32, False, 4096), (24, True, 1000), (64, True, 65536), (48, False, 10 ** 6), (256, False, 2 ** 31 - 1)])
+def test_borders_of_wide_rules(native, buckets, both, distance):
+    """Positions next to where each bucket begins, found by bisection in whole numbers."""
+    table = torch.arange(buckets, dtype=FP32, device=DEV)[:, None].contiguous()
+    n = buckets // 2 if both else buckets
+    for j in range(n // 2, n, max(1, n // 24)):
+        lo, hi = 0, distance
+        while lo < hi:
+            at = (lo + hi) // 2
+            lo, hi = (lo, at) if more.bucket(-at, n, False, distance) >= j else (at + 1, hi)
+        got = ags.relative_position_bias(table, 1, 5, offset=lo + 2, bidirectional=both, max_distance=distance)[0, 0]
+        assert got.int().tolist() == [more.bucket(k - lo - 2, buckets, both, distance) for k in range(5)]
