@@ -1419,7 +1419,7 @@ adasum_status_t adasum_get_last_error(void) {
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return ADASUM_ERR_CUDA;
   Workspace& ws = workspace_for(device);
-  int h = take_update_error();
+  int h = take_update_error(device);
   if (h < 0) return ADASUM_ERR_CUDA;
   if (ws.d_error != nullptr) {
     int w = 0;

@@ -22,9 +22,9 @@ cudaEvent_t profile_start(cudaStream_t stream);
 adasum_status_t profile_launched(int rc, const char* name, cudaEvent_t start, cudaStream_t stream,
                                  double bytes);
 
-// The status word of the current device that the update kernels' waits set (train_muon.cu), 0
-// or more, cleared; -1: a CUDA error.
-int take_update_error();
+// The status word of the current device, `device`, that the update kernels' waits set
+// (train_muon.cu), 0 or more, cleared; -1: a CUDA error.  No CUDA call where none was launched.
+int take_update_error(int device);
 
 // One launch, counted and (when profiling) timed; `f` returns the launch's cudaError_t as
 // int.  `bytes`: its algorithmic bytes.

@@ -28,6 +28,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <vector>
 
@@ -45,6 +46,10 @@ constexpr float kScaleX = 8192.f, kScaleA = 8192.f, kScaleB = 4096.f;
 
 // What a wait that ran out leaves (adasum_get_last_error).
 __device__ int g_error;
+// Devices on which the iteration has been launched or captured, so that g_error may be set (of
+// those beyond the last: any of them).
+std::atomic<bool> g_launched[65];
+int launched_index(int device) { return device >= 0 && device < 64 ? device : 64; }
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
 
 // ------------------------------------------------------------------ momentum and norms
@@ -1068,6 +1073,9 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
     scratch += l.bytes;
   }
   const TileSize size = tile_size(pieces, count, fine);
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return ADASUM_ERR_CUDA;
+  g_launched[launched_index(device)].store(true, std::memory_order_relaxed);
   return counted_launch(stream, fine ? "update_iterate3" : "update_iterate", 0.0, [&] {
     return fine ? launch_flow<3>(f, places, size, stream) : launch_flow<1>(f, places, size, stream);
   });
@@ -1107,7 +1115,8 @@ bool fits(int64_t rows, int64_t cols) { return rows <= ADASUM_NEWTON_SCHULZ_MAX_
 
 }  // namespace
 
-int take_update_error() {
+int take_update_error(int device) {
+  if (!g_launched[launched_index(device)].load(std::memory_order_relaxed)) return 0;
   int h = 0;
   const int zero = 0;
   if (cudaMemcpyFromSymbol(&h, g_error, sizeof h) != cudaSuccess) return -1;
