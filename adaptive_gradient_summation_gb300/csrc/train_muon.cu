@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kMaxBatch = 256;                    // matrices of one launch
 constexpr int64_t kChunkBytes = int64_t(1) << 30;  // scratch of a chunk of equal matrices, about
+// X and A are kept times these, B times kScaleB or less (scale_b).
 constexpr float kScaleX = 8192.f, kScaleA = 8192.f, kScaleB = 4096.f;
 
 // What a wait that ran out leaves (adasum_get_last_error).
@@ -311,7 +312,7 @@ struct Epilogue {
 struct FlowGroup {
   CUtensorMap x_tall[2][2], x_square[2][2], a_tall[2], a_square[2], b_tall[2];  // [buffer][part], [part]
   __half *x[2][2], *a[2], *b[2];
-  float *da, *db;              // A's and B's diagonals, times kScaleA and kScaleB
+  float *da, *db;              // A's and B's diagonals, times kScaleA and the step's scale_b
   int64_t ldx, lda;
   int m, n, batch, first;      // the first matrix' place among all
   int col_tiles[2], tiles[2];  // of A and B (lower triangle), of X
@@ -328,6 +329,7 @@ struct FlowArgs {
   int dest_dtype, dest_vec;     // on a 16-byte boundary
   float keep;
   float coefficients[3 * ADASUM_NEWTON_SCHULZ_MAX_STEPS];
+  float scale_b[ADASUM_NEWTON_SCHULZ_MAX_STEPS];
 };
 
 enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
@@ -583,9 +585,10 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       const int in_parts = TERMS == 3 || (apply && t.step + 2 < a.steps) ? 2 : 1;
       const int out_parts = TERMS == 3 || (apply && t.step + 3 < a.steps) ? 2 : 1;
       const float c_a = a.coefficients[3 * t.step], c_b = a.coefficients[3 * t.step + 1], c_c = a.coefficients[3 * t.step + 2];
+      const float scale_b = a.scale_b[t.step];
       const float scale = t.kind == kGram   ? kScaleA / (kScaleX * kScaleX)
-                          : t.kind == kPoly ? c_c * (kScaleB / (kScaleA * kScaleA))
-                                            : 1.f / kScaleB;
+                          : t.kind == kPoly ? c_c * (scale_b / (kScaleA * kScaleA))
+                                            : 1.f / scale_b;
       const bool even = (t.step & 1) == 0;
       const __half *in0 = apply ? (even ? g.x[0][0] : g.x[1][0]) : g.a[0], *in1 = apply ? (even ? g.x[0][1] : g.x[1][1]) : g.a[1];
       __half *out0 = apply ? (even ? g.x[1][0] : g.x[0][0]) : t.kind == kGram ? g.a[0] : g.b[0];
@@ -741,8 +744,8 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       for (int r = 0; r < E::kPasses; ++r) {
         const int i = i0 + r * E::kRows + sub;
         on_diagonal[r] = kDiagonals && t.kind == kPoly && i < g.m ? __ldcg(diagonal_a + i) : 0.f;
-        of_row[r] = apply ? c_a + (kDiagonals && i < g.m ? __ldcg(g.db + static_cast<int64_t>(t.matrix) * g.lda + i) : 0.f) * (1.f / kScaleB)
-                          : __fmaf_rn(scale, on_diagonal[r], c_b * (kScaleB / kScaleA));
+        of_row[r] = apply ? c_a + (kDiagonals && i < g.m ? __ldcg(g.db + static_cast<int64_t>(t.matrix) * g.lda + i) : 0.f) * scale
+                          : __fmaf_rn(scale, on_diagonal[r], c_b * (scale_b / kScaleA));
       }
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * E::kCols;
       auto release = [&](uint64_t* bar) {
@@ -1002,6 +1005,36 @@ int launch_flow(FlowArgs& a, const Places& places, TileSize s, cudaStream_t stre
   return launch_flow_as<1, 64, TERMS>(a, places, stream);
 }
 
+// The power of two that B = b A + c A A is kept times in every step: B's elements are at most its
+// largest singular value, |b t + c t^2| with t = s^2 for one of X's, s, and have to stay below
+// fp16's 65504.  The singular values are 1 at most at first, then what the steps so far can have
+// made of those, and below 2.8 (the caller's part).  With the usual coefficients |b t + c t^2| is
+// 2.8 at most, and the scale kScaleB.
+void scale_b(const float* coefficients, int steps, float* scale) {
+  double most = 1.01;  // singular value (roundings added)
+  for (int k = 0; k < steps; ++k) {
+    const double a = coefficients[3 * k], b = coefficients[3 * k + 1], c = coefficients[3 * k + 2], end = most * most;
+    double of_b = 0.0, of_x = 0.0;
+    auto at = [&](double t) {  // an end or an extreme value inside
+      if (!(t >= 0.0 && t <= end)) return;
+      of_b = std::max(of_b, std::fabs(t * (b + c * t)));
+      of_x = std::max(of_x, std::sqrt(t) * std::fabs(a + t * (b + c * t)));
+    };
+    at(end);
+    if (c != 0.0) {
+      at(-b / (2.0 * c));
+      const double root = std::sqrt(9.0 * b * b - 20.0 * a * c);  // (NaN: no extreme value)
+      at((-3.0 * b + root) / (10.0 * c));
+      at((-3.0 * b - root) / (10.0 * c));
+    } else if (b != 0.0) {
+      at(-a / (3.0 * b));
+    }
+    scale[k] = kScaleB;
+    while (of_b * scale[k] > 65000.0) scale[k] *= 0.5f;
+    most = std::min(1.01 * of_x, 2.8);
+  }
+}
+
 // Iterates the pieces' matrices, which are at `from`, all in one launch; the results go to `places`.
 adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places, const Piece* pieces, int count, bool fine,
                         const Iteration& it, const Result& res, char* scratch, cudaStream_t stream) {
@@ -1014,6 +1047,7 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
   f.dest_vec = is_aligned(res.dest, 16);
   f.keep = res.keep;
   std::copy(it.coefficients, it.coefficients + 3 * it.steps, f.coefficients);
+  scale_b(it.coefficients, it.steps, f.scale_b);
   src.eps = it.eps;
   src.vec = is_aligned(src.x, 16) && is_aligned(src.momentum, 16);
   int first = 0;
