@@ -8,7 +8,7 @@ Two variants are built from the same sources:
   libadasum_gb300.so       the product: reads no environment variable
   libadasum_gb300_test.so  the test build (-DADASUM_TEST_HOOKS -DADASUM_BOUNDS_CHECK):
                            device-side index checks on every tile, chunk and segment
-                           descriptor (a failure sets a status bit, adasum_get_last_error
+                           descriptor, and on the position bias' 16-byte reads (a failure sets a status bit, adasum_get_last_error
                            reports ADASUM_ERR_BOUNDS; nothing traps), and it also honours the
                            switches the tests use to force a route, switch a kernel off
                            or inject a fault on the host (ADASUM_ONCHIP, ADASUM_TINY,

@@ -1420,7 +1420,9 @@ adasum_status_t adasum_get_last_error(void) {
   if (cudaGetDevice(&device) != cudaSuccess) return ADASUM_ERR_CUDA;
   Workspace& ws = workspace_for(device);
   int h = take_update_error(device);
-  if (h < 0) return ADASUM_ERR_CUDA;
+  const int b = take_bias_error();
+  if (h < 0 || b < 0) return ADASUM_ERR_CUDA;
+  h |= b;
   if (ws.d_error != nullptr) {
     int w = 0;
     if (cudaMemcpy(&w, ws.d_error, sizeof w, cudaMemcpyDeviceToHost) != cudaSuccess ||

@@ -25,6 +25,8 @@ adasum_status_t profile_launched(int rc, const char* name, cudaEvent_t start, cu
 // The status word of the current device, `device`, that the update kernels' waits set
 // (train_muon.cu), 0 or more, cleared; -1: a CUDA error.  No CUDA call where none was launched.
 int take_update_error(int device);
+// The same of the position bias' index checks (train_bias.cu); 0 in the product.
+int take_bias_error();
 
 // One launch, counted and (when profiling) timed; `f` returns the launch's cudaError_t as
 // int.  `bytes`: its algorithmic bytes.

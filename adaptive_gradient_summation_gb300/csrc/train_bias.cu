@@ -19,6 +19,10 @@ namespace {
 constexpr int kMaxBuckets = ADASUM_BIAS_MAX_BUCKETS;
 constexpr int kBiasThreads = 256, kBiasWarps = 8;
 
+#ifdef ADASUM_BOUNDS_CHECK
+__device__ int g_status;  // what an index check leaves (adasum_get_last_error)
+#endif
+
 // Buckets of one direction: distance d belongs to the last j with border[j] <= d.
 struct Buckets {
   int n;               // of one direction
@@ -67,6 +71,27 @@ __device__ __forceinline__ void put_piece(T* to, const float (&v)[E]) {
   else
     y = make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[E - 4], v[E - 3]), pack2_bf16(v[E - 2], v[E - 1]));
   __stcs(reinterpret_cast<uint4*>(to), y);
+}
+
+// A piece of 16 bytes, all of them values of [first, last).
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const uint4* p, const T* first, const T* last) {
+  const bool inside = ADASUM_CHECK(&g_status, reinterpret_cast<const T*>(p) >= first && reinterpret_cast<const T*>(p + 1) <= last);
+  return inside ? __ldcs(p) : make_uint4(0u, 0u, 0u, 0u);
+}
+// A piece of which only some values may be of [first, last): the others are not read, and come as
+// zeros.
+template <typename T>
+__device__ __forceinline__ uint4 load_edge(const uint4* p, const T* first, const T* last) {
+  constexpr int E = 16 / sizeof(T);
+  using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+  const T* at = reinterpret_cast<const T*>(p);
+  uint32_t v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e)  // (all on their way before one is used)
+    v[e] = at + e >= first && at + e < last ? reinterpret_cast<const Bits*>(at)[e] : 0u;
+  if constexpr (sizeof(T) == 4) return make_uint4(v[0], v[1], v[2], v[3]);
+  else return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[E - 4] | v[E - 3] << 16, v[E - 2] | v[E - 1] << 16);
 }
 
 // E keys a lane: neighbours (16 bytes, VEC) or 32 apart.  A CTA has up to 32 rows of one head
@@ -142,11 +167,12 @@ __global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constan
 // 511 x 513 fp32 338, 6.4 TB/s (one value a load and store 293 and 549; rows one by one in pieces
 // shifted by each row's offset 236 and 412).
 constexpr int kFlatPieces = 4 * kBiasThreads, kFlatMaxKeys = 8192;
+constexpr int kFlatCtas = 5;  // of an SM, at the least
 // Rows after the first that the pieces of a CTA may reach into, and the diagonals then.
 __host__ __device__ __forceinline__ int flat_rows(int keys, int E) { return (keys - 1 + (kFlatPieces + 1) * E) / keys; }
 __host__ __device__ __forceinline__ int flat_diagonals(int keys, int E) { return keys + flat_rows(keys, E) + E; }
 template <typename T, int E, bool SCORES>
-__global__ void __launch_bounds__(kBiasThreads) bias_flat_kernel(const __grid_constant__ BiasArgs a) {
+__global__ void __launch_bounds__(kBiasThreads, kFlatCtas) bias_flat_kernel(const __grid_constant__ BiasArgs a) {
   pdl_enter();
   extern __shared__ float lut[];
   const int keys = static_cast<int>(a.keys), rows = flat_rows(keys, E);
@@ -165,39 +191,56 @@ __global__ void __launch_bounds__(kBiasThreads) bias_flat_kernel(const __grid_co
     key[j] = at - row[j] * keys;
   }
   const int64_t b0 = blockIdx.z * a.per_cta, b1 = min(b0 + a.per_cta, a.batch);
-  for (int64_t b = b0; b < b1; ++b) {
-    T* const to = static_cast<T*>(a.out) + (b * a.heads + h) * size;
-    const T* const from = static_cast<const T*>(a.scores) + (b * a.heads + h) * size;
-    const int before = static_cast<int>(reinterpret_cast<uintptr_t>(to) / sizeof(T) % E);  // others' values in the first piece
-    uint4 x[4];
+  auto sweep = [&](auto edge) {  // (inside the run all pieces are whole)
+    constexpr bool EDGE = decltype(edge)::value;
+    for (int64_t b = b0; b < b1; ++b) {
+      T* const to = static_cast<T*>(a.out) + (b * a.heads + h) * size;
+      const T* const from = static_cast<const T*>(a.scores) + (b * a.heads + h) * size;
+      const int before = static_cast<int>(reinterpret_cast<uintptr_t>(to) / sizeof(T) % E);  // others' values in the first piece
+      uint4 x[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t at = first + (threadIdx.x + j * kBiasThreads) * E - before;
-      if (SCORES && at < size) x[j] = __ldcs(reinterpret_cast<const uint4*>(from + at));
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t at = first + (threadIdx.x + j * kBiasThreads) * E - before;
-      if (at >= size) break;
-      int k = key[j] - before, i = k - row[j] + rows;
-      while (k < 0) k += keys, i += keys + 1;  // (the key, in the row before)
-      float v[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float add = lut[i + (i >> 5)];
-        v[e] = SCORES ? value_of<T>(x[j], e) + add : add;
-        const bool ends = ++k == keys;
-        i += ends ? -keys : 1;
-        if (ends) k = 0;
+      for (int j = 0; j < 4; ++j) {
+        const int64_t at = first + (threadIdx.x + j * kBiasThreads) * E - before;
+        uint32_t whole = !EDGE || (at >= 0 && at + E <= size);
+        if (EDGE) asm("" : "+r"(whole));  // (seen to be the store's condition, each load would wait for the one before: 13% more)
+        if (SCORES && whole) x[j] = load_piece(reinterpret_cast<const uint4*>(from + at), from, from + size);
       }
-      if (at >= 0 && at + E <= size) {
-        put_piece(to + at, v);
-      } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (at + e >= 0 && at + e < size) to[at + e] = narrow<T>(v[e]);
+      for (int j = 0; j < 4; ++j) {
+        const int64_t at = first + (threadIdx.x + j * kBiasThreads) * E - before;
+        if (EDGE && at >= size) break;
+        int k = key[j] - before, i = k - row[j] + rows;
+        while (k < 0) k += keys, i += keys + 1;  // (the key, in the row before)
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float add = lut[i + (i >> 5)];
+          v[e] = SCORES ? value_of<T>(x[j], e) + add : add;
+          const bool ends = ++k == keys;
+          i += ends ? -keys : 1;
+          if (ends) k = 0;
+        }
+        if (!EDGE || (at >= 0 && at + E <= size)) put_piece(to + at, v);
       }
     }
+  };
+  if (blockIdx.x > 0 && first + (kFlatPieces + 1) * E <= size) return sweep(std::false_type{});
+  sweep(std::true_type{});
+  // The run's first and last piece of every sequence, where others' values are in them, value by
+  // value: those are not the caller's to have read, or another CTA's to write.
+  for (int64_t item = threadIdx.x; item < (b1 - b0) * 2 * E; item += kBiasThreads) {
+    const int64_t at_b = ((b0 + item / (2 * E)) * a.heads + h) * size;
+    T* const to = static_cast<T*>(a.out) + at_b;
+    const int before = static_cast<int>(reinterpret_cast<uintptr_t>(to) / sizeof(T) % E), e = static_cast<int>(item % E);
+    const int64_t last = (size - 1 + before) / E, piece = item / E % 2 ? last : 0;
+    const int64_t start = piece * E - before, at = start + e;
+    const bool whole = start >= 0 && start + E <= size;
+    if (whole || piece / kFlatPieces != blockIdx.x || (item / E % 2 && last == 0) || at < 0 || at >= size) continue;
+    const int from_k0 = k0 + static_cast<int>(at - first);  // (negative: in the row before)
+    const int r = from_k0 < 0 ? -((keys - 1 - from_k0) / keys) : from_k0 / keys;
+    const int i = from_k0 - r * keys - r + rows;
+    const float add = lut[i + (i >> 5)];
+    to[at] = narrow<T>(SCORES ? widen(static_cast<const T*>(a.scores)[at_b + at]) + add : add);
   }
 }
 
@@ -208,7 +251,7 @@ constexpr int kBiasKeys = 256;  // of a warp at most, eight a lane
 constexpr int kBiasGradCtas = 2;  // of an SM (3 with half as many rows on their way: 140 us against 99)
 
 struct BiasGradArgs {
-  const void* d;
+  const void *d, *end;  // its first value, and past its last
   int64_t stride_b, stride_h, stride_q;
   int64_t heads, queries, keys, offset;
   int rows, width;     // queries and keys of a unit
@@ -243,8 +286,11 @@ __device__ __forceinline__ void put_bucket(const BiasOut& o, int k, int64_t h, i
 // of them bf16 in 161 (loaded value by value, 32 keys apart a lane: 763); one sequence each of 4
 // workers of 16 x 2048 x 2048 in 112 us, 4.8 TB/s.
 // VEC: all rows of keys begin on 16-byte boundaries; else the pieces of 16 bytes that hold them do,
-// and the values move over by less than a lane.
-template <typename T, bool VEC>
+// and the values move over by less than a lane.  Pieces may hold values beside the unit's, which
+// are masked.  EDGE: some pieces reach beyond the first or last value of all, whose rows are looked
+// for in the units that have any (512 x 513 of them behind a stride of 520 bf16 121 us a pass, 113 without the
+// checks; 511 x 513 dense the same; a kernel of its own, since aligned ones of 2048 x 2048 took 115 in it, not 109).
+template <typename T, bool VEC, bool EDGE>
 __global__ void __launch_bounds__(kBiasThreads, kBiasGradCtas) bias_grad_kernel(const __grid_constant__ BiasGradArgs a, const __grid_constant__ BiasOut o) {
   pdl_enter();
   __shared__ float diagonals[kBiasWarps][kBiasRows + kBiasKeys];
@@ -278,6 +324,10 @@ __global__ void __launch_bounds__(kBiasThreads, kBiasGradCtas) bias_grad_kernel(
       const int left = sizeof(T) == 4 ? mine_left - i : mine_left - 2 * i;
       mask[i] = left <= 0 ? 0u : sizeof(T) == 2 && left == 1 ? 0xFFFFu : 0xFFFFFFFFu;
     }
+    const T *const begin = static_cast<const T*>(a.d), *const end = static_cast<const T*>(a.end);
+    // where all pieces of a row are whole
+    const T* const whole_from = reinterpret_cast<const T*>((reinterpret_cast<uintptr_t>(begin) + 15) & ~uintptr_t(15));
+    const T* const whole_to = reinterpret_cast<const T*>(reinterpret_cast<uintptr_t>(end) & ~uintptr_t(15));
     // Pieces of 16 bytes that hold a value of the row (and may hold others').
     auto load = [&](Group& g, int s, const T* at, bool on) {
       int off = 0;
@@ -286,7 +336,20 @@ __global__ void __launch_bounds__(kBiasThreads, kBiasGradCtas) bias_grad_kernel(
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
         const bool there = on && lane * 8 + i * (16 / static_cast<int>(sizeof(T))) - off < width;
-        const uint4 x = there ? __ldcs(from + i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = there ? load_piece(from + i, begin, end) : make_uint4(0u, 0u, 0u, 0u);
+        g.row[s][4 * i] = x.x, g.row[s][4 * i + 1] = x.y, g.row[s][4 * i + 2] = x.z, g.row[s][4 * i + 3] = x.w;
+      }
+    };
+    // The same of a row that may reach into the first or last piece of all.
+    auto load_beyond = [&](Group& g, int s, const T* at, bool on) {
+      if (at >= whole_from && at + width <= whole_to) return load(g, s, at, on);
+      int off = 0;
+      if constexpr (!VEC) g.off[s] = off = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15) / static_cast<int>(sizeof(T));
+      const uint4* from = reinterpret_cast<const uint4*>(at - off) + lane * (kWords / 4);
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const bool there = on && lane * 8 + i * (16 / static_cast<int>(sizeof(T))) - off < width;
+        const uint4 x = there ? load_edge(from + i, begin, end) : make_uint4(0u, 0u, 0u, 0u);
         g.row[s][4 * i] = x.x, g.row[s][4 * i + 1] = x.y, g.row[s][4 * i + 2] = x.z, g.row[s][4 * i + 3] = x.w;
       }
     };
@@ -337,7 +400,7 @@ __global__ void __launch_bounds__(kBiasThreads, kBiasGradCtas) bias_grad_kernel(
       for (int e = 7; e > 0; --e) acc[e] = acc[e - 1];
       acc[0] = lane == 0 ? 0.f : in;
     };
-    auto sweep = [&](auto few) {
+    auto sweep = [&](auto few, auto edge) {
       constexpr bool FEW = decltype(few)::value;
       const int per_query = (nb + kGroup - 1) / kGroup, all = rows * nb;
       const int count = FEW ? (all + kGroup - 1) / kGroup : rows * per_query;
@@ -349,12 +412,14 @@ __global__ void __launch_bounds__(kBiasThreads, kBiasGradCtas) bias_grad_kernel(
 #pragma unroll
         for (int s = 0; s < kGroup; ++s) {
           if constexpr (FEW) {
-            load(g, s, at, row < all);
+            if constexpr (decltype(edge)::value) load_beyond(g, s, at, row < all);
+            else load(g, s, at, row < all);
             ++row;
             if (++at_b == nb) at_b = 0, at = p += a.stride_q;
             else at += a.stride_b;
           } else {
-            load(g, s, at + s * a.stride_b, at_b + s < nb);
+            if constexpr (decltype(edge)::value) load_beyond(g, s, at + s * a.stride_b, at_b + s < nb);
+            else load(g, s, at + s * a.stride_b, at_b + s < nb);
           }
         }
         if constexpr (!FEW) {
@@ -390,8 +455,14 @@ __global__ void __launch_bounds__(kBiasThreads, kBiasGradCtas) bias_grad_kernel(
         take(now);
       }
     };
-    if (nb <= 2) sweep(std::true_type{});
-    else sweep(std::false_type{});
+    // (strides are not negative: the unit's first row begins first, its last ends last)
+    if (EDGE && (p < whole_from || p + (nb - 1) * a.stride_b + (rows - 1) * a.stride_q + width > whole_to)) {
+      if (nb <= 2) sweep(std::true_type{}, std::bool_constant<EDGE>{});
+      else sweep(std::false_type{}, std::bool_constant<EDGE>{});
+    } else {
+      if (nb <= 2) sweep(std::true_type{}, std::false_type{});
+      else sweep(std::false_type{}, std::false_type{});
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) mine[lane * 8 + e] = acc[e];
     __syncwarp();
@@ -568,6 +639,13 @@ int launch_bias(const BiasArgs& a, bool vec, bool flat, dim3 grid, cudaStream_t 
   return launch_pdl(vec ? bias_kernel<T, E, true, SCORES> : bias_kernel<T, E, false, SCORES>, grid, dim3(kBiasThreads), 0, stream, a);
 }
 
+template <typename T>
+int launch_bias_grad(const BiasGradArgs& a, const BiasOut& o, bool vec, bool edge, dim3 grid, cudaStream_t stream) {
+  return launch_pdl(vec ? (edge ? bias_grad_kernel<T, true, true> : bias_grad_kernel<T, true, false>)
+                        : (edge ? bias_grad_kernel<T, false, true> : bias_grad_kernel<T, false, false>),
+                    grid, dim3(kBiasThreads), 0, stream, a, o);
+}
+
 // Units of one worker and head, and how they are dealt.
 struct GradPlan {
   int rows, width, row_units, key_units, batch_units, per_unit, groups;
@@ -601,6 +679,17 @@ GradPlan plan_grad(const int64_t* offs, int K, int64_t heads, int64_t queries, i
 }
 
 }  // namespace
+
+int take_bias_error() {
+  int h = 0;
+#ifdef ADASUM_BOUNDS_CHECK
+  const int zero = 0;
+  if (cudaMemcpyFromSymbol(&h, g_status, sizeof h) != cudaSuccess) return -1;
+  if (h != 0 && cudaMemcpyToSymbol(g_status, &zero, sizeof zero) != cudaSuccess) return -1;
+#endif
+  return h;
+}
+
 }  // namespace adasum
 
 using namespace adasum;
@@ -657,6 +746,14 @@ adasum_status_t adasum_relative_position_bias(const void* table, int buckets, in
   if (x > INT32_MAX) return ADASUM_ERR_UNSUPPORTED;
   // sequences of a CTA: as many as leave eight CTAs an SM, so that the biases serve many of them
   int64_t parts = std::max<int64_t>(1, std::min<int64_t>((batch + step - 1) / step, static_cast<int64_t>(8) * sm_count() / (x * heads)));
+  // (or up to eight times as many, if their waves take less, a CTA's biases taking about two sequences' time:
+  // 64 x 16 x 512 x 513 bf16 in four parts, 2.8 waves, 167 us a pass, in two, 1.4 waves, 189)
+  if (flat) {
+    const int64_t slots = static_cast<int64_t>(kFlatCtas) * sm_count(), base = parts;
+    auto time = [&](int64_t p) { return (x * heads * p + slots - 1) / slots * ((batch + p - 1) / p + 2); };
+    for (int64_t p = base + 1; p <= std::min(batch, 8 * base); ++p)
+      if (time(p) < time(parts)) parts = p;
+  }
   parts = std::max(parts, (batch + (int64_t(1) << 16) - 1) >> 16);
   a.per_cta = (batch + parts - 1) / parts;
   parts = (batch + a.per_cta - 1) / a.per_cta;
@@ -714,6 +811,7 @@ adasum_status_t adasum_relative_position_bias_backward(const void* grad_scores, 
   const GradPlan g = plan_grad(worker_offsets, K, heads, some ? queries : 1, some ? keys : 1, vec);
   if (g.groups < 0) return ADASUM_ERR_UNSUPPORTED;
   a.d = grad_scores;
+  a.end = static_cast<const char*>(grad_scores) + span * e;
   a.stride_b = stride_b;
   a.stride_h = stride_h;
   a.stride_q = stride_q;
@@ -738,10 +836,9 @@ adasum_status_t adasum_relative_position_bias_backward(const void* grad_scores, 
   o.groups = a.groups;
   o.partials = a.partials;
   const dim3 grid(static_cast<unsigned>(a.groups), static_cast<unsigned>(heads), static_cast<unsigned>(K));
+  const bool edge = some && !(is_aligned(a.d, 16) && is_aligned(a.end, 16));
   adasum_status_t st = counted_launch(stream, "position_bias_grad", static_cast<double>(batch) * heads * queries * keys * e, [&] {
-    if (dtype == ADASUM_BF16)
-      return launch_pdl(vec ? bias_grad_kernel<bf16, true> : bias_grad_kernel<bf16, false>, grid, dim3(kBiasThreads), 0, stream, a, o);
-    return launch_pdl(vec ? bias_grad_kernel<float, true> : bias_grad_kernel<float, false>, grid, dim3(kBiasThreads), 0, stream, a, o);
+    return dtype == ADASUM_BF16 ? launch_bias_grad<bf16>(a, o, vec, edge, grid, stream) : launch_bias_grad<float>(a, o, vec, edge, grid, stream);
   });
   if (st || a.partials == nullptr) return st;
   return counted_launch(stream, "position_bias_join", 0.0, [&] {

@@ -537,7 +537,8 @@ ADASUM_API adasum_status_t adasum_gelu_checkpointed_backward(
  *                 ADASUM_BIAS_MAX_BUCKETS, n / 2 < max_distance < 2^31
  *   offset        keys before the first query's own (queries that follow a cache); |offset| <=
  *                 2^61
- *   scores        element (b, h, i, j) at b * stride_b + h * stride_h + i * stride_q + j
+ *   scores        element (b, h, i, j) at b * stride_b + h * stride_h + i * stride_q + j; nothing
+ *                 before the first or after the last is read, what lies between rows may be
  *
  * adasum_relative_position_bias -- out = scores + bias, batch x heads x queries x keys elements
  * of dtype, dense, rounded once; with scores = NULL the bias alone, heads x queries x keys of
