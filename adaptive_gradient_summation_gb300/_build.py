@@ -13,7 +13,8 @@ Two variants are built from the same sources:
                            switches the tests use to force a route, switch a kernel off
                            or inject a fault on the host (ADASUM_ONCHIP, ADASUM_TINY,
                            ADASUM_WARP_GRAM, ADASUM_ONCHIP_FAST, ADASUM_ONCHIP_MAX_CLUSTER,
-                           ADASUM_PAIR_FUSED, ADASUM_PDL, ADASUM_FAULT_INJECT)
+                           ADASUM_PAIR_FUSED, ADASUM_PDL, ADASUM_UPDATE_TILE,
+                           ADASUM_FAULT_INJECT)
 """
 from __future__ import annotations
 

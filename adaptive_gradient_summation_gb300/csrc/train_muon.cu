@@ -30,6 +30,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <vector>
 
 #include "adasum_host.h"
@@ -337,8 +338,11 @@ enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
 // Tiles are 128 * CTAS x NT: CTAS = 2 CTAs (a cluster) share one, each with 128 of its rows, and
 // each copies its rows of the left operand and its half of the columns of the right one.
 // TERMS = 3: products of sums of two parts.  Their sums come in runs along the depth, each drained
-// and added in fp32 registers; shorter ones for A = X X', which has squares on its diagonal.
-// (4096 x 4096 in one run: 9.5e-6 off after five steps.)
+// and added in fp32 registers; shorter ones for A = X X', which has squares on its diagonal and whose
+// errors every later step sees: 16 cut-offs a sum.  (4096 x 4096 in one run: 9.5e-6 off after five
+// steps.  A of 257 x 513 in runs of 32 cut-offs: 3.7e-6 off, of 16 1.7e-6, fp32 throughout 1.7e-6; 24 x
+// (1024 x 4096) takes 1.4% more for it, its step no more.  Runs half as long for the other products too: half
+// the error where the singular values fall off, 4 to 12% more time.)
 template <int CTAS, int NT, int TERMS>
 struct FlowShape {
   static constexpr int kHeight = 128 * CTAS;
@@ -355,7 +359,7 @@ struct FlowShape {
   static constexpr int kSet = 256, kHigh = TERMS == 3 ? 128 : 256, kChains = kHigh / NT, kCols = 512;
   static_assert(NT <= kHigh, "a set holds a tile");
   // stages of 64 along the depth in a run
-  __device__ static int run(int kind) { return TERMS == 1 ? 1 << 30 : kind == kGram ? 8 : 16; }
+  __device__ static int run(int kind) { return TERMS == 1 ? 1 << 30 : kind == kGram ? 4 * kChains : 16; }
   static constexpr int kBlocks = NT / 64;  // of an epilogue warp
 };
 
@@ -946,6 +950,10 @@ TileSize tile_size(const Piece* p, int pieces, bool fine) {
   constexpr TileSize kBf16[3] = {{2, 256, 640, 11000}, {1, 128, 480, 7800}, {1, 64, 400, 3400}};
   constexpr TileSize kFp32[3] = {{2, 128, 850, 14000}, {1, 128, 1000, 12000}, {1, 64, 620, 6600}};
   const TileSize* const kSizes = fine ? kFp32 : kBf16;
+#ifdef ADASUM_TEST_HOOKS
+  if (const char* v = std::getenv("ADASUM_UPDATE_TILE"))
+    if (*v >= '0' && *v <= '2' && v[1] == '\0') return kSizes[*v - '0'];
+#endif
   TileSize best = kSizes[0];
   double least = 1e300;
   for (int which = 0; which < 3; ++which) {

@@ -583,9 +583,10 @@ ADASUM_API int64_t adasum_relative_position_bias_backward_scratch_bytes(
  * below 2.8, else the result is infinite or NaN.
  *
  * All products run on the tensor cores with fp16 operands and fp32 sums.  fp32 results:
- * every operand is the sum of two fp16 numbers; the result is as far from the exact one as
- * if all were computed in fp32, or nearer.  bf16 results: single fp16 operands, the linear
- * term from two; the result is within about 2e-3 of the exact one's norm before its rounding.
+ * every operand is the sum of two fp16 numbers; the result is about as far from the exact
+ * one as if all were computed in fp32, at most twice (2e-7 to 7e-6 of the norm).  bf16
+ * results: single fp16 operands, the linear term from two; the result is within 2^-8 of the
+ * exact one's norm (4e-4 to 3e-3) before its rounding.
  * NaN and infinities in a matrix make all of it NaN; a matrix of zeros stays zero.
  *
  * The conventions of the training operators above hold (scratch memory from the caller, any
