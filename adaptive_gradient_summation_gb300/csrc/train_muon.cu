@@ -31,6 +31,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
+#include <cstring>
 #include <vector>
 
 #include "adasum_host.h"
@@ -52,7 +53,8 @@ __device__ int g_error;
 // those beyond the last: any of them).
 std::atomic<bool> g_launched[65];
 int launched_index(int device) { return device >= 0 && device < 64 ? device : 64; }
-constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
+constexpr long long kWaitCycles = 4000000000ll;  // a wait's limit, about two seconds
+constexpr long long kSettleCycles = 4000000ll;     // what copies or products take at the very most
 
 // ------------------------------------------------------------------ momentum and norms
 
@@ -331,6 +333,10 @@ struct FlowArgs {
   float keep;
   float coefficients[3 * ADASUM_NEWTON_SCHULZ_MAX_STEPS];
   float scale_b[ADASUM_NEWTON_SCHULZ_MAX_STEPS];
+  long long wait_cycles;
+#ifdef ADASUM_TEST_HOOKS
+  int held_step;                // from this one on no product is ever found written
+#endif
 };
 
 enum Kind : int { kGram = 0, kPoly = 1, kApply = 2 };
@@ -430,17 +436,23 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
     if (mbar_try_wait_pair<CTAS>(bar, parity)) return true;
     const long long t0 = clock64();
     while (!mbar_try_wait_pair<CTAS>(bar, parity))
-      if (stop || clock64() - t0 > kWaitCycles) return give_up();
+      if (stop || clock64() - t0 > a.wait_cycles) return give_up();
     return true;
   };
+  // The same by a whole warp, which goes on or gives up together.
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
   // until the products of its matrix before this tile's are written
   auto wait_ready = [&](const Tile& t) {
     const FlowGroup& g = a.group[t.group];
-    const int need = E::kWarps * CTAS * (t.step * (2 * g.tiles[0] + g.tiles[1]) + t.kind * g.tiles[0]);
+    const int need = E::kWarps * CTAS * (t.step * (2 * g.tiles[0] + g.tiles[1]) + t.kind * g.tiles[0])
+#ifdef ADASUM_TEST_HOOKS
+                     + (t.step >= a.held_step ? 1 << 30 : 0)
+#endif
+        ;
     if (load_acquire(g.ready + t.matrix) >= need) return true;
     const long long t0 = clock64();
     while (load_acquire(g.ready + t.matrix) < need) {
-      if (stop || clock64() - t0 > kWaitCycles) return give_up();
+      if (stop || clock64() - t0 > a.wait_cycles) return give_up();
       __nanosleep(32);
     }
     return true;
@@ -513,18 +525,19 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
           if (++s == S::kStages) s = 0, phase ^= 1;
         }
       }
-      // every stage consumed: no arrival is on its way to a CTA that has left
+      // every stage consumed: no arrival is on its way to a CTA that has left, and no product still
+      // reads shared memory or writes TMEM when they are given back
       for (int i = max(0, issued - S::kStages); ok && i < issued; ++i) ok = wait(&empty[i % S::kStages], (i / S::kStages) & 1);
-      if (!ok && warp == 0) {  // copies still in flight
-        for (int i = max(0, issued - S::kStages); rank == 0 && i < issued; ++i) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(&full[i % S::kStages], (i / S::kStages) & 1) && clock64() - t0 < kWaitCycles) {
-          }
-        }
-      }
-      if (!ok) {  // (a pair's second CTA cannot see its copies' barrier)
+      if (!ok) {
         const long long t0 = clock64();
-        while (clock64() - t0 < kWaitCycles / 1000) {
+        // Copies still in flight.  A stage whose copies have all begun tells; one that another copying
+        // thread has not come to, or one of a pair's second CTA, which cannot see its copies' barrier,
+        // does not, but then time has passed, for products of stages that were full too, after which
+        // their thread begins no other; and a pair's CTAs leave together.
+        for (int i = max(0, issued - S::kStages); rank == 0 && i < issued; ++i)
+          while (!mbar_try_wait(&full[i % S::kStages], (i / S::kStages) & 1) && clock64() - t0 < kSettleCycles) {
+          }
+        while (clock64() - t0 < kSettleCycles) {
         }
       }
     }
@@ -737,7 +750,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       bool ok = true;
       const long long t0 = clock64();
       while (load_acquire_cta(&copied) <= tiles)
-        if (stop || clock64() - t0 > kWaitCycles) {
+        if (stop || clock64() - t0 > a.wait_cycles) {
           ok = give_up();
           break;
         }
@@ -767,7 +780,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
           for (int c = 0; c < E::kCols; ++c) v[k][c] = 0.f;
         const int length = S::run(t.kind);
         for (int run = 0; ok && run < ks; run += length, ++acc) {
-          if (!(ok = wait(&acc_full[acc & 1], (acc >> 1) & 1))) break;
+          if (!(ok = wait_warp(&acc_full[acc & 1], (acc >> 1) & 1))) break;
           tc_fence_after();
           const float gain = cut_off<S::kChains>(min(ks - run, length));
           const uint32_t set = from + (acc & 1) * S::kSet;
@@ -789,7 +802,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
           if (t.kind != kGram) fetch(k + 1, next);
         }
       } else {
-        if (!wait(&acc_full[acc & 1], (acc >> 1) & 1)) break;
+        if (!wait_warp(&acc_full[acc & 1], (acc >> 1) & 1)) break;
         tc_fence_after();
         const float gain = TERMS == 3 ? cut_off<S::kChains>(ks) : 1.f;
         const uint32_t set = from + (acc & 1) * S::kSet;
@@ -1056,6 +1069,15 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
   f.keep = res.keep;
   std::copy(it.coefficients, it.coefficients + 3 * it.steps, f.coefficients);
   scale_b(it.coefficients, it.steps, f.scale_b);
+  f.wait_cycles = kWaitCycles;
+#ifdef ADASUM_TEST_HOOKS
+  f.held_step = it.steps;
+  const char* inject = std::getenv("ADASUM_FAULT_INJECT");
+  if (inject != nullptr && std::strcmp(inject, "timeout") == 0) {
+    f.wait_cycles = 2000000;  // about a millisecond
+    f.held_step = std::min(1, it.steps - 1);
+  }
+#endif
   src.eps = it.eps;
   src.vec = is_aligned(src.x, 16) && is_aligned(src.momentum, 16);
   int first = 0;
