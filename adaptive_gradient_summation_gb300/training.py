@@ -528,6 +528,12 @@ def _scores(t: torch.Tensor, what: str):
     return shape, strides[:3]
 
 
+def _positions(max_distance: int, offset: int):
+    """Refuses what the C entries' 64-bit arguments would wrap."""
+    if not -2 ** 63 <= max_distance < 2 ** 63 or not -2 ** 63 <= offset < 2 ** 63:
+        raise ValueError("max_distance and offset must fit 64 bits")
+
+
 def relative_position_bias(table: torch.Tensor, queries: int, keys: int, *, bidirectional: bool = True, max_distance: int = 128,
                            offset: int = 0, scores: torch.Tensor | None = None, out: torch.Tensor | None = None,
                            stream: torch.cuda.Stream | None = None) -> torch.Tensor:
@@ -547,6 +553,7 @@ def relative_position_bias(table: torch.Tensor, queries: int, keys: int, *, bidi
     buckets, heads = table.shape
     if queries < 0 or keys < 0:
         raise ValueError("queries and keys must not be negative")
+    _positions(max_distance, offset)
     code, batch, strides, p = tcode, 1, (0, 0, 0), None
     if scores is not None:
         code, at = _kind(scores, "scores")
@@ -581,8 +588,9 @@ def relative_position_bias_backward(grad_scores: torch.Tensor, num_buckets: int,
     """
     code, index = _kind(grad_scores, "grad_scores")
     (batch, heads, queries, keys), strides = _scores(grad_scores, "grad_scores")
-    if num_buckets < 1:
-        raise ValueError("num_buckets must be positive")
+    if not 1 <= num_buckets < 2 ** 31:
+        raise ValueError("num_buckets must be positive and fit 32 bits")
+    _positions(max_distance, offset)
     if grads is None and accumulate:
         raise ValueError("accumulate needs grads to add to")
     if _elsewhere(index, stream):
