@@ -44,7 +44,8 @@ namespace {
 
 constexpr int kMaxBatch = 256;                    // matrices of one launch
 constexpr int64_t kChunkBytes = int64_t(1) << 30;  // scratch of a chunk of equal matrices, about
-// X and A are kept times these, B times kScaleB or less (scale_b).
+// X and A are kept times these, B times kScaleB or less, and X times another power of two where its
+// norm is far below 1 (plan_scales).
 constexpr float kScaleX = 8192.f, kScaleA = 8192.f, kScaleB = 4096.f;
 
 // What a wait that ran out leaves (adasum_get_last_error).
@@ -72,6 +73,7 @@ struct SourceArgs {
   int nesterov;
   float* partials;     // [matrix][chunk][3]
   int* ready;          // per matrix, to be zeroed
+  int* shift;          // per matrix, see FlowGroup
   int first;           // the first matrix' place among all
   int chunks;
   int64_t per_chunk;
@@ -82,11 +84,11 @@ struct SourceArgs {
 };
 
 // Sums of squares in three ranges, so that no magnitude that fp32 holds is lost: of the
-// values, of the values times 2^-64, and times 2^64.
+// values, of the values times 2^-64, and times 2^96.
 struct Squares {
   F2 mid = f2(0.f), big = f2(0.f), small = f2(0.f);
   __device__ __forceinline__ void add(float x, float y) {
-    const F2 v = f2(x, y), b = mul2(v, f2(0x1p-64f)), s = mul2(v, f2(0x1p64f));
+    const F2 v = f2(x, y), b = mul2(v, f2(0x1p-64f)), s = mul2(v, f2(0x1p96f));
     mid = fma2(v, v, mid);
     big = fma2(b, b, big);
     small = fma2(s, s, small);
@@ -213,8 +215,8 @@ __global__ void __launch_bounds__(256) squares_kernel(const SourceArgs a, const 
   }
 }
 
-// X = update / (|update| + eps), times kScaleX, in its parts; 64 x 64 tiles, eight neighbours a
-// thread on both sides.  Bound by bytes.
+// X = update / (|update| + eps), times kScaleX and 2^shift, in its parts; 64 x 64 tiles, eight
+// neighbours a thread on both sides.  Bound by bytes.
 __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, const __grid_constant__ Places places) {
   pdl_enter();
   __shared__ float tile[64][65];
@@ -229,12 +231,16 @@ __global__ void __launch_bounds__(256) normalize_kernel(const SourceArgs a, cons
     for (int j = 0; j < 3; ++j) s[j] = warp_sum(s[j]);
     if (threadIdx.x == 0) {
       // (the middle range between 2^-80 and 2^100; NaN takes the last branch)
-      float pre = 1.f, norm;
-      if (s[0] > 0x1p100f) pre = 0x1p-64f, norm = sqrtf(s[1]) + a.eps * 0x1p-64f;
-      else if (s[0] < 0x1p-80f) pre = 0x1p64f, norm = sqrtf(s[2]) + a.eps * 0x1p64f;
-      else norm = sqrtf(s[0]) + a.eps;
+      float pre = 1.f, own;
+      if (s[0] > 0x1p100f) pre = 0x1p-64f, own = sqrtf(s[1]);
+      else if (s[0] < 0x1p-80f) pre = 0x1p96f, own = sqrtf(s[2]);
+      else own = sqrtf(s[0]);
+      const float norm = own + a.eps * pre;
+      // X's norm is from 2^-(shift + 1) up to below 2^-shift (zeros, NaN, a norm of 1: 0)
+      const int shift = own > 0.f ? max(0, 126 - static_cast<int>(__float_as_uint(own / norm) >> 23 & 255)) : 0;
+      if (blockIdx.x == 0 && blockIdx.y == 0) a.shift[blockIdx.z] = shift;
       factors[0] = pre;
-      factors[1] = norm > 0.f || norm != norm ? kScaleX / norm : 0.f;
+      factors[1] = norm > 0.f || norm != norm ? kScaleX / norm * __uint_as_float(static_cast<uint32_t>(127 + shift) << 23) : 0.f;
     }
   }
   __syncthreads();
@@ -320,6 +326,7 @@ struct FlowGroup {
   int m, n, batch, first;      // the first matrix' place among all
   int col_tiles[2], tiles[2];  // of A and B (lower triangle), of X
   int* ready;                  // per matrix: warps that have written their part of a tile
+  const int* shift;            // per matrix: X is first kept times 2^shift, in step k times 2^max(0, shift - growth[k])
   float step[2];               // weights: w <- keep w - step x (of a matrix as it is, transposed)
 };
 constexpr int kMaxGroups = 4;  // of one launch
@@ -333,6 +340,7 @@ struct FlowArgs {
   float keep;
   float coefficients[3 * ADASUM_NEWTON_SCHULZ_MAX_STEPS];
   float scale_b[ADASUM_NEWTON_SCHULZ_MAX_STEPS];
+  int growth[ADASUM_NEWTON_SCHULZ_MAX_STEPS];  // X's norm is below 2^growth times the first one's
   long long wait_cycles;
 #ifdef ADASUM_TEST_HOOKS
   int held_step;                // from this one on no product is ever found written
@@ -603,9 +611,14 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       const int out_parts = TERMS == 3 || (apply && t.step + 3 < a.steps) ? 2 : 1;
       const float c_a = a.coefficients[3 * t.step], c_b = a.coefficients[3 * t.step + 1], c_c = a.coefficients[3 * t.step + 2];
       const float scale_b = a.scale_b[t.step];
-      const float scale = t.kind == kGram   ? kScaleA / (kScaleX * kScaleX)
+      // X's further power of two, and the next X's (the result has none)
+      const int shift = __ldg(g.shift + t.matrix), here = max(0, shift - a.growth[t.step]);
+      const int next_shift = last_step ? 0 : max(0, shift - a.growth[t.step + 1]);
+      auto power = [](int n) { return n < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + n) << 23); };
+      const float moved = apply ? power(next_shift - here) : 1.f;
+      const float scale = t.kind == kGram   ? kScaleA / (kScaleX * kScaleX) * power(-2 * here)
                           : t.kind == kPoly ? c_c * (scale_b / (kScaleA * kScaleA))
-                                            : 1.f / scale_b;
+                                            : moved / scale_b;
       const bool even = (t.step & 1) == 0;
       const __half *in0 = apply ? (even ? g.x[0][0] : g.x[1][0]) : g.a[0], *in1 = apply ? (even ? g.x[0][1] : g.x[1][1]) : g.a[1];
       __half *out0 = apply ? (even ? g.x[1][0] : g.x[0][0]) : t.kind == kGram ? g.a[0] : g.b[0];
@@ -761,7 +774,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       for (int r = 0; r < E::kPasses; ++r) {
         const int i = i0 + r * E::kRows + sub;
         on_diagonal[r] = kDiagonals && t.kind == kPoly && i < g.m ? __ldcg(diagonal_a + i) : 0.f;
-        of_row[r] = apply ? c_a + (kDiagonals && i < g.m ? __ldcg(g.db + static_cast<int64_t>(t.matrix) * g.lda + i) : 0.f) * scale
+        of_row[r] = apply ? c_a * moved + (kDiagonals && i < g.m ? __ldcg(g.db + static_cast<int64_t>(t.matrix) * g.lda + i) : 0.f) * scale
                           : __fmaf_rn(scale, on_diagonal[r], c_b * (scale_b / kScaleA));
       }
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * E::kCols;
@@ -878,7 +891,7 @@ int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 // in the scratch memory.
 struct ScratchMap {
   int64_t m, n, ldx, lda;
-  int64_t x[2][2], a[2], b[2], da, db, partials, ready, bytes;
+  int64_t x[2][2], a[2], b[2], da, db, partials, ready, shift, bytes;
   int chunks;
   int64_t per_chunk;
   ScratchMap(int64_t m_, int64_t n_, int64_t batch, bool fine) : m(m_), n(n_), ldx(round_up(n_, 8)), lda(round_up(m_, 8)) {
@@ -901,6 +914,7 @@ struct ScratchMap {
     da = take(batch * lda * 4);
     db = take(batch * lda * 4);
     ready = take(batch * 4);
+    shift = take(batch * 4);
     bytes = at;
   }
 };
@@ -1026,20 +1040,26 @@ int launch_flow(FlowArgs& a, const Places& places, TileSize s, cudaStream_t stre
   return launch_flow_as<1, 64, TERMS>(a, places, stream);
 }
 
-// The power of two that B = b A + c A A is kept times in every step: B's elements are at most its
-// largest singular value, |b t + c t^2| with t = s^2 for one of X's, s, and have to stay below
-// fp16's 65504.  The singular values are 1 at most at first, then what the steps so far can have
-// made of those, and below 2.8 (the caller's part).  With the usual coefficients |b t + c t^2| is
+// The powers of two of every step that follow from the coefficients.  The singular values s of X are
+// 1 at most at first, then what the steps so far can have made of those, and below 2.8 (the caller's
+// part).
+//   scale: B = b A + c A A is kept times it.  B's elements are at most its largest singular value,
+// |b t + c t^2| for some t = s^2, and have to stay below fp16's 65504.  With the usual coefficients that is
 // 2.8 at most, and the scale kScaleB.
-void scale_b(const float* coefficients, int steps, float* scale) {
+//   growth: a step multiplies X's norm by |a + b t + c t^2| at most.  Where the first X is small, since
+// its matrix is far below eps, it is kept times as much more (FlowGroup's shift), which later steps take back as it
+// grows; else its elements would be below what fp16 holds (norms of 2^-19 off by 2e-4, of 2^-29 by 0.2).
+void plan_scales(const float* coefficients, int steps, float* scale, int* growth) {
   double most = 1.01;  // singular value (roundings added)
-  for (int k = 0; k < steps; ++k) {
+  for (int k = 0, grown = 0; k < steps; ++k) {
     const double a = coefficients[3 * k], b = coefficients[3 * k + 1], c = coefficients[3 * k + 2], end = most * most;
-    double of_b = 0.0, of_x = 0.0;
+    double of_b = 0.0, of_x = 0.0, gain = std::fabs(a);
     auto at = [&](double t) {  // an end or an extreme value inside
       if (!(t >= 0.0 && t <= end)) return;
-      of_b = std::max(of_b, std::fabs(t * (b + c * t)));
-      of_x = std::max(of_x, std::sqrt(t) * std::fabs(a + t * (b + c * t)));
+      const double q = t * (b + c * t);
+      of_b = std::max(of_b, std::fabs(q));
+      of_x = std::max(of_x, std::sqrt(t) * std::fabs(a + q));
+      gain = std::max(gain, std::fabs(a + q));
     };
     at(end);
     if (c != 0.0) {
@@ -1052,6 +1072,8 @@ void scale_b(const float* coefficients, int steps, float* scale) {
     }
     scale[k] = kScaleB;
     while (of_b * scale[k] > 65000.0) scale[k] *= 0.5f;
+    growth[k] = grown;
+    for (double g = 1.01 * gain; g > 1.0; g *= 0.5) ++grown;
     most = std::min(1.01 * of_x, 2.8);
   }
 }
@@ -1068,7 +1090,7 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
   f.dest_vec = is_aligned(res.dest, 16);
   f.keep = res.keep;
   std::copy(it.coefficients, it.coefficients + 3 * it.steps, f.coefficients);
-  scale_b(it.coefficients, it.steps, f.scale_b);
+  plan_scales(it.coefficients, it.steps, f.scale_b, f.growth);
   f.wait_cycles = kWaitCycles;
 #ifdef ADASUM_TEST_HOOKS
   f.held_step = it.steps;
@@ -1110,6 +1132,7 @@ adasum_status_t iterate(SourceArgs src, const Places& from, const Places& places
     g.batch = batch;
     g.first = src.first = first;
     g.ready = src.ready = reinterpret_cast<int*>(scratch + l.ready);
+    g.shift = src.shift = reinterpret_cast<int*>(scratch + l.shift);
     std::copy(pieces[i].step, pieces[i].step + 2, g.step);
     src.partials = reinterpret_cast<float*>(scratch + l.partials);
     src.chunks = l.chunks;
