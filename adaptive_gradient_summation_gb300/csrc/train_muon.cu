@@ -12,19 +12,22 @@
 // the rounding errors of X that point into their directions: after five steps one rounding of
 // X to bf16 is 1e-2 to 1e-1 of the result's norm, to fp16 2e-3 to 2e-2 (random, power-law and
 // low-rank spectra).  So
-//   bf16 results: products of X, A and B as single fp16 numbers, but X itself as the sum of two
-//     for the term a X, where the growing errors would come from; the last two steps, whose
-//     errors no longer grow, take the rounded X there too, so that value and slope of the
-//     polynomial fit each other.  Off by 1.4e-3 at most, as much as the result's rounding to bf16.
-//   fp32 results: X, A and B are sums of two fp16 numbers (22 bits), a product is three products
-//     of them (the fourth, of the low parts, is below 2^-22).  The diagonals of A and B, which
-//     dominate once the singular values are near 1, are kept apart in fp32:
-//         A A = E E + (d_i + d_j) E + d^2  with A = E + diag(d),   B X = F X + d_i X,
-//     the rest of which is added to the product in fp32.  For the tensor cores cut every partial sum
-//     off towards zero: 64 cut-offs along a depth of 1024 lose 1.4e-6 of a sum that grows
-//     evenly, which is made good by a factor (kCutOff), but up to twice that where one term
-//     outweighs the others.  Off by 5e-7 to 5e-6, fp32 throughout by 2e-6 to 2e-5.  (1024 x 4096 after
-//     five steps: 1.5e-5 without factor and diagonals apart, 1.2e-5 with the factor alone, 1.5e-6.)
+// The diagonals of A and B, which dominate once the singular values are near 1, are kept apart in
+// fp32, the rest of the two being fp16:
+//     A A = E E + (d_i + d_j) E + d^2  with A = E + diag(d),   B X = F X + d_i X.
+//   bf16 results: products of X and of A and B off their diagonals as single fp16 numbers, but X
+//     itself as the sum of two for the terms a X and d_i X, where the growing errors would come from; the
+//     last two steps, whose errors no longer grow, take the rounded X there too.  Off by 2e-4 to
+//     1.1e-3, less than the result's rounding to bf16 (1.7e-3).  (Random, falling and equal singular
+//     values, 64 x 64 to 4096 x 4096.  With the diagonals in fp16 4e-4 to 2.8e-3, in 1 to 4% less time; with both
+//     parts of X in the last two steps too 1.1e-4 to 1.0e-3, in 6% more.)
+//   fp32 results: X, E and F are sums of two fp16 numbers (22 bits), a product is three products
+//     of them (the fourth, of the low parts, is below 2^-22); the rest is added to the product in fp32.
+//     The tensor cores cut every partial sum off towards zero: 64 cut-offs along a depth of 1024 lose
+//     1.4e-6 of a sum that grows evenly, which is made good by a factor (kCutOff), but up to twice that
+//     where one term outweighs the others, so that sums come in runs.  Off by 2e-7 to 7e-6, fp32
+//     throughout by 5e-7 to 1.1e-5: 0.2 to 1.5 times that.  (1024 x 4096 after five steps: 1.5e-5 without
+//     factor and diagonals apart, 1.2e-5 with the factor alone, now 0.8e-6.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -599,8 +602,6 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
     const int quarter = warp & 3, group = (warp - 2) >> 2;
     float* block = reinterpret_cast<float*>(stages + S::kStages * S::kStageBytes) + (warp - 2) * E::kFloats;
     const int sub = lane / E::kOcts, oct = lane % E::kOcts * 8;  // row, of kRows, and the first of eight columns
-    // A's and B's diagonals apart, so that no sum is dominated by one term (the file's comment)
-    constexpr bool kDiagonals = TERMS == 3;
     int acc = 0, tiles = 0;
     for (int at = first; at < total; at += stride, ++tiles) {
       const Tile t = locate(at);
@@ -630,8 +631,8 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       // (of a symmetric result: the lower triangle in squares of 32 x 32)
       auto there = [&](int k) { return k < S::kBlocks && i0 < g.m && column(k) < cols && (apply || column(k) < i0 + 32); };
       // What X's row is multiplied with beside the product (kApply), or A's (kPoly: with more for
-      // the column), and A's diagonal there.
-      float of_row[E::kPasses], on_diagonal[E::kPasses];
+      // the column).  A's and B's diagonals are kept apart (the file's comment).
+      float of_row[E::kPasses];
       // What is added, of block k: some rows' eight columns of each lane.
       struct Added {
         uint4 part[2][E::kPasses];
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       auto fetch = [&](int k, Added& f) {
         if (t.kind == kGram || !there(k)) return;
         const int c = column(k);
-        if (kDiagonals && !apply) f.diagonal = c + lane % E::kCols < cols ? __ldcg(diagonal_a + c + lane % E::kCols) : 0.f;
+        if (!apply) f.diagonal = c + lane % E::kCols < cols ? __ldcg(diagonal_a + c + lane % E::kCols) : 0.f;
 #pragma unroll
         for (int r = 0; r < E::kPasses; ++r) {
           const int i = i0 + r * E::kRows + sub;
@@ -694,11 +695,29 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       // Block k, whose rows' products the lanes hold.
       auto finish = [&](int k, const float (&v)[E::kCols], const Added& f) {
         const int j0 = column(k);
-        const bool mirror = !apply && j0 < i0, diagonal = kDiagonals && !apply && !mirror;
+        const bool mirror = !apply && j0 < i0;
         __syncwarp();  // the last block has been read
 #pragma unroll
         for (int c = 0; c < E::kCols; ++c) block[E::place(lane, c)] = v[c];
         __syncwarp();
+        float of_column[8];  // (TERMS = 3: in every pass, for want of registers)
+        auto columns = [&] {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) of_column[e] = __shfl_sync(0xFFFFFFFFu, f.diagonal, oct + e);
+        };
+        if (TERMS == 1 && t.kind == kPoly) columns();
+        if (!apply && !mirror) {  // a block on the diagonal: a lane has one of its elements, and leaves 0
+          const int i = j0 + lane;
+          if (lane < E::kCols) {
+            float& at = block[E::place(i - i0, lane)];
+            const float d = at * scale;
+            at = 0.f;
+            const int64_t to = static_cast<int64_t>(t.matrix) * g.lda + i;
+            if (i < g.m && t.kind == kGram) g.da[to] = d;
+            if (i < g.m && t.kind == kPoly) g.db[to] = __fmaf_rn(__fmaf_rn(scale, f.diagonal, c_b * (scale_b / kScaleA)), f.diagonal, d);
+          }
+          __syncwarp();
+        }
         // (a row's last eight columns may reach into its padding)
 #pragma unroll
         for (int r = 0; r < E::kPasses; ++r) {
@@ -710,9 +729,10 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
             float factor[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) factor[e] = of_row[r];
-            if (kDiagonals && !apply) {
+            if (!apply) {
+              if constexpr (TERMS == 3) columns();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) factor[e] = __fmaf_rn(scale, __shfl_sync(0xFFFFFFFFu, f.diagonal, oct + e), factor[e]);
+              for (int e = 0; e < 8; ++e) factor[e] = __fmaf_rn(scale, of_column[e], factor[e]);
             }
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
@@ -725,15 +745,6 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
                 x[2 * e + 1] = __fmaf_rn(factor[2 * e + 1], y.y, x[2 * e + 1]);
               }
             }
-          }
-          if (diagonal) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (i == j0 + oct + e && i < g.m) {
-                if (t.kind == kGram) g.da[static_cast<int64_t>(t.matrix) * g.lda + i] = x[e];
-                else g.db[static_cast<int64_t>(t.matrix) * g.lda + i] = __fmaf_rn(of_row[r], on_diagonal[r], x[e]);
-                x[e] = 0.f;
-              }
           }
           if (mirror || transposed) {
 #pragma unroll
@@ -770,13 +781,11 @@ __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(cons
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       Added next;
       fetch(0, next);
+      // (a lane's row of the diagonal)
+      const float on_diagonal = t.kind == kGram || i0 + lane >= g.m ? 0.f : __ldcg((apply ? g.db : g.da) + static_cast<int64_t>(t.matrix) * g.lda + i0 + lane);
 #pragma unroll
-      for (int r = 0; r < E::kPasses; ++r) {
-        const int i = i0 + r * E::kRows + sub;
-        on_diagonal[r] = kDiagonals && t.kind == kPoly && i < g.m ? __ldcg(diagonal_a + i) : 0.f;
-        of_row[r] = apply ? c_a * moved + (kDiagonals && i < g.m ? __ldcg(g.db + static_cast<int64_t>(t.matrix) * g.lda + i) : 0.f) * scale
-                          : __fmaf_rn(scale, on_diagonal[r], c_b * (scale_b / kScaleA));
-      }
+      for (int r = 0; r < E::kPasses; ++r)
+        of_row[r] = __fmaf_rn(scale, __shfl_sync(0xFFFFFFFFu, on_diagonal, r * E::kRows + sub), apply ? c_a * moved : c_b * (scale_b / kScaleA));
       const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + group * E::kCols;
       auto release = [&](uint64_t* bar) {
         tc_fence_before();
