@@ -747,8 +747,9 @@ adasum_status_t adasum_relative_position_bias(const void* table, int buckets, in
   // sequences of a CTA: as many as leave eight CTAs an SM, so that the biases serve many of them
   int64_t parts = std::max<int64_t>(1, std::min<int64_t>((batch + step - 1) / step, static_cast<int64_t>(8) * sm_count() / (x * heads)));
   // (or up to eight times as many, if their waves take less, a CTA's biases taking about two sequences' time:
-  // 64 x 16 x 512 x 513 bf16 in four parts, 2.8 waves, 167 us a pass, in two, 1.4 waves, 189)
-  if (flat) {
+  // 64 x 16 x 512 x 513 bf16 in four parts, 2.8 waves, 167 us a pass, in two, 1.4 waves, 189; where there
+  // are many parts one more or less changes little)
+  if (flat && parts < 8) {
     const int64_t slots = static_cast<int64_t>(kFlatCtas) * sm_count(), base = parts;
     auto time = [&](int64_t p) { return (x * heads * p + slots - 1) / slots * ((batch + p - 1) / p + 2); };
     for (int64_t p = base + 1; p <= std::min(batch, 8 * base); ++p)
