@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kBiasThreads) bias_kernel(const __grid_constan
 // and sequence as one run of values, in the pieces of 16 bytes that hold them, E values each, four
 // a thread.  A piece may hold the end of a row and the next row's beginning, and the run's first
 // and last are shared with other heads.  The biases of all diagonals that a CTA's kFlatPieces
-// pieces meet are in shared memory, padded as above.  64 x 16 x 511 x 505 bf16 in 180 us, 5.9 TB/s,
-// 511 x 513 fp32 338, 6.4 TB/s (one value a load and store 293 and 549; rows one by one in pieces
+// pieces meet are in shared memory, padded as above.  64 x 16 x 511 x 505 bf16 in 172 us, 6.2 TB/s,
+// 511 x 513 fp32 333, 6.5 TB/s (one value a load and store 293 and 549; rows one by one in pieces
 // shifted by each row's offset 236 and 412).
 constexpr int kFlatPieces = 4 * kBiasThreads, kFlatMaxKeys = 8192;
 constexpr int kFlatCtas = 5;  // of an SM, at the least
@@ -735,8 +735,8 @@ adasum_status_t adasum_relative_position_bias(const void* table, int buckets, in
   const bool vec = is_aligned(out, 16) && keys * e % 16 == 0 &&
                    (scores == nullptr || (is_aligned(scores, 16) && (queries == 1 || stride_q * e % 16 == 0) &&
                                           (heads == 1 || stride_h * e % 16 == 0) && (batch == 1 || stride_b * e % 16 == 0)));
-  // (the biases of a row's diagonals have to serve enough values: bf16, 16 heads of 2047 x 2047 97 us
-  // either way, four sequences of them 196 and 269; one of 4 x 4095 x 8191 450 and 181)
+  // (the biases of a row's diagonals have to serve enough values: bf16, 16 heads of 2047 x 2047 89 us
+  // and value by value 97, four sequences of them 180 and 269; one of 4 x 4095 x 8191 450 and 183)
   const bool flat = !vec && keys <= std::min<int64_t>(kFlatMaxKeys, 2048 * batch) &&
                     (scores == nullptr || (dense && (reinterpret_cast<uintptr_t>(scores) - reinterpret_cast<uintptr_t>(out)) % 16 == 0));
   const int64_t piece = 16 / e, width = 32 * piece, tiles = (keys + width - 1) / width, rows = 4 * a.row_groups;

@@ -405,12 +405,13 @@ struct Tile {
 // matrices the products of one fill the SMs while another's last tiles finish.  (One launch a
 // product: 24 x (4096 x 1024) bf16 5.3 ms at the time against 2.8, one of 256 x 1024 137 us against 119.)
 // Two warps copy (TMA), a thread issues the products, the others take finished sums out of TMEM.
-// What bounds it: with many large matrices the traffic between L2 and the SMs, about 43 bytes a cycle
-// and SM: 24 x (1024 x 4096) bf16 1.62 ms, 1.1 without the results' reads and writes, at 1.7 PFLOP/s
-// then; fp32 4.2 ms, three times the products.  One matrix of 4096 x 4096 bf16 in 0.94 ms, 1.4 PFLOP/s
-// of the products that count.  Small matrices: the latency of 15 products in series, each about
-// 2.5 thousand cycles until the first operands are there, 2 to 13 thousand of products, 3 of
-// results and 2 until others may read them: one of 256 x 1024 in 93 us, fp32 133.
+// What bounds it: with many large matrices the results, of which a tile of 256 columns takes as long
+// as its products of depth 1024, and what they and the operands move between L2 and the SMs (43 bytes a cycle
+// and SM, as bytes over time): 24 x (1024 x 4096) bf16 1.75 ms (when it was 1.62 ms, 1.1 without the results'
+// reads and writes, at 1.7 PFLOP/s then); fp32 4.4 ms, three times the products.  One matrix of 4096 x 4096 bf16
+// in 0.96 ms, 1.4 PFLOP/s of the products that count.  Small matrices: the latency of 15 products in series, each
+// about 2.5 thousand cycles until the first operands are there, 2 to 13 thousand of products, 3 of
+// results and 2 until others may read them: one of 256 x 1024 in 93 us, fp32 134.
 template <int CTAS, int NT, int TERMS>
 __global__ void __launch_bounds__(Epilogue<TERMS>::kThreads, 1) flow_kernel(const __grid_constant__ FlowArgs a, const __grid_constant__ Places places) {
   using S = FlowShape<CTAS, NT, TERMS>;
@@ -976,9 +977,9 @@ int64_t count_tiles(int64_t rows, int64_t cols, int height, int nt, bool sym) {
 // CTAs and columns of a tile: those for which the products of a step, one after the other, take
 // least.  Wide tiles copy less for a product, narrow ones give more CTAs something to do: in
 // cycles, about as measured, a tile takes `deep` for 64 along the depth and `end` for its
-// results.  (us of all five steps by 2 x 256, 128 and 64 columns, bf16: 24 x (1024 x 4096) 1622,
-// 2060, 3030, one of 2048 x 2048 296, 259, 371, one of 256 x 1024 187, 127, 93; by 2 x 128, 128 and 64,
-// fp32: 4238, 4203, 5505; 465, 498, 630; 218, 206, 133.)
+// results.  (us of all five steps by 2 x 256, 128 and 64 columns, bf16: 24 x (1024 x 4096) 1731,
+// 2394, 3134, one of 2048 x 2048 311, 273, 372, one of 256 x 1024 187, 132, 96; by 2 x 128, 128 and 64,
+// fp32: 4532, 4615, 5756; 494, 519, 665; 189, 190, 135.)
 struct TileSize {
   int ctas, nt, deep, end;
 };
