@@ -895,6 +895,13 @@ bool make_map(CUtensorMap* map, const __half* p, int64_t rows, int64_t cols, int
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether results of `dtype` of matrices m x n are computed as fp32 ones are.  Of bf16 results the smallest
+// are: few elements' errors do not average out, and a step's slope at a singular value may be 3.9 (16 x 16 off
+// by up to 1.6e-3, 2 x 3 by 5e-3, 8 x 64 by 0.7e-3 besides the result's rounding, and two steps more by three
+// times that).  One of 31 x 31 takes 72 us for it (54), 48 of 16 x 16 68 (62).
+constexpr int64_t kFewElements = 1024;
+bool fine_for(int dtype, int64_t m, int64_t n) { return dtype == kF32 || m * n < kFewElements; }
+
 int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 // Matrices of one shape m x n (m <= n) that are iterated together, and where their parts lie
@@ -1230,7 +1237,7 @@ extern "C" {
 int64_t adasum_orthogonalize_scratch_bytes(int64_t batch, int64_t rows, int64_t cols, adasum_dtype_t dtype) {
   if (batch < 1 || rows < 1 || cols < 1 || !fits(rows, cols)) return 0;
   const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
-  const bool fine = dtype == ADASUM_F32;
+  const bool fine = fine_for(dtype, m, n);
   return ScratchMap(m, n, chunk_of(m, n, batch, fine), fine).bytes;
 }
 
@@ -1256,7 +1263,7 @@ adasum_status_t adasum_orthogonalize(const void* x, int64_t batch, int64_t rows,
   if (adasum_status_t st = set.check()) return st;
   if (encode_tiled() == nullptr) return ADASUM_ERR_CUDA;
   const int64_t m = std::min(rows, cols), n = std::max(rows, cols);
-  const bool fine = dtype == ADASUM_F32, transposed = rows > cols;
+  const bool fine = fine_for(dtype, m, n), transposed = rows > cols;
   const int64_t chunk = chunk_of(m, n, batch, fine);
   for (int64_t b0 = 0; b0 < batch; b0 += chunk) {
     const int count = static_cast<int>(std::min(chunk, batch - b0));

@@ -586,8 +586,8 @@ ADASUM_API int64_t adasum_relative_position_bias_backward_scratch_bytes(
  * every operand is the sum of two fp16 numbers; the result is about as far from the exact
  * one as if all were computed in fp32, at most twice (2e-7 to 7e-6 of the norm).  bf16
  * results: single fp16 operands, the linear term from two; the result is within 2^-9 of the
- * exact one's norm (2e-4 to 1.1e-3) before its rounding.  (A's and B's diagonals are fp32 in
- * both.)
+ * exact one's norm (2e-4 to 1.1e-3, in five steps) before its rounding; matrices of fewer
+ * than 1024 elements as fp32 ones.  (A's and B's diagonals are fp32 in both.)
  * NaN and infinities in a matrix make all of it NaN; a matrix of zeros stays zero.
  *
  * The conventions of the training operators above hold (scratch memory from the caller, any

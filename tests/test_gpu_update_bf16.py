@@ -14,7 +14,7 @@ import pytest
 import torch
 
 import adaptive_gradient_summation_gb300 as ags
-from test_gpu_update_tiles import matrices, off, tile  # noqa: F401 (a fixture)
+from test_gpu_update_tiles import in_fp32, matrices, off, tile  # noqa: F401 (a fixture)
 from updates_reference import orthogonal
 
 pytestmark = pytest.mark.gpu
@@ -39,3 +39,15 @@ def test_the_product_as_it_is(native):
         x = matrices("random", batch, rows, cols).to(BF16)
         want = orthogonal(x)
         assert all(e <= math.hypot(2.0 ** -9, r) for e, r in zip(off(ags.orthogonalize(x), want), off(want.to(BF16), want)))
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(11, 2, 1), (10, 2, 3), (10, 4, 7), (10, 9, 3), (6, 8, 8), (4, 16, 16), (4, 31, 31), (2, 59, 17), (3, 5, 200)])
+def test_few_elements(native, tile, batch, rows, cols):
+    """Whose errors do not average: computed as fp32 results are, by at most twice fp32's error and
+    2^-22, which the rounding may add twice where it moves a value over a rounding's border."""
+    x = matrices("random", batch, rows, cols).to(BF16)
+    for steps in (1, 3, 5, 7):
+        want = orthogonal(x, steps)
+        rounding, plain = off(want.to(BF16), want), off(in_fp32(x.float(), steps), want)
+        errors = off(ags.orthogonalize(x, steps=steps), want)
+        assert all(e <= r + 2 * (2 * p + 2.0 ** -22) for e, r, p in zip(errors, rounding, plain)), f"steps {steps}"
