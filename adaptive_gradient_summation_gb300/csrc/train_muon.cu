@@ -26,7 +26,7 @@
 //     The tensor cores cut every partial sum off towards zero: 64 cut-offs along a depth of 1024 lose
 //     1.4e-6 of a sum that grows evenly, which is made good by a factor (kCutOff), but up to twice that
 //     where one term outweighs the others, so that sums come in runs.  Off by 2e-7 to 7e-6, fp32
-//     throughout by 5e-7 to 1.1e-5: 0.2 to 1.5 times that.  (1024 x 4096 after five steps: 1.5e-5 without
+//     throughout by 5e-7 to 1.1e-5: 0.2 to 1.5 times that, 2.3 times for some of a few rows in seven steps.  (1024 x 4096 after five steps: 1.5e-5 without
 //     factor and diagonals apart, 1.2e-5 with the factor alone, now 0.8e-6.)
 #include <cuda.h>
 #include <cuda_fp16.h>

@@ -584,7 +584,7 @@ ADASUM_API int64_t adasum_relative_position_bias_backward_scratch_bytes(
  *
  * All products run on the tensor cores with fp16 operands and fp32 sums.  fp32 results:
  * every operand is the sum of two fp16 numbers; the result is about as far from the exact
- * one as if all were computed in fp32, at most twice (2e-7 to 7e-6 of the norm).  bf16
+ * one as if all were computed in fp32 (0.2 to 2.3 times, 2e-7 to 7e-6 of the norm).  bf16
  * results: single fp16 operands, the linear term from two; the result is within 2^-9 of the
  * exact one's norm (2e-4 to 1.1e-3, in five steps) before its rounding; matrices of fewer
  * than 1024 elements as fp32 ones.  (A's and B's diagonals are fp32 in both.)
