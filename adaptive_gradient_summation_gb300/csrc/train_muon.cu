@@ -11,7 +11,7 @@
 // Each step multiplies small singular values by a (3.4 in the usual iteration), and with them
 // the rounding errors of X that point into their directions: after five steps one rounding of
 // X to bf16 is 1e-2 to 1e-1 of the result's norm, to fp16 2e-3 to 2e-2 (random, power-law and
-// low-rank spectra).  So
+// low-rank spectra).
 // The diagonals of A and B, which dominate once the singular values are near 1, are kept apart in
 // fp32, the rest of the two being fp16:
 //     A A = E E + (d_i + d_j) E + d^2  with A = E + diag(d),   B X = F X + d_i X.
@@ -26,8 +26,9 @@
 //     The tensor cores cut every partial sum off towards zero: 64 cut-offs along a depth of 1024 lose
 //     1.4e-6 of a sum that grows evenly, which is made good by a factor (kCutOff), but up to twice that
 //     where one term outweighs the others, so that sums come in runs.  Off by 2e-7 to 7e-6, fp32
-//     throughout by 5e-7 to 1.1e-5: 0.2 to 1.5 times that, 2.3 times for some of a few rows in seven steps.  (1024 x 4096 after five steps: 1.5e-5 without
-//     factor and diagonals apart, 1.2e-5 with the factor alone, now 0.8e-6.)
+//     throughout by 5e-7 to 1.1e-5: 0.2 to 1.5 times that, 2.3 times for some of a few rows in seven
+//     steps.  (1024 x 4096 after five steps: 1.5e-5 without factor and diagonals apart, 1.2e-5 with the
+//     factor alone, now 0.8e-6.)
 #include <cuda.h>
 #include <cuda_fp16.h>
 
